@@ -186,6 +186,123 @@ int mha_sdpa_decode_fwd(int B, int H, int Nq, int Lmax, int d_k, int d_v, int dt
                         size_t ws_bytes, cudaStream_t stream);
 
 /*
+ * The 8-bit key/value cache: generation steps read half the bytes of a bf16 cache, and
+ * positions that attention has no use for can be dropped from it.
+ *   codes   K and V [B, H, Lmax, 64], one byte per value: mha_q8 MHA_Q8_E4M3 (e4m3 floats) or
+ *           MHA_Q8_I8 (signed integers, -127..127).
+ *   scales  fp32 [B, H, ceil(Lmax / block)] each for K and V, contiguous: one per `block` (16,
+ *           32, 64 or 128) consecutive positions of a head; value = code * scale.  What the
+ *           library writes are powers of two: the least 2^e with |x| <= 448 * 2^e (127 * 2^e
+ *           for integers) over the block, e kept within [-40, 40].
+ *   weights fp32 [B, H, Lmax], contiguous, optional: the attention weight each position has
+ *           received so far, summed over queries and heads (what eviction goes by).
+ * mha_kv_append_q8 fills a cache, mha_sdpa_decode_q8_fwd attends it, mha_sdpa_key_weights adds
+ * a prompt's weights, mha_kv_evict_q8 moves the positions worth keeping to another cache.
+ * H is the number of heads of the cache; queries may have a multiple of it (grouped heads:
+ * query head h reads cache head h / (H_q / H)).  Strides of caches count bytes (elements of one
+ * byte): {b, h, n} multiples of 16 and > 0, d stride 1, 16-byte aligned pointers.  Lengths are
+ * device memory, so the calls can be captured into a CUDA graph and replayed with new lengths.
+ * None of the four adds with atomics: results are bitwise reproducible.
+ */
+typedef enum { MHA_Q8_E4M3 = 0, MHA_Q8_I8 = 1 } mha_q8;
+
+/*
+ * mha_kv_append_q8 -- quantise new keys and values into the cache ([JY] Transformer 翻译样例 >
+ * Decoder: each generated position joins what later steps attend):
+ *   token i < new_len[b] of batch element b goes to position cache_len[b] + i, as
+ *   code = round(x / scale) (nearest, ties to even), with its block's scale as above.  Where a
+ *   block holds earlier positions its scale never falls: if the new tokens need a larger one,
+ *   the earlier codes are written again under it (rounded from the codes, not from the values
+ *   they came from).  Infinities saturate and do not enter the scale; a NaN is stored as NaN
+ *   (e4m3) or 0 (integers).
+ *   K, V [B,H,N,64] (dtype); new_len int32[B], clamped to [0, N], or NULL (every sequence gets
+ *   N); cache_len int32[B], the positions there already, clamped to [0, Lmax]; the caller adds
+ *   the new ones to it afterwards.  Tokens past Lmax are dropped.  weights of the new positions
+ *   are set to 0 (NULL: no weights kept).  Nothing else of the cache is written.
+ *   strides: NULL for contiguous, or 16 strides {K, V, K_cache, V_cache} x {b, h, n, d}; those
+ *   of K and V in elements, multiples of 8 (bf16) or 4 (fp32) and > 0, d stride 1, pointers
+ *   16-byte aligned.  d_k == d_v == 64 for both dtypes.
+ */
+int mha_kv_append_q8(int B, int H, int N, int Lmax, int d_k, int d_v, int dtype, int qtype,
+                     int block, const int32_t* new_len, const int32_t* cache_len, const void* K,
+                     const void* V, void* K_cache, void* V_cache, float* k_scale, float* v_scale,
+                     float* weights, const int64_t* strides, cudaStream_t stream);
+
+/*
+ * mha_decode_q8_workspace_size -- bytes of device workspace mha_sdpa_decode_q8_fwd needs
+ * (with_weights: whether weights will be passed).
+ */
+int mha_decode_q8_workspace_size(int B, int H, int Hkv, int Nq, int Lmax, int with_weights,
+                                 size_t* bytes);
+
+/*
+ * mha_sdpa_decode_q8_fwd -- mha_sdpa_decode_fwd against an 8-bit cache, with grouped heads:
+ *     O[b,h,i] = sum_j p_ij v_j,  p_i = softmax_j(Q[b,h,i] . k_j * scale, allowed)
+ *     weights[b,g,j] += sum over the query heads of group g and i of p_ij     (unless NULL)
+ *   Q [B,H,Nq,64], O [B,H,Nq,64] (dtype); caches and scales with Hkv heads, H a multiple of
+ *   Hkv.  cache_len, causal, scale and rows without an allowed key (zeros, no weight) as for
+ *   mha_sdpa_decode_fwd; 1 <= Nq <= 16 and Nq <= Lmax.  Positions past cache_len may hold
+ *   anything.  Scales must be positive and within [2^-40, 2^40]; they need not be powers of two.
+ *   strides: NULL for contiguous, or 16 strides {Q, K, V, O} x {b, h, n, d} (Q, O in elements
+ *   as for mha_kv_append_q8's K).  O may not alias an input.
+ *   workspace: mha_decode_q8_workspace_size() bytes, 256-byte aligned; calls that may run at
+ *   the same time (two streams, two replayed graphs) need one each.
+ */
+int mha_sdpa_decode_q8_fwd(int B, int H, int Hkv, int Nq, int Lmax, int d_k, int d_v, int dtype,
+                           int qtype, int block, int causal, const int32_t* cache_len,
+                           float scale, const void* Q, const void* K_cache, const void* V_cache,
+                           const float* k_scale, const float* v_scale, void* O,
+                           const int64_t* strides, float* weights, void* workspace,
+                           size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * mha_key_weights_workspace_size -- bytes of device workspace mha_sdpa_key_weights needs.
+ */
+int mha_key_weights_workspace_size(int B, int H, int Hkv, int Nq, int Nk, int dtype,
+                                   size_t* bytes);
+
+/*
+ * mha_sdpa_key_weights -- the attention weight each key of a prompt received, from the
+ * forward's log-sum-exp (mha_sdpa_fwd_lse with the same Q, K, mask and scale):
+ *     weights[b,g,j] += sum over the query heads h of group g and i of
+ *                       exp(Q[b,h,i] . K[b,g,j] * scale - lse[b,h,i])          (allowed pairs)
+ *   Q [B,H,Nq,64], K [B,Hkv,Nk,64] (dtype, the values before quantisation), lse fp32 [B,H,Nq]
+ *   contiguous (rows with +inf add nothing).  mask, key_len, scale as for mha_sdpa_fwd;
+ *   query_len int32[B], clamped to [0, Nq], or NULL: rows i >= query_len[b] of a padded batch
+ *   add nothing and may hold anything.  Keys j >= key_len[b] keep their weights.
+ *   weights [B, Hkv, weights_ld], weights_ld >= Nk: only the first Nk of each head change.
+ *   strides: NULL for contiguous, or 8 element strides {Q, K} x {b, h, n, d} as for
+ *   mha_kv_append_q8's K.  workspace: mha_key_weights_workspace_size() bytes, 256-byte aligned
+ *   (may be NULL when that is 0).
+ */
+int mha_sdpa_key_weights(int B, int H, int Hkv, int Nq, int Nk, int d_k, int dtype, int mask,
+                         const int32_t* key_len, const int32_t* query_len, float scale,
+                         const void* Q, const void* K, const float* lse, const int64_t* strides,
+                         float* weights, int64_t weights_ld, void* workspace, size_t ws_bytes,
+                         cudaStream_t stream);
+
+/*
+ * mha_kv_evict_q8 -- move the positions worth keeping into another cache of the same codes and
+ * block size.  Of each head of batch element b, with L = cache_len[b] (clamped to [0, Lmax]):
+ *   L <= keep: every position; else the newest min(recent, keep) positions and, of the others,
+ *   the keep - min(recent, keep) with the largest weights (equal weights: the lower position
+ *   first; a NaN counts as -inf).  Heads choose for themselves; their order is kept.
+ *   Position kept[b,h,r] of the old cache becomes position r < len_out[b] = min(L, keep) of the
+ *   new one: codes, scale and weight.  A block of the new cache takes the largest scale of the
+ *   positions it receives; codes that came under a smaller one are rounded to it.
+ *   kept int32 [B,H,keep], -1 from len_out[b] on; len_out int32[B].  Rows, scales and weights
+ *   of the new cache behind len_out[b] stay as they were.  weights_out may be NULL.
+ *   1 <= keep <= Lmax_out, recent >= 0.  The new cache may not overlap the old one, nor
+ *   len_out cache_len.  strides: NULL for contiguous, or 16 byte strides {K, V, K_out, V_out}.
+ */
+int mha_kv_evict_q8(int B, int H, int Lmax, int Lmax_out, int d_k, int d_v, int qtype, int block,
+                    int keep, int recent, const int32_t* cache_len, const void* K_cache,
+                    const void* V_cache, const float* k_scale, const float* v_scale,
+                    const float* weights, void* K_out, void* V_out, float* k_scale_out,
+                    float* v_scale_out, float* weights_out, int32_t* len_out, int32_t* kept,
+                    const int64_t* strides, cudaStream_t stream);
+
+/*
  * mha_layer_workspace_size -- bytes of device workspace mha_layer_fwd needs for these sizes.
  * The workspace holds the projected Q/K/V, the head-concat buffer and the W^O output.
  */

@@ -32,3 +32,4 @@ from .backward import (  # noqa: F401
     sdpa_lse_ref,
     mha_layer_bwd_ref,
 )
+from . import cache_q8  # noqa: F401

@@ -36,3 +36,13 @@ from .api import (  # noqa: F401
     set_deterministic,
     wait_selftest,
 )
+from .cache_q8 import (  # noqa: F401
+    KvCacheQ8,
+    decode_q8_workspace_size,
+    key_weights_workspace_size,
+    kv_append_q8,
+    kv_cache_q8,
+    kv_evict_q8,
+    sdpa_decode_q8,
+    sdpa_key_weights,
+)

@@ -19,6 +19,8 @@ MHA_ERR_DEVICE_TIMEOUT = -6
 MHA_ERR_DEVICE_BOUNDS = -7
 MHA_F32 = 0
 MHA_BF16 = 1
+MHA_Q8_E4M3 = 0
+MHA_Q8_I8 = 1
 MASKS = {"none": 0, "causal": 1, "key_padding": 2}
 
 _c_int, _c_float, _vp = ctypes.c_int, ctypes.c_float, ctypes.c_void_p
@@ -33,6 +35,14 @@ PROTOTYPES = {
     "mha_decode_workspace_size": (_c_int, [_c_int] * 5 + [ctypes.POINTER(_size)]),
     "mha_sdpa_decode_fwd": (_c_int, [_c_int] * 8 + [_vp, _c_float] + [_vp] * 5
                             + [_vp, _size, _vp]),
+    "mha_kv_append_q8": (_c_int, [_c_int] * 9 + [_vp] * 11),
+    "mha_decode_q8_workspace_size": (_c_int, [_c_int] * 6 + [ctypes.POINTER(_size)]),
+    "mha_sdpa_decode_q8_fwd": (_c_int, [_c_int] * 11 + [_vp, _c_float] + [_vp] * 9
+                               + [_size, _vp]),
+    "mha_key_weights_workspace_size": (_c_int, [_c_int] * 6 + [ctypes.POINTER(_size)]),
+    "mha_sdpa_key_weights": (_c_int, [_c_int] * 8 + [_vp, _vp, _c_float] + [_vp] * 5
+                             + [_i64, _vp, _size, _vp]),
+    "mha_kv_evict_q8": (_c_int, [_c_int] * 10 + [_vp] * 15),
     "mha_layer_workspace_size": (_c_int, [_c_int] * 8 + [ctypes.POINTER(_size)]),
     "mha_layer_fwd": (_c_int, [_c_int] * 9 + [_vp, _c_float] + [_vp] * 10 + [_size, _vp]),
     "mha_layer_bwd_workspace_size": (_c_int, [_c_int] * 9 + [ctypes.POINTER(_size)]),

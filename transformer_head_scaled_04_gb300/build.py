@@ -25,8 +25,10 @@ DEBUG_LIB_PATH = os.path.join(PKG_DIR, "libmha_debug.so")
 SOURCES = ["capi.cu", "gemm_bf16.cu", "gemm_f32.cu", "sdpa_bf16.cu", "sdpa_f32.cu",
            "sdpa_decode.cu", "sdpa_bwd_f32.cu", "sdpa_bwd_bf16.cu", "bwd_util.cu", "layernorm.cu",
            "gemm_ln_bf16.cu", "gemm2_bf16.cu",
-           "layer_noalloc.cu", "layer_host.cu"]
-HEADERS = ["device_common.cuh", "launchers.h"]
+           "layer_noalloc.cu", "layer_host.cu",
+           "capi_q8.cu", "kv_append_q8.cu", "sdpa_decode_q8.cu", "sdpa_key_weights.cu",
+           "kv_evict_q8.cu"]
+HEADERS = ["device_common.cuh", "launchers.h", "nvtx_range.h", "q8_common.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

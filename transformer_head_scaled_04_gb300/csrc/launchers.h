@@ -27,6 +27,15 @@ int check_layer_call(int B, int H, int Nq, int Nk, int D, int d_k, int d_v, int 
                      const void* gamma, const void* beta, const void* y, const void* workspace,
                      size_t ws_bytes, bool builtin_workspace, DevCtx* ctx);
 
+// ---- the current device's context (MHA_ERR_UNSUPPORTED unless it is an sm_103)
+int current_device_ctx(DevCtx* ctx);
+// 4-D maps {64, N, H, B} of a [B, H, N, 64] tensor with element strides st = {b, h, n, d = 1}:
+// bf16 with 128-byte swizzle, 8-bit codes with 64-byte swizzle; box {64, box_rows, 1, 1}
+bool encode_map_bf16(CUtensorMap* m, const void* base, int B, int H, int N, const int64_t* st,
+                     uint32_t box_rows);
+bool encode_map_u8(CUtensorMap* m, const void* base, int B, int H, int N, const int64_t* st,
+                   uint32_t box_rows);
+
 // ---- per-kernel launch preparation: raises the kernel's dynamic shared-memory limit to
 // smem_bytes and reports its register count (num_regs may be null), once per (kernel, device);
 // later calls return the cached result without driver calls.
@@ -150,6 +159,60 @@ int decode_num_splits(int Lmax);  // 256-key chunks per (batch, head)
 cudaError_t launch_sdpa_decode_bf16(const CUtensorMap& tmK, const CUtensorMap& tmV,
                                     const DecodeArgs& a, float* part, const DevCtx& ctx,
                                     cudaStream_t s);
+
+// ---- the 8-bit key/value cache (codes and scales: q8_common.cuh).  n_blocks: scales per head,
+// ceil(Lmax / block); cache strides in bytes {b, h, n, 1}; weights [B, Hkv, Lmax] or null.
+struct KvAppendArgs {
+  int B, H, N, Lmax, block, n_blocks;
+  const int32_t *new_len, *cache_len;  // device, B entries; new_len may be null (= N)
+  const void *K, *V;                   // [B, H, N, 64], element strides sk, sv
+  void *Kc, *Vc;                       // [B, H, Lmax, 64] codes, strides skc, svc
+  float *k_scale, *v_scale;            // [B, H, n_blocks]
+  float* weights;
+  int64_t sk[4], sv[4], skc[4], svc[4];
+};
+cudaError_t launch_kv_append_q8(const KvAppendArgs& a, int dtype, int qtype, cudaStream_t s);
+
+struct DecodeQ8Args {
+  int B, H, Hkv, Nq, Lmax, block, n_blocks;
+  int causal;                // as in DecodeArgs
+  const int32_t* cache_len;  // device, B entries, clamped to [0, Lmax]
+  float scale;
+  const void* Q;             // [B, H, Nq, 64], element strides sq
+  const void *Kc, *Vc;
+  const float *k_scale, *v_scale;
+  void* O;                   // [B, H, Nq, 64], element strides so
+  float* weights;
+  int64_t sq[4], sk[4], sv[4], so[4];
+};
+size_t decode_q8_workspace(int B, int H, int Hkv, int Nq, int Lmax, bool weights);
+cudaError_t launch_sdpa_decode_q8(const DecodeQ8Args& a, int dtype, int qtype, void* ws,
+                                  const DevCtx& ctx, cudaStream_t s);
+
+struct KeyWeightsArgs {
+  int B, H, Hkv, Nq, Nk, mask;          // mask: an mha_mask
+  const int32_t *key_len, *query_len;   // device, B entries; query_len may be null (= Nq)
+  float scale;
+  const void *Q, *K;                    // [B, H, Nq, 64], [B, Hkv, Nk, 64]
+  const float* lse;                     // [B, H, Nq]
+  float* weights;                       // [B, Hkv, ld]
+  int64_t ld;
+  int64_t sq[4], sk[4];
+};
+size_t key_weights_workspace(int B, int H, int Hkv, int Nq, int Nk, int dtype);
+cudaError_t launch_key_weights_simt(const KeyWeightsArgs& a, int dtype, cudaStream_t s);
+
+struct KvEvictArgs {
+  int B, H, Lmax, Lmax_out, block, n_blocks, n_blocks_out, keep, recent;
+  const int32_t* cache_len;
+  const void *Kc, *Vc;
+  const float *k_scale, *v_scale, *weights;
+  void *Ko, *Vo;
+  float *k_scale_out, *v_scale_out, *weights_out;  // weights_out may be null
+  int32_t *len_out, *kept;                         // [B], [B, H, keep]
+  int64_t sk[4], sv[4], sko[4], svo[4];
+};
+cudaError_t launch_kv_evict_q8(const KvEvictArgs& a, int qtype, cudaStream_t s);
 
 // ---- attention backward (dQ, dK, dV) from Q, K, V, O, dO and the forward's log-sum-exp
 struct SdpaBwdArgs {
