@@ -241,7 +241,7 @@ int mha_decode_q8_workspace_size(int B, int H, int Hkv, int Nq, int Lmax, int wi
  *     weights[b,g,j] += sum over the query heads of group g and i of p_ij     (unless NULL)
  *   Q [B,H,Nq,64], O [B,H,Nq,64] (dtype); caches and scales with Hkv heads, H a multiple of
  *   Hkv.  cache_len, causal, scale and rows without an allowed key (zeros, no weight) as for
- *   mha_sdpa_decode_fwd; 1 <= Nq <= 16 and Nq <= Lmax.  Positions past cache_len may hold
+ *   mha_sdpa_decode_fwd; 1 <= Nq <= 16, Nq <= Lmax, H / Hkv * Nq <= 4096.  Positions past cache_len may hold
  *   anything.  Scales must be positive and within [2^-40, 2^40]; they need not be powers of two.
  *   strides: NULL for contiguous, or 16 strides {Q, K, V, O} x {b, h, n, d} (Q, O in elements
  *   as for mha_kv_append_q8's K).  O may not alias an input.

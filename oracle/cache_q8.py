@@ -91,15 +91,16 @@ def dequantised_ref(cache: dict, name: str, b: int, h: int, L: int, block: int, 
 
 
 def decode_ref(Q, cache: dict, cache_len, block: int, code: str, causal: bool, scale=None):
-    """(O, added weights, sum_j p |v|, largest sum |q||k| scale of a row): the attention of
-    Q [B, Hq, Nq, 64] over the cache, and the two sizes its rounding errors go by."""
+    """(O, added weights, sum_j p |v|, max_j(p s) sum_j |code| with s the value's scale, largest
+    sum |q||k| scale of a row): the attention of Q [B, Hq, Nq, 64] over the cache, and the three
+    sizes its rounding errors go by."""
     B, Hq, Nq, D = Q.shape
     H, Lmax = cache["k"].shape[1:3]
     G = Hq // H
     scale = D ** -0.5 if scale is None else scale
     O = np.zeros((B, Hq, Nq, D))
     W = np.zeros((B, H, Lmax))
-    pv, qk = np.zeros_like(O), 0.0
+    pv, low, qk = np.zeros_like(O), np.zeros_like(O), 0.0
     for b in range(B):
         L = int(np.clip(cache_len[b], 0, Lmax))
         for h in range(H):
@@ -117,8 +118,10 @@ def decode_ref(Q, cache: dict, cache_len, block: int, code: str, causal: bool, s
                     O[b, h * G + g, i] = p @ v[:n]
                     pv[b, h * G + g, i] = p @ np.abs(v[:n])
                     W[b, h, :n] += p
+                    s = cache["v_scale"][b, h, np.arange(n) // block]
+                    low[b, h * G + g, i] = (p * s).max() * np.abs(v[:n] / s[:, None]).sum(0)
                     qk = max(qk, float((np.abs(k[:n]) @ np.abs(q)).max() * scale))
-    return O, W, pv, qk
+    return O, W, pv, low, qk
 
 
 def key_weights_ref(Q, K, lse, mask: str, key_len=None, query_len=None, scale=None):

@@ -4,9 +4,13 @@ Bounds, from the arithmetic.  Codes, scales, lengths and positions are equal.  A
 of 64 products, each sum rounded once to fp32 (at most half a step, 2^-24 of the running size),
 so it is off by at most 64 * 2^-24 * S = 2^-18 S with S = scale * sum |q||k|; a softmax weight
 (a ratio of two exponentials) by twice that relatively, plus 2^-19 for the exponentials and the
-division.  With n keys added in fp32 the sums are off by n * 2^-24.  The bf16 path rounds the
-weights to fp16 before their product with v (2^-11) and the output to bf16 (2^-8).  Hence
-    |O - ref| <= r * sum_j p_j |v_j| (+ 2^-8 |ref|),  r = 2^-17 S + n 2^-24 + 2^-19 (+ 2^-11)
+division.  With n keys added in fp32 the sums are off by n * 2^-24.  The weights
+p_j s_j that meet the value codes are fp16, scaled so that the row's largest is 2^13: below 2^-14
+an fp16 (of the fp32 path, the second of its two terms) is off by up to half its least step, 2^-25
+or 2^-38 of that largest, whatever its own size.  The bf16 path rounds those weights once (2^-11)
+and the output to bf16 (2^-8).  Hence
+    |O - ref| <= r * sum_j p_j |v_j| + 2^-38 max_j(p_j s_j) sum_j |code_j| (+ 2^-8 |ref|),
+    r = 2^-17 S + n 2^-24 + 2^-19 (+ 2^-11)
     |W - ref| <= r * ref  without the bf16 terms (weights are fp32 on both paths).
 """
 import numpy as np
@@ -166,9 +170,9 @@ def test_append_without_weights_and_token_by_token():
     assert_same(got, want, "e4m3", "token by token")
 
 
-def close_decode(got, ref, pv, qk, n, dtype, what):
+def close_decode(got, ref, pv, low, qk, n, dtype, what):
     r = 2.0 ** -17 * qk + n * 2.0 ** -24 + 2.0 ** -19 + (2.0 ** -11 if dtype == "bf16" else 0)
-    bound = r * pv + (2.0 ** -8 * np.abs(ref) if dtype == "bf16" else 0) + 1e-30
+    bound = r * pv + 2.0 ** -38 * low + (2.0 ** -8 * np.abs(ref) if dtype == "bf16" else 0) + 1e-30
     assert np.all(np.isfinite(got)), what
     worst = (np.abs(got - ref) / bound).max()
     assert worst <= 1, f"{what}: {worst:.3f} of the bound"
@@ -215,10 +219,10 @@ def test_decode(B, H, Hkv, Nq, Lmax, block, dtype, code, causal, cl, add):
     cache = to_gpu(c, block, code)
     before = c["weights"].copy()
     O = mha.sdpa_decode_q8(dev(Q, DT[dtype]), cache, i32(cl), causal=causal, add_weights=add)
-    ref, W, pv, qk = oq.decode_ref(Q, c, cl, block, code, causal)
+    ref, W, pv, low, qk = oq.decode_ref(Q, c, cl, block, code, causal)
     n = int(np.clip(max(cl), 0, Lmax))
     got = O.double().cpu().numpy()
-    close_decode(got, ref, pv, qk, n, dtype, "decode")
+    close_decode(got, ref, pv, low, qk, n, dtype, "decode")
     assert np.all(got[pv == 0] == 0)            # rows without keys (or with values all zero)
     w = cache.weights.double().cpu().numpy()
     if add:
@@ -246,8 +250,8 @@ def test_decode_token_major_scale_and_workspace():
     ws = torch.empty(mha.decode_q8_workspace_size(B, H, Hkv, Nq, Lmax, False), dtype=torch.uint8,
                      device="cuda")
     mha.sdpa_decode_q8(tq, cache, i32([600, 333]), scale=0.05, workspace=ws, out=out)
-    ref, _, pv, qk = oq.decode_ref(Q, c, [600, 333], block, "int8", True, scale=0.05)
-    close_decode(out.double().cpu().numpy(), ref, pv, qk, 600, "bf16", "token-major")
+    ref, _, pv, low, qk = oq.decode_ref(Q, c, [600, 333], block, "int8", True, scale=0.05)
+    close_decode(out.double().cpu().numpy(), ref, pv, low, qk, 600, "bf16", "token-major")
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -265,8 +269,8 @@ def test_decode_scales_far_apart_and_not_powers_of_two(dtype):
     Q[0, 1, 0] = g.standard_normal(64)
     Q = fin(Q, dtype)
     O = mha.sdpa_decode_q8(dev(Q, DT[dtype]), to_gpu(c, 16, "e4m3"), i32([64]))
-    ref, _, pv, qk = oq.decode_ref(Q, c, [64], 16, "e4m3", True)
-    close_decode(O.double().cpu().numpy(), ref, pv, qk, 64, dtype, "scales far apart")
+    ref, _, pv, low, qk = oq.decode_ref(Q, c, [64], 16, "e4m3", True)
+    close_decode(O.double().cpu().numpy(), ref, pv, low, qk, 64, dtype, "scales far apart")
 
 
 def test_decode_large_and_small_queries():
@@ -283,8 +287,8 @@ def test_decode_large_and_small_queries():
     O = mha.sdpa_decode_q8(dev(Q, torch.bfloat16), to_gpu(c, 32, "int8"), i32([100]))
     got = O.double().cpu().numpy()
     for h in (1, 2, 3, 4):
-        ref, _, pv, qk = oq.decode_ref(Q[:, h:h + 1], c, [100], 32, "int8", True)
-        close_decode(got[:, h:h + 1], ref, pv, qk, 100, "bf16", f"row {h}")
+        ref, _, pv, low, qk = oq.decode_ref(Q[:, h:h + 1], c, [100], 32, "int8", True)
+        close_decode(got[:, h:h + 1], ref, pv, low, qk, 100, "bf16", f"row {h}")
     # scores of 1e30: one key has all the weight
     kk = oq.dequantised_ref(c, "k", 0, 0, 100, 32, "int8")
     vv = oq.dequantised_ref(c, "v", 0, 0, 100, 32, "int8")
@@ -461,8 +465,8 @@ def test_prompt_then_steps_then_eviction(code):
         c = oq.append_ref(c, k, v, n.tolist(), None, block, code)
         n += 2
         O = mha.sdpa_decode_q8(dev(q, torch.bfloat16), small, n, add_weights=True)
-        ref, W, pv, qk = oq.decode_ref(q, c, n.tolist(), block, code, True)
-        close_decode(O.double().cpu().numpy(), ref, pv, qk, keep + 8, "bf16", f"step {step}")
+        ref, W, pv, low, qk = oq.decode_ref(q, c, n.tolist(), block, code, True)
+        close_decode(O.double().cpu().numpy(), ref, pv, low, qk, keep + 8, "bf16", f"step {step}")
         got = from_gpu(small)
         close_weights(got["weights"], c["weights"], W, qk, keep + 8, f"weights {step}")
         c["weights"] = got["weights"]

@@ -92,7 +92,7 @@ def test_decode_is_the_attention_of_the_dequantised_cache(causal):
     c = oq.append_ref(empty(2, 2, 50, 16), g.standard_normal((2, 2, 45, 64)),
                       g.standard_normal((2, 2, 45, 64)), [0, 0], [45, 20], 16, "e4m3")
     Q = g.standard_normal((2, 4, 3, 64))
-    O, W, _, _ = oq.decode_ref(Q, c, [45, 20], 16, "e4m3", causal)
+    O, W, _, _, _ = oq.decode_ref(Q, c, [45, 20], 16, "e4m3", causal)
     k, v = (np.stack([np.stack([oq.dequantised_ref(c, n, b, h // 2, 50, 16, "e4m3")
                                 for h in range(4)]) for b in range(2)]) for n in "kv")
     ref = oracle.sdpa_ref(Q, k, v, "causal_cache" if causal else "key_padding",
