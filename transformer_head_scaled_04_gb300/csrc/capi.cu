@@ -195,22 +195,6 @@ bool map_dq_acc_f32(CUtensorMap* m, const void* base, int B, int H, int rows) {
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// [B, H, N, 64] 8-bit codes with byte strides st = {b, h, n, 1}; box {64, box_rows, 1, 1}.
-bool map_bhnd_u8(CUtensorMap* m, const void* base, int B, int H, int N, const int64_t* st,
-                 uint32_t box_rows) {
-  EncodeTiledFn fn = encode_fn();
-  if (fn == nullptr) return false;
-  cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(H),
-                        static_cast<cuuint64_t>(B)};
-  cuuint64_t strides[3] = {static_cast<cuuint64_t>(st[2]), static_cast<cuuint64_t>(st[1]),
-                           static_cast<cuuint64_t>(st[0])};
-  cuuint32_t box[4] = {64, box_rows, 1, 1};
-  cuuint32_t es[4] = {1, 1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // The sublayer's last two steps as one kernel (W^O fused with the residual LayerNorm) pay off
@@ -484,10 +468,6 @@ int current_device_ctx(DevCtx* ctx) { return device_ctx(ctx); }
 bool encode_map_bf16(CUtensorMap* m, const void* base, int B, int H, int N, const int64_t* st,
                      uint32_t box_rows) {
   return map_bhnd_bf16(m, base, B, H, N, st, box_rows);
-}
-bool encode_map_u8(CUtensorMap* m, const void* base, int B, int H, int N, const int64_t* st,
-                   uint32_t box_rows) {
-  return map_bhnd_u8(m, base, B, H, N, st, box_rows);
 }
 cudaError_t launch_wait_selftest(const DevCtx& ctx, cudaStream_t s) {
   wait_selftest_kernel<<<1, 32, 0, s>>>(ctx.status, ctx.timeout_ns);

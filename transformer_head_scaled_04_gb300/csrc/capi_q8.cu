@@ -86,10 +86,10 @@ int mha_decode_q8_workspace_size(int B, int H, int Hkv, int Nq, int Lmax, int wi
   if (bytes == nullptr || B < 1 || H < 1 || Hkv < 1 || Nq < 1 || Lmax < 1 || H % Hkv != 0 ||
       (with_weights != 0 && with_weights != 1))
     return MHA_ERR_INVALID;
-  // rows of a cache head in the join's shared memory, blocks of its grid
+  // rows of a cache head in the join's shared memory, blocks of its grid, tiles of all heads
   const int64_t rows = static_cast<int64_t>(H / Hkv) * Nq, heads = static_cast<int64_t>(B) * Hkv;
   if (Nq > mha::kDecodeMaxQ || Lmax > (1 << 30) || rows > 4096 || heads * rows > (1 << 28) ||
-      heads * ((Lmax + 511) / 512) > (1 << 30))
+      heads * ((rows + 7) / 8) * ((Lmax + 31) / 32) >= (1LL << 31))
     return MHA_ERR_UNSUPPORTED;
   *bytes = round_up(mha::decode_q8_workspace(B, H, Hkv, Nq, Lmax, with_weights != 0), 256);
   return MHA_OK;

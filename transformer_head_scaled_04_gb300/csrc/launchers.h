@@ -29,12 +29,10 @@ int check_layer_call(int B, int H, int Nq, int Nk, int D, int d_k, int d_v, int 
 
 // ---- the current device's context (MHA_ERR_UNSUPPORTED unless it is an sm_103)
 int current_device_ctx(DevCtx* ctx);
-// 4-D maps {64, N, H, B} of a [B, H, N, 64] tensor with element strides st = {b, h, n, d = 1}:
-// bf16 with 128-byte swizzle, 8-bit codes with 64-byte swizzle; box {64, box_rows, 1, 1}
+// 4-D map {64, N, H, B} of a bf16 [B, H, N, 64] tensor with element strides st = {b, h, n,
+// d = 1}, 128-byte swizzle, box {64, box_rows, 1, 1}
 bool encode_map_bf16(CUtensorMap* m, const void* base, int B, int H, int N, const int64_t* st,
                      uint32_t box_rows);
-bool encode_map_u8(CUtensorMap* m, const void* base, int B, int H, int N, const int64_t* st,
-                   uint32_t box_rows);
 
 // ---- per-kernel launch preparation: raises the kernel's dynamic shared-memory limit to
 // smem_bytes and reports its register count (num_regs may be null), once per (kernel, device);

@@ -12,8 +12,9 @@
 //   - all (head, 32-position tile) pairs of the batch laid out in one line and cut into equal
 //     runs, one per warp of a grid that just fills the GPU, so sequences of any mix of lengths
 //     keep every SM busy to the end, and a run is long enough that partial results are few;
-//   - every warp streams its tiles through a ring of its own (TMA, one mbarrier per slot): no
-//     block-wide barrier in the loop, 12 KB in flight per warp;
+//   - every warp streams its tiles through a ring of its own, 12 KB of 16-byte asynchronous
+//     copies in flight, without a barrier between warps.  (Bulk copies issued by one lane and
+//     waited for on mbarriers cost that warp 1200 of a tile's 3400 cycles.)
 //   - the products on the tensor cores (mma.sync m16n8k16, fp16 operands, fp32 sums), the cache
 //     as the operand with 16 rows and the queries as the one with 8 columns: S^T = K Q^T and
 //     O^T = V^T P^T, since there are often no more than 8 query rows.  tcgen05 would want 64
@@ -34,10 +35,10 @@
 // Runs end at heads' ends: each piece leaves (O, m, l) in the workspace, and a second launch
 // joins a row's pieces, and adds the weights 2^(x_ij - m_i) / l_i from the scores that the first
 // one stored.  No atomics: one order of sums.
-// Every wait is bounded.
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "launchers.h"
 #include "q8_common.cuh"
@@ -51,10 +52,9 @@ constexpr int kTileBytes = kTile * kD;     // 2 KB of K, 2 KB of V
 constexpr int kStages = 3;
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kSmemBytes = 1024 + kWarps * kStages * (2 * kTileBytes + 8);
-constexpr int kErrTimeout = -6;
-constexpr int kSiteDecodeQ8 = 33;
+constexpr int kSmemBytes = kWarps * kStages * 2 * kTileBytes;
 constexpr float kOffset = 13.f;            // weights that meet the codes: 2^13 at most
+constexpr float kNone = -3.402823466e38f;  // maximum of no position (finite: -inf - it is -inf)
 
 // How the rows of a cache head are cut: groups of 8 * NR rows, NR column tiles of the products
 struct RowPlan {
@@ -79,12 +79,11 @@ struct Params {
   DecodeQ8Args a;
   RowPlan rp;
   int workers;        // warps of the first launch's grid
+  int block_shift;    // log2 of the positions per scale
   float* part;        // [slots][RS][64] unnormalised O
   float* stat;        // [slots][RS][2] m, l
   float* scores;      // [B][Hkv][R][Lpad] x in base-2 units (-inf: excluded); null: not kept
   int64_t Lpad;
-  int* status;
-  uint64_t timeout_ns;
 };
 
 __device__ __forceinline__ int cached(const DecodeQ8Args& a, int b) {
@@ -92,55 +91,61 @@ __device__ __forceinline__ int cached(const DecodeQ8Args& a, int b) {
 }
 __device__ __forceinline__ int tiles_of(int L) { return (L + kTile - 1) / kTile; }
 
-// Sums over batch elements by a whole warp: tiles of all, and of those before `b`
-__device__ __forceinline__ void tile_sums(const DecodeQ8Args& a, int b, int64_t* before,
-                                          int64_t* total) {
-  const int lane = threadIdx.x & 31;
-  int64_t all = 0, pre = 0;
-  for (int x = lane; x < a.B; x += 32) {
-    const int t = tiles_of(cached(a, x));
-    all += t;
-    pre += x < b ? t : 0;
-  }
+// The line of tiles, seen by a whole warp: `per` segments (cache heads times row groups) of each
+// batch element in turn, cut into runs of `run` tiles, one per worker (the last may be shorter).
+// 32-bit numbers: the entry point refuses lines of 2^31 tiles.
+struct Line {
+  uint32_t total, run;
+  int here;  // lane i: inclusive sum of the tiles of batch elements 0..i (i < 32)
+};
+__device__ __forceinline__ int scan_add(int v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    all += __shfl_xor_sync(0xffffffffu, all, o);
-    pre += __shfl_xor_sync(0xffffffffu, pre, o);
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 31) >= o) v += u;
   }
-  *before = pre;
-  *total = all;
+  return v;
 }
-// batch element that holds tile x of the line (x < total * per), and the tiles before it
-__device__ __forceinline__ int find_batch(const DecodeQ8Args& a, int64_t x, int64_t per,
-                                          int64_t* before) {
-  const int lane = threadIdx.x & 31;
-  int64_t base = 0;
+// tiles of batch elements x0 + lane, summed over the lanes up to this one
+__device__ __forceinline__ int scan_batch(const DecodeQ8Args& a, int x0, int per) {
+  const int b = x0 + static_cast<int>(threadIdx.x & 31);
+  return scan_add(b < a.B ? tiles_of(cached(a, b)) * per : 0);
+}
+__device__ __forceinline__ Line line_of(const DecodeQ8Args& a, int per, int workers) {
+  Line n;
+  n.here = scan_batch(a, 0, per);
+  n.total = __shfl_sync(0xffffffffu, n.here, 31);
+  for (int x0 = 32; x0 < a.B; x0 += 32)
+    n.total += __shfl_sync(0xffffffffu, scan_batch(a, x0, per), 31);
+  n.run = (n.total + workers - 1) / workers;
+  return n;
+}
+// batch element that holds tile x (x < total), and the tiles before it
+__device__ __forceinline__ int find_batch(const Line& n, const DecodeQ8Args& a, int per, uint32_t x,
+                                          uint32_t* before) {
+  uint32_t base = 0;
   for (int x0 = 0;; x0 += 32) {
-    const int b = x0 + lane;
-    const int64_t n = b < a.B ? tiles_of(cached(a, b)) * per : 0;
-    int64_t incl = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
+    const uint32_t incl = x0 == 0 ? n.here : scan_batch(a, x0, per);
     const uint32_t m = __ballot_sync(0xffffffffu, base + incl > x);
-    if (m != 0) {
-      const int src = __ffs(m) - 1;
-      *before = base + __shfl_sync(0xffffffffu, incl - n, src);
-      return x0 + src;
+    if (m != 0 || x0 + 32 >= a.B) {  // the second: not reached for x < total
+      const int src = max(__ffs(m) - 1, 0);
+      const uint32_t up = __shfl_sync(0xffffffffu, incl, max(src - 1, 0));
+      *before = base + (src == 0 ? 0 : up);
+      return min(x0 + src, a.B - 1);
     }
     base += __shfl_sync(0xffffffffu, incl, 31);
-    if (x0 + 32 >= a.B) {  // past the end: not reached for x < total
-      *before = base;
-      return a.B;
-    }
   }
 }
-// run of worker w of W over T tiles, and the worker of tile x (W <= T: no run is empty)
-__device__ __forceinline__ int64_t run_start(int64_t w, int64_t T, int64_t W) { return w * T / W; }
-__device__ __forceinline__ int64_t worker_of(int64_t x, int64_t T, int64_t W) {
-  return ((x + 1) * W - 1) / T;
+// tiles before batch element b
+__device__ __forceinline__ uint32_t tiles_before(const Line& n, const DecodeQ8Args& a, int per,
+                                                 int b) {
+  uint32_t base = 0;
+  int x0 = 0;
+  for (; x0 + 32 <= b; x0 += 32)
+    base += __shfl_sync(0xffffffffu, x0 == 0 ? n.here : scan_batch(a, x0, per), 31);
+  const int incl = x0 == 0 ? n.here : scan_batch(a, x0, per);
+  const int up = __shfl_sync(0xffffffffu, incl, max(b - x0 - 1, 0));
+  return base + (b == x0 ? 0 : up);
 }
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -150,6 +155,29 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       " {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// the same onto zeros
+__device__ __forceinline__ void mma16816_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                              uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9},"
+      " {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// 16 bytes from global to shared memory, past L1; a lane's copies complete in groups
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void copy_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // four codes to two fp16 pairs (exact)
@@ -204,10 +232,34 @@ __device__ __forceinline__ void load16(const float* p, float (&f)[16]) {
   }
 }
 
-// a place on the line of tiles: tile kt of nt of head-and-row-group hr of batch element b
+// a place on the line of tiles: tile kt of nt of row group rg of head hk of batch element b
 struct Cursor {
-  int b, hr, kt, nt, L;
+  int b, hk, rg, kt, nt, L;
 };
+// the first tile of the next row group, head or batch element that has any
+__device__ __forceinline__ void next_segment(const Params& p, Cursor& k) {
+  k.kt = 0;
+  if (++k.rg < p.rp.RG) return;
+  k.rg = 0;
+  if (++k.hk < p.a.Hkv) return;
+  k.hk = 0;
+  do {
+    k.L = ++k.b < p.a.B ? cached(p.a, k.b) : kTile;  // past the last: never used
+    k.nt = tiles_of(k.L);
+  } while (k.nt == 0);
+}
+// log2 of a positive normal number, exact for powers of two
+__device__ __forceinline__ float log2_approx(float x) {
+  const uint32_t u = __float_as_uint(x);
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(__uint_as_float((u & 0x7fffffu) | 0x3f800000u)));
+  return y + (__uint_as_float((u >> 23) | 0x4b000000u) - 8388735.f);  // + the exponent
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   uint32_t d;
@@ -218,96 +270,96 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
 // T: float (two fp16 terms per operand) or bf16 (one).  NR: column tiles of 8 query rows
 template <typename T, int QT, int NR>
 __global__ void __launch_bounds__(kThreads, blocks_per_sm(sizeof(T) / 2, NR))
-    decode_q8_kernel(const __grid_constant__ CUtensorMap tmK,
-                     const __grid_constant__ CUtensorMap tmV, const Params p) {
+    decode_q8_kernel(const Params p) {
   constexpr int kTerms = sizeof(T) == 4 ? 2 : 1;
   const DecodeQ8Args& a = p.a;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = align_smem_1024(smem_raw);
+  extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   uint8_t* ring = smem + warp * (kStages * 2 * kTileBytes);
-  uint64_t* bars =
-      reinterpret_cast<uint64_t*>(smem + kWarps * kStages * 2 * kTileBytes) + warp * kStages;
-  if (lane == 0) {
-    prefetch_tmap(&tmK);
-    prefetch_tmap(&tmV);
-#pragma unroll
-    for (int s = 0; s < kStages; ++s) mbar_init(smem_u32(bars + s), 1);
-    fence_mbar_init();
-  }
-  __syncwarp();
-  pdl_launch_dependents();
   pdl_wait();  // the previous kernel's output is complete from here on
+  pdl_launch_dependents();  // after the wait: the join reads cache_len before its own
 
   // this warp's run of tiles.  Consecutive workers sit in different blocks, so that few tiles
   // spread over the SMs
   const int per = a.Hkv * p.rp.RG;
-  int64_t unused, T_all;
-  tile_sums(a, 0, &unused, &T_all);
-  T_all *= per;
-  const int64_t W = min(static_cast<int64_t>(p.workers), T_all);
-  const int64_t worker = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;
-  if (worker >= W) return;
-  const int64_t x0 = run_start(worker, T_all, W);
-  const int count = static_cast<int>(run_start(worker + 1, T_all, W) - x0);
+  const Line line = line_of(a, per, p.workers);
+  const uint32_t worker = warp * gridDim.x + blockIdx.x;
+  const uint32_t x0 = worker * line.run;
+  if (x0 >= line.total) return;
+  const int count = static_cast<int>(min(line.run, line.total - x0));
 
   Cursor c;
   {
-    int64_t before;
-    c.b = find_batch(a, x0, per, &before);
+    uint32_t before;
+    c.b = find_batch(line, a, per, x0, &before);
     c.L = cached(a, c.b);
     c.nt = tiles_of(c.L);
-    c.hr = static_cast<int>((x0 - before) / c.nt);
+    const int hr = static_cast<int>((x0 - before) / c.nt);
     c.kt = static_cast<int>((x0 - before) % c.nt);
+    c.hk = hr / p.rp.RG;
+    c.rg = hr % p.rp.RG;
   }
-  auto advance = [&](Cursor& k) {
-    if (++k.kt < k.nt) return;
-    k.kt = 0;
-    if (++k.hr < per) return;
-    k.hr = 0;
-    do {
-      k.L = ++k.b < a.B ? cached(a, k.b) : kTile;  // past the last: never used
-      k.nt = tiles_of(k.L);
-    } while (k.nt == 0);
+  // The next tile to ask for.  A lane copies chunk t of rows g, g + 8, g + 16 and g + 24 of K and
+  // of V; chunk i of row r is stored at i ^ ((r >> 1) & 3), so that eight rows' chunks read
+  // together, or a row's pairs, meet different banks.
+  Cursor ahead = c;
+  const uint8_t *k_next = nullptr, *v_next = nullptr;
+  auto place = [&]() {
+    const int64_t row = static_cast<int64_t>(ahead.kt) * kTile + g;
+    k_next = static_cast<const uint8_t*>(a.Kc) + ahead.b * a.sk[0] + ahead.hk * a.sk[1] +
+             row * a.sk[2] + t * 16;
+    v_next = static_cast<const uint8_t*>(a.Vc) + ahead.b * a.sv[0] + ahead.hk * a.sv[1] +
+             row * a.sv[2] + t * 16;
   };
-  Cursor ahead = c;  // the next tile to ask for
+  place();
   int asked = 0;
-  auto ask = [&]() {
-    const int s = asked % kStages;
-    if (lane == 0) {
-      const uint32_t bar = smem_u32(bars + s);
-      uint8_t* dst = ring + s * 2 * kTileBytes;
-      mbar_arrive_expect_tx(bar, 2 * kTileBytes);
-      tma_load_4d(smem_u32(dst), &tmK, bar, 0, ahead.kt * kTile, ahead.hr / p.rp.RG, ahead.b);
-      tma_load_4d(smem_u32(dst + kTileBytes), &tmV, bar, 0, ahead.kt * kTile,
-                  ahead.hr / p.rp.RG, ahead.b);
+  const int64_t k_step = 8 * a.sk[2], v_step = 8 * a.sv[2];
+  const int k_at = (t ^ ((g >> 1) & 3)) << 4;  // chunk t of a row 8i + g
+  const uint32_t dst0 = smem_u32(ring) + g * kD + k_at;
+  auto ask = [&](int slot) {
+    if (asked < count) {
+      const uint32_t dst = dst0 + slot * 2 * kTileBytes;
+      if ((ahead.kt + 1) * kTile <= a.Lmax) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          copy16_async(dst + i * 8 * kD, k_next + i * k_step);
+          copy16_async(dst + kTileBytes + i * 8 * kD, v_next + i * v_step);
+        }
+      } else {  // rows behind the cache: the slot keeps what it held, unused
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (ahead.kt * kTile + i * 8 + g < a.Lmax) {
+            copy16_async(dst + i * 8 * kD, k_next + i * k_step);
+            copy16_async(dst + kTileBytes + i * 8 * kD, v_next + i * v_step);
+          }
+      }
+      ++asked;
+      k_next += 4 * k_step;
+      v_next += 4 * v_step;
+      if (++ahead.kt == ahead.nt && asked < count) {
+        next_segment(p, ahead);
+        place();
+      }
     }
-    advance(ahead);
-    ++asked;
+    copy_async_commit();  // a group per tile, also an empty one
   };
-  while (asked < min(kStages, count)) ask();
+#pragma unroll
+  for (int s = 0; s < kStages; ++s) ask(s);
 
-  // scales of a tile: lanes 0, 1 those of its two 16-position groups' keys, 2, 3 values'.  A
-  // group behind the last position counts as 1 (its scores are excluded below).
-  auto load_scale = [&](const Cursor& k) -> float {
-    const int pos = k.kt * kTile + (lane & 1) * 16;
-    if (lane >= 4 || pos >= k.L) return 1.f;
-    const int64_t at =
-        (static_cast<int64_t>(k.b) * a.Hkv + k.hr / p.rp.RG) * a.n_blocks + pos / a.block;
-    return __ldg((lane < 2 ? a.k_scale : a.v_scale) + at);
-  };
+  const int v_at = (((g >> 1) ^ t) << 4) + (g & 1) * 8;  // columns 8g.. of a row 8i + 2t + {0, 1}
 
   // In the products' results a lane holds positions g and g + 8 of each 16 for the two rows
   // 8 nr + 2t + {0, 1}: the row statistics below are those rows'.
   uint32_t qf[kTerms][NR][4][2];  // queries, row 8 nr + g: operand fragments of four inner steps
-  float qs[NR][2];                // what a score is to be multiplied by for its row
+  float2 qs[NR];                  // what a score is to be multiplied by for its row
   int lim[NR][2];                 // last position that the row may see
-  float o[NR][4][4], l[NR][2], m[NR][2];
+  float o[NR][4][4], m[NR][2];
+  float2 l[NR];  // of the lane's own positions
   const float c2 = a.scale * 1.4426950408889634f;
 
   auto start_segment = [&]() {
-    const int hk = c.hr / p.rp.RG, r0 = c.hr % p.rp.RG * (8 * NR);
+    const int hk = c.hk, r0 = c.rg * (8 * NR);
 #pragma unroll
     for (int nr = 0; nr < NR; ++nr) {
       const int r = r0 + nr * 8 + g;
@@ -326,8 +378,10 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(sizeof(T) / 2, NR))
       for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(f[i]));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      const int ex = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -100);
-      const float up = pow2i(13 - ex), down = pow2i(ex - 13) * c2;
+      // (2^-60 and 2^-80 keep the factors normal numbers, so that an excluded score's -inf stays
+      // -inf; scores that small are 0 to the softmax)
+      const int ex = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -60);
+      const float up = pow2i(13 - ex), down = fmaxf(pow2i(ex - 13) * c2, pow2i(-80));
       // inner step k: lane t supplies dims 16t + 4k + {0, 1} and {2, 3}
 #pragma unroll
       for (int k = 0; k < 4; ++k)
@@ -340,11 +394,11 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(sizeof(T) / 2, NR))
         }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        qs[nr][e] = __shfl_sync(0xffffffffu, down, (2 * t + e) * 4);
+        (e ? qs[nr].y : qs[nr].x) = __shfl_sync(0xffffffffu, down, (2 * t + e) * 4);
         lim[nr][e] = a.causal ? c.L - a.Nq + (r0 + nr * 8 + 2 * t + e) % a.Nq : c.L - 1;
-        l[nr][e] = 0.f;
-        m[nr][e] = -INFINITY;
+        m[nr][e] = kNone;
       }
+      l[nr] = make_float2(0.f, 0.f);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -353,14 +407,14 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(sizeof(T) / 2, NR))
   };
 
   auto end_segment = [&]() {
-    const int64_t slot = worker + static_cast<int64_t>(c.b) * per + c.hr;
-    const int r0 = c.hr % p.rp.RG * (8 * NR);
+    const int64_t slot = worker + static_cast<int64_t>(c.b) * per + c.hk * p.rp.RG + c.rg;
+    const int r0 = c.rg * (8 * NR);
 #pragma unroll
     for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int rl = nr * 8 + 2 * t + e;
-        float s = l[nr][e];
+        float s = e ? l[nr].y : l[nr].x;
         s += __shfl_xor_sync(0xffffffffu, s, 4);
         s += __shfl_xor_sync(0xffffffffu, s, 8);
         s += __shfl_xor_sync(0xffffffffu, s, 16);
@@ -376,263 +430,271 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(sizeof(T) / 2, NR))
       }
   };
 
-  bool fresh = true;
-  float sc_next = load_scale(c);
-  for (int it = 0; it < count; ++it) {
-    if (fresh) start_segment();
-    const float sc = sc_next;
-    Cursor nx = c;
-    advance(nx);
-    if (it + 1 < count) sc_next = load_scale(nx);  // a tile ahead of its use
-    const float sc_log = log2f(sc), sc_inv = 1.f / sc;
-    const int s = it % kStages;
-    if (!__all_sync(0xffffffffu,
-                    mbar_wait(smem_u32(bars + s), (it / kStages) & 1, p.timeout_ns))) {
-      if (lane == 0) record_error(p.status, kErrTimeout, kSiteDecodeQ8);
-      for (int x = it; x < asked; ++x)  // copies in flight land (bounded) before the block ends
-        (void)mbar_wait(smem_u32(bars + x % kStages), (x / kStages) & 1, p.timeout_ns);
-      return;
-    }
-    const uint8_t* sK = ring + s * 2 * kTileBytes;
-    const uint8_t* sV = sK + kTileBytes;
-    const int pos = c.kt * kTile;
-    // some row may not see the whole tile
-    const bool edge = pos + kTile - 1 > c.L - (a.causal ? a.Nq : 1);
-
-    // ---- scores of two groups of 16 positions
-    float x[2][NR][4], ev[2], inv[2];
+  int slot = 0, done = 0;
+  while (done < count) {
+    // tiles kt .. of one row group and head
+    start_segment();
+    const int64_t head = static_cast<int64_t>(c.b) * a.Hkv + c.hk;
+    // scales of a tile: lanes 0, 1 those of its two 16-position groups' keys, 2, 3 values'.  A
+    // group behind the last position counts as 1 (its scores are excluded below).
+    const float* scale_row = (lane < 2 ? a.k_scale : a.v_scale) + head * a.n_blocks;
+    auto load_scale = [&](int kt) -> float {
+      const int at = kt * kTile + (lane & 1) * 16;
+      return lane < 4 && at < c.L ? __ldg(scale_row + (at >> p.block_shift)) : 1.f;
+    };
+    float* score_row = nullptr;  // of row 2t of the group
+    const int rows_here = p.rp.R - c.rg * (8 * NR) - 2 * t;  // live rows from there on
+    if (p.scores != nullptr)
+      score_row = p.scores + (head * p.rp.R + c.rg * (8 * NR) + 2 * t) * p.Lpad + g;
+    // A maximum's rounding beyond 2^20 is too coarse for exponents that are rounded once: there
+    // they are taken from scores rounded as the maximum was
+    bool huge = false;
+    float sc_next = load_scale(c.kt);
+    const int last = min(c.nt, c.kt + count - done);
+    done += last - c.kt;
+    for (; c.kt < last; ++c.kt) {
+      const float sc = sc_next;
+      if (c.kt + 1 < last) sc_next = load_scale(c.kt + 1);  // a tile ahead of its use
+      const float sc_log = log2_approx(sc), sc_inv = rcp_approx(sc);
+      copy_async_wait<kStages - 1>();  // this lane's copies of the tile have landed
+      __syncwarp();                    // and every lane's
+      const uint8_t* sK = ring + slot * 2 * kTileBytes;
+      const uint8_t* sV = sK + kTileBytes;
+      const int pos = c.kt * kTile;
+      // kEdge: some row may not see the whole tile (or `huge`).  Its code apart: in one body it
+      // cost the other tiles 78 of 562 instructions and 14% of the time (16 rows, 8 x 8 x 16384
+      // positions)
+      auto tile = [&](auto edge_type) -> bool {
+        constexpr bool kEdge = decltype(edge_type)::value;
+        // ---- scores of two groups of 16 positions
+        float x[2][NR][4];
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      uint32_t h[2][8];  // positions g and g + 8: 16-byte chunk t of a row, 64-byte swizzle
+        for (int q = 0; q < 2; ++q) {
+          uint32_t h[2][8];  // positions g and g + 8: 16-byte chunk t of a row
 #pragma unroll
-      for (int z = 0; z < 2; ++z) {
-        const int row = q * 16 + z * 8 + g;
-        const uint4 u = *reinterpret_cast<const uint4*>(
-            sK + row * kD + ((t ^ ((row >> 1) & 3)) << 4));
-        codes_to_half<QT>(u.x, h[z][0], h[z][1]);
-        codes_to_half<QT>(u.y, h[z][2], h[z][3]);
-        codes_to_half<QT>(u.z, h[z][4], h[z][5]);
-        codes_to_half<QT>(u.w, h[z][6], h[z][7]);
-      }
-#pragma unroll
-      for (int nr = 0; nr < NR; ++nr) {
-        float part[kTerms == 2 ? 4 : 1][4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t fa[4] = {h[0][2 * k], h[1][2 * k], h[0][2 * k + 1], h[1][2 * k + 1]};
-          float (&d)[4] = part[kTerms == 2 ? k : 0];
-          if (kTerms == 2 || k == 0) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) d[i] = 0.f;
+          for (int z = 0; z < 2; ++z) {
+            const int row = q * 16 + z * 8 + g;
+            const uint4 u = *reinterpret_cast<const uint4*>(sK + row * kD + k_at);
+            codes_to_half<QT>(u.x, h[z][0], h[z][1]);
+            codes_to_half<QT>(u.y, h[z][2], h[z][3]);
+            codes_to_half<QT>(u.z, h[z][4], h[z][5]);
+            codes_to_half<QT>(u.w, h[z][6], h[z][7]);
           }
-          if constexpr (kTerms == 2)
-            mma16816(d, fa, qf[kTerms - 1][nr][k][0], qf[kTerms - 1][nr][k][1]);
-          mma16816(d, fa, qf[0][nr][k][0], qf[0][nr][k][1]);
-        }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          x[q][nr][i] = kTerms == 2 ? (part[0][i] + part[kTerms - 1][i]) +
-                                          (part[kTerms == 2 ? 2 : 0][i] + part[kTerms == 2 ? 3 : 0][i])
-                                    : part[0][i];
-      }
-    }
-    // ---- scaled scores, kept for the weights; + log2 of the value's scale; running maximum
-    float top[NR][2];
+          for (int nr = 0; nr < NR; ++nr) {
+            float part[kTerms == 2 ? 4 : 1][4];
 #pragma unroll
-    for (int nr = 0; nr < NR; ++nr) top[nr][0] = top[nr][1] = -INFINITY;
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t fa[4] = {h[0][2 * k], h[1][2 * k], h[0][2 * k + 1], h[1][2 * k + 1]};
+              float (&d)[4] = part[kTerms == 2 ? k : 0];
+              if constexpr (kTerms == 2)
+                mma16816_zero(d, fa, qf[kTerms - 1][nr][k][0], qf[kTerms - 1][nr][k][1]);
+              if (kTerms == 1 && k == 0)
+                mma16816_zero(d, fa, qf[0][nr][k][0], qf[0][nr][k][1]);
+              else
+                mma16816(d, fa, qf[0][nr][k][0], qf[0][nr][k][1]);
+            }
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const float ks = __shfl_sync(0xffffffffu, sc, q);
-      ev[q] = __shfl_sync(0xffffffffu, sc_log, 2 + q);
-      inv[q] = __shfl_sync(0xffffffffu, sc_inv, 2 + q);
-#pragma unroll
-      for (int nr = 0; nr < NR; ++nr) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[q][nr][i] *= ks * qs[nr][i & 1];
-          if (edge && pos + q * 16 + (i >> 1) * 8 + g > lim[nr][i & 1]) x[q][nr][i] = -INFINITY;
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          top[nr][e] = fmaxf(top[nr][e], fmaxf(x[q][nr][e], x[q][nr][2 + e]) + ev[q]);
-      }
-    }
-    if (p.scores != nullptr) {
-      const int64_t row0 =
-          (static_cast<int64_t>(c.b) * a.Hkv + c.hr / p.rp.RG) * p.rp.R +
-          c.hr % p.rp.RG * (8 * NR);
-#pragma unroll
-      for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int rl = nr * 8 + 2 * t + e;
-          if (c.hr % p.rp.RG * (8 * NR) + rl < p.rp.R) {
-            float* dst = p.scores + (row0 + rl) * p.Lpad + pos + g;
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              dst[q * 16] = x[q][nr][e];
-              dst[q * 16 + 8] = x[q][nr][2 + e];
+            for (int i = 0; i < 4; ++i) {
+              x[q][nr][i] = part[0][i];
+              if constexpr (kTerms == 2)
+                x[q][nr][i] = (part[0][i] + part[1][i]) + (part[2][i] + part[3][i]);
+              if (kEdge && pos + q * 16 + (i >> 1) * 8 + g > lim[nr][i & 1])
+                x[q][nr][i] = -INFINITY;
             }
           }
         }
-    }
-    bool grew = false;
+        // ---- the scales: a score is x * f, its exponent x * f + log2 of the value's scale
+        float2 f[2][NR];
+        float ev[2], inv[2];
 #pragma unroll
-    for (int nr = 0; nr < NR; ++nr)
+        for (int q = 0; q < 2; ++q) {
+          const float ks = __shfl_sync(0xffffffffu, sc, q);
+          ev[q] = __shfl_sync(0xffffffffu, sc_log, 2 + q);
+          inv[q] = __shfl_sync(0xffffffffu, sc_inv, 2 + q);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float v = top[nr][e];
-        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-        top[nr][e] = fmaxf(m[nr][e], v);
-        grew |= top[nr][e] > m[nr][e];
-      }
-    if (__any_sync(0xffffffffu, grew)) {
-#pragma unroll
-      for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          // a first maximum (m = -inf) finds O = l = 0
-          const float f = top[nr][e] == m[nr][e] ? 1.f : ex2_approx(m[nr][e] - top[nr][e]);
-          m[nr][e] = top[nr][e];
-          l[nr][e] *= f;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            o[nr][j][e] *= f;
-            o[nr][j][2 + e] *= f;
-          }
+          for (int nr = 0; nr < NR; ++nr)
+            f[q][nr] = fmul2(make_float2(ks, ks), qs[nr]);
         }
-    }
-    // ---- weights, 16 positions at a time, and their product with the value codes
-    float po[kTerms == 2 ? NR : 1][4][4];
-    if constexpr (kTerms == 2) {
+        if (score_row != nullptr) {  // kept for the weights
 #pragma unroll
-      for (int nr = 0; nr < NR; ++nr)
+          for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+            for (int e = 0; e < 2; ++e)
+              if (nr * 8 + e < rows_here) {
+                float* dst = score_row + (nr * 8 + e) * p.Lpad + pos;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) po[nr][j][i] = 0.f;
-    }
+                for (int q = 0; q < 2; ++q) {
+                  const float fe = e ? f[q][nr].y : f[q][nr].x;
+                  dst[q * 16] = x[q][nr][e] * fe;
+                  dst[q * 16 + 8] = x[q][nr][2 + e] * fe;
+                }
+              }
+        }
+        // ---- running maximum
+        float top[NR][2];
+        bool grew = false;
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      uint32_t pf[kTerms][NR][2];
+        for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-      for (int nr = 0; nr < NR; ++nr) {
-        float w[4];
+          for (int e = 0; e < 2; ++e) {
+            top[nr][e] = fmaxf(
+                fmaf(fmaxf(x[0][nr][e], x[0][nr][2 + e]), e ? f[0][nr].y : f[0][nr].x, ev[0]),
+                fmaf(fmaxf(x[1][nr][e], x[1][nr][2 + e]), e ? f[1][nr].y : f[1][nr].x, ev[1]));
+            grew |= top[nr][e] > m[nr][e];
+          }
+        if (__any_sync(0xffffffffu, grew)) {  // seldom, once a row has seen many positions
+          bool far = false;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float mm = m[nr][e] == -INFINITY ? 0.f : m[nr][e];
+          for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float v = top[nr][e];
+              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+              v = fmaxf(m[nr][e], v);
+              // a first maximum finds O = l = 0
+              const float u = v == m[nr][e] ? 1.f : ex2_approx(m[nr][e] - v);
+              m[nr][e] = v;
+              far |= fabsf(v) > 1048576.f && v != kNone;
+              (e ? l[nr].y : l[nr].x) *= u;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                o[nr][j][e] *= u;
+                o[nr][j][2 + e] *= u;
+              }
+            }
+          huge = __any_sync(0xffffffffu, far);
+        }
+        if (!kEdge && huge) return false;  // taken again below: nothing so far depends on it
+        // ---- weights, 16 positions at a time, and their product with the value codes
+        float po[kTerms == 2 ? NR : 1][4][4];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t pf[kTerms][NR][2];
           // the fp32 path keeps the offset out of the exponent, whose rounding it would coarsen
-          const float shift = ev[q] - mm + (kTerms == 2 ? 0.f : kOffset);
+          const float up = ev[q] + (kTerms == 2 ? 0.f : kOffset);
+#pragma unroll
+          for (int nr = 0; nr < NR; ++nr) {
+            const float2 shift = make_float2(up - m[nr][0], up - m[nr][1]);
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              float2 w = make_float2(x[q][nr][2 * z], x[q][nr][2 * z + 1]);
+              if constexpr (kEdge)  // two roundings (a packed pair of operations may be fused)
+                w = make_float2(__fadd_rn(__fmul_rn(w.x, f[q][nr].x), shift.x),
+                                __fadd_rn(__fmul_rn(w.y, f[q][nr].y), shift.y));
+              else
+                w = ffma2(w, f[q][nr], shift);
+              w.x = ex2_approx(w.x);
+              w.y = ex2_approx(w.y);
+              if constexpr (kTerms == 2) w = fmul2(w, make_float2(8192.f, 8192.f));  // 2^kOffset
+              l[nr] = ffma2(w, make_float2(inv[q], inv[q]), l[nr]);
+              const uint32_t hi = pack_half(w.x, w.y);
+              pf[0][nr][z] = transpose8x8(hi);
+              if constexpr (kTerms == 2)
+                pf[kTerms - 1][nr][z] = transpose8x8(pack_rest(w.x, w.y, hi));
+            }
+          }
+          // value rows 2t, 2t+1, 2t+8, 2t+9 of the 16, columns 8g .. 8g+7
+          uint2 v[4];
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            const int row = q * 16 + 2 * t + (z >> 1) * 8 + (z & 1);
+            v[z] = *reinterpret_cast<const uint2*>(sV + row * kD + v_at);
+            if constexpr (kEdge) {
+              // rows behind the last position hold anything: 0.  A NaN among the rows that some
+              // query may not see must reach only those that do: taken out of the product here,
+              // put into O below
+              if (pos + row >= c.L) v[z] = make_uint2(0u, 0u);
+              if constexpr (QT == kE4m3) {
+                v[z].x &= ~__vcmpeq4(v[z].x & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                v[z].y &= ~__vcmpeq4(v[z].y & 0x7f7f7f7fu, 0x7f7f7f7fu);
+              }
+            }
+          }
+          uint32_t b0[8], b1[8];  // column 8g + j: rows 2t, 2t+1, and 2t+8, 2t+9
 #pragma unroll
           for (int z = 0; z < 2; ++z) {
-            float v = ex2_approx(x[q][nr][2 * z + e] + shift);
-            if constexpr (kTerms == 2) v *= 8192.f;  // 2^kOffset
-            w[2 * z + e] = v;
-            l[nr][e] = fmaf(v, inv[q], l[nr][e]);
+            const uint32_t a0 = z ? v[0].y : v[0].x, a1 = z ? v[1].y : v[1].x;
+            const uint32_t a2 = z ? v[2].y : v[2].x, a3 = z ? v[3].y : v[3].x;
+            codes_to_half<QT>(__byte_perm(a0, a1, 0x5140), b0[4 * z], b0[4 * z + 1]);
+            codes_to_half<QT>(__byte_perm(a0, a1, 0x7362), b0[4 * z + 2], b0[4 * z + 3]);
+            codes_to_half<QT>(__byte_perm(a2, a3, 0x5140), b1[4 * z], b1[4 * z + 1]);
+            codes_to_half<QT>(__byte_perm(a2, a3, 0x7362), b1[4 * z + 2], b1[4 * z + 3]);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t fa[4] = {b0[2 * j], b0[2 * j + 1], b1[2 * j], b1[2 * j + 1]};
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr) {
+              if constexpr (kTerms == 2) {
+                if (q == 0)
+                  mma16816_zero(po[nr][j], fa, pf[kTerms - 1][nr][0], pf[kTerms - 1][nr][1]);
+                else
+                  mma16816(po[nr][j], fa, pf[kTerms - 1][nr][0], pf[kTerms - 1][nr][1]);
+                mma16816(po[nr][j], fa, pf[0][nr][0], pf[0][nr][1]);
+              } else {
+                mma16816(o[nr][j], fa, pf[0][nr][0], pf[0][nr][1]);
+              }
+            }
           }
         }
+        if constexpr (kTerms == 2) {
 #pragma unroll
-        for (int z = 0; z < 2; ++z) {
-          const uint32_t hi = pack_half(w[2 * z], w[2 * z + 1]);
-          pf[0][nr][z] = transpose8x8(hi);
-          if constexpr (kTerms == 2)
-            pf[kTerms - 1][nr][z] = transpose8x8(pack_rest(w[2 * z], w[2 * z + 1], hi));
+          for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) o[nr][j][i] += po[nr][j][i];
         }
-      }
-      // value rows 2t, 2t+1, 2t+8, 2t+9 of the 16, columns 8g .. 8g+7
-      uint2 v[4];
+        if constexpr (QT == kE4m3 && kEdge) {
+          // columns 8g .. 8g+7 of each position: NaN into the rows that see it
+          for (int row = 0; row < kTile && pos + row < c.L; ++row) {
+            const uint2 u = *reinterpret_cast<const uint2*>(
+                sV + row * kD + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + (g & 1) * 8);
+            if ((__vcmpeq4(u.x & 0x7f7f7f7fu, 0x7f7f7f7fu) |
+                 __vcmpeq4(u.y & 0x7f7f7f7fu, 0x7f7f7f7fu)) == 0)
+              continue;
 #pragma unroll
-      for (int z = 0; z < 4; ++z) {
-        const int row = q * 16 + 2 * t + (z >> 1) * 8 + (z & 1);
-        v[z] = *reinterpret_cast<const uint2*>(
-            sV + row * kD + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + (g & 1) * 8);
-        if (edge) {
-          // rows behind the last position hold anything: 0.  A NaN among the rows that some
-          // query may not see must reach only those that do: taken out of the product here,
-          // put into O below
-          if (pos + row >= c.L) v[z] = make_uint2(0u, 0u);
-          if constexpr (QT == kE4m3) {
-            v[z].x &= ~__vcmpeq4(v[z].x & 0x7f7f7f7fu, 0x7f7f7f7fu);
-            v[z].y &= ~__vcmpeq4(v[z].y & 0x7f7f7f7fu, 0x7f7f7f7fu);
+            for (int i = 0; i < 8; ++i)
+              if ((((i < 4 ? u.x : u.y) >> (8 * (i & 3))) & 127u) == 127u)
+#pragma unroll
+                for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e)
+                    if (pos + row <= lim[nr][e])
+                      o[nr][i >> 1][2 * (i & 1) + e] = __int_as_float(0x7fffffff);
           }
         }
-      }
-      uint32_t b0[8], b1[8];  // column 8g + j: rows 2t, 2t+1, and 2t+8, 2t+9
-#pragma unroll
-      for (int z = 0; z < 2; ++z) {
-        const uint32_t a0 = z ? v[0].y : v[0].x, a1 = z ? v[1].y : v[1].x;
-        const uint32_t a2 = z ? v[2].y : v[2].x, a3 = z ? v[3].y : v[3].x;
-        codes_to_half<QT>(__byte_perm(a0, a1, 0x5140), b0[4 * z], b0[4 * z + 1]);
-        codes_to_half<QT>(__byte_perm(a0, a1, 0x7362), b0[4 * z + 2], b0[4 * z + 3]);
-        codes_to_half<QT>(__byte_perm(a2, a3, 0x5140), b1[4 * z], b1[4 * z + 1]);
-        codes_to_half<QT>(__byte_perm(a2, a3, 0x7362), b1[4 * z + 2], b1[4 * z + 3]);
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t fa[4] = {b0[2 * j], b0[2 * j + 1], b1[2 * j], b1[2 * j + 1]};
-#pragma unroll
-        for (int nr = 0; nr < NR; ++nr) {
-          if constexpr (kTerms == 2) {
-            mma16816(po[nr][j], fa, pf[kTerms - 1][nr][0], pf[kTerms - 1][nr][1]);
-            mma16816(po[nr][j], fa, pf[0][nr][0], pf[0][nr][1]);
-          } else {
-            mma16816(o[nr][j], fa, pf[0][nr][0], pf[0][nr][1]);
-          }
-        }
-      }
+        return true;
+      };
+      if (pos + kTile - 1 > c.L - (a.causal ? a.Nq : 1) || !tile(std::false_type{}))
+        tile(std::true_type{});
+      __syncwarp();  // every lane has read the slot
+      ask(slot);
+      if (++slot == kStages) slot = 0;
     }
-    if constexpr (kTerms == 2) {
-#pragma unroll
-      for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[nr][j][i] += po[nr][j][i];
-    }
-    if (QT == kE4m3 && edge) {
-      // columns 8g .. 8g+7 of each position: NaN into the rows that see it
-      for (int row = 0; row < kTile && pos + row < c.L; ++row) {
-        const uint2 u = *reinterpret_cast<const uint2*>(
-            sV + row * kD + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + (g & 1) * 8);
-        if ((__vcmpeq4(u.x & 0x7f7f7f7fu, 0x7f7f7f7fu) |
-             __vcmpeq4(u.y & 0x7f7f7f7fu, 0x7f7f7f7fu)) == 0)
-          continue;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if ((((i < 4 ? u.x : u.y) >> (8 * (i & 3))) & 127u) == 127u)
-#pragma unroll
-            for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                if (pos + row <= lim[nr][e])
-                  o[nr][i >> 1][2 * (i & 1) + e] = __int_as_float(0x7fffffff);
-      }
-    }
-    __syncwarp();  // every lane has read the slot
-    if (asked < count) ask();
-    fresh = nx.hr != c.hr || nx.b != c.b;
-    if (fresh || it + 1 == count) end_segment();
-    c = nx;
+    end_segment();
+    if (c.kt == c.nt) next_segment(p, c);
   }
 }
 
 // ---- joining the pieces
-// the workers that hold pieces of segment hr of batch element b (whole warp); false: none
-__device__ __forceinline__ bool pieces_of(const Params& p, int b, int hr, int64_t* first,
-                                          int64_t* last) {
-  const int per = p.a.Hkv * p.rp.RG;
-  int64_t before, total;
-  tile_sums(p.a, b, &before, &total);
-  const int nt = tiles_of(cached(p.a, b));
-  if (nt == 0) return false;
-  const int64_t T = total * per, W = min(static_cast<int64_t>(p.workers), T);
-  const int64_t x = before * per + static_cast<int64_t>(hr) * nt;
-  *first = worker_of(x, T, W);
-  *last = worker_of(x + nt - 1, T, W);
-  return true;
-}
+// the workers that hold pieces of segment hr of batch element b (which has tiles)
+struct Pieces {
+  uint32_t start, run;  // tiles before b's first segment, tiles of a run
+  int nt;               // tiles of one of b's segments
+  __device__ __forceinline__ Pieces(const Params& p, int b) {
+    const int per = p.a.Hkv * p.rp.RG;
+    const Line line = line_of(p.a, per, p.workers);
+    start = tiles_before(line, p.a, per, b);
+    run = line.run;
+    nt = tiles_of(cached(p.a, b));
+  }
+  __device__ __forceinline__ int first(int hr) const { return (start + hr * nt) / run; }
+  __device__ __forceinline__ int last(int hr) const { return (start + hr * nt + nt - 1) / run; }
+};
 
 __device__ __forceinline__ void put2(__nv_bfloat16* q, float a, float b) {
   *reinterpret_cast<uint32_t*>(q) = pack_bf16x2(a, b);
@@ -641,45 +703,66 @@ __device__ __forceinline__ void put2(float* q, float a, float b) {
   *reinterpret_cast<float2*>(q) = make_float2(a, b);
 }
 
-constexpr int kWeightKeys = 4096;  // positions per block of the weights' part
 
-// Blocks 0 .. row_blocks-1: O.  kWide: the eight warps of a block split the pieces of one row;
-// otherwise each takes a row of its own.  The blocks behind: weights, 4096 positions each.
-template <typename T, bool kWide>
-__global__ void __launch_bounds__(kThreads) decode_q8_join_kernel(const Params p, int row_blocks,
-                                                                  int weight_blocks) {
+// Merges (m2, l2) into (m, l): sums l under the larger maximum (kNone: nothing there; a NaN sum
+// must not be lost).  Returns the two factors.
+__device__ __forceinline__ float2 merge(float& m, float& l, float m2, float l2) {
+  const float top = fmaxf(m, m2);
+  const float2 f = make_float2(m == top ? 1.f : ex2_approx(m - top),
+                               m2 == top ? 1.f : ex2_approx(m2 - top));
+  m = top;
+  l = l * f.x + l2 * f.y;
+  return f;
+}
+
+// Blocks 0 .. row_blocks-1: O.  kWide: the warps of a block split the pieces of one row;
+// otherwise each takes a row of its own.  The blocks behind (kQuads > 0): weights, 1024 kQuads
+// positions each.  What depends on the lengths alone is done before the pieces are waited for.
+// At most 64 registers, for all of a step's blocks to be resident at once: with the 95 that four
+// quads want, grouped heads' 1024 rows took four rounds.
+template <typename T, bool kWide, int kQuads>
+__global__ void __launch_bounds__(kThreads, 4) decode_q8_join_kernel(const Params p, int row_blocks,
+                                                                     int weight_blocks) {
   const DecodeQ8Args& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per = a.Hkv * p.rp.RG, G = a.H / a.Hkv;
   const int group = 8 * p.rp.NR;
   pdl_launch_dependents();
-  pdl_wait();  // the pieces are complete from here on
   if (static_cast<int>(blockIdx.x) < row_blocks) {
     __shared__ float so[kWarps][kD], sm[kWarps], sl[kWarps];
-    const int64_t row = kWide ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * kWarps + warp;
-    const int64_t rows = static_cast<int64_t>(a.B) * a.Hkv * p.rp.R;
+    const int row = kWide ? blockIdx.x : blockIdx.x * kWarps + warp;
+    const int rows = a.B * a.Hkv * p.rp.R;
     if (row >= rows) return;  // a whole warp (kWide: no warp)
-    const int r = static_cast<int>(row % p.rp.R);
-    const int hk = static_cast<int>(row / p.rp.R % a.Hkv);
-    const int b = static_cast<int>(row / p.rp.R / a.Hkv);
+    const int r = row % p.rp.R;
+    const int hk = row / p.rp.R % a.Hkv;
+    const int b = row / p.rp.R / a.Hkv;
     const int hr = hk * p.rp.RG + r / group;
-    int64_t first = 0, last = -1;
-    if (!pieces_of(p, b, hr, &first, &last)) last = first - 1;
-    const int64_t seg = static_cast<int64_t>(b) * per + hr;
-    float m = -INFINITY, l = 0.f;
+    const Pieces pieces(p, b);
+    const int first = pieces.nt > 0 ? pieces.first(hr) : 0;
+    const int last = pieces.nt > 0 ? pieces.last(hr) : -1;
+    const int64_t at0 = (static_cast<int64_t>(b) * per + hr) * p.rp.RS + r % group;
+    pdl_wait();  // the pieces are complete from here on
+    float m = kNone, l = 0.f;
     float2 o = make_float2(0.f, 0.f);
-    for (int64_t w = first + (kWide ? warp : 0); w <= last; w += kWide ? kWarps : 1) {
-      const int64_t at = (w + seg) * p.rp.RS + r % group;
-      const float2 st = *reinterpret_cast<const float2*>(p.stat + at * 2);
-      const float2 v = *reinterpret_cast<const float2*>(p.part + at * kD + 2 * lane);
-      // -inf: no position of the piece is allowed.  (A NaN sum must not be lost here.)
-      const float top = fmaxf(m, st.x);
-      const float f = m == top ? 1.f : ex2_approx(m - top);
-      const float h = st.x == top ? 1.f : ex2_approx(st.x - top);
-      m = top;
-      l = l * f + st.y * h;
-      o.x = o.x * f + v.x * h;
-      o.y = o.y * f + v.y * h;
+    constexpr int kStep = kWide ? kWarps : 1, kBatch = 4;  // pieces asked for at once
+    for (int w = first + (kWide ? warp : 0); w <= last; w += kStep * kBatch) {
+      float2 st[kBatch], v[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        st[k] = make_float2(kNone, 0.f);
+        v[k] = make_float2(0.f, 0.f);
+        if (w + k * kStep <= last) {
+          const int64_t at = static_cast<int64_t>(w + k * kStep) * p.rp.RS + at0;
+          st[k] = *reinterpret_cast<const float2*>(p.stat + at * 2);
+          v[k] = *reinterpret_cast<const float2*>(p.part + at * kD + 2 * lane);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const float2 f = merge(m, l, st[k].x, st[k].y);
+        o.x = o.x * f.x + v[k].x * f.y;
+        o.y = o.y * f.x + v[k].y * f.y;
+      }
     }
     if constexpr (kWide) {
       so[warp][2 * lane] = o.x;
@@ -690,17 +773,14 @@ __global__ void __launch_bounds__(kThreads) decode_q8_join_kernel(const Params p
       }
       __syncthreads();
       if (warp != 0) return;
-      m = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm[w]);
+      m = kNone;
       l = 0.f;
       o = make_float2(0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float h = sm[w] == m ? 1.f : ex2_approx(sm[w] - m);
-        l += sl[w] * h;
-        o.x += so[w][2 * lane] * h;
-        o.y += so[w][2 * lane + 1] * h;
+        const float2 f = merge(m, l, sm[w], sl[w]);
+        o.x = o.x * f.x + so[w][2 * lane] * f.y;
+        o.y = o.y * f.x + so[w][2 * lane + 1] * f.y;
       }
     }
     const float y = l == 0.f ? 0.f : 1.f / l;  // no allowed position: zeros
@@ -709,73 +789,84 @@ __global__ void __launch_bounds__(kThreads) decode_q8_join_kernel(const Params p
          o.x * y, o.y * y);
     return;
   }
-  // ---- weights: m and 1 / l of every row of the cache head, then its positions
-  const int64_t x = static_cast<int64_t>(blockIdx.x) - row_blocks;
-  const int64_t bh = x / weight_blocks;
-  const int hk = static_cast<int>(bh % a.Hkv), b = static_cast<int>(bh / a.Hkv);
-  const int L = cached(a, b);
-  const int j0 = static_cast<int>(x % weight_blocks) * kWeightKeys;
-  if (j0 >= L) return;
-  extern __shared__ float rowstat[];  // [R][2]
-  // the first row's scores and the totals are asked for before the statistics are known
-  constexpr int kQuads = kWeightKeys / 4 / kThreads;
-  const float* sc = p.scores + bh * p.rp.R * p.Lpad;
-  float* out = a.weights + bh * a.Lmax;
-  float4 x0[kQuads];
-  float w[kQuads][4];
+  if constexpr (kQuads > 0) {
+    // ---- weights: m and 1 / l of every row of the cache head, then its positions
+    const int x = static_cast<int>(blockIdx.x) - row_blocks;
+    const int bh = x / weight_blocks;
+    const int hk = bh % a.Hkv, b = bh / a.Hkv;
+    const int L = cached(a, b);
+    const int j0 = x % weight_blocks * (4 * kThreads * kQuads);
+    if (j0 >= L) return;
+    extern __shared__ float rowstat[];  // [R][2]
+    const Pieces pieces(p, b);          // L > 0: there are some
+    pdl_wait();                         // pieces and scores are complete from here on
+    const int R = p.rp.R;
+    const float* sc = p.scores + static_cast<int64_t>(bh) * R * p.Lpad;
+    float* out = a.weights + static_cast<int64_t>(bh) * a.Lmax;
+    // scores of up to four rows and quads at a time; the first are asked for before the
+    // statistics are known
+    constexpr int kRows = 4 / kQuads;
+    float4 xs[kRows][kQuads];
+    auto load = [&](int r) {
 #pragma unroll
-  for (int k = 0; k < kQuads; ++k) {
-    const int j = j0 + (k * kThreads + static_cast<int>(threadIdx.x)) * 4;
-    if (j < L) x0[k] = *reinterpret_cast<const float4*>(sc + j);
+      for (int k = 0; k < kQuads; ++k) {
+        const int j = j0 + (k * kThreads + static_cast<int>(threadIdx.x)) * 4;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[k][i] = j + i < L ? out[j + i] : 0.f;
-  }
-  for (int r = warp; r < p.rp.R; r += kWarps) {
-    int64_t first, last;
-    const int hr = hk * p.rp.RG + r / group;
-    pieces_of(p, b, hr, &first, &last);  // L > 0: there are some
-    const int64_t seg = static_cast<int64_t>(b) * per + hr;
-    float m = -INFINITY, l = 0.f;
-    for (int64_t s = first + lane; s <= last; s += 32) {
-      const float2 st =
-          *reinterpret_cast<const float2*>(p.stat + ((s + seg) * p.rp.RS + r % group) * 2);
-      const float top = fmaxf(m, st.x);
-      l = l * (m == top ? 1.f : ex2_approx(m - top)) +
-          st.y * (st.x == top ? 1.f : ex2_approx(st.x - top));
-      m = top;
+        for (int u = 0; u < kRows; ++u)
+          if (j < L && r + u < R)
+            xs[u][k] = *reinterpret_cast<const float4*>(sc + (r + u) * p.Lpad + j);
+      }
+    };
+    load(0);
+    for (int r = warp; r < R; r += kWarps) {
+      const int hr = hk * p.rp.RG + r / group;
+      const int last = pieces.last(hr);
+      const int64_t at0 = (static_cast<int64_t>(b) * per + hr) * p.rp.RS + r % group;
+      float m = kNone, l = 0.f;
+      for (int w = pieces.first(hr) + lane; w <= last; w += 32) {
+        const float2 st = *reinterpret_cast<const float2*>(
+            p.stat + (static_cast<int64_t>(w) * p.rp.RS + at0) * 2);
+        merge(m, l, st.x, st.y);
+      }
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, m, s);
+        const float l2 = __shfl_xor_sync(0xffffffffu, l, s);
+        merge(m, l, m2, l2);
+      }
+      if (lane == 0) {  // weight = 2^(x + offset - m) / l (the pieces' own reference)
+        rowstat[2 * r] = kOffset - m;
+        rowstat[2 * r + 1] = l == 0.f ? 0.f : 1.f / l;
+      }
+    }
+    __syncthreads();
+    float w[kQuads][4];
+#pragma unroll
+    for (int k = 0; k < kQuads; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[k][i] = 0.f;
+    for (int r = 0; r < R; r += kRows) {
+      if (r > 0) load(r);
+#pragma unroll
+      for (int u = 0; u < kRows; ++u) {
+        if (r + u >= R) break;
+        const float2 st = *reinterpret_cast<const float2*>(rowstat + 2 * (r + u));
+#pragma unroll
+        for (int k = 0; k < kQuads; ++k) {
+          const float v[4] = {xs[u][k].x, xs[u][k].y, xs[u][k].z, xs[u][k].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)  // an excluded position takes nothing of a NaN row
+            if (v[i] != -INFINITY) w[k][i] = fmaf(ex2_approx(v[i] + st.x), st.y, w[k][i]);
+        }
+      }
     }
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) {
-      const float m2 = __shfl_xor_sync(0xffffffffu, m, s);
-      const float l2 = __shfl_xor_sync(0xffffffffu, l, s);
-      const float top = fmaxf(m, m2);
-      l = l * (m == top ? 1.f : ex2_approx(m - top)) + l2 * (m2 == top ? 1.f : ex2_approx(m2 - top));
-      m = top;
-    }
-    if (lane == 0) {  // weight = 2^(x + offset - m) / l (the pieces' own reference)
-      rowstat[2 * r] = m == -INFINITY ? 0.f : kOffset - m;
-      rowstat[2 * r + 1] = l == 0.f ? 0.f : 1.f / l;
-    }
-  }
-  __syncthreads();
+    for (int k = 0; k < kQuads; ++k) {
+      const int j = j0 + (k * kThreads + static_cast<int>(threadIdx.x)) * 4;
 #pragma unroll
-  for (int k = 0; k < kQuads; ++k) {
-    const int j = j0 + (k * kThreads + static_cast<int>(threadIdx.x)) * 4;
-    if (j >= L) break;
-    float4 x = x0[k];
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int r = 0;;) {
-      const float shift = rowstat[2 * r], inv = rowstat[2 * r + 1];
-      const float xs[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i)  // an excluded position takes nothing of a NaN row
-        if (xs[i] != -INFINITY) s[i] = fmaf(ex2_approx(xs[i] + shift), inv, s[i]);
-      if (++r == p.rp.R) break;
-      x = *reinterpret_cast<const float4*>(sc + r * p.Lpad + j);
+      for (int i = 0; i < 4; ++i)
+        if (j + i < L) out[j + i] += w[k][i];
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (j + i < L) out[j + i] = w[k][i] + s[i];
   }
 }
 
@@ -797,40 +888,45 @@ Workspace plan(int B, int H, int Hkv, int Nq, int Lmax, int dtype, bool weights)
 }
 
 template <typename T, int QT, int NR>
-cudaError_t launch_main(const CUtensorMap& tk, const CUtensorMap& tv, const Params& p, int blocks,
-                        cudaStream_t s) {
+cudaError_t launch_main(const Params& p, int blocks, cudaStream_t s) {
   auto kern = decode_q8_kernel<T, QT, NR>;
   const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(kern), kSmemBytes, nullptr);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(blocks), dim3(kThreads), kSmemBytes, s, tk, tv, p);
+  return launch_pdl(kern, dim3(blocks), dim3(kThreads), kSmemBytes, s, p);
 }
 template <typename T>
-cudaError_t launch_all(const CUtensorMap& tk, const CUtensorMap& tv, const Params& p, int qtype,
-                       int blocks, cudaStream_t s) {
+cudaError_t launch_all(const Params& p, int qtype, int blocks, cudaStream_t s) {
   constexpr int kMost = sizeof(T) == 4 ? 2 : 4;  // row_plan's
   cudaError_t e;
   if (p.rp.NR == 1)
-    e = qtype == kE4m3 ? launch_main<T, kE4m3, 1>(tk, tv, p, blocks, s)
-                       : launch_main<T, kInt8, 1>(tk, tv, p, blocks, s);
+    e = qtype == kE4m3 ? launch_main<T, kE4m3, 1>(p, blocks, s)
+                       : launch_main<T, kInt8, 1>(p, blocks, s);
   else if (p.rp.NR == 2)
-    e = qtype == kE4m3 ? launch_main<T, kE4m3, 2>(tk, tv, p, blocks, s)
-                       : launch_main<T, kInt8, 2>(tk, tv, p, blocks, s);
+    e = qtype == kE4m3 ? launch_main<T, kE4m3, 2>(p, blocks, s)
+                       : launch_main<T, kInt8, 2>(p, blocks, s);
   else
-    e = qtype == kE4m3 ? launch_main<T, kE4m3, kMost>(tk, tv, p, blocks, s)
-                       : launch_main<T, kInt8, kMost>(tk, tv, p, blocks, s);
+    e = qtype == kE4m3 ? launch_main<T, kE4m3, kMost>(p, blocks, s)
+                       : launch_main<T, kInt8, kMost>(p, blocks, s);
   if (e != cudaSuccess) return e;
   // a row's pieces where all sequences are alike: workers / segments, and the ends
   const int64_t heads = static_cast<int64_t>(p.a.B) * p.a.Hkv, rows = heads * p.rp.R;
   const bool wide = p.workers / (heads * p.rp.RG) > 8;
   const int row_blocks = static_cast<int>(wide ? rows : (rows + kWarps - 1) / kWarps);
-  const int weight_blocks =
-      p.scores != nullptr ? (p.a.Lmax + kWeightKeys - 1) / kWeightKeys : 0;
+  // four quads of positions to a thread where that still fills the GPU: the blocks' fixed cost
+  // (statistics of the rows) is paid less often
+  const bool quads = p.rp.R <= 2 && heads * ((p.a.Lmax + 4095) / 4096) >= 2 * 152;
+  const int chunk = 4 * kThreads * (quads ? 4 : 1);
+  const int weight_blocks = p.scores != nullptr ? (p.a.Lmax + chunk - 1) / chunk : 0;
   const dim3 grid(static_cast<unsigned>(row_blocks + heads * weight_blocks));
   const size_t smem = p.scores != nullptr ? p.rp.R * 2 * sizeof(float) : 0;
-  return wide ? launch_pdl(decode_q8_join_kernel<T, true>, grid, dim3(kThreads), smem, s, p,
-                           row_blocks, weight_blocks)
-              : launch_pdl(decode_q8_join_kernel<T, false>, grid, dim3(kThreads), smem, s, p,
-                           row_blocks, weight_blocks);
+  void (*kern)(Params, int, int);
+  if (p.scores == nullptr)
+    kern = wide ? decode_q8_join_kernel<T, true, 0> : decode_q8_join_kernel<T, false, 0>;
+  else if (quads)
+    kern = wide ? decode_q8_join_kernel<T, true, 4> : decode_q8_join_kernel<T, false, 4>;
+  else
+    kern = wide ? decode_q8_join_kernel<T, true, 1> : decode_q8_join_kernel<T, false, 1>;
+  return launch_pdl(kern, grid, dim3(kThreads), smem, s, p, row_blocks, weight_blocks);
 }
 
 }  // namespace
@@ -842,10 +938,6 @@ size_t decode_q8_workspace(int B, int H, int Hkv, int Nq, int Lmax, bool weights
 
 cudaError_t launch_sdpa_decode_q8(const DecodeQ8Args& a, int dtype, int qtype, void* ws,
                                   const DevCtx& ctx, cudaStream_t s) {
-  CUtensorMap tk, tv;
-  if (!encode_map_u8(&tk, a.Kc, a.B, a.Hkv, a.Lmax, a.sk, kTile) ||
-      !encode_map_u8(&tv, a.Vc, a.B, a.Hkv, a.Lmax, a.sv, kTile))
-    return cudaErrorInvalidValue;
   const Workspace w = plan(a.B, a.H, a.Hkv, a.Nq, a.Lmax, dtype, a.weights != nullptr);
   Params p;
   p.a = a;
@@ -854,15 +946,15 @@ cudaError_t launch_sdpa_decode_q8(const DecodeQ8Args& a, int dtype, int qtype, v
   const int blocks = std::min(ctx.num_sms * blocks_per_sm(terms, p.rp.NR),
                               max_workers(terms, p.rp.NR) / kWarps);
   p.workers = blocks * kWarps;
+  p.block_shift = 0;
+  while ((1 << p.block_shift) < a.block) ++p.block_shift;
   p.part = static_cast<float*>(ws);
   p.stat = reinterpret_cast<float*>(static_cast<char*>(ws) + w.stat);
   p.scores = a.weights != nullptr
                  ? reinterpret_cast<float*>(static_cast<char*>(ws) + w.scores) : nullptr;
   p.Lpad = w.Lpad;
-  p.status = ctx.status;
-  p.timeout_ns = ctx.timeout_ns;
-  return dtype == 1 ? launch_all<__nv_bfloat16>(tk, tv, p, qtype, blocks, s)
-                    : launch_all<float>(tk, tv, p, qtype, blocks, s);
+  return dtype == 1 ? launch_all<__nv_bfloat16>(p, qtype, blocks, s)
+                    : launch_all<float>(p, qtype, blocks, s);
 }
 
 }  // namespace mha
