@@ -50,9 +50,9 @@ constexpr int kD = 64;
 constexpr int kTile = 32;                  // positions per tile
 constexpr int kTileBytes = kTile * kD;     // 2 KB of K, 2 KB of V
 constexpr int kStages = 3;
-constexpr int kWarps = 8;
+constexpr int kSlotBytes = 2 * kTileBytes;
+constexpr int kWarps = 8;                  // of the join
 constexpr int kThreads = kWarps * 32;
-constexpr int kSmemBytes = kWarps * kStages * 2 * kTileBytes;
 constexpr float kOffset = 13.f;            // weights that meet the codes: 2^13 at most
 constexpr float kNone = -3.402823466e38f;  // maximum of no position (finite: -inf - it is -inf)
 
@@ -70,10 +70,13 @@ RowPlan row_plan(int H, int Hkv, int Nq, int dtype) {
   p.RS = std::min(p.R, 8 * p.NR);
   return p;
 }
-// blocks of the first launch that share an SM: two at up to 128 registers a thread
-constexpr int blocks_per_sm(int terms, int nr) { return terms * nr <= 2 ? 2 : 1; }
-// warps of its grid at most, as far as the workspace goes (a GB300 has 152 SMs)
-constexpr int max_workers(int terms, int nr) { return 160 * kWarps * blocks_per_sm(terms, nr); }
+// Warps of the first launch's one block per SM, by the registers that its operands take.  Twelve
+// where 168 registers a thread do: sixteen at 128 spilled (16 rows, 8 x 8 x 65536 positions 95.9
+// -> 99.5 us) or kept more requests in flight than HBM takes well (64 x 16 heads x 4096 positions,
+// three slots each, 87.4 -> 91.9 us), eight left the tensor cores waiting (95.9 -> 102.4 us).
+constexpr int main_warps(int terms, int nr) { return terms * nr <= 2 ? 12 : 8; }
+// workers at most, as far as the workspace goes (a GB300 has 152 SMs)
+constexpr int max_workers(int terms, int nr) { return 160 * main_warps(terms, nr); }
 
 struct Params {
   DecodeQ8Args a;
@@ -167,9 +170,18 @@ __device__ __forceinline__ void mma16816_zero(float (&d)[4], const uint32_t (&a)
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// 16 bytes from global to shared memory, past L1; a lane's copies complete in groups
-__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src)
+// 16 bytes from global to shared memory, past L1; a lane's copies complete in groups.  `policy`:
+// the cache streams through L2 and is the first to leave it, so that the scores and pieces that
+// the join reads stay there (64 x 16 heads x 4096 positions 87.3 -> 84.8 us, with weights 106.8
+// -> 102.5).
+__device__ __forceinline__ uint64_t evict_first_policy() {
+  uint64_t policy;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+  return policy;
+}
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint.L2::256B [%0], [%1], 16, %2;" ::"r"(dst),
+               "l"(src), "l"(policy)
                : "memory");
 }
 __device__ __forceinline__ void copy_async_commit() {
@@ -269,14 +281,14 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
 
 // T: float (two fp16 terms per operand) or bf16 (one).  NR: column tiles of 8 query rows
 template <typename T, int QT, int NR>
-__global__ void __launch_bounds__(kThreads, blocks_per_sm(sizeof(T) / 2, NR))
+__global__ void __launch_bounds__(main_warps(sizeof(T) / 2, NR) * 32, 1)
     decode_q8_kernel(const Params p) {
   constexpr int kTerms = sizeof(T) == 4 ? 2 : 1;
   const DecodeQ8Args& a = p.a;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  uint8_t* ring = smem + warp * (kStages * 2 * kTileBytes);
+  uint8_t* ring = smem + warp * (kStages * kSlotBytes);
   pdl_wait();  // the previous kernel's output is complete from here on
   pdl_launch_dependents();  // after the wait: the join reads cache_len before its own
 
@@ -314,24 +326,25 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(sizeof(T) / 2, NR))
   };
   place();
   int asked = 0;
+  const uint64_t policy = evict_first_policy();
   const int64_t k_step = 8 * a.sk[2], v_step = 8 * a.sv[2];
   const int k_at = (t ^ ((g >> 1) & 3)) << 4;  // chunk t of a row 8i + g
   const uint32_t dst0 = smem_u32(ring) + g * kD + k_at;
   auto ask = [&](int slot) {
     if (asked < count) {
-      const uint32_t dst = dst0 + slot * 2 * kTileBytes;
+      const uint32_t dst = dst0 + slot * kSlotBytes;
       if ((ahead.kt + 1) * kTile <= a.Lmax) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          copy16_async(dst + i * 8 * kD, k_next + i * k_step);
-          copy16_async(dst + kTileBytes + i * 8 * kD, v_next + i * v_step);
+          copy16_async(dst + i * 8 * kD, k_next + i * k_step, policy);
+          copy16_async(dst + kTileBytes + i * 8 * kD, v_next + i * v_step, policy);
         }
       } else {  // rows behind the cache: the slot keeps what it held, unused
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (ahead.kt * kTile + i * 8 + g < a.Lmax) {
-            copy16_async(dst + i * 8 * kD, k_next + i * k_step);
-            copy16_async(dst + kTileBytes + i * 8 * kD, v_next + i * v_step);
+            copy16_async(dst + i * 8 * kD, k_next + i * k_step, policy);
+            copy16_async(dst + kTileBytes + i * 8 * kD, v_next + i * v_step, policy);
           }
       }
       ++asked;
@@ -458,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(sizeof(T) / 2, NR))
       const float sc_log = log2_approx(sc), sc_inv = rcp_approx(sc);
       copy_async_wait<kStages - 1>();  // this lane's copies of the tile have landed
       __syncwarp();                    // and every lane's
-      const uint8_t* sK = ring + slot * 2 * kTileBytes;
+      const uint8_t* sK = ring + slot * kSlotBytes;
       const uint8_t* sV = sK + kTileBytes;
       const int pos = c.kt * kTile;
       // kEdge: some row may not see the whole tile (or `huge`).  Its code apart: in one body it
@@ -744,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 4) decode_q8_join_kernel(const Param
     pdl_wait();  // the pieces are complete from here on
     float m = kNone, l = 0.f;
     float2 o = make_float2(0.f, 0.f);
-    constexpr int kStep = kWide ? kWarps : 1, kBatch = 4;  // pieces asked for at once
+    constexpr int kStep = kWide ? kWarps : 1, kBatch = kWide ? 8 : 4;  // pieces asked for at once
     for (int w = first + (kWide ? warp : 0); w <= last; w += kStep * kBatch) {
       float2 st[kBatch], v[kBatch];
 #pragma unroll
@@ -818,23 +831,24 @@ __global__ void __launch_bounds__(kThreads, 4) decode_q8_join_kernel(const Param
       }
     };
     load(0);
-    for (int r = warp; r < R; r += kWarps) {
+    for (int r0 = 2 * warp; r0 < R; r0 += 2 * kWarps) {  // a row to each half of the warp
+      const int r = min(r0 + (lane >> 4), R - 1);
       const int hr = hk * p.rp.RG + r / group;
       const int last = pieces.last(hr);
       const int64_t at0 = (static_cast<int64_t>(b) * per + hr) * p.rp.RS + r % group;
       float m = kNone, l = 0.f;
-      for (int w = pieces.first(hr) + lane; w <= last; w += 32) {
+      for (int w = pieces.first(hr) + (lane & 15); w <= last; w += 16) {
         const float2 st = *reinterpret_cast<const float2*>(
             p.stat + (static_cast<int64_t>(w) * p.rp.RS + at0) * 2);
         merge(m, l, st.x, st.y);
       }
 #pragma unroll
-      for (int s = 16; s > 0; s >>= 1) {
+      for (int s = 8; s > 0; s >>= 1) {
         const float m2 = __shfl_xor_sync(0xffffffffu, m, s);
         const float l2 = __shfl_xor_sync(0xffffffffu, l, s);
         merge(m, l, m2, l2);
       }
-      if (lane == 0) {  // weight = 2^(x + offset - m) / l (the pieces' own reference)
+      if ((lane & 15) == 0) {  // weight = 2^(x + offset - m) / l (the pieces' own reference)
         rowstat[2 * r] = kOffset - m;
         rowstat[2 * r + 1] = l == 0.f ? 0.f : 1.f / l;
       }
@@ -890,9 +904,11 @@ Workspace plan(int B, int H, int Hkv, int Nq, int Lmax, int dtype, bool weights)
 template <typename T, int QT, int NR>
 cudaError_t launch_main(const Params& p, int blocks, cudaStream_t s) {
   auto kern = decode_q8_kernel<T, QT, NR>;
-  const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(kern), kSmemBytes, nullptr);
+  constexpr int kMainWarps = main_warps(sizeof(T) / 2, NR);
+  constexpr int kSmem = kMainWarps * kStages * kSlotBytes;
+  const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(kern), kSmem, nullptr);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(blocks), dim3(kThreads), kSmemBytes, s, p);
+  return launch_pdl(kern, dim3(blocks), dim3(kMainWarps * 32), kSmem, s, p);
 }
 template <typename T>
 cudaError_t launch_all(const Params& p, int qtype, int blocks, cudaStream_t s) {
@@ -912,21 +928,24 @@ cudaError_t launch_all(const Params& p, int qtype, int blocks, cudaStream_t s) {
   const int64_t heads = static_cast<int64_t>(p.a.B) * p.a.Hkv, rows = heads * p.rp.R;
   const bool wide = p.workers / (heads * p.rp.RG) > 8;
   const int row_blocks = static_cast<int>(wide ? rows : (rows + kWarps - 1) / kWarps);
-  // four quads of positions to a thread where that still fills the GPU: the blocks' fixed cost
-  // (statistics of the rows) is paid less often
-  const bool quads = p.rp.R <= 2 && heads * ((p.a.Lmax + 4095) / 4096) >= 2 * 152;
-  const int chunk = 4 * kThreads * (quads ? 4 : 1);
+  // more positions to a thread where that still fills the GPU: the blocks' fixed cost (statistics
+  // of the rows) is paid less often (one row, 64 x 16 heads x 4096 positions: four quads 102 us,
+  // one 113 us)
+  auto fills = [&](int n) { return heads * ((p.a.Lmax + 1024 * n - 1) / (1024 * n)) >= 2 * 152; };
+  const int quads = p.rp.R <= 2 && fills(4) ? 4 : fills(2) ? 2 : 1;
+  const int chunk = 4 * kThreads * quads;
   const int weight_blocks = p.scores != nullptr ? (p.a.Lmax + chunk - 1) / chunk : 0;
   const dim3 grid(static_cast<unsigned>(row_blocks + heads * weight_blocks));
   const size_t smem = p.scores != nullptr ? p.rp.R * 2 * sizeof(float) : 0;
-  void (*kern)(Params, int, int);
-  if (p.scores == nullptr)
-    kern = wide ? decode_q8_join_kernel<T, true, 0> : decode_q8_join_kernel<T, false, 0>;
-  else if (quads)
-    kern = wide ? decode_q8_join_kernel<T, true, 4> : decode_q8_join_kernel<T, false, 4>;
-  else
-    kern = wide ? decode_q8_join_kernel<T, true, 1> : decode_q8_join_kernel<T, false, 1>;
-  return launch_pdl(kern, grid, dim3(kThreads), smem, s, p, row_blocks, weight_blocks);
+  auto pick = [&](auto w) -> void (*)(Params, int, int) {
+    constexpr bool kWide = decltype(w)::value;
+    if (p.scores == nullptr) return decode_q8_join_kernel<T, kWide, 0>;
+    return quads == 4   ? decode_q8_join_kernel<T, kWide, 4>
+           : quads == 2 ? decode_q8_join_kernel<T, kWide, 2>
+                        : decode_q8_join_kernel<T, kWide, 1>;
+  };
+  return launch_pdl(wide ? pick(std::true_type{}) : pick(std::false_type{}), grid, dim3(kThreads),
+                    smem, s, p, row_blocks, weight_blocks);
 }
 
 }  // namespace
@@ -942,10 +961,8 @@ cudaError_t launch_sdpa_decode_q8(const DecodeQ8Args& a, int dtype, int qtype, v
   Params p;
   p.a = a;
   p.rp = row_plan(a.H, a.Hkv, a.Nq, dtype);
-  const int terms = dtype == 1 ? 1 : 2;
-  const int blocks = std::min(ctx.num_sms * blocks_per_sm(terms, p.rp.NR),
-                              max_workers(terms, p.rp.NR) / kWarps);
-  p.workers = blocks * kWarps;
+  const int blocks = std::min(ctx.num_sms, 160);
+  p.workers = blocks * main_warps(dtype == 1 ? 1 : 2, p.rp.NR);
   p.block_shift = 0;
   while ((1 << p.block_shift) < a.block) ++p.block_shift;
   p.part = static_cast<float*>(ws);
