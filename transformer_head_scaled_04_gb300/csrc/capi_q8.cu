@@ -144,6 +144,11 @@ int mha_key_weights_workspace_size(int B, int H, int Hkv, int Nq, int Nk, int dt
   if (bytes == nullptr || B < 1 || H < 1 || Hkv < 1 || Nq < 1 || Nk < 1 || H % Hkv != 0 ||
       !valid_dtype(dtype))
     return MHA_ERR_INVALID;
+  // blocks of the launch's grids
+  const int64_t heads = static_cast<int64_t>(B) * Hkv;
+  if (heads > 65535 || heads * ((Nk + 127) / 128) > (1 << 30) || Nq > (1 << 30) ||
+      static_cast<int64_t>(H / Hkv) * ((Nq + 127) / 128) > (1 << 30))
+    return MHA_ERR_UNSUPPORTED;
   *bytes = round_up(mha::key_weights_workspace(B, H, Hkv, Nq, Nk, dtype), 256);
   return MHA_OK;
 }
@@ -185,7 +190,7 @@ int mha_sdpa_key_weights(int B, int H, int Hkv, int Nq, int Nk, int d_k, int dty
   a.query_len = query_len;
   a.scale = scale_of(scale);
   a.Q = Q; a.K = K; a.lse = lse; a.weights = weights; a.ld = weights_ld;
-  return done(mha::launch_key_weights_simt(a, dtype, stream));
+  return done(mha::launch_key_weights(a, dtype, workspace, ctx, stream));
 }
 
 int mha_kv_evict_q8(int B, int H, int Lmax, int Lmax_out, int d_k, int d_v, int qtype, int block,

@@ -198,7 +198,8 @@ struct KeyWeightsArgs {
   int64_t sq[4], sk[4];
 };
 size_t key_weights_workspace(int B, int H, int Hkv, int Nq, int Nk, int dtype);
-cudaError_t launch_key_weights_simt(const KeyWeightsArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_key_weights(const KeyWeightsArgs& a, int dtype, void* ws, const DevCtx& ctx,
+                               cudaStream_t s);
 
 struct KvEvictArgs {
   int B, H, Lmax, Lmax_out, block, n_blocks, n_blocks_out, keep, recent;

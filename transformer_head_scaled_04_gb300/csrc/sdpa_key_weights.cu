@@ -4,9 +4,19 @@
 // the column sums of the attention matrix, which is never stored.  A key belongs to one CTA, so
 // the sums have one order and need no atomics.
 //
-// key_weights_simt_kernel: 32 keys per CTA, each warp taking every eighth query of the group's
-// heads; lane = key, its row in registers, the queries broadcast from shared memory.
+// bf16 (key_weights_bf16_kernel): bound by the exponentials, one per (query, key) pair; the
+// product itself is a quarter of the attention forward's tensor work.  One CTA per 128 keys:
+// S^T = K Q^T (tcgen05.mma 128x128x16 into one of two TMEM buffers) for every 128-query tile of
+// the group's heads that sees the keys, so a key's row lies in one thread and its sum needs no
+// other: x = s * scale log2 e - lse log2 e, sum += 2^x, in paired fp32 operations.  Two CTAs share
+// an SM (192 threads, 65 KB, 256 TMEM columns each).  Where the key tiles alone leave SMs idle the
+// query tiles are split over several CTAs, their sums added by a second launch in a fixed order.
+//
+// fp32 (key_weights_simt_kernel): 32 keys per CTA, each warp taking every eighth query of the
+// group's heads; lane = key, its row in registers, the queries broadcast from shared memory.
 #include <cuda_bf16.h>
+
+#include <algorithm>
 
 #include "launchers.h"
 #include "device_common.cuh"
@@ -15,14 +25,11 @@ namespace mha {
 namespace {
 
 constexpr int kD = 64;
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kKeys = 32;     // keys per CTA
 constexpr int kQueries = 32;  // queries staged at a time
 constexpr int kWarps = 8;
 
-__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_f32(float x) { return x; }
-
-template <typename T>
 __global__ void __launch_bounds__(kWarps * 32) key_weights_simt_kernel(const KeyWeightsArgs a) {
   pdl_launch_dependents();
   pdl_wait();  // the previous kernel's output is complete from here on
@@ -36,24 +43,24 @@ __global__ void __launch_bounds__(kWarps * 32) key_weights_simt_kernel(const Key
   __shared__ float slse[kQueries];
   __shared__ float part[kWarps][kKeys];
   float k[kD];
-  const T* kr = static_cast<const T*>(a.K) + b * a.sk[0] + g * a.sk[1] + min(j, nk - 1) * a.sk[2];
+  const float* kr = static_cast<const float*>(a.K) + b * a.sk[0] + g * a.sk[1] + min(j, nk - 1) * a.sk[2];
 #pragma unroll
-  for (int d = 0; d < kD; ++d) k[d] = to_f32(kr[d]);
+  for (int d = 0; d < kD; ++d) k[d] = kr[d];
   const int G = a.H / a.Hkv;
-  const float c = a.scale * 1.4426950408889634f;
+  const float c = a.scale * kLog2e;
   const int first = a.mask == 1 ? k0 : 0;  // queries before the first key see none of these
   float sum = 0.f;
   for (int h = g * G; h < (g + 1) * G; ++h) {
-    const T* q = static_cast<const T*>(a.Q) + b * a.sq[0] + h * a.sq[1];
+    const float* q = static_cast<const float*>(a.Q) + b * a.sq[0] + h * a.sq[1];
     const float* lse = a.lse + (static_cast<int64_t>(b) * a.H + h) * a.Nq;
     for (int i0 = first; i0 < nq; i0 += kQueries) {
       __syncthreads();
       for (int t = tid; t < kQueries * kD; t += kWarps * 32) {
         const int i = i0 + t / kD;
-        reinterpret_cast<float*>(sq)[t] = i < nq ? to_f32(q[i * a.sq[2] + t % kD]) : 0.f;
+        reinterpret_cast<float*>(sq)[t] = i < nq ? q[i * a.sq[2] + t % kD] : 0.f;
       }
       if (tid < kQueries)  // +inf (a row without keys, or none at all): every weight 0
-        slse[tid] = i0 + tid < nq ? lse[i0 + tid] * 1.4426950408889634f : INFINITY;
+        slse[tid] = i0 + tid < nq ? lse[i0 + tid] * kLog2e : INFINITY;
       __syncthreads();
       for (int t = warp; t < kQueries && i0 + t < nq; t += kWarps) {
         float s = 0.f;
@@ -80,18 +87,296 @@ __global__ void __launch_bounds__(kWarps * 32) key_weights_simt_kernel(const Key
   }
 }
 
+// ============================================================================ bf16
+constexpr int kT = 128;                   // keys and queries per tile
+constexpr int kTileBytes = kT * kD * 2;   // 16 KB
+constexpr int kStages = 3;                // query tiles in flight
+constexpr int kTcThreads = 192;           // warps 0-3 sums, 4 TMA, 5 MMA and TMEM
+constexpr uint32_t kTmemCols = 256;       // two S^T buffers
+constexpr int kErrTimeout = -6;
+enum : int { kSiteKwProducer = 34, kSiteKwMma = 35, kSiteKwMath = 36 };
+constexpr int kOffQ = kTileBytes;
+constexpr int kOffLse = kOffQ + kStages * kTileBytes;  // [2][128] -lse log2 e
+constexpr int kOffBar = kOffLse + 2 * kT * 4;
+constexpr int kBarK = 0, kBarQ = 1, kBarQFree = kBarQ + kStages, kBarS = kBarQFree + kStages,
+              kBarSFree = kBarS + 2, kBarDrain = kBarSFree + 2, kNumBars = kBarDrain + 1;
+constexpr int kTcSmem = 1024 + kOffBar + kNumBars * 8 + 16;
+
+struct TcParams {
+  KeyWeightsArgs a;
+  int split;      // CTAs that share a key tile's query tiles
+  float* part;    // [split][B * Hkv][Nk] (split > 1)
+  int* status;
+  uint64_t timeout_ns;
+};
+
+__device__ __forceinline__ bool warp_all(bool v) { return __all_sync(0xffffffffu, v); }
+
+// 32 queries of one key: adds 2^(s c - lse2) for the columns first <= c0 + i < last (kMask: only
+// those; the others' scores may be anything)
+template <bool kMask>
+__device__ __forceinline__ void add_chunk(const uint32_t (&s)[32], const float* nl, float2 c2,
+                                          int c0, int first, int last, float2 (&acc)[2]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float4 n = *reinterpret_cast<const float4*>(nl + c0 + 4 * i);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k = 4 * i + 2 * h;
+      float2 x = ffma2(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), c2,
+                       h ? make_float2(n.z, n.w) : make_float2(n.x, n.y));
+      x.x = ex2_approx(x.x);
+      x.y = ex2_approx(x.y);
+      if (kMask) {
+        if (c0 + k < first || c0 + k >= last) x.x = 0.f;
+        if (c0 + k + 1 < first || c0 + k + 1 >= last) x.y = 0.f;
+      }
+      acc[h] = fadd2(acc[h], x);
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kTcThreads, 2)
+    key_weights_bf16_kernel(const __grid_constant__ CUtensorMap tmQ,
+                            const __grid_constant__ CUtensorMap tmK, const TcParams p) {
+  const KeyWeightsArgs& a = p.a;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align_smem_1024(smem_raw);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kNumBars);
+  auto bar = [&](int i) { return smem_u32(bars + i); };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // key tile, cache head, batch element and share of the query tiles.  Causal: the tiles with the
+  // most queries first over all heads; otherwise a head's tiles next to one another (its queries
+  // stay in L2)
+  const int tiles = (a.Nk + kT - 1) / kT, heads = a.B * a.Hkv;
+  int unit = static_cast<int>(blockIdx.x);
+  const int z = unit % p.split;
+  unit /= p.split;
+  const int kt = a.mask == 1 ? unit / heads : unit % tiles;
+  const int bg = a.mask == 1 ? unit % heads : unit / tiles;
+  const int g = bg % a.Hkv, b = bg / a.Hkv;
+  const int k0 = kt * kT;
+
+  pdl_wait();  // the previous kernel's output is complete from here on
+  pdl_launch_dependents();
+  const int nk = a.mask == 2 ? min(max(__ldg(a.key_len + b), 0), a.Nk) : a.Nk;
+  const int nq = a.query_len != nullptr ? min(max(__ldg(a.query_len + b), 0), a.Nq) : a.Nq;
+  if (k0 >= nk) return;
+  // (head, query tile) pairs: tiles first_q .. of each head of the group
+  const int G = a.H / a.Hkv;
+  const int first_q = a.mask == 1 ? kt : 0;
+  const int per_head = max((nq + kT - 1) / kT - first_q, 0);
+  const int64_t all = static_cast<int64_t>(G) * per_head;
+  const int u0 = static_cast<int>(all * z / p.split);
+  const int n = static_cast<int>(all * (z + 1) / p.split) - u0;
+  float* out = p.split == 1 ? a.weights + static_cast<int64_t>(bg) * a.ld
+                            : p.part + (static_cast<int64_t>(z) * heads + bg) * a.Nk;
+  if (n == 0) {
+    if (p.split > 1)
+      for (int j = k0 + static_cast<int>(threadIdx.x); j < min(k0 + kT, nk); j += kTcThreads)
+        out[j] = 0.f;
+    return;
+  }
+
+  if (threadIdx.x == 0) {
+    mbar_init(bar(kBarK), 1);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(bar(kBarQ + i), 1);
+      mbar_init(bar(kBarQFree + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(kBarS + i), 1);
+      mbar_init(bar(kBarSFree + i), 4);  // one arrival per summing warp
+    }
+    mbar_init(bar(kBarDrain), 1);
+    fence_mbar_init();
+  }
+  if (warp == 5) {
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 4) {
+    // ------------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      prefetch_tmap(&tmQ);
+      prefetch_tmap(&tmK);
+      mbar_arrive_expect_tx(bar(kBarK), kTileBytes);
+      tma_load_4d(smem_u32(smem), &tmK, bar(kBarK), 0, k0, g, b);
+      bool ok = true;
+      int asked = 0;
+      for (int j = 0; j < n; ++j) {
+        const int s = j % kStages;
+        if (!mbar_wait_backoff(bar(kBarQFree + s), ((j / kStages) & 1) ^ 1, p.timeout_ns)) {
+          ok = false;
+          break;
+        }
+        const int u = u0 + j;
+        mbar_arrive_expect_tx(bar(kBarQ + s), kTileBytes);
+        tma_load_4d(smem_u32(smem + kOffQ + s * kTileBytes), &tmQ, bar(kBarQ + s), 0,
+                    (first_q + u % per_head) * kT, g * G + u / per_head, b);
+        asked = j + 1;
+      }
+      if (!ok) record_error(p.status, kErrTimeout, kSiteKwProducer);
+      // every copy started here lands before the CTA can exit
+      (void)mbar_wait(bar(kBarK), 0, p.timeout_ns);
+      for (int j = max(asked - kStages, 0); j < asked; ++j)
+        (void)mbar_wait(bar(kBarQ + j % kStages), (j / kStages) & 1, p.timeout_ns);
+    }
+  } else if (warp == 5) {
+    // ------------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t idS = idesc_bf16_f32(kT, kT, false, false);
+      const uint64_t dK = smem_desc_sw128(smem_u32(smem), 1024, 1024);
+      const uint64_t dQ = smem_desc_sw128(smem_u32(smem + kOffQ), 1024, 1024);
+      bool ok = mbar_wait(bar(kBarK), 0, p.timeout_ns);
+      for (int j = 0; ok && j < n; ++j) {
+        const int s = j % kStages, buf = j & 1;
+        if (!mbar_wait(bar(kBarQ + s), (j / kStages) & 1, p.timeout_ns) ||
+            (j > 1 && !mbar_wait(bar(kBarSFree + buf), ((j >> 1) - 1) & 1, p.timeout_ns))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint64_t bq = dQ + static_cast<uint64_t>((s * kTileBytes) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < kD / 16; ++kk)
+          mma_bf16_ss(tmem + buf * kT, dK + kk * 2, bq + kk * 2, idS, kk > 0 ? 1u : 0u);
+        mma_commit(bar(kBarQFree + s));
+        mma_commit(bar(kBarS + buf));
+      }
+      if (!ok) record_error(p.status, kErrTimeout, kSiteKwMma);
+      mma_commit(bar(kBarDrain));
+      (void)mbar_wait(bar(kBarDrain), 0, p.timeout_ns);  // no MMA in flight past this point
+    }
+  } else {
+    // ------------------------------------------------------------------ sums
+    const int tid = static_cast<int>(threadIdx.x);  // 0..127: this thread's key and TMEM lane
+    const int key = k0 + tid;
+    float* lse_s = reinterpret_cast<float*>(smem + kOffLse);
+    const float2 c2 = make_float2(a.scale * kLog2e, a.scale * kLog2e);
+    const uint32_t t_s = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    const float* lse = a.lse + (static_cast<int64_t>(b) * a.H + g * G) * a.Nq;
+    // this thread's entry of tile j's -lse log2 e; rows that do not count: 2^-inf = 0
+    auto load_lse = [&](int j) -> float {
+      const int u = u0 + j, i = (first_q + u % per_head) * kT + tid;
+      return i < nq ? -__ldg(lse + static_cast<int64_t>(u / per_head) * a.Nq + i) * kLog2e
+                    : -INFINITY;
+    };
+    lse_s[tid] = load_lse(0);
+    named_bar_sync(1, 128);
+    float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      const float next = j + 1 < n ? load_lse(j + 1) : 0.f;
+      const int buf = j & 1, q0 = (first_q + (u0 + j) % per_head) * kT;
+      if (ok && !warp_all(mbar_wait(bar(kBarS + buf), (j >> 1) & 1, p.timeout_ns))) {
+        if (lane == 0) record_error(p.status, kErrTimeout, kSiteKwMath);
+        ok = false;
+      }
+      tc_fence_after();
+      // columns that count for this key: from the diagonal on, before the last query
+      const int first = a.mask == 1 ? key - q0 : 0, last = nq - q0;
+      const bool mask = last < kT || (a.mask == 1 && k0 + kT - 1 > q0);
+      const float* nl = lse_s + buf * kT;
+      if (ok) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t r0[32], r1[32];
+          tmem_ld32(t_s + buf * kT + half * 64, r0);
+          tmem_ld32(t_s + buf * kT + half * 64 + 32, r1);
+          tmem_wait_ld();
+          reg_fence(r0);
+          reg_fence(r1);
+          if (half == 1) {  // the buffer may be overwritten
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarSFree + buf));
+          }
+          if (mask) {
+            add_chunk<true>(r0, nl, c2, half * 64, first, last, acc);
+            add_chunk<true>(r1, nl, c2, half * 64 + 32, first, last, acc);
+          } else {
+            add_chunk<false>(r0, nl, c2, half * 64, first, last, acc);
+            add_chunk<false>(r1, nl, c2, half * 64 + 32, first, last, acc);
+          }
+        }
+      }
+      lse_s[(buf ^ 1) * kT + tid] = next;
+      named_bar_sync(1, 128);  // entries written; all have read this tile's
+    }
+    if (key < nk && ok) {
+      const float2 s = fadd2(acc[0], acc[1]);
+      out[key] = (p.split == 1 ? out[key] : 0.f) + (s.x + s.y);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// weights += the shares' sums, in order
+__global__ void __launch_bounds__(256) key_weights_add_kernel(const TcParams p) {
+  const KeyWeightsArgs& a = p.a;
+  pdl_launch_dependents();
+  pdl_wait();  // the shares are complete from here on
+  const int bg = blockIdx.y, j = blockIdx.x * 256 + threadIdx.x;
+  const int nk = a.mask == 2 ? min(max(__ldg(a.key_len + bg / a.Hkv), 0), a.Nk) : a.Nk;
+  if (j >= nk) return;
+  float s = 0.f;
+  for (int z = 0; z < p.split; ++z)
+    s += p.part[(static_cast<int64_t>(z) * gridDim.y + bg) * a.Nk + j];
+  a.weights[static_cast<int64_t>(bg) * a.ld + j] += s;
+}
+
+// CTAs per key tile: enough for two on each of 152 SMs, no more than there are query tiles
+int key_weights_split(int B, int H, int Hkv, int Nq, int Nk) {
+  const int64_t units = static_cast<int64_t>(B) * Hkv * ((Nk + kT - 1) / kT);
+  const int64_t queries = static_cast<int64_t>(H / Hkv) * ((Nq + kT - 1) / kT);
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(queries, 304 / units)));
+}
+
 }  // namespace
 
 size_t key_weights_workspace(int B, int H, int Hkv, int Nq, int Nk, int dtype) {
-  (void)B, (void)H, (void)Hkv, (void)Nq, (void)Nk, (void)dtype;
-  return 0;
+  if (dtype != 1) return 0;
+  const int split = key_weights_split(B, H, Hkv, Nq, Nk);
+  return split == 1 ? 0 : static_cast<size_t>(split) * B * Hkv * Nk * sizeof(float);
 }
 
-cudaError_t launch_key_weights_simt(const KeyWeightsArgs& a, int dtype, cudaStream_t s) {
-  const dim3 grid((a.Nk + kKeys - 1) / kKeys, a.Hkv, a.B);
-  return dtype == 1
-             ? launch_pdl(key_weights_simt_kernel<__nv_bfloat16>, grid, dim3(kWarps * 32), 0, s, a)
-             : launch_pdl(key_weights_simt_kernel<float>, grid, dim3(kWarps * 32), 0, s, a);
+cudaError_t launch_key_weights(const KeyWeightsArgs& a, int dtype, void* ws, const DevCtx& ctx,
+                               cudaStream_t s) {
+  if (dtype != 1)
+    return launch_pdl(key_weights_simt_kernel, dim3((a.Nk + kKeys - 1) / kKeys, a.Hkv, a.B),
+                      dim3(kWarps * 32), 0, s, a);
+  CUtensorMap tq, tk;
+  if (!encode_map_bf16(&tq, a.Q, a.B, a.H, a.Nq, a.sq, kT) ||
+      !encode_map_bf16(&tk, a.K, a.B, a.Hkv, a.Nk, a.sk, kT))
+    return cudaErrorInvalidValue;
+  cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(key_weights_bf16_kernel), kTcSmem,
+                                 nullptr);
+  if (e != cudaSuccess) return e;
+  TcParams p;
+  p.a = a;
+  p.split = key_weights_split(a.B, a.H, a.Hkv, a.Nq, a.Nk);
+  p.part = static_cast<float*>(ws);
+  p.status = ctx.status;
+  p.timeout_ns = ctx.timeout_ns;
+  const int units = a.B * a.Hkv * ((a.Nk + kT - 1) / kT);
+  e = launch_pdl(key_weights_bf16_kernel, dim3(units * p.split), dim3(kTcThreads), kTcSmem, s, tq,
+                 tk, p);
+  if (e != cudaSuccess || p.split == 1) return e;
+  return launch_pdl(key_weights_add_kernel, dim3((a.Nk + 255) / 256, a.B * a.Hkv), dim3(256), 0, s,
+                    p);
 }
 
 }  // namespace mha
