@@ -8,8 +8,9 @@
 // product itself is a quarter of the attention forward's tensor work.  One CTA per 128 keys:
 // S^T = K Q^T (tcgen05.mma 128x128x16 into one of two TMEM buffers) for every 128-query tile of
 // the group's heads that sees the keys, so a key's row lies in one thread and its sum needs no
-// other: x = s * scale log2 e - lse log2 e, sum += 2^x, in paired fp32 operations.  Two CTAs share
-// an SM (192 threads, 65 KB, 256 TMEM columns each).  Where the key tiles alone leave SMs idle the
+// other: x = s * scale log2 e - lse log2 e, sum += 2^x, in paired fp32 operations.  Eight warps
+// sum, a key's 128 columns in two halves, and two CTAs share an SM (320 threads, 67 KB, 256 TMEM
+// columns each): four summing warps per scheduler.  Where the key tiles alone leave SMs idle the
 // query tiles are split over several CTAs, their sums added by a second launch in a fixed order.
 //
 // fp32 (key_weights_simt_kernel): 32 keys per CTA, each warp taking every eighth query of the
@@ -91,13 +92,15 @@ __global__ void __launch_bounds__(kWarps * 32) key_weights_simt_kernel(const Key
 constexpr int kT = 128;                   // keys and queries per tile
 constexpr int kTileBytes = kT * kD * 2;   // 16 KB
 constexpr int kStages = 3;                // query tiles in flight
-constexpr int kTcThreads = 192;           // warps 0-3 sums, 4 TMA, 5 MMA and TMEM
+constexpr int kSumWarps = 8;              // warp w: TMEM lanes 32 (w % 4).., columns 64 (w / 4)..
+constexpr int kWarpTma = kSumWarps, kWarpMma = kSumWarps + 1;
+constexpr int kTcThreads = (kSumWarps + 2) * 32;
 constexpr uint32_t kTmemCols = 256;       // two S^T buffers
 constexpr int kErrTimeout = -6;
 enum : int { kSiteKwProducer = 34, kSiteKwMma = 35, kSiteKwMath = 36 };
 constexpr int kOffQ = kTileBytes;
-constexpr int kOffLse = kOffQ + kStages * kTileBytes;  // [2][128] -lse log2 e
-constexpr int kOffBar = kOffLse + 2 * kT * 4;
+constexpr int kOffLse = kOffQ + kStages * kTileBytes;  // [stages][128] -lse log2 e
+constexpr int kOffBar = kOffLse + kStages * kT * 4;
 constexpr int kBarK = 0, kBarQ = 1, kBarQFree = kBarQ + kStages, kBarS = kBarQFree + kStages,
               kBarSFree = kBarS + 2, kBarDrain = kBarSFree + 2, kNumBars = kBarDrain + 1;
 constexpr int kTcSmem = 1024 + kOffBar + kNumBars * 8 + 16;
@@ -184,16 +187,16 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     mbar_init(bar(kBarK), 1);
     for (int i = 0; i < kStages; ++i) {
       mbar_init(bar(kBarQ + i), 1);
-      mbar_init(bar(kBarQFree + i), 1);
+      mbar_init(bar(kBarQFree + i), 1 + kSumWarps);  // the products, and the warps' use of lse
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kBarS + i), 1);
-      mbar_init(bar(kBarSFree + i), 4);  // one arrival per summing warp
+      mbar_init(bar(kBarSFree + i), kSumWarps);
     }
     mbar_init(bar(kBarDrain), 1);
     fence_mbar_init();
   }
-  if (warp == 5) {
+  if (warp == kWarpMma) {
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
   }
@@ -202,34 +205,49 @@ __global__ void __launch_bounds__(kTcThreads, 2)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 4) {
-    // ------------------------------------------------------------------ TMA producer
+  float* lse_s = reinterpret_cast<float*>(smem + kOffLse);
+  if (warp == kWarpTma) {
+    // ------------------------------------------------------------------ queries and their lse
+    const float* lse = a.lse + (static_cast<int64_t>(b) * a.H + g * G) * a.Nq;
     if (lane == 0) {
       prefetch_tmap(&tmQ);
       prefetch_tmap(&tmK);
       mbar_arrive_expect_tx(bar(kBarK), kTileBytes);
       tma_load_4d(smem_u32(smem), &tmK, bar(kBarK), 0, k0, g, b);
-      bool ok = true;
-      int asked = 0;
-      for (int j = 0; j < n; ++j) {
-        const int s = j % kStages;
-        if (!mbar_wait_backoff(bar(kBarQFree + s), ((j / kStages) & 1) ^ 1, p.timeout_ns)) {
-          ok = false;
-          break;
-        }
-        const int u = u0 + j;
-        mbar_arrive_expect_tx(bar(kBarQ + s), kTileBytes);
-        tma_load_4d(smem_u32(smem + kOffQ + s * kTileBytes), &tmQ, bar(kBarQ + s), 0,
-                    (first_q + u % per_head) * kT, g * G + u / per_head, b);
-        asked = j + 1;
+    }
+    bool ok = true;
+    int asked = 0;
+    for (int j = 0; j < n; ++j) {
+      const int s = j % kStages, u = u0 + j, q0 = (first_q + u % per_head) * kT, h = u / per_head;
+      float l[4];  // rows that do not count: 2^-inf = 0
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = q0 + 32 * i + lane;
+        l[i] = row < nq ? -__ldg(lse + static_cast<int64_t>(h) * a.Nq + row) * kLog2e : -INFINITY;
       }
+      if (!warp_all(mbar_wait_backoff(bar(kBarQFree + s), ((j / kStages) & 1) ^ 1,
+                                      p.timeout_ns))) {
+        ok = false;
+        break;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) lse_s[s * kT + 32 * i + lane] = l[i];
+      __syncwarp();
+      if (lane == 0) {  // the arrival releases the entries too
+        mbar_arrive_expect_tx(bar(kBarQ + s), kTileBytes);
+        tma_load_4d(smem_u32(smem + kOffQ + s * kTileBytes), &tmQ, bar(kBarQ + s), 0, q0,
+                    g * G + h, b);
+      }
+      asked = j + 1;
+    }
+    if (lane == 0) {
       if (!ok) record_error(p.status, kErrTimeout, kSiteKwProducer);
       // every copy started here lands before the CTA can exit
       (void)mbar_wait(bar(kBarK), 0, p.timeout_ns);
       for (int j = max(asked - kStages, 0); j < asked; ++j)
         (void)mbar_wait(bar(kBarQ + j % kStages), (j / kStages) & 1, p.timeout_ns);
     }
-  } else if (warp == 5) {
+  } else if (warp == kWarpMma) {
     // ------------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       constexpr uint32_t idS = idesc_bf16_f32(kT, kT, false, false);
@@ -257,68 +275,59 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     }
   } else {
     // ------------------------------------------------------------------ sums
-    const int tid = static_cast<int>(threadIdx.x);  // 0..127: this thread's key and TMEM lane
-    const int key = k0 + tid;
-    float* lse_s = reinterpret_cast<float*>(smem + kOffLse);
+    const int quarter = warp & 3, col0 = (warp >> 2) * 64;
+    const int key = k0 + quarter * 32 + lane;
     const float2 c2 = make_float2(a.scale * kLog2e, a.scale * kLog2e);
-    const uint32_t t_s = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    const float* lse = a.lse + (static_cast<int64_t>(b) * a.H + g * G) * a.Nq;
-    // this thread's entry of tile j's -lse log2 e; rows that do not count: 2^-inf = 0
-    auto load_lse = [&](int j) -> float {
-      const int u = u0 + j, i = (first_q + u % per_head) * kT + tid;
-      return i < nq ? -__ldg(lse + static_cast<int64_t>(u / per_head) * a.Nq + i) * kLog2e
-                    : -INFINITY;
-    };
-    lse_s[tid] = load_lse(0);
-    named_bar_sync(1, 128);
+    const uint32_t t_s = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + col0;
     float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     bool ok = true;
     for (int j = 0; j < n; ++j) {
-      const float next = j + 1 < n ? load_lse(j + 1) : 0.f;
-      const int buf = j & 1, q0 = (first_q + (u0 + j) % per_head) * kT;
-      if (ok && !warp_all(mbar_wait(bar(kBarS + buf), (j >> 1) & 1, p.timeout_ns))) {
+      const int buf = j & 1, s = j % kStages;
+      // the product, and (its queries' barrier) the tile's lse entries
+      if (!warp_all(mbar_wait(bar(kBarS + buf), (j >> 1) & 1, p.timeout_ns) &&
+                    mbar_wait(bar(kBarQ + s), (j / kStages) & 1, p.timeout_ns))) {
         if (lane == 0) record_error(p.status, kErrTimeout, kSiteKwMath);
         ok = false;
+        break;
       }
       tc_fence_after();
+      uint32_t r0[32], r1[32];
+      tmem_ld32(t_s + buf * kT, r0);
+      tmem_ld32(t_s + buf * kT + 32, r1);
+      tmem_wait_ld();
+      reg_fence(r0);
+      reg_fence(r1);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarSFree + buf));  // the buffer may be overwritten
       // columns that count for this key: from the diagonal on, before the last query
+      const int q0 = (first_q + (u0 + j) % per_head) * kT;
       const int first = a.mask == 1 ? key - q0 : 0, last = nq - q0;
-      const bool mask = last < kT || (a.mask == 1 && k0 + kT - 1 > q0);
-      const float* nl = lse_s + buf * kT;
-      if (ok) {
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t r0[32], r1[32];
-          tmem_ld32(t_s + buf * kT + half * 64, r0);
-          tmem_ld32(t_s + buf * kT + half * 64 + 32, r1);
-          tmem_wait_ld();
-          reg_fence(r0);
-          reg_fence(r1);
-          if (half == 1) {  // the buffer may be overwritten
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kBarSFree + buf));
-          }
-          if (mask) {
-            add_chunk<true>(r0, nl, c2, half * 64, first, last, acc);
-            add_chunk<true>(r1, nl, c2, half * 64 + 32, first, last, acc);
-          } else {
-            add_chunk<false>(r0, nl, c2, half * 64, first, last, acc);
-            add_chunk<false>(r1, nl, c2, half * 64 + 32, first, last, acc);
-          }
-        }
+      const float* nl = lse_s + s * kT;
+      if (last < kT || (a.mask == 1 && k0 + kT - 1 > q0)) {
+        add_chunk<true>(r0, nl, c2, col0, first, last, acc);
+        add_chunk<true>(r1, nl, c2, col0 + 32, first, last, acc);
+      } else {
+        add_chunk<false>(r0, nl, c2, col0, first, last, acc);
+        add_chunk<false>(r1, nl, c2, col0 + 32, first, last, acc);
       }
-      lse_s[(buf ^ 1) * kT + tid] = next;
-      named_bar_sync(1, 128);  // entries written; all have read this tile's
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarQFree + s));
     }
-    if (key < nk && ok) {
-      const float2 s = fadd2(acc[0], acc[1]);
-      out[key] = (p.split == 1 ? out[key] : 0.f) + (s.x + s.y);
+    // the two column halves of a key through the (now unused) key tile's memory.  After a time-out
+    // nothing is written
+    float* half = reinterpret_cast<float*>(smem);
+    const float2 t = fadd2(acc[0], acc[1]);
+    if (col0 > 0) half[quarter * 32 + lane] = ok ? t.x + t.y : NAN;
+    named_bar_sync(1, kSumWarps * 32);
+    if (col0 == 0 && key < nk && ok) {
+      const float sum = t.x + t.y + half[quarter * 32 + lane];
+      out[key] = p.split == 1 ? out[key] + sum : sum;
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == kWarpMma) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
