@@ -18,6 +18,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "launchers.h"
 #include "device_common.cuh"
@@ -91,7 +92,7 @@ __global__ void __launch_bounds__(kWarps * 32) key_weights_simt_kernel(const Key
 // ============================================================================ bf16
 constexpr int kT = 128;                   // keys and queries per tile
 constexpr int kTileBytes = kT * kD * 2;   // 16 KB
-constexpr int kStages = 3;                // query tiles in flight
+constexpr int kStages = 4;                // query tiles in flight
 constexpr int kSumWarps = 8;              // warp w: TMEM lanes 32 (w % 4).., columns 64 (w / 4)..
 constexpr int kWarpTma = kSumWarps, kWarpMma = kSumWarps + 1;
 constexpr int kTcThreads = (kSumWarps + 2) * 32;
@@ -115,14 +116,12 @@ struct TcParams {
 
 __device__ __forceinline__ bool warp_all(bool v) { return __all_sync(0xffffffffu, v); }
 
-// 32 queries of one key: adds 2^(s c - lse2) for the columns first <= c0 + i < last (kMask: only
-// those; the others' scores may be anything)
-template <bool kMask>
+// 32 queries of one key: acc += 2^(s c + nl)
 __device__ __forceinline__ void add_chunk(const uint32_t (&s)[32], const float* nl, float2 c2,
-                                          int c0, int first, int last, float2 (&acc)[2]) {
+                                          float2 (&acc)[4]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float4 n = *reinterpret_cast<const float4*>(nl + c0 + 4 * i);
+    const float4 n = *reinterpret_cast<const float4*>(nl + 4 * i);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int k = 4 * i + 2 * h;
@@ -130,13 +129,15 @@ __device__ __forceinline__ void add_chunk(const uint32_t (&s)[32], const float* 
                        h ? make_float2(n.z, n.w) : make_float2(n.x, n.y));
       x.x = ex2_approx(x.x);
       x.y = ex2_approx(x.y);
-      if (kMask) {
-        if (c0 + k < first || c0 + k >= last) x.x = 0.f;
-        if (c0 + k + 1 < first || c0 + k + 1 >= last) x.y = 0.f;
-      }
-      acc[h] = fadd2(acc[h], x);
+      acc[k / 2 % 4] = fadd2(acc[k / 2 % 4], x);
     }
   }
+}
+// the scores of columns outside first <= i < last, which may be anything: -inf
+__device__ __forceinline__ void exclude(uint32_t (&s)[32], int first, int last) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    if (i < first || i >= last) s[i] = 0xff800000u;
 }
 
 __global__ void __launch_bounds__(kTcThreads, 2)
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       mbar_init(bar(kBarQFree + i), 1 + kSumWarps);  // the products, and the warps' use of lse
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(kBarS + i), 1);
+      mbar_init(bar(kBarS + i), 2);  // the products, and their issuer (see there)
       mbar_init(bar(kBarSFree + i), kSumWarps);
     }
     mbar_init(bar(kBarDrain), 1);
@@ -216,17 +217,17 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       tma_load_4d(smem_u32(smem), &tmK, bar(kBarK), 0, k0, g, b);
     }
     bool ok = true;
-    int asked = 0;
+    int asked = 0, s = 0, tile = u0 % per_head, h = u0 / per_head;
+    uint32_t phase = 1;
     for (int j = 0; j < n; ++j) {
-      const int s = j % kStages, u = u0 + j, q0 = (first_q + u % per_head) * kT, h = u / per_head;
+      const int q0 = (first_q + tile) * kT;
       float l[4];  // rows that do not count: 2^-inf = 0
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int row = q0 + 32 * i + lane;
         l[i] = row < nq ? -__ldg(lse + static_cast<int64_t>(h) * a.Nq + row) * kLog2e : -INFINITY;
       }
-      if (!warp_all(mbar_wait_backoff(bar(kBarQFree + s), ((j / kStages) & 1) ^ 1,
-                                      p.timeout_ns))) {
+      if (!warp_all(mbar_wait_backoff(bar(kBarQFree + s), phase, p.timeout_ns))) {
         ok = false;
         break;
       }
@@ -239,6 +240,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                     g * G + h, b);
       }
       asked = j + 1;
+      if (++s == kStages) s = 0, phase ^= 1;
+      if (++tile == per_head) tile = 0, ++h;
     }
     if (lane == 0) {
       if (!ok) record_error(p.status, kErrTimeout, kSiteKwProducer);
@@ -268,6 +271,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
           mma_bf16_ss(tmem + buf * kT, dK + kk * 2, bq + kk * 2, idS, kk > 0 ? 1u : 0u);
         mma_commit(bar(kBarQFree + s));
         mma_commit(bar(kBarS + buf));
+        // releases to the summing warps what this thread acquired with the tile: its lse entries
+        mbar_arrive(bar(kBarS + buf));
       }
       if (!ok) record_error(p.status, kErrTimeout, kSiteKwMma);
       mma_commit(bar(kBarDrain));
@@ -277,47 +282,63 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     // ------------------------------------------------------------------ sums
     const int quarter = warp & 3, col0 = (warp >> 2) * 64;
     const int key = k0 + quarter * 32 + lane;
-    const float2 c2 = make_float2(a.scale * kLog2e, a.scale * kLog2e);
+    const float c = fmaxf(a.scale * kLog2e, 1.2e-38f);  // -inf * c stays -inf
+    const float2 c2 = make_float2(c, c);
     const uint32_t t_s = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + col0;
-    float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-    bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      const int buf = j & 1, s = j % kStages;
-      // the product, and (its queries' barrier) the tile's lse entries
-      if (!warp_all(mbar_wait(bar(kBarS + buf), (j >> 1) & 1, p.timeout_ns) &&
-                    mbar_wait(bar(kBarQ + s), (j / kStages) & 1, p.timeout_ns))) {
-        if (lane == 0) record_error(p.status, kErrTimeout, kSiteKwMath);
-        ok = false;
-        break;
-      }
+    float2 acc[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = make_float2(0.f, 0.f);
+    int slot = 0, tile = u0 % per_head;  // of the ring; of the head, from first_q
+    uint32_t phase = 0;                  // bit `buf` that of S buffer buf
+    auto wait_s = [&](int buf) -> bool {
+      const bool got = warp_all(mbar_wait(bar(kBarS + buf), (phase >> buf) & 1, p.timeout_ns));
+      if (!got && lane == 0) record_error(p.status, kErrTimeout, kSiteKwMath);
+      phase ^= 1u << buf;
       tc_fence_after();
-      uint32_t r0[32], r1[32];
-      tmem_ld32(t_s + buf * kT, r0);
-      tmem_ld32(t_s + buf * kT + 32, r1);
-      tmem_wait_ld();
-      reg_fence(r0);
-      reg_fence(r1);
-      tc_fence_before();
+      return got;
+    };
+    // 32 columns are worked on while the next 32 are on their way from TMEM
+    uint32_t r0[32], r1[32];
+    bool ok = wait_s(0);
+    tmem_ld32(t_s, r0);
+    for (int j = 0; ok && j < n; ++j) {
+      const int buf = j & 1, q0 = (first_q + tile) * kT;
+      const float* nl = lse_s + slot * kT + col0;
+      // kMask: some columns do not count for some key.  Its code apart from the first load on: with
+      // a branch behind the loads the other tiles' took 446 instead of 391 us (8 x 16 heads x 4096)
+      auto add_tile = [&](auto mask_type) {
+        constexpr bool kMask = decltype(mask_type)::value;
+        // from the diagonal on, before the last query
+        const int first = (a.mask == 1 ? key - q0 : 0) - col0, last = nq - q0 - col0;
+        tmem_wait_ld();
+        reg_fence(r0);
+        tmem_ld32(t_s + buf * kT + 32, r1);
+        if constexpr (kMask) exclude(r0, first, last);
+        add_chunk(r0, nl, c2, acc);
+        tmem_wait_ld();
+        reg_fence(r1);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarSFree + buf));  // the buffer may be overwritten
+        if (j + 1 < n) ok = wait_s(buf ^ 1);
+        tmem_ld32(t_s + (buf ^ 1) * kT, r0);  // behind the last tile: unused
+        if constexpr (kMask) exclude(r1, first - 32, last - 32);
+        add_chunk(r1, nl + 32, c2, acc);
+      };
+      if (nq - q0 < kT || (a.mask == 1 && k0 + kT - 1 > q0))
+        add_tile(std::true_type{});
+      else
+        add_tile(std::false_type{});
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarSFree + buf));  // the buffer may be overwritten
-      // columns that count for this key: from the diagonal on, before the last query
-      const int q0 = (first_q + (u0 + j) % per_head) * kT;
-      const int first = a.mask == 1 ? key - q0 : 0, last = nq - q0;
-      const float* nl = lse_s + s * kT;
-      if (last < kT || (a.mask == 1 && k0 + kT - 1 > q0)) {
-        add_chunk<true>(r0, nl, c2, col0, first, last, acc);
-        add_chunk<true>(r1, nl, c2, col0 + 32, first, last, acc);
-      } else {
-        add_chunk<false>(r0, nl, c2, col0, first, last, acc);
-        add_chunk<false>(r1, nl, c2, col0 + 32, first, last, acc);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarQFree + s));
+      if (lane == 0) mbar_arrive(bar(kBarQFree + slot));
+      if (++slot == kStages) slot = 0;
+      if (++tile == per_head) tile = 0;
     }
+    tmem_wait_ld();
     // the two column halves of a key through the (now unused) key tile's memory.  After a time-out
     // nothing is written
     float* half = reinterpret_cast<float*>(smem);
-    const float2 t = fadd2(acc[0], acc[1]);
+    const float2 t = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
     if (col0 > 0) half[quarter * 32 + lane] = ok ? t.x + t.y : NAN;
     named_bar_sync(1, kSumWarps * 32);
     if (col0 == 0 && key < nk && ok) {
