@@ -218,7 +218,7 @@ int mha_kv_evict_q8(int B, int H, int Lmax, int Lmax_out, int d_k, int d_v, int 
       if (out[i] == out[k]) return MHA_ERR_INVALID;
   }
   if (d_k != 64 || d_v != 64 || !valid_block(block) || B > 65535 || H > 65535 ||
-      Lmax > (1 << 30) || Lmax_out > (1 << 30))
+      static_cast<int64_t>(B) * H > (1 << 27) || Lmax > (1 << 30) || Lmax_out > (1 << 30))
     return MHA_ERR_UNSUPPORTED;
   mha::KvEvictArgs a;
   int st = take_strides(strides, 0, H, Lmax, 16, a.sk);

@@ -3,9 +3,12 @@
 //
 // Two launches.  select: per (batch element, head) the kept positions, ascending: the newest
 // `recent` and, of the others, those with the largest weights (equal weights: the lower
-// position).  The k-th largest weight is found by a radix descent over the weights' bits, eight
-// at a time (the counts of one digit in shared memory), which reads the weights from L2 four
-// times instead of sorting them; one more pass writes the positions in order.
+// position).  A cluster of up to eight CTAs holds a head's weights in registers, 16 neighbours to
+// a thread, so they are read from memory once (heads longer than that are read again for every
+// step).  The k-th largest weight is found by a radix descent over the weights' bits, eight at a
+// time, with the counts of one digit in shared memory and added up over the cluster; then one
+// prefix sum over threads and CTAs gives every kept position its place.  No sorting, no order that
+// depends on timing: the counts are sums of integers.
 // gather: one CTA per (block of the new cache, head, batch element) copies the block's rows; the
 // block takes the largest scale of the tokens it receives, and codes that came under a smaller
 // one are written under it.  Bound by HBM: 64 bytes read and written per row of K and of V.
@@ -17,8 +20,7 @@
 namespace mha {
 namespace {
 
-constexpr int kSelThreads = 1024;
-constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kEach = 16;  // weights per thread
 
 // fp32 to an unsigned integer of the same order; -0 equals +0 and NaN the lowest value
 __device__ __forceinline__ uint32_t order_key(float w) {
@@ -27,144 +29,297 @@ __device__ __forceinline__ uint32_t order_key(float w) {
   return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
-__global__ void __launch_bounds__(kSelThreads) kv_evict_select_kernel(const KvEvictArgs a) {
+__device__ __forceinline__ int ld_cluster(uint32_t addr) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// kThreads a power of two.  The grid's x is B * H clusters of `ctas` CTAs.
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads) kv_evict_select_kernel(const KvEvictArgs a, int ctas) {
   pdl_launch_dependents();
   pdl_wait();  // the previous kernel's output is complete from here on
-  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
-  const int lane = tid & 31, warp = tid >> 5;
-  const int64_t bh = static_cast<int64_t>(b) * a.H + h;
+  constexpr int kWarps = kThreads / 32;
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+  const int rank = static_cast<int>(blockIdx.x) % ctas;  // CTA of the cluster
+  const int64_t bh = blockIdx.x / ctas;
+  const int b = static_cast<int>(bh / a.H);
   const int L = min(max(__ldg(a.cache_len + b), 0), a.Lmax);
   int32_t* kept = a.kept + bh * a.keep;
   const int n_out = min(L, a.keep);
-  if (h == 0 && tid == 0) a.len_out[b] = n_out;
-  for (int i = n_out + tid; i < a.keep; i += kSelThreads) kept[i] = -1;
-  if (L <= a.keep) {  // nothing to drop
-    for (int i = tid; i < L; i += kSelThreads) kept[i] = i;
+  if (bh % a.H == 0 && rank == 0 && tid == 0) a.len_out[b] = n_out;
+  for (int i = n_out + rank * kThreads + tid; i < a.keep; i += ctas * kThreads) kept[i] = -1;
+  if (L <= a.keep) {  // nothing to drop (the same for the whole cluster)
+    for (int i = rank * kThreads + tid; i < L; i += ctas * kThreads) kept[i] = i;
     return;
   }
   const float* w = a.weights + bh * a.Lmax;
   const int recent = min(a.recent, a.keep);
-  const int m = L - recent;       // candidates: positions 0..m-1
-  int k = a.keep - recent;        // of which the k largest stay, 0 <= k < m
-  __shared__ int hist[256];
-  __shared__ int s_digit, s_above;
-  __shared__ int s_sum[2][kSelWarps];
-  uint32_t prefix = 0;            // the high bits of the k-th largest key
-  int above = 0;                  // candidates above the prefix so far
-  for (int shift = 24; k > 0 && shift >= 0; shift -= 8) {
-    for (int i = tid; i < 256; i += kSelThreads) hist[i] = 0;
+  const int m = L - recent;      // candidates: positions 0..m-1
+  const int k = a.keep - recent;  // of which the k largest stay, 0 <= k < m
+  // position of a thread's first weight in step c of `steps`
+  const int per_step = ctas * kThreads * kEach;
+  const int steps = (L + per_step - 1) / per_step;
+  auto first = [&](int c) { return ((c * ctas + rank) * kThreads + tid) * kEach; };
+  uint32_t key[kEach];
+  const bool vector = (reinterpret_cast<uintptr_t>(w) & 15) == 0;
+  auto load = [&](int c) {
+    const int j0 = first(c);
+    if (vector && j0 + kEach <= m) {
+#pragma unroll
+      for (int i = 0; i < kEach / 4; ++i) {
+        const float4 v = *reinterpret_cast<const float4*>(w + j0 + 4 * i);
+        key[4 * i] = order_key(v.x);
+        key[4 * i + 1] = order_key(v.y);
+        key[4 * i + 2] = order_key(v.z);
+        key[4 * i + 3] = order_key(v.w);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) key[i] = j0 + i < m ? order_key(w[j0 + i]) : 0u;
+    }
+  };
+  __shared__ int hist[2][256];  // of the digit: this CTA's; two, so that one round can be read
+                                // by the cluster while the next is cleared
+  __shared__ int s_warp[kWarps], s_pick[2], s_total[2][2];
+  auto sync_all = [&]() {
+    if (ctas == 1)
+      __syncthreads();
+    else
+      cluster_sync_all();
+  };
+
+  // ---- the k-th largest key
+  uint32_t prefix = 0;  // its high bits
+  int above = 0;        // candidates above the prefix
+  load(0);
+  for (int shift = 24, round = 0; k > 0 && shift >= 0; shift -= 8, round ^= 1) {
+    int* h = hist[round];
+    for (int i = tid; i < 256; i += kThreads) h[i] = 0;
     __syncthreads();
-    for (int j = tid; j < m; j += kSelThreads) {
-      const uint32_t key = order_key(w[j]);
-      if (shift == 24 || (key >> (shift + 8)) == (prefix >> (shift + 8)))
-        atomicAdd(&hist[(key >> shift) & 255u], 1);  // integers: any order gives the same count
+    for (int c = 0; c < steps; ++c) {
+      if (steps > 1) load(c);
+      const int j0 = first(c);
+#pragma unroll
+      for (int i = 0; i < kEach; ++i)
+        if (j0 + i < m &&
+            (shift == 24 || (key[i] >> ((shift + 8) & 31)) == (prefix >> ((shift + 8) & 31))))
+          atomicAdd(&h[(key[i] >> shift) & 255u], 1);
+    }
+    sync_all();
+    if (warp == 0) {  // lane l: digits 255 - 8l downwards, eight of them
+      int n[8], sum = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int d = 255 - 8 * lane - i;
+        n[i] = 0;
+        if (ctas == 1) {
+          n[i] = h[d];
+        } else {
+          const uint32_t at = smem_u32(h + d);
+          for (int r = 0; r < ctas; ++r) n[i] += ld_cluster(mapa_shared(at, r));
+        }
+        sum += n[i];
+      }
+      int before = sum;  // exclusive sum over the lanes, then digit by digit
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += v;
+      }
+      before += above - sum;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (before < k && before + n[i] >= k) {  // one lane's one digit
+          s_pick[0] = 255 - 8 * lane - i;
+          s_pick[1] = before;
+        }
+        before += n[i];
+      }
     }
     __syncthreads();
-    if (tid == 0) {
-      int c = above, d = 255;
-      while (d > 0 && c + hist[d] < k) c += hist[d--];
-      s_digit = d;
-      s_above = c;
-    }
-    __syncthreads();
-    prefix |= static_cast<uint32_t>(s_digit) << shift;
-    above = s_above;
+    prefix |= static_cast<uint32_t>(s_pick[0]) << shift;
+    above = s_pick[1];
   }
   const int ties = k - above;  // candidates equal to the k-th largest that stay, lowest first
-  // kept positions in order: running counts of the kept and of the ties
-  int base = 0, tie_base = 0;
-  for (int j0 = 0; j0 < L; j0 += kSelThreads) {
-    const int j = j0 + tid;
-    const uint32_t key = j < m ? order_key(w[j]) : 0u;
-    const bool eq = k > 0 && j < m && key == prefix;
-    const bool gt = (k > 0 && j < m && key > prefix) || (j >= m && j < L);
-    const uint32_t be = __ballot_sync(0xffffffffu, eq);
-    if (lane == 0) s_sum[0][warp] = __popc(be);
-    __syncthreads();
-    int tie = tie_base + __popc(be & ((1u << lane) - 1u)), ties_here = 0;
-    for (int x = 0; x < kSelWarps; ++x) {
-      if (x < warp) tie += s_sum[0][x];
-      ties_here += s_sum[0][x];
+
+  // ---- places: behind all kept weights above it, and those ties before it that stay
+  int gt0 = 0, eq0 = 0;  // of the steps before
+  for (int c = 0; c < steps; ++c) {
+    if (steps > 1) load(c);
+    const int j0 = first(c);
+    uint32_t gt = 0, eq = 0;  // bit i: weight i stays whatever the ties; is one
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int j = j0 + i;
+      if (j < m) {
+        gt |= (k > 0 && key[i] > prefix ? 1u : 0u) << i;
+        eq |= (k > 0 && key[i] == prefix ? 1u : 0u) << i;
+      } else if (j < L) {
+        gt |= 1u << i;
+      }
     }
-    const bool keep = gt || (eq && tie < ties);
-    const uint32_t bk = __ballot_sync(0xffffffffu, keep);
-    if (lane == 0) s_sum[1][warp] = __popc(bk);
-    __syncthreads();
-    int at = base + __popc(bk & ((1u << lane) - 1u)), here = 0;
-    for (int x = 0; x < kSelWarps; ++x) {
-      if (x < warp) at += s_sum[1][x];
-      here += s_sum[1][x];
+    // both counts in one scan: at most 16384 each
+    const int mine = (__popc(gt) << 16) | __popc(eq);
+    int scan = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, scan, o);
+      if (lane >= o) scan += v;
     }
-    if (keep) kept[at] = j;
-    base += here;
-    tie_base += ties_here;
+    if (lane == 31) s_warp[warp] = scan;
     __syncthreads();
+    if (warp == 0) {
+      const int v = lane < kWarps ? s_warp[lane] : 0;
+      int t = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, t, o);
+        if (lane >= o) t += u;
+      }
+      if (lane < kWarps) s_warp[lane] = t - v;
+      if (lane == 31) {
+        s_total[c & 1][0] = static_cast<int>(static_cast<uint32_t>(t) >> 16);
+        s_total[c & 1][1] = t & 0xffff;
+      }
+    }
+    sync_all();
+    int g = gt0, e = eq0;  // of the CTAs before, and (gt0, eq0) of all up to this step
+    for (int r = 0; r < ctas; ++r) {
+      int rg = s_total[c & 1][0], re = s_total[c & 1][1];
+      if (ctas > 1) {
+        rg = ld_cluster(mapa_shared(smem_u32(&s_total[c & 1][0]), r));
+        re = ld_cluster(mapa_shared(smem_u32(&s_total[c & 1][1]), r));
+      }
+      if (r < rank) g += rg, e += re;
+      gt0 += rg;
+      eq0 += re;
+    }
+    const uint32_t before = static_cast<uint32_t>(s_warp[warp] + scan - mine);
+    g += static_cast<int>(before >> 16);
+    e += static_cast<int>(before & 0xffffu);
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const bool is_gt = (gt >> i) & 1u, is_eq = (eq >> i) & 1u;
+      if (is_gt || (is_eq && e < ties)) kept[g + min(e, ties)] = j0 + i;
+      g += is_gt;
+      e += is_eq;
+    }
+    __syncthreads();  // s_warp is written again
   }
+  if (ctas > 1) cluster_sync_all();  // no CTA leaves while others may read its counts
 }
 
 constexpr int kGatherThreads = 256;  // 128 for K, 128 for V
 
-template <int QT>
+// BLOCK: tokens per scale.  Four threads to a row; a row is asked for as soon as its position is
+// known, together with its scale.
+template <int QT, int BLOCK>
 __global__ void __launch_bounds__(kGatherThreads) kv_evict_gather_kernel(const KvEvictArgs a) {
   pdl_launch_dependents();
   pdl_wait();  // the select kernel's positions are complete from here on
+  constexpr int kRows = (BLOCK + 31) / 32;  // of a thread
   const int h = blockIdx.y, b = blockIdx.z;
   const int64_t bh = static_cast<int64_t>(b) * a.H + h;
   const int n_out = min(min(max(__ldg(a.cache_len + b), 0), a.Lmax), a.keep);
-  const int lo = static_cast<int>(blockIdx.x) * a.block;
-  const int rows = min(a.block, n_out - lo);
+  const int lo = static_cast<int>(blockIdx.x) * BLOCK;
+  const int rows = min(BLOCK, n_out - lo);
   if (rows <= 0) return;
-  __shared__ int src[128];
-  __shared__ float ssc[2][128];
   __shared__ float smax[8];
-  const int part = threadIdx.x >> 7, tid = threadIdx.x & 127;
+  const int part = threadIdx.x >> 7, tid = threadIdx.x & 127, chunk = (tid & 3) * 16;
   const float* scale = (part ? a.v_scale : a.k_scale) + bh * a.n_blocks;
-  float sc = 0.f;
-  if (tid < rows) {
-    const int j = a.kept[bh * a.keep + lo + tid];
-    sc = scale[j / a.block];
-    ssc[part][tid] = sc;
-    if (part == 0) {
-      src[tid] = j;
-      if (a.weights_out != nullptr)
-        a.weights_out[bh * a.Lmax_out + lo + tid] = a.weights[bh * a.Lmax + j];
+  const int64_t* si = part ? a.sv : a.sk;
+  const uint8_t* in = static_cast<const uint8_t*>(part ? a.Vc : a.Kc) + b * si[0] + h * si[1];
+  const int32_t* kept = a.kept + bh * a.keep + lo;
+  int j[kRows];
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    const int r = (tid >> 2) + 32 * k;
+    j[k] = r < rows ? kept[r] : -1;
+  }
+  uint4 u[kRows];
+  float sc[kRows], most = 0.f;
+#pragma unroll
+  for (int k = 0; k < kRows; ++k)
+    if (j[k] >= 0) {
+      u[k] = *reinterpret_cast<const uint4*>(in + j[k] * si[2] + chunk);
+      sc[k] = scale[j[k] / BLOCK];
     }
+  if (a.weights_out != nullptr && part == 0 && chunk == 0) {
+#pragma unroll
+    for (int k = 0; k < kRows; ++k)
+      if (j[k] >= 0)
+        a.weights_out[bh * a.Lmax_out + lo + (tid >> 2) + 32 * k] = a.weights[bh * a.Lmax + j[k]];
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sc = fmaxf(sc, __shfl_xor_sync(0xffffffffu, sc, o));
-  if ((threadIdx.x & 31) == 0) smax[threadIdx.x >> 5] = sc;
+  for (int k = 0; k < kRows; ++k)
+    if (j[k] >= 0) most = fmaxf(most, sc[k]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+  if ((threadIdx.x & 31) == 0) smax[threadIdx.x >> 5] = most;
   __syncthreads();
   const float now = fmaxf(fmaxf(smax[part * 4], smax[part * 4 + 1]),
                           fmaxf(smax[part * 4 + 2], smax[part * 4 + 3]));
   if (tid == 0) (part ? a.v_scale_out : a.k_scale_out)[bh * a.n_blocks_out + blockIdx.x] = now;
-  const int64_t* si = part ? a.sv : a.sk;
   const int64_t* so = part ? a.svo : a.sko;
-  const uint8_t* in = static_cast<const uint8_t*>(part ? a.Vc : a.Kc) + b * si[0] + h * si[1] +
-                      (tid & 3) * 16;
-  uint8_t* out = static_cast<uint8_t*>(part ? a.Vo : a.Ko) + b * so[0] + h * so[1] + lo * so[2] +
-                 (tid & 3) * 16;
-  for (int r = tid >> 2; r < rows; r += 32) {
-    uint4 u = *reinterpret_cast<const uint4*>(in + src[r] * si[2]);
-    const float was = ssc[part][r];
-    if (was < now) {
-      const float ratio = was / now;  // exact: powers of two
-      u = make_uint4(q8_rescale4<QT>(u.x, ratio), q8_rescale4<QT>(u.y, ratio),
-                     q8_rescale4<QT>(u.z, ratio), q8_rescale4<QT>(u.w, ratio));
+  uint8_t* out = static_cast<uint8_t*>(part ? a.Vo : a.Ko) + b * so[0] + h * so[1] +
+                 static_cast<int64_t>(lo) * so[2] + chunk;
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    if (j[k] < 0) continue;
+    if (sc[k] < now) {
+      const float ratio = sc[k] / now;  // exact for powers of two
+      u[k] = make_uint4(q8_rescale4<QT>(u[k].x, ratio), q8_rescale4<QT>(u[k].y, ratio),
+                        q8_rescale4<QT>(u[k].z, ratio), q8_rescale4<QT>(u[k].w, ratio));
     }
-    *reinterpret_cast<uint4*>(out + r * so[2]) = u;
+    *reinterpret_cast<uint4*>(out + ((tid >> 2) + 32 * k) * so[2]) = u[k];
   }
+}
+
+template <int kThreads>
+cudaError_t launch_select(const KvEvictArgs& a, int ctas, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.B) * a.H * ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = ctas;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kv_evict_select_kernel<kThreads>, a, ctas);
+}
+
+template <int QT>
+cudaError_t launch_gather(const KvEvictArgs& a, cudaStream_t s) {
+  const dim3 grid((a.keep + a.block - 1) / a.block, a.H, a.B);
+  auto kern = a.block == 16   ? kv_evict_gather_kernel<QT, 16>
+              : a.block == 32 ? kv_evict_gather_kernel<QT, 32>
+              : a.block == 64 ? kv_evict_gather_kernel<QT, 64>
+                              : kv_evict_gather_kernel<QT, 128>;
+  return launch_pdl(kern, grid, dim3(kGatherThreads), 0, s, a);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_evict_q8(const KvEvictArgs& a, int qtype, cudaStream_t s) {
-  cudaError_t e =
-      launch_pdl(kv_evict_select_kernel, dim3(a.H, a.B), dim3(kSelThreads), 0, s, a);
+  // threads for one step over the cache: 256 to 4096 positions (eight CTAs share an SM), then
+  // 1024 in one to eight CTAs
+  cudaError_t e;
+  if (a.Lmax <= 256 * kEach) {
+    e = launch_select<256>(a, 1, s);
+  } else {
+    int ctas = 1;
+    while (ctas < 8 && a.Lmax > ctas * 1024 * kEach) ctas *= 2;
+    e = launch_select<1024>(a, ctas, s);
+  }
   if (e != cudaSuccess) return e;
-  const dim3 grid((a.keep + a.block - 1) / a.block, a.H, a.B);
-  return qtype == kE4m3
-             ? launch_pdl(kv_evict_gather_kernel<kE4m3>, grid, dim3(kGatherThreads), 0, s, a)
-             : launch_pdl(kv_evict_gather_kernel<kInt8>, grid, dim3(kGatherThreads), 0, s, a);
+  return qtype == kE4m3 ? launch_gather<kE4m3>(a, s) : launch_gather<kInt8>(a, s);
 }
 
 }  // namespace mha
