@@ -17,12 +17,11 @@ namespace {
 constexpr int kD = 64;
 constexpr int kThreads = 256;  // 128 for K, 128 for V
 
-__device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&f)[16]) {
-  const uint4* q = reinterpret_cast<const uint4*>(p);
+// 16 values as they are stored, and as fp32
+__device__ __forceinline__ void widen(const uint4 (&u)[2], float (&f)[16]) {  // bf16
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const uint4 u = q[i];
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       f[8 * i + 2 * k] = __uint_as_float(w[k] << 16);
@@ -30,14 +29,13 @@ __device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&f)[16]) {
     }
   }
 }
-__device__ __forceinline__ void load16(const float* p, float (&f)[16]) {
+__device__ __forceinline__ void widen(const uint4 (&u)[4], float (&f)[16]) {  // fp32
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float4 u = reinterpret_cast<const float4*>(p)[i];
-    f[4 * i] = u.x;
-    f[4 * i + 1] = u.y;
-    f[4 * i + 2] = u.z;
-    f[4 * i + 3] = u.w;
+    f[4 * i] = __uint_as_float(u[i].x);
+    f[4 * i + 1] = __uint_as_float(u[i].y);
+    f[4 * i + 2] = __uint_as_float(u[i].z);
+    f[4 * i + 3] = __uint_as_float(u[i].w);
   }
 }
 
@@ -71,16 +69,26 @@ __global__ void __launch_bounds__(kThreads) kv_append_q8_kernel(const KvAppendAr
   cache += b * sc[0] + h * sc[1] + lo * sc[2] + chunk * 16;
 
   // largest finite magnitude of the block's new tokens
-  float f[kRows][16];
+  constexpr int kQuads = sizeof(T);  // 16-byte loads of 16 values
+  uint4 raw[kRows][kQuads];          // as stored: half the registers of fp32 for bf16
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    const int r = row0 + 32 * k;
+    if (r >= first && r < end)
+#pragma unroll
+      for (int i = 0; i < kQuads; ++i)
+        raw[k][i] = reinterpret_cast<const uint4*>(x + r * sx[2])[i];
+  }
   float amax = 0.f;
 #pragma unroll
   for (int k = 0; k < kRows; ++k) {
     const int r = row0 + 32 * k;
     if (r >= first && r < end) {
-      load16(x + r * sx[2], f[k]);
+      float f[16];
+      widen(raw[k], f);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const float m = fabsf(f[k][i]);
+        const float m = fabsf(f[i]);
         amax = m <= 3.402823466e38f ? fmaxf(amax, m) : amax;  // false for inf and NaN
       }
     }
@@ -102,11 +110,13 @@ __global__ void __launch_bounds__(kThreads) kv_append_q8_kernel(const KvAppendAr
     const int r = row0 + 32 * k;
     uint4* dst = reinterpret_cast<uint4*>(cache + r * sc[2]);
     if (r >= first && r < end) {
+      float f[16];
+      widen(raw[k], f);
       uint32_t w[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        w[i] = q8_encode4<QT>(f[k][4 * i] * inv, f[k][4 * i + 1] * inv, f[k][4 * i + 2] * inv,
-                              f[k][4 * i + 3] * inv);
+        w[i] = q8_encode4<QT>(f[4 * i] * inv, f[4 * i + 1] * inv, f[4 * i + 2] * inv,
+                              f[4 * i + 3] * inv);
       *dst = make_uint4(w[0], w[1], w[2], w[3]);
     } else if (r < first && now > was) {  // tokens that were there, under the larger scale
       const float ratio = was * inv;

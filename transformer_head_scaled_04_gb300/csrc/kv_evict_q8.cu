@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kThreads) kv_evict_select_kernel(const KvEvict
   };
   __shared__ int hist[2][256];  // of the digit: this CTA's; two, so that one round can be read
                                 // by the cluster while the next is cleared
-  __shared__ int s_warp[kWarps], s_pick[2], s_total[2][2];
+  __shared__ int s_count[256], s_warp[kWarps], s_pick[2], s_total[2][2];
   auto sync_all = [&]() {
     if (ctas == 1)
       __syncthreads();
@@ -108,18 +108,23 @@ __global__ void __launch_bounds__(kThreads) kv_evict_select_kernel(const KvEvict
           atomicAdd(&h[(key[i] >> shift) & 255u], 1);
     }
     sync_all();
+    if (ctas > 1) {  // a thread per digit adds up the cluster's
+      if (tid < 256) {
+        const uint32_t at = smem_u32(h + tid);
+        int n = 0;
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          if (r < ctas) n += ld_cluster(mapa_shared(at, r));
+        s_count[tid] = n;
+      }
+      __syncthreads();
+      h = s_count;
+    }
     if (warp == 0) {  // lane l: digits 255 - 8l downwards, eight of them
       int n[8], sum = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int d = 255 - 8 * lane - i;
-        n[i] = 0;
-        if (ctas == 1) {
-          n[i] = h[d];
-        } else {
-          const uint32_t at = smem_u32(h + d);
-          for (int r = 0; r < ctas; ++r) n[i] += ld_cluster(mapa_shared(at, r));
-        }
+        n[i] = h[255 - 8 * lane - i];
         sum += n[i];
       }
       int before = sum;  // exclusive sum over the lanes, then digit by digit
@@ -211,69 +216,82 @@ __global__ void __launch_bounds__(kThreads) kv_evict_select_kernel(const KvEvict
   if (ctas > 1) cluster_sync_all();  // no CTA leaves while others may read its counts
 }
 
-constexpr int kGatherThreads = 256;  // 128 for K, 128 for V
+constexpr int kGatherThreads = 128;
 
-// BLOCK: tokens per scale.  Four threads to a row; a row is asked for as soon as its position is
-// known, together with its scale.
+// BLOCK: tokens per scale.  Four threads to a row, of K and of V; a row is asked for as soon as
+// its position is known (-1: there is none), together with its scale.
 template <int QT, int BLOCK>
 __global__ void __launch_bounds__(kGatherThreads) kv_evict_gather_kernel(const KvEvictArgs a) {
   pdl_launch_dependents();
   pdl_wait();  // the select kernel's positions are complete from here on
   constexpr int kRows = (BLOCK + 31) / 32;  // of a thread
-  const int h = blockIdx.y, b = blockIdx.z;
+  const int h = blockIdx.y, b = blockIdx.z, tid = static_cast<int>(threadIdx.x);
   const int64_t bh = static_cast<int64_t>(b) * a.H + h;
-  const int n_out = min(min(max(__ldg(a.cache_len + b), 0), a.Lmax), a.keep);
-  const int lo = static_cast<int>(blockIdx.x) * BLOCK;
-  const int rows = min(BLOCK, n_out - lo);
-  if (rows <= 0) return;
-  __shared__ float smax[8];
-  const int part = threadIdx.x >> 7, tid = threadIdx.x & 127, chunk = (tid & 3) * 16;
-  const float* scale = (part ? a.v_scale : a.k_scale) + bh * a.n_blocks;
-  const int64_t* si = part ? a.sv : a.sk;
-  const uint8_t* in = static_cast<const uint8_t*>(part ? a.Vc : a.Kc) + b * si[0] + h * si[1];
+  const int lo = static_cast<int>(blockIdx.x) * BLOCK, chunk = (tid & 3) * 16;
   const int32_t* kept = a.kept + bh * a.keep + lo;
   int j[kRows];
 #pragma unroll
   for (int k = 0; k < kRows; ++k) {
     const int r = (tid >> 2) + 32 * k;
-    j[k] = r < rows ? kept[r] : -1;
+    j[k] = r < BLOCK && lo + r < a.keep ? kept[r] : -1;
   }
-  uint4 u[kRows];
-  float sc[kRows], most = 0.f;
+  const uint8_t* ki = static_cast<const uint8_t*>(a.Kc) + b * a.sk[0] + h * a.sk[1] + chunk;
+  const uint8_t* vi = static_cast<const uint8_t*>(a.Vc) + b * a.sv[0] + h * a.sv[1] + chunk;
+  uint4 u[2][kRows];
+  float sc[2][kRows], w[kRows];
 #pragma unroll
   for (int k = 0; k < kRows; ++k)
     if (j[k] >= 0) {
-      u[k] = *reinterpret_cast<const uint4*>(in + j[k] * si[2] + chunk);
-      sc[k] = scale[j[k] / BLOCK];
+      u[0][k] = *reinterpret_cast<const uint4*>(ki + j[k] * a.sk[2]);
+      u[1][k] = *reinterpret_cast<const uint4*>(vi + j[k] * a.sv[2]);
+      sc[0][k] = a.k_scale[bh * a.n_blocks + j[k] / BLOCK];
+      sc[1][k] = a.v_scale[bh * a.n_blocks + j[k] / BLOCK];
+      if (chunk == 0) w[k] = a.weights[bh * a.Lmax + j[k]];
     }
-  if (a.weights_out != nullptr && part == 0 && chunk == 0) {
-#pragma unroll
-    for (int k = 0; k < kRows; ++k)
-      if (j[k] >= 0)
-        a.weights_out[bh * a.Lmax_out + lo + (tid >> 2) + 32 * k] = a.weights[bh * a.Lmax + j[k]];
-  }
+  float most[2] = {0.f, 0.f};
 #pragma unroll
   for (int k = 0; k < kRows; ++k)
-    if (j[k] >= 0) most = fmaxf(most, sc[k]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-  if ((threadIdx.x & 31) == 0) smax[threadIdx.x >> 5] = most;
-  __syncthreads();
-  const float now = fmaxf(fmaxf(smax[part * 4], smax[part * 4 + 1]),
-                          fmaxf(smax[part * 4 + 2], smax[part * 4 + 3]));
-  if (tid == 0) (part ? a.v_scale_out : a.k_scale_out)[bh * a.n_blocks_out + blockIdx.x] = now;
-  const int64_t* so = part ? a.svo : a.sko;
-  uint8_t* out = static_cast<uint8_t*>(part ? a.Vo : a.Ko) + b * so[0] + h * so[1] +
-                 static_cast<int64_t>(lo) * so[2] + chunk;
-#pragma unroll
-  for (int k = 0; k < kRows; ++k) {
-    if (j[k] < 0) continue;
-    if (sc[k] < now) {
-      const float ratio = sc[k] / now;  // exact for powers of two
-      u[k] = make_uint4(q8_rescale4<QT>(u[k].x, ratio), q8_rescale4<QT>(u[k].y, ratio),
-                        q8_rescale4<QT>(u[k].z, ratio), q8_rescale4<QT>(u[k].w, ratio));
+    if (j[k] >= 0) {
+      most[0] = fmaxf(most[0], sc[0][k]);
+      most[1] = fmaxf(most[1], sc[1][k]);
     }
-    *reinterpret_cast<uint4*>(out + ((tid >> 2) + 32 * k) * so[2]) = u[k];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    most[0] = fmaxf(most[0], __shfl_xor_sync(0xffffffffu, most[0], o));
+    most[1] = fmaxf(most[1], __shfl_xor_sync(0xffffffffu, most[1], o));
+  }
+  __shared__ float smax[2][4];
+  if ((tid & 31) == 0) {
+    smax[0][tid >> 5] = most[0];
+    smax[1][tid >> 5] = most[1];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const float now =
+        fmaxf(fmaxf(smax[x][0], smax[x][1]), fmaxf(smax[x][2], smax[x][3]));
+    // (a block without rows keeps its scale: the first row belongs to thread 0)
+    if (tid == 0 && j[0] >= 0)
+      (x ? a.v_scale_out : a.k_scale_out)[bh * a.n_blocks_out + blockIdx.x] = now;
+    const int64_t* so = x ? a.svo : a.sko;
+    uint8_t* out = static_cast<uint8_t*>(x ? a.Vo : a.Ko) + b * so[0] + h * so[1] +
+                   static_cast<int64_t>(lo) * so[2] + chunk;
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      if (j[k] < 0) continue;
+      uint4 v = u[x][k];
+      if (sc[x][k] < now) {
+        const float ratio = sc[x][k] / now;  // exact for powers of two
+        v = make_uint4(q8_rescale4<QT>(v.x, ratio), q8_rescale4<QT>(v.y, ratio),
+                       q8_rescale4<QT>(v.z, ratio), q8_rescale4<QT>(v.w, ratio));
+      }
+      *reinterpret_cast<uint4*>(out + ((tid >> 2) + 32 * k) * so[2]) = v;
+    }
+  }
+  if (a.weights_out != nullptr && chunk == 0) {
+#pragma unroll
+    for (int k = 0; k < kRows; ++k)
+      if (j[k] >= 0) a.weights_out[bh * a.Lmax_out + lo + (tid >> 2) + 32 * k] = w[k];
   }
 }
 
