@@ -137,7 +137,7 @@ def test_evict_refusals(lib, kw, code):
 
 
 def test_wrappers_check_shapes_and_types():
-    cpu = torch.device("cpu")
+    cpu = -1
     c = kv_cache_q8(2, 3, 50, 16, torch.int8, device="cpu")
     assert cache_q8._check_cache(c, cpu) == (2, 3, 50, C.MHA_Q8_I8)
     assert c.k_scale.shape == (2, 3, 4) and c.weights.shape == (2, 3, 50)

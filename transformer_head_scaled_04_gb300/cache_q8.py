@@ -4,6 +4,7 @@ and eviction by accumulated weight."""
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple, Optional
 
 import torch
@@ -42,51 +43,68 @@ def kv_cache_q8(B, H, Lmax, block=64, dtype=torch.float8_e4m3fn, weights=True, d
                      torch.zeros((B, H, Lmax), device=device) if weights else None, block)
 
 
+# The calls here are as short as the kernels behind them (a generation step of one sequence takes
+# 5 us on the GPU), so checks and marshalling are written for speed: devices are compared by index,
+# sizes of workspaces are remembered by the numbers they follow from.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+_f32, _i32 = torch.float32, torch.int32
+
+
 def _need(ok, what):
     if not ok:
         raise ValueError(what)
 
 
 def _dense(t, dtype, shape, dev, what):
-    if (t.dtype is not dtype or tuple(t.shape) != shape or not t.is_contiguous()
-            or t.device != dev):
-        raise ValueError(f"{what} must be a contiguous {dtype} tensor {list(shape)} on {dev}")
+    if (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()
+            or t.get_device() != dev):
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor {list(shape)} on the device "
+                         "of the other tensors")
 
 
 def _check_cache(c, dev, what="cache"):
-    """(B, H, Lmax, code type) of a cache whose tensors fit together and live on ``dev``."""
-    if c.k.dtype not in _CODES:
-        raise TypeError(f"{what}: unsupported code dtype {c.k.dtype}; use torch.float8_e4m3fn or "
+    """(B, H, Lmax, code type) of a cache whose tensors fit together and live on device ``dev``
+    (an index, -1 for the host)."""
+    k, v, k_scale, v_scale, weights, block = c
+    code = _CODES.get(k.dtype)
+    if code is None:
+        raise TypeError(f"{what}: unsupported code dtype {k.dtype}; use torch.float8_e4m3fn or "
                         "torch.int8")
-    _need(c.block in _BLOCKS, f"{what}: block must be one of {_BLOCKS}")
-    _need(c.k.dim() == 4 and c.k.shape[3] == 64 and c.v.shape == c.k.shape
-          and c.v.dtype is c.k.dtype and c.k.device == dev and c.v.device == dev,
-          f"{what}: k and v must be [B, H, Lmax, 64] codes of one type on {dev}")
-    B, H, Lmax, _ = c.k.shape
-    nb = (B, H, -(-Lmax // c.block))
-    _dense(c.k_scale, torch.float32, nb, dev, f"{what}.k_scale")
-    _dense(c.v_scale, torch.float32, nb, dev, f"{what}.v_scale")
-    if c.weights is not None:
-        _dense(c.weights, torch.float32, (B, H, Lmax), dev, f"{what}.weights")
-    return B, H, Lmax, _CODES[c.k.dtype]
+    if block not in _BLOCKS:
+        raise ValueError(f"{what}: block must be one of {_BLOCKS}")
+    shape = k.shape
+    if (len(shape) != 4 or shape[3] != 64 or v.shape != shape or v.dtype is not k.dtype
+            or k.get_device() != dev or v.get_device() != dev):
+        raise ValueError(f"{what}: k and v must be [B, H, Lmax, 64] codes of one type on the "
+                         "device of the other tensors")
+    B, H, Lmax, _ = shape
+    nb = (B, H, -(-Lmax // block))
+    _dense(k_scale, _f32, nb, dev, f"{what}.k_scale")
+    _dense(v_scale, _f32, nb, dev, f"{what}.v_scale")
+    if weights is not None:
+        _dense(weights, _f32, (B, H, Lmax), dev, f"{what}.weights")
+    return B, H, Lmax, code
 
 
-def _tensor4(t, like, shape, what):
-    if t.dtype is not like.dtype or t.device != like.device or tuple(t.shape) != shape:
+def _same(t, like, shape, dev, what):
+    if t.dtype is not like.dtype or t.get_device() != dev or t.shape != shape:
         raise ValueError(f"{what} must be a {like.dtype} tensor {list(shape)} on {like.device}")
 
 
 def _cuda_device(t):
-    if not t.is_cuda:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError("tensors must live on a CUDA device")
-    return t.device
+    return dev
 
 
 def _strides(*ts):
     """None where every tensor is contiguous, else their strides as the C ABI takes them."""
-    if all(t.is_contiguous() for t in ts):
-        return None
-    return (ctypes.c_int64 * (4 * len(ts)))(*[x for t in ts for x in t.stride()])
+    for t in ts:
+        if not t.is_contiguous():
+            return (ctypes.c_int64 * (4 * len(ts)))(*[x for t in ts for x in t.stride()])
+    return None
 
 
 def _p(t):
@@ -94,22 +112,24 @@ def _p(t):
 
 
 def _call(dev, name, *args):
-    """The entry point ``name`` on the current stream of ``dev`` (appended to the arguments),
-    with ``dev`` the current device."""
+    """The entry point ``name`` on the current stream of device ``dev`` (appended to the
+    arguments), with ``dev`` the current device."""
     fn = getattr(C.load(), name)
-    if torch.cuda.current_device() == dev.index:
-        code = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if _current_device() == dev:
+        code = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            code = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
-    C.check(code, name)
+            code = fn(*args, _raw_stream(dev))
+    if code:
+        C.check(code, name)
 
 
-def _workspace(workspace, need, dev, what):
+def _workspace(workspace, need, like, dev, what):
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=dev)
-    _need(workspace.dtype is torch.uint8 and workspace.device == dev
-          and workspace.is_contiguous(), f"{what}: workspace must be a uint8 tensor on {dev}")
+        return torch.empty(need, dtype=torch.uint8, device=like.device)
+    _need(workspace.dtype is torch.uint8 and workspace.get_device() == dev
+          and workspace.is_contiguous(),
+          f"{what}: workspace must be a contiguous uint8 tensor on {like.device}")
     return workspace
 
 
@@ -124,18 +144,20 @@ def kv_append_q8(cache, k, v, cache_len, new_len=None):
     dev = _cuda_device(k)
     B, H, Lmax, qt = _check_cache(cache, dev)
     dt = _dt(k)
-    _need(k.dim() == 4 and k.shape[0] == B and k.shape[1] == H and k.shape[3] == 64,
-          f"kv_append_q8: k must be [{B}, {H}, N, 64]")
-    _tensor4(v, k, tuple(k.shape), "kv_append_q8: v")
-    _dense(cache_len, torch.int32, (B,), dev, "cache_len")
+    shape = k.shape
+    if len(shape) != 4 or shape[0] != B or shape[1] != H or shape[3] != 64:
+        raise ValueError(f"kv_append_q8: k must be [{B}, {H}, N, 64]")
+    _same(v, k, shape, dev, "kv_append_q8: v")
+    _dense(cache_len, _i32, (B,), dev, "cache_len")
     if new_len is not None:
-        _dense(new_len, torch.int32, (B,), dev, "new_len")
-    _call(dev, "mha_kv_append_q8", B, H, k.shape[2], Lmax, 64, 64, dt, qt, cache.block,
+        _dense(new_len, _i32, (B,), dev, "new_len")
+    _call(dev, "mha_kv_append_q8", B, H, shape[2], Lmax, 64, 64, dt, qt, cache.block,
           _p(new_len), cache_len.data_ptr(), k.data_ptr(), v.data_ptr(), cache.k.data_ptr(),
           cache.v.data_ptr(), cache.k_scale.data_ptr(), cache.v_scale.data_ptr(),
           _p(cache.weights), _strides(k, v, cache.k, cache.v))
 
 
+@functools.lru_cache(maxsize=1024)
 def decode_q8_workspace_size(B, H, Hkv, Nq, Lmax, with_weights) -> int:
     n = ctypes.c_size_t(0)
     C.check(C.load().mha_decode_q8_workspace_size(B, H, Hkv, Nq, Lmax, int(bool(with_weights)),
@@ -157,21 +179,22 @@ def sdpa_decode_q8(q, cache, cache_len, causal=True, scale=None, add_weights=Fal
     dev = _cuda_device(q)
     Bc, Hkv, Lmax, qt = _check_cache(cache, dev)
     dt = _dt(q)
-    _need(q.dim() == 4 and q.shape[0] == Bc and q.shape[3] == 64 and q.shape[1] % Hkv == 0,
-          f"sdpa_decode_q8: q must be [{Bc}, a multiple of {Hkv}, Nq, 64]")
-    _need(not add_weights or cache.weights is not None,
-          "sdpa_decode_q8: add_weights needs a cache with weights")
-    B, H, Nq, _ = q.shape
-    _dense(cache_len, torch.int32, (B,), dev, "cache_len")
+    shape = q.shape
+    if len(shape) != 4 or shape[0] != Bc or shape[3] != 64 or shape[1] % Hkv != 0:
+        raise ValueError(f"sdpa_decode_q8: q must be [{Bc}, a multiple of {Hkv}, Nq, 64]")
+    if add_weights and cache.weights is None:
+        raise ValueError("sdpa_decode_q8: add_weights needs a cache with weights")
+    B, H, Nq, _ = shape
+    _dense(cache_len, _i32, (B,), dev, "cache_len")
     if out is None:
-        out = torch.empty((B, H, Nq, 64), dtype=q.dtype, device=dev)
+        out = torch.empty(shape, dtype=q.dtype, device=q.device)
     else:
-        _tensor4(out, q, (B, H, Nq, 64), "sdpa_decode_q8: out")
+        _same(out, q, shape, dev, "sdpa_decode_q8: out")
     if workspace is None:
-        workspace = torch.empty(decode_q8_workspace_size(B, H, Hkv, Nq, Lmax, add_weights),
-                                dtype=torch.uint8, device=dev)
+        workspace = torch.empty(decode_q8_workspace_size(B, H, Hkv, Nq, Lmax, bool(add_weights)),
+                                dtype=torch.uint8, device=q.device)
     else:
-        workspace = _workspace(workspace, 0, dev, "sdpa_decode_q8")
+        _workspace(workspace, 0, q, dev, "sdpa_decode_q8")
     _call(dev, "mha_sdpa_decode_q8_fwd", B, H, Hkv, Nq, Lmax, 64, 64, dt, qt, cache.block,
           1 if causal else 0, cache_len.data_ptr(), float(scale or 0.0), q.data_ptr(),
           cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scale.data_ptr(),
@@ -181,6 +204,7 @@ def sdpa_decode_q8(q, cache, cache_len, causal=True, scale=None, add_weights=Fal
     return out
 
 
+@functools.lru_cache(maxsize=1024)
 def key_weights_workspace_size(B, H, Hkv, Nq, Nk, dtype) -> int:
     n = ctypes.c_size_t(0)
     dt = _DTYPES[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
@@ -200,29 +224,32 @@ def sdpa_key_weights(q, k, lse, mask="none", key_len=None, query_len=None, scale
     8-bit cache, say); zeros [B, H, Nk] are made if None.  Returns weights."""
     dev = _cuda_device(q)
     dt = _dt(q)
-    _need(q.dim() == 4 and k.dim() == 4 and q.shape[3] == 64 and k.shape[3] == 64
-          and k.shape[0] == q.shape[0] and q.shape[1] % k.shape[1] == 0
-          and k.dtype is q.dtype and k.device == dev,
-          "sdpa_key_weights: q [B, Hq, Nq, 64] and k [B, H, Nk, 64] of one type on one device "
-          "expected, Hq a multiple of H")
-    B, H, Nq, _ = q.shape
-    Hkv, Nk = k.shape[1], k.shape[2]
-    _dense(lse, torch.float32, (B, H, Nq), dev, "lse")
-    for t, what in ((key_len, "key_len"), (query_len, "query_len")):
-        if t is not None:
-            _dense(t, torch.int32, (B,), dev, what)
+    shape, kshape = q.shape, k.shape
+    if (len(shape) != 4 or len(kshape) != 4 or shape[3] != 64 or kshape[3] != 64
+            or kshape[0] != shape[0] or kshape[1] < 1 or shape[1] % kshape[1] != 0
+            or k.dtype is not q.dtype or k.get_device() != dev):
+        raise ValueError("sdpa_key_weights: q [B, Hq, Nq, 64] and k [B, H, Nk, 64] of one type on "
+                         "one device expected, Hq a multiple of H")
+    B, H, Nq, _ = shape
+    Hkv, Nk = kshape[1], kshape[2]
+    _dense(lse, _f32, (B, H, Nq), dev, "lse")
+    if key_len is not None:
+        _dense(key_len, _i32, (B,), dev, "key_len")
+    if query_len is not None:
+        _dense(query_len, _i32, (B,), dev, "query_len")
     if weights is None:
-        weights = torch.zeros((B, Hkv, Nk), device=dev)
+        weights = torch.zeros((B, Hkv, Nk), device=q.device)
     else:
         _need(weights.dim() == 3 and weights.shape[2] >= Nk,
               f"sdpa_key_weights: weights must be [{B}, {Hkv}, at least {Nk}]")
-        _dense(weights, torch.float32, (B, Hkv, weights.shape[2]), dev, "weights")
+        _dense(weights, _f32, (B, Hkv, weights.shape[2]), dev, "weights")
     need = key_weights_workspace_size(B, H, Hkv, Nq, Nk, dt)
-    workspace = _workspace(workspace, need, dev, "sdpa_key_weights")
+    if need or workspace is not None:
+        workspace = _workspace(workspace, need, q, dev, "sdpa_key_weights")
     _call(dev, "mha_sdpa_key_weights", B, H, Hkv, Nq, Nk, 64, dt, _mask(mask), _p(key_len),
           _p(query_len), float(scale or 0.0), q.data_ptr(), k.data_ptr(), lse.data_ptr(),
-          _strides(q, k), weights.data_ptr(), weights.shape[2], workspace.data_ptr(),
-          workspace.numel())
+          _strides(q, k), weights.data_ptr(), weights.shape[2], _p(workspace),
+          0 if workspace is None else workspace.numel())
     return weights
 
 
@@ -238,19 +265,21 @@ def kv_evict_q8(cache, out, cache_len, keep, recent=0, len_out=None, kept=None):
     dev = _cuda_device(cache.k)
     B, H, Lmax, qt = _check_cache(cache, dev)
     B2, H2, Lout, qt2 = _check_cache(out, dev, "out")
-    _need((B2, H2, qt2, out.block) == (B, H, qt, cache.block),
-          "kv_evict_q8: out must have the batch, heads, code type and block of cache")
-    _need(cache.weights is not None, "kv_evict_q8: the cache keeps no weights to go by")
-    _dense(cache_len, torch.int32, (B,), dev, "cache_len")
+    if (B2, H2, qt2, out.block) != (B, H, qt, cache.block):
+        raise ValueError("kv_evict_q8: out must have the batch, heads, code type and block of cache")
+    if cache.weights is None:
+        raise ValueError("kv_evict_q8: the cache keeps no weights to go by")
+    _dense(cache_len, _i32, (B,), dev, "cache_len")
+    keep = int(keep)
     if len_out is None:
-        len_out = torch.empty(B, dtype=torch.int32, device=dev)
+        len_out = torch.empty(B, dtype=_i32, device=cache.k.device)
     else:
-        _dense(len_out, torch.int32, (B,), dev, "len_out")
+        _dense(len_out, _i32, (B,), dev, "len_out")
     if kept is None:
-        kept = torch.empty((B, H, max(int(keep), 0)), dtype=torch.int32, device=dev)
+        kept = torch.empty((B, H, max(keep, 0)), dtype=_i32, device=cache.k.device)
     else:
-        _dense(kept, torch.int32, (B, H, int(keep)), dev, "kept")
-    _call(dev, "mha_kv_evict_q8", B, H, Lmax, Lout, 64, 64, qt, cache.block, int(keep),
+        _dense(kept, _i32, (B, H, keep), dev, "kept")
+    _call(dev, "mha_kv_evict_q8", B, H, Lmax, Lout, 64, 64, qt, cache.block, keep,
           int(recent), cache_len.data_ptr(), cache.k.data_ptr(), cache.v.data_ptr(),
           cache.k_scale.data_ptr(), cache.v_scale.data_ptr(), cache.weights.data_ptr(),
           out.k.data_ptr(), out.v.data_ptr(), out.k_scale.data_ptr(), out.v_scale.data_ptr(),
