@@ -13,8 +13,10 @@
 // columns each): four summing warps per scheduler.  Where the key tiles alone leave SMs idle the
 // query tiles are split over several CTAs, their sums added by a second launch in a fixed order.
 //
-// fp32 (key_weights_simt_kernel): 32 keys per CTA, each warp taking every eighth query of the
-// group's heads; lane = key, its row in registers, the queries broadcast from shared memory.
+// fp32 (key_weights_simt_kernel): bound by the fp32 units, 64 multiply-adds per pair.  32 keys per
+// CTA, the (head, 32 queries) chunks that see them split over CTAs as above; lane = key, its row in
+// registers, a warp takes four queries of a chunk at once, broadcast from shared memory, while the
+// next chunk is on its way from global memory.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -28,55 +30,89 @@ namespace {
 
 constexpr int kD = 64;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kKeys = 32;     // keys per CTA
-constexpr int kQueries = 32;  // queries staged at a time
-constexpr int kWarps = 8;
+struct KwParams {
+  KeyWeightsArgs a;
+  int split;      // CTAs that share a key tile's queries
+  float* part;    // [split][B * Hkv][Nk] (split > 1)
+  int* status;
+  uint64_t timeout_ns;
+};
 
-__global__ void __launch_bounds__(kWarps * 32) key_weights_simt_kernel(const KeyWeightsArgs a) {
+// ============================================================================ fp32
+constexpr int kKeys = 32;     // keys per CTA
+constexpr int kQueries = 32;  // queries per chunk
+constexpr int kWarps = 8;
+constexpr int kPerWarp = kQueries / kWarps;
+
+__global__ void __launch_bounds__(kWarps * 32, 2) key_weights_simt_kernel(const KwParams p) {
+  const KeyWeightsArgs& a = p.a;
   pdl_launch_dependents();
   pdl_wait();  // the previous kernel's output is complete from here on
   const int g = blockIdx.y, b = blockIdx.z;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int k0 = blockIdx.x * kKeys, j = k0 + lane;
+  const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+  const int z = static_cast<int>(blockIdx.x) % p.split;
+  const int k0 = static_cast<int>(blockIdx.x) / p.split * kKeys, j = k0 + lane;
   const int nk = a.mask == 2 ? min(max(__ldg(a.key_len + b), 0), a.Nk) : a.Nk;
   const int nq = a.query_len != nullptr ? min(max(__ldg(a.query_len + b), 0), a.Nq) : a.Nq;
   if (k0 >= nk) return;
+  const int G = a.H / a.Hkv;
+  const int first = a.mask == 1 ? k0 : 0;  // queries before the first key see none of these
+  const int per_head = nq > first ? (nq - first + kQueries - 1) / kQueries : 0;
+  const int64_t all = static_cast<int64_t>(G) * per_head;
+  const int u0 = static_cast<int>(all * z / p.split);
+  const int u1 = static_cast<int>(all * (z + 1) / p.split);
   __shared__ float4 sq[kQueries][kD / 4];
   __shared__ float slse[kQueries];
   __shared__ float part[kWarps][kKeys];
-  float k[kD];
-  const float* kr = static_cast<const float*>(a.K) + b * a.sk[0] + g * a.sk[1] + min(j, nk - 1) * a.sk[2];
+  float4 k[kD / 4];
+  const float4* kr = reinterpret_cast<const float4*>(
+      static_cast<const float*>(a.K) + b * a.sk[0] + g * a.sk[1] + min(j, nk - 1) * a.sk[2]);
 #pragma unroll
-  for (int d = 0; d < kD; ++d) k[d] = kr[d];
-  const int G = a.H / a.Hkv;
+  for (int d = 0; d < kD / 4; ++d) k[d] = kr[d];
   const float c = a.scale * kLog2e;
-  const int first = a.mask == 1 ? k0 : 0;  // queries before the first key see none of these
-  float sum = 0.f;
-  for (int h = g * G; h < (g + 1) * G; ++h) {
+  // a chunk: two 16-byte pieces of the queries and, 32 threads, an lse each
+  float4 next[2];
+  float next_lse = 0.f;
+  auto load = [&](int u) {
+    const int h = g * G + u / per_head, i0 = first + u % per_head * kQueries;
     const float* q = static_cast<const float*>(a.Q) + b * a.sq[0] + h * a.sq[1];
-    const float* lse = a.lse + (static_cast<int64_t>(b) * a.H + h) * a.Nq;
-    for (int i0 = first; i0 < nq; i0 += kQueries) {
-      __syncthreads();
-      for (int t = tid; t < kQueries * kD; t += kWarps * 32) {
-        const int i = i0 + t / kD;
-        reinterpret_cast<float*>(sq)[t] = i < nq ? q[i * a.sq[2] + t % kD] : 0.f;
-      }
-      if (tid < kQueries)  // +inf (a row without keys, or none at all): every weight 0
-        slse[tid] = i0 + tid < nq ? lse[i0 + tid] * kLog2e : INFINITY;
-      __syncthreads();
-      for (int t = warp; t < kQueries && i0 + t < nq; t += kWarps) {
-        float s = 0.f;
 #pragma unroll
-        for (int d = 0; d < kD / 4; ++d) {
-          const float4 v = sq[t][d];
-          s = fmaf(v.x, k[4 * d], s);
-          s = fmaf(v.y, k[4 * d + 1], s);
-          s = fmaf(v.z, k[4 * d + 2], s);
-          s = fmaf(v.w, k[4 * d + 3], s);
-        }
-        const float l2 = slse[t];
-        if (l2 != INFINITY && (a.mask != 1 || j <= i0 + t)) sum += exp2f(fmaf(s, c, -l2));
+    for (int x = 0; x < 2; ++x) {
+      const int t = tid + x * kWarps * 32, i = i0 + t / (kD / 4);
+      next[x] = i < nq ? reinterpret_cast<const float4*>(q + i * a.sq[2])[t % (kD / 4)]
+                       : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    if (tid < kQueries)  // +inf (a row without keys, or none at all): no weight
+      next_lse = i0 + tid < nq
+                     ? a.lse[(static_cast<int64_t>(b) * a.H + h) * a.Nq + i0 + tid] * kLog2e
+                     : INFINITY;
+  };
+  if (u0 < u1) load(u0);
+  float sum = 0.f;
+  for (int u = u0; u < u1; ++u) {
+    const int i0 = first + u % per_head * kQueries;
+    __syncthreads();  // all have read the chunk before
+#pragma unroll
+    for (int x = 0; x < 2; ++x) (&sq[0][0])[tid + x * kWarps * 32] = next[x];
+    if (tid < kQueries) slse[tid] = next_lse;
+    __syncthreads();
+    if (u + 1 < u1) load(u + 1);
+    float2 s[kPerWarp];
+#pragma unroll
+    for (int t = 0; t < kPerWarp; ++t) s[t] = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int d = 0; d < kD / 4; ++d)
+#pragma unroll
+      for (int t = 0; t < kPerWarp; ++t) {
+        const float4 v = sq[warp + t * kWarps][d];
+        s[t] = ffma2(make_float2(v.x, v.y), make_float2(k[d].x, k[d].y), s[t]);
+        s[t] = ffma2(make_float2(v.z, v.w), make_float2(k[d].z, k[d].w), s[t]);
       }
+#pragma unroll
+    for (int t = 0; t < kPerWarp; ++t) {
+      const int i = i0 + warp + t * kWarps;
+      const float l2 = slse[warp + t * kWarps];
+      if (l2 != INFINITY && (a.mask != 1 || j <= i)) sum += exp2f(fmaf(s[t].x + s[t].y, c, -l2));
     }
   }
   part[warp][lane] = sum;
@@ -85,7 +121,11 @@ __global__ void __launch_bounds__(kWarps * 32) key_weights_simt_kernel(const Key
     float s = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) s += part[w][lane];
-    a.weights[(static_cast<int64_t>(b) * a.Hkv + g) * a.ld + j] += s;
+    const int64_t bg = static_cast<int64_t>(b) * a.Hkv + g;
+    if (p.split == 1)
+      a.weights[bg * a.ld + j] += s;
+    else
+      p.part[(static_cast<int64_t>(z) * a.B * a.Hkv + bg) * a.Nk + j] = s;
   }
 }
 
@@ -105,14 +145,6 @@ constexpr int kOffBar = kOffLse + kStages * kT * 4;
 constexpr int kBarK = 0, kBarQ = 1, kBarQFree = kBarQ + kStages, kBarS = kBarQFree + kStages,
               kBarSFree = kBarS + 2, kBarDrain = kBarSFree + 2, kNumBars = kBarDrain + 1;
 constexpr int kTcSmem = 1024 + kOffBar + kNumBars * 8 + 16;
-
-struct TcParams {
-  KeyWeightsArgs a;
-  int split;      // CTAs that share a key tile's query tiles
-  float* part;    // [split][B * Hkv][Nk] (split > 1)
-  int* status;
-  uint64_t timeout_ns;
-};
 
 __device__ __forceinline__ bool warp_all(bool v) { return __all_sync(0xffffffffu, v); }
 
@@ -142,7 +174,7 @@ __device__ __forceinline__ void exclude(uint32_t (&s)[32], int first, int last) 
 
 __global__ void __launch_bounds__(kTcThreads, 2)
     key_weights_bf16_kernel(const __grid_constant__ CUtensorMap tmQ,
-                            const __grid_constant__ CUtensorMap tmK, const TcParams p) {
+                            const __grid_constant__ CUtensorMap tmK, const KwParams p) {
   const KeyWeightsArgs& a = p.a;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_smem_1024(smem_raw);
@@ -374,7 +406,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
 }
 
 // weights += the shares' sums, in order
-__global__ void __launch_bounds__(256) key_weights_add_kernel(const TcParams p) {
+__global__ void __launch_bounds__(256) key_weights_add_kernel(const KwParams p) {
   const KeyWeightsArgs& a = p.a;
   pdl_launch_dependents();
   pdl_wait();  // the shares are complete from here on
@@ -387,42 +419,47 @@ __global__ void __launch_bounds__(256) key_weights_add_kernel(const TcParams p) 
   a.weights[static_cast<int64_t>(bg) * a.ld + j] += s;
 }
 
-// CTAs per key tile: enough for two on each of 152 SMs, no more than there are query tiles
-int key_weights_split(int B, int H, int Hkv, int Nq, int Nk) {
-  const int64_t units = static_cast<int64_t>(B) * Hkv * ((Nk + kT - 1) / kT);
-  const int64_t queries = static_cast<int64_t>(H / Hkv) * ((Nq + kT - 1) / kT);
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(queries, 304 / units)));
+// CTAs per key tile: enough for two on each of 152 SMs (fp32: twice that, for shorter CTAs), no
+// more than there are query tiles
+int key_weights_split(int B, int H, int Hkv, int Nq, int Nk, int dtype) {
+  const int keys = dtype == 1 ? kT : kKeys, rows = dtype == 1 ? kT : kQueries;
+  const int64_t units = static_cast<int64_t>(B) * Hkv * ((Nk + keys - 1) / keys);
+  const int64_t queries = static_cast<int64_t>(H / Hkv) * ((Nq + rows - 1) / rows);
+  const int64_t want = dtype == 1 ? 304 : 608;
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(queries, want / units)));
 }
 
 }  // namespace
 
 size_t key_weights_workspace(int B, int H, int Hkv, int Nq, int Nk, int dtype) {
-  if (dtype != 1) return 0;
-  const int split = key_weights_split(B, H, Hkv, Nq, Nk);
+  const int split = key_weights_split(B, H, Hkv, Nq, Nk, dtype);
   return split == 1 ? 0 : static_cast<size_t>(split) * B * Hkv * Nk * sizeof(float);
 }
 
 cudaError_t launch_key_weights(const KeyWeightsArgs& a, int dtype, void* ws, const DevCtx& ctx,
                                cudaStream_t s) {
-  if (dtype != 1)
-    return launch_pdl(key_weights_simt_kernel, dim3((a.Nk + kKeys - 1) / kKeys, a.Hkv, a.B),
-                      dim3(kWarps * 32), 0, s, a);
-  CUtensorMap tq, tk;
-  if (!encode_map_bf16(&tq, a.Q, a.B, a.H, a.Nq, a.sq, kT) ||
-      !encode_map_bf16(&tk, a.K, a.B, a.Hkv, a.Nk, a.sk, kT))
-    return cudaErrorInvalidValue;
-  cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(key_weights_bf16_kernel), kTcSmem,
-                                 nullptr);
-  if (e != cudaSuccess) return e;
-  TcParams p;
+  KwParams p;
   p.a = a;
-  p.split = key_weights_split(a.B, a.H, a.Hkv, a.Nq, a.Nk);
+  p.split = key_weights_split(a.B, a.H, a.Hkv, a.Nq, a.Nk, dtype);
   p.part = static_cast<float*>(ws);
   p.status = ctx.status;
   p.timeout_ns = ctx.timeout_ns;
-  const int units = a.B * a.Hkv * ((a.Nk + kT - 1) / kT);
-  e = launch_pdl(key_weights_bf16_kernel, dim3(units * p.split), dim3(kTcThreads), kTcSmem, s, tq,
-                 tk, p);
+  cudaError_t e;
+  if (dtype != 1) {
+    e = launch_pdl(key_weights_simt_kernel,
+                   dim3((a.Nk + kKeys - 1) / kKeys * p.split, a.Hkv, a.B), dim3(kWarps * 32), 0, s,
+                   p);
+  } else {
+    CUtensorMap tq, tk;
+    if (!encode_map_bf16(&tq, a.Q, a.B, a.H, a.Nq, a.sq, kT) ||
+        !encode_map_bf16(&tk, a.K, a.B, a.Hkv, a.Nk, a.sk, kT))
+      return cudaErrorInvalidValue;
+    e = prepare_kernel(reinterpret_cast<const void*>(key_weights_bf16_kernel), kTcSmem, nullptr);
+    if (e != cudaSuccess) return e;
+    const int units = a.B * a.Hkv * ((a.Nk + kT - 1) / kT);
+    e = launch_pdl(key_weights_bf16_kernel, dim3(units * p.split), dim3(kTcThreads), kTcSmem, s,
+                   tq, tk, p);
+  }
   if (e != cudaSuccess || p.split == 1) return e;
   return launch_pdl(key_weights_add_kernel, dim3((a.Nk + 255) / 256, a.B * a.Hkv), dim3(256), 0, s,
                     p);
