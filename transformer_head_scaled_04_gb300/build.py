@@ -28,7 +28,8 @@ SOURCES = ["capi.cu", "gemm_bf16.cu", "gemm_f32.cu", "sdpa_bf16.cu", "sdpa_f32.c
            "layer_noalloc.cu", "layer_host.cu",
            "capi_q8.cu", "kv_append_q8.cu", "sdpa_decode_q8.cu", "sdpa_key_weights.cu",
            "kv_evict_q8.cu"]
-HEADERS = ["device_common.cuh", "launchers.h", "nvtx_range.h", "q8_common.cuh"]
+HEADERS = ["device_common.cuh", "launchers.h", "mma_f16.cuh", "nvtx_range.h",
+           "q8_common.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

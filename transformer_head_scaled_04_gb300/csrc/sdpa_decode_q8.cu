@@ -41,6 +41,7 @@
 #include <type_traits>
 
 #include "launchers.h"
+#include "mma_f16.cuh"
 #include "q8_common.cuh"
 
 namespace mha {
@@ -151,25 +152,6 @@ __device__ __forceinline__ uint32_t tiles_before(const Line& n, const DecodeQ8Ar
   return base + (b == x0 ? 0 : up);
 }
 
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9},"
-      " {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// the same onto zeros
-__device__ __forceinline__ void mma16816_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                              uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9},"
-      " {%10,%10,%10,%10};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
-}
-
 // 16 bytes from global to shared memory, past L1; a lane's copies complete in groups.  `policy`:
 // the cache streams through L2 and is the first to leave it, so that the scores and pieces that
 // the join reads stay there (64 x 16 heads x 4096 positions 87.3 -> 84.8 us, with weights 106.8
@@ -211,16 +193,6 @@ __device__ __forceinline__ void codes_to_half(uint32_t u, uint32_t& h0, uint32_t
     h1 = *reinterpret_cast<uint32_t*>(&q);
   }
 }
-__device__ __forceinline__ uint32_t pack_half(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-// what fp16 rounding left of a and b, rounded to fp16
-__device__ __forceinline__ uint32_t pack_rest(float a, float b, uint32_t hi) {
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-  return pack_half(a - f.x, b - f.y);
-}
-
 __device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&f)[16]) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {

@@ -13,17 +13,24 @@
 // columns each): four summing warps per scheduler.  Where the key tiles alone leave SMs idle the
 // query tiles are split over several CTAs, their sums added by a second launch in a fixed order.
 //
-// fp32 (key_weights_simt_kernel): bound by the fp32 units, 64 multiply-adds per pair.  32 keys per
-// CTA, the (head, 32 queries) chunks that see them split over CTAs as above; lane = key, its row in
-// registers, a warp takes four queries of a chunk at once, broadcast from shared memory, while the
-// next chunk is on its way from global memory.
+// fp32 (key_weights_f32_kernel): the same sums with mma.sync m16n8k16.  Rows of Q and K are scaled
+// by a power of two (largest value to [2^13, 2^14)) and split into two fp16 terms, 22 bits; three
+// products (hi hi, hi lo, lo hi) give S = K Q^T, the four inner steps apart and added in fp32, as
+// the tensor cores' own accumulation truncates.  One CTA per 128 keys, 16 to a warp with their
+// terms in registers; chunks of 32 queries are split into terms once per CTA, in shared memory,
+// the next chunk on its way from global memory meanwhile.  The (head, chunk) pairs are split over
+// CTAs as above.  8 heads x 8 padded prompts of up to 1000 take 59 us, a causal prompt of 1024 23 us;
+// with one fp32 multiply-add per term and lane = key, whose operands came from shared memory at a
+// quarter of the units' rate, 156 and 58 us.  Bound by the products and their scaling: each score
+// costs three products of 64 terms, its four parts' sum and one exponential.
 #include <cuda_bf16.h>
 
 #include <algorithm>
 #include <type_traits>
 
-#include "launchers.h"
 #include "device_common.cuh"
+#include "launchers.h"
+#include "mma_f16.cuh"
 
 namespace mha {
 namespace {
@@ -39,19 +46,26 @@ struct KwParams {
 };
 
 // ============================================================================ fp32
-constexpr int kKeys = 32;     // keys per CTA
+constexpr int kKeys = 128;    // keys per CTA
 constexpr int kQueries = 32;  // queries per chunk
 constexpr int kWarps = 8;
-constexpr int kPerWarp = kQueries / kWarps;
+static_assert(kKeys == 16 * kWarps && kWarps * 32 == 8 * kQueries, "a key tile per warp, eight threads to a query");
 
-__global__ void __launch_bounds__(kWarps * 32, 2) key_weights_simt_kernel(const KwParams p) {
+// the power of two that brings a row's largest magnitude to [2^13, 2^14), and its inverse
+__device__ __forceinline__ float2 row_scale(float amax) {
+  const int ex = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -60);
+  return make_float2(__uint_as_float((13 - ex + 127) << 23), __uint_as_float((ex - 13 + 127) << 23));
+}
+
+__global__ void __launch_bounds__(kWarps * 32, 2) key_weights_f32_kernel(const KwParams p) {
   const KeyWeightsArgs& a = p.a;
   pdl_launch_dependents();
   pdl_wait();  // the previous kernel's output is complete from here on
   const int g = blockIdx.y, b = blockIdx.z;
   const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+  const int r = lane >> 2, t = lane & 3;  // fragment row (or column) and place in it
   const int z = static_cast<int>(blockIdx.x) % p.split;
-  const int k0 = static_cast<int>(blockIdx.x) / p.split * kKeys, j = k0 + lane;
+  const int k0 = static_cast<int>(blockIdx.x) / p.split * kKeys;
   const int nk = a.mask == 2 ? min(max(__ldg(a.key_len + b), 0), a.Nk) : a.Nk;
   const int nq = a.query_len != nullptr ? min(max(__ldg(a.query_len + b), 0), a.Nq) : a.Nq;
   if (k0 >= nk) return;
@@ -61,71 +75,146 @@ __global__ void __launch_bounds__(kWarps * 32, 2) key_weights_simt_kernel(const 
   const int64_t all = static_cast<int64_t>(G) * per_head;
   const int u0 = static_cast<int>(all * z / p.split);
   const int u1 = static_cast<int>(all * (z + 1) / p.split);
-  __shared__ float4 sq[kQueries][kD / 4];
-  __shared__ float slse[kQueries];
-  __shared__ float part[kWarps][kKeys];
-  float4 k[kD / 4];
-  const float4* kr = reinterpret_cast<const float4*>(
-      static_cast<const float*>(a.K) + b * a.sk[0] + g * a.sk[1] + min(j, nk - 1) * a.sk[2]);
-#pragma unroll
-  for (int d = 0; d < kD / 4; ++d) k[d] = kr[d];
+
+  // queries of a chunk, two terms, 16-byte piece i of row q stored at i ^ (q & 7); their scales
+  // and lse log2 e
+  __shared__ uint4 s_hi[2][kQueries][8], s_lo[2][kQueries][8];
+  __shared__ float s_scale[2][kQueries], s_lse[2][kQueries];
+
+  // this warp's keys: rows r and r + 8 of 16; lane t holds values 16t.. of a row, inner step k the
+  // four from 16t + 4k on
+  uint32_t khi[4][4], klo[4][4];
+  float kscale[2];
   const float c = a.scale * kLog2e;
-  // a chunk: two 16-byte pieces of the queries and, 32 threads, an lse each
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int j = min(k0 + warp * 16 + e * 8 + r, nk - 1);
+    const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(a.K) +
+                                                        b * a.sk[0] + g * a.sk[1] + j * a.sk[2]) +
+                        t * 4;
+    float f[16], amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 v = src[i];
+      f[4 * i] = v.x;
+      f[4 * i + 1] = v.y;
+      f[4 * i + 2] = v.z;
+      f[4 * i + 3] = v.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(f[i]));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    const float2 sc = row_scale(amax);
+    kscale[e] = sc.y * c;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float u = f[4 * k + 2 * x] * sc.x, v = f[4 * k + 2 * x + 1] * sc.x;
+        khi[k][2 * x + e] = pack_half(u, v);
+        klo[k][2 * x + e] = pack_rest(u, v, khi[k][2 * x + e]);
+      }
+  }
+
+  // a thread's part of a chunk: values 8 (tid % 8).. of query tid / 8
   float4 next[2];
   float next_lse = 0.f;
   auto load = [&](int u) {
-    const int h = g * G + u / per_head, i0 = first + u % per_head * kQueries;
-    const float* q = static_cast<const float*>(a.Q) + b * a.sq[0] + h * a.sq[1];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int t = tid + x * kWarps * 32, i = i0 + t / (kD / 4);
-      next[x] = i < nq ? reinterpret_cast<const float4*>(q + i * a.sq[2])[t % (kD / 4)]
-                       : make_float4(0.f, 0.f, 0.f, 0.f);
+    const int h = g * G + u / per_head, i = first + u % per_head * kQueries + (tid >> 3);
+    next[0] = next[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+    next_lse = INFINITY;  // a row that does not count
+    if (i < nq) {
+      const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(a.Q) +
+                                                        b * a.sq[0] + h * a.sq[1] + i * a.sq[2]);
+      next[0] = q[(tid & 7) * 2];
+      next[1] = q[(tid & 7) * 2 + 1];
+      next_lse = a.lse[(static_cast<int64_t>(b) * a.H + h) * a.Nq + i];
     }
-    if (tid < kQueries)  // +inf (a row without keys, or none at all): no weight
-      next_lse = i0 + tid < nq
-                     ? a.lse[(static_cast<int64_t>(b) * a.H + h) * a.Nq + i0 + tid] * kLog2e
-                     : INFINITY;
   };
-  if (u0 < u1) load(u0);
-  float sum = 0.f;
-  for (int u = u0; u < u1; ++u) {
+  auto store = [&](int buf) {
+    const float f[8] = {next[0].x, next[0].y, next[0].z, next[0].w,
+                        next[1].x, next[1].y, next[1].z, next[1].w};
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[i]));
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const float2 sc = row_scale(amax);
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float u = f[2 * i] * sc.x, v = f[2 * i + 1] * sc.x;
+      hi[i] = pack_half(u, v);
+      lo[i] = pack_rest(u, v, hi[i]);
+    }
+    const int q = tid >> 3, at = (tid & 7) ^ (q & 7);
+    s_hi[buf][q][at] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    s_lo[buf][q][at] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    if ((tid & 7) == 0) {
+      s_scale[buf][q] = sc.y;
+      s_lse[buf][q] = next_lse * kLog2e;
+    }
+  };
+  if (u0 < u1) {
+    load(u0);
+    store(0);
+  }
+  __syncthreads();
+  float sum[2] = {0.f, 0.f};
+  for (int u = u0, buf = 0; u < u1; ++u, buf ^= 1) {
     const int i0 = first + u % per_head * kQueries;
-    __syncthreads();  // all have read the chunk before
-#pragma unroll
-    for (int x = 0; x < 2; ++x) (&sq[0][0])[tid + x * kWarps * 32] = next[x];
-    if (tid < kQueries) slse[tid] = next_lse;
-    __syncthreads();
     if (u + 1 < u1) load(u + 1);
-    float2 s[kPerWarp];
 #pragma unroll
-    for (int t = 0; t < kPerWarp; ++t) s[t] = make_float2(0.f, 0.f);
+    for (int n = 0; n < kQueries / 8; ++n) {  // queries 8n + r as the product's columns
+      uint32_t qh[8], ql[8];
 #pragma unroll
-    for (int d = 0; d < kD / 4; ++d)
+      for (int x = 0; x < 2; ++x) {
+        const uint4 v = s_hi[buf][8 * n + r][(2 * t + x) ^ r];
+        const uint4 w = s_lo[buf][8 * n + r][(2 * t + x) ^ r];
+        qh[4 * x] = v.x, qh[4 * x + 1] = v.y, qh[4 * x + 2] = v.z, qh[4 * x + 3] = v.w;
+        ql[4 * x] = w.x, ql[4 * x + 1] = w.y, ql[4 * x + 2] = w.z, ql[4 * x + 3] = w.w;
+      }
+      float part[4][4];
 #pragma unroll
-      for (int t = 0; t < kPerWarp; ++t) {
-        const float4 v = sq[warp + t * kWarps][d];
-        s[t] = ffma2(make_float2(v.x, v.y), make_float2(k[d].x, k[d].y), s[t]);
-        s[t] = ffma2(make_float2(v.z, v.w), make_float2(k[d].z, k[d].w), s[t]);
+      for (int k = 0; k < 4; ++k) {
+        mma16816_zero(part[k], klo[k], qh[2 * k], qh[2 * k + 1]);
+        mma16816(part[k], khi[k], ql[2 * k], ql[2 * k + 1]);
+        mma16816(part[k], khi[k], qh[2 * k], qh[2 * k + 1]);
       }
 #pragma unroll
-    for (int t = 0; t < kPerWarp; ++t) {
-      const int i = i0 + warp + t * kWarps;
-      const float l2 = slse[warp + t * kWarps];
-      if (l2 != INFINITY && (a.mask != 1 || j <= i)) sum += exp2f(fmaf(s[t].x + s[t].y, c, -l2));
-    }
-  }
-  part[warp][lane] = sum;
-  __syncthreads();
-  if (warp == 0 && j < nk) {
-    float s = 0.f;
+      for (int e = 0; e < 2; ++e) {  // queries 8n + 2t + e, keys r and r + 8
+        const int q = 8 * n + 2 * t + e;
+        const float l2 = s_lse[buf][q], qs = s_scale[buf][q];
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) s += part[w][lane];
+        for (int x = 0; x < 2; ++x) {
+          const int i = 2 * x + e;
+          const float s = (part[0][i] + part[1][i]) + (part[2][i] + part[3][i]);
+          const bool counts =
+              l2 != INFINITY && (a.mask != 1 || k0 + warp * 16 + x * 8 + r <= i0 + q);
+          if (counts) sum[x] += exp2f(fmaf(s, qs * kscale[x], -l2));
+        }
+      }
+    }
+    if (u + 1 < u1) store(buf ^ 1);
+    __syncthreads();
+  }
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {  // over the lanes that had other queries of the key
+    sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 1);
+    sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 2);
+  }
+  if (t == 0) {
     const int64_t bg = static_cast<int64_t>(b) * a.Hkv + g;
-    if (p.split == 1)
-      a.weights[bg * a.ld + j] += s;
-    else
-      p.part[(static_cast<int64_t>(z) * a.B * a.Hkv + bg) * a.Nk + j] = s;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int j = k0 + warp * 16 + x * 8 + r;
+      if (j >= nk) continue;
+      if (p.split == 1)
+        a.weights[bg * a.ld + j] += sum[x];
+      else
+        p.part[(static_cast<int64_t>(z) * a.B * a.Hkv + bg) * a.Nk + j] = sum[x];
+    }
   }
 }
 
@@ -420,7 +509,7 @@ __global__ void __launch_bounds__(256) key_weights_add_kernel(const KwParams p) 
 }
 
 // CTAs per key tile: enough for two on each of 152 SMs (fp32: twice that, for shorter CTAs), no
-// more than there are query tiles
+// more than there are query tiles or chunks
 int key_weights_split(int B, int H, int Hkv, int Nq, int Nk, int dtype) {
   const int keys = dtype == 1 ? kT : kKeys, rows = dtype == 1 ? kT : kQueries;
   const int64_t units = static_cast<int64_t>(B) * Hkv * ((Nk + keys - 1) / keys);
@@ -446,7 +535,7 @@ cudaError_t launch_key_weights(const KeyWeightsArgs& a, int dtype, void* ws, con
   p.timeout_ns = ctx.timeout_ns;
   cudaError_t e;
   if (dtype != 1) {
-    e = launch_pdl(key_weights_simt_kernel,
+    e = launch_pdl(key_weights_f32_kernel,
                    dim3((a.Nk + kKeys - 1) / kKeys * p.split, a.Hkv, a.B), dim3(kWarps * 32), 0, s,
                    p);
   } else {
