@@ -214,7 +214,8 @@ typedef enum { MHA_Q8_E4M3 = 0, MHA_Q8_I8 = 1 } mha_q8;
  *   block holds earlier positions its scale never falls: if the new tokens need a larger one,
  *   the earlier codes are written again under it (rounded from the codes, not from the values
  *   they came from).  Infinities saturate and do not enter the scale; a NaN is stored as NaN
- *   (e4m3) or 0 (integers).
+ *   (e4m3) or 0 (integers).  Scales that are there already must be positive; under one that is
+ *   not a power of two, x * (1 / scale), the inverse rounded to fp32, is what is rounded.
  *   K, V [B,H,N,64] (dtype); new_len int32[B], clamped to [0, N], or NULL (every sequence gets
  *   N); cache_len int32[B], the positions there already, clamped to [0, Lmax]; the caller adds
  *   the new ones to it afterwards.  Tokens past Lmax are dropped.  weights of the new positions
@@ -241,8 +242,9 @@ int mha_decode_q8_workspace_size(int B, int H, int Hkv, int Nq, int Lmax, int wi
  *     weights[b,g,j] += sum over the query heads of group g and i of p_ij     (unless NULL)
  *   Q [B,H,Nq,64], O [B,H,Nq,64] (dtype); caches and scales with Hkv heads, H a multiple of
  *   Hkv.  cache_len, causal, scale and rows without an allowed key (zeros, no weight) as for
- *   mha_sdpa_decode_fwd; 1 <= Nq <= 16, Nq <= Lmax, H / Hkv * Nq <= 4096.  Positions past cache_len may hold
- *   anything.  Scales must be positive and within [2^-40, 2^40]; they need not be powers of two.
+ *   mha_sdpa_decode_fwd; 1 <= Nq <= 16, Nq <= Lmax, H / Hkv * Nq <= 4096.  Positions past
+ *   cache_len may hold anything.  Scales must be positive and within [2^-40, 2^40]; they need
+ *   not be powers of two.
  *   strides: NULL for contiguous, or 16 strides {Q, K, V, O} x {b, h, n, d} (Q, O in elements
  *   as for mha_kv_append_q8's K).  O may not alias an input.
  *   workspace: mha_decode_q8_workspace_size() bytes, 256-byte aligned; calls that may run at
@@ -267,7 +269,7 @@ int mha_key_weights_workspace_size(int B, int H, int Hkv, int Nq, int Nk, int dt
  *     weights[b,g,j] += sum over the query heads h of group g and i of
  *                       exp(Q[b,h,i] . K[b,g,j] * scale - lse[b,h,i])          (allowed pairs)
  *   Q [B,H,Nq,64], K [B,Hkv,Nk,64] (dtype, the values before quantisation), lse fp32 [B,H,Nq]
- *   contiguous (rows with +inf add nothing).  mask, key_len, scale as for mha_sdpa_fwd;
+ *   contiguous (rows with +inf, whose Q must be finite, add nothing).  mask, key_len, scale as for mha_sdpa_fwd;
  *   query_len int32[B], clamped to [0, Nq], or NULL: rows i >= query_len[b] of a padded batch
  *   add nothing and may hold anything.  Keys j >= key_len[b] keep their weights.
  *   weights [B, Hkv, weights_ld], weights_ld >= Nk: only the first Nk of each head change.

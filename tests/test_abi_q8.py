@@ -89,11 +89,19 @@ def test_workspace_sizes(lib):
     assert size(64, 16, 5, 1, 4096, 1, ctypes.byref(n)) == INVALID
     assert size(64, 16, 16, 1, 4096, 2, ctypes.byref(n)) == INVALID
     assert size(64, 16, 16, 17, 4096, 1, ctypes.byref(n)) == UNSUPPORTED
+    assert size(1, 256, 1, 16, 4096, 1, ctypes.byref(n)) == 0
+    assert size(1, 257, 1, 16, 4096, 1, ctypes.byref(n)) == UNSUPPORTED      # rows of a head
+    assert size(1, 1, 1, 1, (1 << 30) + 1, 0, ctypes.byref(n)) == UNSUPPORTED
+    assert size(65535, 65535, 65535, 1, 16, 0, ctypes.byref(n)) == UNSUPPORTED  # rows of a batch
+    assert size(64, 64, 64, 1, 1 << 30, 0, ctypes.byref(n)) == UNSUPPORTED   # tiles of a batch
     size = lib.mha_key_weights_workspace_size
     assert size(8, 16, 16, 4096, 4096, 1, ctypes.byref(n)) == 0 and n.value % 256 == 0
     assert size(8, 16, 16, 4096, 4096, 1, None) == INVALID
     assert size(8, 16, 3, 4096, 4096, 1, ctypes.byref(n)) == INVALID
     assert size(8, 16, 16, 4096, 4096, 2, ctypes.byref(n)) == INVALID
+    assert size(65536, 1, 1, 1, 1, 1, ctypes.byref(n)) == UNSUPPORTED        # heads of a batch
+    assert size(60000, 1, 1, 1, 1 << 30, 1, ctypes.byref(n)) == UNSUPPORTED  # key tiles
+    assert size(1, 65535, 1, 1 << 30, 1, 0, ctypes.byref(n)) == UNSUPPORTED  # query tiles of a head
 
 
 def keyw(lib, B=1, H=4, Hkv=2, Nq=8, Nk=8, dk=64, dt=1, mask=0, kl=None, ql=None, scale=0.0,
@@ -128,7 +136,8 @@ def evict(lib, B=1, H=1, Lmax=64, Lout=32, dk=64, dv=64, qt=0, block=16, keep=20
     (dict(kept=None), INVALID), (dict(n=None), INVALID), (dict(ko=None), INVALID),
     (dict(ko=at(2)), INVALID), (dict(vo=at(7)), INVALID), (dict(n=at(1)), INVALID),
     (dict(wo=at(6)), INVALID), (dict(vso=at(5)), INVALID), (dict(dk=32), UNSUPPORTED),
-    (dict(block=20), UNSUPPORTED), (dict(H=65536), UNSUPPORTED), (dict(vo=EIGHT), ALIGN),
+    (dict(block=20), UNSUPPORTED), (dict(H=65536), UNSUPPORTED), (dict(B=65535, H=65535), UNSUPPORTED),
+    (dict(vo=EIGHT), ALIGN),
     (dict(kept=ODD), ALIGN), (dict(st=strides(4, _8=-16)), INVALID),
     (dict(st=strides(4, _11=0)), UNSUPPORTED), (dict(st=strides(4, _14=8)), ALIGN),
 ])

@@ -197,6 +197,10 @@ DECODE = [  # B, H, Hkv, Nq, Lmax, block, dtype, code, causal, cache_len
     (2, 5, 5, 7, 197, 16, "bf16", "int8", False, [-4, 190]),
     (1, 8, 1, 3, 5000, 64, "bf16", "int8", True, [4999]),              # one long head
     (70, 3, 3, 1, 40, 16, "f32", "int8", True, [i % 41 for i in range(70)]),
+    (1, 64, 4, 16, 300, 16, "f32", "e4m3", True, [300]),               # 256 rows
+    (1, 256, 1, 16, 40, 16, "bf16", "int8", False, [40]),              # 4096 rows, the most
+    (8, 40, 40, 1, 4100, 64, "bf16", "e4m3", True, [4100, 0, 4096, 4097, 1, 33, 2048, 777]),
+    (2, 320, 80, 1, 2100, 32, "f32", "int8", True, [2100, 1025]),
 ]
 
 
@@ -331,6 +335,11 @@ KEYW = [  # B, H, Hkv, Nq, Nk, dtype, mask, key_len, query_len
     (2, 2, 2, 65, 33, "f32", "key_padding", [33, 31], None),
     (1, 3, 3, 300, 40, "f32", "none", None, None),
     (2, 1, 1, 1, 500, "bf16", "none", None, None),
+    (1, 4, 2, 1500, 1500, "bf16", "causal", None, [1400]),             # queries split over CTAs
+    (160, 2, 2, 130, 130, "bf16", "causal", None, None),               # not split
+    (1, 4, 2, 700, 700, "f32", "causal", None, [650]),
+    (2, 4, 1, 300, 500, "f32", "key_padding", [500, 0], [300, 20]),
+    (320, 2, 1, 20, 150, "f32", "none", None, None),
 ]
 
 
@@ -391,6 +400,11 @@ EVICT = [  # B, H, Lmax, Lout, keep, recent, block, code, cache_len
     (2, 1, 50, 7, 1, 5, 128, "e4m3", [50, -3]),
     (1, 2, 5000, 1300, 1025, 100, 128, "e4m3", [9999]),
     (1, 1, 2049, 2049, 2048, 1000, 16, "int8", [2049]),
+    (1, 2, 9000, 5000, 4999, 64, 64, "e4m3", [9000]),                  # one CTA of 1024 threads,
+    (2, 1, 20001, 9000, 9000, 0, 64, "int8", [20001, 16385]),          # two, four and eight,
+    (1, 1, 60000, 300, 257, 100, 32, "e4m3", [55555]),
+    (1, 1, 131072, 4096, 4096, 7, 128, "int8", [131072]),
+    (2, 1, 140000, 600, 600, 11, 64, "e4m3", [140000, 131073]),        # more than they hold
 ]
 
 
@@ -543,3 +557,112 @@ def test_two_streams_with_their_own_workspaces():
                 outs.append(mha.sdpa_decode_q8(q, cache, n))
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(alone, outs))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Nq", [5, 300])
+def test_key_weights_rows_of_infinite_lse(dtype, Nq):
+    g = rng(760)
+    q, k = fin(g.standard_normal((1, 2, Nq, 64)), dtype), fin(g.standard_normal((1, 2, 70, 64)),
+                                                             dtype)
+    lse = oracle.sdpa_lse_ref(q, k, "none").astype(np.float32)
+    lse[0, :, 1::2] = np.inf
+    w = mha.sdpa_key_weights(dev(q, DT[dtype]), dev(k, DT[dtype]), dev(lse))
+    keep = np.ascontiguousarray(q[:, :, ::2]), np.ascontiguousarray(lse[:, :, ::2])
+    ref = oq.key_weights_ref(keep[0], k, keep[1], "none")
+    assert np.allclose(w.cpu().numpy(), ref, rtol=1e-4)
+
+
+def odd(t):
+    """A copy whose first element is 4 bytes off any larger boundary."""
+    flat = torch.empty(t.numel() + 1, dtype=t.dtype, device=t.device)
+    flat[1:] = t.flatten()
+    return flat[1:].view(t.shape)
+
+
+def test_small_alignments_and_odd_sizes_give_the_same_bits():
+    # weights, scales, lse and lengths need 4 bytes only
+    g = rng(980)
+    B, H, Lmax, block = 2, 2, 5001, 16
+    c = finite(strange(g, B, H, Lmax, block, "e4m3"), "e4m3")
+    for n in "kv":
+        c[n + "_scale"] *= 2.0 ** -6
+    d = strange(g, B, H, 1001, block, "e4m3")
+    q, k, v = (dev(fin(g.standard_normal((B, h, 3, 64)), "bf16"), torch.bfloat16)
+               for h in (4, 2, 2))
+    prompt = [dev(fin(g.standard_normal((B, h, 333, 64)), "bf16"), torch.bfloat16) for h in (4, 2)]
+    results = []
+    for shift in (lambda t: t, odd):
+        cache, out = to_gpu(c, block, "e4m3"), to_gpu(d, block, "e4m3")
+        cache, out = (x._replace(k_scale=shift(x.k_scale), v_scale=shift(x.v_scale),
+                                 weights=shift(x.weights)) for x in (cache, out))
+        n = shift(i32([4998, 77]))
+        mha.kv_append_q8(cache, k, v, n, shift(i32([3, 2])))
+        n = shift(i32([5001, 79]))
+        O = mha.sdpa_decode_q8(q, cache, n, add_weights=True)
+        for x in (prompt, [t.float() for t in prompt]):
+            lse = shift(torch.full((B, 4, 333), 2.0, device="cuda"))
+            mha.sdpa_key_weights(*x, lse, "causal", None, shift(i32([333, 70])),
+                                 weights=cache.weights)
+        m, kept = mha.kv_evict_q8(cache, out, n, 1000, 17, len_out=shift(i32([0, 0])),
+                                  kept=shift(torch.zeros(B, H, 1000, dtype=torch.int32,
+                                                         device="cuda")))
+        results.append((O, m, kept, from_gpu(cache), from_gpu(out)))
+    a, b = results
+    assert all(torch.equal(x, y) for x, y in zip(a[:3], b[:3]))
+    assert_same(a[3], b[3], "e4m3", "cache")
+    assert_same(a[4], b[4], "e4m3", "evicted")
+
+
+def test_offsets_beyond_32_bits():
+    """Two heads of 40 million positions: 2.56e9 bytes each in K and in V.  All keys are zero but
+    three at the end, which hold all the weight (e^64 over e^0 for every other)."""
+    L, dt = 40_000_000, torch.bfloat16
+    cache = mha.kv_cache_q8(1, 2, L, 64)
+    k = torch.empty(1, 2, 3, 64, dtype=dt, device="cuda")
+    k[:, :, 0], k[:, :, 1], k[:, :, 2] = 8, -8, 8
+    v = dev(rng(990).integers(-8, 9, (1, 2, 3, 64)).astype(np.float32), dt)
+    mha.kv_append_q8(cache, k, v, i32([L - 3]))
+    for codes, scale, x in ((cache.k, cache.k_scale, k), (cache.v, cache.v_scale, v)):
+        assert torch.equal(codes[:, :, -3:].float() * scale[:, :, -1:, None], x.float())
+        assert not codes[:, :, -6:-3].view(torch.uint8).any()
+    O = mha.sdpa_decode_q8(torch.ones(1, 4, 1, 64, dtype=dt, device="cuda"), cache, i32([L]),
+                           add_weights=True)
+    want = ((v[:, :, 0] + v[:, :, 2]).float() / 2).repeat_interleave(2, 1)[:, :, None]
+    # the weights are rounded to 2^-11, the output to 2^-8 (values of both signs: of the larger)
+    assert torch.all((O.float() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -10 * 8)
+    w = cache.weights
+    assert torch.all((w[:, :, [-3, -1]] - 1).abs() < 1e-4)      # a half from each of two queries
+    assert w[:, :, :-3].max() < 1e-20 and w[:, :, -2].max() < 1e-20
+    w[0, 0, 12_345_678] = w[0, 1, 39_000_001] = 0.25
+    out = mha.kv_cache_q8(1, 2, 3, 64)
+    n, kept = mha.kv_evict_q8(cache, out, i32([L]), 3, 1)
+    assert n.tolist() == [3]
+    assert kept.tolist() == [[[12_345_678, L - 3, L - 1], [39_000_001, L - 3, L - 1]]]
+    got = out.v.float() * out.v_scale[..., None]
+    assert torch.equal(got[:, :, 1:], v[:, :, [0, 2]].float()) and not got[:, :, 0].any()
+
+
+def test_wrappers_refuse():
+    cache, out = mha.kv_cache_q8(1, 2, 64, 16), mha.kv_cache_q8(1, 2, 32, 16)
+    n, q = i32([10]), torch.zeros(1, 2, 1, 64, device="cuda")
+    for keep, recent in ((0, 0), (33, 0), (-1, 0), (2 ** 32 + 4, 0), (8, -1)):
+        with pytest.raises(ValueError):
+            mha.kv_evict_q8(cache, out, n, keep, recent)
+    mha.kv_evict_q8(cache, out, n, 8, 2 ** 40)          # every kept position a recent one
+    for call in (lambda: mha.kv_evict_q8(cache, mha.kv_cache_q8(1, 2, 32, 32), n, 8),
+                 lambda: mha.kv_evict_q8(cache._replace(weights=None), out, n, 8),
+                 lambda: mha.kv_evict_q8(cache, out, n.long(), 8),
+                 lambda: mha.sdpa_decode_q8(q[:, :1].expand(1, 3, 1, 64), cache, n),
+                 lambda: mha.sdpa_decode_q8(q, cache._replace(weights=None), n, add_weights=True),
+                 lambda: mha.sdpa_decode_q8(q, cache, n, out=q.bfloat16()),
+                 lambda: mha.kv_append_q8(cache, q, q[:, :1], n),
+                 lambda: mha.kv_append_q8(cache, q, q.cpu(), n),
+                 lambda: mha.sdpa_key_weights(q, q, q[..., 0].double())):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(mha.MhaError):                   # too small a workspace
+        mha.sdpa_decode_q8(q, cache, n, workspace=torch.empty(256, dtype=torch.uint8,
+                                                              device="cuda"))
+    with pytest.raises(mha.MhaError):                   # a broadcast tensor has strides of 0
+        mha.kv_append_q8(cache, q[:, :1].expand(1, 2, 1, 64), q, n)

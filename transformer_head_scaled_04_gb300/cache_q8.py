@@ -46,8 +46,8 @@ def kv_cache_q8(B, H, Lmax, block=64, dtype=torch.float8_e4m3fn, weights=True, d
 # The calls here are as short as the kernels behind them (a generation step of one sequence takes
 # 5 us on the GPU), so checks and marshalling are written for speed: devices are compared by index,
 # sizes of workspaces are remembered by the numbers they follow from.
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # absent without CUDA
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 _f32, _i32 = torch.float32, torch.int32
 
 
@@ -266,21 +266,24 @@ def kv_evict_q8(cache, out, cache_len, keep, recent=0, len_out=None, kept=None):
     B, H, Lmax, qt = _check_cache(cache, dev)
     B2, H2, Lout, qt2 = _check_cache(out, dev, "out")
     if (B2, H2, qt2, out.block) != (B, H, qt, cache.block):
-        raise ValueError("kv_evict_q8: out must have the batch, heads, code type and block of cache")
+        raise ValueError("kv_evict_q8: out must have the batch, heads, code type and block of "
+                         "cache")
     if cache.weights is None:
         raise ValueError("kv_evict_q8: the cache keeps no weights to go by")
     _dense(cache_len, _i32, (B,), dev, "cache_len")
-    keep = int(keep)
+    keep, recent = int(keep), int(recent)
+    _need(1 <= keep <= Lout and recent >= 0,
+          f"kv_evict_q8: keep must be 1..{Lout} (the room in out) and recent not negative")
     if len_out is None:
         len_out = torch.empty(B, dtype=_i32, device=cache.k.device)
     else:
         _dense(len_out, _i32, (B,), dev, "len_out")
     if kept is None:
-        kept = torch.empty((B, H, max(keep, 0)), dtype=_i32, device=cache.k.device)
+        kept = torch.empty((B, H, keep), dtype=_i32, device=cache.k.device)
     else:
         _dense(kept, _i32, (B, H, keep), dev, "kept")
     _call(dev, "mha_kv_evict_q8", B, H, Lmax, Lout, 64, 64, qt, cache.block, keep,
-          int(recent), cache_len.data_ptr(), cache.k.data_ptr(), cache.v.data_ptr(),
+          min(recent, keep), cache_len.data_ptr(), cache.k.data_ptr(), cache.v.data_ptr(),
           cache.k_scale.data_ptr(), cache.v_scale.data_ptr(), cache.weights.data_ptr(),
           out.k.data_ptr(), out.v.data_ptr(), out.k_scale.data_ptr(), out.v_scale.data_ptr(),
           _p(out.weights), len_out.data_ptr(), kept.data_ptr(),

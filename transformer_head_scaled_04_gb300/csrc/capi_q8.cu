@@ -147,7 +147,7 @@ int mha_key_weights_workspace_size(int B, int H, int Hkv, int Nq, int Nk, int dt
   // blocks of the launch's grids
   const int64_t heads = static_cast<int64_t>(B) * Hkv;
   if (heads > 65535 || heads * ((Nk + 127) / 128) > (1 << 30) || Nq > (1 << 30) ||
-      static_cast<int64_t>(H / Hkv) * ((Nq + 127) / 128) > (1 << 30))
+      static_cast<int64_t>(H / Hkv) * ((Nq + 31) / 32) > (1 << 30))
     return MHA_ERR_UNSUPPORTED;
   *bytes = round_up(mha::key_weights_workspace(B, H, Hkv, Nq, Nk, dtype), 256);
   return MHA_OK;

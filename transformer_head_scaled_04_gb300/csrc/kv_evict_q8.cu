@@ -12,8 +12,6 @@
 // gather: one CTA per (block of the new cache, head, batch element) copies the block's rows; the
 // block takes the largest scale of the tokens it receives, and codes that came under a smaller
 // one are written under it.  Bound by HBM: 64 bytes read and written per row of K and of V.
-#include <climits>
-
 #include "launchers.h"
 #include "q8_common.cuh"
 

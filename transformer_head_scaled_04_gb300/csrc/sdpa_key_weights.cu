@@ -19,8 +19,8 @@
 // the tensor cores' own accumulation truncates.  One CTA per 128 keys, 16 to a warp with their
 // terms in registers; chunks of 32 queries are split into terms once per CTA, in shared memory,
 // the next chunk on its way from global memory meanwhile.  The (head, chunk) pairs are split over
-// CTAs as above.  8 heads x 8 padded prompts of up to 1000 take 59 us, a causal prompt of 1024 23 us;
-// with one fp32 multiply-add per term and lane = key, whose operands came from shared memory at a
+// CTAs as above.  8 heads x 8 padded prompts of up to 1000 take 59 us, a causal prompt of 1024 23
+// us; with one fp32 multiply-add per term and lane = key, whose operands came from shared memory at a
 // quarter of the units' rate, 156 and 58 us.  Bound by the products and their scaling: each score
 // costs three products of 64 terms, its four parts' sum and one exponential.
 #include <cuda_bf16.h>
@@ -49,12 +49,14 @@ struct KwParams {
 constexpr int kKeys = 128;    // keys per CTA
 constexpr int kQueries = 32;  // queries per chunk
 constexpr int kWarps = 8;
-static_assert(kKeys == 16 * kWarps && kWarps * 32 == 8 * kQueries, "a key tile per warp, eight threads to a query");
+static_assert(kKeys == 16 * kWarps && kWarps * 32 == 8 * kQueries,
+              "a key tile per warp, eight threads to a query");
 
-// the power of two that brings a row's largest magnitude to [2^13, 2^14), and its inverse
+// the power of two that brings a row's largest magnitude to [2^13, 2^14) (below 2^-60: less), and
+// its inverse
 __device__ __forceinline__ float2 row_scale(float amax) {
   const int ex = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -60);
-  return make_float2(__uint_as_float((13 - ex + 127) << 23), __uint_as_float((ex - 13 + 127) << 23));
+  return make_float2(__uint_as_float((140 - ex) << 23), __uint_as_float((114 + ex) << 23));
 }
 
 __global__ void __launch_bounds__(kWarps * 32, 2) key_weights_f32_kernel(const KwParams p) {
