@@ -56,9 +56,32 @@ __device__ __forceinline__ void q8_decode4(uint32_t u, float (&f)[4]) {
   }
 }
 
-// codes under a scale that is 1 / ratio times as large (ratio a power of two <= 1)
+// Codes under a scale that is 1 / ratio times as large, ratio <= 1.  Powers of two, as the library's
+// own scales have, in fp16: a product that is not exact there is below 2^-20, or rounded once.
 template <int QT>
 __device__ __forceinline__ uint32_t q8_rescale4(uint32_t u, float ratio) {
+  if ((__float_as_uint(ratio) & 0x7fffffu) == 0) {
+    // (2^-24, fp16's least: every code becomes 0 there)
+    const __half2 r = __float2half2_rn(fmaxf(ratio, 5.9604645e-8f));
+    if constexpr (QT == kE4m3) {
+      auto two = [&](uint32_t x) -> uint32_t {
+        const __half2 h(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(x),
+                                                   __NV_E4M3));
+        return __nv_cvt_halfraw2_to_fp8x2(__hmul2(h, r), __NV_SATFINITE, __NV_E4M3);
+      };
+      return two(u & 0xffffu) | (two(u >> 16) << 16);
+    } else {
+      // code + 128 in the low bits of an fp16 between 1024 and 2048, minus 1152; the product plus
+      // 1536 is rounded to an integer, which is then the low byte
+      const uint32_t v = u ^ 0x80808080u;
+      const __half2 off = __float2half2_rn(1152.f), to = __float2half2_rn(1536.f);
+      uint32_t x = __byte_perm(v, 0x64646464u, 0x4140), y = __byte_perm(v, 0x64646464u, 0x4342);
+      const __half2 p = __hfma2(__hsub2(*reinterpret_cast<__half2*>(&x), off), r, to);
+      const __half2 q = __hfma2(__hsub2(*reinterpret_cast<__half2*>(&y), off), r, to);
+      return __byte_perm(*reinterpret_cast<const uint32_t*>(&p),
+                         *reinterpret_cast<const uint32_t*>(&q), 0x6420);
+    }
+  }
   float f[4];
   q8_decode4<QT>(u, f);
   return q8_encode4<QT>(f[0] * ratio, f[1] * ratio, f[2] * ratio, f[3] * ratio);
