@@ -227,9 +227,12 @@ __device__ __forceinline__ uint4 load_row(const uint8_t* p) {
 }
 
 // BLOCK: tokens per scale.  Four threads to a row, of K and of V; a row is asked for as soon as
-// its position is known (-1: there is none), together with its scale.
+// its position is known (-1: there is none), together with its scale.  Twelve CTAs to an SM where
+// a thread has two rows at most (64 x 16 heads 4096 -> 1024 67.7 -> 65 us over the ten that its
+// registers would leave; four rows spill: 8 heads 131072 -> 8001 20.5 -> 25.7 us).
 template <int QT, int BLOCK>
-__global__ void __launch_bounds__(kGatherThreads) kv_evict_gather_kernel(const KvEvictArgs a) {
+__global__ void __launch_bounds__(kGatherThreads, BLOCK <= 64 ? 12 : 7)
+    kv_evict_gather_kernel(const KvEvictArgs a) {
   pdl_launch_dependents();
   pdl_wait();  // the select kernel's positions are complete from here on
   constexpr int kRows = (BLOCK + 31) / 32;  // of a thread
