@@ -337,16 +337,19 @@ cudaError_t launch_gather(const KvEvictArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_kv_evict_q8(const KvEvictArgs& a, int qtype, cudaStream_t s) {
-  // threads for one step over the cache: 256 to 4096 positions (eight CTAs share an SM), then
-  // 1024 in one to eight CTAs
-  cudaError_t e;
-  if (a.Lmax <= 256 * kEach) {
-    e = launch_select<256>(a, 1, s);
-  } else {
-    int ctas = 1;
-    while (ctas < 8 && a.Lmax > ctas * 1024 * kEach) ctas *= 2;
-    e = launch_select<1024>(a, ctas, s);
-  }
+  // Threads that hold a head's weights at once: 256 for up to 4096 positions, then 512 in one to
+  // eight CTAs, then 1024 in eight.  Small CTAs share an SM: 64 x 16 heads of 4096 65 us with 256
+  // threads and 111 with 1024; 512 x 8192 46 us with 512 threads, 48 with two CTAs of 256, 64 with
+  // 1024 (53 where 256 threads read the weights twice); 16 x 32768 12.7, 13.3 and 15.4 us; 64 x
+  // 65536 36 us with eight CTAs of 512, 34 with four of 1024.
+  auto ctas_for = [&](int threads) {
+    int n = 1;
+    while (n < 8 && a.Lmax > n * threads * kEach) n *= 2;
+    return n;
+  };
+  const cudaError_t e = a.Lmax <= 256 * kEach       ? launch_select<256>(a, 1, s)
+                        : a.Lmax <= 8 * 512 * kEach ? launch_select<512>(a, ctas_for(512), s)
+                                                    : launch_select<1024>(a, 8, s);
   if (e != cudaSuccess) return e;
   return qtype == kE4m3 ? launch_gather<kE4m3>(a, s) : launch_gather<kInt8>(a, s);
 }

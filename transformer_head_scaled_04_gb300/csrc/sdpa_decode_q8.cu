@@ -64,9 +64,11 @@ struct RowPlan {
 RowPlan row_plan(int H, int Hkv, int Nq, int dtype) {
   RowPlan p;
   p.R = H / Hkv * Nq;
-  // the column tiles of a group share each converted operand; fp32's second terms leave the
-  // registers for two, bf16 for four
-  p.NR = p.R <= 8 ? 1 : p.R <= 16 || dtype != 1 ? 2 : 4;
+  // The column tiles of a group share each converted operand; fp32's second terms leave the
+  // registers for two, bf16's for four, but then for eight warps instead of twelve: 8 x 8 heads x
+  // 16384 positions with 128 rows each 182 us against 207 with two, 64 rows 116 against 108, 32
+  // rows 63 against 62
+  p.NR = p.R <= 8 ? 1 : p.R <= 64 || dtype != 1 ? 2 : 4;
   p.RG = (p.R + 8 * p.NR - 1) / (8 * p.NR);
   p.RS = std::min(p.R, 8 * p.NR);
   return p;
@@ -896,13 +898,18 @@ cudaError_t launch_all(const Params& p, int qtype, int blocks, cudaStream_t s) {
     e = qtype == kE4m3 ? launch_main<T, kE4m3, kMost>(p, blocks, s)
                        : launch_main<T, kInt8, kMost>(p, blocks, s);
   if (e != cudaSuccess) return e;
-  // a row's pieces where all sequences are alike: workers / segments, and the ends
+  // A block per row where a row has many pieces (if all sequences are alike: workers / segments,
+  // and no more than tiles) and rows are few, else a warp.  Pieces and rows, block and warp: 228
+  // and 8 31 and 48 us, 57 and 512 27 and 33, 28 and 256 22.5 and 23.8, 28 and 512 26.3 and 24.9,
+  // 28 and 1024 37.3 and 34.0
   const int64_t heads = static_cast<int64_t>(p.a.B) * p.a.Hkv, rows = heads * p.rp.R;
-  const bool wide = p.workers / (heads * p.rp.RG) > 8;
+  const int64_t pieces =
+      std::min<int64_t>(p.workers / (heads * p.rp.RG), (p.a.Lmax + kTile - 1) / kTile);
+  const bool wide = pieces > 8 && rows <= 16 * pieces;
   const int row_blocks = static_cast<int>(wide ? rows : (rows + kWarps - 1) / kWarps);
   // more positions to a thread where that still fills the GPU: the blocks' fixed cost (statistics
   // of the rows) is paid less often (one row, 64 x 16 heads x 4096 positions: four quads 102 us,
-  // one 113 us)
+  // one 113 us; three rows: two 116, one 123)
   auto fills = [&](int n) { return heads * ((p.a.Lmax + 1024 * n - 1) / (1024 * n)) >= 2 * 152; };
   const int quads = p.rp.R <= 2 && fills(4) ? 4 : fills(2) ? 2 : 1;
   const int chunk = 4 * kThreads * quads;

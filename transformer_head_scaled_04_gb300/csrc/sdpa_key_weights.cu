@@ -511,7 +511,8 @@ __global__ void __launch_bounds__(256) key_weights_add_kernel(const KwParams p) 
 }
 
 // CTAs per key tile: enough for two on each of 152 SMs (fp32: twice that, for shorter CTAs), no
-// more than there are query tiles or chunks
+// more than there are query tiles or chunks.  Against one CTA per key tile: a bf16 head of 4096
+// 10.3 and 22.3 us, four 20.1 and 22.3; three fp32 prompts of 333 13.6 and 43.9
 int key_weights_split(int B, int H, int Hkv, int Nq, int Nk, int dtype) {
   const int keys = dtype == 1 ? kT : kKeys, rows = dtype == 1 ? kT : kQueries;
   const int64_t units = static_cast<int64_t>(B) * Hkv * ((Nk + keys - 1) / keys);
