@@ -702,6 +702,24 @@ __device__ __forceinline__ float2 merge(float& m, float& l, float m2, float l2) 
   return f;
 }
 
+// Joins (m, l) with the maxima and sums st of 2 kHalf lanes (kNone, 0: none), the same for all of
+// them.  Returns the factor of the lane's own; `old`: that of what was in (m, l)
+template <int kHalf>
+__device__ __forceinline__ float join_lanes(float& m, float& l, float2 st, float& old) {
+  float top = st.x;
+#pragma unroll
+  for (int s = kHalf; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+  top = fmaxf(top, m);
+  const float f = st.x == top ? 1.f : ex2_approx(st.x - top);
+  old = m == top ? 1.f : ex2_approx(m - top);
+  float sum = st.y * f;
+#pragma unroll
+  for (int s = kHalf; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+  l = l * old + sum;
+  m = top;
+  return f;
+}
+
 // Blocks 0 .. row_blocks-1: O.  kWide: the warps of a block split the pieces of one row;
 // otherwise each takes a row of its own.  The blocks behind (kQuads > 0): weights, 1024 kQuads
 // positions each.  What depends on the lengths alone is done before the pieces are waited for.
@@ -729,26 +747,40 @@ __global__ void __launch_bounds__(kThreads, 4) decode_q8_join_kernel(const Param
     const int last = pieces.nt > 0 ? pieces.last(hr) : -1;
     const int64_t at0 = (static_cast<int64_t>(b) * per + hr) * p.rp.RS + r % group;
     pdl_wait();  // the pieces are complete from here on
+    // 32 pieces at a time: a lane has the maximum and sum of one, so that the largest maximum, each
+    // piece's factor and the sum take one exponential; then the pieces' O under their factors
     float m = kNone, l = 0.f;
     float2 o = make_float2(0.f, 0.f);
-    constexpr int kStep = kWide ? kWarps : 1, kBatch = kWide ? 8 : 4;  // pieces asked for at once
-    for (int w = first + (kWide ? warp : 0); w <= last; w += kStep * kBatch) {
-      float2 st[kBatch], v[kBatch];
+    constexpr int kStep = kWide ? kWarps : 1, kBatch = 8;  // pieces asked for at once
+    for (int w = first + (kWide ? warp : 0); w <= last; w += 32 * kStep) {
+      const int n = min(32, (last - w) / kStep + 1);
+      const int64_t at = static_cast<int64_t>(w) * p.rp.RS + at0;
+      float2 st = make_float2(kNone, 0.f), v[kBatch];
+      if (lane < n)
+        st = *reinterpret_cast<const float2*>(
+            p.stat + (at + static_cast<int64_t>(lane) * kStep * p.rp.RS) * 2);
+      auto load = [&](int k0) {
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        st[k] = make_float2(kNone, 0.f);
-        v[k] = make_float2(0.f, 0.f);
-        if (w + k * kStep <= last) {
-          const int64_t at = static_cast<int64_t>(w + k * kStep) * p.rp.RS + at0;
-          st[k] = *reinterpret_cast<const float2*>(p.stat + at * 2);
-          v[k] = *reinterpret_cast<const float2*>(p.part + at * kD + 2 * lane);
+        for (int k = 0; k < kBatch; ++k) {
+          v[k] = make_float2(0.f, 0.f);
+          if (k0 + k < n)
+            v[k] = *reinterpret_cast<const float2*>(
+                p.part + (at + static_cast<int64_t>(k0 + k) * kStep * p.rp.RS) * kD + 2 * lane);
         }
-      }
+      };
+      load(0);
+      float old;
+      const float f = join_lanes<16>(m, l, st, old);
+      o.x *= old;
+      o.y *= old;
+      for (int k0 = 0; k0 < n; k0 += kBatch) {
+        if (k0 > 0) load(k0);
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const float2 f = merge(m, l, st[k].x, st[k].y);
-        o.x = o.x * f.x + v[k].x * f.y;
-        o.y = o.y * f.x + v[k].y * f.y;
+        for (int k = 0; k < kBatch; ++k) {
+          const float fk = __shfl_sync(0xffffffffu, f, (k0 + k) & 31);
+          o.x = fmaf(v[k].x, fk, o.x);
+          o.y = fmaf(v[k].y, fk, o.y);
+        }
       }
     }
     if constexpr (kWide) {
@@ -786,25 +818,42 @@ __global__ void __launch_bounds__(kThreads, 4) decode_q8_join_kernel(const Param
     if (j0 >= L) return;
     extern __shared__ float rowstat[];  // [R][2]
     const Pieces pieces(p, b);          // L > 0: there are some
-    pdl_wait();                         // pieces and scores are complete from here on
     const int R = p.rp.R;
     const float* sc = p.scores + static_cast<int64_t>(bh) * R * p.Lpad;
     float* out = a.weights + static_cast<int64_t>(bh) * a.Lmax;
-    // scores of up to four rows and quads at a time; the first are asked for before the
-    // statistics are known
-    constexpr int kRows = 4 / kQuads;
-    float4 xs[kRows][kQuads];
-    auto load = [&](int r) {
+    // position of the thread's quad k; what its weights were is asked for before the pieces are
+    // waited for
+    auto quad = [&](int k) { return j0 + (k * kThreads + static_cast<int>(threadIdx.x)) * 4; };
+    const bool vec = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+    float was[kQuads][4];
+#pragma unroll
+    for (int k = 0; k < kQuads; ++k) {
+      const int j = quad(k);
+      if (vec && j + 4 <= L) {
+        const float4 v = *reinterpret_cast<const float4*>(out + j);
+        was[k][0] = v.x, was[k][1] = v.y, was[k][2] = v.z, was[k][3] = v.w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (j + i < L) was[k][i] = out[j + i];
+      }
+    }
+    pdl_wait();  // pieces and scores are complete from here on
+    // scores of up to four rows and quads at a time, the next ones on their way meanwhile; the first
+    // are asked for before the statistics are known
+    constexpr int kRows = 4 / kQuads, kBufs = kQuads == 4 ? 1 : 2;
+    float4 xs[kBufs][kRows][kQuads];
+    auto load = [&](int r, float4 (&x)[kRows][kQuads]) {
 #pragma unroll
       for (int k = 0; k < kQuads; ++k) {
-        const int j = j0 + (k * kThreads + static_cast<int>(threadIdx.x)) * 4;
+        const int j = quad(k);
 #pragma unroll
         for (int u = 0; u < kRows; ++u)
           if (j < L && r + u < R)
-            xs[u][k] = *reinterpret_cast<const float4*>(sc + (r + u) * p.Lpad + j);
+            x[u][k] = *reinterpret_cast<const float4*>(sc + (r + u) * p.Lpad + j);
       }
     };
-    load(0);
+    load(0, xs[0]);
     for (int r0 = 2 * warp; r0 < R; r0 += 2 * kWarps) {  // a row to each half of the warp
       const int r = min(r0 + (lane >> 4), R - 1);
       const int hr = hk * p.rp.RG + r / group;
@@ -816,12 +865,11 @@ __global__ void __launch_bounds__(kThreads, 4) decode_q8_join_kernel(const Param
             p.stat + (static_cast<int64_t>(w) * p.rp.RS + at0) * 2);
         merge(m, l, st.x, st.y);
       }
-#pragma unroll
-      for (int s = 8; s > 0; s >>= 1) {
-        const float m2 = __shfl_xor_sync(0xffffffffu, m, s);
-        const float l2 = __shfl_xor_sync(0xffffffffu, l, s);
-        merge(m, l, m2, l2);
-      }
+      const float2 mine = make_float2(m, l);
+      float old;
+      m = kNone;
+      l = 0.f;
+      join_lanes<8>(m, l, mine, old);
       if ((lane & 15) == 0) {  // weight = 2^(x + offset - m) / l (the pieces' own reference)
         rowstat[2 * r] = kOffset - m;
         rowstat[2 * r + 1] = l == 0.f ? 0.f : 1.f / l;
@@ -833,27 +881,43 @@ __global__ void __launch_bounds__(kThreads, 4) decode_q8_join_kernel(const Param
     for (int k = 0; k < kQuads; ++k)
 #pragma unroll
       for (int i = 0; i < 4; ++i) w[k][i] = 0.f;
-    for (int r = 0; r < R; r += kRows) {
-      if (r > 0) load(r);
+    auto add = [&](int r, float4 (&x)[kRows][kQuads]) {
 #pragma unroll
       for (int u = 0; u < kRows; ++u) {
         if (r + u >= R) break;
         const float2 st = *reinterpret_cast<const float2*>(rowstat + 2 * (r + u));
 #pragma unroll
         for (int k = 0; k < kQuads; ++k) {
-          const float v[4] = {xs[u][k].x, xs[u][k].y, xs[u][k].z, xs[u][k].w};
+          const float v[4] = {x[u][k].x, x[u][k].y, x[u][k].z, x[u][k].w};
 #pragma unroll
           for (int i = 0; i < 4; ++i)  // an excluded position takes nothing of a NaN row
             if (v[i] != -INFINITY) w[k][i] = fmaf(ex2_approx(v[i] + st.x), st.y, w[k][i]);
         }
       }
+    };
+    for (int r = 0; r < R; r += kBufs * kRows) {
+      if constexpr (kBufs == 1) {
+        if (r > 0) load(r, xs[0]);
+        add(r, xs[0]);
+      } else {
+        load(r + kRows, xs[1]);
+        add(r, xs[0]);
+        load(r + 2 * kRows, xs[0]);
+        add(r + kRows, xs[1]);
+      }
     }
 #pragma unroll
     for (int k = 0; k < kQuads; ++k) {
-      const int j = j0 + (k * kThreads + static_cast<int>(threadIdx.x)) * 4;
+      const int j = quad(k);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (j + i < L) out[j + i] += w[k][i];
+      for (int i = 0; i < 4; ++i) w[k][i] += was[k][i];
+      if (vec && j + 4 <= L) {
+        *reinterpret_cast<float4*>(out + j) = make_float4(w[k][0], w[k][1], w[k][2], w[k][3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (j + i < L) out[j + i] = w[k][i];
+      }
     }
   }
 }
