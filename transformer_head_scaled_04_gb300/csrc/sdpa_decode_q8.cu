@@ -964,12 +964,12 @@ cudaError_t launch_all(const Params& p, int qtype, int blocks, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   // A block per row where a row has many pieces (if all sequences are alike: workers / segments,
   // and no more than tiles) and rows are few, else a warp.  Pieces and rows, block and warp: 228
-  // and 8 31 and 48 us, 57 and 512 27 and 33, 28 and 256 22.5 and 23.8, 28 and 512 26.3 and 24.9,
-  // 28 and 1024 37.3 and 34.0
+  // and 8 29.4 and 39.3 us, 57 and 512 27.2 and 29.1, 28 and 256 21.6 and 22.3, 28 and 512 25.8
+  // and 23.6, 28 and 1024 36.9 and 32.8, 16 and 16 5.5 and 5.9, 14 and 128 30.6 and 28.7
   const int64_t heads = static_cast<int64_t>(p.a.B) * p.a.Hkv, rows = heads * p.rp.R;
   const int64_t pieces =
       std::min<int64_t>(p.workers / (heads * p.rp.RG), (p.a.Lmax + kTile - 1) / kTile);
-  const bool wide = pieces > 8 && rows <= 16 * pieces;
+  const bool wide = pieces >= 16 && rows <= 16 * pieces;
   const int row_blocks = static_cast<int>(wide ? rows : (rows + kWarps - 1) / kWarps);
   // more positions to a thread where that still fills the GPU: the blocks' fixed cost (statistics
   // of the rows) is paid less often (one row, 64 x 16 heads x 4096 positions: four quads 102 us,
