@@ -247,8 +247,9 @@ int mha_decode_q8_workspace_size(int B, int H, int Hkv, int Nq, int Lmax, int wi
  *   not be powers of two.
  *   strides: NULL for contiguous, or 16 strides {Q, K, V, O} x {b, h, n, d} (Q, O in elements
  *   as for mha_kv_append_q8's K).  O may not alias an input.
- *   workspace: mha_decode_q8_workspace_size() bytes, 256-byte aligned; calls that may run at
- *   the same time (two streams, two replayed graphs) need one each.
+ *   workspace: mha_decode_q8_workspace_size() bytes, 256-byte aligned (may be NULL when that is
+ *   0: short caches of few heads); calls that may run at the same time (two
+ *   streams, two replayed graphs) need one each.
  */
 int mha_sdpa_decode_q8_fwd(int B, int H, int Hkv, int Nq, int Lmax, int d_k, int d_v, int dtype,
                            int qtype, int block, int causal, const int32_t* cache_len,

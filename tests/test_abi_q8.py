@@ -75,7 +75,8 @@ def decode(lib, B=1, H=4, Hkv=2, Nq=1, Lmax=16, dk=64, dv=64, dt=1, qt=0, block=
     (dict(q=EIGHT), ALIGN), (dict(kc=EIGHT), ALIGN), (dict(ks=ODD), ALIGN), (dict(w=ODD), ALIGN),
     (dict(st=strides(4, _13=-8)), INVALID), (dict(st=strides(4, _7=2)), UNSUPPORTED),
     (dict(st=strides(4, _6=24)), ALIGN), (dict(st=strides(4, _14=0)), ALIGN),
-    (dict(ws=None), WORKSPACE), (dict(n=16), WORKSPACE), (dict(ws=EIGHT), ALIGN),
+    (dict(ws=None, Lmax=4096), WORKSPACE), (dict(n=16, Lmax=4096), WORKSPACE),
+    (dict(ws=EIGHT, Lmax=4096), ALIGN),
 ])
 def test_decode_refusals(lib, kw, code):
     assert decode(lib, **kw) == code
@@ -136,7 +137,8 @@ def evict(lib, B=1, H=1, Lmax=64, Lout=32, dk=64, dv=64, qt=0, block=16, keep=20
     (dict(kept=None), INVALID), (dict(n=None), INVALID), (dict(ko=None), INVALID),
     (dict(ko=at(2)), INVALID), (dict(vo=at(7)), INVALID), (dict(n=at(1)), INVALID),
     (dict(wo=at(6)), INVALID), (dict(vso=at(5)), INVALID), (dict(dk=32), UNSUPPORTED),
-    (dict(block=20), UNSUPPORTED), (dict(H=65536), UNSUPPORTED), (dict(B=65535, H=65535), UNSUPPORTED),
+    (dict(block=20), UNSUPPORTED), (dict(H=65536), UNSUPPORTED),
+    (dict(B=65535, H=65535), UNSUPPORTED),
     (dict(vo=EIGHT), ALIGN),
     (dict(kept=ODD), ALIGN), (dict(st=strides(4, _8=-16)), INVALID),
     (dict(st=strides(4, _11=0)), UNSUPPORTED), (dict(st=strides(4, _14=8)), ALIGN),

@@ -201,6 +201,10 @@ DECODE = [  # B, H, Hkv, Nq, Lmax, block, dtype, code, causal, cache_len
     (1, 256, 1, 16, 40, 16, "bf16", "int8", False, [40]),              # 4096 rows, the most
     (8, 40, 40, 1, 4100, 64, "bf16", "e4m3", True, [4100, 0, 4096, 4097, 1, 33, 2048, 777]),
     (2, 320, 80, 1, 2100, 32, "f32", "int8", True, [2100, 1025]),
+    (1, 16, 8, 8, 768, 64, "bf16", "e4m3", True, [766]),               # one launch
+    (4, 4, 4, 16, 383, 16, "f32", "e4m3", False, [383, 0, 33, 2]),
+    (150, 1, 1, 1, 100, 32, "bf16", "int8", True, [i % 103 for i in range(150)]),
+    (300, 1, 1, 1, 100, 32, "bf16", "int8", True, [i % 103 for i in range(300)]),
 ]
 
 
@@ -662,7 +666,7 @@ def test_wrappers_refuse():
         with pytest.raises(ValueError):
             call()
     with pytest.raises(mha.MhaError):                   # too small a workspace
-        mha.sdpa_decode_q8(q, cache, n, workspace=torch.empty(256, dtype=torch.uint8,
-                                                              device="cuda"))
+        mha.sdpa_decode_q8(torch.zeros(1, 2, 1, 64, device="cuda"), mha.kv_cache_q8(1, 2, 4096), n,
+                           workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
     with pytest.raises(mha.MhaError):                   # a broadcast tensor has strides of 0
         mha.kv_append_q8(cache, q[:, :1].expand(1, 2, 1, 64), q, n)

@@ -191,16 +191,17 @@ def sdpa_decode_q8(q, cache, cache_len, causal=True, scale=None, add_weights=Fal
     else:
         _same(out, q, shape, dev, "sdpa_decode_q8: out")
     if workspace is None:
-        workspace = torch.empty(decode_q8_workspace_size(B, H, Hkv, Nq, Lmax, bool(add_weights)),
-                                dtype=torch.uint8, device=q.device)
+        need = decode_q8_workspace_size(B, H, Hkv, Nq, Lmax, bool(add_weights))
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     else:
         _workspace(workspace, 0, q, dev, "sdpa_decode_q8")
     _call(dev, "mha_sdpa_decode_q8_fwd", B, H, Hkv, Nq, Lmax, 64, 64, dt, qt, cache.block,
           1 if causal else 0, cache_len.data_ptr(), float(scale or 0.0), q.data_ptr(),
           cache.k.data_ptr(), cache.v.data_ptr(), cache.k_scale.data_ptr(),
           cache.v_scale.data_ptr(), out.data_ptr(), _strides(q, cache.k, cache.v, out),
-          cache.weights.data_ptr() if add_weights else None, workspace.data_ptr(),
-          workspace.numel())
+          cache.weights.data_ptr() if add_weights else None, _p(workspace),
+          0 if workspace is None else workspace.numel())
     return out
 
 

@@ -126,8 +126,8 @@ int mha_sdpa_decode_q8_fwd(int B, int H, int Hkv, int Nq, int Lmax, int d_k, int
   size_t need = 0;
   st = mha_decode_q8_workspace_size(B, H, Hkv, Nq, Lmax, weights != nullptr ? 1 : 0, &need);
   if (st != MHA_OK) return st;
-  if (workspace == nullptr || ws_bytes < need) return MHA_ERR_WORKSPACE;
-  if (!aligned(workspace, 256)) return MHA_ERR_ALIGN;
+  if (need > 0 && (workspace == nullptr || ws_bytes < need)) return MHA_ERR_WORKSPACE;
+  if (need > 0 && !aligned(workspace, 256)) return MHA_ERR_ALIGN;
   DevCtx ctx;
   st = mha::current_device_ctx(&ctx);
   if (st != MHA_OK) return st;

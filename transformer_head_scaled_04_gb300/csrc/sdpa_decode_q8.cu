@@ -34,7 +34,8 @@
 // (the tensor cores' own accumulation truncates).
 // Runs end at heads' ends: each piece leaves (O, m, l) in the workspace, and a second launch
 // joins a row's pieces, and adds the weights 2^(x_ij - m_i) / l_i from the scores that the first
-// one stored.  No atomics: one order of sums.
+// one stored.  Short caches of few heads take one launch, a block to a head, whose warps' pieces
+// and scores meet in shared memory.  No atomics: one order of sums.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -51,6 +52,8 @@ constexpr int kD = 64;
 constexpr int kTile = 32;                  // positions per tile
 constexpr int kTileBytes = kTile * kD;     // 2 KB of K, 2 KB of V
 constexpr int kStages = 3;
+constexpr int kAloneMax = 768, kAloneSegments = 152;  // see alone()
+constexpr int kAlonePad = 4;               // floats between rows of scores: other banks
 constexpr int kSlotBytes = 2 * kTileBytes;
 constexpr int kWarps = 8;                  // of the join
 constexpr int kThreads = kWarps * 32;
@@ -253,8 +256,36 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   return d;
 }
 
-// T: float (two fp16 terms per operand) or bf16 (one).  NR: column tiles of 8 query rows
-template <typename T, int QT, int NR>
+__device__ __forceinline__ void put2(__nv_bfloat16* q, float a, float b) {
+  *reinterpret_cast<uint32_t*>(q) = pack_bf16x2(a, b);
+}
+__device__ __forceinline__ void put2(float* q, float a, float b) {
+  *reinterpret_cast<float2*>(q) = make_float2(a, b);
+}
+
+
+// Joins (m, l) with the maxima and sums st of 2 kHalf lanes (kNone, 0: none), the same for all of
+// them.  Returns the factor of the lane's own; `old`: that of what was in (m, l)
+template <int kHalf>
+__device__ __forceinline__ float join_lanes(float& m, float& l, float2 st, float& old) {
+  float top = st.x;
+#pragma unroll
+  for (int s = kHalf; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+  top = fmaxf(top, m);
+  const float f = st.x == top ? 1.f : ex2_approx(st.x - top);
+  old = m == top ? 1.f : ex2_approx(m - top);
+  float sum = st.y * f;
+#pragma unroll
+  for (int s = kHalf; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+  l = l * old + sum;
+  m = top;
+  return f;
+}
+
+// T: float (two fp16 terms per operand) or bf16 (one).  NR: column tiles of 8 query rows.
+// kAlone: a block per cache head (of one row group), whose tiles its warps share; pieces and scores
+// meet in shared memory, and no second launch is needed.
+template <typename T, int QT, int NR, bool kAlone>
 __global__ void __launch_bounds__(main_warps(sizeof(T) / 2, NR) * 32, 1)
     decode_q8_kernel(const Params p) {
   constexpr int kTerms = sizeof(T) == 4 ? 2 : 1;
@@ -268,15 +299,29 @@ __global__ void __launch_bounds__(main_warps(sizeof(T) / 2, NR) * 32, 1)
 
   // this warp's run of tiles.  Consecutive workers sit in different blocks, so that few tiles
   // spread over the SMs
+  constexpr int kMainWarps = main_warps(sizeof(T) / 2, NR);
+  // kAlone: [rows][2] of the statistics, then [rows][Lpad] of the scores, behind the rings
+  float* const alone_stat = reinterpret_cast<float*>(smem + kMainWarps * (kStages * kSlotBytes));
+  float* const alone_scores = alone_stat + 8 * NR * 2;
   const int per = a.Hkv * p.rp.RG;
-  const Line line = line_of(a, per, p.workers);
   const uint32_t worker = warp * gridDim.x + blockIdx.x;
-  const uint32_t x0 = worker * line.run;
-  if (x0 >= line.total) return;
-  const int count = static_cast<int>(min(line.run, line.total - x0));
-
+  int count, live = 0;  // tiles; kAlone: warps that have any
   Cursor c;
-  {
+  if constexpr (kAlone) {
+    c.b = static_cast<int>(blockIdx.x) / a.Hkv;
+    c.hk = static_cast<int>(blockIdx.x) % a.Hkv;
+    c.rg = 0;
+    c.L = cached(a, c.b);
+    c.nt = tiles_of(c.L);
+    const int each = max((c.nt + kMainWarps - 1) / kMainWarps, 1);
+    live = (c.nt + each - 1) / each;
+    c.kt = warp * each;
+    count = max(min(each, c.nt - c.kt), 0);
+  } else {
+    const Line line = line_of(a, per, p.workers);
+    const uint32_t x0 = worker * line.run;
+    if (x0 >= line.total) return;
+    count = static_cast<int>(min(line.run, line.total - x0));
     uint32_t before;
     c.b = find_batch(line, a, per, x0, &before);
     c.L = cached(a, c.b);
@@ -394,7 +439,11 @@ __global__ void __launch_bounds__(main_warps(sizeof(T) / 2, NR) * 32, 1)
   };
 
   auto end_segment = [&]() {
-    const int64_t slot = worker + static_cast<int64_t>(c.b) * per + c.hk * p.rp.RG + c.rg;
+    const int64_t slot =
+        kAlone ? 0 : worker + static_cast<int64_t>(c.b) * per + c.hk * p.rp.RG + c.rg;
+    // (kAlone: the warp's ring, whose copies have all landed and been read)
+    float* part = kAlone ? reinterpret_cast<float*>(ring) : p.part;
+    float* stat = kAlone ? part + 8 * NR * kD : p.stat;
     const int r0 = c.rg * (8 * NR);
 #pragma unroll
     for (int nr = 0; nr < NR; ++nr)
@@ -407,12 +456,11 @@ __global__ void __launch_bounds__(main_warps(sizeof(T) / 2, NR) * 32, 1)
         s += __shfl_xor_sync(0xffffffffu, s, 16);
         if (r0 + rl < p.rp.R) {
           // columns 8g + 2j and 8g + 2j + 1
-          float4* dst = reinterpret_cast<float4*>(p.part + (slot * p.rp.RS + rl) * kD + g * 8);
+          float4* dst = reinterpret_cast<float4*>(part + (slot * p.rp.RS + rl) * kD + g * 8);
           dst[0] = make_float4(o[nr][0][e], o[nr][0][2 + e], o[nr][1][e], o[nr][1][2 + e]);
           dst[1] = make_float4(o[nr][2][e], o[nr][2][2 + e], o[nr][3][e], o[nr][3][2 + e]);
           if (g == 0)
-            *reinterpret_cast<float2*>(p.stat + (slot * p.rp.RS + rl) * 2) =
-                make_float2(m[nr][e], s);
+            *reinterpret_cast<float2*>(stat + (slot * p.rp.RS + rl) * 2) = make_float2(m[nr][e], s);
         }
       }
   };
@@ -431,7 +479,9 @@ __global__ void __launch_bounds__(main_warps(sizeof(T) / 2, NR) * 32, 1)
     };
     float* score_row = nullptr;  // of row 2t of the group
     const int rows_here = p.rp.R - c.rg * (8 * NR) - 2 * t;  // live rows from there on
-    if (p.scores != nullptr)
+    if (kAlone && a.weights != nullptr)
+      score_row = alone_scores + 2 * t * p.Lpad + g;
+    if (!kAlone && p.scores != nullptr)
       score_row = p.scores + (head * p.rp.R + c.rg * (8 * NR) + 2 * t) * p.Lpad + g;
     // A maximum's rounding beyond 2^20 is too coarse for exponents that are rounded once: there
     // they are taken from scores rounded as the maximum was
@@ -556,7 +606,7 @@ __global__ void __launch_bounds__(main_warps(sizeof(T) / 2, NR) * 32, 1)
         }
         if (!kEdge && huge) return false;  // taken again below: nothing so far depends on it
         // ---- weights, 16 positions at a time, and their product with the value codes
-        float po[kTerms == 2 ? NR : 1][4][4];
+        [[maybe_unused]] float po[kTerms == 2 ? NR : 1][4][4];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           uint32_t pf[kTerms][NR][2];
@@ -663,7 +713,42 @@ __global__ void __launch_bounds__(main_warps(sizeof(T) / 2, NR) * 32, 1)
       if (++slot == kStages) slot = 0;
     }
     end_segment();
-    if (c.kt == c.nt) next_segment(p, c);
+    if (!kAlone && c.kt == c.nt) next_segment(p, c);
+  }
+  if constexpr (kAlone) {
+    __syncthreads();
+    for (int r = warp; r < p.rp.R; r += kMainWarps) {
+      auto piece = [&](int w) {
+        return reinterpret_cast<const float*>(smem + w * (kStages * kSlotBytes));
+      };
+      float2 st = make_float2(kNone, 0.f), o2 = make_float2(0.f, 0.f);
+      if (lane < live) st = *reinterpret_cast<const float2*>(piece(lane) + 8 * NR * kD + 2 * r);
+      float top = kNone, sum = 0.f, old;
+      const float f = join_lanes<16>(top, sum, st, old);
+      for (int w = 0; w < live; ++w) {
+        const float fw = __shfl_sync(0xffffffffu, f, w);
+        const float2 v = *reinterpret_cast<const float2*>(piece(w) + r * kD + 2 * lane);
+        o2.x = fmaf(v.x, fw, o2.x);
+        o2.y = fmaf(v.y, fw, o2.y);
+      }
+      const float y = sum == 0.f ? 0.f : 1.f / sum;  // no allowed position: zeros
+      const int h = c.hk * (a.H / a.Hkv) + r / a.Nq;
+      put2(static_cast<T*>(a.O) + c.b * a.so[0] + h * a.so[1] + (r % a.Nq) * a.so[2] + 2 * lane,
+           o2.x * y, o2.y * y);
+      if (lane == 0) *reinterpret_cast<float2*>(alone_stat + 2 * r) = make_float2(kOffset - top, y);
+    }
+    if (a.weights == nullptr) return;
+    __syncthreads();
+    float* out = a.weights + (static_cast<int64_t>(c.b) * a.Hkv + c.hk) * a.Lmax;
+    for (int j = threadIdx.x; j < c.L; j += kMainWarps * 32) {
+      float w = 0.f;
+      for (int r = 0; r < p.rp.R; ++r) {
+        const float2 st = *reinterpret_cast<const float2*>(alone_stat + 2 * r);
+        const float x = alone_scores[r * p.Lpad + j];
+        if (x != -INFINITY) w = fmaf(ex2_approx(x + st.x), st.y, w);
+      }
+      out[j] += w;
+    }
   }
 }
 
@@ -683,12 +768,6 @@ struct Pieces {
   __device__ __forceinline__ int last(int hr) const { return (start + hr * nt + nt - 1) / run; }
 };
 
-__device__ __forceinline__ void put2(__nv_bfloat16* q, float a, float b) {
-  *reinterpret_cast<uint32_t*>(q) = pack_bf16x2(a, b);
-}
-__device__ __forceinline__ void put2(float* q, float a, float b) {
-  *reinterpret_cast<float2*>(q) = make_float2(a, b);
-}
 
 
 // Merges (m2, l2) into (m, l): sums l under the larger maximum (kNone: nothing there; a NaN sum
@@ -699,24 +778,6 @@ __device__ __forceinline__ float2 merge(float& m, float& l, float m2, float l2) 
                                m2 == top ? 1.f : ex2_approx(m2 - top));
   m = top;
   l = l * f.x + l2 * f.y;
-  return f;
-}
-
-// Joins (m, l) with the maxima and sums st of 2 kHalf lanes (kNone, 0: none), the same for all of
-// them.  Returns the factor of the lane's own; `old`: that of what was in (m, l)
-template <int kHalf>
-__device__ __forceinline__ float join_lanes(float& m, float& l, float2 st, float& old) {
-  float top = st.x;
-#pragma unroll
-  for (int s = kHalf; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-  top = fmaxf(top, m);
-  const float f = st.x == top ? 1.f : ex2_approx(st.x - top);
-  old = m == top ? 1.f : ex2_approx(m - top);
-  float sum = st.y * f;
-#pragma unroll
-  for (int s = kHalf; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-  l = l * old + sum;
-  m = top;
   return f;
 }
 
@@ -839,8 +900,8 @@ __global__ void __launch_bounds__(kThreads, 4) decode_q8_join_kernel(const Param
       }
     }
     pdl_wait();  // pieces and scores are complete from here on
-    // scores of up to four rows and quads at a time, the next ones on their way meanwhile; the first
-    // are asked for before the statistics are known
+    // scores of up to four rows and quads at a time, the next ones on their way meanwhile; the
+    // first are asked for before the statistics are known
     constexpr int kRows = 4 / kQuads, kBufs = kQuads == 4 ? 1 : 2;
     float4 xs[kBufs][kRows][kQuads];
     auto load = [&](int r, float4 (&x)[kRows][kQuads]) {
@@ -939,14 +1000,37 @@ Workspace plan(int B, int H, int Hkv, int Nq, int Lmax, int dtype, bool weights)
   return w;
 }
 
-template <typename T, int QT, int NR>
+template <typename T, int QT, int NR, bool kAlone = false>
 cudaError_t launch_main(const Params& p, int blocks, cudaStream_t s) {
-  auto kern = decode_q8_kernel<T, QT, NR>;
+  auto kern = decode_q8_kernel<T, QT, NR, kAlone>;
   constexpr int kMainWarps = main_warps(sizeof(T) / 2, NR);
-  constexpr int kSmem = kMainWarps * kStages * kSlotBytes;
+  static_assert(!kAlone || 8 * NR * (kD + 2) * 4 <= kStages * kSlotBytes, "a piece in a ring");
+  constexpr int kRing = kMainWarps * kStages * kSlotBytes, kRows = 8 * NR;
+  constexpr int kSmem = kRing + (kAlone ? kRows * (2 + kAloneMax + kAlonePad) * 4 : 0);
   const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(kern), kSmem, nullptr);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(blocks), dim3(kMainWarps * 32), kSmem, s, p);
+  const size_t smem =
+      kAlone && p.a.weights != nullptr ? kRing + (kRows * 2 + p.rp.R * p.Lpad) * 4
+                                       : kRing + (kAlone ? kRows * 2 * 4 : 0);
+  return launch_pdl(kern, dim3(blocks), dim3(kMainWarps * 32), smem, s, p);
+}
+// Whether one launch does it all: short caches of few heads (a block each, one per SM), whose rows
+// are one group.  One and two launches, bf16, a row per head: 16 heads of 128 4.1 and 5.2 us, 64 of
+// 384 4.8 and 6.2, 144 of 768 6.2 and 7.9 (with weights 7.5 and 8.2), 16 of 768 5.8 and 5.8 (6.9
+// and 6.2), 16 of 1000 6.5 and 5.8; 304 heads, a second round of blocks, of 384 8.9 and 7.9
+bool alone(int B, int H, int Hkv, int Nq, int Lmax) {
+  return Lmax <= kAloneMax && H / Hkv * Nq <= 16 &&
+         static_cast<int64_t>(B) * Hkv <= kAloneSegments;
+}
+template <typename T>
+cudaError_t launch_alone(Params p, int qtype, cudaStream_t s) {
+  p.Lpad += kAlonePad;
+  const int blocks = p.a.B * p.a.Hkv;
+  if (p.rp.NR == 1)
+    return qtype == kE4m3 ? launch_main<T, kE4m3, 1, true>(p, blocks, s)
+                          : launch_main<T, kInt8, 1, true>(p, blocks, s);
+  return qtype == kE4m3 ? launch_main<T, kE4m3, 2, true>(p, blocks, s)
+                        : launch_main<T, kInt8, 2, true>(p, blocks, s);
 }
 template <typename T>
 cudaError_t launch_all(const Params& p, int qtype, int blocks, cudaStream_t s) {
@@ -994,6 +1078,7 @@ cudaError_t launch_all(const Params& p, int qtype, int blocks, cudaStream_t s) {
 }  // namespace
 
 size_t decode_q8_workspace(int B, int H, int Hkv, int Nq, int Lmax, bool weights) {
+  if (alone(B, H, Hkv, Nq, Lmax)) return 0;
   return std::max(plan(B, H, Hkv, Nq, Lmax, 0, weights).total,
                   plan(B, H, Hkv, Nq, Lmax, 1, weights).total);
 }
@@ -1013,6 +1098,8 @@ cudaError_t launch_sdpa_decode_q8(const DecodeQ8Args& a, int dtype, int qtype, v
   p.scores = a.weights != nullptr
                  ? reinterpret_cast<float*>(static_cast<char*>(ws) + w.scores) : nullptr;
   p.Lpad = w.Lpad;
+  if (alone(a.B, a.H, a.Hkv, a.Nq, a.Lmax))
+    return dtype == 1 ? launch_alone<__nv_bfloat16>(p, qtype, s) : launch_alone<float>(p, qtype, s);
   return dtype == 1 ? launch_all<__nv_bfloat16>(p, qtype, blocks, s)
                     : launch_all<float>(p, qtype, blocks, s);
 }
