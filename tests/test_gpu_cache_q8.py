@@ -670,3 +670,67 @@ def test_wrappers_refuse():
                            workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
     with pytest.raises(mha.MhaError):                   # a broadcast tensor has strides of 0
         mha.kv_append_q8(cache, q[:, :1].expand(1, 2, 1, 64), q, n)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_views_of_one_projection(dtype):
+    """q, k and v as views of one [B, N, 3, H, 64] buffer give what copies of them give."""
+    g = rng(1000)
+    B, N, H = 2, 150, 3
+    x = dev(fin(g.standard_normal((B, N, 3, H, 64)), dtype), DT[dtype])
+    views = [x[:, :, i].transpose(1, 2) for i in range(3)]
+    results = []
+    for q, k, v in (views, [t.contiguous() for t in views]):
+        cache = mha.kv_cache_q8(B, H, 200, 32)
+        n = i32([0, 3])
+        mha.kv_append_q8(cache, k, v, n, i32([150, 99]))
+        _, lse = mha.sdpa_with_lse(q, k, v, "causal")
+        mha.sdpa_key_weights(q, k, lse, "causal", None, i32([150, 99]), weights=cache.weights)
+        O = mha.sdpa_decode_q8(q[:, :, 5:9], cache, i32([150, 102]), add_weights=True)
+        results.append((O, lse, from_gpu(cache)))
+    a, b = results
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert_same(a[2], b[2], "e4m3", "views")
+
+
+@pytest.mark.parametrize("dtype,N", [("bf16", 130), ("bf16", 700), ("f32", 40), ("f32", 333)])
+def test_captured_prompts_replay(dtype, N):
+    """A prompt's append, attention weights and eviction in a graph, replayed with new prompts and
+    lengths, give what the same calls give outside (queries split over CTAs and not)."""
+    g = rng(1010)
+    B, H, G = 2, 2, 2
+    prompts = [[dev(fin(g.standard_normal((B, h, N, 64)), dtype), DT[dtype])
+                for h in (H * G, H, H)] + [i32(n)] for n in ([N, N // 2], [1, N], [0, N - 1])]
+
+    def run(cache, small, q, k, v, lens, lse, zero, n_out, kept):
+        cache.weights.zero_()
+        mha.kv_append_q8(cache, k, v, zero, lens)
+        mha.sdpa_key_weights(q, k, lse, "causal", None, lens, weights=cache.weights)
+        mha.kv_evict_q8(cache, small, lens, 30, 3, len_out=n_out, kept=kept)
+
+    def buffers():
+        return (mha.kv_cache_q8(B, H, N + 5, 16, weights=True), mha.kv_cache_q8(B, H, 30, 16),
+                i32([0, 0]), i32([0, 0]), torch.zeros(B, H, 30, dtype=torch.int32, device="cuda"))
+
+    def lse_of(q, k, v):
+        return mha.sdpa_with_lse(q, k.repeat_interleave(G, 1), v.repeat_interleave(G, 1),
+                                 "causal")[1]
+
+    cache, small, zero, n_out, kept = buffers()
+    want = []
+    for q, k, v, lens in prompts:
+        run(cache, small, q, k, v, lens, lse_of(q, k, v), zero, n_out, kept)
+        want.append((n_out.clone(), kept.clone(), from_gpu(cache), from_gpu(small)))
+    cache, small, zero, n_out, kept = buffers()
+    q, k, v, lens = (t.clone() for t in prompts[0])
+    lse = lse_of(q, k, v)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(cache, small, q, k, v, lens, lse, zero, n_out, kept)
+    for p, (wn, wkept, wcache, wsmall) in zip(prompts, want):
+        for a, x in zip((q, k, v, lens, lse), p + [lse_of(*p[:3])]):
+            a.copy_(x)
+        graph.replay()
+        assert torch.equal(n_out, wn) and torch.equal(kept, wkept)
+        assert_same(from_gpu(cache), wcache, "e4m3", "cache")
+        assert_same(from_gpu(small), wsmall, "e4m3", "evicted")
