@@ -56,8 +56,9 @@ __device__ __forceinline__ void q8_decode4(uint32_t u, float (&f)[4]) {
   }
 }
 
-// Codes under a scale that is 1 / ratio times as large, ratio <= 1.  Powers of two, as the library's
-// own scales have, in fp16: a product that is not exact there is below 2^-20, or rounded once.
+// Codes under a scale that is 1 / ratio times as large, ratio <= 1.  Powers of two, as the
+// library's own scales have, in fp16: a product that is not exact there is below 2^-20, or rounded
+// once.
 template <int QT>
 __device__ __forceinline__ uint32_t q8_rescale4(uint32_t u, float ratio) {
   if ((__float_as_uint(ratio) & 0x7fffffu) == 0) {

@@ -20,8 +20,8 @@
 // terms in registers; chunks of 32 queries are split into terms once per CTA, in shared memory,
 // the next chunk on its way from global memory meanwhile.  The (head, chunk) pairs are split over
 // CTAs as above.  8 heads x 8 padded prompts of up to 1000 take 59 us, a causal prompt of 1024 23
-// us; with one fp32 multiply-add per term and lane = key, whose operands came from shared memory at a
-// quarter of the units' rate, 156 and 58 us.  Bound by the products and their scaling: each score
+// us; with one fp32 multiply-add per term and lane = key, whose operands came from shared memory
+// at a quarter of the units' rate, 156 and 58 us.  Bound by the products and their scaling: each score
 // costs three products of 64 terms, its four parts' sum and one exponential.
 #include <cuda_bf16.h>
 
