@@ -12,6 +12,7 @@
 // gather: one CTA per (block of the new cache, head, batch element) copies the block's rows; the
 // block takes the largest scale of the tokens it receives, and codes that came under a smaller
 // one are written under it.  Bound by HBM: 64 bytes read and written per row of K and of V.
+// 64 x 16 heads 4096 -> 1024: 65 us, 17 of them the select; 8 heads 131072 -> 8001 20 us.
 #include "launchers.h"
 #include "q8_common.cuh"
 

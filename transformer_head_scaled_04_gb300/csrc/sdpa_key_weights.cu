@@ -12,6 +12,7 @@
 // sum, a key's 128 columns in two halves, and two CTAs share an SM (320 threads, 99 KB, 256 TMEM
 // columns each): four summing warps per scheduler.  Where the key tiles alone leave SMs idle the
 // query tiles are split over several CTAs, their sums added by a second launch in a fixed order.
+// 8 x 16 heads x 4096 372 us (60% of the exponential unit's rate), causal 217; 32 x 8 x 256 12.
 //
 // fp32 (key_weights_f32_kernel): the same sums with mma.sync m16n8k16.  Rows of Q and K are scaled
 // by a power of two (largest value to [2^13, 2^14)) and split into two fp16 terms, 22 bits; three
@@ -21,8 +22,8 @@
 // the next chunk on its way from global memory meanwhile.  The (head, chunk) pairs are split over
 // CTAs as above.  8 heads x 8 padded prompts of up to 1000 take 59 us, a causal prompt of 1024 23
 // us; with one fp32 multiply-add per term and lane = key, whose operands came from shared memory
-// at a quarter of the units' rate, 156 and 58 us.  Bound by the products and their scaling: each score
-// costs three products of 64 terms, its four parts' sum and one exponential.
+// at a quarter of the units' rate, 156 and 58 us.  Bound by the products and their scaling: each
+// score costs three products of 64 terms, its four parts' sum and one exponential.
 #include <cuda_bf16.h>
 
 #include <algorithm>
