@@ -30,10 +30,19 @@ __device__ __forceinline__ uint32_t q8_encode4(float a, float b, float c, float 
     const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
     return lo | (hi << 16);
   } else {
-    auto one = [](float x) -> uint32_t {  // __float2int_rn(NaN) is 0
-      return static_cast<uint32_t>(max(-127, min(127, __float2int_rn(x)))) & 0xffu;
+    auto one = [](float x) -> int {  // (the maximum keeps a NaN, whose integer is 0)
+      float y;
+      asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(-127.f));
+      return __float2int_rn(y);
     };
-    return one(a) | (one(b) << 8) | (one(c) << 16) | (one(d) << 24);
+    // Two integers to bytes at a time, 127 at most: prompts of 4096 to 8 x 16 heads 36 us; with
+    // clamped integers shifted into place 41, with integers rounded by adding 1.5 * 2^23 45
+    uint32_t u;
+    asm("{\n\t.reg .b32 t;\n\tcvt.pack.sat.s8.s32.b32 t, %4, %3, 0;\n\t"
+        "cvt.pack.sat.s8.s32.b32 %0, %2, %1, t;\n\t}"
+        : "=r"(u)
+        : "r"(one(a)), "r"(one(b)), "r"(one(c)), "r"(one(d)));
+    return u;
   }
 }
 
