@@ -5,9 +5,9 @@
 // keys and 128 for the values, so a block's scale has one writer and needs no atomics.  Bound by
 // HBM for prompts (2 or 4 bytes read and 1 written per value); for single tokens by the launch.
 // Each thread holds 16 values of a row: four threads read a row's 64 values, so a warp's loads
-// cover whole rows.  Prompts of 4096 tokens to 8 x 16 heads, bf16: 36 us in integers, 35 in e4m3, 5.6
-// TB/s (integers took 49 us instead of 44 when values were widened to fp32 as they arrived: fewer
-// loads in flight); one token to 64 x 16 heads 4.2 us.
+// cover whole rows.  Prompts of 4096 tokens to 8 x 16 heads, bf16: 36 us in integers, 35 in e4m3,
+// 5.6 TB/s (integers took 49 us instead of 44 when values were widened to fp32 as they arrived:
+// fewer loads in flight); one token to 64 x 16 heads 4.2 us.
 #include <cuda_bf16.h>
 
 #include "launchers.h"
