@@ -1,0 +1,119 @@
+"""The 8-bit cache at the ends of what its entry points take: huge scores, value scales far apart,
+rows far below or above 1, scales that are no powers of two, many heads, and the special rows on
+every launch path of the generation step.
+
+A generation step has three paths: one launch (up to 768 positions, 152 cache heads, 16 rows to a
+head), and two whose second joins a row's pieces, with a block to a row where rows are few and
+pieces many, else with a warp to a row.  ``PATHS`` has sizes for each.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from oracle import cache_q8 as oq
+from test_gpu_cache_q8 import (CODE, DT, assert_same, close_decode, close_weights, dev, fin, finite,
+                               from_gpu, i32, rng, strange, to_gpu)
+
+pytestmark = pytest.mark.gpu
+
+mha = pytest.importorskip("transformer_head_scaled_04_gb300")
+
+PATHS = {"one launch": (1, 2, 100), "block join": (1, 1, 5000), "warp join": (40, 4, 790)}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from transformer_head_scaled_04_gb300 import build
+
+    build.build()
+    mha.load_library()
+    torch.cuda.set_device(0)
+    mha.device_status()
+    yield
+    assert mha.device_status() == 0, "a kernel recorded a device-side error"
+
+
+def check_path(path, B, Hkv, rows, Lmax):
+    need = mha.decode_q8_workspace_size(B, Hkv * rows, Hkv, 1, Lmax, True)
+    assert (need == 0) == (path == "one launch")
+
+
+def one_key_cache(g, B, H, Lmax, block, code, sign, flip):
+    """Key codes that lie along `sign` [64].  With a query sign * a, position j0 of every head has a
+    score of 104 * 64 a (flip: -56 * 64 a) and every other one at most 80 (-96) * 64 a."""
+    c = finite(strange(g, B, H, Lmax, block, code), code)
+    along = np.array([oq.encode_ref(x * sign, code) for x in range(-104, 104, 8)])
+    pick = g.integers(0, 2 if flip else 24, (B, H, Lmax))      # -104, -96 or anything to 80
+    c["k"] = along[pick]
+    j0 = int(g.integers(0, Lmax))
+    c["k"][:, :, j0] = oq.encode_ref((-56 if flip else 104) * sign, code)
+    c["k_scale"][...] = 2.0 ** -10
+    c["weights"][...] = 0
+    return c, j0
+
+
+def rounded_apart(target):
+    return 2.0 ** -22 * 1.4427 * target if target * 1.4427 < 4096 else 0.0
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("code,flip", [("e4m3", False), ("int8", True)])
+@pytest.mark.parametrize("target", [1e3, 1e5, 3e6, 2.2e7, 1e8, 1e9, 1e30])
+def test_decode_weights_of_rows_with_huge_scores(path, dtype, code, flip, target):
+    """The best key is 24/104 of the target or more ahead of every other, so it has all the weight
+    (e^-173 for any other where the target is 1e3): 1 from each row, up to the rounding of the
+    exponential and the division (2^-19).  Up to 4096 in base 2 the score, its maximum and the
+    exponent's shift may each be rounded to fp32 apart: 3 * 2^-24 ln 2 of the base-2 score, less
+    than 2^-22."""
+    B, H, Lmax = PATHS[path]
+    check_path(path, B, H, 3, Lmax)
+    g = rng(1100 + int(flip))
+    sign = g.choice([-1.0, 1.0], 64)
+    c, j0 = one_key_cache(g, B, H, Lmax, 32, code, sign, flip)
+    Q = np.empty((B, 3 * H, 1, 64))
+    Q[...] = sign * target / (104 * 64 / 8 * 2.0 ** -10)
+    Q[:, ::3] *= 0.75
+    Q = fin(Q, dtype)
+    cache = to_gpu(c, 32, code)
+    O = mha.sdpa_decode_q8(dev(Q, DT[dtype]), cache, i32([Lmax] * B), add_weights=True)
+    w = cache.weights.double().cpu().numpy()
+    r = 2.0 ** -19 + rounded_apart(target)
+    assert np.abs(w[:, :, j0] - 3).max() <= 3 * r
+    w[:, :, j0] = 0
+    assert np.abs(w).max() <= 1e-20
+    v = oq.values_ref(c["v"][:, :, j0], code) * c["v_scale"][:, :, j0 // 32, None]
+    err = np.abs(O.double().cpu().numpy()[:, :, 0] - np.repeat(v, 3, 1))
+    bound = (2.0 ** -8 + 2.0 ** -11 if dtype == "bf16" else r) * np.abs(v) + 1e-30
+    assert np.all(err <= np.repeat(bound, 3, 1))
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("target", [1e3, 1e5, 2.2e7, 1e9, 1e30])
+@pytest.mark.parametrize("flip", [False, True])
+def test_decode_equal_huge_scores_share_the_weight(path, dtype, target, flip):
+    """Two equal keys in blocks whose values' scales differ: a half each, whatever the scores."""
+    B, H, Lmax = PATHS[path]
+    g = rng(1150)
+    sign = g.choice([-1.0, 1.0], 64)
+    c, j0 = one_key_cache(g, B, H, Lmax, 32, "int8", sign, flip)
+    j1 = (j0 + Lmax // 2) % Lmax
+    c["k"][:, :, j1] = c["k"][:, :, j0]
+    c["v_scale"][:, :, j0 // 32], c["v_scale"][:, :, j1 // 32] = 2.0 ** -6, 2.0 ** 3
+    Q = np.empty((B, H, 1, 64))
+    Q[...] = sign * target / (104 * 64 / 8 * 2.0 ** -10)
+    cache = to_gpu(c, 32, "int8")
+    O = mha.sdpa_decode_q8(dev(fin(Q, dtype), DT[dtype]), cache, i32([Lmax] * B), add_weights=True)
+    r = 2.0 ** -19 + rounded_apart(target)
+    w = cache.weights.double().cpu().numpy()
+    assert np.abs(w[:, :, [j0, j1]] - 0.5).max() <= 0.5 * r
+    v = [oq.values_ref(c["v"][:, :, j], "int8") * c["v_scale"][:, :, j // 32, None]
+         for j in (j0, j1)]
+    pv = (np.abs(v[0]) + np.abs(v[1])) / 2
+    if dtype == "bf16":
+        r += 2.0 ** -11
+    want = (v[0] + v[1]) / 2
+    bound = r * pv + (2.0 ** -8 * np.abs(want) if dtype == "bf16" else 0)
+    assert np.all(np.abs(O.double().cpu().numpy()[:, :, 0] - want) <= bound + 1e-30)

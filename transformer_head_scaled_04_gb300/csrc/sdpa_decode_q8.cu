@@ -31,7 +31,10 @@
 // row's largest value to [2^13, 2^14)) and rounded to fp16, which holds every bf16 significand;
 // fp32 queries and weights are split into two fp16 terms (22 bits) and their products done
 // twice, each inner step's part of a score and each tile's PV summed apart and added in fp32
-// (the tensor cores' own accumulation truncates).
+// (the tensor cores' own accumulation truncates).  With bf16 queries the four inner steps and the
+// tiles' PV are summed by the tensor cores and a weight is one fp16 term, 2^-12 off at most: an
+// eighth of the output's own rounding to bf16 even if all of a row's weights erred alike.  Beyond
+// references of 4096 exponents are differences of two scores, rounded as the stored ones.
 // Runs end at heads' ends: each piece leaves (O, m, l) in the workspace, and a second launch
 // joins a row's pieces, and adds the weights 2^(x_ij - m_i) / l_i from the scores that the first
 // one stored.  Short caches of few heads take one launch, a block to a head, whose warps' pieces
@@ -60,6 +63,8 @@ constexpr int kSlotBytes = 2 * kTileBytes;
 constexpr int kWarps = 8;                  // of the join
 constexpr int kThreads = kWarps * 32;
 constexpr float kOffset = 13.f;            // weights that meet the codes: 2^13 at most
+constexpr float kLift = 8192.f;            // 2^kOffset
+constexpr float kHuge = 4096.f;            // references beyond it: careful_tile()
 constexpr float kNone = -3.402823466e38f;  // maximum of no position (finite: -inf - it is -inf)
 
 // How the rows of a cache head are cut: groups of 8 * NR rows, NR column tiles of the products
@@ -83,6 +88,12 @@ RowPlan row_plan(int H, int Hkv, int Nq, int dtype) {
 // -> 99.5 us) or kept more requests in flight than HBM takes well (64 x 16 heads x 4096 positions,
 // three slots each, 87.4 -> 91.9 us), eight left the tensor cores waiting (95.9 -> 102.4 us).
 constexpr int main_warps(int terms, int nr) { return terms * nr <= 2 ? 12 : 8; }
+// Threads that the registers are shared out for.  bf16 queries of one column tile take 128 each at
+// most, as for 16 warps, which leaves room for a block of the join to wait on the SM (one sequence
+// of 131072, 8 heads: 27.1 us; with the 137 they would take 28.6)
+constexpr int register_threads(int terms, int nr) {
+  return terms * nr == 1 ? 512 : main_warps(terms, nr) * 32;
+}
 // workers at most, as far as the workspace goes (a GB300 has 152 SMs)
 constexpr int max_workers(int terms, int nr) { return 160 * main_warps(terms, nr); }
 
@@ -288,7 +299,7 @@ __device__ __forceinline__ float join_lanes(float& m, float& l, float2 st, float
 // kAlone: a block per cache head (of one row group), whose tiles its warps share; pieces and scores
 // meet in shared memory, and no second launch is needed.
 template <typename T, int QT, int NR, bool kAlone>
-__global__ void __launch_bounds__(main_warps(sizeof(T) / 2, NR) * 32, 1)
+__global__ void __launch_bounds__(register_threads(sizeof(T) / 2, NR), 1)
     decode_q8_kernel(const Params p) {
   constexpr int kTerms = sizeof(T) == 4 ? 2 : 1;
   const DecodeQ8Args& a = p.a;
@@ -485,211 +496,307 @@ __global__ void __launch_bounds__(main_warps(sizeof(T) / 2, NR) * 32, 1)
       score_row = alone_scores + 2 * t * p.Lpad + g;
     if (!kAlone && p.scores != nullptr)
       score_row = p.scores + (head * p.rp.R + c.rg * (8 * NR) + 2 * t) * p.Lpad + g;
-    // A maximum's rounding beyond 2^20 is too coarse for exponents that are rounded once: there
-    // they are taken from scores rounded as the maximum was
+    // Beyond kHuge a reference is too coarse for exponents in which the offset and the value's
+    // scale are rounded together with it (from 2^24 on they would be lost)
     bool huge = false;
-    float sc_next = load_scale(c.kt);
+    float sc_next = load_scale(c.kt), sc = 1.f, sc_log = 0.f, sc_inv = 1.f;
     const int last = min(c.nt, c.kt + count - done);
     done += last - c.kt;
-    for (; c.kt < last; ++c.kt) {
-      const float sc = sc_next;
+    const uint8_t *sK = nullptr, *sV = nullptr;
+    int pos = 0;
+    // tile c.kt once it has landed, and the next one to ask for into its slot
+    auto begin_tile = [&]() {
+      sc = sc_next;
       if (c.kt + 1 < last) sc_next = load_scale(c.kt + 1);  // a tile ahead of its use
-      const float sc_log = log2_approx(sc), sc_inv = rcp_approx(sc);
+      sc_log = log2_approx(sc);
+      sc_inv = rcp_approx(sc);
       copy_async_wait<kStages - 1>();  // this lane's copies of the tile have landed
       __syncwarp();                    // and every lane's
-      const uint8_t* sK = ring + slot * kSlotBytes;
-      const uint8_t* sV = sK + kTileBytes;
-      const int pos = c.kt * kTile;
-      // kEdge: some row may not see the whole tile (or `huge`).  Its code apart: in one body it
-      // cost the other tiles 78 of 562 instructions and 14% of the time (16 rows, 8 x 8 x 16384
-      // positions)
-      auto tile = [&](auto edge_type) -> bool {
-        constexpr bool kEdge = decltype(edge_type)::value;
-        // ---- scores of two groups of 16 positions
-        float x[2][NR][4];
+      sK = ring + slot * kSlotBytes;
+      sV = sK + kTileBytes;
+      pos = c.kt * kTile;
+    };
+    auto end_tile = [&]() {
+      __syncwarp();  // every lane has read the slot
+      ask(slot);
+      if (++slot == kStages) slot = 0;
+    };
+    // ---- what both forms of a tile do with a group q of 16 positions
+    // products of its keys and the queries: positions g, g + 8 (rows 2t, 2t + 1 of row group nr)
+    auto scores = [&](int q, float (&x)[NR][4]) {
+      uint32_t h[2][8];  // positions g and g + 8: 16-byte chunk t of a row
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t h[2][8];  // positions g and g + 8: 16-byte chunk t of a row
+      for (int z = 0; z < 2; ++z) {
+        const int row = q * 16 + z * 8 + g;
+        const uint4 u = *reinterpret_cast<const uint4*>(sK + row * kD + k_at);
+        codes_to_half<QT>(u.x, h[z][0], h[z][1]);
+        codes_to_half<QT>(u.y, h[z][2], h[z][3]);
+        codes_to_half<QT>(u.z, h[z][4], h[z][5]);
+        codes_to_half<QT>(u.w, h[z][6], h[z][7]);
+      }
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr) {
+        float part[kTerms == 2 ? 4 : 1][4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t fa[4] = {h[0][2 * k], h[1][2 * k], h[0][2 * k + 1], h[1][2 * k + 1]};
+          float (&d)[4] = part[kTerms == 2 ? k : 0];
+          if constexpr (kTerms == 2)
+            mma16816_zero(d, fa, qf[kTerms - 1][nr][k][0], qf[kTerms - 1][nr][k][1]);
+          if (kTerms == 1 && k == 0)
+            mma16816_zero(d, fa, qf[0][nr][k][0], qf[0][nr][k][1]);
+          else
+            mma16816(d, fa, qf[0][nr][k][0], qf[0][nr][k][1]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[nr][i] = part[0][i];
+          if constexpr (kTerms == 2)
+            x[nr][i] = (part[0][i] + part[1][i]) + (part[2][i] + part[3][i]);
+        }
+      }
+    };
+    // its value rows 2t, 2t+1, 2t+8, 2t+9, columns 8g .. 8g+7
+    auto value_codes = [&](int q, uint2 (&v)[4]) {
+#pragma unroll
+      for (int z = 0; z < 4; ++z) {
+        const int row = q * 16 + 2 * t + (z >> 1) * 8 + (z & 1);
+        v[z] = *reinterpret_cast<const uint2*>(sV + row * kD + v_at);
+      }
+    };
+    // the same as product operands: column 8g + j, rows 2t, 2t+1 in b0[j], 2t+8, 2t+9 in b1[j]
+    auto value_halves = [&](const uint2 (&v)[4], uint32_t (&b0)[8], uint32_t (&b1)[8]) {
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        const uint32_t a0 = z ? v[0].y : v[0].x, a1 = z ? v[1].y : v[1].x;
+        const uint32_t a2 = z ? v[2].y : v[2].x, a3 = z ? v[3].y : v[3].x;
+        codes_to_half<QT>(__byte_perm(a0, a1, 0x5140), b0[4 * z], b0[4 * z + 1]);
+        codes_to_half<QT>(__byte_perm(a0, a1, 0x7362), b0[4 * z + 2], b0[4 * z + 3]);
+        codes_to_half<QT>(__byte_perm(a2, a3, 0x5140), b1[4 * z], b1[4 * z + 1]);
+        codes_to_half<QT>(__byte_perm(a2, a3, 0x7362), b1[4 * z + 2], b1[4 * z + 3]);
+      }
+    };
+    // the largest value of a row's 16 positions
+    auto row_max = [](float v) -> float {
+      v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+      v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+      return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+    };
+    // the rows' references rise to `top`, and O and l with them
+    auto rise = [&](const float (&top)[NR][2]) {
+      bool far = false;
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float v = fmaxf(m[nr][e], top[nr][e]);
+          // a first maximum finds O = l = 0
+          const float u = v == m[nr][e] ? 1.f : ex2_approx(m[nr][e] - v);
+          m[nr][e] = v;
+          far |= fabsf(v) > kHuge && v != kNone;
+          (e ? l[nr].y : l[nr].x) *= u;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            o[nr][j][e] *= u;
+            o[nr][j][2 + e] *= u;
+          }
+        }
+      huge = __any_sync(0xffffffffu, far);
+    };
+    // A tile that every row sees, under references that are not huge.  False: one became so.  The
+    // tile is to be taken again then, by the other form: nothing but the references, O and l under
+    // them has changed
+    auto tile = [&]() -> bool {
+      float x[2][NR][4];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) scores(q, x[q]);
+      // ---- the scales: a score is x * f, its exponent x * f + log2 of the value's scale
+      float2 f[2][NR];
+      float ev[2], inv[2];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const float ks = __shfl_sync(0xffffffffu, sc, q);
+        ev[q] = __shfl_sync(0xffffffffu, sc_log, 2 + q);
+        inv[q] = __shfl_sync(0xffffffffu, sc_inv, 2 + q);
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr)
+          f[q][nr] = fmul2(make_float2(ks, ks), qs[nr]);
+      }
+      if (score_row != nullptr) {  // kept for the weights
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (nr * 8 + e < rows_here) {
+              float* dst = score_row + (nr * 8 + e) * p.Lpad + pos;
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                const float fe = e ? f[q][nr].y : f[q][nr].x;
+                dst[q * 16] = x[q][nr][e] * fe;
+                dst[q * 16 + 8] = x[q][nr][2 + e] * fe;
+              }
+            }
+      }
+      // ---- running maximum
+      float top[NR][2];
+      bool grew = false;
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          top[nr][e] = fmaxf(
+              fmaf(fmaxf(x[0][nr][e], x[0][nr][2 + e]), e ? f[0][nr].y : f[0][nr].x, ev[0]),
+              fmaf(fmaxf(x[1][nr][e], x[1][nr][2 + e]), e ? f[1][nr].y : f[1][nr].x, ev[1]));
+          grew |= top[nr][e] > m[nr][e];
+        }
+      if (__any_sync(0xffffffffu, grew)) {  // seldom, once a row has seen many positions
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) top[nr][e] = row_max(top[nr][e]);
+        rise(top);
+        if (huge) return false;
+      }
+      // ---- weights, 16 positions at a time, and their product with the value codes
+      [[maybe_unused]] float po[kTerms == 2 ? NR : 1][4][4];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t pf[kTerms][NR][2];
+        // the fp32 path keeps the offset out of the exponent, whose rounding it would coarsen
+        const float up = ev[q] + (kTerms == 2 ? 0.f : kOffset);
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) {
+          const float2 shift = make_float2(up - m[nr][0], up - m[nr][1]);
 #pragma unroll
           for (int z = 0; z < 2; ++z) {
-            const int row = q * 16 + z * 8 + g;
-            const uint4 u = *reinterpret_cast<const uint4*>(sK + row * kD + k_at);
-            codes_to_half<QT>(u.x, h[z][0], h[z][1]);
-            codes_to_half<QT>(u.y, h[z][2], h[z][3]);
-            codes_to_half<QT>(u.z, h[z][4], h[z][5]);
-            codes_to_half<QT>(u.w, h[z][6], h[z][7]);
+            float2 w = make_float2(x[q][nr][2 * z], x[q][nr][2 * z + 1]);
+            w = ffma2(w, f[q][nr], shift);
+            w.x = ex2_approx(w.x);
+            w.y = ex2_approx(w.y);
+            if constexpr (kTerms == 2) w = fmul2(w, make_float2(kLift, kLift));
+            l[nr] = ffma2(w, make_float2(inv[q], inv[q]), l[nr]);
+            const uint32_t hi = pack_half(w.x, w.y);
+            pf[0][nr][z] = transpose8x8(hi);
+            if constexpr (kTerms == 2)
+              pf[kTerms - 1][nr][z] = transpose8x8(pack_rest(w.x, w.y, hi));
           }
+        }
+        uint2 v[4];
+        uint32_t b0[8], b1[8];
+        value_codes(q, v);
+        value_halves(v, b0, b1);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t fa[4] = {b0[2 * j], b0[2 * j + 1], b1[2 * j], b1[2 * j + 1]};
 #pragma unroll
           for (int nr = 0; nr < NR; ++nr) {
-            float part[kTerms == 2 ? 4 : 1][4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t fa[4] = {h[0][2 * k], h[1][2 * k], h[0][2 * k + 1], h[1][2 * k + 1]};
-              float (&d)[4] = part[kTerms == 2 ? k : 0];
-              if constexpr (kTerms == 2)
-                mma16816_zero(d, fa, qf[kTerms - 1][nr][k][0], qf[kTerms - 1][nr][k][1]);
-              if (kTerms == 1 && k == 0)
-                mma16816_zero(d, fa, qf[0][nr][k][0], qf[0][nr][k][1]);
+            if constexpr (kTerms == 2) {
+              if (q == 0)
+                mma16816_zero(po[nr][j], fa, pf[kTerms - 1][nr][0], pf[kTerms - 1][nr][1]);
               else
-                mma16816(d, fa, qf[0][nr][k][0], qf[0][nr][k][1]);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              x[q][nr][i] = part[0][i];
-              if constexpr (kTerms == 2)
-                x[q][nr][i] = (part[0][i] + part[1][i]) + (part[2][i] + part[3][i]);
-              if (kEdge && pos + q * 16 + (i >> 1) * 8 + g > lim[nr][i & 1])
-                x[q][nr][i] = -INFINITY;
+                mma16816(po[nr][j], fa, pf[kTerms - 1][nr][0], pf[kTerms - 1][nr][1]);
+              mma16816(po[nr][j], fa, pf[0][nr][0], pf[0][nr][1]);
+            } else {
+              mma16816(o[nr][j], fa, pf[0][nr][0], pf[0][nr][1]);
             }
           }
         }
-        // ---- the scales: a score is x * f, its exponent x * f + log2 of the value's scale
-        float2 f[2][NR];
-        float ev[2], inv[2];
+      }
+      if constexpr (kTerms == 2) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const float ks = __shfl_sync(0xffffffffu, sc, q);
-          ev[q] = __shfl_sync(0xffffffffu, sc_log, 2 + q);
-          inv[q] = __shfl_sync(0xffffffffu, sc_inv, 2 + q);
+        for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-          for (int nr = 0; nr < NR; ++nr)
-            f[q][nr] = fmul2(make_float2(ks, ks), qs[nr]);
-        }
-        if (score_row != nullptr) {  // kept for the weights
+          for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              if (nr * 8 + e < rows_here) {
-                float* dst = score_row + (nr * 8 + e) * p.Lpad + pos;
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                  const float fe = e ? f[q][nr].y : f[q][nr].x;
-                  dst[q * 16] = x[q][nr][e] * fe;
-                  dst[q * 16 + 8] = x[q][nr][2 + e] * fe;
-                }
-              }
-        }
-        // ---- running maximum
-        float top[NR][2];
+            for (int i = 0; i < 4; ++i) o[nr][j][i] += po[nr][j][i];
+      }
+      return true;
+    };
+    // Any tile, its two groups in turn, which takes half the code (in one body with the above, masks
+    // cost the other tiles 78 of 562 instructions and 14% of the time: 16 rows, 8 x 8 x 16384
+    // positions; both groups at once as above 153 us instead of 141 at 128 rows, for its
+    // registers).  Weights are 2^(x - ref) under the largest score of the row's 16 positions: the
+    // difference of two scores is exact where it counts, whatever their size.  2^(ref - m) brings
+    // their sum under the row's reference and, with the values' scale, their product.
+    auto careful_tile = [&]() {
+#pragma unroll 1
+      for (int q = 0; q < 2; ++q) {
+        float x[NR][4], ref[NR][2], top[NR][2];
+        scores(q, x);
+        const float ks = __shfl_sync(0xffffffffu, sc, q);
+        const float vs = __shfl_sync(0xffffffffu, sc, 2 + q);
+        const float ev = __shfl_sync(0xffffffffu, sc_log, 2 + q);
         bool grew = false;
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            top[nr][e] = fmaxf(
-                fmaf(fmaxf(x[0][nr][e], x[0][nr][2 + e]), e ? f[0][nr].y : f[0][nr].x, ev[0]),
-                fmaf(fmaxf(x[1][nr][e], x[1][nr][2 + e]), e ? f[1][nr].y : f[1][nr].x, ev[1]));
+            const float f = ks * (e ? qs[nr].y : qs[nr].x);
+            const int at = pos + q * 16 + g;
+            x[nr][e] = at > lim[nr][e] ? -INFINITY : __fmul_rn(x[nr][e], f);
+            x[nr][2 + e] = at + 8 > lim[nr][e] ? -INFINITY : __fmul_rn(x[nr][2 + e], f);
+            if (score_row != nullptr && nr * 8 + e < rows_here) {
+              float* dst = score_row + (nr * 8 + e) * p.Lpad + pos + q * 16;
+              dst[0] = x[nr][e];
+              dst[8] = x[nr][2 + e];
+            }
+            float v = fmaxf(x[nr][e], x[nr][2 + e]);
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+            ref[nr][e] = v;
+            top[nr][e] = v + ev;
             grew |= top[nr][e] > m[nr][e];
           }
-        if (__any_sync(0xffffffffu, grew)) {  // seldom, once a row has seen many positions
-          bool far = false;
+        if (__any_sync(0xffffffffu, grew)) rise(top);
+        uint2 v[4];
+        uint32_t b0[8], b1[8];
+        value_codes(q, v);
 #pragma unroll
-          for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float v = top[nr][e];
-              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-              v = fmaxf(m[nr][e], v);
-              // a first maximum finds O = l = 0
-              const float u = v == m[nr][e] ? 1.f : ex2_approx(m[nr][e] - v);
-              m[nr][e] = v;
-              far |= fabsf(v) > 1048576.f && v != kNone;
-              (e ? l[nr].y : l[nr].x) *= u;
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                o[nr][j][e] *= u;
-                o[nr][j][2 + e] *= u;
-              }
-            }
-          huge = __any_sync(0xffffffffu, far);
+        for (int z = 0; z < 4; ++z) {
+          // rows behind the last position hold anything: 0.  A NaN among the rows that some query
+          // may not see must reach only those that do: taken out of the product here, put into O
+          // below
+          if (pos + q * 16 + 2 * t + (z >> 1) * 8 + (z & 1) >= c.L) v[z] = make_uint2(0u, 0u);
+          if constexpr (QT == kE4m3) {
+            v[z].x &= ~__vcmpeq4(v[z].x & 0x7f7f7f7fu, 0x7f7f7f7fu);
+            v[z].y &= ~__vcmpeq4(v[z].y & 0x7f7f7f7fu, 0x7f7f7f7fu);
+          }
         }
-        if (!kEdge && huge) return false;  // taken again below: nothing so far depends on it
-        // ---- weights, 16 positions at a time, and their product with the value codes
-        [[maybe_unused]] float po[kTerms == 2 ? NR : 1][4][4];
+        value_halves(v, b0, b1);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t pf[kTerms][NR][2];
-          // the fp32 path keeps the offset out of the exponent, whose rounding it would coarsen
-          const float up = ev[q] + (kTerms == 2 ? 0.f : kOffset);
+        for (int nr = 0; nr < NR; ++nr) {
+          uint32_t pf[kTerms][2];
+          float into_l[2], into_o[2];
 #pragma unroll
-          for (int nr = 0; nr < NR; ++nr) {
-            const float2 shift = make_float2(up - m[nr][0], up - m[nr][1]);
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              float2 w = make_float2(x[q][nr][2 * z], x[q][nr][2 * z + 1]);
-              if constexpr (kEdge)  // two roundings (a packed pair of operations may be fused)
-                w = make_float2(__fadd_rn(__fmul_rn(w.x, f[q][nr].x), shift.x),
-                                __fadd_rn(__fmul_rn(w.y, f[q][nr].y), shift.y));
-              else
-                w = ffma2(w, f[q][nr], shift);
-              w.x = ex2_approx(w.x);
-              w.y = ex2_approx(w.y);
-              if constexpr (kTerms == 2) w = fmul2(w, make_float2(8192.f, 8192.f));  // 2^kOffset
-              l[nr] = ffma2(w, make_float2(inv[q], inv[q]), l[nr]);
-              const uint32_t hi = pack_half(w.x, w.y);
-              pf[0][nr][z] = transpose8x8(hi);
-              if constexpr (kTerms == 2)
-                pf[kTerms - 1][nr][z] = transpose8x8(pack_rest(w.x, w.y, hi));
-            }
+          for (int e = 0; e < 2; ++e) {
+            into_l[e] = ex2_approx(ref[nr][e] - m[nr][e]);
+            into_o[e] = into_l[e] * vs;
+            if (ref[nr][e] == -INFINITY) ref[nr][e] = 0.f;  // none allowed: weights of 0
           }
-          // value rows 2t, 2t+1, 2t+8, 2t+9 of the 16, columns 8g .. 8g+7
-          uint2 v[4];
-#pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            const int row = q * 16 + 2 * t + (z >> 1) * 8 + (z & 1);
-            v[z] = *reinterpret_cast<const uint2*>(sV + row * kD + v_at);
-            if constexpr (kEdge) {
-              // rows behind the last position hold anything: 0.  A NaN among the rows that some
-              // query may not see must reach only those that do: taken out of the product here,
-              // put into O below
-              if (pos + row >= c.L) v[z] = make_uint2(0u, 0u);
-              if constexpr (QT == kE4m3) {
-                v[z].x &= ~__vcmpeq4(v[z].x & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                v[z].y &= ~__vcmpeq4(v[z].y & 0x7f7f7f7fu, 0x7f7f7f7fu);
-              }
-            }
-          }
-          uint32_t b0[8], b1[8];  // column 8g + j: rows 2t, 2t+1, and 2t+8, 2t+9
 #pragma unroll
           for (int z = 0; z < 2; ++z) {
-            const uint32_t a0 = z ? v[0].y : v[0].x, a1 = z ? v[1].y : v[1].x;
-            const uint32_t a2 = z ? v[2].y : v[2].x, a3 = z ? v[3].y : v[3].x;
-            codes_to_half<QT>(__byte_perm(a0, a1, 0x5140), b0[4 * z], b0[4 * z + 1]);
-            codes_to_half<QT>(__byte_perm(a0, a1, 0x7362), b0[4 * z + 2], b0[4 * z + 3]);
-            codes_to_half<QT>(__byte_perm(a2, a3, 0x5140), b1[4 * z], b1[4 * z + 1]);
-            codes_to_half<QT>(__byte_perm(a2, a3, 0x7362), b1[4 * z + 2], b1[4 * z + 3]);
+            const float w0 = ex2_approx(x[nr][2 * z] - ref[nr][0]) * kLift;
+            const float w1 = ex2_approx(x[nr][2 * z + 1] - ref[nr][1]) * kLift;
+            l[nr].x = fmaf(w0, into_l[0], l[nr].x);
+            l[nr].y = fmaf(w1, into_l[1], l[nr].y);
+            const uint32_t hi = pack_half(w0, w1);
+            pf[0][z] = transpose8x8(hi);
+            if constexpr (kTerms == 2) pf[kTerms - 1][z] = transpose8x8(pack_rest(w0, w1, hi));
           }
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const uint32_t fa[4] = {b0[2 * j], b0[2 * j + 1], b1[2 * j], b1[2 * j + 1]};
+            float d[4];
+            mma16816_zero(d, fa, pf[kTerms - 1][0], pf[kTerms - 1][1]);
+            if constexpr (kTerms == 2) mma16816(d, fa, pf[0][0], pf[0][1]);
 #pragma unroll
-            for (int nr = 0; nr < NR; ++nr) {
-              if constexpr (kTerms == 2) {
-                if (q == 0)
-                  mma16816_zero(po[nr][j], fa, pf[kTerms - 1][nr][0], pf[kTerms - 1][nr][1]);
-                else
-                  mma16816(po[nr][j], fa, pf[kTerms - 1][nr][0], pf[kTerms - 1][nr][1]);
-                mma16816(po[nr][j], fa, pf[0][nr][0], pf[0][nr][1]);
-              } else {
-                mma16816(o[nr][j], fa, pf[0][nr][0], pf[0][nr][1]);
-              }
-            }
+            for (int i = 0; i < 4; ++i) o[nr][j][i] = fmaf(d[i], into_o[i & 1], o[nr][j][i]);
           }
         }
-        if constexpr (kTerms == 2) {
-#pragma unroll
-          for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) o[nr][j][i] += po[nr][j][i];
-        }
-        if constexpr (QT == kE4m3 && kEdge) {
+        if constexpr (QT == kE4m3) {
           // columns 8g .. 8g+7 of each position: NaN into the rows that see it
-          for (int row = 0; row < kTile && pos + row < c.L; ++row) {
+          for (int row = q * 16; row < q * 16 + 16 && pos + row < c.L; ++row) {
             const uint2 u = *reinterpret_cast<const uint2*>(
                 sV + row * kD + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + (g & 1) * 8);
             if ((__vcmpeq4(u.x & 0x7f7f7f7fu, 0x7f7f7f7fu) |
@@ -706,13 +813,24 @@ __global__ void __launch_bounds__(main_warps(sizeof(T) / 2, NR) * 32, 1)
                       o[nr][i >> 1][2 * (i & 1) + e] = __int_as_float(0x7fffffff);
           }
         }
-        return true;
-      };
-      if (pos + kTile - 1 > c.L - (a.causal ? a.Nq : 1) || !tile(std::false_type{}))
-        tile(std::true_type{});
-      __syncwarp();  // every lane has read the slot
-      ask(slot);
-      if (++slot == kStages) slot = 0;
+      }
+    };
+    // tiles that every row sees, then the others; a tile that `tile` could not finish is begun
+    const int seen = min(last, max((c.L - (a.causal ? a.Nq : 1) + 1) / kTile, 0));
+    bool begun = false;
+    for (; c.kt < seen; ++c.kt) {
+      begin_tile();
+      if (!tile()) {
+        begun = true;
+        break;
+      }
+      end_tile();
+    }
+    for (; c.kt < last; ++c.kt) {
+      if (!begun) begin_tile();
+      begun = false;
+      careful_tile();
+      end_tile();
     }
     end_segment();
     if (!kAlone && c.kt == c.nt) next_segment(p, c);
@@ -737,7 +855,8 @@ __global__ void __launch_bounds__(main_warps(sizeof(T) / 2, NR) * 32, 1)
       const int h = c.hk * (a.H / a.Hkv) + r / a.Nq;
       put2(static_cast<T*>(a.O) + c.b * a.so[0] + h * a.so[1] + (r % a.Nq) * a.so[2] + 2 * lane,
            o2.x * y, o2.y * y);
-      if (lane == 0) *reinterpret_cast<float2*>(alone_stat + 2 * r) = make_float2(kOffset - top, y);
+      // weight = 2^(x - top) 2^kOffset / sum: the difference of two scores first, as above
+      if (lane == 0) *reinterpret_cast<float2*>(alone_stat + 2 * r) = make_float2(top, y * kLift);
     }
     if (a.weights == nullptr) return;
     __syncthreads();
@@ -747,7 +866,7 @@ __global__ void __launch_bounds__(main_warps(sizeof(T) / 2, NR) * 32, 1)
       for (int r = 0; r < p.rp.R; ++r) {
         const float2 st = *reinterpret_cast<const float2*>(alone_stat + 2 * r);
         const float x = alone_scores[r * p.Lpad + j];
-        if (x != -INFINITY) w = fmaf(ex2_approx(x + st.x), st.y, w);
+        if (x != -INFINITY) w = fmaf(ex2_approx(x - st.x), st.y, w);
       }
       out[j] += w;
     }
@@ -933,9 +1052,9 @@ __global__ void __launch_bounds__(kThreads, 4) decode_q8_join_kernel(const Param
       m = kNone;
       l = 0.f;
       join_lanes<8>(m, l, mine, old);
-      if ((lane & 15) == 0) {  // weight = 2^(x + offset - m) / l (the pieces' own reference)
-        rowstat[2 * r] = kOffset - m;
-        rowstat[2 * r + 1] = l == 0.f ? 0.f : 1.f / l;
+      if ((lane & 15) == 0) {  // weight = 2^(x - m) 2^kOffset / l, x - m first as in the pieces
+        rowstat[2 * r] = m;
+        rowstat[2 * r + 1] = l == 0.f ? 0.f : kLift / l;
       }
     }
     __syncthreads();
@@ -954,7 +1073,7 @@ __global__ void __launch_bounds__(kThreads, 4) decode_q8_join_kernel(const Param
           const float v[4] = {x[u][k].x, x[u][k].y, x[u][k].z, x[u][k].w};
 #pragma unroll
           for (int i = 0; i < 4; ++i)  // an excluded position takes nothing of a NaN row
-            if (v[i] != -INFINITY) w[k][i] = fmaf(ex2_approx(v[i] + st.x), st.y, w[k][i]);
+            if (v[i] != -INFINITY) w[k][i] = fmaf(ex2_approx(v[i] - st.x), st.y, w[k][i]);
         }
       }
     };
