@@ -117,3 +117,53 @@ def test_decode_equal_huge_scores_share_the_weight(path, dtype, target, flip):
     want = (v[0] + v[1]) / 2
     bound = r * pv + (2.0 ** -8 * np.abs(want) if dtype == "bf16" else 0)
     assert np.all(np.abs(O.double().cpu().numpy()[:, :, 0] - want) <= bound + 1e-30)
+
+
+def weights_of(Q, c, b, h, row, L, block, code, scale=0.125):
+    s = oq.dequantised_ref(c, "k", b, h, L, block, code) @ np.asarray(Q[b, row, 0], np.float64)
+    p = np.exp(s * scale - (s * scale).max())
+    return p / p.sum()
+
+
+@pytest.mark.parametrize("copies,Lmax", [(1, 96), (1, 768), (240, 790)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("block", [16, 64])
+@pytest.mark.parametrize("apart", [11, 28, 38, 78])
+@pytest.mark.parametrize("order", ["large first", "small first", "mixed"])
+def test_decode_values_of_small_scale_beside_large(copies, Lmax, dtype, code, block, apart, order):
+    """Columns that only the blocks of small scale have values in are as exact as the others.
+
+    A weight p that meets the codes is fp16 (two terms in the fp32 path) under the largest p s of
+    the row so far, 2^13, and off by up to 2^-25 below 2^-14.  Scales less than 2^10 below the
+    largest of the tiles so far are summed with them: an error of 2^-38 2^10 max p in p; scales
+    further below are summed under their own largest p.  Hence, next to the relative terms,
+    2^-28 max p sum_j |v_j| in each column, without any other block's scale."""
+    g = rng(1200 + apart)
+    c = finite(strange(g, 1, 1, Lmax, block, code), code)
+    nb = c["v_scale"].shape[2]
+    small = {"large first": np.arange(nb) >= (nb + 1) // 2, "small first": np.arange(nb) < nb // 2,
+             "mixed": g.random(nb) < 0.5}[order]
+    small[0], small[1] = order == "small first", order != "small first"   # some of either
+    c["v_scale"][0, 0] = np.where(small, 2.0 ** -(apart - apart // 2), 2.0 ** (apart // 2))
+    large = ~small[np.arange(Lmax) // block]
+    c["v"][0, 0, large, :32] = 0
+    c["k_scale"][...] = 2.0 ** -9
+    Q = np.zeros((1, 3, 1, 64))                  # row 0 attends evenly
+    Q[0, 1, 0] = g.standard_normal(64)
+    Q[0, 2, 0] = g.standard_normal(64) * 4
+    Q = fin(Q, dtype)
+    L = Lmax - 3
+    # (equal heads, for runs of several tiles to a warp that begin anywhere in a head)
+    cache = to_gpu({n: np.repeat(a, copies, 0) for n, a in c.items()}, block, code)
+    before = c["weights"].copy()
+    O = mha.sdpa_decode_q8(dev(np.repeat(Q, copies, 0), DT[dtype]), cache, i32([L] * copies),
+                           add_weights=True)
+    got = O.double().cpu().numpy()
+    ref, W, pv, _, qk = oq.decode_ref(Q, c, [L], block, code, True)
+    close_weights(cache.weights.double().cpu().numpy(), before, W, qk, L, "weights")
+    v = np.abs(oq.dequantised_ref(c, "v", 0, 0, L, block, code)).sum(0)
+    for row in range(3):
+        p = weights_of(Q, c, 0, 0, row, L, block, code)
+        close_decode(got[:, row], ref[:, row], pv[:, row], 2.0 ** 10 * p.max() * v, qk, L, dtype,
+                     f"row {row}")

@@ -25,8 +25,9 @@
 //     at a time (movmatrix);
 //   - the scales stay out of the operands: a key's multiplies its score, a value's enters the
 //     exponent (p_j = 2^(x_j + log2 s_j - m)) and the softmax sum takes p_j / s_j.  With m the
-//     maximum of x_j + log2 s_j the weights p_j that meet the value codes lie in [0, 2^13],
-//     within fp16 whatever the scales are.
+//     maximum of x_j + log2 s_j the weights p_j that meet the value codes lie in [0, 2^13].
+//     Blocks whose scales are more than 2^10 apart are summed under references of their own
+//     (careful_tile), since fp16 holds nothing below 2^-25.
 // Precision: scores, statistics and sums are fp32.  Queries are scaled by a power of two (their
 // row's largest value to [2^13, 2^14)) and rounded to fp16, which holds every bf16 significand;
 // fp32 queries and weights are split into two fp16 terms (22 bits) and their products done
@@ -65,6 +66,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr float kOffset = 13.f;            // weights that meet the codes: 2^13 at most
 constexpr float kLift = 8192.f;            // 2^kOffset
 constexpr float kHuge = 4096.f;            // references beyond it: careful_tile()
+constexpr float kApart = 10.f;             // log2 of value scales' ratio: careful_tile()
 constexpr float kNone = -3.402823466e38f;  // maximum of no position (finite: -inf - it is -inf)
 
 // How the rows of a cache head are cut: groups of 8 * NR rows, NR column tiles of the products
@@ -499,6 +501,11 @@ __global__ void __launch_bounds__(register_threads(sizeof(T) / 2, NR), 1)
     // Beyond kHuge a reference is too coarse for exponents in which the offset and the value's
     // scale are rounded together with it (from 2^24 on they would be lost)
     bool huge = false;
+    // A tile whose value scales are 2^kApart below the largest so far, or apart by that, has weights
+    // that fp16 would round away under the row's reference (2^-38 of its largest at the least),
+    // whatever its share of a column: it is taken with a reference of its own as well
+    float most_log = -INFINITY, value_log[2] = {0.f, 0.f};
+    bool apart = false;
     float sc_next = load_scale(c.kt), sc = 1.f, sc_log = 0.f, sc_inv = 1.f;
     const int last = min(c.nt, c.kt + count - done);
     done += last - c.kt;
@@ -510,6 +517,10 @@ __global__ void __launch_bounds__(register_threads(sizeof(T) / 2, NR), 1)
       if (c.kt + 1 < last) sc_next = load_scale(c.kt + 1);  // a tile ahead of its use
       sc_log = log2_approx(sc);
       sc_inv = rcp_approx(sc);
+      value_log[0] = __shfl_sync(0xffffffffu, sc_log, 2);
+      value_log[1] = __shfl_sync(0xffffffffu, sc_log, 3);
+      most_log = fmaxf(most_log, fmaxf(value_log[0], value_log[1]));
+      apart = fminf(value_log[0], value_log[1]) < most_log - kApart;
       copy_async_wait<kStages - 1>();  // this lane's copies of the tile have landed
       __syncwarp();                    // and every lane's
       sK = ring + slot * kSlotBytes;
@@ -612,11 +623,11 @@ __global__ void __launch_bounds__(register_threads(sizeof(T) / 2, NR), 1)
       for (int q = 0; q < 2; ++q) scores(q, x[q]);
       // ---- the scales: a score is x * f, its exponent x * f + log2 of the value's scale
       float2 f[2][NR];
-      float ev[2], inv[2];
+      float inv[2];
+      const float (&ev)[2] = value_log;
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         const float ks = __shfl_sync(0xffffffffu, sc, q);
-        ev[q] = __shfl_sync(0xffffffffu, sc_log, 2 + q);
         inv[q] = __shfl_sync(0xffffffffu, sc_inv, 2 + q);
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr)
@@ -815,12 +826,13 @@ __global__ void __launch_bounds__(register_threads(sizeof(T) / 2, NR), 1)
         }
       }
     };
-    // tiles that every row sees, then the others; a tile that `tile` could not finish is begun
+    // tiles that every row sees, then, from the first one that is not for `tile` on, the others; a
+    // tile that `tile` did not finish is begun already
     const int seen = min(last, max((c.L - (a.causal ? a.Nq : 1) + 1) / kTile, 0));
     bool begun = false;
     for (; c.kt < seen; ++c.kt) {
       begin_tile();
-      if (!tile()) {
+      if (apart || !tile()) {
         begun = true;
         break;
       }
