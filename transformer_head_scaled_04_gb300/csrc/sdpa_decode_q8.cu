@@ -93,8 +93,8 @@ constexpr int main_warps(int terms, int nr) { return terms * nr <= 2 ? 12 : 8; }
 // Threads that the registers are shared out for.  bf16 queries of one column tile take 128 each at
 // most, as for 16 warps, which leaves room for a block of the join to wait on the SM (one sequence
 // of 131072, 8 heads: 27.1 us; with the 137 they would take 28.6)
-constexpr int register_threads(int terms, int nr) {
-  return terms * nr == 1 ? 512 : main_warps(terms, nr) * 32;
+constexpr int register_threads(int terms, int nr, bool alone) {
+  return terms * nr == 1 && !alone ? 512 : main_warps(terms, nr) * 32;
 }
 // workers at most, as far as the workspace goes (a GB300 has 152 SMs)
 constexpr int max_workers(int terms, int nr) { return 160 * main_warps(terms, nr); }
@@ -301,7 +301,7 @@ __device__ __forceinline__ float join_lanes(float& m, float& l, float2 st, float
 // kAlone: a block per cache head (of one row group), whose tiles its warps share; pieces and scores
 // meet in shared memory, and no second launch is needed.
 template <typename T, int QT, int NR, bool kAlone>
-__global__ void __launch_bounds__(register_threads(sizeof(T) / 2, NR), 1)
+__global__ void __launch_bounds__(register_threads(sizeof(T) / 2, NR, kAlone), 1)
     decode_q8_kernel(const Params p) {
   constexpr int kTerms = sizeof(T) == 4 ? 2 : 1;
   const DecodeQ8Args& a = p.a;
@@ -501,9 +501,9 @@ __global__ void __launch_bounds__(register_threads(sizeof(T) / 2, NR), 1)
     // Beyond kHuge a reference is too coarse for exponents in which the offset and the value's
     // scale are rounded together with it (from 2^24 on they would be lost)
     bool huge = false;
-    // A tile whose value scales are 2^kApart below the largest so far, or apart by that, has weights
-    // that fp16 would round away under the row's reference (2^-38 of its largest at the least),
-    // whatever its share of a column: it is taken with a reference of its own as well
+    // A tile with a value scale 2^kApart or more below the largest so far has weights that fp16
+    // would round away under the row's reference (what is below 2^-38 of its largest), and they may
+    // be all that a column has: it is taken under references of its own as well
     float most_log = -INFINITY, value_log[2] = {0.f, 0.f};
     bool apart = false;
     float sc_next = load_scale(c.kt), sc = 1.f, sc_log = 0.f, sc_inv = 1.f;
@@ -723,91 +723,100 @@ __global__ void __launch_bounds__(register_threads(sizeof(T) / 2, NR), 1)
       }
       return true;
     };
-    // Any tile, its two groups in turn, which takes half the code (in one body with the above, masks
-    // cost the other tiles 78 of 562 instructions and 14% of the time: 16 rows, 8 x 8 x 16384
-    // positions; both groups at once as above 153 us instead of 141 at 128 rows, for its
-    // registers).  Weights are 2^(x - ref) under the largest score of the row's 16 positions: the
-    // difference of two scores is exact where it counts, whatever their size.  2^(ref - m) brings
-    // their sum under the row's reference and, with the values' scale, their product.
+    // Any tile.  (In one body with the above, masks cost the other tiles 78 of 562 instructions and
+    // 14% of the time: 16 rows, 8 x 8 x 16384 positions.)  Weights are 2^(x - ref) under the
+    // largest score of the row's 16 positions: the difference of two scores is exact where it
+    // counts, whatever their size.  2^(ref - m) brings their sum under the row's reference and, with the
+    // values' scale, their product.  The two groups follow one another, which takes half the code
+    // and registers (128 rows to a head 145 us; both at once 153), but where one launch does it all
+    // and this tile is the last thing that is waited for (8 heads x 37 4.2 and 4.5 us).
     auto careful_tile = [&]() {
+      constexpr int kAtOnce = kAlone ? 2 : 1;
 #pragma unroll 1
-      for (int q = 0; q < 2; ++q) {
-        float x[NR][4], ref[NR][2], top[NR][2];
-        scores(q, x);
-        const float ks = __shfl_sync(0xffffffffu, sc, q);
-        const float vs = __shfl_sync(0xffffffffu, sc, 2 + q);
-        const float ev = __shfl_sync(0xffffffffu, sc_log, 2 + q);
+      for (int q0 = 0; q0 < 2; q0 += kAtOnce) {
+        float x[kAtOnce][NR][4], ref[kAtOnce][NR][2], top[NR][2];
         bool grew = false;
 #pragma unroll
-        for (int nr = 0; nr < NR; ++nr)
+        for (int i = 0; i < kAtOnce; ++i) scores(q0 + i, x[i]);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float f = ks * (e ? qs[nr].y : qs[nr].x);
-            const int at = pos + q * 16 + g;
-            x[nr][e] = at > lim[nr][e] ? -INFINITY : __fmul_rn(x[nr][e], f);
-            x[nr][2 + e] = at + 8 > lim[nr][e] ? -INFINITY : __fmul_rn(x[nr][2 + e], f);
-            if (score_row != nullptr && nr * 8 + e < rows_here) {
-              float* dst = score_row + (nr * 8 + e) * p.Lpad + pos + q * 16;
-              dst[0] = x[nr][e];
-              dst[8] = x[nr][2 + e];
+        for (int i = 0; i < kAtOnce; ++i) {
+          const float ks = __shfl_sync(0xffffffffu, sc, q0 + i);
+          const float ev = __shfl_sync(0xffffffffu, sc_log, 2 + q0 + i);
+          const int at = pos + (q0 + i) * 16 + g;
+#pragma unroll
+          for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float f = ks * (e ? qs[nr].y : qs[nr].x);
+              float &x0 = x[i][nr][e], &x1 = x[i][nr][2 + e];
+              x0 = at > lim[nr][e] ? -INFINITY : __fmul_rn(x0, f);
+              x1 = at + 8 > lim[nr][e] ? -INFINITY : __fmul_rn(x1, f);
+              if (score_row != nullptr && nr * 8 + e < rows_here) {
+                float* dst = score_row + (nr * 8 + e) * p.Lpad + at - g;
+                dst[0] = x0;
+                dst[8] = x1;
+              }
+              const float v = row_max(fmaxf(x0, x1));
+              ref[i][nr][e] = v;
+              top[nr][e] = i == 0 ? v + ev : fmaxf(top[nr][e], v + ev);
+              grew |= top[nr][e] > m[nr][e];
             }
-            float v = fmaxf(x[nr][e], x[nr][2 + e]);
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-            ref[nr][e] = v;
-            top[nr][e] = v + ev;
-            grew |= top[nr][e] > m[nr][e];
-          }
-        if (__any_sync(0xffffffffu, grew)) rise(top);
-        uint2 v[4];
-        uint32_t b0[8], b1[8];
-        value_codes(q, v);
-#pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          // rows behind the last position hold anything: 0.  A NaN among the rows that some query
-          // may not see must reach only those that do: taken out of the product here, put into O
-          // below
-          if (pos + q * 16 + 2 * t + (z >> 1) * 8 + (z & 1) >= c.L) v[z] = make_uint2(0u, 0u);
-          if constexpr (QT == kE4m3) {
-            v[z].x &= ~__vcmpeq4(v[z].x & 0x7f7f7f7fu, 0x7f7f7f7fu);
-            v[z].y &= ~__vcmpeq4(v[z].y & 0x7f7f7f7fu, 0x7f7f7f7fu);
-          }
         }
-        value_halves(v, b0, b1);
+        if (__any_sync(0xffffffffu, grew)) rise(top);
 #pragma unroll
-        for (int nr = 0; nr < NR; ++nr) {
-          uint32_t pf[kTerms][2];
-          float into_l[2], into_o[2];
+        for (int i = 0; i < kAtOnce; ++i) {
+          const float vs = __shfl_sync(0xffffffffu, sc, 2 + q0 + i);
+          uint2 v[4];
+          uint32_t b0[8], b1[8];
+          value_codes(q0 + i, v);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            into_l[e] = ex2_approx(ref[nr][e] - m[nr][e]);
-            into_o[e] = into_l[e] * vs;
-            if (ref[nr][e] == -INFINITY) ref[nr][e] = 0.f;  // none allowed: weights of 0
+          for (int z = 0; z < 4; ++z) {
+            // rows behind the last position hold anything: 0.  A NaN among the rows that some query
+            // may not see must reach only those that do: taken out of the product here, put into O
+            // below
+            if (pos + (q0 + i) * 16 + 2 * t + (z >> 1) * 8 + (z & 1) >= c.L)
+              v[z] = make_uint2(0u, 0u);
+            if constexpr (QT == kE4m3) {
+              v[z].x &= ~__vcmpeq4(v[z].x & 0x7f7f7f7fu, 0x7f7f7f7fu);
+              v[z].y &= ~__vcmpeq4(v[z].y & 0x7f7f7f7fu, 0x7f7f7f7fu);
+            }
           }
+          value_halves(v, b0, b1);
 #pragma unroll
-          for (int z = 0; z < 2; ++z) {
-            const float w0 = ex2_approx(x[nr][2 * z] - ref[nr][0]) * kLift;
-            const float w1 = ex2_approx(x[nr][2 * z + 1] - ref[nr][1]) * kLift;
-            l[nr].x = fmaf(w0, into_l[0], l[nr].x);
-            l[nr].y = fmaf(w1, into_l[1], l[nr].y);
-            const uint32_t hi = pack_half(w0, w1);
-            pf[0][z] = transpose8x8(hi);
-            if constexpr (kTerms == 2) pf[kTerms - 1][z] = transpose8x8(pack_rest(w0, w1, hi));
-          }
+          for (int nr = 0; nr < NR; ++nr) {
+            uint32_t pf[kTerms][2];
+            float into_l[2], into_o[2];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t fa[4] = {b0[2 * j], b0[2 * j + 1], b1[2 * j], b1[2 * j + 1]};
-            float d[4];
-            mma16816_zero(d, fa, pf[kTerms - 1][0], pf[kTerms - 1][1]);
-            if constexpr (kTerms == 2) mma16816(d, fa, pf[0][0], pf[0][1]);
+            for (int e = 0; e < 2; ++e) {
+              into_l[e] = ex2_approx(ref[i][nr][e] - m[nr][e]);
+              into_o[e] = into_l[e] * vs;
+              if (ref[i][nr][e] == -INFINITY) ref[i][nr][e] = 0.f;  // none allowed: weights of 0
+            }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[nr][j][i] = fmaf(d[i], into_o[i & 1], o[nr][j][i]);
+            for (int z = 0; z < 2; ++z) {
+              const float w0 = ex2_approx(x[i][nr][2 * z] - ref[i][nr][0]) * kLift;
+              const float w1 = ex2_approx(x[i][nr][2 * z + 1] - ref[i][nr][1]) * kLift;
+              l[nr].x = fmaf(w0, into_l[0], l[nr].x);
+              l[nr].y = fmaf(w1, into_l[1], l[nr].y);
+              const uint32_t hi = pack_half(w0, w1);
+              pf[0][z] = transpose8x8(hi);
+              if constexpr (kTerms == 2) pf[kTerms - 1][z] = transpose8x8(pack_rest(w0, w1, hi));
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t fa[4] = {b0[2 * j], b0[2 * j + 1], b1[2 * j], b1[2 * j + 1]};
+              float d[4];
+              mma16816_zero(d, fa, pf[kTerms - 1][0], pf[kTerms - 1][1]);
+              if constexpr (kTerms == 2) mma16816(d, fa, pf[0][0], pf[0][1]);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) o[nr][j][k] = fmaf(d[k], into_o[k & 1], o[nr][j][k]);
+            }
           }
         }
         if constexpr (QT == kE4m3) {
           // columns 8g .. 8g+7 of each position: NaN into the rows that see it
-          for (int row = q * 16; row < q * 16 + 16 && pos + row < c.L; ++row) {
+          const int end = min((q0 + kAtOnce) * 16, c.L - pos);
+          for (int row = q0 * 16; row < end; ++row) {
             const uint2 u = *reinterpret_cast<const uint2*>(
                 sV + row * kD + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + (g & 1) * 8);
             if ((__vcmpeq4(u.x & 0x7f7f7f7fu, 0x7f7f7f7fu) |
