@@ -167,3 +167,24 @@ def test_decode_values_of_small_scale_beside_large(copies, Lmax, dtype, code, bl
         p = weights_of(Q, c, 0, 0, row, L, block, code)
         close_decode(got[:, row], ref[:, row], pv[:, row], 2.0 ** 10 * p.max() * v, qk, L, dtype,
                      f"row {row}")
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("size,scale", [(1e-30, 1e30), (1e-38, 3e37), (1e30, 1e-31)])
+def test_decode_small_and_large_rows_under_a_scale_that_evens_them(path, dtype, size, scale):
+    B, H, Lmax = PATHS[path]
+    B = min(B, 2) if path != "warp join" else B
+    g = rng(1250)
+    c = finite(strange(g, B, H, Lmax, 64, "int8"), "int8")
+    for n in "kv":
+        c[n + "_scale"] *= 2.0 ** -6
+    c["weights"][...] = 0
+    Q = fin(g.standard_normal((B, H, 1, 64)) * size, dtype)
+    scale = float(np.float32(scale))
+    lens = [Lmax - 5 * (b % 7) for b in range(B)]
+    cache = to_gpu(c, 64, "int8")
+    O = mha.sdpa_decode_q8(dev(Q, DT[dtype]), cache, i32(lens), scale=scale, add_weights=True)
+    ref, W, pv, low, qk = oq.decode_ref(Q, c, lens, 64, "int8", True, scale=scale)
+    close_decode(O.double().cpu().numpy(), ref, pv, low, qk, Lmax, dtype, "rows")
+    close_weights(cache.weights.double().cpu().numpy(), 0 * W, W, qk, Lmax, "weights")

@@ -425,10 +425,10 @@ __global__ void __launch_bounds__(register_threads(sizeof(T) / 2, NR, kAlone), 1
       for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(f[i]));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      // (2^-60 and 2^-80 keep the factors normal numbers, so that an excluded score's -inf stays
-      // -inf; scores that small are 0 to the softmax)
-      const int ex = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -60);
-      const float up = pow2i(13 - ex), down = fmaxf(pow2i(ex - 13) * c2, pow2i(-80));
+      // (2^-113 keeps both powers normal numbers.  Rows below that are multiples of 2^-149, which
+      // 2^126 makes exact in fp16's two terms)
+      const int ex = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -113);
+      const float up = pow2i(13 - ex), down = pow2i(ex - 13) * c2;
       // inner step k: lane t supplies dims 16t + 4k + {0, 1} and {2, 3}
 #pragma unroll
       for (int k = 0; k < 4; ++k)
