@@ -188,3 +188,20 @@ def test_decode_small_and_large_rows_under_a_scale_that_evens_them(path, dtype, 
     ref, W, pv, low, qk = oq.decode_ref(Q, c, lens, 64, "int8", True, scale=scale)
     close_decode(O.double().cpu().numpy(), ref, pv, low, qk, Lmax, dtype, "rows")
     close_weights(cache.weights.double().cpu().numpy(), 0 * W, W, qk, Lmax, "weights")
+
+
+@pytest.mark.parametrize("dtype,q_size,k_size", [
+    ("bf16", 1e30, 1e-30), ("bf16", 1e-30, 1e30), ("f32", 1e30, 1e-30), ("f32", 1e-30, 1e30),
+    ("f32", 3e37, 1e-37), ("f32", 1e-37, 1e37), ("f32", 5e37, 1e-42), ("f32", 1.0, 1e-44)])
+def test_key_weights_of_rows_far_below_and_above_one(dtype, q_size, k_size):
+    """Scores of ordinary size from rows whose values are anything but.  The bound is that of
+    test_key_weights."""
+    g = rng(1300)
+    Q = fin(g.standard_normal((1, 2, 70, 64)) * q_size, dtype)
+    K = fin(g.standard_normal((1, 1, 90, 64)) * k_size, dtype)
+    lse = oracle.sdpa_lse_ref(Q, np.repeat(K, 2, 1), "none").astype(np.float32)
+    w = mha.sdpa_key_weights(dev(Q, DT[dtype]), dev(K, DT[dtype]), dev(lse))
+    ref = oq.key_weights_ref(Q, K, lse, "none")
+    S = np.abs(Q[0]).astype(np.float64) @ np.abs(K[0, 0]).astype(np.float64).T / 8
+    r = 2.0 ** -18 * S.max() + 2.0 ** -23 * np.abs(lse).max() + 2.0 ** -20 + 140 * 2.0 ** -24
+    assert np.all(np.abs(w.double().cpu().numpy() - ref) <= r * ref)

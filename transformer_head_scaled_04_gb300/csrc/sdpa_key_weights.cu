@@ -53,10 +53,11 @@ constexpr int kWarps = 8;
 static_assert(kKeys == 16 * kWarps && kWarps * 32 == 8 * kQueries,
               "a key tile per warp, eight threads to a query");
 
-// the power of two that brings a row's largest magnitude to [2^13, 2^14) (below 2^-60: less), and
-// its inverse
+// the power of two that brings a row's largest magnitude to [2^13, 2^14), and its inverse.  2^-113
+// keeps both normal numbers; rows below that are multiples of 2^-149, which 2^126 makes exact in
+// fp16's two terms
 __device__ __forceinline__ float2 row_scale(float amax) {
-  const int ex = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -60);
+  const int ex = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -113);
   return make_float2(__uint_as_float((140 - ex) << 23), __uint_as_float((114 + ex) << 23));
 }
 
