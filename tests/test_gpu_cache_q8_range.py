@@ -205,3 +205,17 @@ def test_key_weights_of_rows_far_below_and_above_one(dtype, q_size, k_size):
     S = np.abs(Q[0]).astype(np.float64) @ np.abs(K[0, 0]).astype(np.float64).T / 8
     r = 2.0 ** -18 * S.max() + 2.0 ** -23 * np.abs(lse).max() + 2.0 ** -20 + 140 * 2.0 ** -24
     assert np.all(np.abs(w.double().cpu().numpy() - ref) <= r * ref)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_key_weights_of_more_than_65535_heads(dtype):
+    B, H, N = 67, 1000, 3
+    g = rng(1350)
+    q, k = (dev(fin(g.standard_normal((B, H, N, 64)), dtype), DT[dtype]) for _ in range(2))
+    _, lse = mha.sdpa_with_lse(q, k, k, "causal")
+    w = mha.sdpa_key_weights(q, k, lse, "causal")
+    s = (q.double() @ k.double().transpose(2, 3) / 8).tril()
+    p = torch.exp(s - lse.double()[..., None]).tril()
+    # sum |q||k| / 8 is below 16: 64 roundings to fp32 are 2^-14 in all; lse is below 16: 2^-20
+    assert torch.all((w - p.sum(2)).abs() <= 2.0 ** -11 * p.sum(2))
+    assert torch.allclose(w.sum(-1), torch.full((B, H), 3.0, device="cuda"), rtol=2.0 ** -11)

@@ -144,9 +144,10 @@ int mha_key_weights_workspace_size(int B, int H, int Hkv, int Nq, int Nk, int dt
   if (bytes == nullptr || B < 1 || H < 1 || Hkv < 1 || Nq < 1 || Nk < 1 || H % Hkv != 0 ||
       !valid_dtype(dtype))
     return MHA_ERR_INVALID;
-  // blocks of the launch's grids
+  // blocks of the launch's grids (queries are split, and heads a grid's y, only where key tiles
+  // are few)
   const int64_t heads = static_cast<int64_t>(B) * Hkv;
-  if (heads > 65535 || heads * ((Nk + 127) / 128) > (1 << 30) || Nq > (1 << 30) ||
+  if (B > 65535 || H > 65535 || heads * ((Nk + 127) / 128) > (1 << 30) || Nq > (1 << 30) ||
       static_cast<int64_t>(H / Hkv) * ((Nq + 31) / 32) > (1 << 30))
     return MHA_ERR_UNSUPPORTED;
   *bytes = round_up(mha::key_weights_workspace(B, H, Hkv, Nq, Nk, dtype), 256);
