@@ -6,6 +6,10 @@ A generation step has three paths: one launch (up to 768 positions, 152 cache he
 head), and two whose second joins a row's pieces, with a block to a row where rows are few and
 pieces many, else with a warp to a row.  ``PATHS`` has sizes for each.
 """
+import ctypes
+import os
+import subprocess
+
 import numpy as np
 import pytest
 import torch
@@ -219,3 +223,45 @@ def test_key_weights_of_more_than_65535_heads(dtype):
     # sum |q||k| / 8 is below 16: 64 roundings to fp32 are 2^-14 in all; lse is below 16: 2^-20
     assert torch.all((w - p.sum(2)).abs() <= 2.0 ** -11 * p.sum(2))
     assert torch.allclose(w.sum(-1), torch.full((B, H), 3.0, device="cuda"), rtol=2.0 ** -11)
+
+
+SHARES = r"""
+#include "sdpa_key_weights.cu"
+// the second launch on its own: shares [split][heads][keys] onto weights [heads][keys]
+extern "C" int add_shares(int heads, int keys, int split, float* shares, float* weights) {
+  mha::KwParams p = {};
+  p.a.Hkv = heads;
+  p.a.Nk = keys;
+  p.a.ld = keys;
+  p.a.weights = weights;
+  p.split = split;
+  p.part = shares;
+  mha::key_weights_add_kernel<<<dim3((keys + 255) / 256, heads), dim3(256)>>>(p);
+  return cudaDeviceSynchronize();
+}
+"""
+
+
+def test_key_weights_stay_where_a_share_is_missing(tmp_path):
+    """A share that a time-out left out is marked, and the keys' running totals stay as they were.
+    (The mark is made here: a wait is not made to run out with copies in flight.)"""
+    from transformer_head_scaled_04_gb300 import build
+
+    src, lib = tmp_path / "shares.cu", tmp_path / "shares.so"
+    src.write_text(SHARES)
+    subprocess.run([build._nvcc(), *build.ARCH, *build.NVCC_FLAGS, "-shared", str(src), "-o",
+                    str(lib)], check=True)
+    # (lazily: what the file needs of others for the first launch stays unresolved, and uncalled)
+    add = ctypes.CDLL(str(lib), mode=os.RTLD_LAZY).add_shares
+    g = rng(1380)
+    shares = g.random((5, 3, 300)).astype(np.float32)
+    shares[2, 1, 250:] = -1
+    shares[4, 0, 7] = -1
+    before = g.random((3, 300)).astype(np.float32)
+    w, s = dev(before), dev(shares)
+    assert add(3, 300, 5, ctypes.c_void_p(s.data_ptr()), ctypes.c_void_p(w.data_ptr())) == 0
+    missing = (shares < 0).any(0)
+    got = w.cpu().numpy()
+    assert np.array_equal(got[missing], before[missing])
+    want = before + shares.astype(np.float64).sum(0)
+    assert np.all(np.abs(got - want)[~missing] <= 5 * 2.0 ** -24 * 6)

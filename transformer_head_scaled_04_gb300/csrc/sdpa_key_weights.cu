@@ -38,6 +38,7 @@ namespace {
 
 constexpr int kD = 64;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kMissing = -1.f;  // for a sum that a time-out left out (sums are not negative)
 struct KwParams {
   KeyWeightsArgs a;
   int split;      // CTAs that share a key tile's queries
@@ -480,14 +481,18 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     }
     tmem_wait_ld();
     // the two column halves of a key through the (now unused) key tile's memory.  After a time-out
-    // nothing is written
+    // the key's weight stays as it was: nothing is added here, nor where the shares are added up
     float* half = reinterpret_cast<float*>(smem);
     const float2 t = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
-    if (col0 > 0) half[quarter * 32 + lane] = ok ? t.x + t.y : NAN;
+    if (col0 > 0) half[quarter * 32 + lane] = ok ? t.x + t.y : kMissing;
     named_bar_sync(1, kSumWarps * 32);
-    if (col0 == 0 && key < nk && ok) {
-      const float sum = t.x + t.y + half[quarter * 32 + lane];
-      out[key] = p.split == 1 ? out[key] + sum : sum;
+    if (col0 == 0 && key < nk) {
+      const float other = half[quarter * 32 + lane], sum = t.x + t.y + other;
+      const bool whole = ok && other != kMissing;
+      if (p.split > 1)
+        out[key] = whole ? sum : kMissing;
+      else if (whole)
+        out[key] += sum;
     }
   }
   tc_fence_before();
@@ -498,7 +503,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
   }
 }
 
-// weights += the shares' sums, in order
+// weights += the shares' sums, in order; keys with a share missing keep what they have
 __global__ void __launch_bounds__(256) key_weights_add_kernel(const KwParams p) {
   const KeyWeightsArgs& a = p.a;
   pdl_launch_dependents();
@@ -507,8 +512,11 @@ __global__ void __launch_bounds__(256) key_weights_add_kernel(const KwParams p) 
   const int nk = a.mask == 2 ? min(max(__ldg(a.key_len + bg / a.Hkv), 0), a.Nk) : a.Nk;
   if (j >= nk) return;
   float s = 0.f;
-  for (int z = 0; z < p.split; ++z)
-    s += p.part[(static_cast<int64_t>(z) * gridDim.y + bg) * a.Nk + j];
+  for (int z = 0; z < p.split; ++z) {
+    const float share = p.part[(static_cast<int64_t>(z) * gridDim.y + bg) * a.Nk + j];
+    if (share == kMissing) return;
+    s += share;
+  }
   a.weights[static_cast<int64_t>(bg) * a.ld + j] += s;
 }
 
