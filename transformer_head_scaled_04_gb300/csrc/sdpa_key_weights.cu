@@ -512,12 +512,13 @@ __global__ void __launch_bounds__(256) key_weights_add_kernel(const KwParams p) 
   const int nk = a.mask == 2 ? min(max(__ldg(a.key_len + bg / a.Hkv), 0), a.Nk) : a.Nk;
   if (j >= nk) return;
   float s = 0.f;
+  bool missing = false;
   for (int z = 0; z < p.split; ++z) {
     const float share = p.part[(static_cast<int64_t>(z) * gridDim.y + bg) * a.Nk + j];
-    if (share == kMissing) return;
+    missing |= share == kMissing;  // (no branch: the loads of all shares go out together)
     s += share;
   }
-  a.weights[static_cast<int64_t>(bg) * a.ld + j] += s;
+  if (!missing) a.weights[static_cast<int64_t>(bg) * a.ld + j] += s;
 }
 
 // CTAs per key tile: enough for two on each of 152 SMs (fp32: twice that, for shorter CTAs), no
