@@ -290,7 +290,6 @@ __global__ void __launch_bounds__(kTcThreads, 2)
   const int k0 = kt * kT;
 
   pdl_wait();  // the previous kernel's output is complete from here on
-  pdl_launch_dependents();
   const int nk = a.mask == 2 ? min(max(__ldg(a.key_len + b), 0), a.Nk) : a.Nk;
   const int nq = a.query_len != nullptr ? min(max(__ldg(a.query_len + b), 0), a.Nq) : a.Nq;
   if (k0 >= nk) return;
@@ -331,6 +330,9 @@ __global__ void __launch_bounds__(kTcThreads, 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // (not before: a following kernel that takes its TMEM ahead of its own wait must not get there
+  // first, since it gives it back only after this one has ended)
+  pdl_launch_dependents();
 
   float* lse_s = reinterpret_cast<float*>(smem + kOffLse);
   if (warp == kWarpTma) {
