@@ -56,6 +56,13 @@ def scale_ref(x, code: str) -> float:
     return 2.0 ** e
 
 
+def times_ref(x, factor) -> np.ndarray:
+    """x * factor, exact for powers of two, else as the header says: factor and product in fp32."""
+    x, factor = np.broadcast_arrays(np.asarray(x, np.float64), np.asarray(factor, np.float64))
+    rounded = x.astype(np.float32) * factor.astype(np.float32)
+    return np.where(np.frexp(factor)[0] == 0.5, x * factor, rounded)
+
+
 def append_ref(cache: dict, k, v, cache_len, new_len, block: int, code: str) -> dict:
     """The cache after token i < new_len[b] of k, v went to position cache_len[b] + i."""
     out = {n: np.array(a) for n, a in cache.items()}
@@ -77,10 +84,10 @@ def append_ref(cache: dict, k, v, cache_len, new_len, block: int, code: str) -> 
                         s = max(s, was)
                         if s > was:
                             rows = slice(blk * block, lo)
-                            old = values_ref(out[name][b, h, rows], code) * (was / s)
+                            old = times_ref(values_ref(out[name][b, h, rows], code), was / s)
                             out[name][b, h, rows] = encode_ref(old, code)
                     out[name + "_scale"][b, h, blk] = s
-                    out[name][b, h, lo:hi] = encode_ref(new / s, code)
+                    out[name][b, h, lo:hi] = encode_ref(times_ref(new, 1 / s), code)
                 out["weights"][b, h, lo:hi] = 0.0
     return out
 
@@ -170,7 +177,7 @@ def evict_ref(cache: dict, out: dict, cache_len, keep: int, recent: int, block: 
                 for name in ("k", "v"):
                     was = cache[name + "_scale"][b, h, src // block]
                     s = was.max()
-                    vals = values_ref(cache[name][b, h, src], code) * (was / s)[:, None]
+                    vals = times_ref(values_ref(cache[name][b, h, src], code), (was / s)[:, None])
                     out[name][b, h, lo:lo + len(src)] = np.where(
                         (was == s)[:, None], cache[name][b, h, src], encode_ref(vals, code))
                     out[name + "_scale"][b, h, lo // block] = s

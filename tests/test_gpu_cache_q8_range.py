@@ -271,3 +271,38 @@ def test_key_weights_stay_where_a_share_is_missing(tmp_path):
     assert np.array_equal(got[missing], before[missing])
     want = before + shares.astype(np.float64).sum(0)
     assert np.all(np.abs(got - want)[~missing] <= 5 * 2.0 ** -24 * 6)
+
+
+APPEND = [  # N, cache_len, scales of the begun blocks
+    (3, [20, 33], 0.011), (40, [5, 63], 0.3), (1, [47, 1], 3e-10), (70, [16, 9], 1e4)]
+
+
+@pytest.mark.parametrize("N,cl,scale", APPEND)
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("size", [1e-3, 30.0])      # the begun block keeps its scale, or not
+def test_append_under_scales_that_are_no_powers_of_two(N, cl, scale, code, dtype, size):
+    g = rng(1400 + N)
+    c = strange(g, 2, 3, 200, 32, code)
+    c["k_scale"][...] = np.float32(scale)
+    c["v_scale"][...] = np.float32(scale) * g.uniform(0.5, 2, c["v_scale"].shape)
+    for n in "kv":
+        c[n + "_scale"] = c[n + "_scale"].astype(np.float32).astype(np.float64)
+    k, v = (fin(g.standard_normal((2, 3, N, 64)) * size, dtype) for _ in range(2))
+    cache = to_gpu(c, 32, code)
+    mha.kv_append_q8(cache, dev(k, DT[dtype]), dev(v, DT[dtype]), i32(cl))
+    assert_same(from_gpu(cache), oq.append_ref(c, k, v, cl, None, 32, code), code, "append")
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("block", [16, 128])
+def test_evict_under_scales_that_are_no_powers_of_two(code, block):
+    g = rng(1450)
+    c, d = strange(g, 2, 2, 900, block, code), strange(g, 2, 2, 400, block, code)
+    for n in "kv":
+        s = np.exp(g.uniform(-5, 5, c[n + "_scale"].shape))
+        c[n + "_scale"] = s.astype(np.float32).astype(np.float64)
+    src, out = to_gpu(c, block, code), to_gpu(d, block, code)
+    mha.kv_evict_q8(src, out, i32([900, 431]), 333, 20)
+    want, _, _ = oq.evict_ref(c, d, [900, 431], 333, 20, block, code)
+    assert_same(from_gpu(out), want, code, "evict")
