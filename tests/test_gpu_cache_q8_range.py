@@ -306,3 +306,172 @@ def test_evict_under_scales_that_are_no_powers_of_two(code, block):
     mha.kv_evict_q8(src, out, i32([900, 431]), 333, 20)
     want, _, _ = oq.evict_ref(c, d, [900, 431], 333, 20, block, code)
     assert_same(from_gpu(out), want, code, "evict")
+
+
+# ---- special rows on every path of the generation step
+def plain_cache(g, B, H, Lmax, block, code):
+    c = finite(strange(g, B, H, Lmax, block, code), code)
+    for n in "kv":
+        c[n + "_scale"] *= 2.0 ** -6
+    return c
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_decode_token_major_with_a_workspace_on_every_path(path, dtype):
+    B, H, Lmax = PATHS[path]
+    g = rng(1500)
+    c = plain_cache(g, B, H, Lmax, 64, "int8")
+    c["weights"][...] = 0
+    lens = [Lmax - 7 * (b % 5) for b in range(B)]
+    cache = to_gpu(c, 64, "int8", token_major=True)
+    Q = fin(g.standard_normal((B, 2 * H, 2, 64)), dtype)
+    tq = dev(Q, DT[dtype]).permute(0, 2, 1, 3).contiguous().permute(0, 2, 1, 3)
+    out = torch.zeros(B, 2, 2 * H, 64, dtype=DT[dtype], device="cuda").permute(0, 2, 1, 3)
+    ws = torch.empty(mha.decode_q8_workspace_size(B, 2 * H, H, 2, Lmax, True), dtype=torch.uint8,
+                     device="cuda")
+    assert (ws.numel() == 0) == (path == "one launch")
+    results = []
+    for _ in range(2):                      # the same bits again, the weights' among them
+        cache.weights.zero_()
+        mha.sdpa_decode_q8(tq, cache, i32(lens), scale=0.05, workspace=ws, out=out,
+                           add_weights=True)
+        results.append((out.clone(), cache.weights.clone()))
+        ws.fill_(255)
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+    few = min(B, 2)
+    ref, W, pv, low, qk = oq.decode_ref(Q[:few], {n: a[:few] for n, a in c.items()}, lens, 64,
+                                        "int8", True, scale=0.05)
+    close_decode(out[:few].double().cpu().numpy(), ref, pv, low, qk, Lmax, dtype, path)
+    close_weights(cache.weights[:few].double().cpu().numpy(), 0 * W, W, qk, Lmax, path)
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_decode_rows_without_keys_on_every_path(path, dtype):
+    """Lengths shorter than the number of new queries: the first rows see nothing."""
+    B, H, Lmax = PATHS[path]
+    g = rng(1520)
+    c = plain_cache(g, B, H, Lmax, 32, "e4m3")
+    before = c["weights"].copy()
+    lens = [b % 4 if b or B > 1 else 3 for b in range(B)]
+    Q = fin(g.standard_normal((B, H, 5, 64)), dtype)
+    cache = to_gpu(c, 32, "e4m3")
+    O = mha.sdpa_decode_q8(dev(Q, DT[dtype]), cache, i32(lens), add_weights=True)
+    ref, W, pv, low, qk = oq.decode_ref(Q, c, lens, 32, "e4m3", True)
+    got = O.double().cpu().numpy()
+    close_decode(got, ref, pv, low, qk, 5, dtype, path)
+    assert np.all(got[pv == 0] == 0)
+    w = cache.weights.double().cpu().numpy()
+    close_weights(w, before, W, qk, 5, path)
+    assert np.array_equal(w[W == 0], before[W == 0])
+
+
+@pytest.mark.parametrize("path", PATHS)
+def test_decode_nan_on_every_path(path):
+    """NaN in one query row, in a value and in a key, of sequence 0: it reaches the rows that see
+    it and nothing else, and the weights of a NaN row's positions only."""
+    B, H, Lmax = PATHS[path]
+    g = rng(1540)
+    Nq, L = 4, Lmax - 3
+    for what in ("query", "value", "key"):
+        for at in (L - 2, L // 2):
+            c = plain_cache(g, B, H, Lmax, 16, "e4m3")
+            c["weights"][...] = 0
+            Q = fin(g.standard_normal((B, 2 * H, Nq, 64)), "bf16")
+            want = torch.zeros(B, 2 * H, Nq, 64, dtype=torch.bool)
+            sees = slice(2 if at == L - 2 else 0, Nq)
+            if what == "query":
+                Q[0, 1, 0] = np.nan
+                want[0, 1, 0] = True
+            elif what == "value":
+                c["v"][0, 0, at, 7] = 127
+                want[0, :2, sees, 7] = True
+            else:
+                c["k"][0, 0, at, 9] = 255
+                want[0, :2, sees] = True
+            cache = to_gpu(c, 16, "e4m3")
+            O = mha.sdpa_decode_q8(dev(Q, torch.bfloat16), cache, i32([L] * B), add_weights=True)
+            assert torch.equal(torch.isnan(O).cpu(), want), f"{what} {at}"
+            bad = torch.isnan(cache.weights).cpu()
+            seen = torch.zeros(B, H, Lmax, dtype=torch.bool)
+            if what == "query":
+                seen[0, 0, :L - Nq + 1] = True
+            elif what == "key":
+                seen[0, 0, :L] = True
+            assert torch.equal(bad, seen), f"{what} {at}: weights"
+
+
+@pytest.mark.parametrize("path", PATHS)
+def test_captured_steps_on_every_path(path):
+    """Append and attention with weights in a graph, replayed while the lengths grow over tile and
+    block ends, give what the same calls give outside."""
+    B, H, Lmax = PATHS[path]
+    g = rng(1560)
+    base = plain_cache(g, B, H, Lmax, 64, "int8")
+    steps = [[dev(fin(g.standard_normal((B, H, 1, 64)), "bf16"), torch.bfloat16)
+              for _ in range(3)] for _ in range(5)]
+    ws = torch.empty(mha.decode_q8_workspace_size(B, H, H, 1, Lmax, True), dtype=torch.uint8,
+                     device="cuda")
+
+    def step(cache, q, k, v, n, out):
+        mha.kv_append_q8(cache, k, v, n)
+        n.add_(1)
+        mha.sdpa_decode_q8(q, cache, n, add_weights=True, out=out, workspace=ws)
+
+    def begin():
+        n = i32([(b * 31) % 60 for b in range(B)])
+        n[0] = Lmax - 5
+        return to_gpu(base, 64, "int8"), n, torch.zeros_like(steps[0][0])
+
+    cache, n, out = begin()
+    want = []
+    for s in steps:
+        step(cache, *s, n, out)
+        want.append(out.clone())
+    final = from_gpu(cache)
+    cache, n, out = begin()
+    q, k, v = (torch.empty_like(x) for x in steps[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(cache, q, k, v, n, out)
+    for s, o in zip(steps, want):
+        for a, x in zip((q, k, v), s):
+            a.copy_(x)
+        graph.replay()
+        assert torch.equal(out, o)
+    assert_same(from_gpu(cache), final, "int8", "replayed")
+
+
+def test_prompt_eviction_and_steps_in_two_launches():
+    """The whole sequence of calls on a cache too long for the one-launch step."""
+    g = rng(1580)
+    B, H, N, Lmax, keep, block = 2, 1, 1900, 2000, 1200, 64
+    lens = [1900, 1300]
+    q, k, v = (fin(g.standard_normal((B, H, N, 64)), "bf16") for _ in range(3))
+    tq, tk, tv = (dev(x, torch.bfloat16) for x in (q, k, v))
+    cache = mha.kv_cache_q8(B, H, Lmax, block)
+    n = i32([0, 0])
+    mha.kv_append_q8(cache, tk, tv, n, i32(lens))
+    _, lse = mha.sdpa_with_lse(tq, tk, tv, "causal")
+    mha.sdpa_key_weights(tq, tk, lse, "causal", None, i32(lens), weights=cache.weights)
+    c = from_gpu(cache)
+    small = mha.kv_cache_q8(B, H, keep + 50, block)
+    blank = from_gpu(small)
+    n, kept = mha.kv_evict_q8(cache, small, i32(lens), keep, 100)
+    c, wn, wkept = oq.evict_ref(c, blank, lens, keep, 100, block, "e4m3")
+    assert np.array_equal(kept.cpu().numpy(), wkept) and n.tolist() == wn.tolist()
+    assert mha.decode_q8_workspace_size(B, 2 * H, H, 3, keep + 50, True) > 0
+    for step in range(2):
+        k, v = (fin(g.standard_normal((B, H, 3, 64)), "bf16") for _ in range(2))
+        q = fin(g.standard_normal((B, 2 * H, 3, 64)), "bf16")
+        mha.kv_append_q8(small, dev(k, torch.bfloat16), dev(v, torch.bfloat16), n)
+        c = oq.append_ref(c, k, v, n.tolist(), None, block, "e4m3")
+        n = n + 3
+        O = mha.sdpa_decode_q8(dev(q, torch.bfloat16), small, n, add_weights=True)
+        ref, W, pv, low, qk = oq.decode_ref(q, c, n.tolist(), block, "e4m3", True)
+        close_decode(O.double().cpu().numpy(), ref, pv, low, qk, keep + 8, "bf16", f"step {step}")
+        got = from_gpu(small)
+        close_weights(got["weights"], c["weights"], W, qk, keep + 8, f"weights {step}")
+        c["weights"] = got["weights"]
+        assert_same(got, c, "e4m3", f"cache {step}")
