@@ -1157,12 +1157,20 @@ cudaError_t launch_main(const Params& p, int blocks, cudaStream_t s) {
   return launch_pdl(kern, dim3(blocks), dim3(kMainWarps * 32), smem, s, p);
 }
 // Whether one launch does it all: short caches of few heads (a block each, one per SM), whose rows
-// are one group.  One and two launches, bf16, a row per head: 16 heads of 128 4.1 and 5.2 us, 64 of
-// 384 4.8 and 6.2, 144 of 768 6.2 and 7.9 (with weights 7.5 and 8.2), 16 of 768 5.8 and 5.8 (6.9
-// and 6.2), 16 of 1000 6.5 and 5.8; 304 heads, a second round of blocks, of 384 8.9 and 7.9
+// are one group.  One and two launches in us, bf16 and fp32 without weights, the same with:
+//   8 heads of 128, 1 row    3.6 5.0, 3.9 5.2; 4.1 5.4, 4.2 5.4
+//   8 heads of 768, 1 row    5.2 5.7, 5.7 6.0; 6.0 5.9, 6.4 6.3
+//   8 heads of 768, 8 rows   5.7 5.7, 6.0 6.4; 6.5 6.5, 7.0 7.0
+//   144 heads of 768, 8 rows 5.9 7.9, 6.5 10.3; 7.2 9.3, 7.7 10.3
+//   8 heads of 384, 16 rows  9.0 9.2, 9.6 9.3; 9.8 10.1, 10.8 10.2
+//   8 heads of 768, 16 rows  10.0 9.3, 11.1 9.6; 11.5 10.9, 13.0 11.0
+//   32 heads of 768, 16 rows 10.3 11.0, 11.4 12.1; 11.6 11.7, 13.1 12.5
+// One row of 16 heads of 1000 6.5 and 5.8; 304 heads, a second round of blocks, of 384 8.9 and 7.9.
 bool alone(int B, int H, int Hkv, int Nq, int Lmax) {
-  return Lmax <= kAloneMax && H / Hkv * Nq <= 16 &&
-         static_cast<int64_t>(B) * Hkv <= kAloneSegments;
+  const int rows = H / Hkv * Nq;
+  const int64_t heads = static_cast<int64_t>(B) * Hkv;
+  return rows <= 16 && heads <= kAloneSegments &&
+         Lmax <= (rows > 8 && heads < 32 ? kAloneMax / 2 : kAloneMax);
 }
 template <typename T>
 cudaError_t launch_alone(Params p, int qtype, cudaStream_t s) {
