@@ -202,7 +202,7 @@ int mha_sdpa_decode_fwd(int B, int H, int Nq, int Lmax, int d_k, int d_v, int dt
  * query head h reads cache head h / (H_q / H)).  Strides of caches count bytes (elements of one
  * byte): {b, h, n} multiples of 16 and > 0, d stride 1, 16-byte aligned pointers.  Lengths are
  * device memory, so the calls can be captured into a CUDA graph and replayed with new lengths.
- * None of the four adds with atomics: results are bitwise reproducible.
+ * None of the four adds floating-point numbers with atomics: results are bitwise reproducible.
  */
 typedef enum { MHA_Q8_E4M3 = 0, MHA_Q8_I8 = 1 } mha_q8;
 
@@ -243,8 +243,8 @@ int mha_decode_q8_workspace_size(int B, int H, int Hkv, int Nq, int Lmax, int wi
  *   Q [B,H,Nq,64], O [B,H,Nq,64] (dtype); caches and scales with Hkv heads, H a multiple of
  *   Hkv.  cache_len, causal, scale and rows without an allowed key (zeros, no weight) as for
  *   mha_sdpa_decode_fwd; 1 <= Nq <= 16, Nq <= Lmax, H / Hkv * Nq <= 4096.  Positions past
- *   cache_len may hold anything.  Scales must be positive and within [2^-40, 2^40]; they need
- *   not be powers of two.
+ *   cache_len may hold anything.  Scales must be positive and within [2^-40, 2^40], however far
+ *   apart; they need not be powers of two.
  *   strides: NULL for contiguous, or 16 strides {Q, K, V, O} x {b, h, n, d} (Q, O in elements
  *   as for mha_kv_append_q8's K).  O may not alias an input.
  *   workspace: mha_decode_q8_workspace_size() bytes, 256-byte aligned (may be NULL when that is
@@ -270,9 +270,9 @@ int mha_key_weights_workspace_size(int B, int H, int Hkv, int Nq, int Nk, int dt
  *     weights[b,g,j] += sum over the query heads h of group g and i of
  *                       exp(Q[b,h,i] . K[b,g,j] * scale - lse[b,h,i])          (allowed pairs)
  *   Q [B,H,Nq,64], K [B,Hkv,Nk,64] (dtype, the values before quantisation), lse fp32 [B,H,Nq]
- *   contiguous (rows with +inf, whose Q must be finite, add nothing).  mask, key_len, scale as for mha_sdpa_fwd;
- *   query_len int32[B], clamped to [0, Nq], or NULL: rows i >= query_len[b] of a padded batch
- *   add nothing and may hold anything.  Keys j >= key_len[b] keep their weights.
+ *   contiguous (rows with +inf, whose Q must be finite, add nothing).  mask, key_len, scale as
+ *   for mha_sdpa_fwd; query_len int32[B], clamped to [0, Nq], or NULL: rows i >= query_len[b] of
+ *   a padded batch add nothing and may hold anything.  Keys j >= key_len[b] keep their weights.
  *   weights [B, Hkv, weights_ld], weights_ld >= Nk: only the first Nk of each head change.
  *   strides: NULL for contiguous, or 8 element strides {Q, K} x {b, h, n, d} as for
  *   mha_kv_append_q8's K.  workspace: mha_key_weights_workspace_size() bytes, 256-byte aligned

@@ -40,8 +40,8 @@
 // joins a row's pieces, and adds the weights 2^(x_ij - m_i) / l_i from the scores that the first
 // one stored.  Short caches of few heads take one launch, a block to a head, whose warps' pieces
 // and scores meet in shared memory.  No atomics: one order of sums.
-// 64 x 16 heads x 4096 positions 84 us (6.4 TB/s), with weights 101; 8 x 8 heads of 16 rows and up
-// to 16384 positions, with weights, 33; 8 heads x 131072, fp32, 30; 8 heads x 37 4.1.
+// 64 x 16 heads x 4096 positions 85 us (6.3 TB/s), with weights 101; 8 x 8 heads of 16 rows and up
+// to 16384 positions, with weights, 33; 8 heads x 131072, fp32, 29; 8 heads x 37 4.2.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -277,7 +277,6 @@ __device__ __forceinline__ void put2(__nv_bfloat16* q, float a, float b) {
 __device__ __forceinline__ void put2(float* q, float a, float b) {
   *reinterpret_cast<float2*>(q) = make_float2(a, b);
 }
-
 
 // Joins (m, l) with the maxima and sums st of 2 kHalf lanes (kNone, 0: none), the same for all of
 // them.  Returns the factor of the lane's own; `old`: that of what was in (m, l)
@@ -909,8 +908,6 @@ struct Pieces {
   __device__ __forceinline__ int first(int hr) const { return (start + hr * nt) / run; }
   __device__ __forceinline__ int last(int hr) const { return (start + hr * nt + nt - 1) / run; }
 };
-
-
 
 // Merges (m2, l2) into (m, l): sums l under the larger maximum (kNone: nothing there; a NaN sum
 // must not be lost).  Returns the two factors.
