@@ -125,8 +125,8 @@ __global__ void __launch_bounds__(kThreads) kv_append_q8_kernel(const KvAppendAr
   const float fresh = pow2i(q8_exponent<QT>(amax));
   const float now = fmaxf(was, fresh);
   if (tid == 0) *scale = now;
-  // (exact for the library's own scales, powers of two; under another that was there x * inv is what
-  // is rounded to the code)
+  // (exact for the library's own scales, powers of two; under another that was there x * inv is
+  // what is rounded to the code)
   const float inv = 1.f / now;
 #pragma unroll
   for (int k = 0; k < kRows; ++k) {

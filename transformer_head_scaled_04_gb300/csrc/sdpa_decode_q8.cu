@@ -41,7 +41,7 @@
 // one stored.  Short caches of few heads take one launch, a block to a head, whose warps' pieces
 // and scores meet in shared memory.  No atomics: one order of sums.
 // 64 x 16 heads x 4096 positions 85 us (6.3 TB/s), with weights 101; 8 x 8 heads of 16 rows and up
-// to 16384 positions, with weights, 33; 8 heads x 131072, fp32, 29; 8 heads x 37 4.2.
+// to 16384 positions, with weights, 31; 8 heads x 131072, fp32, 29; 8 heads x 37 4.1.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -58,7 +58,7 @@ constexpr int kD = 64;
 constexpr int kTile = 32;                  // positions per tile
 constexpr int kTileBytes = kTile * kD;     // 2 KB of K, 2 KB of V
 constexpr int kStages = 3;
-constexpr int kAloneMax = 768, kAloneSegments = 152;  // see alone()
+constexpr int kAloneMax = 768, kAloneFewer = 512, kAloneSegments = 152;  // see alone()
 constexpr int kAlonePad = 4;               // floats between rows of scores: other banks
 constexpr int kSlotBytes = 2 * kTileBytes;
 constexpr int kWarps = 8;                  // of the join
@@ -722,100 +722,95 @@ __global__ void __launch_bounds__(register_threads(sizeof(T) / 2, NR, kAlone), 1
       }
       return true;
     };
-    // Any tile.  (In one body with the above, masks cost the other tiles 78 of 562 instructions and
-    // 14% of the time: 16 rows, 8 x 8 x 16384 positions.)  Weights are 2^(x - ref) under the
-    // largest score of the row's 16 positions: the difference of two scores is exact where it
-    // counts, whatever their size.  2^(ref - m) brings their sum under the row's reference and, with the
-    // values' scale, their product.  The two groups follow one another, which takes half the code
-    // and registers (128 rows to a head 145 us; both at once 153), but where one launch does it all
-    // and this tile is the last thing that is waited for (8 heads x 37 4.2 and 4.5 us).
+    // Any tile, its two groups one after the other, for half the code and registers.  (In one body
+    // with the above, masks cost the other tiles 78 of 562 instructions and 14% of the time: 16
+    // rows, 8 x 8 x 16384 positions.  Both groups at once: 128 rows to a head 153 us, not 143; 8
+    // heads x 37 4.1 either way.)  Weights are 2^(x - ref) under the largest score of the row's 16
+    // positions: the difference of two scores is exact where it counts, whatever their size.
+    // 2^(ref - m) brings their sum under the row's reference and, with the values' scale, their
+    // product.
     auto careful_tile = [&]() {
-      constexpr int kAtOnce = kAlone ? 2 : 1;
 #pragma unroll 1
-      for (int q0 = 0; q0 < 2; q0 += kAtOnce) {
-        float x[kAtOnce][NR][4], ref[kAtOnce][NR][2], top[NR][2];
+      for (int q = 0; q < 2; ++q) {
+        float x[NR][4], ref[NR][2], top[NR][2];
         bool grew = false;
+        scores(q, x);
+        const float ks = __shfl_sync(0xffffffffu, sc, q);
+        const float vs = __shfl_sync(0xffffffffu, sc, 2 + q);
+        const float ev = __shfl_sync(0xffffffffu, sc_log, 2 + q);
+        const int at = pos + q * 16;
 #pragma unroll
-        for (int i = 0; i < kAtOnce; ++i) scores(q0 + i, x[i]);
+        for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-        for (int i = 0; i < kAtOnce; ++i) {
-          const float ks = __shfl_sync(0xffffffffu, sc, q0 + i);
-          const float ev = __shfl_sync(0xffffffffu, sc_log, 2 + q0 + i);
-          const int at = pos + (q0 + i) * 16 + g;
-#pragma unroll
-          for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float f = ks * (e ? qs[nr].y : qs[nr].x);
-              float &x0 = x[i][nr][e], &x1 = x[i][nr][2 + e];
-              x0 = at > lim[nr][e] ? -INFINITY : __fmul_rn(x0, f);
-              x1 = at + 8 > lim[nr][e] ? -INFINITY : __fmul_rn(x1, f);
-              if (score_row != nullptr && nr * 8 + e < rows_here) {
-                float* dst = score_row + (nr * 8 + e) * p.Lpad + at - g;
-                dst[0] = x0;
-                dst[8] = x1;
-              }
-              const float v = row_max(fmaxf(x0, x1));
-              ref[i][nr][e] = v;
-              top[nr][e] = i == 0 ? v + ev : fmaxf(top[nr][e], v + ev);
-              grew |= top[nr][e] > m[nr][e];
+          for (int e = 0; e < 2; ++e) {
+            const float f = ks * (e ? qs[nr].y : qs[nr].x);
+            float &x0 = x[nr][e], &x1 = x[nr][2 + e];
+            x0 = at + g > lim[nr][e] ? -INFINITY : __fmul_rn(x0, f);
+            x1 = at + g + 8 > lim[nr][e] ? -INFINITY : __fmul_rn(x1, f);
+            if (score_row != nullptr && nr * 8 + e < rows_here) {
+              float* dst = score_row + (nr * 8 + e) * p.Lpad + at;
+              dst[0] = x0;
+              dst[8] = x1;
             }
-        }
+            ref[nr][e] = row_max(fmaxf(x0, x1));
+            top[nr][e] = ref[nr][e] + ev;
+            grew |= top[nr][e] > m[nr][e];
+          }
         if (__any_sync(0xffffffffu, grew)) rise(top);
+        uint2 v[4];
+        uint32_t b0[8], b1[8];
+        [[maybe_unused]] uint32_t nan = 0;
+        value_codes(q, v);
 #pragma unroll
-        for (int i = 0; i < kAtOnce; ++i) {
-          const float vs = __shfl_sync(0xffffffffu, sc, 2 + q0 + i);
-          uint2 v[4];
-          uint32_t b0[8], b1[8];
-          value_codes(q0 + i, v);
-#pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            // rows behind the last position hold anything: 0.  A NaN among the rows that some query
-            // may not see must reach only those that do: taken out of the product here, put into O
-            // below
-            if (pos + (q0 + i) * 16 + 2 * t + (z >> 1) * 8 + (z & 1) >= c.L)
-              v[z] = make_uint2(0u, 0u);
-            if constexpr (QT == kE4m3) {
-              v[z].x &= ~__vcmpeq4(v[z].x & 0x7f7f7f7fu, 0x7f7f7f7fu);
-              v[z].y &= ~__vcmpeq4(v[z].y & 0x7f7f7f7fu, 0x7f7f7f7fu);
-            }
-          }
-          value_halves(v, b0, b1);
-#pragma unroll
-          for (int nr = 0; nr < NR; ++nr) {
-            uint32_t pf[kTerms][2];
-            float into_l[2], into_o[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              into_l[e] = ex2_approx(ref[i][nr][e] - m[nr][e]);
-              into_o[e] = into_l[e] * vs;
-              if (ref[i][nr][e] == -INFINITY) ref[i][nr][e] = 0.f;  // none allowed: weights of 0
-            }
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              const float w0 = ex2_approx(x[i][nr][2 * z] - ref[i][nr][0]) * kLift;
-              const float w1 = ex2_approx(x[i][nr][2 * z + 1] - ref[i][nr][1]) * kLift;
-              l[nr].x = fmaf(w0, into_l[0], l[nr].x);
-              l[nr].y = fmaf(w1, into_l[1], l[nr].y);
-              const uint32_t hi = pack_half(w0, w1);
-              pf[0][z] = transpose8x8(hi);
-              if constexpr (kTerms == 2) pf[kTerms - 1][z] = transpose8x8(pack_rest(w0, w1, hi));
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t fa[4] = {b0[2 * j], b0[2 * j + 1], b1[2 * j], b1[2 * j + 1]};
-              float d[4];
-              mma16816_zero(d, fa, pf[kTerms - 1][0], pf[kTerms - 1][1]);
-              if constexpr (kTerms == 2) mma16816(d, fa, pf[0][0], pf[0][1]);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) o[nr][j][k] = fmaf(d[k], into_o[k & 1], o[nr][j][k]);
-            }
+        for (int z = 0; z < 4; ++z) {
+          // rows behind the last position hold anything: 0.  A NaN among the rows that some query
+          // may not see must reach only those that do: taken out of the product here, put into O
+          // below
+          if (at + 2 * t + (z >> 1) * 8 + (z & 1) >= c.L) v[z] = make_uint2(0u, 0u);
+          if constexpr (QT == kE4m3) {
+            const uint32_t nx = __vcmpeq4(v[z].x & 0x7f7f7f7fu, 0x7f7f7f7fu);
+            const uint32_t ny = __vcmpeq4(v[z].y & 0x7f7f7f7fu, 0x7f7f7f7fu);
+            v[z].x &= ~nx;
+            v[z].y &= ~ny;
+            nan |= nx | ny;
           }
         }
-        if constexpr (QT == kE4m3) {
-          // columns 8g .. 8g+7 of each position: NaN into the rows that see it
-          const int end = min((q0 + kAtOnce) * 16, c.L - pos);
-          for (int row = q0 * 16; row < end; ++row) {
+        value_halves(v, b0, b1);
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) {
+          uint32_t pf[kTerms][2];
+          float into_l[2], into_o[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            into_l[e] = ex2_approx(ref[nr][e] - m[nr][e]);
+            into_o[e] = into_l[e] * vs;
+            if (ref[nr][e] == -INFINITY) ref[nr][e] = 0.f;  // none allowed: weights of 0
+          }
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            const float w0 = ex2_approx(x[nr][2 * z] - ref[nr][0]) * kLift;
+            const float w1 = ex2_approx(x[nr][2 * z + 1] - ref[nr][1]) * kLift;
+            l[nr].x = fmaf(w0, into_l[0], l[nr].x);
+            l[nr].y = fmaf(w1, into_l[1], l[nr].y);
+            const uint32_t hi = pack_half(w0, w1);
+            pf[0][z] = transpose8x8(hi);
+            if constexpr (kTerms == 2) pf[kTerms - 1][z] = transpose8x8(pack_rest(w0, w1, hi));
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t fa[4] = {b0[2 * j], b0[2 * j + 1], b1[2 * j], b1[2 * j + 1]};
+            float d[4];
+            mma16816_zero(d, fa, pf[kTerms - 1][0], pf[kTerms - 1][1]);
+            if constexpr (kTerms == 2) mma16816(d, fa, pf[0][0], pf[0][1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[nr][j][i] = fmaf(d[i], into_o[i & 1], o[nr][j][i]);
+          }
+        }
+        if (QT == kE4m3 && __any_sync(0xffffffffu, nan != 0)) {
+          // columns 8g .. 8g+7 of each position: NaN into the rows that see it (looked for in every
+          // last tile, row by row, this took 16 rows of 8 x 8 heads x 8192 28.4 us instead of 26.8)
+          const int end = min(q * 16 + 16, c.L - pos);
+          for (int row = q * 16; row < end; ++row) {
             const uint2 u = *reinterpret_cast<const uint2*>(
                 sV + row * kD + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + (g & 1) * 8);
             if ((__vcmpeq4(u.x & 0x7f7f7f7fu, 0x7f7f7f7fu) |
@@ -1155,19 +1150,19 @@ cudaError_t launch_main(const Params& p, int blocks, cudaStream_t s) {
 }
 // Whether one launch does it all: short caches of few heads (a block each, one per SM), whose rows
 // are one group.  One and two launches in us, bf16 and fp32 without weights, the same with:
-//   8 heads of 128, 1 row    3.6 5.0, 3.9 5.2; 4.1 5.4, 4.2 5.4
-//   8 heads of 768, 1 row    5.2 5.7, 5.7 6.0; 6.0 5.9, 6.4 6.3
-//   8 heads of 768, 8 rows   5.7 5.7, 6.0 6.4; 6.5 6.5, 7.0 7.0
-//   144 heads of 768, 8 rows 5.9 7.9, 6.5 10.3; 7.2 9.3, 7.7 10.3
-//   8 heads of 384, 16 rows  9.0 9.2, 9.6 9.3; 9.8 10.1, 10.8 10.2
-//   8 heads of 768, 16 rows  10.0 9.3, 11.1 9.6; 11.5 10.9, 13.0 11.0
-//   32 heads of 768, 16 rows 10.3 11.0, 11.4 12.1; 11.6 11.7, 13.1 12.5
+//   8 heads of 128, 1 row     3.7 4.9, 3.8 4.8;  4.2 5.1, 4.2 5.2
+//   8 heads of 768, 1 row     5.1 5.4, 5.6 5.7;  5.9 5.9, 6.5 6.2
+//   8 heads of 768, 8 rows    5.4 5.6, 6.2 6.4;  6.4 6.5, 7.0 6.8
+//   144 heads of 768, 8 rows  5.9 7.9, 6.6 10.3; 7.2 9.2, 7.8 10.3
+//   8 heads of 512, 16 rows   7.0 7.4, 7.8 8.0;  8.2 8.7, 9.1 9.1
+//   8 heads of 768, 16 rows   8.0 7.4, 9.0 8.2;  9.3 9.0, 10.8 9.3
+//   32 heads of 768, 16 rows  8.4 9.0, 9.4 10.3; 9.7 9.7, 11.1 11.0
 // One row of 16 heads of 1000 6.5 and 5.8; 304 heads, a second round of blocks, of 384 8.9 and 7.9.
 bool alone(int B, int H, int Hkv, int Nq, int Lmax) {
   const int rows = H / Hkv * Nq;
   const int64_t heads = static_cast<int64_t>(B) * Hkv;
   return rows <= 16 && heads <= kAloneSegments &&
-         Lmax <= (rows > 8 && heads < 32 ? kAloneMax / 2 : kAloneMax);
+         Lmax <= (rows > 8 && heads < 32 ? kAloneFewer : kAloneMax);
 }
 template <typename T>
 cudaError_t launch_alone(Params p, int qtype, cudaStream_t s) {
