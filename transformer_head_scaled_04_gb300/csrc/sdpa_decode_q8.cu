@@ -77,18 +77,19 @@ RowPlan row_plan(int H, int Hkv, int Nq, int dtype) {
   RowPlan p;
   p.R = H / Hkv * Nq;
   // The column tiles of a group share each converted operand; fp32's second terms leave the
-  // registers for two, bf16's for four, but then for eight warps instead of twelve: 8 x 8 heads x
-  // 16384 positions with 128 rows each 182 us against 207 with two, 64 rows 116 against 108, 32
-  // rows 63 against 62
+  // registers for two, bf16's for four, but then for eight warps instead of twelve.  Four against
+  // two: 8 x 8 heads x 16384 positions with 128 rows each 143 and 163 us (with weights 294 and
+  // 379), 64 rows 80 and 83, lengths up to that 52.4 and 52.5, up to 2048 19.5 and 16.1; 32 rows
+  // up to 16384 35.9 and 34.3
   p.NR = p.R <= 8 ? 1 : p.R <= 64 || dtype != 1 ? 2 : 4;
   p.RG = (p.R + 8 * p.NR - 1) / (8 * p.NR);
   p.RS = std::min(p.R, 8 * p.NR);
   return p;
 }
 // Warps of the first launch's one block per SM, by the registers that its operands take.  Twelve
-// where 168 registers a thread do: sixteen at 128 spilled (16 rows, 8 x 8 x 65536 positions 95.9
-// -> 99.5 us) or kept more requests in flight than HBM takes well (64 x 16 heads x 4096 positions,
-// three slots each, 87.4 -> 91.9 us), eight left the tensor cores waiting (95.9 -> 102.4 us).
+// where 168 registers a thread do.  Sixteen at 128 spill (16 rows, 8 x 8 x 65536 positions 89.5 ->
+// 97.7 us) or keep more requests in flight than HBM takes well (64 x 16 heads x 4096 positions 86.7
+// -> 90.2 us); eight leave the tensor cores waiting (92.5 and 125 us).
 constexpr int main_warps(int terms, int nr) { return terms * nr <= 2 ? 12 : 8; }
 // Threads that the registers are shared out for.  bf16 queries of one column tile take 128 each at
 // most, as for 16 warps, which leaves room for a block of the join to wait on the SM (one sequence

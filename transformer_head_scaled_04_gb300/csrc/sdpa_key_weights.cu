@@ -22,8 +22,10 @@
 // the next chunk on its way from global memory meanwhile.  The (head, chunk) pairs are split over
 // CTAs as above.  8 heads x 8 padded prompts of up to 1000 take 59 us, a causal prompt of 1024 23
 // us; with one fp32 multiply-add per term and lane = key, whose operands came from shared memory
-// at a quarter of the units' rate, 156 and 58 us.  Bound by the products and their scaling: each
-// score costs three products of 64 terms, its four parts' sum and one exponential.
+// at a quarter of the units' rate, 156 and 58 us.  The price of 22 bits: a weight is off by 7e-8 to
+// 9e-8 (rms, padded prompts of 333), with products in fp32 4e-8 to 5e-8.  Bound by waits inside a
+// warp: of 3.5 warps per scheduler 2.9 wait for the product before theirs in a chain of three or
+// for its sums (47% of issue slots used, 37% of the mma.sync pipe).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -525,7 +527,7 @@ __global__ void __launch_bounds__(256) key_weights_add_kernel(const KwParams p) 
 
 // CTAs per key tile: enough for two on each of 152 SMs (fp32: twice that, for shorter CTAs), no
 // more than there are query tiles or chunks.  Against one CTA per key tile: a bf16 head of 4096
-// 10.3 and 22.3 us, four 20.1 and 22.3; three fp32 prompts of 333 13.6 and 43.9
+// 9.9 and 22.3 us, four 20.1 and 22.3; three fp32 prompts of 333 12.5 and 43.9
 int key_weights_split(int B, int H, int Hkv, int Nq, int Nk, int dtype) {
   const int keys = dtype == 1 ? kT : kKeys, rows = dtype == 1 ? kT : kQueries;
   const int64_t units = static_cast<int64_t>(B) * Hkv * ((Nk + keys - 1) / keys);
