@@ -33,7 +33,7 @@
 // fp32 queries and weights are split into two fp16 terms (22 bits) and their products done
 // twice, each inner step's part of a score and each tile's PV summed apart and added in fp32
 // (the tensor cores' own accumulation truncates).  With bf16 queries the four inner steps and the
-// tiles' PV are summed by the tensor cores and a weight is one fp16 term, 2^-12 off at most: an
+// tiles' PV are summed by the tensor cores and a weight is one fp16 term, 2^-11 off at most: an
 // eighth of the output's own rounding to bf16 even if all of a row's weights erred alike.  Beyond
 // references of 4096 exponents are differences of two scores, rounded as the stored ones.
 // Runs end at heads' ends: each piece leaves (O, m, l) in the workspace, and a second launch
@@ -809,7 +809,7 @@ __global__ void __launch_bounds__(register_threads(sizeof(T) / 2, NR, kAlone), 1
         }
         if (QT == kE4m3 && __any_sync(0xffffffffu, nan != 0)) {
           // columns 8g .. 8g+7 of each position: NaN into the rows that see it (looked for in every
-          // last tile, row by row, this took 16 rows of 8 x 8 heads x 8192 28.4 us instead of 26.8)
+          // last tile, row by row: 16 rows of 8 x 8 heads x up to 16384 28.4 us instead of 26.8)
           const int end = min(q * 16 + 16, c.L - pos);
           for (int row = q * 16; row < end; ++row) {
             const uint2 u = *reinterpret_cast<const uint2*>(
