@@ -503,7 +503,8 @@ __global__ void __launch_bounds__(register_threads(sizeof(T) / 2, NR, kAlone), 1
     bool huge = false;
     // A tile with a value scale 2^kApart or more below the largest so far has weights that fp16
     // would round away under the row's reference (what is below 2^-38 of its largest), and they may
-    // be all that a column has: it is taken under references of its own as well
+    // be all that a column has: it is taken under references of its own as well (64 x 16 heads x
+    // 4096 with every other block 2^15 smaller 99 us instead of 84, scores of 1e5 102)
     float most_log = -INFINITY, value_log[2] = {0.f, 0.f};
     bool apart = false;
     float sc_next = load_scale(c.kt), sc = 1.f, sc_log = 0.f, sc_inv = 1.f;
