@@ -306,6 +306,92 @@ int mha_kv_evict_q8(int B, int H, int Lmax, int Lmax_out, int d_k, int d_v, int 
                     const int64_t* strides, cudaStream_t stream);
 
 /*
+ * Attention with a learned relative position bias: the score of query position i and key position j
+ * gets a number that is learned per head and bucket of their distance d = j - i,
+ *     S[b,h,i,j] = Q[b,h,i] . K[b,h,j] * scale + bias[bucket(j - i), h].
+ * This is position information from the neighbourhood that [JY] Self-Attention的优势 speaks of, put
+ * where the softmax weighs the positions; the pages themselves add positions to the embeddings.
+ *   bias     [num_buckets, H], contiguous, of type bias_dtype (fp32 or bf16, whatever dtype is; the
+ *            layout of an embedding over the buckets).  Read as fp32.  A value below -1e30 (-inf, the
+ *            lowest value of a type) excludes its bucket; +inf and NaN give NaN.
+ *   buckets  2 <= num_buckets <= 128.  bidirectional = 1: num_buckets even and at least 4, keys
+ *            after the query (d > 0) have the upper half of the buckets, the others the lower half;
+ *            bidirectional = 0: all buckets are for keys up to the query, and keys after it share
+ *            bucket 0.  With per = buckets of a side, e = per / 2 (rounded down), n = |d| (0 for
+ *            keys after the query if not bidirectional):
+ *              n < e: bucket n;  else min(per - 1, e + floor((per - e) log(n / e) /
+ *                                                        log(max_distance / e)))
+ *            in exact arithmetic (a distance on a border belongs to the farther bucket);
+ *            max_distance > e, from which on all distances share a side's last bucket.
+ *   lengths  up to 2^24 positions.
+ *   d_k, d_v bf16: 64.  fp32: 1..128, computed on the tensor cores with every value split into two
+ *            tf32 terms (relative error 2^-22 per factor; sums in fp32).
+ * Keys past key_len[b] (cache_len[b]) may hold anything, infinities and NaN included.
+ */
+
+/*
+ * mha_rel_bucket -- bucket(distance), 0 .. num_buckets - 1, on the host; a negative mha_status for
+ * numbers that describe no buckets (MHA_ERR_INVALID; more than 128: MHA_ERR_UNSUPPORTED).
+ */
+int mha_rel_bucket(int distance, int num_buckets, int max_distance, int bidirectional);
+
+/*
+ * mha_sdpa_rel_fwd -- mha_sdpa_fwd (lse NULL) or mha_sdpa_fwd_lse with the bias.  Q, K, V, O, mask,
+ * key_len, scale, strides and lse as there, but strides of d are 1 for both types, and those of O
+ * positive.  A row without an allowed key (key_len = 0, or all its buckets excluded) is written as
+ * zeros with lse +inf.
+ */
+int mha_sdpa_rel_fwd(int B, int H, int Nq, int Nk, int d_k, int d_v, int dtype, int mask,
+                     const int32_t* key_len, float scale, const void* Q, const void* K,
+                     const void* V, const void* bias, int bias_dtype, int num_buckets,
+                     int max_distance, int bidirectional, void* O, const int64_t* strides,
+                     float* lse, cudaStream_t stream);
+
+/*
+ * mha_sdpa_rel_bwd_workspace_size -- bytes of device workspace mha_sdpa_rel_bwd needs: that of
+ * mha_sdpa_bwd and num_buckets fp32 sums per (b, h, 128 keys) (fp32: per 64 queries).
+ */
+int mha_sdpa_rel_bwd_workspace_size(int B, int H, int Nq, int Nk, int dtype, int num_buckets,
+                                    size_t* bytes);
+
+/*
+ * mha_sdpa_rel_bwd -- mha_sdpa_bwd with the bias, from O and lse of mha_sdpa_rel_fwd with the same
+ * arguments; also the gradient of the bias,
+ *     dbias[u,h] = sum over b and the allowed (i, j) with bucket(j - i) = u of dS[b,h,i,j],
+ * written (not added) as [num_buckets, H] of type bias_dtype; buckets that no allowed pair falls
+ * into get 0.  It is summed in fp32 in a fixed order: bitwise reproducible, whatever
+ * mha_set_deterministic says (that switch works on dQ as it does for mha_sdpa_bwd).  Strides and
+ * workspace as for mha_sdpa_bwd; calls that may run at the same time need a workspace each.
+ */
+int mha_sdpa_rel_bwd(int B, int H, int Nq, int Nk, int d_k, int d_v, int dtype, int mask,
+                     const int32_t* key_len, float scale, const void* Q, const void* K,
+                     const void* V, const void* bias, int bias_dtype, int num_buckets,
+                     int max_distance, int bidirectional, const void* O, const void* dO,
+                     const float* lse, void* dQ, void* dK, void* dV, void* dbias,
+                     const int64_t* strides, void* workspace, size_t ws_bytes,
+                     cudaStream_t stream);
+
+/*
+ * mha_sdpa_rel_decode_workspace_size -- bytes of device workspace mha_sdpa_rel_decode_fwd needs
+ * (0 for short caches of many heads).
+ */
+int mha_sdpa_rel_decode_workspace_size(int B, int H, int Nq, int Lmax, int d_k, int d_v, int dtype,
+                                       size_t* bytes);
+
+/*
+ * mha_sdpa_rel_decode_fwd -- mha_sdpa_decode_fwd with the bias: query r of batch element b is at
+ * position cache_len[b] - Nq + r, whether causal or not.  1 <= Nq <= 16 for both types; cache_len,
+ * causal, scale and rows without an allowed key as there; strides of d are 1.  workspace:
+ * mha_sdpa_rel_decode_workspace_size() bytes, 256-byte aligned (may be NULL when that is 0); calls
+ * that may run at the same time need one each.
+ */
+int mha_sdpa_rel_decode_fwd(int B, int H, int Nq, int Lmax, int d_k, int d_v, int dtype, int causal,
+                            const int32_t* cache_len, float scale, const void* Q, const void* K,
+                            const void* V, const void* bias, int bias_dtype, int num_buckets,
+                            int max_distance, int bidirectional, void* O, const int64_t* strides,
+                            void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/*
  * mha_layer_workspace_size -- bytes of device workspace mha_layer_fwd needs for these sizes.
  * The workspace holds the projected Q/K/V, the head-concat buffer and the W^O output.
  */

@@ -33,3 +33,4 @@ from .backward import (  # noqa: F401
     mha_layer_bwd_ref,
 )
 from . import cache_q8  # noqa: F401
+from . import rel_bias  # noqa: F401

@@ -46,3 +46,12 @@ from .cache_q8 import (  # noqa: F401
     sdpa_decode_q8,
     sdpa_key_weights,
 )
+from .rel_bias import (  # noqa: F401
+    rel_bucket,
+    sdpa_rel,
+    sdpa_rel_backward,
+    sdpa_rel_bwd_workspace_size,
+    sdpa_rel_decode,
+    sdpa_rel_decode_workspace_size,
+    sdpa_rel_with_lse,
+)

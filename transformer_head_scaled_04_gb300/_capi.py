@@ -43,6 +43,15 @@ PROTOTYPES = {
     "mha_sdpa_key_weights": (_c_int, [_c_int] * 8 + [_vp, _vp, _c_float] + [_vp] * 5
                              + [_i64, _vp, _size, _vp]),
     "mha_kv_evict_q8": (_c_int, [_c_int] * 10 + [_vp] * 15),
+    "mha_rel_bucket": (_c_int, [_c_int] * 4),
+    "mha_sdpa_rel_fwd": (_c_int, [_c_int] * 8 + [_vp, _c_float] + [_vp] * 4 + [_c_int] * 4
+                         + [_vp] * 4),
+    "mha_sdpa_rel_bwd_workspace_size": (_c_int, [_c_int] * 6 + [ctypes.POINTER(_size)]),
+    "mha_sdpa_rel_bwd": (_c_int, [_c_int] * 8 + [_vp, _c_float] + [_vp] * 4 + [_c_int] * 4
+                         + [_vp] * 9 + [_size, _vp]),
+    "mha_sdpa_rel_decode_workspace_size": (_c_int, [_c_int] * 7 + [ctypes.POINTER(_size)]),
+    "mha_sdpa_rel_decode_fwd": (_c_int, [_c_int] * 8 + [_vp, _c_float] + [_vp] * 4 + [_c_int] * 4
+                                + [_vp] * 3 + [_size, _vp]),
     "mha_layer_workspace_size": (_c_int, [_c_int] * 8 + [ctypes.POINTER(_size)]),
     "mha_layer_fwd": (_c_int, [_c_int] * 9 + [_vp, _c_float] + [_vp] * 10 + [_size, _vp]),
     "mha_layer_bwd_workspace_size": (_c_int, [_c_int] * 9 + [ctypes.POINTER(_size)]),

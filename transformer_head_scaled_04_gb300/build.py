@@ -27,9 +27,10 @@ SOURCES = ["capi.cu", "gemm_bf16.cu", "gemm_f32.cu", "sdpa_bf16.cu", "sdpa_f32.c
            "gemm_ln_bf16.cu", "gemm2_bf16.cu",
            "layer_noalloc.cu", "layer_host.cu",
            "capi_q8.cu", "kv_append_q8.cu", "sdpa_decode_q8.cu", "sdpa_key_weights.cu",
-           "kv_evict_q8.cu"]
-HEADERS = ["device_common.cuh", "launchers.h", "mma_f16.cuh", "nvtx_range.h",
-           "q8_common.cuh"]
+           "kv_evict_q8.cu",
+           "capi_rel.cu", "rel_plan.cu", "sdpa_rel_f32.cu", "sdpa_rel_decode.cu"]
+HEADERS = ["device_common.cuh", "launchers.h", "mma_f16.cuh", "mma_tf32.cuh", "nvtx_range.h",
+           "q8_common.cuh", "rel_bias.cuh", "rel_plan.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

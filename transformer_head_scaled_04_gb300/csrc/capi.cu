@@ -469,6 +469,9 @@ bool encode_map_bf16(CUtensorMap* m, const void* base, int B, int H, int N, cons
                      uint32_t box_rows) {
   return map_bhnd_bf16(m, base, B, H, N, st, box_rows);
 }
+bool encode_map_dq_acc(CUtensorMap* m, const void* base, int B, int H, int rows) {
+  return map_dq_acc_f32(m, base, B, H, rows);
+}
 cudaError_t launch_wait_selftest(const DevCtx& ctx, cudaStream_t s) {
   wait_selftest_kernel<<<1, 32, 0, s>>>(ctx.status, ctx.timeout_ns);
   return cudaGetLastError();

@@ -7,6 +7,8 @@
 #include <cstdint>
 #include <utility>
 
+#include "rel_plan.h"
+
 namespace mha {
 
 // Per-launch device context: where kernels record errors, and how long a bounded wait may
@@ -33,6 +35,8 @@ int current_device_ctx(DevCtx* ctx);
 // d = 1}, 128-byte swizzle, box {64, box_rows, 1, 1}
 bool encode_map_bf16(CUtensorMap* m, const void* base, int B, int H, int N, const int64_t* st,
                      uint32_t box_rows);
+// map of the fp32 dQ accumulator [B, H, rows, 64]: box {32, 32, 1, 1}, 128-byte swizzle
+bool encode_map_dq_acc(CUtensorMap* m, const void* base, int B, int H, int rows);
 
 // ---- per-kernel launch preparation: raises the kernel's dynamic shared-memory limit to
 // smem_bytes and reports its register count (num_regs may be null), once per (kernel, device);
@@ -258,6 +262,38 @@ cudaError_t launch_sdpa_bwd_bf16(const CUtensorMap& tmQ, const CUtensorMap& tmK,
                                  const CUtensorMap& tmV, const CUtensorMap& tmG,
                                  const CUtensorMap& tmDQ, const SdpaBwdArgs& a,
                                  const DevCtx& ctx, cudaStream_t s);
+
+// ---- attention with a learned relative position bias (rel_bias.cuh): as the launches above with
+// the bias added; SdpaArgs::lse may be null, masks are those of mha_mask
+cudaError_t launch_sdpa_rel_bf16(const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                                 const CUtensorMap& tmV, const CUtensorMap& tmO,
+                                 const SdpaArgs& a, const RelBias& rel, const DevCtx& ctx,
+                                 cudaStream_t s);
+cudaError_t launch_sdpa_rel_f32(const SdpaArgs& a, const RelBias& rel, cudaStream_t s);
+// rel.partial: fp32 [B, H, rel_bwd_tiles(..), nseg] sums of dS, written by every tile; a.Dv as for
+// the launches without bias (fp32: written by the first of the two kernels)
+cudaError_t launch_sdpa_rel_bwd_bf16(const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                                     const CUtensorMap& tmV, const CUtensorMap& tmG,
+                                     const CUtensorMap& tmDQ, const SdpaBwdArgs& a,
+                                     const RelBias& rel, const DevCtx& ctx, cudaStream_t s);
+cudaError_t launch_sdpa_rel_bwd_f32(const SdpaBwdArgs& a, const RelBias& rel, cudaStream_t s);
+int rel_bwd_tiles(int Nq, int Nk, int dtype);
+// dtable [num_buckets, H] (the table's type) from those sums
+cudaError_t launch_rel_table_grad(const RelBias& rel, void* dtable, int B, int tiles,
+                                  cudaStream_t s);
+
+struct RelDecodeArgs {
+  int B, H, Nq, Lmax, d_k, d_v;  // Nq <= kDecodeMaxQ
+  int causal;                    // as in DecodeArgs
+  const int32_t* cache_len;      // device, B entries, clamped to [0, Lmax]
+  float scale;
+  const void *Q, *K, *V;
+  void* O;
+  int64_t st[4][4];              // element strides b, h, n, d = 1 of Q, K, V, O
+};
+size_t rel_decode_workspace(int B, int H, int Nq, int Lmax, int d_k, int d_v, int dtype);
+cudaError_t launch_sdpa_rel_decode(const RelDecodeArgs& a, const RelBias& rel, int dtype,
+                                   float* part, cudaStream_t s);
 
 // ---- memory-bound steps of the sublayer backward (bwd_util.cu)
 int bwd_row_chunks(int M);  // chunks of rows the partial column sums use

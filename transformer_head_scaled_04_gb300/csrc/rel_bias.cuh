@@ -1,0 +1,65 @@
+// rel_bias.cuh -- the learned relative position bias of the attention kernels: how a distance
+// d = (key's position) - (query's position) finds its number in the table [num_buckets, H].
+//
+// Buckets are intervals of d: near distances have one each, farther ones share buckets that grow
+// with the logarithm of the distance, and all from max_distance on share the last.  Read in the
+// order of d they are `nseg` segments, segment s holding start[s] <= d < start[s + 1].  The host
+// works the borders out once per call and hands them over as a kernel parameter, so a kernel
+// neither takes logarithms nor reads a map: it copies the borders and its head's bias into shared
+// memory, and a tile of scores whose corner distances fall into one segment (most tiles: beyond
+// max_distance there is one segment on either side) adds a constant, which the exponential's
+// multiply-add takes in for nothing.  Only tiles that a border crosses look distances up.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+
+#include "rel_plan.h"
+
+namespace mha {
+
+// stands in for RelBias in kernels that add no bias
+struct NoRel {};
+template <class Rel>
+struct IsRel {
+  static constexpr bool value = true;
+};
+template <>
+struct IsRel<NoRel> {
+  static constexpr bool value = false;
+};
+
+// A CTA's copy in shared memory: borders (INT_MAX behind the last segment) and bias.
+struct RelShared {
+  int start[kRelMaxSeg + 1];
+  float bias[kRelMaxSeg + 1];
+};
+static_assert(sizeof(RelShared) == 8 * (kRelMaxSeg + 1), "");
+
+// Entry s of the copy, for head h, the bias times `mul` (log2 e where exponentials are powers of
+// two).  A value below -1e30 (a mask's lowest value, -inf) leaves its bucket out: it becomes -inf.
+__device__ __forceinline__ void rel_load(RelShared& sh, const RelBias& r, int h, int s, float mul) {
+  if (s > kRelMaxSeg) return;
+  int at = INT_MAX;
+  float v = 0.f;
+  if (s < r.nseg) {
+    at = r.start[s];
+    const int64_t i = static_cast<int64_t>(r.bucket[s]) * r.H + h;
+    v = r.table_f32 ? __ldg(static_cast<const float*>(r.table) + i)
+                    : __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(r.table) + i));
+    v = v < -1e30f ? -INFINITY : v * mul;
+  }
+  sh.start[s] = at;
+  sh.bias[s] = v;
+}
+
+// The segment of distance d: borders behind the last segment are INT_MAX, start[0] INT_MIN.
+__device__ __forceinline__ int rel_segment(const RelShared& sh, int d) {
+  int s = 0;
+#pragma unroll
+  for (int step = kRelMaxSeg / 2; step > 0; step >>= 1)
+    if (sh.start[s + step] <= d) s += step;
+  return s;
+}
+
+}  // namespace mha

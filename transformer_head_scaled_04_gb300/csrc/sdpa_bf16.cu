@@ -32,12 +32,20 @@
 // causal mask (tile k costs k + 1 key tiles) all heads' heaviest tiles launch first.  Every
 // wait is bounded (see device_common.cuh); a timeout records MHA_ERR_DEVICE_TIMEOUT and the
 // CTA winds down.
+//
+// Instantiated with a RelBias, the kernel adds a learned bias per head and bucket of j - i to the
+// scores (rel_bias.cuh): p = 2^(s c + t - m), t = bias log2(e).  Every warp follows the segment of
+// its tile's smallest distance; a tile within one segment adds a constant inside the exponential's
+// multiply-add, a tile that a border crosses takes t from a table of the warp's 159 distances in
+// shared memory (row r, column q at q + 31 - r: no bank conflicts).  No barrier is added.  Keys past
+// key_len[b] may hold anything there: the rows of V past it are cleared in shared memory.
 #include <cuda_bf16.h>
 
 #include <cmath>
 
 #include "device_common.cuh"
 #include "launchers.h"
+#include "rel_bias.cuh"
 
 namespace mha {
 namespace {
@@ -57,6 +65,12 @@ constexpr int kOffK = kOffQ + kTileBytes;
 constexpr int kOffV = kOffK + kKRing * kTileBytes;
 constexpr int kOffBar = kOffV + kVRing * kTileBytes;
 constexpr int kSmemBytes = 1024 + kOffBar + 256;
+// with a relative bias: the borders and biases, a table of distances for every softmax warp
+constexpr int kOffRel = kOffBar + 256;
+constexpr int kRelTable = 160;  // 128 columns + 31 rows, rounded up
+constexpr int kOffRelTable = kOffRel + static_cast<int>(sizeof(RelShared));
+constexpr int kSmemBytesRel = 1024 + kOffRelTable + 4 * kRelTable * 4;
+static_assert(2 * (kSmemBytesRel + 1024) <= 227 * 1024, "two CTAs per SM");
 // TMEM columns: S [0,128) O [128,192) P [192,256) (P: 128 bf16 per row, two per column)
 constexpr uint32_t kTmemCols = 256;
 constexpr uint32_t kColO = 128;
@@ -102,12 +116,15 @@ __device__ __forceinline__ bool warp_all(bool v) { return __all_sync(0xffffffffu
 // kHeavyFirst (causal masks): the launch order maps to query tiles heaviest first across all
 // heads; the other masks keep the query tiles of a head adjacent.  Two instantiations, because
 // the remapping in the same code slowed unmasked attention ~1% (461 against 457 us in A/B).
-template <bool kHeavyFirst>
+// Rel: NoRel, or a RelBias to add to the scores.
+template <bool kHeavyFirst, class Rel>
 __global__ void __launch_bounds__(kThreads, 2)
     sdpa_fwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ,
                            const __grid_constant__ CUtensorMap tmK,
                            const __grid_constant__ CUtensorMap tmV,
-                           const __grid_constant__ CUtensorMap tmO, const Params p) {
+                           const __grid_constant__ CUtensorMap tmO, const Params p,
+                           const __grid_constant__ Rel rel) {
+  constexpr bool kRel = IsRel<Rel>::value;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -185,6 +202,13 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (warp == 5) {
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
+  }
+  if constexpr (kRel) {
+    if (warp < 4) {
+      pdl_wait();  // the table may be the previous kernel's output
+      for (int s = threadIdx.x; s <= kRelMaxSeg; s += kBQ)
+        rel_load(*reinterpret_cast<RelShared*>(smem + kOffRel), rel, h, s, 1.4426950408889634f);
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -279,7 +303,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint32_t tO = tmem + kColO + lane_off;
     const uint32_t tP = tmem + kColP + lane_off;
     const float c = p.scale_log2;
-    const float2 c2 = make_float2(c, c);
     // allowed keys of this row: first <= key <= limit; both grow with the row, so the warp's
     // smallest limit is its first row's and its largest first key its last row's
     const int limit = (p.mask == 1)             ? row
@@ -294,7 +317,37 @@ __global__ void __launch_bounds__(kThreads, 2)
     bool ok = true;
     float m_used = -INFINITY;
     float l = 0.f;
+    // relative bias: the segment of the warp's smallest distance in the tile, where the next one
+    // begins, this segment's bias; `unseen`: no key of this row has had a weight so far
+    [[maybe_unused]] const RelShared& rs = *reinterpret_cast<const RelShared*>(smem + kOffRel);
+    [[maybe_unused]] float* table =
+        reinterpret_cast<float*>(smem + kOffRelTable) + quarter * kRelTable;
+    [[maybe_unused]] int seg = 0, seg_next = INT_MIN;
+    [[maybe_unused]] float seg_bias = 0.f;
+    [[maybe_unused]] bool unseen = true;
     for (int j = 0; j < nt; ++j) {
+      // Rel: the scores become s mul + add - m_used (powers of two), mul and add the same for all
+      [[maybe_unused]] bool near = false;
+      [[maybe_unused]] float mul = c, add = 0.f;
+      if constexpr (kRel) {
+        const int d0 = (kt0 + j) * kBKV - (wr0 + 31);  // the warp's smallest distance
+        if (d0 >= seg_next) {
+          seg = rel_segment(rs, d0);
+          seg_next = rs.start[seg + 1];
+          seg_bias = rs.bias[seg];
+        }
+        near = d0 + kBKV + 30 >= seg_next;
+        add = seg_bias;
+        if (near) {
+          __syncwarp();  // the previous tile's reads of the table are done
+#pragma unroll
+          for (int e = 0; e < kRelTable / 32; ++e)
+            table[lane + 32 * e] = rs.bias[rel_segment(rs, d0 + lane + 32 * e)];
+          __syncwarp();
+          mul = 1.f;
+          add = 0.f;
+        }
+      }
       if (!warp_all(mbar_wait(bar(kBarSFull), j & 1, p.timeout_ns))) {
         record_error(p.status, kErrTimeout, kSiteSoftmaxS);
         ok = false;
@@ -324,6 +377,13 @@ __global__ void __launch_bounds__(kThreads, 2)
           sv[32 + q] = __uint_as_float(r1[q]);
           sv[64 + q] = __uint_as_float(r2[q]);
           sv[96 + q] = __uint_as_float(r3[q]);
+        }
+        if constexpr (kRel) {
+          if (near) {
+            const float* t = table + 31 - lane;
+#pragma unroll
+            for (int q = 0; q < 128; ++q) sv[q] = fmaf(sv[q], c, t[q]);
+          }
         }
         // excluded keys get -inf (p = 0): one compare against a per-row bound per key,
         // one-sided where no row of the warp has the other end inside the tile
@@ -355,7 +415,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       uint32_t pk[64];
       float tile_sum;
       auto exp_tile = [&]() {
-        const float2 n2 = make_float2(-m_used * c, -m_used * c);
+        const float n1 = kRel ? add - m_used : -m_used * c;
+        const float2 n2 = make_float2(n1, n1);
+        const float2 c2 = kRel ? make_float2(mul, mul) : make_float2(c, c);
         float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
 #pragma unroll
         for (int q = 0; q < 64; ++q) {
@@ -375,7 +437,17 @@ __global__ void __launch_bounds__(kThreads, 2)
       // m_used only guards the exponentials against overflow (p and l share it, O / l is
       // taken at the end): the exact max of the first key tile, reused by later tiles, and a
       // tile whose row sum leaves [0, 2^64] is redone with the true max
-      if (j == 0) {
+      if constexpr (kRel) {  // a row whose first keys have no weight (bias -inf) waits for its max
+        if (__any_sync(0xffffffffu, unseen)) {
+          const float mt = fmaf(row_max(), mul, add);
+          if (unseen && mt != -INFINITY) {
+            m_used = mt;
+            unseen = false;
+          } else if (unseen) {
+            m_used = 0.f;
+          }
+        }
+      } else if (j == 0) {
         const float mt = row_max();
         m_used = (mt == -INFINITY) ? 0.f : mt;
       }
@@ -385,10 +457,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       const bool redo = j > 0 && !(tile_sum <= 1.8446744e19f);  // 2^64
       if (__any_sync(0xffffffffu, redo)) {  // rare; S(j) is still in TMEM
         load_s();
-        const float m_new = fmaxf(m_used, row_max());
+        const float m_new = fmaxf(m_used, kRel ? fmaf(row_max(), mul, add) : row_max());
         if (m_new > m_used) {
           grow = true;
-          alpha = ex2_approx((m_used - m_new) * c);
+          alpha = ex2_approx(kRel ? m_used - m_new : (m_used - m_new) * c);
           l *= alpha;
           m_used = m_new;
         }
@@ -428,6 +500,25 @@ __global__ void __launch_bounds__(kThreads, 2)
         tmem_st32(tP + 32, hi32);
       }
       l += tile_sum;
+      if constexpr (kRel) {
+        // rows of V past key_len may hold anything, and 0 times that may not be 0
+        if (p.mask == 2 && j == nt - 1 && (kt0 + j + 1) * kBKV > L) {
+          if (!warp_all(mbar_wait(bar(kBarVFull + j % kVRing), (j / kVRing) & 1, p.timeout_ns))) {
+            tmem_wait_st();
+            record_error(p.status, kErrTimeout, kSiteSoftmaxO);
+            ok = false;
+            break;
+          }
+          const int r = quarter * 32 + lane;
+          if (col0 + r >= L) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              st_shared_v4(sV + (j % kVRing) * kTileBytes + r * 128 + u * 16,
+                           make_uint4(0u, 0u, 0u, 0u));
+          }
+          fence_proxy_async_smem();
+        }
+      }
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(bar(kBarPFull));
@@ -437,7 +528,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int64_t lse_i = (static_cast<int64_t>(b) * p.H + h) * p.Nq + row;
     if (p.lse != nullptr && row < p.Nq &&
         bounds_ok(lse_i, static_cast<int64_t>(p.B) * p.H * p.Nq, p.status, kSiteLse))
-      p.lse[lse_i] = (ok && l > 0.f) ? (m_used * c + log2f(l)) * 0.6931471805599453f : INFINITY;
+      p.lse[lse_i] = (ok && l > 0.f) ? ((kRel ? m_used : m_used * c) + log2f(l)) *
+                                           0.6931471805599453f
+                                     : INFINITY;
     if (nt > 0) {
       float o[64];
 #pragma unroll
@@ -505,9 +598,12 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 }  // namespace
 
-cudaError_t launch_sdpa_bf16(const CUtensorMap& tmQ, const CUtensorMap& tmK,
-                             const CUtensorMap& tmV, const CUtensorMap& tmO, const SdpaArgs& a,
-                             const DevCtx& ctx, cudaStream_t s) {
+namespace {
+template <class Rel>
+cudaError_t launch(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                   const CUtensorMap& tmO, const SdpaArgs& a, const Rel& rel, const DevCtx& ctx,
+                   cudaStream_t s) {
+  constexpr int kSmem = IsRel<Rel>::value ? kSmemBytesRel : kSmemBytes;
   Params p;
   p.B = a.B;
   p.H = a.H;
@@ -524,17 +620,27 @@ cudaError_t launch_sdpa_bf16(const CUtensorMap& tmQ, const CUtensorMap& tmK,
   p.so_n = a.so[2];
   p.status = ctx.status;
   p.timeout_ns = ctx.timeout_ns;
-  const bool heavy_first = a.mask == 1;
-  const void* fn = heavy_first ? reinterpret_cast<const void*>(sdpa_fwd_bf16_kernel<true>)
-                               : reinterpret_cast<const void*>(sdpa_fwd_bf16_kernel<false>);
-  cudaError_t e = prepare_kernel(fn, kSmemBytes, nullptr);
-  if (e != cudaSuccess) return e;
-  dim3 grid((a.Nq + kBQ - 1) / kBQ, a.H, a.B);
-  if (heavy_first)
-    return launch_pdl(sdpa_fwd_bf16_kernel<true>, grid, dim3(kThreads), kSmemBytes, s, tmQ, tmK,
-                      tmV, tmO, p);
-  return launch_pdl(sdpa_fwd_bf16_kernel<false>, grid, dim3(kThreads), kSmemBytes, s, tmQ, tmK,
-                    tmV, tmO, p);
+  const dim3 grid((a.Nq + kBQ - 1) / kBQ, a.H, a.B);
+  auto go = [&](auto kernel) {
+    cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(kernel), kSmem, nullptr);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kernel, grid, dim3(kThreads), kSmem, s, tmQ, tmK, tmV, tmO, p, rel);
+  };
+  return a.mask == 1 ? go(sdpa_fwd_bf16_kernel<true, Rel>) : go(sdpa_fwd_bf16_kernel<false, Rel>);
+}
+}  // namespace
+
+cudaError_t launch_sdpa_bf16(const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                             const CUtensorMap& tmV, const CUtensorMap& tmO, const SdpaArgs& a,
+                             const DevCtx& ctx, cudaStream_t s) {
+  return launch(tmQ, tmK, tmV, tmO, a, NoRel{}, ctx, s);
+}
+
+cudaError_t launch_sdpa_rel_bf16(const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                                 const CUtensorMap& tmV, const CUtensorMap& tmO,
+                                 const SdpaArgs& a, const RelBias& rel, const DevCtx& ctx,
+                                 cudaStream_t s) {
+  return launch(tmQ, tmK, tmV, tmO, a, rel, ctx, s);
 }
 
 }  // namespace mha

@@ -32,6 +32,17 @@
 // in-flight copies and MMAs land, frees TMEM.
 // Masks: none, causal (j <= i) and key padding (j < key_len[b]); fully masked tiles are
 // skipped, and the d = 64 heads of the forward kernel are assumed.
+//
+// Instantiated with a RelBias (rel_bias.cuh) both kernels rebuild P with the learned bias of the
+// distance j - i, p = 2^(c s' + t), and the dkdv kernel also sums dS per segment of distances, the
+// gradient of the bias.  A warp's 32 keys x 64 queries that lie within one segment take t as a
+// constant and add their dS up in two registers, one addition per pair of elements; where a border
+// crosses them t comes from a table of the warp's 95 distances and dS is summed along the
+// diagonals: the running sum of a diagonal moves to the next lane with every column (one shuffle and
+// one addition per column, four column blocks side by side), and a segmented scan over the diagonals
+// gives the segments' sums.  Lane s % 32 owns segment s; the CTA writes one sum per segment, and a
+// last launch adds those of a head in a fixed order, so the gradient is bitwise reproducible.  Keys
+// past key_len[b] may hold anything there: their dS is set to 0, their rows of K cleared.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -39,6 +50,7 @@
 
 #include "device_common.cuh"
 #include "launchers.h"
+#include "rel_bias.cuh"
 
 namespace mha {
 namespace {
@@ -105,10 +117,12 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* dst, const uint32_t* r0
 // dS of one 64-key half of a query row: p = 2^(s*c - lse2) (0 past the row's last key when
 // kMask), dS = p * (dP - D), packed to bf16 pairs; nl = -lse2 and nd = -D, two keys per paired
 // fp32 instruction
-template <bool kMask>
+// kTable: the relative bias of the half's columns is added from tab[0..63]
+template <bool kMask, bool kTable = false>
 __device__ __forceinline__ void dq_half(const uint32_t* s0, const uint32_t* s1,
                                         const uint32_t* g0, const uint32_t* g1, int col0,
-                                        int limit, float c, float nl, float nd, uint32_t* ds) {
+                                        int limit, float c, float nl, float nd, uint32_t* ds,
+                                        const float* tab = nullptr) {
   const float2 c2 = make_float2(c, c), nl2 = make_float2(nl, nl), nd2 = make_float2(nd, nd);
 #pragma unroll
   for (int i = 0; i < 32; ++i) {
@@ -117,6 +131,7 @@ __device__ __forceinline__ void dq_half(const uint32_t* s0, const uint32_t* s1,
     const float2 gv = make_float2(__uint_as_float(i < 16 ? g0[2 * i] : g1[2 * i - 32]),
                                   __uint_as_float(i < 16 ? g0[2 * i + 1] : g1[2 * i + 1 - 32]));
     float2 pv = ffma2(sv, c2, nl2);
+    if (kTable) pv = fadd2(pv, make_float2(tab[2 * i], tab[2 * i + 1]));
     pv.x = ex2_approx(pv.x);
     pv.y = ex2_approx(pv.y);
     if (kMask) {
@@ -125,6 +140,22 @@ __device__ __forceinline__ void dq_half(const uint32_t* s0, const uint32_t* s1,
     }
     const float2 dv = fmul2(pv, fadd2(gv, nd2));
     ds[i] = pack_bf16x2(dv.x, dv.y);
+  }
+}
+
+// dq_half with a relative bias: masked keys may hold anything, so their dS is set to 0
+template <bool kMask, bool kTable>
+__device__ __forceinline__ void dq_half_rel(const uint32_t* s0, const uint32_t* s1,
+                                            const uint32_t* g0, const uint32_t* g1, int col0,
+                                            int limit, float c, float nl, float nd, uint32_t* ds,
+                                            const float* tab) {
+  dq_half<kMask, kTable>(s0, s1, g0, g1, col0, limit, c, nl, nd, ds, tab);
+  if (kMask) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      if (col0 + 2 * i > limit) ds[i] &= 0xffff0000u;
+      if (col0 + 2 * i + 1 > limit) ds[i] &= 0x0000ffffu;
+    }
   }
 }
 
@@ -158,6 +189,133 @@ __device__ __forceinline__ void dkdv_half(const uint32_t* s0, const uint32_t* s1
   }
 }
 
+// dkdv_half with a relative bias: p = 2^(c s' + t), t the constant `add`, or (kTable) tab[-ca]
+// for query column ca0 + ca.  far gets the sums of dS (even and odd columns); with kTable dS stays
+// in the registers of g0 and g1 instead, as floats.  Masked pairs may hold anything (rows of K and
+// V past key_len), so their dS is set to 0.
+template <bool kMask, bool kTable>
+__device__ __forceinline__ void dkdv_half_rel(const uint32_t* s0, const uint32_t* s1, uint32_t* g0,
+                                              uint32_t* g1, int ca0, bool row_ok, int first_ok,
+                                              float c, float add, const float* tab, float2& far,
+                                              uint32_t* pp, uint32_t* ds) {
+  const float2 c2 = make_float2(c, c), add2 = make_float2(add, add);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const int ca = ca0 + 2 * i;  // query column within the tile
+    const float2 sv = make_float2(__uint_as_float(i < 16 ? s0[2 * i] : s1[2 * i - 32]),
+                                  __uint_as_float(i < 16 ? s0[2 * i + 1] : s1[2 * i + 1 - 32]));
+    uint32_t& gx = i < 16 ? g0[2 * i] : g1[2 * i - 32];
+    uint32_t& gy = i < 16 ? g0[2 * i + 1] : g1[2 * i + 1 - 32];
+    const float2 gv = make_float2(__uint_as_float(gx), __uint_as_float(gy));
+    float2 pv = ffma2(sv, c2, kTable ? make_float2(tab[-2 * i], tab[-2 * i - 1]) : add2);
+    pv.x = ex2_approx(pv.x);
+    pv.y = ex2_approx(pv.y);
+    float2 dv = fmul2(pv, gv);
+    if (kMask) {
+      if (!row_ok || ca < first_ok) pv.x = dv.x = 0.f;
+      if (!row_ok || ca + 1 < first_ok) pv.y = dv.y = 0.f;
+    }
+    pp[i] = pack_bf16x2(pv.x, pv.y);
+    ds[i] = pack_bf16x2(dv.x, dv.y);
+    if (kTable) {
+      gx = __float_as_uint(dv.x);
+      gy = __float_as_uint(dv.y);
+    } else {
+      far = fadd2(far, dv);
+    }
+  }
+}
+
+// The sums of a warp's 32 x 64 dS over the diagonals e = lane + 63 - ca (0..94), in buf[0..94]
+// (96 floats of the warp; column ca's values in g0, then g1).  Sixteen columns at a time: a
+// diagonal's running sum passes from lane to lane, lane 31's is complete and added to buf.
+__device__ __forceinline__ void diagonal_sums(const uint32_t* g0, const uint32_t* g1, int lane,
+                                              float* buf) {
+#pragma unroll
+  for (int u = 0; u < 3; ++u) buf[lane + 32 * u] = 0.f;
+  __syncwarp();
+  float acc[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) acc[k] = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int ca = 16 * k + i;
+      if (i > 0) {
+        const float up = __shfl_up_sync(0xffffffffu, acc[k], 1);
+        if (lane == 31) buf[95 - ca] += acc[k];  // column ca - 1, lane 31
+        acc[k] = lane == 0 ? 0.f : up;
+      }
+      acc[k] += __uint_as_float(ca < 32 ? g0[ca] : g1[ca - 32]);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    __syncwarp();
+    buf[lane + 48 - 16 * k] += acc[k];
+  }
+  __syncwarp();
+}
+
+// Adds the sums over the segments (distance d0 + e for diagonal e) to their owners: running sums of
+// buf[0..94] that start anew at every segment's first diagonal (three diagonals to a lane, lanes
+// joined by a segmented scan), of which a segment's last one is its sum.  No differences are taken,
+// so a bucket without pairs keeps an exact 0.
+__device__ __forceinline__ void segment_sums(const RelShared& rs, int nseg, int d0, int lane,
+                                             float* buf, float (&own)[kRelMaxSeg / 32]) {
+  uint32_t first[3] = {0u, 0u, 0u};  // bit e: diagonal e begins a segment
+#pragma unroll
+  for (int k = 0; k < kRelMaxSeg / 32; ++k) {
+    const int s = lane + 32 * k, at = s < nseg ? rs.start[s] : INT_MIN;
+    if (at > d0 && at <= d0 + 94) {
+      const uint32_t bit = 1u << ((at - d0) & 31);
+      const int w = (at - d0) >> 5;
+      first[0] |= w == 0 ? bit : 0u;
+      first[1] |= w == 1 ? bit : 0u;
+      first[2] |= w == 2 ? bit : 0u;
+    }
+  }
+  bool h[3];
+  float v[3];
+#pragma unroll
+  for (int i = 0; i < 3; ++i) first[i] = __reduce_or_sync(0xffffffffu, first[i]);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const int e = 3 * lane + i;
+    const uint32_t word = e < 32 ? first[0] : e < 64 ? first[1] : first[2];
+    h[i] = (word >> (e & 31)) & 1u;
+    v[i] = buf[e];
+  }
+  float sum = h[1] ? v[1] : v[0] + v[1];  // since the lane's last beginning
+  sum = h[2] ? v[2] : sum + v[2];
+  bool begins = h[0] || h[1] || h[2];
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const float up = __shfl_up_sync(0xffffffffu, sum, off);
+    const bool b = __shfl_up_sync(0xffffffffu, begins ? 1 : 0, off) != 0;
+    if (lane >= off) {
+      if (!begins) sum += up;
+      begins = begins || b;
+    }
+  }
+  float carry = __shfl_up_sync(0xffffffffu, sum, 1);
+  if (lane == 0) carry = 0.f;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    carry = h[i] ? v[i] : carry + v[i];
+    buf[3 * lane + i] = carry;
+  }
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < kRelMaxSeg / 32; ++k) {
+    const int s = lane + 32 * k;
+    if (s < nseg && rs.start[s] <= d0 + 94 && rs.start[s + 1] > d0)
+      own[k] += buf[rs.start[s + 1] > d0 + 94 ? 94 : rs.start[s + 1] - 1 - d0];
+  }
+  __syncwarp();
+}
+
 // store 32 fp32 values (times mul) of half a row as bf16
 __device__ __forceinline__ void store_half_row(__nv_bfloat16* dst, const uint32_t* r,
                                                float mul) {
@@ -182,6 +340,11 @@ constexpr int kQOffK = kQOffG + kTileBytes;
 constexpr int kQOffV = kQOffK + kStages * kTileBytes;
 constexpr int kQOffBar = kQOffV + kStages * kTileBytes;
 constexpr int kQSmem = 1024 + kQOffBar + 256;
+// with a relative bias: borders and biases, a table of 95 distances per math warp
+constexpr int kRelTable = 96;
+constexpr int kQOffRel = kQOffBar + 256;
+constexpr int kQOffTable = kQOffRel + static_cast<int>(sizeof(RelShared));
+constexpr int kQSmemRel = 1024 + kQOffTable + kMathWarps * kRelTable * 4;
 // TMEM: S [0,128) dP [128,256) dS of even tiles (bf16 pairs) [256,320) dQ [320,384) dS of
 // odd tiles [384,448): the math warps write dS(j+1) while dQ += dS(j) K_j still reads dS(j)
 constexpr uint32_t kQColS = 0, kQColP = 128, kQColDQ = 320;
@@ -197,11 +360,14 @@ constexpr int kQBarDQDone = kQBarDSFull + 2; // [2] dQ MMA done with that dS buf
 constexpr int kQBarDrain = kQBarDQDone + 2;
 constexpr int kQNumBars = kQBarDrain + 1;
 
+template <class Rel>
 __global__ void __launch_bounds__(kQThreads, 1)
     sdpa_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ,
                        const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV,
-                       const __grid_constant__ CUtensorMap tmG, const BwdParams p) {
+                       const __grid_constant__ CUtensorMap tmG, const BwdParams p,
+                       const __grid_constant__ Rel rel) {
+  constexpr bool kRel = IsRel<Rel>::value;
   pdl_launch_dependents();
   pdl_wait();  // the previous kernel's output is complete from here on
   extern __shared__ uint8_t smem_raw[];
@@ -231,6 +397,10 @@ __global__ void __launch_bounds__(kQThreads, 1)
     }
     mbar_init(bar(kQBarDrain), 2);
     fence_mbar_init();
+  }
+  if constexpr (kRel) {
+    if (threadIdx.x <= kRelMaxSeg)
+      rel_load(*reinterpret_cast<RelShared*>(smem + kQOffRel), rel, h, threadIdx.x, kLog2e);
   }
   if (warp == kWarpMma) {
     tmem_alloc(smem_u32(tmem_slot), 512);
@@ -342,8 +512,31 @@ __global__ void __launch_bounds__(kQThreads, 1)
     const float nd = __ldg(tile_st + kT + r_local);  // -D
     const float c = p.scale * kLog2e;
     const int limit = (p.mask == 1) ? min(row, L - 1) : L - 1;  // keys j <= limit
+    [[maybe_unused]] const RelShared& rs = *reinterpret_cast<const RelShared*>(smem + kQOffRel);
+    [[maybe_unused]] float* table =
+        reinterpret_cast<float*>(smem + kQOffTable) + warp * kRelTable;
+    [[maybe_unused]] int seg_next = INT_MIN;
+    [[maybe_unused]] float seg_bias = 0.f;
     bool ok = true;
     for (int j = 0; j < nk; ++j) {
+      [[maybe_unused]] bool near = false;
+      if constexpr (kRel) {
+        // the half's distances are d0 + e, e = column + 31 - lane in 0..94
+        const int d0 = j * kT + half * 64 - (q0 + quarter * 32 + 31);
+        if (d0 >= seg_next) {
+          const int seg = rel_segment(rs, d0);
+          seg_next = rs.start[seg + 1];
+          seg_bias = rs.bias[seg];
+        }
+        near = d0 + 94 >= seg_next;
+        if (near) {
+          __syncwarp();  // the previous tile's reads of the table are done
+#pragma unroll
+          for (int e = 0; e < kRelTable / 32; ++e)
+            table[lane + 32 * e] = rs.bias[rel_segment(rs, d0 + lane + 32 * e)];
+          __syncwarp();
+        }
+      }
       if (!warp_all(mbar_wait(bar(kQBarSFull), j & 1, p.timeout_ns))) {
         record_error(p.status, kErrTimeout, kSiteBwdMath);
         ok = false;
@@ -366,7 +559,26 @@ __global__ void __launch_bounds__(kQThreads, 1)
       if (lane == 0) mbar_arrive(bar(kQBarSFree));
       const int col0 = j * kT + half * 64;
       uint32_t ds[32];
-      if (warp_all(col0 + 63 <= limit))  // no key of this half is masked for any row here
+      if constexpr (kRel) {
+        const bool open = warp_all(col0 + 63 <= limit);
+        const float* tab = table + 31 - lane;
+        if (near && open)
+          dq_half_rel<false, true>(s0, s1, g0, g1, col0, limit, c, nl, nd, ds, tab);
+        else if (near)
+          dq_half_rel<true, true>(s0, s1, g0, g1, col0, limit, c, nl, nd, ds, tab);
+        else if (open)
+          dq_half_rel<false, false>(s0, s1, g0, g1, col0, limit, c, nl + seg_bias, nd, ds, tab);
+        else
+          dq_half_rel<true, false>(s0, s1, g0, g1, col0, limit, c, nl + seg_bias, nd, ds, tab);
+        // rows of K past key_len may hold anything: cleared before dQ reads them
+        if (p.mask == 2 && j == nk - 1 && j * kT + r_local >= L) {
+          const uint32_t k_row = smem_u32(smem + kQOffK + (j % kStages) * kTileBytes) +
+                                 r_local * 128 + half * 64;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) st_shared_v4(k_row + u * 16, make_uint4(0u, 0u, 0u, 0u));
+          fence_proxy_async_smem();
+        }
+      } else if (warp_all(col0 + 63 <= limit))  // no key of this half is masked for any row here
         dq_half<false>(s0, s1, g0, g1, col0, limit, c, nl, nd, ds);
       else
         dq_half<true>(s0, s1, g0, g1, col0, limit, c, nl, nd, ds);
@@ -431,9 +643,17 @@ constexpr int kStageBytes = 32 * 32 * 4;
 __host__ __device__ constexpr int k_off_bar(bool fused) {
   return fused ? kKOffStage + kMathWarps * kStageBytes : kKOffDS;
 }
-__host__ __device__ constexpr int k_smem(bool fused) { return 1024 + k_off_bar(fused) + 256; }
+// with a relative bias: borders and biases, then 128 floats per math warp (the table of 95
+// distances, later the diagonals' sums, at the end the warp's sums of segments)
+__host__ __device__ constexpr int k_off_rel(bool fused) { return k_off_bar(fused) + 256; }
+__host__ __device__ constexpr int k_off_table(bool fused) {
+  return k_off_rel(fused) + static_cast<int>(sizeof(RelShared));
+}
+__host__ __device__ constexpr int k_smem(bool fused, bool rel = false) {
+  return 1024 + (rel ? k_off_table(fused) + kMathWarps * kRelMaxSeg * 4 : k_off_bar(fused) + 256);
+}
 static_assert(kKOffDS % 1024 == 0 && kKOffStage % 1024 == 0, "swizzled buffers need 1 KB alignment");
-static_assert(k_smem(true) <= 227 * 1024, "fused dkdv shared memory");
+static_assert(k_smem(true, true) <= 227 * 1024, "fused dkdv shared memory");
 // TMEM: S^T [0,128) dP^T [128,256) P^T [256,320) dS^T (fused: dQ of one query tile) [320,384)
 // dV [384,448) dK [448,512)
 constexpr uint32_t kKColS = 0, kKColP = 128, kKColPT = 256, kKColDS = 320, kKColDQ = 320,
@@ -459,13 +679,15 @@ __device__ __forceinline__ void st_row_sw128(uint32_t row_addr, int lane, const 
                  make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]));
 }
 
-template <bool kFused>
+template <bool kFused, class Rel>
 __global__ void __launch_bounds__(kKThreads, 1)
     sdpa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ,
                          const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV,
                          const __grid_constant__ CUtensorMap tmG,
-                         const __grid_constant__ CUtensorMap tmDQ, const BwdParams p) {
+                         const __grid_constant__ CUtensorMap tmDQ, const BwdParams p,
+                         const __grid_constant__ Rel rel) {
+  constexpr bool kRel = IsRel<Rel>::value;
   pdl_launch_dependents();
   pdl_wait();  // the previous kernel's output is complete from here on
   extern __shared__ uint8_t smem_raw[];
@@ -504,6 +726,11 @@ __global__ void __launch_bounds__(kKThreads, 1)
     st_shared_v4(row, make_uint4(0x3F803F80u, 0x00003F80u, 0u, 0u));
     st_shared_v4(row + kT * 16, make_uint4(0u, 0u, 0u, 0u));
     fence_proxy_async_smem();
+  }
+  if constexpr (kRel) {
+    if (threadIdx.x <= kRelMaxSeg)
+      rel_load(*reinterpret_cast<RelShared*>(smem + k_off_rel(kFused)), rel, h, threadIdx.x,
+               kLog2e);
   }
   if (warp == kWarpMma) {
     tmem_alloc(smem_u32(tmem_slot), 512);
@@ -665,9 +892,46 @@ __global__ void __launch_bounds__(kKThreads, 1)
         bulk_commit_group();
       }
     };
+    // relative bias: the segment of the half's largest distance, its first distance and its bias;
+    // dS summed within it (far) and what this lane's segments have so far
+    [[maybe_unused]] const RelShared& rs =
+        *reinterpret_cast<const RelShared*>(smem + k_off_rel(kFused));
+    [[maybe_unused]] float* buf =
+        reinterpret_cast<float*>(smem + k_off_table(kFused)) + warp * kRelMaxSeg;
+    [[maybe_unused]] int seg = 0, seg_start = INT_MAX;
+    [[maybe_unused]] float seg_bias = 0.f;
+    [[maybe_unused]] float2 far = make_float2(0.f, 0.f);
+    [[maybe_unused]] float own[kRelMaxSeg / 32] = {};
+    [[maybe_unused]] auto flush_far = [&]() {
+      float v = far.x + far.y;
+      far = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+#pragma unroll
+      for (int k = 0; k < kRelMaxSeg / 32; ++k)
+        if (lane + 32 * k == seg) own[k] += v;
+    };
     bool ok = true;
     for (int t = 0; t < ni; ++t) {
       const int q0 = (i0 + t) * kT;
+      [[maybe_unused]] const int d0 = k0 + quarter * 32 - (q0 + half * 64 + 63);
+      [[maybe_unused]] bool near = false;
+      if constexpr (kRel) {
+        // the half's distances are d0 + e, e = lane + 63 - column in 0..94; d0 falls with t
+        if (d0 + 94 < seg_start || (t & 15) == 0) {
+          if (t > 0) flush_far();  // also every 16 tiles, which bounds the length of a sum
+          seg = rel_segment(rs, d0 + 94);
+          seg_start = rs.start[seg];
+          seg_bias = rs.bias[seg];
+        }
+        near = d0 < seg_start;
+        if (near) {
+#pragma unroll
+          for (int e = 0; e < 3; ++e)
+            buf[lane + 32 * e] = rs.bias[rel_segment(rs, d0 + lane + 32 * e)];
+          __syncwarp();
+        }
+      }
       if (!warp_all(mbar_wait(bar(kKBarSFull), t & 1, p.timeout_ns))) {
         record_error(p.status, kErrTimeout, kSiteBwdMath);
         ok = false;
@@ -691,7 +955,29 @@ __global__ void __launch_bounds__(kKThreads, 1)
       // key j = key is seen by query q0 + ca when j < L and, for the causal mask, j <= q
       const bool row_ok = key < L;
       const int first_ok = (p.mask == 1) ? key - q0 : -kT;
-      if (warp_all(row_ok && first_ok <= half * 64))  // every pair of this half is allowed
+      if constexpr (kRel) {
+        const bool open = warp_all(row_ok && first_ok <= half * 64);
+        const float* tab = buf + 63 + lane;
+        if (near && open)
+          dkdv_half_rel<false, true>(s0, s1, g0, g1, half * 64, row_ok, first_ok, c, 0.f, tab, far,
+                                     pp, ds);
+        else if (near)
+          dkdv_half_rel<true, true>(s0, s1, g0, g1, half * 64, row_ok, first_ok, c, 0.f, tab, far,
+                                    pp, ds);
+        else if (open)
+          dkdv_half_rel<false, false>(s0, s1, g0, g1, half * 64, row_ok, first_ok, c, seg_bias, tab,
+                                      far, pp, ds);
+        else
+          dkdv_half_rel<true, false>(s0, s1, g0, g1, half * 64, row_ok, first_ok, c, seg_bias, tab,
+                                     far, pp, ds);
+        if (kFused && t == 0 && !row_ok) {
+          // rows of K past key_len may hold anything: cleared before the first dQ reads them (the
+          // product S^T of the next tile may see either, it only fills masked rows)
+          const uint32_t k_row = smem_u32(smem + kKOffK) + r_local * 128 + half * 64;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) st_shared_v4(k_row + u * 16, make_uint4(0u, 0u, 0u, 0u));
+        }
+      } else if (warp_all(row_ok && first_ok <= half * 64))  // every pair of this half is allowed
         dkdv_half<false>(s0, s1, g0, g1, half * 64, row_ok, first_ok, c, pp, ds);
       else
         dkdv_half<true>(s0, s1, g0, g1, half * 64, row_ok, first_ok, c, pp, ds);
@@ -732,6 +1018,17 @@ __global__ void __launch_bounds__(kKThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kKBarPFull));
       }
+      if constexpr (kRel) {
+        if (near) {  // after the products have what they wait for
+          diagonal_sums(g0, g1, lane, buf);
+          segment_sums(rs, rel.nseg, d0, lane, buf, own);
+        }
+      }
+    }
+    if constexpr (kRel) {
+      if (ni > 0) flush_far();
+#pragma unroll
+      for (int k = 0; k < kRelMaxSeg / 32; ++k) buf[lane + 32 * k] = own[k];
     }
     if constexpr (kFused) {
       // the last query tile's dQ box
@@ -782,6 +1079,16 @@ __global__ void __launch_bounds__(kKThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (kRel) {  // the tile's sums of dS per segment
+    const int s = threadIdx.x;
+    if (s < rel.nseg) {
+      const float* w = reinterpret_cast<const float*>(smem + k_off_table(kFused)) + s;
+      float v = w[0];
+#pragma unroll
+      for (int i = 1; i < kMathWarps; ++i) v += w[i * kRelMaxSeg];
+      rel.partial[((static_cast<int64_t>(b) * p.H + h) * gridDim.x + kt) * rel.nseg + s] = v;
+    }
+  }
   if (warp == kWarpMma) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
@@ -815,12 +1122,11 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-}  // namespace
-
-cudaError_t launch_sdpa_bwd_bf16(const CUtensorMap& tmQ, const CUtensorMap& tmK,
-                                 const CUtensorMap& tmV, const CUtensorMap& tmG,
-                                 const CUtensorMap& tmDQ, const SdpaBwdArgs& a,
-                                 const DevCtx& ctx, cudaStream_t s) {
+template <class Rel>
+cudaError_t launch(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                   const CUtensorMap& tmG, const CUtensorMap& tmDQ, const SdpaBwdArgs& a,
+                   const Rel& rel, const DevCtx& ctx, cudaStream_t s) {
+  constexpr bool kRel = IsRel<Rel>::value;
   BwdParams p;
   p.H = a.H;
   p.Nq = a.Nq;
@@ -833,24 +1139,25 @@ cudaError_t launch_sdpa_bwd_bf16(const CUtensorMap& tmQ, const CUtensorMap& tmK,
   p.status = ctx.status;
   p.timeout_ns = ctx.timeout_ns;
   const bool fused = !a.deterministic;
-  const void* kdkdv = fused ? reinterpret_cast<const void*>(sdpa_bwd_dkdv_kernel<true>)
-                            : reinterpret_cast<const void*>(sdpa_bwd_dkdv_kernel<false>);
+  const void* kdkdv = fused ? reinterpret_cast<const void*>(sdpa_bwd_dkdv_kernel<true, Rel>)
+                            : reinterpret_cast<const void*>(sdpa_bwd_dkdv_kernel<false, Rel>);
   int regs = 0;
-  cudaError_t e = prepare_kernel(kdkdv, k_smem(fused), &regs);
+  cudaError_t e = prepare_kernel(kdkdv, k_smem(fused, kRel), &regs);
   if (e != cudaSuccess) return e;
   // the dkdv kernel's setmaxnreg split must fit in what its blocks launch with, or the
   // increase would wait forever: refuse to launch if the compiled register count is too small
   if (regs * kKThreads < kMathWarps * 32 * kKMathRegs + 4 * 32 * kKControlRegs)
     return cudaErrorInvalidConfiguration;
   if (!fused) {
-    e = prepare_kernel(reinterpret_cast<const void*>(sdpa_bwd_dq_kernel), kQSmem, nullptr);
+    constexpr int kSmem = kRel ? kQSmemRel : kQSmem;
+    e = prepare_kernel(reinterpret_cast<const void*>(sdpa_bwd_dq_kernel<Rel>), kSmem, nullptr);
     if (e != cudaSuccess) return e;
     p.out0 = static_cast<__nv_bfloat16*>(a.dQ);
     p.o0_b = a.st[5][0];
     p.o0_h = a.st[5][1];
     p.o0_n = a.st[5][2];
-    (void)launch_pdl(sdpa_bwd_dq_kernel, dim3((a.Nq + kT - 1) / kT, a.H, a.B), dim3(kQThreads),
-                     kQSmem, s, tmQ, tmK, tmV, tmG, p);
+    (void)launch_pdl(sdpa_bwd_dq_kernel<Rel>, dim3((a.Nq + kT - 1) / kT, a.H, a.B),
+                     dim3(kQThreads), kSmem, s, tmQ, tmK, tmV, tmG, p, rel);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
@@ -864,11 +1171,11 @@ cudaError_t launch_sdpa_bwd_bf16(const CUtensorMap& tmQ, const CUtensorMap& tmK,
   p.o1_n = a.st[7][2];
   const dim3 grid((a.Nk + kT - 1) / kT, a.H, a.B);
   if (fused)
-    (void)launch_pdl(sdpa_bwd_dkdv_kernel<true>, grid, dim3(kKThreads), k_smem(true), s, tmQ, tmK,
-                     tmV, tmG, tmDQ, p);
+    (void)launch_pdl(sdpa_bwd_dkdv_kernel<true, Rel>, grid, dim3(kKThreads), k_smem(true, kRel), s,
+                     tmQ, tmK, tmV, tmG, tmDQ, p, rel);
   else
-    (void)launch_pdl(sdpa_bwd_dkdv_kernel<false>, grid, dim3(kKThreads), k_smem(false), s, tmQ,
-                     tmK, tmV, tmG, tmDQ, p);
+    (void)launch_pdl(sdpa_bwd_dkdv_kernel<false, Rel>, grid, dim3(kKThreads), k_smem(false, kRel), s,
+                     tmQ, tmK, tmV, tmG, tmDQ, p, rel);
   e = cudaGetLastError();
   if (e != cudaSuccess || !fused) return e;
   const int rows = (a.Nq + kT - 1) / kT * kT;
@@ -881,6 +1188,22 @@ cudaError_t launch_sdpa_bwd_bf16(const CUtensorMap& tmQ, const CUtensorMap& tmK,
                    static_cast<__nv_bfloat16*>(a.dQ), a.H, a.Nq, rows, a.st[5][0], a.st[5][1],
                    a.st[5][2], a.scale, total);
   return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_sdpa_bwd_bf16(const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                                 const CUtensorMap& tmV, const CUtensorMap& tmG,
+                                 const CUtensorMap& tmDQ, const SdpaBwdArgs& a,
+                                 const DevCtx& ctx, cudaStream_t s) {
+  return launch(tmQ, tmK, tmV, tmG, tmDQ, a, NoRel{}, ctx, s);
+}
+
+cudaError_t launch_sdpa_rel_bwd_bf16(const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                                     const CUtensorMap& tmV, const CUtensorMap& tmG,
+                                     const CUtensorMap& tmDQ, const SdpaBwdArgs& a,
+                                     const RelBias& rel, const DevCtx& ctx, cudaStream_t s) {
+  return launch(tmQ, tmK, tmV, tmG, tmDQ, a, rel, ctx, s);
 }
 
 }  // namespace mha
