@@ -322,8 +322,9 @@ int mha_kv_evict_q8(int B, int H, int Lmax, int Lmax_out, int d_k, int d_v, int 
  *              n < e: bucket n;  else min(per - 1, e + floor((per - e) log(n / e) /
  *                                                        log(max_distance / e)))
  *            in exact arithmetic (a distance on a border belongs to the farther bucket);
- *            max_distance > e, from which on all distances share a side's last bucket.
+ *            max_distance > e (and < 2^24), from which on all distances share a side's last bucket.
  *   lengths  up to 2^24 positions.
+ *   scale    as for mha_sdpa_fwd, within [2^-64, 2^64] where it is given.
  *   d_k, d_v bf16: 64.  fp32: 1..128, computed on the tensor cores with every value split into two
  *            tf32 terms (relative error 2^-22 per factor; sums in fp32).
  * Keys past key_len[b] (cache_len[b]) may hold anything, infinities and NaN included.

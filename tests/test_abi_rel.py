@@ -38,7 +38,7 @@ def strides(n, **changed):
 
 BIAS = [
     (dict(bias=None), INVALID), (dict(bt=2), INVALID), (dict(nb=1), INVALID),
-    (dict(nb=129), UNSUPPORTED), (dict(both=2), INVALID), (dict(both=-1), INVALID),
+    (dict(nb=129), UNSUPPORTED), (dict(reach=1 << 24), UNSUPPORTED), (dict(both=2), INVALID), (dict(both=-1), INVALID),
     (dict(nb=33), INVALID), (dict(nb=2), INVALID),           # both sides: even, 4 at least
     (dict(reach=8), INVALID), (dict(reach=0), INVALID), (dict(reach=-5), INVALID),
     (dict(nb=33, both=0, reach=16), INVALID),
@@ -48,6 +48,7 @@ SIZES = [
     (dict(Bn=0), INVALID), (dict(H=0), INVALID), (dict(Nq=0), INVALID), (dict(dk=0), INVALID),
     (dict(dt=2), INVALID), (dict(scale=float("nan")), INVALID),
     (dict(scale=float("inf")), INVALID), (dict(Bn=65536), UNSUPPORTED),
+    (dict(scale=1e-20), UNSUPPORTED), (dict(scale=1e20), UNSUPPORTED),
     (dict(H=65536), UNSUPPORTED), (dict(dk=32), UNSUPPORTED), (dict(dv=128), UNSUPPORTED),
     (dict(dt=F32, dk=129), UNSUPPORTED), (dict(dt=F32, dv=129), UNSUPPORTED),
     (dict(q=None), INVALID), (dict(k=None), INVALID), (dict(v=None), INVALID),

@@ -28,7 +28,7 @@ int take_bias(const void* bias, int bias_dtype, int H, int num_buckets, int max_
               int bidirectional, mha::RelBias* r) {
   if (bias == nullptr || !valid_dtype(bias_dtype) || (bidirectional != 0 && bidirectional != 1))
     return MHA_ERR_INVALID;
-  if (num_buckets > mha::kRelMaxSeg) return MHA_ERR_UNSUPPORTED;
+  if (num_buckets > mha::kRelMaxSeg || max_distance > mha::kRelFar) return MHA_ERR_UNSUPPORTED;
   if (!mha::rel_plan(num_buckets, max_distance, bidirectional != 0, r)) return MHA_ERR_INVALID;
   if (!aligned(bias, bias_dtype == MHA_F32 ? 4 : 2)) return MHA_ERR_ALIGN;
   r->table = bias;
@@ -62,6 +62,8 @@ int take_strides(const int64_t* strides, int count, int H, const int* rows, cons
 // checks that all three calls share; rows: the longer of the sequences' lengths
 int check_sizes(int B, int H, int rows, int d_k, int d_v, int dtype, float scale) {
   if (std::isnan(scale) || std::isinf(scale)) return MHA_ERR_INVALID;
+  // the bf16 kernel adds bias / scale
+  if (scale > 0.f && (scale < 0x1p-64f || scale > 0x1p64f)) return MHA_ERR_UNSUPPORTED;
   if (B > 65535 || H > 65535 || rows > kMaxRows) return MHA_ERR_UNSUPPORTED;
   if (dtype == MHA_BF16 ? d_k != 64 || d_v != 64 : d_k > 128 || d_v > 128)
     return MHA_ERR_UNSUPPORTED;
@@ -87,7 +89,7 @@ extern "C" {
 
 int mha_rel_bucket(int distance, int num_buckets, int max_distance, int bidirectional) {
   mha::RelBias r;
-  if (num_buckets > mha::kRelMaxSeg) return MHA_ERR_UNSUPPORTED;
+  if (num_buckets > mha::kRelMaxSeg || max_distance > mha::kRelFar) return MHA_ERR_UNSUPPORTED;
   if ((bidirectional != 0 && bidirectional != 1) ||
       !mha::rel_plan(num_buckets, max_distance, bidirectional != 0, &r))
     return MHA_ERR_INVALID;

@@ -43,8 +43,9 @@ __device__ __forceinline__ void rel_load(RelShared& sh, const RelBias& r, int h,
   int at = INT_MAX;
   float v = 0.f;
   if (s < r.nseg) {
-    at = r.start[s];
-    const int64_t i = static_cast<int64_t>(r.bucket[s]) * r.H + h;
+    const int32_t seg = r.seg[s];
+    at = s == 0 ? INT_MIN : rel_start(seg);
+    const int64_t i = static_cast<int64_t>(rel_row(seg)) * r.H + h;
     v = r.table_f32 ? __ldg(static_cast<const float*>(r.table) + i)
                     : __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(r.table) + i));
     v = v < -1e30f ? -INFINITY : v * mul;
@@ -53,13 +54,28 @@ __device__ __forceinline__ void rel_load(RelShared& sh, const RelBias& r, int h,
   sh.bias[s] = v;
 }
 
-// The segment of distance d: borders behind the last segment are INT_MAX, start[0] INT_MIN.
-__device__ __forceinline__ int rel_segment(const RelShared& sh, int d) {
-  int s = 0;
+// The segment of each of N distances: borders behind the last segment are INT_MAX, start[0] INT_MIN.
+// `steps` (rel_steps) is the same for all threads; the N searches run side by side.
+__device__ __forceinline__ int rel_steps(int nseg) { return nseg <= 32 ? 16 : kRelMaxSeg / 2; }
+template <int N>
+__device__ __forceinline__ void rel_segments(const RelShared& sh, int steps, const int (&d)[N],
+                                             int (&s)[N]) {
 #pragma unroll
-  for (int step = kRelMaxSeg / 2; step > 0; step >>= 1)
-    if (sh.start[s + step] <= d) s += step;
-  return s;
+  for (int i = 0; i < N; ++i) s[i] = 0;
+#pragma unroll 1
+  for (int step = steps; step > 0; step >>= 1) {
+    int at[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) at[i] = sh.start[s[i] + step];
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] += at[i] <= d[i] ? step : 0;
+  }
+}
+__device__ __forceinline__ int rel_segment(const RelShared& sh, int steps, int d) {
+  const int one[1] = {d};
+  int s[1];
+  rel_segments<1>(sh, steps, one, s);
+  return s[0];
 }
 
 }  // namespace mha

@@ -29,13 +29,13 @@ bool rel_plan(int num_buckets, int max_distance, bool bidirectional, RelBias* r)
   if (bidirectional && (num_buckets < 4 || num_buckets % 2 != 0)) return false;
   const int per = bidirectional ? num_buckets / 2 : num_buckets;
   const int e = per / 2;
-  if (max_distance <= e) return false;
+  if (max_distance <= e || max_distance > kRelFar) return false;
   int first[kRelMaxSeg + 1];
   for (int u = 0; u < per; ++u) first[u] = u < e ? u : first_of(u - e, per, e, max_distance);
   int n = 0;
   auto add = [&](int start, int bucket) {
-    r->start[n] = n == 0 ? INT_MIN : start;
-    r->bucket[n++] = static_cast<uint8_t>(bucket);
+    r->seg[n] = (n == 0 ? -kRelFar : start) * 128 + bucket;
+    ++n;
   };
   // keys before the query, farthest first; a bucket whose successor starts at the same n is empty
   for (int u = per - 1; u >= 0; --u) {
@@ -55,8 +55,8 @@ bool rel_plan(int num_buckets, int max_distance, bool bidirectional, RelBias* r)
 
 int rel_bucket_of(const RelBias& r, int d) {
   int s = 0;
-  while (s + 1 < r.nseg && r.start[s + 1] <= d) ++s;
-  return r.bucket[s];
+  while (s + 1 < r.nseg && rel_start(r.seg[s + 1]) <= d) ++s;
+  return rel_row(r.seg[s]);
 }
 
 }  // namespace mha

@@ -17,13 +17,18 @@ struct RelBias {
   int nseg;                     // segments in the order of the distance (see rel_bias.cuh)
   int num_buckets;
   float* partial;               // backward: the tiles' sums of dS per segment (device scratch)
-  int32_t start[kRelMaxSeg];    // first distance of a segment; start[0] = INT_MIN
-  uint8_t bucket[kRelMaxSeg];   // the segment's row of the table
+  // segment s: its first distance << 7 | its row of the table, one word, because lanes that read
+  // different words of a parameter are served one after another (of the first segment, which has
+  // no first distance, -kRelFar)
+  int32_t seg[kRelMaxSeg];
 };
+constexpr int kRelFar = (1 << 24) - 1;  // positions are at most 2^24, distances less
+constexpr int rel_start(int32_t seg) { return seg >> 7; }
+constexpr int rel_row(int32_t seg) { return seg & 127; }
 
-// Fills start, bucket and nseg; false where the numbers describe no buckets:
+// Fills seg and nseg; false where the numbers describe no buckets:
 // 2 <= num_buckets <= 128 (4 at least, and even, when bidirectional), max_distance above the
-// distances that have a bucket of their own.
+// distances that have a bucket of their own and at most kRelFar.
 bool rel_plan(int num_buckets, int max_distance, bool bidirectional, RelBias* r);
 // The bucket of distance d.
 int rel_bucket_of(const RelBias& r, int d);

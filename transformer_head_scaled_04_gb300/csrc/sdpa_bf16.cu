@@ -34,14 +34,16 @@
 // CTA winds down.
 //
 // Instantiated with a RelBias, the kernel adds a learned bias per head and bucket of j - i to the
-// scores (rel_bias.cuh): p = 2^(s c + t - m), t = bias log2(e).  Every warp follows the segment of
-// its tile's smallest distance; a tile within one segment adds a constant inside the exponential's
-// multiply-add, a tile that a border crosses takes t from a table of the warp's 159 distances in
-// shared memory (row r, column q at q + 31 - r: no bank conflicts).  No barrier is added.  Keys past
+// scores (rel_bias.cuh), in units of the raw score: p = 2^((s + t - m) c), t = bias / scale.  Every
+// warp follows the segment of its tile's smallest distance; a tile within one segment takes t into
+// the exponential's constant, (t - m) c, and runs the code of attention without bias.  Where a border
+// crosses the tile, t comes from a table of the warp's 159 distances in shared memory (row r, column q
+// at q + 31 - r: no bank conflicts).  No barrier is added.  Keys past
 // key_len[b] may hold anything there: the rows of V past it are cleared in shared memory.
 #include <cuda_bf16.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "device_common.cuh"
 #include "launchers.h"
@@ -104,6 +106,7 @@ struct Params {
   int B, H, Nq, Nk, mask, window;
   const int32_t* key_len;
   float scale_log2;
+  float inv_scale;  // relative bias: bias / scale is added to the raw scores
   float* lse;
   __nv_bfloat16* O;  // direct stores for rows that see no key (zeros)
   int64_t so_b, so_h, so_n;
@@ -202,13 +205,6 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (warp == 5) {
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
-  }
-  if constexpr (kRel) {
-    if (warp < 4) {
-      pdl_wait();  // the table may be the previous kernel's output
-      for (int s = threadIdx.x; s <= kRelMaxSeg; s += kBQ)
-        rel_load(*reinterpret_cast<RelShared*>(smem + kOffRel), rel, h, s, 1.4426950408889634f);
-    }
   }
   tc_fence_before();
   __syncthreads();
@@ -317,35 +313,40 @@ __global__ void __launch_bounds__(kThreads, 2)
     bool ok = true;
     float m_used = -INFINITY;
     float l = 0.f;
-    // relative bias: the segment of the warp's smallest distance in the tile, where the next one
-    // begins, this segment's bias; `unseen`: no key of this row has had a weight so far
-    [[maybe_unused]] const RelShared& rs = *reinterpret_cast<const RelShared*>(smem + kOffRel);
+    // relative bias: a segment's bias and where the next one begins; `unseen`: no key of this row
+    // has had a weight so far, `waiting`: of any row
+    [[maybe_unused]] RelShared& rs =
+        *reinterpret_cast<RelShared*>(align_smem_1024(smem_raw) + kOffRel);
+    if constexpr (kRel) {  // while Q and K arrive; every softmax warp passes here
+      for (int s = threadIdx.x; s <= kRelMaxSeg; s += kBQ) rel_load(rs, rel, h, s, p.inv_scale);
+      named_bar_sync(1, kBQ);
+    }
     [[maybe_unused]] float* table =
-        reinterpret_cast<float*>(smem + kOffRelTable) + quarter * kRelTable;
-    [[maybe_unused]] int seg = 0, seg_next = INT_MIN;
+        reinterpret_cast<float*>(align_smem_1024(smem_raw) + kOffRelTable) + quarter * kRelTable;
+    [[maybe_unused]] int seg_next = INT_MIN;
     [[maybe_unused]] float seg_bias = 0.f;
-    [[maybe_unused]] bool unseen = true;
+    [[maybe_unused]] bool unseen = true, waiting = true;
     for (int j = 0; j < nt; ++j) {
-      // Rel: the scores become s mul + add - m_used (powers of two), mul and add the same for all
-      [[maybe_unused]] bool near = false;
-      [[maybe_unused]] float mul = c, add = 0.f;
+      [[maybe_unused]] bool from_table = false;
       if constexpr (kRel) {
         const int d0 = (kt0 + j) * kBKV - (wr0 + 31);  // the warp's smallest distance
-        if (d0 >= seg_next) {
-          seg = rel_segment(rs, d0);
-          seg_next = rs.start[seg + 1];
-          seg_bias = rs.bias[seg];
-        }
-        near = d0 + kBKV + 30 >= seg_next;
-        add = seg_bias;
-        if (near) {
+        from_table = waiting || d0 + kBKV + 30 >= seg_next;
+        if (from_table) {
+          constexpr int kN = kRelTable / 32;
+          int d[kN], seg[kN];
+#pragma unroll
+          for (int e = 0; e < kN; ++e) d[e] = d0 + lane + 32 * e;
+          rel_segments<kN>(rs, rel_steps(rel.nseg), d, seg);
           __syncwarp();  // the previous tile's reads of the table are done
 #pragma unroll
-          for (int e = 0; e < kRelTable / 32; ++e)
-            table[lane + 32 * e] = rs.bias[rel_segment(rs, d0 + lane + 32 * e)];
+          for (int e = 0; e < kN; ++e)  // later keys are out under the causal mask
+            table[lane + 32 * e] = p.mask == 1 && d[e] > 0 ? -INFINITY : rs.bias[seg[e]];
+          // the next tile's smallest distance, d0 + 128: if its segment reaches past that tile's
+          // largest, this is the next tile's bias
+          const int next_seg = __shfl_sync(0xffffffffu, seg[kBKV / 32], 0);
+          seg_next = rs.start[next_seg + 1];
+          seg_bias = rs.bias[next_seg];
           __syncwarp();
-          mul = 1.f;
-          add = 0.f;
         }
       }
       if (!warp_all(mbar_wait(bar(kBarSFull), j & 1, p.timeout_ns))) {
@@ -360,7 +361,12 @@ __global__ void __launch_bounds__(kThreads, 2)
       const bool mask_hi = lim_min - col0 < kBKV - 1;
       const bool mask_lo = first_max - col0 > 0;
       float sv[128];
-      auto load_s = [&]() {
+      // Rel: tiles that take the table (kNear) and tiles of one segment run code of their own from
+      // here to the end of the step, with marks at both ends that keep the compiler from merging
+      // parts of them, and tiles of one segment take no maximum (predicated, it was executed in every
+      // tile): for the big model's heads 800 us with nothing apart, 521 with the maximum in both
+      auto load_s = [&](auto kind) {
+        constexpr bool kNear = decltype(kind)::value;
         uint32_t r0[32], r1[32], r2[32], r3[32];
         tmem_ld32(tS + 0, r0);
         tmem_ld32(tS + 32, r1);
@@ -378,16 +384,23 @@ __global__ void __launch_bounds__(kThreads, 2)
           sv[64 + q] = __uint_as_float(r2[q]);
           sv[96 + q] = __uint_as_float(r3[q]);
         }
-        if constexpr (kRel) {
-          if (near) {
-            const float* t = table + 31 - lane;
+        if constexpr (kNear) {
+          const float* t = table + 31 - lane;
 #pragma unroll
-            for (int q = 0; q < 128; ++q) sv[q] = fmaf(sv[q], c, t[q]);
+          for (int q = 0; q < 128; q += 2) {
+            const float2 x = fadd2(make_float2(sv[q], sv[q + 1]), make_float2(t[q], t[q + 1]));
+            sv[q] = x.x;
+            sv[q + 1] = x.y;
           }
         }
         // excluded keys get -inf (p = 0): one compare against a per-row bound per key,
         // one-sided where no row of the warp has the other end inside the tile
-        if (mask_hi || mask_lo) {
+        if constexpr (kRel) {
+          if (mask_hi && (!kNear || p.mask != 1)) {  // the table has the causal mask
+#pragma unroll
+            for (int q = 0; q < 128; ++q) sv[q] = q > hi ? -INFINITY : sv[q];
+          }
+        } else if (mask_hi || mask_lo) {
           if (!mask_lo) {
 #pragma unroll
             for (int q = 0; q < 128; ++q) sv[q] = q > hi ? -INFINITY : sv[q];
@@ -414,10 +427,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       };
       uint32_t pk[64];
       float tile_sum;
-      auto exp_tile = [&]() {
-        const float n1 = kRel ? add - m_used : -m_used * c;
+      auto exp_tile = [&](float add) {  // add: relative bias of the whole tile
+        const float n1 = kRel ? (add - m_used) * c : -m_used * c;
         const float2 n2 = make_float2(n1, n1);
-        const float2 c2 = kRel ? make_float2(mul, mul) : make_float2(c, c);
+        const float2 c2 = make_float2(c, c);
         float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
 #pragma unroll
         for (int q = 0; q < 64; ++q) {
@@ -433,104 +446,120 @@ __global__ void __launch_bounds__(kThreads, 2)
         const float2 acc = fadd2(acc0, acc1);
         tile_sum = acc.x + acc.y;
       };
-      load_s();
+      float alpha = 1.f;
+      bool grow = false;
       // m_used only guards the exponentials against overflow (p and l share it, O / l is
       // taken at the end): the exact max of the first key tile, reused by later tiles, and a
       // tile whose row sum leaves [0, 2^64] is redone with the true max
-      if constexpr (kRel) {  // a row whose first keys have no weight (bias -inf) waits for its max
-        if (__any_sync(0xffffffffu, unseen)) {
-          const float mt = fmaf(row_max(), mul, add);
-          if (unseen && mt != -INFINITY) {
-            m_used = mt;
-            unseen = false;
-          } else if (unseen) {
-            m_used = 0.f;
+      auto weigh = [&](auto kind) -> bool {
+        constexpr bool kNear = decltype(kind)::value;
+        const float add = kRel && !kNear ? seg_bias : 0.f;
+        load_s(kind);
+        if constexpr (kRel) {
+          // a row whose first keys have no weight (bias -inf) waits for its maximum; tiles of one
+          // segment hold no such code
+          if constexpr (kNear) {
+            if (waiting) {
+              const float mt = row_max();
+              if (unseen) m_used = mt == -INFINITY ? 0.f : mt;
+              unseen = unseen && mt == -INFINITY;
+              waiting = __any_sync(0xffffffffu, unseen);
+            }
           }
+        } else if (j == 0) {
+          const float mt = row_max();
+          m_used = (mt == -INFINITY) ? 0.f : mt;
         }
-      } else if (j == 0) {
-        const float mt = row_max();
-        m_used = (mt == -INFINITY) ? 0.f : mt;
-      }
-      exp_tile();
-      float alpha = 1.f;
-      bool grow = false;
-      const bool redo = j > 0 && !(tile_sum <= 1.8446744e19f);  // 2^64
-      if (__any_sync(0xffffffffu, redo)) {  // rare; S(j) is still in TMEM
-        load_s();
-        const float m_new = fmaxf(m_used, kRel ? fmaf(row_max(), mul, add) : row_max());
-        if (m_new > m_used) {
-          grow = true;
-          alpha = ex2_approx(kRel ? m_used - m_new : (m_used - m_new) * c);
-          l *= alpha;
-          m_used = m_new;
+        exp_tile(add);
+        const bool redo = j > 0 && !(tile_sum <= 1.8446744e19f);  // 2^64
+        if (__any_sync(0xffffffffu, redo)) {  // rare; S(j) is still in TMEM
+          load_s(kind);
+          const float m_new = fmaxf(m_used, kRel ? row_max() + add : row_max());
+          if (m_new > m_used) {
+            grow = true;
+            alpha = ex2_approx((m_used - m_new) * c);
+            l *= alpha;
+            m_used = m_new;
+          }
+          exp_tile(add);
         }
-        exp_tile();
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarSFree));  // S may now be overwritten
-      // the previous P.V product must be done before O is rescaled or P overwritten
-      if (j > 0 && !warp_all(mbar_wait(bar(kBarODone), (j - 1) & 1, p.timeout_ns))) {
-        record_error(p.status, kErrTimeout, kSiteSoftmaxO);
-        ok = false;
-        break;
-      }
-      if (__any_sync(0xffffffffu, grow)) {  // TMEM access is warp-collective
-        tc_fence_after();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarSFree));  // S may now be overwritten
+        // the previous P.V product must be done before O is rescaled or P overwritten
+        if (j > 0 && !warp_all(mbar_wait(bar(kBarODone), (j - 1) & 1, p.timeout_ns))) {
+          record_error(p.status, kErrTimeout, kSiteSoftmaxO);
+          return false;
+        }
+        if (__any_sync(0xffffffffu, grow)) {  // TMEM access is warp-collective
+          tc_fence_after();
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t o[32];
-          tmem_ld32(tO + half * 32, o);
-          tmem_wait_ld();
-          reg_fence(o);
+          for (int half = 0; half < 2; ++half) {
+            uint32_t o[32];
+            tmem_ld32(tO + half * 32, o);
+            tmem_wait_ld();
+            reg_fence(o);
 #pragma unroll
-          for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * alpha);
-          tmem_st32(tO + half * 32, o);
+            for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * alpha);
+            tmem_st32(tO + half * 32, o);
+          }
+          tmem_wait_st();
+        }
+        {
+          uint32_t lo32[32], hi32[32];
+#pragma unroll
+          for (int q = 0; q < 32; ++q) {
+            lo32[q] = pk[q];
+            hi32[q] = pk[32 + q];
+          }
+          tmem_st32(tP, lo32);
+          tmem_st32(tP + 32, hi32);
+        }
+        l += tile_sum;
+        if constexpr (kRel) {
+          // rows of V past key_len may hold anything, and 0 times that may not be 0
+          if (p.mask == 2 && j == nt - 1 && (kt0 + j + 1) * kBKV > L) {
+            if (!warp_all(mbar_wait(bar(kBarVFull + j % kVRing), (j / kVRing) & 1, p.timeout_ns))) {
+              tmem_wait_st();
+              record_error(p.status, kErrTimeout, kSiteSoftmaxO);
+              return false;
+            }
+            const int r = quarter * 32 + lane;
+            if (col0 + r >= L) {
+#pragma unroll
+              for (int u = 0; u < 8; ++u)
+                st_shared_v4(sV + (j % kVRing) * kTileBytes + r * 128 + u * 16,
+                             make_uint4(0u, 0u, 0u, 0u));
+            }
+            fence_proxy_async_smem();
+          }
         }
         tmem_wait_st();
-      }
-      {
-        uint32_t lo32[32], hi32[32];
-#pragma unroll
-        for (int q = 0; q < 32; ++q) {
-          lo32[q] = pk[q];
-          hi32[q] = pk[32 + q];
-        }
-        tmem_st32(tP, lo32);
-        tmem_st32(tP + 32, hi32);
-      }
-      l += tile_sum;
+        tc_fence_before();
+        mbar_arrive(bar(kBarPFull));
+        return true;
+      };
       if constexpr (kRel) {
-        // rows of V past key_len may hold anything, and 0 times that may not be 0
-        if (p.mask == 2 && j == nt - 1 && (kt0 + j + 1) * kBKV > L) {
-          if (!warp_all(mbar_wait(bar(kBarVFull + j % kVRing), (j / kVRing) & 1, p.timeout_ns))) {
-            tmem_wait_st();
-            record_error(p.status, kErrTimeout, kSiteSoftmaxO);
-            ok = false;
-            break;
-          }
-          const int r = quarter * 32 + lane;
-          if (col0 + r >= L) {
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-              st_shared_v4(sV + (j % kVRing) * kTileBytes + r * 128 + u * 16,
-                           make_uint4(0u, 0u, 0u, 0u));
-          }
-          fence_proxy_async_smem();
+        if (from_table) {
+          asm volatile("// several segments");
+          ok = weigh(std::true_type{});
+          asm volatile("// end of several segments");
+        } else {
+          asm volatile("// one segment");
+          ok = weigh(std::false_type{});
+          asm volatile("// end of one segment");
         }
+      } else {
+        ok = weigh(std::false_type{});
       }
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(bar(kBarPFull));
+      if (!ok) break;
     }
 
     // -------------------------------------------------------------- epilogue: O / l
     const int64_t lse_i = (static_cast<int64_t>(b) * p.H + h) * p.Nq + row;
     if (p.lse != nullptr && row < p.Nq &&
         bounds_ok(lse_i, static_cast<int64_t>(p.B) * p.H * p.Nq, p.status, kSiteLse))
-      p.lse[lse_i] = (ok && l > 0.f) ? ((kRel ? m_used : m_used * c) + log2f(l)) *
-                                           0.6931471805599453f
-                                     : INFINITY;
+      p.lse[lse_i] = (ok && l > 0.f) ? (m_used * c + log2f(l)) * 0.6931471805599453f : INFINITY;
     if (nt > 0) {
       float o[64];
 #pragma unroll
@@ -613,6 +642,7 @@ cudaError_t launch(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtenso
   p.window = a.window;
   p.key_len = a.key_len;
   p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
+  p.inv_scale = static_cast<float>(1.0 / a.scale);
   p.lse = a.lse;
   p.O = static_cast<__nv_bfloat16*>(a.O);
   p.so_b = a.so[0];

@@ -35,18 +35,19 @@
 //
 // Instantiated with a RelBias (rel_bias.cuh) both kernels rebuild P with the learned bias of the
 // distance j - i, p = 2^(c s' + t), and the dkdv kernel also sums dS per segment of distances, the
-// gradient of the bias.  A warp's 32 keys x 64 queries that lie within one segment take t as a
-// constant and add their dS up in two registers, one addition per pair of elements; where a border
-// crosses them t comes from a table of the warp's 95 distances and dS is summed along the
-// diagonals: the running sum of a diagonal moves to the next lane with every column (one shuffle and
-// one addition per column, four column blocks side by side), and a segmented scan over the diagonals
-// gives the segments' sums.  Lane s % 32 owns segment s; the CTA writes one sum per segment, and a
-// last launch adds those of a head in a fixed order, so the gradient is bitwise reproducible.  Keys
-// past key_len[b] may hold anything there: their dS is set to 0, their rows of K cleared.
+// gradient of the bias.  A math warp's 32 keys x 64 queries that lie within one segment take t as a
+// constant and add their dS up in a register pair.  Where a border crosses them, or a mask, t comes
+// from a table of the warp's 95 distances in shared memory (-inf where masked), and after the products
+// have what they wait for dS is summed along the diagonals: lane r takes column i's value from lane
+// (r + i) % 32, which puts a distance's values into one lane, and a segmented scan over the lanes gives
+// the segments' sums.  Lane s % 32 owns segment s; the CTA writes one sum per segment, and a last launch
+// adds those of a head in a fixed order, so the gradient is bitwise reproducible.  Keys past key_len[b]
+// may hold anything there: their rows of K and V are cleared before the first product.
 #include <cuda_bf16.h>
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "device_common.cuh"
 #include "launchers.h"
@@ -72,7 +73,12 @@ constexpr int kQThreads = (kMathWarps + 3) * 32;
 constexpr int kKThreads = (kMathWarps + 4) * 32;
 constexpr int kKMathRegs = 200;
 constexpr int kKControlRegs = 72;
-static_assert(kMathWarps * 32 * kKMathRegs + 4 * 32 * kKControlRegs <= kKThreads * 168,
+// with a relative bias: all that the launch allocates (at 200 the math warps spilled 15 loads a step)
+constexpr int kKMathRegsRel = 216;
+__host__ __device__ constexpr int k_split_regs(bool rel) {
+  return kMathWarps * 32 * (rel ? kKMathRegsRel : kKMathRegs) + 4 * 32 * kKControlRegs;
+}
+static_assert(k_split_regs(false) <= kKThreads * 168 && k_split_regs(true) <= kKThreads * 168,
               "dkdv register split exceeds the launch allocation");
 constexpr int kErrTimeout = -6;
 enum : int { kSiteBwdProducer = 41, kSiteBwdMma = 42, kSiteBwdMath = 43, kSiteBwdEpi = 44 };
@@ -189,33 +195,26 @@ __device__ __forceinline__ void dkdv_half(const uint32_t* s0, const uint32_t* s1
   }
 }
 
-// dkdv_half with a relative bias: p = 2^(c s' + t), t the constant `add`, or (kTable) tab[-ca]
-// for query column ca0 + ca.  far gets the sums of dS (even and odd columns); with kTable dS stays
-// in the registers of g0 and g1 instead, as floats.  Masked pairs may hold anything (rows of K and
-// V past key_len), so their dS is set to 0.
-template <bool kMask, bool kTable>
-__device__ __forceinline__ void dkdv_half_rel(const uint32_t* s0, const uint32_t* s1, uint32_t* g0,
-                                              uint32_t* g1, int ca0, bool row_ok, int first_ok,
-                                              float c, float add, const float* tab, float2& far,
-                                              uint32_t* pp, uint32_t* ds) {
+// dkdv_half with a relative bias: p = 2^(c s' + t).  kTable: t = tab[-i] for the half's i-th column
+// (-inf where the pair is masked), and dS stays in g0 and g1 as fp32.  Otherwise t is the constant
+// `add`, and far gets the sums of dS (even and odd columns).
+template <bool kTable>
+__device__ __forceinline__ void dkdv_half_rel(const uint32_t (&s0)[32], const uint32_t (&s1)[32],
+                                              uint32_t (&g0)[32], uint32_t (&g1)[32], float c,
+                                              float add, const float* tab, float2& far,
+                                              uint32_t (&pp)[32], uint32_t (&ds)[32]) {
   const float2 c2 = make_float2(c, c), add2 = make_float2(add, add);
 #pragma unroll
   for (int i = 0; i < 32; ++i) {
-    const int ca = ca0 + 2 * i;  // query column within the tile
     const float2 sv = make_float2(__uint_as_float(i < 16 ? s0[2 * i] : s1[2 * i - 32]),
                                   __uint_as_float(i < 16 ? s0[2 * i + 1] : s1[2 * i + 1 - 32]));
     uint32_t& gx = i < 16 ? g0[2 * i] : g1[2 * i - 32];
     uint32_t& gy = i < 16 ? g0[2 * i + 1] : g1[2 * i + 1 - 32];
-    const float2 gv = make_float2(__uint_as_float(gx), __uint_as_float(gy));
     float2 pv = ffma2(sv, c2, kTable ? make_float2(tab[-2 * i], tab[-2 * i - 1]) : add2);
     pv.x = ex2_approx(pv.x);
     pv.y = ex2_approx(pv.y);
-    float2 dv = fmul2(pv, gv);
-    if (kMask) {
-      if (!row_ok || ca < first_ok) pv.x = dv.x = 0.f;
-      if (!row_ok || ca + 1 < first_ok) pv.y = dv.y = 0.f;
-    }
     pp[i] = pack_bf16x2(pv.x, pv.y);
+    const float2 dv = fmul2(pv, make_float2(__uint_as_float(gx), __uint_as_float(gy)));
     ds[i] = pack_bf16x2(dv.x, dv.y);
     if (kTable) {
       gx = __float_as_uint(dv.x);
@@ -226,92 +225,42 @@ __device__ __forceinline__ void dkdv_half_rel(const uint32_t* s0, const uint32_t
   }
 }
 
-// The sums of a warp's 32 x 64 dS over the diagonals e = lane + 63 - ca (0..94), in buf[0..94]
-// (96 floats of the warp; column ca's values in g0, then g1).  Sixteen columns at a time: a
-// diagonal's running sum passes from lane to lane, lane 31's is complete and added to buf.
-__device__ __forceinline__ void diagonal_sums(const uint32_t* g0, const uint32_t* g1, int lane,
-                                              float* buf) {
+// The sums of 32 x 32 dS along the diagonals: lane r adds what lies at distance r (lane - column = r)
+// to `up` and at distance r - 32 to `down`.
+__device__ __forceinline__ void diagonal_sums(const uint32_t (&g)[32], int lane, float& up,
+                                              float& down) {
+  float a[2] = {0.f, 0.f}, b[2] = {0.f, 0.f};
 #pragma unroll
-  for (int u = 0; u < 3; ++u) buf[lane + 32 * u] = 0.f;
-  __syncwarp();
-  float acc[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) acc[k] = 0.f;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int ca = 16 * k + i;
-      if (i > 0) {
-        const float up = __shfl_up_sync(0xffffffffu, acc[k], 1);
-        if (lane == 31) buf[95 - ca] += acc[k];  // column ca - 1, lane 31
-        acc[k] = lane == 0 ? 0.f : up;
-      }
-      acc[k] += __uint_as_float(ca < 32 ? g0[ca] : g1[ca - 32]);
-    }
+  for (int i = 0; i < 32; ++i) {
+    const float v = __shfl_sync(0xffffffffu, __uint_as_float(g[i]), lane + i);  // lane (r + i) % 32
+    if (lane + i < 32)
+      a[i & 1] += v;
+    else
+      b[i & 1] += v;
   }
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    __syncwarp();
-    buf[lane + 48 - 16 * k] += acc[k];
-  }
-  __syncwarp();
+  up += a[0] + a[1];
+  down += b[0] + b[1];
 }
 
-// Adds the sums over the segments (distance d0 + e for diagonal e) to their owners: running sums of
-// buf[0..94] that start anew at every segment's first diagonal (three diagonals to a lane, lanes
-// joined by a segmented scan), of which a segment's last one is its sum.  No differences are taken,
-// so a bucket without pairs keeps an exact 0.
-__device__ __forceinline__ void segment_sums(const RelShared& rs, int nseg, int d0, int lane,
-                                             float* buf, float (&own)[kRelMaxSeg / 32]) {
-  uint32_t first[3] = {0u, 0u, 0u};  // bit e: diagonal e begins a segment
-#pragma unroll
-  for (int k = 0; k < kRelMaxSeg / 32; ++k) {
-    const int s = lane + 32 * k, at = s < nseg ? rs.start[s] : INT_MIN;
-    if (at > d0 && at <= d0 + 94) {
-      const uint32_t bit = 1u << ((at - d0) & 31);
-      const int w = (at - d0) >> 5;
-      first[0] |= w == 0 ? bit : 0u;
-      first[1] |= w == 1 ? bit : 0u;
-      first[2] |= w == 2 ? bit : 0u;
-    }
-  }
-  bool h[3];
-  float v[3];
-#pragma unroll
-  for (int i = 0; i < 3; ++i) first[i] = __reduce_or_sync(0xffffffffu, first[i]);
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    const int e = 3 * lane + i;
-    const uint32_t word = e < 32 ? first[0] : e < 64 ? first[1] : first[2];
-    h[i] = (word >> (e & 31)) & 1u;
-    v[i] = buf[e];
-  }
-  float sum = h[1] ? v[1] : v[0] + v[1];  // since the lane's last beginning
-  sum = h[2] ? v[2] : sum + v[2];
-  bool begins = h[0] || h[1] || h[2];
+// Adds v of the lanes of each segment (seg, which does not fall with the lane) up and the sums to
+// their owners, by way of part[0..31] (one float per segment from `first` on).  own is indexed by a
+// variable on purpose: it stays in local memory, away from the registers of steps that need none.
+__device__ __forceinline__ void segment_sums(float v, int seg, int lane, float* part,
+                                             float (&own)[kRelMaxSeg / 32]) {
+  const int first = __shfl_sync(0xffffffffu, seg, 0), last = __shfl_sync(0xffffffffu, seg, 31);
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const float up = __shfl_up_sync(0xffffffffu, sum, off);
-    const bool b = __shfl_up_sync(0xffffffffu, begins ? 1 : 0, off) != 0;
-    if (lane >= off) {
-      if (!begins) sum += up;
-      begins = begins || b;
-    }
+    const float up = __shfl_up_sync(0xffffffffu, v, off);
+    const int other = __shfl_up_sync(0xffffffffu, seg, off);
+    if (lane >= off && other == seg) v += up;
   }
-  float carry = __shfl_up_sync(0xffffffffu, sum, 1);
-  if (lane == 0) carry = 0.f;
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    carry = h[i] ? v[i] : carry + v[i];
-    buf[3 * lane + i] = carry;
-  }
+  const int next = __shfl_down_sync(0xffffffffu, seg, 1);
+  if (lane == 31 || next != seg) part[seg - first] = v;  // the segment's last lane
   __syncwarp();
-#pragma unroll
-  for (int k = 0; k < kRelMaxSeg / 32; ++k) {
+#pragma unroll 1
+  for (int k = first >> 5; k <= last >> 5; ++k) {
     const int s = lane + 32 * k;
-    if (s < nseg && rs.start[s] <= d0 + 94 && rs.start[s + 1] > d0)
-      own[k] += buf[rs.start[s + 1] > d0 + 94 ? 94 : rs.start[s + 1] - 1 - d0];
+    if (s >= first && s <= last) own[k] += part[s - first];
   }
   __syncwarp();
 }
@@ -397,10 +346,6 @@ __global__ void __launch_bounds__(kQThreads, 1)
     }
     mbar_init(bar(kQBarDrain), 2);
     fence_mbar_init();
-  }
-  if constexpr (kRel) {
-    if (threadIdx.x <= kRelMaxSeg)
-      rel_load(*reinterpret_cast<RelShared*>(smem + kQOffRel), rel, h, threadIdx.x, kLog2e);
   }
   if (warp == kWarpMma) {
     tmem_alloc(smem_u32(tmem_slot), 512);
@@ -512,7 +457,11 @@ __global__ void __launch_bounds__(kQThreads, 1)
     const float nd = __ldg(tile_st + kT + r_local);  // -D
     const float c = p.scale * kLog2e;
     const int limit = (p.mask == 1) ? min(row, L - 1) : L - 1;  // keys j <= limit
-    [[maybe_unused]] const RelShared& rs = *reinterpret_cast<const RelShared*>(smem + kQOffRel);
+    [[maybe_unused]] RelShared& rs = *reinterpret_cast<RelShared*>(smem + kQOffRel);
+    if constexpr (kRel) {  // while the first tiles arrive; every math warp passes here
+      if (threadIdx.x <= kRelMaxSeg) rel_load(rs, rel, h, threadIdx.x, kLog2e);
+      named_bar_sync(1, kMathWarps * 32);
+    }
     [[maybe_unused]] float* table =
         reinterpret_cast<float*>(smem + kQOffTable) + warp * kRelTable;
     [[maybe_unused]] int seg_next = INT_MIN;
@@ -524,16 +473,18 @@ __global__ void __launch_bounds__(kQThreads, 1)
         // the half's distances are d0 + e, e = column + 31 - lane in 0..94
         const int d0 = j * kT + half * 64 - (q0 + quarter * 32 + 31);
         if (d0 >= seg_next) {
-          const int seg = rel_segment(rs, d0);
+          const int seg = rel_segment(rs, rel_steps(rel.nseg), d0);
           seg_next = rs.start[seg + 1];
           seg_bias = rs.bias[seg];
         }
         near = d0 + 94 >= seg_next;
         if (near) {
+          const int d[3] = {d0 + lane, d0 + lane + 32, d0 + lane + 64};
+          int seg[3];
+          rel_segments<3>(rs, rel_steps(rel.nseg), d, seg);
           __syncwarp();  // the previous tile's reads of the table are done
 #pragma unroll
-          for (int e = 0; e < kRelTable / 32; ++e)
-            table[lane + 32 * e] = rs.bias[rel_segment(rs, d0 + lane + 32 * e)];
+          for (int e = 0; e < 3; ++e) table[lane + 32 * e] = rs.bias[seg[e]];
           __syncwarp();
         }
       }
@@ -644,13 +595,14 @@ __host__ __device__ constexpr int k_off_bar(bool fused) {
   return fused ? kKOffStage + kMathWarps * kStageBytes : kKOffDS;
 }
 // with a relative bias: borders and biases, then 128 floats per math warp (the table of 95
-// distances, later the diagonals' sums, at the end the warp's sums of segments)
+// distances, 32 for segments' sums; at the end the warp's sums of all segments), 64 of -inf
 __host__ __device__ constexpr int k_off_rel(bool fused) { return k_off_bar(fused) + 256; }
 __host__ __device__ constexpr int k_off_table(bool fused) {
   return k_off_rel(fused) + static_cast<int>(sizeof(RelShared));
 }
 __host__ __device__ constexpr int k_smem(bool fused, bool rel = false) {
-  return 1024 + (rel ? k_off_table(fused) + kMathWarps * kRelMaxSeg * 4 : k_off_bar(fused) + 256);
+  return 1024 + (rel ? k_off_table(fused) + kMathWarps * kRelMaxSeg * 4 + 64 * 4
+                     : k_off_bar(fused) + 256);
 }
 static_assert(kKOffDS % 1024 == 0 && kKOffStage % 1024 == 0, "swizzled buffers need 1 KB alignment");
 static_assert(k_smem(true, true) <= 227 * 1024, "fused dkdv shared memory");
@@ -727,11 +679,6 @@ __global__ void __launch_bounds__(kKThreads, 1)
     st_shared_v4(row + kT * 16, make_uint4(0u, 0u, 0u, 0u));
     fence_proxy_async_smem();
   }
-  if constexpr (kRel) {
-    if (threadIdx.x <= kRelMaxSeg)
-      rel_load(*reinterpret_cast<RelShared*>(smem + k_off_rel(kFused)), rel, h, threadIdx.x,
-               kLog2e);
-  }
   if (warp == kWarpMma) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
@@ -743,7 +690,7 @@ __global__ void __launch_bounds__(kKThreads, 1)
 
   // register split (setmaxnreg): 384 threads launch with 168 registers each (64512); the
   // control warpgroup (producer, three issuers) drops to 72 so the math warps can take 200:
-  // 256 x 200 + 128 x 72 = 60416 <= 64512
+  // 256 x 200 + 128 x 72 = 60416 <= 64512 (216 with a relative bias: 64512)
   if (warp >= kMathWarps) regs_dec<kKControlRegs>();  // first: the math warps' increase waits on it
   if (warp == kWarpProducer) {
     // ------------------------------------------------------------ producer (TMA)
@@ -782,6 +729,17 @@ __global__ void __launch_bounds__(kKThreads, 1)
     }
   } else if (warp == kWarpMma) {
     // ------------------------------------------------------------ S^T and dP^T issuer
+    if constexpr (kRel) {
+      if (ni > 0 && k0 + kT > L && mbar_wait(bar(kKBarIn), 0, p.timeout_ns)) {
+        // rows of K and V past key_len may hold anything, and 0 times that may not be 0
+        for (int e = (L - k0) * 8 + lane; e < kT * 8; e += 32) {
+          st_shared_v4(smem_u32(smem + kKOffK) + e * 16, make_uint4(0u, 0u, 0u, 0u));
+          st_shared_v4(smem_u32(smem + kKOffV) + e * 16, make_uint4(0u, 0u, 0u, 0u));
+        }
+        fence_proxy_async_smem();
+      }
+      __syncwarp();
+    }
     if (lane == 0 && ni > 0) {
       constexpr uint32_t idS = idesc_bf16_f32(kT, kT, false, false);
       const uint64_t dKd = smem_desc_sw128(smem_u32(smem + kKOffK), 1024, 1024);
@@ -872,7 +830,7 @@ __global__ void __launch_bounds__(kKThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ math warps (one key row each)
-    regs_inc<kKMathRegs>();
+    regs_inc<(kRel ? kKMathRegsRel : kKMathRegs)>();
     const int quarter = warp & 3, half = warp >> 2;
     const int r_local = quarter * 32 + lane;
     const int key = k0 + r_local;
@@ -892,43 +850,51 @@ __global__ void __launch_bounds__(kKThreads, 1)
         bulk_commit_group();
       }
     };
-    // relative bias: the segment of the half's largest distance, its first distance and its bias;
-    // dS summed within it (far) and what this lane's segments have so far
-    [[maybe_unused]] const RelShared& rs =
-        *reinterpret_cast<const RelShared*>(smem + k_off_rel(kFused));
+    // relative bias: the segment of the smallest distance so far (distances fall with t), its first
+    // distance and bias, dS summed within it, and what this lane's segments have so far.  The sums are
+    // touched only by steps that take the table: in local memory they cost the others no registers.
+    [[maybe_unused]] RelShared& rs = *reinterpret_cast<RelShared*>(smem + k_off_rel(kFused));
     [[maybe_unused]] float* buf =
         reinterpret_cast<float*>(smem + k_off_table(kFused)) + warp * kRelMaxSeg;
+    [[maybe_unused]] float* none =  // 64 of -inf, the table of a key past key_len
+        reinterpret_cast<float*>(smem + k_off_table(kFused)) + kMathWarps * kRelMaxSeg;
     [[maybe_unused]] int seg = 0, seg_start = INT_MAX;
-    [[maybe_unused]] float seg_bias = 0.f;
-    [[maybe_unused]] float2 far = make_float2(0.f, 0.f);
+    [[maybe_unused]] float seg_bias = 0.f, far = 0.f;
+    if constexpr (kRel) {  // while the first tiles arrive; every math warp passes here
+      if (threadIdx.x <= kRelMaxSeg) rel_load(rs, rel, h, threadIdx.x, kLog2e);
+      if (threadIdx.x >= 192) none[threadIdx.x - 192] = -INFINITY;
+      named_bar_sync(1, kMathWarps * 32);
+      seg = rel_segment(rs, rel_steps(rel.nseg), k0 + quarter * 32 + 31 - (i0 * kT + half * 64));
+      seg_start = rs.start[seg];
+      seg_bias = rs.bias[seg];
+    }
     [[maybe_unused]] float own[kRelMaxSeg / 32] = {};
     [[maybe_unused]] auto flush_far = [&]() {
-      float v = far.x + far.y;
-      far = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-#pragma unroll
-      for (int k = 0; k < kRelMaxSeg / 32; ++k)
-        if (lane + 32 * k == seg) own[k] += v;
+      for (int off = 16; off > 0; off >>= 1) far += __shfl_xor_sync(0xffffffffu, far, off);
+      if (lane == (seg & 31)) own[seg >> 5] += far;
+      far = 0.f;
     };
+    const int key_last = k0 + quarter * 32 + 31;  // the warp's last key
     bool ok = true;
     for (int t = 0; t < ni; ++t) {
       const int q0 = (i0 + t) * kT;
-      [[maybe_unused]] const int d0 = k0 + quarter * 32 - (q0 + half * 64 + 63);
-      [[maybe_unused]] bool near = false;
+      [[maybe_unused]] bool table = false;
+      [[maybe_unused]] int at[3];  // segments of the distances db + lane, db + lane - 32 and - 64
       if constexpr (kRel) {
-        // the half's distances are d0 + e, e = lane + 63 - column in 0..94; d0 falls with t
-        if (d0 + 94 < seg_start || (t & 15) == 0) {
-          if (t > 0) flush_far();  // also every 16 tiles, which bounds the length of a sum
-          seg = rel_segment(rs, d0 + 94);
-          seg_start = rs.start[seg];
-          seg_bias = rs.bias[seg];
-        }
-        near = d0 < seg_start;
-        if (near) {
+        // distances are db + lane - column: db - 63 .. db + 31
+        const int db = k0 + quarter * 32 - (q0 + half * 64);
+        table = db - 63 < seg_start || key_last >= L || (p.mask == 1 && db + 31 > 0);
+        if (table) {
+          flush_far();
+          const int d[3] = {db + lane, db + lane - 32, db + lane - 64};
+          rel_segments<3>(rs, rel_steps(rel.nseg), d, at);
 #pragma unroll
           for (int e = 0; e < 3; ++e)
-            buf[lane + 32 * e] = rs.bias[rel_segment(rs, d0 + lane + 32 * e)];
+            buf[64 - 32 * e + lane] = p.mask == 1 && d[e] > 0 ? -INFINITY : rs.bias[at[e]];
+          seg = __shfl_sync(0xffffffffu, at[2], 1);  // of db - 63
+          seg_start = rs.start[seg];
+          seg_bias = rs.bias[seg];
           __syncwarp();
         }
       }
@@ -937,96 +903,104 @@ __global__ void __launch_bounds__(kKThreads, 1)
         ok = false;
         break;
       }
-      tc_fence_after();
-      uint32_t s0[32], s1[32], g0[32], g1[32];
-      tmem_ld32(tmem + kKColS + lane_off + half * 64, s0);
-      tmem_ld32(tmem + kKColS + lane_off + half * 64 + 32, s1);
-      tmem_ld32(tmem + kKColP + lane_off + half * 64, g0);
-      tmem_ld32(tmem + kKColP + lane_off + half * 64 + 32, g1);
-      tmem_wait_ld();
-      reg_fence(s0);
-      reg_fence(s1);
-      reg_fence(g0);
-      reg_fence(g1);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kKBarSFree));
-      uint32_t pp[32], ds[32];
-      // key j = key is seen by query q0 + ca when j < L and, for the causal mask, j <= q
-      const bool row_ok = key < L;
-      const int first_ok = (p.mask == 1) ? key - q0 : -kT;
-      if constexpr (kRel) {
-        const bool open = warp_all(row_ok && first_ok <= half * 64);
-        const float* tab = buf + 63 + lane;
-        if (near && open)
-          dkdv_half_rel<false, true>(s0, s1, g0, g1, half * 64, row_ok, first_ok, c, 0.f, tab, far,
-                                     pp, ds);
-        else if (near)
-          dkdv_half_rel<true, true>(s0, s1, g0, g1, half * 64, row_ok, first_ok, c, 0.f, tab, far,
-                                    pp, ds);
-        else if (open)
-          dkdv_half_rel<false, false>(s0, s1, g0, g1, half * 64, row_ok, first_ok, c, seg_bias, tab,
-                                      far, pp, ds);
-        else
-          dkdv_half_rel<true, false>(s0, s1, g0, g1, half * 64, row_ok, first_ok, c, seg_bias, tab,
-                                     far, pp, ds);
-        if (kFused && t == 0 && !row_ok) {
-          // rows of K past key_len may hold anything: cleared before the first dQ reads them (the
-          // product S^T of the next tile may see either, it only fills masked rows)
-          const uint32_t k_row = smem_u32(smem + kKOffK) + r_local * 128 + half * 64;
-#pragma unroll
-          for (int u = 0; u < 4; ++u) st_shared_v4(k_row + u * 16, make_uint4(0u, 0u, 0u, 0u));
-        }
-      } else if (warp_all(row_ok && first_ok <= half * 64))  // every pair of this half is allowed
-        dkdv_half<false>(s0, s1, g0, g1, half * 64, row_ok, first_ok, c, pp, ds);
-      else
-        dkdv_half<true>(s0, s1, g0, g1, half * 64, row_ok, first_ok, c, pp, ds);
-      // the previous dV product must have read P^T, and the previous dK (and dQ) product
-      // dS^T, before they change
-      if (t > 0 && !warp_all(mbar_wait(bar(kKBarDVDone), (t - 1) & 1, p.timeout_ns))) {
-        record_error(p.status, kErrTimeout, kSiteBwdMath);
-        ok = false;
-        break;
-      }
-      tmem_st32(tmem + kKColPT + lane_off + half * 32, pp);
-      if (t > 0 && !warp_all(mbar_wait(bar(kKBarDKDone), (t - 1) & 1, p.timeout_ns))) {
-        tmem_wait_st();
-        record_error(p.status, kErrTimeout, kSiteBwdMath);
-        ok = false;
-        break;
-      }
-      if constexpr (kFused) {
-        // dQ_{t-1} leaves TMEM before dQ_t (issued after this tile's PFull) overwrites it
-        uint32_t dq[32];
+      // Rel: a step that takes the table and one of two blocks of one segment each run code of their
+      // own, with marks at both ends that keep the compiler from merging parts of them: moves between
+      // the variants' registers cost 200 instructions a step (2025 us for the big model's heads)
+      auto step = [&](auto kind) -> bool {
+        [[maybe_unused]] constexpr bool kTable = decltype(kind)::value;
         tc_fence_after();
-        if (t > 0) tmem_ld32(tmem + kKColDQ + lane_off + half * 32, dq);
-        st_row_sw128(smem_u32(smem + kKOffDS + half * kTileBytes) + r_local * 128, lane, ds);
-        tmem_wait_st();
-        if (t > 0) {
-          tmem_wait_ld();
-          reg_fence(dq);
+        uint32_t s0[32], s1[32], g0[32], g1[32];
+        tmem_ld32(tmem + kKColS + lane_off + half * 64, s0);
+        tmem_ld32(tmem + kKColS + lane_off + half * 64 + 32, s1);
+        tmem_ld32(tmem + kKColP + lane_off + half * 64, g0);
+        tmem_ld32(tmem + kKColP + lane_off + half * 64 + 32, g1);
+        tmem_wait_ld();
+        reg_fence(s0);
+        reg_fence(s1);
+        reg_fence(g0);
+        reg_fence(g1);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kKBarSFree));
+        uint32_t pp[32], ds[32];
+        if constexpr (!kRel) {
+          // key j = key is seen by query q0 + ca when j < L and, for the causal mask, j <= q
+          const bool row_ok = key < L;
+          const int first_ok = (p.mask == 1) ? key - q0 : -kT;
+          if (warp_all(row_ok && first_ok <= half * 64))  // every pair of this half is allowed
+            dkdv_half<false>(s0, s1, g0, g1, half * 64, row_ok, first_ok, c, pp, ds);
+          else
+            dkdv_half<true>(s0, s1, g0, g1, half * 64, row_ok, first_ok, c, pp, ds);
+        } else {
+          float2 f = make_float2(0.f, 0.f);
+          dkdv_half_rel<kTable>(s0, s1, g0, g1, c, seg_bias, key < L ? buf + 64 + lane : none + 63, f,
+                                pp, ds);
+          if (!kTable) far += f.x + f.y;
         }
-        fence_proxy_async_smem();  // dS^T visible to the tensor core
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kKBarPFull));
-        if (t > 0) reduce_dq(dq, q0 - kT);
-      } else {
-        tmem_st32(tmem + kKColDS + lane_off + half * 32, ds);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kKBarPFull));
-      }
+        // the previous dV product must have read P^T, and the previous dK (and dQ) product
+        // dS^T, before they change
+        if (t > 0 && !warp_all(mbar_wait(bar(kKBarDVDone), (t - 1) & 1, p.timeout_ns))) {
+          record_error(p.status, kErrTimeout, kSiteBwdMath);
+          return false;
+        }
+        tmem_st32(tmem + kKColPT + lane_off + half * 32, pp);
+        if (t > 0 && !warp_all(mbar_wait(bar(kKBarDKDone), (t - 1) & 1, p.timeout_ns))) {
+          tmem_wait_st();
+          record_error(p.status, kErrTimeout, kSiteBwdMath);
+          return false;
+        }
+        if constexpr (kFused) {
+          // dQ_{t-1} leaves TMEM before dQ_t (issued after this tile's PFull) overwrites it
+          uint32_t dq[32];
+          tc_fence_after();
+          if (t > 0) tmem_ld32(tmem + kKColDQ + lane_off + half * 32, dq);
+          st_row_sw128(smem_u32(smem + kKOffDS + half * kTileBytes) + r_local * 128, lane, ds);
+          tmem_wait_st();
+          if (t > 0) {
+            tmem_wait_ld();
+            reg_fence(dq);
+          }
+          fence_proxy_async_smem();  // dS^T visible to the tensor core
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kKBarPFull));
+          if (t > 0) reduce_dq(dq, q0 - kT);
+        } else {
+          tmem_st32(tmem + kKColDS + lane_off + half * 32, ds);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kKBarPFull));
+        }
+        if constexpr (kRel) {
+          if constexpr (kTable) {  // after the products have what they wait for
+            float v[3] = {0.f, 0.f, 0.f};
+            diagonal_sums(g0, lane, v[0], v[1]);
+            diagonal_sums(g1, lane, v[1], v[2]);
+#pragma unroll
+            for (int e = 0; e < 3; ++e) segment_sums(v[e], at[e], lane, buf + 96, own);
+          }
+        }
+        return true;
+      };
       if constexpr (kRel) {
-        if (near) {  // after the products have what they wait for
-          diagonal_sums(g0, g1, lane, buf);
-          segment_sums(rs, rel.nseg, d0, lane, buf, own);
+        if (table) {
+          asm volatile("// table");
+          ok = step(std::true_type{});
+          asm volatile("// end of table");
+        } else {
+          asm volatile("// constants");
+          ok = step(std::false_type{});
+          asm volatile("// end of constants");
         }
+      } else {
+        ok = step(std::false_type{});
       }
+      if (!ok) break;
     }
     if constexpr (kRel) {
-      if (ni > 0) flush_far();
+      flush_far();
+      __syncwarp();
 #pragma unroll
       for (int k = 0; k < kRelMaxSeg / 32; ++k) buf[lane + 32 * k] = own[k];
     }
@@ -1146,7 +1120,7 @@ cudaError_t launch(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtenso
   if (e != cudaSuccess) return e;
   // the dkdv kernel's setmaxnreg split must fit in what its blocks launch with, or the
   // increase would wait forever: refuse to launch if the compiled register count is too small
-  if (regs * kKThreads < kMathWarps * 32 * kKMathRegs + 4 * 32 * kKControlRegs)
+  if (regs * kKThreads < k_split_regs(kRel))
     return cudaErrorInvalidConfiguration;
   if (!fused) {
     constexpr int kSmem = kRel ? kQSmemRel : kQSmem;

@@ -111,10 +111,11 @@ struct Rows {
 struct Where {
   int L, Nq, limit[2];  // rows g, g + 8 see positions up to limit
   int row[2];
-  int seg_next;
+  int seg_next, steps;
   float seg_bias;
-  __device__ __forceinline__ Where(const Params& p, int L_, int end, int g) {
+  __device__ __forceinline__ Where(const Params& p, const RelBias& rel, int L_, int end, int g) {
     L = L_;
+    steps = rel_steps(rel.nseg);
     Nq = p.Nq;
     seg_next = INT_MIN;
     seg_bias = 0.f;
@@ -130,7 +131,7 @@ struct Where {
                                          float c) {
     const int d0 = j0 - (L - 1);  // the tile's distances lie in d0 .. d0 + 8 NS - 1 + Nq - 1
     if (d0 >= seg_next) {
-      const int seg = rel_segment(rs, d0);
+      const int seg = rel_segment(rs, steps, d0);
       seg_next = rs.start[seg + 1];
       seg_bias = rs.bias[seg];
     }
@@ -141,7 +142,7 @@ struct Where {
       for (int i = 0; i < 4; ++i) {
         const int j = j0 + 8 * n + 2 * t + (i & 1);
         float bias = seg_bias;
-        if (near) bias = rs.bias[rel_segment(rs, j - (L - Nq + row[i >> 1]))];
+        if (near) bias = rs.bias[rel_segment(rs, steps, j - (L - Nq + row[i >> 1]))];
         x[n][i] = j <= limit[i >> 1] ? fmaf(x[n][i], c, bias) : -INFINITY;
       }
   }
@@ -271,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 4)
   }
   __syncthreads();
   const float c = p.scale * kLog2e;
-  Where where(p, L, end, g);
+  Where where(p, rel, L, end, g);
   Rows<8> r;
   r.clear();
   for (; j0 < end; j0 += 16 * kWarps) {
@@ -380,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 4 : 2)
     const uint4 x = at[0], y = at[1];
     return Tf32FragA{{x.x, x.y, x.z, x.w}, {y.x, y.y, y.z, y.w}};
   };
-  Where where(p, L, end, g);
+  Where where(p, rel, L, end, g);
   Rows<DP / 8> r;
   r.clear();
   for (; j0 < end; j0 += 8 * kWarps) {

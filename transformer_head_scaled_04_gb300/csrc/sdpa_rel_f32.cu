@@ -235,14 +235,14 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 3 : 2)
     if (j + 1 < nt) load(j + 1);
     const int d0 = j * kK - (q0 + kRows - 1);  // the tile's smallest distance
     if (d0 >= seg_next) {
-      const int seg = rel_segment(rs, d0);
+      const int seg = rel_segment(rs, rel_steps(rel.nseg), d0);
       seg_next = rs.start[seg + 1];
       seg_bias = rs.bias[seg];
     }
     const bool near = d0 + kRows + kK - 2 >= seg_next;
     if (near)
       for (int e = threadIdx.x; e < kRows + kK - 1; e += kThreads)
-        table[e] = rs.bias[rel_segment(rs, d0 + e)];
+        table[e] = rs.bias[rel_segment(rs, rel_steps(rel.nseg), d0 + e)];
     if (j + 1 < nt)
       copy_wait<1>();
     else
@@ -403,12 +403,12 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 3 : 2)
     const int d0 = j * kBwdRows - (q0 + kRows - 1);
     if (d0 >= seg_next || (j & 63) == 0) {
       if (j > 0) flush_far();  // also every 64 steps, which bounds the length of a sum
-      seg = rel_segment(rs, d0);
+      seg = rel_segment(rs, rel_steps(rel.nseg), d0);
       seg_next = rs.start[seg + 1];
       seg_bias = rs.bias[seg];
     }
     const bool near = d0 + kDist - 1 >= seg_next;
-    if (near && tid < kDist) table[tid] = rs.bias[rel_segment(rs, d0 + tid)];
+    if (near && tid < kDist) table[tid] = rs.bias[rel_segment(rs, rel_steps(rel.nseg), d0 + tid)];
     copy_wait<0>();
     __syncthreads();
     const bool skip = p.mask == 1 && j * kBwdRows > q0 + 16 * warp + 15;
@@ -522,12 +522,12 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 3 : 2)
     }
     const int d0 = k0 - (q0 + kBwdRows - 1);  // distances d0 + e, e = key row + 31 - query
     if (d0 + kDist - 1 < seg_start) {
-      const int seg = rel_segment(rs, d0 + kDist - 1);
+      const int seg = rel_segment(rs, rel_steps(rel.nseg), d0 + kDist - 1);
       seg_start = rs.start[seg];
       seg_bias = rs.bias[seg];
     }
     const bool near = d0 < seg_start;
-    if (near && tid < kDist) table[tid] = rs.bias[rel_segment(rs, d0 + tid)];
+    if (near && tid < kDist) table[tid] = rs.bias[rel_segment(rs, rel_steps(rel.nseg), d0 + tid)];
     copy_wait<0>();
     __syncthreads();
     float s[kNT][4], ds[kNT][4];
@@ -575,7 +575,8 @@ __global__ void __launch_bounds__(512)
   };
   if (threadIdx.x < rel.num_buckets) {
     bool held = false;
-    for (int s = 0; s < rel.nseg; ++s) held |= rel.bucket[s] == threadIdx.x;
+    for (int s = 0; s < rel.nseg; ++s)
+      held |= rel_row(rel.seg[s]) == static_cast<int>(threadIdx.x);
     if (!held) put(threadIdx.x, 0.f);
   }
   for (int s0 = 0; s0 < rel.nseg; s0 += 32) {
@@ -595,7 +596,7 @@ __global__ void __launch_bounds__(512)
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < 16; ++i) sum += part[i][lane];
-      put(rel.bucket[s], sum);
+      put(rel_row(rel.seg[s]), sum);
     }
     __syncthreads();
   }
