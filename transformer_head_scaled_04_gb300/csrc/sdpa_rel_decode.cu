@@ -21,6 +21,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "device_common.cuh"
 #include "launchers.h"
@@ -148,29 +149,12 @@ struct Where {
   }
 };
 
-// The warps' results meet in shared memory (o: [kWarps][Nq][DP], ml: [kWarps][Nq][2]) and leave as
-// O, or as this run's part.  col(n, i): the column of o[n][i] in its row.
-template <int DP, typename T, int NO, class Col>
-__device__ __forceinline__ void finish(const Params& p, Rows<NO>& r, float* so, float* sml,
-                                       float unit, int warp, int lane, int64_t bh, int split, T* O,
-                                       Col col) {
-  const int g = lane >> 2, t = lane & 3, Nq = p.Nq;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    r.l[i] += __shfl_xor_sync(0xffffffffu, r.l[i], 1);
-    r.l[i] += __shfl_xor_sync(0xffffffffu, r.l[i], 2);
-    const int row = g + 8 * i;
-    if (row < Nq) {
-      if (t == 0) {
-        sml[(warp * Nq + row) * 2] = r.m[i];
-        sml[(warp * Nq + row) * 2 + 1] = r.l[i];
-      }
-#pragma unroll
-      for (int n = 0; n < NO; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) so[(warp * Nq + row) * DP + col(n, e)] = r.o[n][2 * i + e];
-    }
-  }
+// The warps' results in shared memory (so: [kWarps][Nq][DP], sml: [kWarps][Nq] {m, l}) leave as O, or
+// as this run's part.
+template <int DP, typename T>
+__device__ __forceinline__ void join_warps(const Params& p, const float* so, const float* sml,
+                                           float unit, int64_t bh, int split, T* O) {
+  const int Nq = p.Nq;
   __syncthreads();
   for (int e = threadIdx.x; e < Nq * DP; e += kThreads) {
     const int row = e / DP, d = e % DP;
@@ -197,6 +181,31 @@ __device__ __forceinline__ void finish(const Params& p, Rows<NO>& r, float* so, 
       }
     }
   }
+}
+
+// The fragments of each warp go to shared memory; col(n, i): the column of o[n][i] in its row.
+template <int DP, typename T, int NO, class Col>
+__device__ __forceinline__ void finish(const Params& p, Rows<NO>& r, float* so, float* sml,
+                                       float unit, int warp, int lane, int64_t bh, int split, T* O,
+                                       Col col) {
+  const int g = lane >> 2, t = lane & 3, Nq = p.Nq;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    r.l[i] += __shfl_xor_sync(0xffffffffu, r.l[i], 1);
+    r.l[i] += __shfl_xor_sync(0xffffffffu, r.l[i], 2);
+    const int row = g + 8 * i;
+    if (row < Nq) {
+      if (t == 0) {
+        sml[(warp * Nq + row) * 2] = r.m[i];
+        sml[(warp * Nq + row) * 2 + 1] = r.l[i];
+      }
+#pragma unroll
+      for (int n = 0; n < NO; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) so[(warp * Nq + row) * DP + col(n, e)] = r.o[n][2 * i + e];
+    }
+  }
+  join_warps<DP>(p, so, sml, unit, bh, split, O);
 }
 
 // a run that holds no cached position
@@ -421,12 +430,155 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 4 : 2)
              [t](int n, int e) { return 32 * (n >> 2) + 8 * t + 4 * e + (n & 3); });
 }
 
+// ---- few queries: fused multiply-adds instead of products of 16 rows.  Lane (g, t) sums a quarter of
+// position g's score (the quarters meet in two shuffles) and has the values' pieces of positions 2 t
+// and 2 t + 1, whose weights it takes from their lanes; the four partial outputs meet at the end.
+// Multiply-adds instead of splits and products of 16 mostly empty rows: 8 heads of 131072 positions 124
+// us -> 81 (0.98 of the measured bandwidth); with 4 queries the two take the same time (69 and 71 us for
+// 8 x 16 heads of 4096), so the products take over from 3.
+template <int DP, bool kVec, int NQ>
+__global__ void __launch_bounds__(kThreads, DP * NQ <= 64 ? 4 : DP * NQ <= 128 ? 3 : 2)
+    sdpa_rel_decode_few_f32_kernel(const __grid_constant__ Params p,
+                                   const __grid_constant__ RelBias rel) {
+  pdl_launch_dependents();
+  pdl_wait();  // the previous kernel's output is complete from here on
+  using Tile = TileF32<DP, kVec>;
+  __shared__ RelShared rs;
+  __shared__ float sml[kWarps * NQ * 2];
+  __shared__ __align__(16) float so[kWarps * NQ * DP];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int split = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+  const int64_t bh = static_cast<int64_t>(b) * p.H + h;
+  const int L = min(max(__ldg(p.cache_len + b), 0), p.Lmax);
+  const int begin = split * p.chunk, end = min(begin + p.chunk, L);
+  float* O = static_cast<float*>(p.O) + b * p.so[0] + h * p.so[1];
+  if (begin >= L) return finish_empty<DP>(p, bh, split, O);
+  const float* K = static_cast<const float*>(p.K) + b * p.sk[0] + h * p.sk[1];
+  const float* V = static_cast<const float*>(p.V) + b * p.sv[0] + h * p.sv[1];
+  Tile tile;
+  int j0 = begin + 8 * warp;
+  tile.load(K, V, p, j0, end, g, t);
+  for (int s = threadIdx.x; s <= kRelMaxSeg; s += kThreads) rel_load(rs, rel, h, s, 1.f);
+  const float* Q = static_cast<const float*>(p.Q) + b * p.sq[0] + h * p.sq[1];
+  float4 q[NQ][DP / 16];
+  int limit[NQ];
+#pragma unroll
+  for (int i = 0; i < NQ; ++i) {
+    limit[i] = i < p.Nq ? min(p.causal ? L - p.Nq + i : L - 1, end - 1) : -1;
+#pragma unroll
+    for (int u = 0; u < DP / 16; ++u)
+      q[i][u] = Tile::piece(Q + i * p.sq[2], 4 * (t + 4 * u), p.d_k, i < p.Nq);
+  }
+  __syncthreads();
+  float m[NQ], l[NQ], o[NQ][DP / 8];
+#pragma unroll
+  for (int i = 0; i < NQ; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+#pragma unroll
+    for (int d = 0; d < DP / 8; ++d) o[i][d] = 0.f;
+  }
+  const int steps = rel_steps(rel.nseg);
+  int seg_next = INT_MIN;
+  float seg_bias = 0.f;
+  for (; j0 < end; j0 += 8 * kWarps) {
+    float x[NQ];
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      float a = 0.f, c = 0.f;
+#pragma unroll
+      for (int u = 0; u < DP / 16; ++u) {
+        a = fmaf(q[i][u].x, tile.k[u].x, a);
+        c = fmaf(q[i][u].y, tile.k[u].y, c);
+        a = fmaf(q[i][u].z, tile.k[u].z, a);
+        c = fmaf(q[i][u].w, tile.k[u].w, c);
+      }
+      x[i] = a + c;
+    }
+    float4 v[2][DP / 32];
+#pragma unroll
+    for (int u = 0; u < DP / 32; ++u) {
+      v[0][u] = tile.v[0][u];
+      v[1][u] = tile.v[1][u];
+    }
+    tile.load(K, V, p, j0 + 8 * kWarps, end, g, t);
+    const int d0 = j0 - (L - 1);  // the tile's distances lie in d0 .. d0 + 7 + Nq - 1
+    if (d0 >= seg_next) {
+      const int seg = rel_segment(rs, steps, d0);
+      seg_next = rs.start[seg + 1];
+      seg_bias = rs.bias[seg];
+    }
+    const bool near = d0 + 6 + p.Nq >= seg_next;
+    const int j = j0 + g;
+    bool raise = false;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      x[i] += __shfl_xor_sync(0xffffffffu, x[i], 1);
+      x[i] += __shfl_xor_sync(0xffffffffu, x[i], 2);
+      float bias = seg_bias;
+      if (near) bias = rs.bias[rel_segment(rs, steps, j - (L - p.Nq + i))];
+      x[i] = j <= limit[i] ? fmaf(x[i], p.scale, bias) : -INFINITY;
+      raise |= x[i] > m[i] + kSlack / kLog2e;
+    }
+    if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) {
+        float top = fmaxf(m[i], x[i]);
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1)
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        const float a = top == -INFINITY ? 1.f : ex2_approx((m[i] - top) * kLog2e);
+        m[i] = top;
+        l[i] *= a;
+#pragma unroll
+        for (int d = 0; d < DP / 8; ++d) o[i][d] *= a;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      const float w = ex2_approx((x[i] - (m[i] == -INFINITY ? 0.f : m[i])) * kLog2e);
+      l[i] += w;  // the same in the four lanes of a position
+      const float w0 = __shfl_sync(0xffffffffu, w, 8 * t), w1 = __shfl_sync(0xffffffffu, w, 8 * t + 4);
+#pragma unroll
+      for (int u = 0; u < DP / 32; ++u) {
+        o[i][4 * u + 0] = fmaf(w0, v[0][u].x, fmaf(w1, v[1][u].x, o[i][4 * u + 0]));
+        o[i][4 * u + 1] = fmaf(w0, v[0][u].y, fmaf(w1, v[1][u].y, o[i][4 * u + 1]));
+        o[i][4 * u + 2] = fmaf(w0, v[0][u].z, fmaf(w1, v[1][u].z, o[i][4 * u + 2]));
+        o[i][4 * u + 3] = fmaf(w0, v[0][u].w, fmaf(w1, v[1][u].w, o[i][4 * u + 3]));
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NQ; ++i) {
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], off);
+#pragma unroll
+    for (int d = 0; d < DP / 8; ++d) {
+      o[i][d] += __shfl_xor_sync(0xffffffffu, o[i][d], 1);
+      o[i][d] += __shfl_xor_sync(0xffffffffu, o[i][d], 2);
+    }
+    if (i < p.Nq) {
+      if (lane == 0) {
+        sml[(warp * p.Nq + i) * 2] = m[i];
+        sml[(warp * p.Nq + i) * 2 + 1] = l[i];
+      }
+      if (t == 0) {
+#pragma unroll
+        for (int u = 0; u < DP / 32; ++u)
+          *reinterpret_cast<float4*>(so + (warp * p.Nq + i) * DP + 32 * u + 4 * g) =
+              make_float4(o[i][4 * u], o[i][4 * u + 1], o[i][4 * u + 2], o[i][4 * u + 3]);
+      }
+    }
+  }
+  join_warps<DP>(p, so, sml, kLog2e, bh, split, O);
+}
+
 // ============================================================================ the runs' results
-// one block per (query row, head, batch element): DP columns x kThreads * 2 / DP groups of runs
-constexpr int kJoinThreads = 256;
+// one block per (query row, head, batch element): DP columns x kJoinThreads / DP groups of runs, 1024
+// threads for more than 32 runs, else 256
 constexpr int kMaxSplit = 1024;
 
-template <int DP, typename T>
+template <int DP, typename T, int kJoinThreads>
 __global__ void __launch_bounds__(kJoinThreads)
     sdpa_rel_join_kernel(const __grid_constant__ Params p, float unit) {
   pdl_launch_dependents();
@@ -465,7 +617,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   for (int i = 1; i < kJoinThreads / 32; ++i) l += total[i];
   float o = 0.f;
   const int d = tid % DP;
-#pragma unroll 4
+#pragma unroll 8
   for (int s = tid / DP; s < n; s += kGroups)
     if (w[s] > 0.f) o = fmaf(w[s], p.part[at(s) * DP + d], o);
   sum[tid] = o;
@@ -478,15 +630,28 @@ __global__ void __launch_bounds__(kJoinThreads)
   }
 }
 
-// Positions per CTA: about three rounds of the CTAs that fit on the GPU at once, at least 256.
-void plan(int B, int H, int Lmax, int dp, int* chunk, int* n_split) {
+// Runs of a head and positions of a run (a multiple of 64, 16 for each warp).  A round of CTAs that fit
+// on the GPU at once takes about the time of a run's positions and 96 more (start and the warps' join),
+// the second launch that of 150 and of some per run; of 1 to 8 full rounds the cheapest is taken.
+// Measured (us) for the rounds taken and for others: 64 x 16 heads of 4096 in bf16 166 with 4 runs
+// against 169 with 1 and 174 with 3, 8 x 16 heads of 16384 with 4 queries 87 with 19 runs against 119
+// with 5 and 93 with 29, 8 heads of 131072 44 with 76 runs against 48 with 228.
+void plan(int B, int H, int Nq, int Lmax, int dp, int dtype, int* chunk, int* n_split) {
   const int64_t heads = static_cast<int64_t>(B) * H;
-  const int64_t fit = 152 * (dp == 64 ? 4 : 2);
-  int64_t n = std::max<int64_t>(1, (3 * fit + heads - 1) / heads);
-  n = std::min<int64_t>({n, (Lmax + 255) / 256, kMaxSplit});
-  const int64_t c = ((Lmax + n - 1) / n + 63) / 64 * 64;
-  *chunk = static_cast<int>(c);
-  *n_split = static_cast<int>((Lmax + c - 1) / c);
+  const int64_t fit = 152 * (dtype == 1 ? 4 : dp == 64 ? (Nq == 2 ? 3 : 4) : (Nq == 1 ? 3 : 2));
+  int64_t best = -1;
+  for (int rounds = 1; rounds <= 8; ++rounds) {
+    int64_t n = std::max<int64_t>(1, rounds * fit / heads);
+    n = std::min<int64_t>({n, (Lmax + 63) / 64, kMaxSplit});
+    const int64_t c = ((Lmax + n - 1) / n + 63) / 64 * 64;
+    n = (Lmax + c - 1) / c;
+    const int64_t cost = (heads * n + fit - 1) / fit * (c + 96) + (n > 1 ? 150 + n * (Nq + 3) / 10 : 0);
+    if (best < 0 || cost < best) {
+      best = cost;
+      *chunk = static_cast<int>(c);
+      *n_split = static_cast<int>(n);
+    }
+  }
 }
 
 int padded(int dtype, int d_k, int d_v) { return dtype == 1 || (d_k <= 64 && d_v <= 64) ? 64 : 128; }
@@ -496,7 +661,7 @@ int padded(int dtype, int d_k, int d_v) { return dtype == 1 || (d_k <= 64 && d_v
 size_t rel_decode_workspace(int B, int H, int Nq, int Lmax, int d_k, int d_v, int dtype) {
   const int dp = padded(dtype, d_k, d_v);
   int chunk, n;
-  plan(B, H, Lmax, dp, &chunk, &n);
+  plan(B, H, Nq, Lmax, dp, dtype, &chunk, &n);
   return n == 1 ? 0 : static_cast<size_t>(B) * H * n * Nq * (dp + 2) * sizeof(float);
 }
 
@@ -505,7 +670,7 @@ cudaError_t launch_sdpa_rel_decode(const RelDecodeArgs& a, const RelBias& rel, i
   Params p = {};
   p.H = a.H; p.Nq = a.Nq; p.Lmax = a.Lmax; p.causal = a.causal; p.d_k = a.d_k; p.d_v = a.d_v;
   const int dp = padded(dtype, a.d_k, a.d_v);
-  plan(a.B, a.H, a.Lmax, dp, &p.chunk, &p.n_split);
+  plan(a.B, a.H, a.Nq, a.Lmax, dp, dtype, &p.chunk, &p.n_split);
   p.cache_len = a.cache_len;
   p.scale = a.scale;
   p.Q = a.Q; p.K = a.K; p.V = a.V; p.O = a.O;
@@ -517,31 +682,40 @@ cudaError_t launch_sdpa_rel_decode(const RelDecodeArgs& a, const RelBias& rel, i
   }
   p.part = part;
   const dim3 grid(p.n_split, a.H, a.B), rows(a.Nq, a.H, a.B);
-  cudaError_t e;
-  if (dtype == 1) {
-    e = launch_pdl(sdpa_rel_decode_bf16_kernel, grid, dim3(kThreads), 0, s, p, rel);
-    if (e == cudaSuccess && p.n_split > 1)
-      e = launch_pdl(sdpa_rel_join_kernel<64, __nv_bfloat16>, rows, dim3(kJoinThreads), 0, s, p,
-                     1.f);
+  auto go = [&](auto kernel, auto join, auto join_many, float unit) {
+    cudaError_t e = launch_pdl(kernel, grid, dim3(kThreads), 0, s, p, rel);
+    if (e == cudaSuccess && p.n_split > 32)
+      e = launch_pdl(join_many, rows, dim3(1024), 0, s, p, unit);
+    else if (e == cudaSuccess && p.n_split > 1)
+      e = launch_pdl(join, rows, dim3(256), 0, s, p, unit);
     return e;
-  }
+  };
+  if (dtype == 1)
+    return go(sdpa_rel_decode_bf16_kernel, sdpa_rel_join_kernel<64, __nv_bfloat16, 256>,
+              sdpa_rel_join_kernel<64, __nv_bfloat16, 1024>, 1.f);
   bool vec = a.d_k % 4 == 0 && a.d_v % 4 == 0;
   const void* ptr[3] = {a.Q, a.K, a.V};
   for (int t = 0; t < 3; ++t) {
     vec = vec && reinterpret_cast<uintptr_t>(ptr[t]) % 16 == 0;
     for (int i = 0; i < 3; ++i) vec = vec && a.st[t][i] % 4 == 0;
   }
-  auto go = [&](auto kernel, auto join) {
-    cudaError_t err = launch_pdl(kernel, grid, dim3(kThreads), 0, s, p, rel);
-    if (err == cudaSuccess && p.n_split > 1)
-      err = launch_pdl(join, rows, dim3(kJoinThreads), 0, s, p, kLog2e);
-    return err;
+  auto go_f32 = [&](auto dim, auto quads) {
+    constexpr int DP = decltype(dim)::value;
+    constexpr bool kVec = decltype(quads)::value;
+    auto f = [&](auto kernel) {
+      return go(kernel, sdpa_rel_join_kernel<DP, float, 256>, sdpa_rel_join_kernel<DP, float, 1024>,
+                kLog2e);
+    };
+    if (a.Nq == 1) return f(sdpa_rel_decode_few_f32_kernel<DP, kVec, 1>);
+    if (a.Nq == 2) return f(sdpa_rel_decode_few_f32_kernel<DP, kVec, 2>);
+    return f(sdpa_rel_decode_f32_kernel<DP, kVec>);
   };
+  using std::integral_constant;
   if (dp == 64)
-    return vec ? go(sdpa_rel_decode_f32_kernel<64, true>, sdpa_rel_join_kernel<64, float>)
-               : go(sdpa_rel_decode_f32_kernel<64, false>, sdpa_rel_join_kernel<64, float>);
-  return vec ? go(sdpa_rel_decode_f32_kernel<128, true>, sdpa_rel_join_kernel<128, float>)
-             : go(sdpa_rel_decode_f32_kernel<128, false>, sdpa_rel_join_kernel<128, float>);
+    return vec ? go_f32(integral_constant<int, 64>{}, std::true_type{})
+               : go_f32(integral_constant<int, 64>{}, std::false_type{});
+  return vec ? go_f32(integral_constant<int, 128>{}, std::true_type{})
+             : go_f32(integral_constant<int, 128>{}, std::false_type{});
 }
 
 }  // namespace mha
