@@ -210,12 +210,10 @@ int mha_sdpa_rel_bwd(int B, int H, int Nq, int Nk, int d_k, int d_v, int dtype, 
       return MHA_ERR_CUDA;
     e = mha::launch_sdpa_bwd_rowdot(a, dtype, stream);
     if (e == cudaSuccess)
-      e = mha::launch_sdpa_rel_bwd_bf16(tq, tk, tv, tg, tdq, a, rel, ctx, stream);
+      e = mha::launch_sdpa_rel_bwd_bf16(tq, tk, tv, tg, tdq, a, rel, dbias, ctx, stream);
   } else {
-    e = mha::launch_sdpa_rel_bwd_f32(a, rel, stream);
+    e = mha::launch_sdpa_rel_bwd_f32(a, rel, dbias, stream);
   }
-  if (e == cudaSuccess)
-    e = mha::launch_rel_table_grad(rel, dbias, B, mha::rel_bwd_tiles(Nq, Nk, dtype), stream);
   return done(e);
 }
 

@@ -270,15 +270,18 @@ cudaError_t launch_sdpa_rel_bf16(const CUtensorMap& tmQ, const CUtensorMap& tmK,
                                  const SdpaArgs& a, const RelBias& rel, const DevCtx& ctx,
                                  cudaStream_t s);
 cudaError_t launch_sdpa_rel_f32(const SdpaArgs& a, const RelBias& rel, cudaStream_t s);
-// rel.partial: fp32 [B, H, rel_bwd_tiles(..), nseg] sums of dS, written by every tile; a.Dv as for
-// the launches without bias (fp32: written by the first of the two kernels)
+// rel.partial: fp32 [B, H, rel_bwd_tiles(..), nseg] sums of dS, written by every tile, from which the
+// last launch takes dtable [num_buckets, H] (the table's type); a.Dv as for the launches without bias
+// (fp32: written by the first of the kernels)
 cudaError_t launch_sdpa_rel_bwd_bf16(const CUtensorMap& tmQ, const CUtensorMap& tmK,
                                      const CUtensorMap& tmV, const CUtensorMap& tmG,
                                      const CUtensorMap& tmDQ, const SdpaBwdArgs& a,
-                                     const RelBias& rel, const DevCtx& ctx, cudaStream_t s);
-cudaError_t launch_sdpa_rel_bwd_f32(const SdpaBwdArgs& a, const RelBias& rel, cudaStream_t s);
+                                     const RelBias& rel, void* dtable, const DevCtx& ctx,
+                                     cudaStream_t s);
+cudaError_t launch_sdpa_rel_bwd_f32(const SdpaBwdArgs& a, const RelBias& rel, void* dtable,
+                                    cudaStream_t s);
 int rel_bwd_tiles(int Nq, int Nk, int dtype);
-// dtable [num_buckets, H] (the table's type) from those sums
+// that last launch where nothing else is left to do
 cudaError_t launch_rel_table_grad(const RelBias& rel, void* dtable, int B, int tiles,
                                   cudaStream_t s);
 

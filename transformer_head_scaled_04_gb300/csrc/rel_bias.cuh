@@ -78,4 +78,54 @@ __device__ __forceinline__ int rel_segment(const RelShared& sh, int steps, int d
   return s[0];
 }
 
+// The gradient of head h's column of the table, by a block of kRelGradThreads threads:
+// dtable[bucket of s, h] = sum over batch elements and tiles of partial[b, h, tile, s], in a fixed
+// order; buckets without a segment get 0.
+constexpr int kRelGradThreads = 256;
+__device__ __forceinline__ void rel_table_grad(const RelBias& rel, void* dtable, int B, int tiles,
+                                               int h) {
+  constexpr int kWarps = kRelGradThreads / 32;
+  __shared__ float part[kWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto put = [&](int u, float v) {
+    const int64_t i = static_cast<int64_t>(u) * rel.H + h;
+    if (rel.table_f32)
+      static_cast<float*>(dtable)[i] = v;
+    else
+      static_cast<__nv_bfloat16*>(dtable)[i] = __float2bfloat16_rn(v);
+  };
+  if (static_cast<int>(threadIdx.x) < rel.num_buckets) {
+    bool held = false;
+    for (int s = 0; s < rel.nseg; ++s)
+      held |= rel_row(rel.seg[s]) == static_cast<int>(threadIdx.x);
+    if (!held) put(threadIdx.x, 0.f);
+  }
+  for (int s0 = 0; s0 < rel.nseg; s0 += 32) {
+    const int s = s0 + lane;
+    float v = 0.f;
+    if (s < rel.nseg) {
+      const float* head = rel.partial + static_cast<int64_t>(h) * tiles * rel.nseg + s;
+      const int64_t rows = static_cast<int64_t>(B) * tiles;
+      const int64_t skip = static_cast<int64_t>(rel.H - 1) * tiles;  // rows of the other heads
+      int64_t b = 0, tile = warp;  // row r = b * tiles + tile, every kWarps-th
+      while (tile >= tiles) tile -= tiles, ++b;
+#pragma unroll 4
+      for (int64_t r = warp; r < rows; r += kWarps) {
+        v += head[(r + b * skip) * rel.nseg];
+        tile += kWarps;
+        while (tile >= tiles) tile -= tiles, ++b;
+      }
+    }
+    part[warp][lane] = v;
+    __syncthreads();
+    if (warp == 0 && s < rel.nseg) {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) sum += part[i][lane];
+      put(rel_row(rel.seg[s]), sum);
+    }
+    __syncthreads();
+  }
+}
+
 }  // namespace mha

@@ -1069,15 +1069,25 @@ __global__ void __launch_bounds__(kKThreads, 1)
   }
 }
 
-// dQ = scale * accumulator, as bf16 in dQ's layout; one thread per 8 consecutive values
+// dQ = scale * accumulator, as bf16 in dQ's layout; one thread per 8 consecutive values.  With a
+// relative bias the first H blocks take the heads' columns of the table's gradient instead.
+template <class Rel>
 __global__ void __launch_bounds__(256)
     sdpa_bwd_dq_convert_kernel(const float* __restrict__ acc, __nv_bfloat16* __restrict__ dq,
                                int H, int Nq, int rows, int64_t sb, int64_t sh, int64_t sn,
-                               float scale, int64_t total) {
+                               float scale, int64_t total, const __grid_constant__ Rel rel,
+                               void* dtable, int B, int tiles) {
   pdl_launch_dependents();
   pdl_wait();  // the fused kernel's reductions are complete from here on
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+  int block = static_cast<int>(blockIdx.x), blocks = static_cast<int>(gridDim.x);
+  if constexpr (IsRel<Rel>::value) {
+    static_assert(kRelGradThreads == 256, "");
+    if (block < H) return rel_table_grad(rel, dtable, B, tiles, block);
+    block -= H;
+    blocks -= H;
+  }
+  for (int64_t i = static_cast<int64_t>(block) * blockDim.x + threadIdx.x; i < total;
+       i += static_cast<int64_t>(blocks) * blockDim.x) {
     const int part = static_cast<int>(i & 7);
     const int64_t r = i >> 3;  // (b, h, n) with n < Nq
     const int n = static_cast<int>(r % Nq);
@@ -1099,7 +1109,8 @@ __global__ void __launch_bounds__(256)
 template <class Rel>
 cudaError_t launch(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                    const CUtensorMap& tmG, const CUtensorMap& tmDQ, const SdpaBwdArgs& a,
-                   const Rel& rel, const DevCtx& ctx, cudaStream_t s) {
+                   const Rel& rel, [[maybe_unused]] void* dtable, const DevCtx& ctx,
+                   cudaStream_t s) {
   constexpr bool kRel = IsRel<Rel>::value;
   BwdParams p;
   p.H = a.H;
@@ -1151,16 +1162,21 @@ cudaError_t launch(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtenso
     (void)launch_pdl(sdpa_bwd_dkdv_kernel<false, Rel>, grid, dim3(kKThreads), k_smem(false, kRel), s,
                      tmQ, tmK, tmV, tmG, tmDQ, p, rel);
   e = cudaGetLastError();
-  if (e != cudaSuccess || !fused) return e;
+  if (e != cudaSuccess) return e;
+  const int tiles = (a.Nk + kT - 1) / kT;  // rel_bwd_tiles
+  if (!fused) {
+    if constexpr (kRel) return launch_rel_table_grad(rel, dtable, a.B, tiles, s);
+    return e;
+  }
   const int rows = (a.Nq + kT - 1) / kT * kT;
   const int64_t total = static_cast<int64_t>(a.B) * a.H * a.Nq * 8;
   const int64_t want = (total + 255) / 256;
   const int blocks = static_cast<int>(std::min<int64_t>(want, static_cast<int64_t>(ctx.num_sms) * 8));
-  (void)launch_pdl(sdpa_bwd_dq_convert_kernel, dim3(blocks), dim3(256), 0, s,
+  (void)launch_pdl(sdpa_bwd_dq_convert_kernel<Rel>, dim3(blocks + (kRel ? a.H : 0)), dim3(256), 0, s,
                    reinterpret_cast<const float*>(reinterpret_cast<const char*>(a.Dv) +
                                                   sdpa_bwd_dq_acc_offset(a.B, a.H, a.Nq)),
                    static_cast<__nv_bfloat16*>(a.dQ), a.H, a.Nq, rows, a.st[5][0], a.st[5][1],
-                   a.st[5][2], a.scale, total);
+                   a.st[5][2], a.scale, total, rel, dtable, a.B, tiles);
   return cudaGetLastError();
 }
 
@@ -1170,14 +1186,15 @@ cudaError_t launch_sdpa_bwd_bf16(const CUtensorMap& tmQ, const CUtensorMap& tmK,
                                  const CUtensorMap& tmV, const CUtensorMap& tmG,
                                  const CUtensorMap& tmDQ, const SdpaBwdArgs& a,
                                  const DevCtx& ctx, cudaStream_t s) {
-  return launch(tmQ, tmK, tmV, tmG, tmDQ, a, NoRel{}, ctx, s);
+  return launch(tmQ, tmK, tmV, tmG, tmDQ, a, NoRel{}, nullptr, ctx, s);
 }
 
 cudaError_t launch_sdpa_rel_bwd_bf16(const CUtensorMap& tmQ, const CUtensorMap& tmK,
                                      const CUtensorMap& tmV, const CUtensorMap& tmG,
                                      const CUtensorMap& tmDQ, const SdpaBwdArgs& a,
-                                     const RelBias& rel, const DevCtx& ctx, cudaStream_t s) {
-  return launch(tmQ, tmK, tmV, tmG, tmDQ, a, rel, ctx, s);
+                                     const RelBias& rel, void* dtable, const DevCtx& ctx,
+                                     cudaStream_t s) {
+  return launch(tmQ, tmK, tmV, tmG, tmDQ, a, rel, dtable, ctx, s);
 }
 
 }  // namespace mha

@@ -557,49 +557,12 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 3 : 2)
     }
 }
 
-// ============================================================================ gradient of the table
-// dtable[bucket of s, h] = sum over batch elements and tiles of partial[b, h, tile, s], in a fixed
-// order; buckets without a segment get 0.  One block per head.
-__global__ void __launch_bounds__(512)
+// the gradient of the table alone, one block per head
+__global__ void __launch_bounds__(kRelGradThreads)
     rel_table_grad_kernel(const __grid_constant__ RelBias rel, void* dtable, int B, int tiles) {
   pdl_launch_dependents();
   pdl_wait();  // the partial sums are complete from here on
-  __shared__ float part[16][32];
-  const int h = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  auto put = [&](int u, float v) {
-    const int64_t i = static_cast<int64_t>(u) * rel.H + h;
-    if (rel.table_f32)
-      static_cast<float*>(dtable)[i] = v;
-    else
-      static_cast<__nv_bfloat16*>(dtable)[i] = __float2bfloat16_rn(v);
-  };
-  if (threadIdx.x < rel.num_buckets) {
-    bool held = false;
-    for (int s = 0; s < rel.nseg; ++s)
-      held |= rel_row(rel.seg[s]) == static_cast<int>(threadIdx.x);
-    if (!held) put(threadIdx.x, 0.f);
-  }
-  for (int s0 = 0; s0 < rel.nseg; s0 += 32) {
-    const int s = s0 + lane;
-    float v = 0.f;
-    if (s < rel.nseg) {
-      const int64_t rows = static_cast<int64_t>(B) * tiles;
-#pragma unroll 4
-      for (int64_t r = warp; r < rows; r += 16) {
-        const int64_t bb = r / tiles, tile = r % tiles;
-        v += rel.partial[((bb * rel.H + h) * tiles + tile) * rel.nseg + s];
-      }
-    }
-    part[warp][lane] = v;
-    __syncthreads();
-    if (warp == 0 && s < rel.nseg) {
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) sum += part[i][lane];
-      put(rel_row(rel.seg[s]), sum);
-    }
-    __syncthreads();
-  }
+  rel_table_grad(rel, dtable, B, tiles, static_cast<int>(blockIdx.x));
 }
 
 template <class F>
@@ -646,7 +609,8 @@ int rel_bwd_tiles(int Nq, int Nk, int dtype) {
   return dtype == 1 ? (Nk + 127) / 128 : (Nq + kRows - 1) / kRows;
 }
 
-cudaError_t launch_sdpa_rel_bwd_f32(const SdpaBwdArgs& a, const RelBias& rel, cudaStream_t s) {
+cudaError_t launch_sdpa_rel_bwd_f32(const SdpaBwdArgs& a, const RelBias& rel, void* dtable,
+                                    cudaStream_t s) {
   RelF32 p = {};
   p.Q = static_cast<const float*>(a.Q);
   p.K = static_cast<const float*>(a.K);
@@ -680,15 +644,19 @@ cudaError_t launch_sdpa_rel_bwd_f32(const SdpaBwdArgs& a, const RelBias& rel, cu
             : go(sdpa_rel_dq_f32_kernel<128, false>, gq, dq_smem<128>(), p, rel, s);
   if (e != cudaSuccess) return e;
   if (small)
-    return vec ? go(sdpa_rel_dkdv_f32_kernel<64, true>, gk, dkdv_smem<64>(), p, rel, s)
-               : go(sdpa_rel_dkdv_f32_kernel<64, false>, gk, dkdv_smem<64>(), p, rel, s);
-  return vec ? go(sdpa_rel_dkdv_f32_kernel<128, true>, gk, dkdv_smem<128>(), p, rel, s)
-             : go(sdpa_rel_dkdv_f32_kernel<128, false>, gk, dkdv_smem<128>(), p, rel, s);
+    e = vec ? go(sdpa_rel_dkdv_f32_kernel<64, true>, gk, dkdv_smem<64>(), p, rel, s)
+            : go(sdpa_rel_dkdv_f32_kernel<64, false>, gk, dkdv_smem<64>(), p, rel, s);
+  else
+    e = vec ? go(sdpa_rel_dkdv_f32_kernel<128, true>, gk, dkdv_smem<128>(), p, rel, s)
+            : go(sdpa_rel_dkdv_f32_kernel<128, false>, gk, dkdv_smem<128>(), p, rel, s);
+  return e == cudaSuccess ? launch_rel_table_grad(rel, dtable, a.B, rel_bwd_tiles(a.Nq, a.Nk, 0), s)
+                          : e;
 }
 
 cudaError_t launch_rel_table_grad(const RelBias& rel, void* dtable, int B, int tiles,
                                   cudaStream_t s) {
-  return launch_pdl(rel_table_grad_kernel, dim3(rel.H), dim3(512), 0, s, rel, dtable, B, tiles);
+  return launch_pdl(rel_table_grad_kernel, dim3(rel.H), dim3(kRelGradThreads), 0, s, rel, dtable, B,
+                    tiles);
 }
 
 }  // namespace mha

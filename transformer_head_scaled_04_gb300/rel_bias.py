@@ -14,7 +14,7 @@ import torch
 
 from . import _capi as C
 from .api import _DTYPES, _dt, _mask
-from .cache_q8 import _call, _cuda_device, _dense, _i32, _p, _same, _workspace
+from .cache_q8 import _call, _dense, _i32, _p, _same, _workspace
 
 
 def rel_bucket(distance, num_buckets=32, max_distance=128, bidirectional=True) -> int:
@@ -39,15 +39,29 @@ def _strides(*ts):
 
 def _qkv(what, q, k, v):
     """(device, dtype code, B, H, Nq, Nk, d_k, d_v) of tensors that fit together."""
-    dev = _cuda_device(q)
-    dt = _dt(q)
-    qs, ks, vs = q.shape, k.shape, v.shape
-    if (len(qs) != 4 or len(ks) != 4 or len(vs) != 4 or ks[0] != qs[0] or ks[1] != qs[1]
-            or ks[3] != qs[3] or vs[:3] != ks[:3] or k.dtype is not q.dtype
-            or v.dtype is not q.dtype or k.get_device() != dev or v.get_device() != dev):
+    dev = q.get_device()
+    if dev < 0:
+        raise ValueError("tensors must live on a CUDA device")
+    dtype = q.dtype
+    dt = _DTYPES.get(dtype)
+    if dt is None:
+        dt = _dt(q)  # raises
+    try:
+        (B, H, Nq, d_k), (Bk, Hk, Nk, dk), (Bv, Hv, Nv, d_v) = q.shape, k.shape, v.shape
+    except ValueError:
+        B, Bk = 0, 1
+    if (Bk != B or Bv != B or Hk != H or Hv != H or Nv != Nk or dk != d_k or k.dtype is not dtype
+            or v.dtype is not dtype or k.get_device() != dev or v.get_device() != dev):
         raise ValueError(f"{what}: q [B, H, Nq, d_k], k [B, H, Nk, d_k] and v [B, H, Nk, d_v] of "
                          "one type on one device expected")
-    return dev, dt, qs[0], qs[1], qs[2], ks[2], qs[3], vs[3]
+    return dev, dt, B, H, Nq, Nk, d_k, d_v
+
+
+def _new(like, B, H, N, d):
+    """A contiguous tensor [B, H, N, d] of like's type and device."""
+    if like.shape == (B, H, N, d) and like.is_contiguous():
+        return torch.empty_like(like)
+    return torch.empty((B, H, N, d), dtype=like.dtype, device=like.device)
 
 
 def _table(what, rel_bias, H, dev):
@@ -66,7 +80,7 @@ def _forward(what, q, k, v, rel_bias, mask, key_len, scale, max_distance, bidire
     if key_len is not None:
         _dense(key_len, _i32, (B,), dev, "key_len")
     if out is None:
-        out = torch.empty((B, H, Nq, d_v), dtype=q.dtype, device=q.device)
+        out = _new(q, B, H, Nq, d_v)
     else:
         _same(out, q, (B, H, Nq, d_v), dev, f"{what}: out")
     if lse:
@@ -123,9 +137,7 @@ def sdpa_rel_backward(q, k, v, rel_bias, o, do, lse, mask="none", key_len=None, 
     _dense(lse, torch.float32, (B, H, Nq), dev, "lse")
     if key_len is not None:
         _dense(key_len, _i32, (B,), dev, "key_len")
-    dq = torch.empty((B, H, Nq, d_k), dtype=q.dtype, device=q.device)
-    dk = torch.empty((B, H, Nk, d_k), dtype=q.dtype, device=q.device)
-    dv = torch.empty((B, H, Nk, d_v), dtype=q.dtype, device=q.device)
+    dq, dk, dv = _new(q, B, H, Nq, d_k), _new(k, B, H, Nk, d_k), _new(v, B, H, Nk, d_v)
     dbias = torch.empty_like(rel_bias)
     workspace = _workspace(workspace, sdpa_rel_bwd_workspace_size(B, H, Nq, Nk, dt, nb), q, dev,
                            what)
@@ -161,7 +173,7 @@ def sdpa_rel_decode(q, k_cache, v_cache, rel_bias, cache_len, causal=True, scale
     bt, nb = _table(what, rel_bias, H, dev)
     _dense(cache_len, _i32, (B,), dev, "cache_len")
     if out is None:
-        out = torch.empty((B, H, Nq, d_v), dtype=q.dtype, device=q.device)
+        out = _new(q, B, H, Nq, d_v)
     else:
         _same(out, q, (B, H, Nq, d_v), dev, f"{what}: out")
     if workspace is None:
