@@ -1,40 +1,50 @@
-// sdpa_rel_f32.cu -- fp32 attention with a learned relative position bias, forward and backward,
-// on the tensor cores (fp32 values as two tf32 terms, three products: mma_tf32.cuh).
+// sdpa_rel_f32.cu -- fp32 attention with a learned relative position bias, forward and backward, on
+// the tensor cores.
 //
 //   forward   x = scale q.k + t (t: rel_bias.cuh), O = softmax(x) V, lse = log sum exp x
 //   backward  p = exp(x - lse), D = rowsum(dO O), dS = p (dO.v - D),
 //             dQ = scale dS K, dK = scale dS^T Q, dV = p^T dO, dt(segment) = sum of its dS
 //
-// Warp products of 16 x 8 x 8 have register fragments that need no exchange between a score and its
-// use as the next product's operand, if the inner dimension is read in a fitting order (any order
-// gives the same sum): with lane = 4 g + t,
-//   products over d: inner positions t and t + 4 of a step are two neighbouring d, and a lane reads
-//     four of them at once, d = 32 u + 8 t + 4 v .. + 3;
-//   products over keys (or queries): positions t and t + 4 are rows 8 n + 2 t and 8 n + 2 t + 1, which
-//     are the two columns of the score fragment that the lane holds; the output's columns are
-//     d = 4 g + e + 32 u, so that a lane again reads four at once.
-// Rows in shared memory are d + 4 floats apart: both kinds of 16-byte reads are free of conflicts.
-// Tiles are 64 rows of the operand that a CTA owns (16 per warp) against 32 of the other, d
-// padded to 64 or 128 with zeros.  The bias of a tile that lies within one segment is a constant;
-// otherwise the CTA looks its distances up once into a table.  Bound by the products: three per
-// multiply-add of the formulas.
+// Every operand is scaled by a power of two that brings its tile's largest value to 2^13 .. 2^14 and
+// split into two fp16 terms, a = hi + lo (mma_f16.cuh); a product is hi hi + hi lo + lo hi with fp32 sums.  What is
+// left of a value is at most 2^-23 of it or 2^-39 of the tile's largest, and the dropped lo lo is at
+// most 2^-22 of the product: fp32's own accuracy.  (Two tf32 terms give the same at twice the time of
+// the tensor cores: 322 us forward for 8 x 8 heads of 1001, xxx in fp16.)  The tensor cores cut sums
+// off instead of rounding them, 2^-24 of the sum per step towards zero (9e-6 of a gradient over 900
+// keys in one chain), so the large products are kept apart from the small ones, a chain spans one
+// tile at most, and tiles are added up with ordinary additions.
+//
+// A CTA owns 64 rows (16 per warp) and goes over the other operand in tiles of 32 rows: while one tile
+// is computed the next one's fp32 values arrive (asynchronous copies); then its largest value is
+// found and it is split into one or both of
+//   rows   [row][d] halves, for products over d: a lane (lane = 4 g + t) reads 16 bytes of a row, eight
+//          neighbouring d, as the inner positions of two steps (any order of the inner dimension
+//          gives the same sum); 16-byte units of odd rows are swapped by 4, which frees the reads of
+//          bank conflicts
+//   pairs  [row / 2][d] words of two rows' halves, for products over rows: the inner positions of a
+//          score fragment are the columns a lane holds, 2 t and 2 t + 1, and the output's columns are
+//          d = 4 g + e + 32 u, so that a lane reads the words of four d at once
+// so that scores go into the next product without any exchange.  d is padded to 64 or 128 with zeros.
+// The bias of a tile that lies within one segment is a constant; otherwise the CTA looks its distances
+// up once into a table.  Bound by the products: three per multiply-add of the formulas, and in the
+// backward S and dP twice (dQ by its own kernel: no atomics, reproducible).
 #include <cmath>
 
 #include "device_common.cuh"
 #include "launchers.h"
-#include "mma_tf32.cuh"
+#include "mma_f16.cuh"
 #include "rel_bias.cuh"
 
 namespace mha {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kRows = 64;    // rows that a CTA owns, 16 per warp
-constexpr int kBwdRows = 32;  // rows per step of the backward kernels
+constexpr int kWarps = kThreads / 32;
+constexpr int kRows = 64;   // rows that a CTA owns, 16 per warp
+constexpr int kTile = 32;   // rows of the other operand's tile
+constexpr int kNT = kTile / 8;
+constexpr int kDist = kRows + kTile - 1;  // distances of a tile
 constexpr float kLog2e = 1.4426950408889634f;
-
-__host__ __device__ constexpr int pitch_of(int dp) { return dp + 4; }
-constexpr int kFwdKeys = 32;  // keys per step of the forward (two steps in shared memory)
 
 struct RelF32 {
   const float *Q, *K, *V, *O, *dO;
@@ -47,8 +57,9 @@ struct RelF32 {
   float scale;
 };
 
-__device__ __forceinline__ void copy_async(uint32_t dst, const float* src, bool valid, int bytes16) {
-  if (bytes16)
+template <bool kVec>
+__device__ __forceinline__ void copy_async(uint32_t dst, const float* src, bool valid) {
+  if (kVec)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                  "r"(valid ? 16 : 0)
                  : "memory");
@@ -58,89 +69,229 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const float* src, bool 
                  : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
-// rows n0 .. n0 + kN - 1 of a [N, d] matrix with row stride sn into dst [kN][DP + 4]; rows from
+// rows n0 .. n0 + kTile - 1 of a [N, d] matrix with row stride sn into raw [kTile][DP]; rows from
 // `limit` on and columns from d on become zeros (nothing of them is read)
-template <int DP, bool kVec, int kN>
-__device__ __forceinline__ void load_rows(float* dst, const float* src, int64_t sn, int n0,
+template <int DP, bool kVec>
+__device__ __forceinline__ void load_rows(float* raw, const float* src, int64_t sn, int n0,
                                           int limit, int d) {
-  constexpr int kUnit = kVec ? 4 : 1;
-  constexpr int kPer = DP / kUnit;
-  static_assert(kN * kPer % kThreads == 0, "");
+  constexpr int kUnit = kVec ? 4 : 1, kPer = DP / kUnit;
+  static_assert(kTile * kPer % kThreads == 0, "");
 #pragma unroll 4
-  for (int i = 0; i < kN * kPer / kThreads; ++i) {
+  for (int i = 0; i < kTile * kPer / kThreads; ++i) {
     const int e = i * kThreads + threadIdx.x;
     const int r = e / kPer, c = e % kPer * kUnit;
     const bool ok = n0 + r < limit && c < d;
-    const float* from = ok ? src + static_cast<int64_t>(n0 + r) * sn + c : src;
-    copy_async(smem_u32(dst + r * pitch_of(DP) + c), from, ok, kVec);
+    copy_async<kVec>(smem_u32(raw + r * DP + c),
+                     ok ? src + static_cast<int64_t>(n0 + r) * sn + c : src, ok);
   }
 }
 
-// the lane's four values of row r for chunk cc of a product over d
-template <int DP>
-__device__ __forceinline__ float4 row4(const float* m, int r, int cc, int t) {
-  return *reinterpret_cast<const float4*>(m + r * pitch_of(DP) + 32 * (cc >> 1) + 8 * t +
-                                          4 * (cc & 1));
-}
-// the lane's four values of row r for half u of a product over rows
-template <int DP>
-__device__ __forceinline__ float4 col4(const float* m, int r, int u, int g) {
-  return *reinterpret_cast<const float4*>(m + r * pitch_of(DP) + 32 * u + 4 * g);
+// ---- scales: powers of two, the largest value goes to 2^13 .. 2^14 (below 2^-112 to less)
+struct Scale {
+  float mul, inv;
+};
+__device__ __forceinline__ Scale scale_for(uint32_t top) {  // the bits of the largest |value|
+  const int e = max(static_cast<int>(top >> 23), 15);       // its exponent, plus 127
+  return {__uint_as_float(static_cast<uint32_t>(267 - e) << 23),
+          __uint_as_float(static_cast<uint32_t>(e - 13) << 23)};
 }
 
-template <int N>
-__device__ __forceinline__ void add_up(float (&d)[N][4], const float (&hi)[N][4],
-                                       const float (&lo)[N][4]) {
-#pragma unroll
-  for (int n = 0; n < N; ++n)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) d[n][i] = hi[n][i] + lo[n][i];
+// ---- a tile of fp32 values -> two fp16 terms
+// The halves of unit u (8 values) of row r, in [rows][DP]: units of odd rows are swapped by 4.
+template <int DP>
+__device__ __forceinline__ int unit_at(int r, int u) {
+  return r * (DP / 8) + (u ^ ((r & 1) << 2));
+}
+template <int DP>
+__host__ __device__ constexpr int pair_pitch() {
+  return DP + 8;  // words
+}
+template <int DP>
+__host__ __device__ constexpr int rows_bytes(int rows) {
+  return 2 * rows * DP * 2;  // hi, then lo
+}
+template <int DP>
+__host__ __device__ constexpr int pairs_bytes() {
+  return 2 * kTile / 2 * pair_pitch<DP>() * 4;
 }
 
-// s[n] = A B^T over d: A's rows a_row + g, + 8; B's rows 8 n + g
-template <int DP, int NT>
-__device__ __forceinline__ void product_d(float (&s)[NT][4], const float* A, int a_row,
-                                          const float* B, int g, int t) {
-  float hi[NT][4] = {}, lo[NT][4] = {};
+// This thread's share of a raw tile: two rows x four columns per item.
+template <int DP>
+struct Share {
+  static constexpr int kItems = kTile / 2 * (DP / 4) / kThreads;
+  float4 a[kItems], b[kItems];
+  __device__ __forceinline__ static int pair(int i) { return (i * kThreads + threadIdx.x) / (DP / 4); }
+  __device__ __forceinline__ static int col(int i) {
+    return (i * kThreads + threadIdx.x) % (DP / 4) * 4;
+  }
+  // reads the share; the bits of its largest |value|
+  __device__ __forceinline__ uint32_t read(const float* raw) {
+    float m = 0.f;
 #pragma unroll
-  for (int cc = 0; cc < DP / 16; ++cc) {
-    const float4 x = row4<DP>(A, a_row + g, cc, t), y = row4<DP>(A, a_row + g + 8, cc, t);
-    const Tf32FragA a0 = frag_a(x.x, y.x, x.y, y.y), a1 = frag_a(x.z, y.z, x.w, y.w);
+    for (int i = 0; i < kItems; ++i) {
+      const float* at = raw + 2 * pair(i) * DP + col(i);
+      a[i] = *reinterpret_cast<const float4*>(at);
+      b[i] = *reinterpret_cast<const float4*>(at + DP);
+      m = fmaxf(fmax3(m, fabsf(a[i].x), fabsf(a[i].y)), fmaxf(fabsf(a[i].z), fabsf(a[i].w)));
+      m = fmaxf(fmax3(m, fabsf(b[i].x), fabsf(b[i].y)), fmaxf(fabsf(b[i].z), fabsf(b[i].w)));
+    }
+    return __float_as_uint(m);
+  }
+  // writes its terms as rows (at row0 of an array of `rows`) and as pairs, either may be null
+  __device__ __forceinline__ void write(float mul, uint8_t* to_rows, int rows, int row0,
+                                        uint32_t* to_pairs) const {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const float4 b = row4<DP>(B, 8 * n + g, cc, t);
-      mma_f32(hi[n], lo[n], a0, b.x, b.y);
-      mma_f32(hi[n], lo[n], a1, b.z, b.w);
+    for (int i = 0; i < kItems; ++i) {
+      const float4 x = make_float4(a[i].x * mul, a[i].y * mul, a[i].z * mul, a[i].w * mul);
+      const float4 y = make_float4(b[i].x * mul, b[i].y * mul, b[i].z * mul, b[i].w * mul);
+      const uint2 xh = make_uint2(pack_half(x.x, x.y), pack_half(x.z, x.w));
+      const uint2 yh = make_uint2(pack_half(y.x, y.y), pack_half(y.z, y.w));
+      const uint2 xl = make_uint2(pack_rest(x.x, x.y, xh.x), pack_rest(x.z, x.w, xh.y));
+      const uint2 yl = make_uint2(pack_rest(y.x, y.y, yh.x), pack_rest(y.z, y.w, yh.y));
+      const int p = pair(i), c = col(i);
+      if (to_rows != nullptr) {
+        const int r = row0 + 2 * p, half = (c & 4) * 2;
+        uint8_t* h0 = to_rows + unit_at<DP>(r, c >> 3) * 16 + half;
+        uint8_t* h1 = to_rows + unit_at<DP>(r + 1, c >> 3) * 16 + half;
+        *reinterpret_cast<uint2*>(h0) = xh;
+        *reinterpret_cast<uint2*>(h1) = yh;
+        *reinterpret_cast<uint2*>(h0 + rows * DP * 2) = xl;
+        *reinterpret_cast<uint2*>(h1 + rows * DP * 2) = yl;
+      }
+      if (to_pairs != nullptr) {
+        auto mix = [](const uint2& u, const uint2& v) {
+          return make_uint4(__byte_perm(u.x, v.x, 0x5410), __byte_perm(u.x, v.x, 0x7632),
+                            __byte_perm(u.y, v.y, 0x5410), __byte_perm(u.y, v.y, 0x7632));
+        };
+        uint32_t* w = to_pairs + p * pair_pitch<DP>() + c;
+        *reinterpret_cast<uint4*>(w) = mix(xh, yh);
+        *reinterpret_cast<uint4*>(w + kTile / 2 * pair_pitch<DP>()) = mix(xl, yl);
+      }
     }
   }
-  add_up(s, hi, lo);
+};
+
+// the largest of all threads' bits, by way of one word per warp (a barrier inside)
+__device__ __forceinline__ uint32_t block_max(uint32_t top, uint32_t* red) {
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = top;
+  __syncthreads();
+  return max(max(red[0], red[1]), max(red[2], red[3]));
 }
 
-// o[4 u + e] += P B over rows: P the fragments of 16 x 8 NT scores, B's rows 8 n + 2 t, + 1
-template <int DP, int NT>
-__device__ __forceinline__ void product_rows(float (&o)[DP / 8][4], const float (&p)[NT][4],
-                                             const float* B, int g, int t) {
+// The CTA's own 64 rows, split as rows; returns the factor that undoes their scale.  raw is scratch.
+template <int DP, bool kVec>
+__device__ __forceinline__ float own_rows(uint8_t* to, float* raw, uint32_t* red, const float* src,
+                                          int64_t sn, int n0, int limit, int d) {
+  Share<DP> s[2];
+  uint32_t top = 0u;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    load_rows<DP, kVec>(raw, src, sn, n0 + i * kTile, limit, d);
+    copy_commit();
+    copy_wait();
+    __syncthreads();
+    top = max(top, s[i].read(raw));
+    __syncthreads();
+  }
+  const Scale f = scale_for(block_max(top, red));
+#pragma unroll
+  for (int i = 0; i < 2; ++i) s[i].write(f.mul, to, kRows, i * kTile, nullptr);
+  __syncthreads();  // red may be used again
+  return f.inv;
+}
+
+// ---- products
+template <int DP>
+__device__ __forceinline__ uint4 unit16(const uint8_t* rows, int r, int u) {
+  return *reinterpret_cast<const uint4*>(rows + unit_at<DP>(r, u) * 16);
+}
+
+// s[n] = A B^T over d: A's rows a_row + g, + 8 of kRows, B's rows 8 n + g of kTile
+template <int DP>
+__device__ __forceinline__ void product_d(float (&s)[kNT][4], const uint8_t* A, int a_row,
+                                          const uint8_t* B, int g, int t) {
+  constexpr int kLoA = kRows * DP * 2, kLoB = kTile * DP * 2;
+  float hi[kNT][4] = {}, lo[kNT][4] = {};
+#pragma unroll
+  for (int h = 0; h < DP / 32; ++h) {
+    const uint4 x = unit16<DP>(A, a_row + g, t + 4 * h), y = unit16<DP>(A, a_row + g + 8, t + 4 * h);
+    const uint4 xl = unit16<DP>(A + kLoA, a_row + g, t + 4 * h);
+    const uint4 yl = unit16<DP>(A + kLoA, a_row + g + 8, t + 4 * h);
+    const uint32_t a0[4] = {x.x, y.x, x.y, y.y}, a1[4] = {x.z, y.z, x.w, y.w};
+    const uint32_t l0[4] = {xl.x, yl.x, xl.y, yl.y}, l1[4] = {xl.z, yl.z, xl.w, yl.w};
+#pragma unroll
+    for (int n = 0; n < kNT; ++n) {
+      const uint4 b = unit16<DP>(B, 8 * n + g, t + 4 * h);
+      const uint4 bl = unit16<DP>(B + kLoB, 8 * n + g, t + 4 * h);
+      mma16816(lo[n], l0, b.x, b.y);
+      mma16816(lo[n], a0, bl.x, bl.y);
+      mma16816(hi[n], a0, b.x, b.y);
+      mma16816(lo[n], l1, b.z, b.w);
+      mma16816(lo[n], a1, bl.z, bl.w);
+      mma16816(hi[n], a1, b.z, b.w);
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < kNT; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[n][i] = hi[n][i] + lo[n][i];
+}
+
+// the fragments of 16 x 32 scores, times mul, as the operand of a product over rows
+struct ScoreFrags {
+  uint32_t hi[kNT / 2][4], lo[kNT / 2][4];
+  __device__ __forceinline__ ScoreFrags(const float (&p)[kNT][4], float mul) {
+#pragma unroll
+    for (int s = 0; s < kNT / 2; ++s)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // (g, 2 t), (g + 8, 2 t), then the next eight columns
+        const float* c = p[2 * s + (i >> 1)];
+        const float x = c[2 * (i & 1)] * mul, y = c[2 * (i & 1) + 1] * mul;
+        hi[s][i] = pack_half(x, y);
+        lo[s][i] = pack_rest(x, y, hi[s][i]);
+      }
+  }
+};
+// the scale for a warp's scores
+__device__ __forceinline__ Scale score_scale(const float (&p)[kNT][4]) {
+  float m = 0.f;
+#pragma unroll
+  for (int n = 0; n < kNT; ++n)
+    m = fmaxf(fmax3(m, fabsf(p[n][0]), fabsf(p[n][1])), fmaxf(fabsf(p[n][2]), fabsf(p[n][3])));
+  return scale_for(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+}
+
+// o[4 u + e] += inv * P B over the tile's rows (B as pairs)
+template <int DP>
+__device__ __forceinline__ void product_rows(float (&o)[DP / 8][4], const ScoreFrags& p,
+                                             const uint32_t* B, float inv, int g, int t) {
+  constexpr int kP = pair_pitch<DP>(), kLo = kTile / 2 * kP;
 #pragma unroll
   for (int u = 0; u < DP / 32; ++u) {
     float hi[4][4] = {}, lo[4][4] = {};
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const Tf32FragA a = frag_a(p[n][0], p[n][2], p[n][1], p[n][3]);
-      const float4 x = col4<DP>(B, 8 * n + 2 * t, u, g), y = col4<DP>(B, 8 * n + 2 * t + 1, u, g);
-      mma_f32(hi[0], lo[0], a, x.x, y.x);
-      mma_f32(hi[1], lo[1], a, x.y, y.y);
-      mma_f32(hi[2], lo[2], a, x.z, y.z);
-      mma_f32(hi[3], lo[3], a, x.w, y.w);
+    for (int s = 0; s < kNT / 2; ++s) {
+      const uint32_t* at = B + (8 * s + t) * kP + 32 * u + 4 * g;
+      const uint4 b0 = *reinterpret_cast<const uint4*>(at);
+      const uint4 b1 = *reinterpret_cast<const uint4*>(at + 4 * kP);
+      const uint4 l0 = *reinterpret_cast<const uint4*>(at + kLo);
+      const uint4 l1 = *reinterpret_cast<const uint4*>(at + kLo + 4 * kP);
+      const uint32_t x0[4] = {b0.x, b0.y, b0.z, b0.w}, x1[4] = {b1.x, b1.y, b1.z, b1.w};
+      const uint32_t y0[4] = {l0.x, l0.y, l0.z, l0.w}, y1[4] = {l1.x, l1.y, l1.z, l1.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        mma16816(lo[e], p.lo[s], x0[e], x1[e]);
+        mma16816(lo[e], p.hi[s], y0[e], y1[e]);
+        mma16816(hi[e], p.hi[s], x0[e], x1[e]);
+      }
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[4 * u + e][i] += hi[e][i] + lo[e][i];
+      for (int i = 0; i < 4; ++i) o[4 * u + e][i] = fmaf(hi[e][i] + lo[e][i], inv, o[4 * u + e][i]);
   }
 }
 
@@ -174,56 +325,41 @@ __device__ __forceinline__ int keys_of(const RelF32& p, int b) {
 
 // ============================================================================ forward
 template <int DP>
-__host__ __device__ constexpr int fwd_smem() {
-  return (4 * kFwdKeys * pitch_of(DP) + kRows + kFwdKeys) * 4 +
-         static_cast<int>(sizeof(RelShared));
-}
+struct FwdSmem {
+  uint8_t Q[rows_bytes<DP>(kRows)], K[rows_bytes<DP>(kTile)];
+  uint32_t V[pairs_bytes<DP>() / 4];
+  float rawK[kTile * DP], rawV[kTile * DP];
+  float table[kDist + 1];
+  uint32_t red[2][kWarps];
+  RelShared rs;
+};
 
-// One CTA per 64 queries of a head; K and V in steps of 32 keys, the next step's
-// copies in flight while one is computed.
+// One CTA per 64 queries of a head.
 template <int DP, bool kVec>
 __global__ void __launch_bounds__(kThreads, DP == 64 ? 3 : 2)
     sdpa_rel_f32_kernel(const RelF32 p, const __grid_constant__ RelBias rel) {
   pdl_launch_dependents();
   pdl_wait();  // the previous kernel's output is complete from here on
-  constexpr int kK = kFwdKeys, kNT = kK / 8, kP = pitch_of(DP);
-  extern __shared__ float smem[];
-  float* sK = smem;                       // [2][kK][kP]
-  float* sV = sK + 2 * kK * kP;           // [2][kK][kP]
-  float* table = sV + 2 * kK * kP;        // bias of distance d0 + e at e
-  RelShared& rs = *reinterpret_cast<RelShared*>(table + kRows + kK);
+  extern __shared__ __align__(16) uint8_t smem[];
+  FwdSmem<DP>& sm = *reinterpret_cast<FwdSmem<DP>*>(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int h = blockIdx.y, b = blockIdx.z;
   const int q0 = (p.mask == 1 ? static_cast<int>(gridDim.x - 1 - blockIdx.x)  // longest first
                               : static_cast<int>(blockIdx.x)) * kRows;
   const int L = keys_of(p, b);
   const int last = min(q0 + kRows, p.Nq) - 1;
-  const int nt = p.mask == 1 ? last / kK + 1 : (L + kK - 1) / kK;
+  const int nt = p.mask == 1 ? last / kTile + 1 : (L + kTile - 1) / kTile;
   const float* kb = p.K + b * p.st[1][0] + h * p.st[1][1];
   const float* vb = p.V + b * p.st[2][0] + h * p.st[2][1];
   auto load = [&](int j) {
-    load_rows<DP, kVec, kK>(sK + (j & 1) * kK * kP, kb, p.st[1][2], j * kK, L, p.d_k);
-    load_rows<DP, kVec, kK>(sV + (j & 1) * kK * kP, vb, p.st[2][2], j * kK, L, p.d_v);
+    load_rows<DP, kVec>(sm.rawK, kb, p.st[1][2], j * kTile, L, p.d_k);
+    load_rows<DP, kVec>(sm.rawV, vb, p.st[2][2], j * kTile, L, p.d_v);
     copy_commit();
   };
-  for (int s = threadIdx.x; s <= kRelMaxSeg; s += kThreads) rel_load(rs, rel, h, s, 1.f);
-  // Q through the K buffer into registers: the A fragments' values, not yet split
-  float qa[DP / 16][4], qb[DP / 16][4];
-  {
-    const float* qs = p.Q + b * p.st[0][0] + h * p.st[0][1];
-    static_assert(2 * kK >= kRows, "");
-    load_rows<DP, kVec, kRows>(sK, qs, p.st[0][2], q0, p.Nq, p.d_k);
-    copy_commit();
-    copy_wait<0>();
-    __syncthreads();
-#pragma unroll
-    for (int cc = 0; cc < DP / 16; ++cc) {
-      const float4 x = row4<DP>(sK, 16 * warp + g, cc, t), y = row4<DP>(sK, 16 * warp + g + 8, cc, t);
-      qa[cc][0] = x.x; qa[cc][1] = x.y; qa[cc][2] = x.z; qa[cc][3] = x.w;
-      qb[cc][0] = y.x; qb[cc][1] = y.y; qb[cc][2] = y.z; qb[cc][3] = y.w;
-    }
-    __syncthreads();
-  }
+  for (int s = threadIdx.x; s <= kRelMaxSeg; s += kThreads) rel_load(sm.rs, rel, h, s, 1.f);
+  const float q_inv =
+      own_rows<DP, kVec>(sm.Q, sm.rawK, sm.red[0], p.Q + b * p.st[0][0] + h * p.st[0][1], p.st[0][2],
+                         q0, p.Nq, p.d_k) * p.scale;
   const int row[2] = {q0 + 16 * warp + g, q0 + 16 * warp + g + 8};
   const int limit[2] = {p.mask == 1 ? row[0] : L - 1, p.mask == 1 ? row[1] : L - 1};
   float o[DP / 8][4] = {};
@@ -232,46 +368,46 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 3 : 2)
   float seg_bias = 0.f;
   if (nt > 0) load(0);
   for (int j = 0; j < nt; ++j) {
-    if (j + 1 < nt) load(j + 1);
-    const int d0 = j * kK - (q0 + kRows - 1);  // the tile's smallest distance
+    const int d0 = j * kTile - (q0 + kRows - 1);  // the tile's smallest distance
     if (d0 >= seg_next) {
-      const int seg = rel_segment(rs, rel_steps(rel.nseg), d0);
-      seg_next = rs.start[seg + 1];
-      seg_bias = rs.bias[seg];
+      const int seg = rel_segment(sm.rs, rel_steps(rel.nseg), d0);
+      seg_next = sm.rs.start[seg + 1];
+      seg_bias = sm.rs.bias[seg];
     }
-    const bool near = d0 + kRows + kK - 2 >= seg_next;
-    if (near)
-      for (int e = threadIdx.x; e < kRows + kK - 1; e += kThreads)
-        table[e] = rs.bias[rel_segment(rs, rel_steps(rel.nseg), d0 + e)];
-    if (j + 1 < nt)
-      copy_wait<1>();
-    else
-      copy_wait<0>();
+    const bool near = d0 + kDist - 1 >= seg_next;
+    copy_wait();
+    __syncthreads();  // the tile is there, the previous one done with
+    if (near && threadIdx.x < kDist)
+      sm.table[threadIdx.x] =
+          sm.rs.bias[rel_segment(sm.rs, rel_steps(rel.nseg), d0 + threadIdx.x)];
+    float k_inv, v_inv;
+    {
+      Share<DP> k, v;
+      const uint32_t tk = __reduce_max_sync(0xffffffffu, k.read(sm.rawK));
+      const uint32_t tv = block_max(v.read(sm.rawV), (sm.red[1][warp] = tk, sm.red[0]));
+      const Scale fk = scale_for(max(max(sm.red[1][0], sm.red[1][1]),
+                                     max(sm.red[1][2], sm.red[1][3])));
+      const Scale fv = scale_for(tv);
+      k.write(fk.mul, sm.K, kTile, 0, nullptr);
+      v.write(fv.mul, nullptr, 0, 0, sm.V);
+      k_inv = fk.inv;
+      v_inv = fv.inv;
+    }
     __syncthreads();
-    if (p.mask != 1 || j * kK <= q0 + 16 * warp + 15) {
-      const float* k = sK + (j & 1) * kK * kP;
-      const float* v = sV + (j & 1) * kK * kP;
-      float s[kNT][4], hi[kNT][4] = {}, lo[kNT][4] = {};
-#pragma unroll
-      for (int cc = 0; cc < DP / 16; ++cc) {
-        const Tf32FragA a0 = frag_a(qa[cc][0], qb[cc][0], qa[cc][1], qb[cc][1]);
-        const Tf32FragA a1 = frag_a(qa[cc][2], qb[cc][2], qa[cc][3], qb[cc][3]);
-#pragma unroll
-        for (int n = 0; n < kNT; ++n) {
-          const float4 x = row4<DP>(k, 8 * n + g, cc, t);
-          mma_f32(hi[n], lo[n], a0, x.x, x.y);
-          mma_f32(hi[n], lo[n], a1, x.z, x.w);
-        }
-      }
-      add_up(s, hi, lo);
+    if (j + 1 < nt) load(j + 1);
+    if (p.mask != 1 || j * kTile <= q0 + 16 * warp + 15) {
+      float s[kNT][4];
+      product_d<DP>(s, sm.Q, 16 * warp, sm.K, g, t);
+      const float f = k_inv * q_inv;
       float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
       for (int n = 0; n < kNT; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int c = 8 * n + 2 * t + (i & 1);  // the tile's key
-          const float bias = near ? table[c - (16 * warp + g + 8 * (i >> 1)) + kRows - 1] : seg_bias;
-          s[n][i] = j * kK + c <= limit[i >> 1] ? fmaf(s[n][i], p.scale, bias) : -INFINITY;
+          const float bias =
+              near ? sm.table[c - (16 * warp + g + 8 * (i >> 1)) + kRows - 1] : seg_bias;
+          s[n][i] = j * kTile + c <= limit[i >> 1] ? fmaf(s[n][i], f, bias) : -INFINITY;
           mx[i >> 1] = fmaxf(mx[i >> 1], s[n][i]);
         }
       float alpha[2], ref[2];
@@ -298,9 +434,8 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 3 : 2)
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[u][i] *= alpha[i >> 1];
       }
-      product_rows<DP, kNT>(o, s, v, g, t);
+      product_rows<DP>(o, ScoreFrags(s, 0x1p14f), sm.V, v_inv * 0x1p-14f, g, t);
     }
-    __syncthreads();  // this step's buffers and table may be written again
   }
   float* ob = p.out + b * p.st[3][0] + h * p.st[3][1];
 #pragma unroll
@@ -318,70 +453,79 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 3 : 2)
 }
 
 // ============================================================================ backward
-// dS of one step's element: p = exp(s scale + bias - lse), 0 where the pair is not allowed
-__device__ __forceinline__ float weight(float s, float scale, float bias, float lse, bool ok) {
-  return ok ? ex2_approx(fmaf(s, scale, bias - lse) * kLog2e) : 0.f;
+// p = exp(x - lse), x = s f + bias; 0 where the pair is not allowed
+__device__ __forceinline__ float weight(float s, float f, float bias, float lse, bool ok) {
+  return ok ? ex2_approx(fmaf(s, f, bias - lse) * kLog2e) : 0.f;
 }
 
 template <int DP>
-__host__ __device__ constexpr int dq_smem() {
-  return ((2 * kRows + 2 * kBwdRows) * pitch_of(DP) + kRows * (kBwdRows + 1) + 2 * kRows + 96 +
-          96 + 4) * 4 + static_cast<int>(sizeof(RelShared));
-}
+struct DqSmem {
+  uint8_t Q[rows_bytes<DP>(kRows)], G[rows_bytes<DP>(kRows)];  // G: dO
+  uint32_t Kp[pairs_bytes<DP>() / 4];
+  union {
+    struct {
+      uint8_t K[rows_bytes<DP>(kTile)], V[rows_bytes<DP>(kTile)];
+    };
+    float S[kRows * (kTile + 1)];  // dS where segments meet, when K and V are done with
+  };
+  float rawK[kTile * DP], rawV[kTile * DP];
+  float D[kRows], lse[kRows];
+  float table[kDist + 1], diag[kDist + 1];
+  uint32_t red[2][kWarps];
+  float far[kWarps];
+  RelShared rs;
+};
 
 // One CTA per 64 queries: D, dQ and the tile's sums of dS per segment (thread s owns segment s).
 template <int DP, bool kVec>
-__global__ void __launch_bounds__(kThreads, DP == 64 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
     sdpa_rel_dq_f32_kernel(const RelF32 p, const __grid_constant__ RelBias rel) {
   pdl_launch_dependents();
   pdl_wait();  // the previous kernel's output is complete from here on
-  constexpr int kP = pitch_of(DP), kNT = kBwdRows / 8, kDist = kRows + kBwdRows - 1;
-  extern __shared__ float smem[];
-  float* sQ = smem;                              // [64][kP]
-  float* sG = sQ + kRows * kP;                   // [64][kP]: dO
-  float* sK = sG + kRows * kP;                   // [32][kP]
-  float* sV = sK + kBwdRows * kP;                // [32][kP]
-  float* sS = sV + kBwdRows * kP;                // [64][33]: dS where segments meet
-  float* sD = sS + kRows * (kBwdRows + 1);       // [64]: D
-  float* sL = sD + kRows;                        // [64]: lse
-  float* table = sL + kRows;                     // [95]
-  float* diag = table + 96;                      // [95]: sums over the diagonals
-  float* red = diag + 96;                        // [4]
-  RelShared& rs = *reinterpret_cast<RelShared*>(red + 4);
+  extern __shared__ __align__(16) uint8_t smem[];
+  DqSmem<DP>& sm = *reinterpret_cast<DqSmem<DP>*>(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int h = blockIdx.y, b = blockIdx.z;
   const int q0 = (p.mask == 1 ? static_cast<int>(gridDim.x - 1 - blockIdx.x)
                               : static_cast<int>(blockIdx.x)) * kRows;
   const int L = keys_of(p, b);
   const int last = min(q0 + kRows, p.Nq) - 1;
-  const int nt = p.mask == 1 ? last / kBwdRows + 1 : (L + kBwdRows - 1) / kBwdRows;
+  const int nt = p.mask == 1 ? last / kTile + 1 : (L + kTile - 1) / kTile;
   const int64_t bh = static_cast<int64_t>(b) * p.H + h;
   const float* kb = p.K + b * p.st[1][0] + h * p.st[1][1];
   const float* vb = p.V + b * p.st[2][0] + h * p.st[2][1];
-  load_rows<DP, kVec, kRows>(sQ, p.Q + b * p.st[0][0] + h * p.st[0][1], p.st[0][2], q0, p.Nq,
-                             p.d_k);
-  load_rows<DP, kVec, kRows>(sG, p.dO + b * p.st[4][0] + h * p.st[4][1], p.st[4][2], q0, p.Nq,
-                             p.d_v);
-  copy_commit();
-  for (int s = tid; s <= kRelMaxSeg; s += kThreads) rel_load(rs, rel, h, s, 1.f);
-  copy_wait<0>();
-  __syncthreads();
-  {  // two threads to a row
+  const float* gb = p.dO + b * p.st[4][0] + h * p.st[4][1];
+  auto load = [&](int j) {
+    load_rows<DP, kVec>(sm.rawK, kb, p.st[1][2], j * kTile, L, p.d_k);
+    load_rows<DP, kVec>(sm.rawV, vb, p.st[2][2], j * kTile, L, p.d_v);
+    copy_commit();
+  };
+  for (int s = tid; s <= kRelMaxSeg; s += kThreads) rel_load(sm.rs, rel, h, s, 1.f);
+  {  // D, two threads to a row
     const int r = tid >> 1;
-    const float* orow = p.O + b * p.st[3][0] + h * p.st[3][1] +
-                        static_cast<int64_t>(q0 + r) * p.st[3][2];
+    const bool live = q0 + r < p.Nq;
     float acc = 0.f;
-    if (q0 + r < p.Nq)
-      for (int d = tid & 1; d < p.d_v; d += 2) acc = fmaf(sG[r * kP + d], orow[d], acc);
+    if (live) {
+      const float* orow = p.O + b * p.st[3][0] + h * p.st[3][1] +
+                          static_cast<int64_t>(q0 + r) * p.st[3][2];
+      const float* grow = gb + static_cast<int64_t>(q0 + r) * p.st[4][2];
+      for (int d = tid & 1; d < p.d_v; d += 2) acc = fmaf(grow[d], orow[d], acc);
+    }
     acc += __shfl_xor_sync(0xffffffffu, acc, 1);
     if ((tid & 1) == 0) {
-      sD[r] = acc;
-      sL[r] = q0 + r < p.Nq ? p.lse[bh * p.Nq + q0 + r] : INFINITY;
-      if (q0 + r < p.Nq) p.Dv[bh * p.Nq + q0 + r] = acc;
+      sm.D[r] = acc;
+      sm.lse[r] = live ? p.lse[bh * p.Nq + q0 + r] : INFINITY;
+      if (live) p.Dv[bh * p.Nq + q0 + r] = acc;
     }
   }
+  const float q_inv =
+      own_rows<DP, kVec>(sm.Q, sm.rawK, sm.red[0], p.Q + b * p.st[0][0] + h * p.st[0][1], p.st[0][2],
+                         q0, p.Nq, p.d_k) * p.scale;
+  const float g_inv =
+      own_rows<DP, kVec>(sm.G, sm.rawK, sm.red[0], gb, p.st[4][2], q0, p.Nq, p.d_v);
   const int r_loc[2] = {16 * warp + g, 16 * warp + g + 8};
   const int limit[2] = {p.mask == 1 ? q0 + r_loc[0] : L - 1, p.mask == 1 ? q0 + r_loc[1] : L - 1};
+  const float lse[2] = {sm.lse[r_loc[0]], sm.lse[r_loc[1]]}, D[2] = {sm.D[r_loc[0]], sm.D[r_loc[1]]};
   float dq[DP / 8][4] = {};
   float far = 0.f, own = 0.f;
   int seg = 0, seg_next = INT_MIN;
@@ -389,57 +533,74 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 3 : 2)
   auto flush_far = [&]() {  // by all threads
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) far += __shfl_xor_sync(0xffffffffu, far, off);
-    if (lane == 0) red[warp] = far;
+    if (lane == 0) sm.far[warp] = far;
     far = 0.f;
     __syncthreads();
-    if (tid == seg) own += (red[0] + red[1]) + (red[2] + red[3]);
+    if (tid == seg) own += (sm.far[0] + sm.far[1]) + (sm.far[2] + sm.far[3]);
     __syncthreads();
   };
+  if (nt > 0) load(0);
   for (int j = 0; j < nt; ++j) {
-    __syncthreads();  // the previous step is done with the buffers
-    load_rows<DP, kVec, kBwdRows>(sK, kb, p.st[1][2], j * kBwdRows, L, p.d_k);
-    load_rows<DP, kVec, kBwdRows>(sV, vb, p.st[2][2], j * kBwdRows, L, p.d_v);
-    copy_commit();
-    const int d0 = j * kBwdRows - (q0 + kRows - 1);
+    const int d0 = j * kTile - (q0 + kRows - 1);
     if (d0 >= seg_next || (j & 63) == 0) {
-      if (j > 0) flush_far();  // also every 64 steps, which bounds the length of a sum
-      seg = rel_segment(rs, rel_steps(rel.nseg), d0);
-      seg_next = rs.start[seg + 1];
-      seg_bias = rs.bias[seg];
+      if (j > 0) flush_far();  // also every 64 tiles, which bounds the length of a sum
+      seg = rel_segment(sm.rs, rel_steps(rel.nseg), d0);
+      seg_next = sm.rs.start[seg + 1];
+      seg_bias = sm.rs.bias[seg];
     }
     const bool near = d0 + kDist - 1 >= seg_next;
-    if (near && tid < kDist) table[tid] = rs.bias[rel_segment(rs, rel_steps(rel.nseg), d0 + tid)];
-    copy_wait<0>();
+    copy_wait();
+    __syncthreads();  // the tile is there, the previous one done with
+    if (near && tid < kDist)
+      sm.table[tid] = sm.rs.bias[rel_segment(sm.rs, rel_steps(rel.nseg), d0 + tid)];
+    float k_inv, v_inv;
+    {
+      Share<DP> k, v;
+      const uint32_t tk = __reduce_max_sync(0xffffffffu, k.read(sm.rawK));
+      const uint32_t tv = block_max(v.read(sm.rawV), (sm.red[1][warp] = tk, sm.red[0]));
+      const Scale fk = scale_for(max(max(sm.red[1][0], sm.red[1][1]),
+                                     max(sm.red[1][2], sm.red[1][3])));
+      const Scale fv = scale_for(tv);
+      k.write(fk.mul, sm.K, kTile, 0, sm.Kp);
+      v.write(fv.mul, sm.V, kTile, 0, nullptr);
+      k_inv = fk.inv;
+      v_inv = fv.inv;
+    }
     __syncthreads();
-    const bool skip = p.mask == 1 && j * kBwdRows > q0 + 16 * warp + 15;
+    if (j + 1 < nt) load(j + 1);
+    const bool skip = p.mask == 1 && j * kTile > q0 + 16 * warp + 15;
     float s[kNT][4] = {};
     if (!skip) {
       float dp[kNT][4];
-      product_d<DP, kNT>(s, sQ, 16 * warp, sK, g, t);
-      product_d<DP, kNT>(dp, sG, 16 * warp, sV, g, t);
-      const float lse[2] = {sL[r_loc[0]], sL[r_loc[1]]}, D[2] = {sD[r_loc[0]], sD[r_loc[1]]};
+      product_d<DP>(s, sm.Q, 16 * warp, sm.K, g, t);
+      product_d<DP>(dp, sm.G, 16 * warp, sm.V, g, t);
+      const float f = k_inv * q_inv, fg = v_inv * g_inv;
 #pragma unroll
       for (int n = 0; n < kNT; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int c = 8 * n + 2 * t + (i & 1);
-          const float bias = near ? table[c - r_loc[i >> 1] + kRows - 1] : seg_bias;
-          const float w = weight(s[n][i], p.scale, bias, lse[i >> 1],
-                                 j * kBwdRows + c <= limit[i >> 1]);
-          s[n][i] = w * (dp[n][i] - D[i >> 1]);
+          const float bias = near ? sm.table[c - r_loc[i >> 1] + kRows - 1] : seg_bias;
+          const float w =
+              weight(s[n][i], f, bias, lse[i >> 1], j * kTile + c <= limit[i >> 1]);
+          s[n][i] = w * fmaf(dp[n][i], fg, -D[i >> 1]);
         }
     }
     if (near) {
+      __syncthreads();  // K and V as rows are done with
 #pragma unroll
       for (int n = 0; n < kNT; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          sS[r_loc[i >> 1] * (kBwdRows + 1) + 8 * n + 2 * t + (i & 1)] = s[n][i];
+          sm.S[r_loc[i >> 1] * (kTile + 1) + 8 * n + 2 * t + (i & 1)] = s[n][i];
     } else {
 #pragma unroll
       for (int n = 0; n < kNT; ++n) far += (s[n][0] + s[n][1]) + (s[n][2] + s[n][3]);
     }
-    if (!skip) product_rows<DP, kNT>(dq, s, sK, g, t);
+    if (!skip) {
+      const Scale f = score_scale(s);
+      product_rows<DP>(dq, ScoreFrags(s, f.mul), sm.Kp, f.inv * k_inv, g, t);
+    }
     if (near) {  // sums over the diagonals, then over each segment's diagonals
       __syncthreads();
       if (tid < kDist) {
@@ -447,15 +608,16 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 3 : 2)
 #pragma unroll 8
         for (int r = 0; r < kRows; ++r) {
           const int c = r + tid - (kRows - 1);
-          if (c >= 0 && c < kBwdRows) acc += sS[r * (kBwdRows + 1) + c];
+          if (c >= 0 && c < kTile) acc += sm.S[r * (kTile + 1) + c];
         }
-        diag[tid] = acc;
+        sm.diag[tid] = acc;
       }
       __syncthreads();
       if (tid < rel.nseg) {
-        const int lo = rs.start[tid] <= d0 ? 0 : min(rs.start[tid] - d0, kDist);
-        const int hi = rs.start[tid + 1] > d0 + kDist - 1 ? kDist - 1 : rs.start[tid + 1] - 1 - d0;
-        for (int e = lo; e <= hi; ++e) own += diag[e];
+        const int lo = sm.rs.start[tid] <= d0 ? 0 : min(sm.rs.start[tid] - d0, kDist);
+        const int hi = sm.rs.start[tid + 1] > d0 + kDist - 1 ? kDist - 1
+                                                             : sm.rs.start[tid + 1] - 1 - d0;
+        for (int e = lo; e <= hi; ++e) own += sm.diag[e];
       }
     }
   }
@@ -473,80 +635,102 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 3 : 2)
 }
 
 template <int DP>
-__host__ __device__ constexpr int dkdv_smem() {
-  return ((2 * kRows + 2 * kBwdRows) * pitch_of(DP) + 2 * kBwdRows + 96) * 4 +
-         static_cast<int>(sizeof(RelShared));
-}
+struct DkdvSmem {
+  uint8_t K[rows_bytes<DP>(kRows)], V[rows_bytes<DP>(kRows)];
+  uint8_t Q[rows_bytes<DP>(kTile)], G[rows_bytes<DP>(kTile)];  // G: dO
+  uint32_t Qp[pairs_bytes<DP>() / 4], Gp[pairs_bytes<DP>() / 4];
+  float rawQ[kTile * DP], rawG[kTile * DP];
+  float D[kTile], lse[kTile];
+  float table[kDist + 1];
+  uint32_t red[2][kWarps];
+  RelShared rs;
+};
 
-// One CTA per 64 keys: dK and dV from steps of 32 queries (after the dq kernel, which leaves D).
+// One CTA per 64 keys: dK and dV from tiles of 32 queries (after the dq kernel, which leaves D).
 template <int DP, bool kVec>
-__global__ void __launch_bounds__(kThreads, DP == 64 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
     sdpa_rel_dkdv_f32_kernel(const RelF32 p, const __grid_constant__ RelBias rel) {
   pdl_launch_dependents();
   pdl_wait();  // the previous kernel's output is complete from here on
-  constexpr int kP = pitch_of(DP), kNT = kBwdRows / 8, kDist = kRows + kBwdRows - 1;
-  extern __shared__ float smem[];
-  float* sK = smem;                   // [64][kP]
-  float* sV = sK + kRows * kP;        // [64][kP]
-  float* sQ = sV + kRows * kP;        // [32][kP]
-  float* sG = sQ + kBwdRows * kP;     // [32][kP]: dO
-  float* sD = sG + kBwdRows * kP;     // [32]
-  float* sL = sD + kBwdRows;          // [32]
-  float* table = sL + kBwdRows;       // [95]
-  RelShared& rs = *reinterpret_cast<RelShared*>(table + 96);
+  extern __shared__ __align__(16) uint8_t smem[];
+  DkdvSmem<DP>& sm = *reinterpret_cast<DkdvSmem<DP>*>(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int h = blockIdx.y, b = blockIdx.z, k0 = static_cast<int>(blockIdx.x) * kRows;
   const int L = keys_of(p, b);
   const int64_t bh = static_cast<int64_t>(b) * p.H + h;
   const float* qb = p.Q + b * p.st[0][0] + h * p.st[0][1];
   const float* gb = p.dO + b * p.st[4][0] + h * p.st[4][1];
-  const int i0 = p.mask == 1 ? k0 / kBwdRows : 0;  // the first query step that sees a key
-  const int ni = k0 < L ? (p.Nq + kBwdRows - 1) / kBwdRows : 0;
-  load_rows<DP, kVec, kRows>(sK, p.K + b * p.st[1][0] + h * p.st[1][1], p.st[1][2], k0, L, p.d_k);
-  load_rows<DP, kVec, kRows>(sV, p.V + b * p.st[2][0] + h * p.st[2][1], p.st[2][2], k0, L, p.d_v);
-  copy_commit();
-  for (int s = tid; s <= kRelMaxSeg; s += kThreads) rel_load(rs, rel, h, s, 1.f);
+  const int i0 = p.mask == 1 ? k0 / kTile : 0;  // the first tile of queries that sees a key
+  const int ni = k0 < L ? (p.Nq + kTile - 1) / kTile : 0;
   const int key[2] = {k0 + 16 * warp + g, k0 + 16 * warp + g + 8};
   float dk[DP / 8][4] = {}, dv[DP / 8][4] = {};
-  int seg_start = INT_MAX;
-  float seg_bias = 0.f;
-  for (int i = i0; i < ni; ++i) {
-    __syncthreads();  // the previous step is done with the buffers (the first: rs is there)
-    const int q0 = i * kBwdRows;
-    load_rows<DP, kVec, kBwdRows>(sQ, qb, p.st[0][2], q0, p.Nq, p.d_k);
-    load_rows<DP, kVec, kBwdRows>(sG, gb, p.st[4][2], q0, p.Nq, p.d_v);
-    copy_commit();
-    if (tid < kBwdRows) {
-      sD[tid] = q0 + tid < p.Nq ? p.Dv[bh * p.Nq + q0 + tid] : 0.f;
-      sL[tid] = q0 + tid < p.Nq ? p.lse[bh * p.Nq + q0 + tid] : INFINITY;
-    }
-    const int d0 = k0 - (q0 + kBwdRows - 1);  // distances d0 + e, e = key row + 31 - query
-    if (d0 + kDist - 1 < seg_start) {
-      const int seg = rel_segment(rs, rel_steps(rel.nseg), d0 + kDist - 1);
-      seg_start = rs.start[seg];
-      seg_bias = rs.bias[seg];
-    }
-    const bool near = d0 < seg_start;
-    if (near && tid < kDist) table[tid] = rs.bias[rel_segment(rs, rel_steps(rel.nseg), d0 + tid)];
-    copy_wait<0>();
-    __syncthreads();
-    float s[kNT][4], ds[kNT][4];
-    product_d<DP, kNT>(s, sK, 16 * warp, sQ, g, t);
-    product_d<DP, kNT>(ds, sV, 16 * warp, sG, g, t);
-#pragma unroll
-    for (int n = 0; n < kNT; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int c = 8 * n + 2 * t + (e & 1), j = key[e >> 1];
-        const float bias = near ? table[j - k0 - c + kBwdRows - 1] : seg_bias;
-        const bool ok = j < L && (p.mask != 1 || j <= q0 + c);
-        s[n][e] = weight(s[n][e], p.scale, bias, sL[c], ok);
-        ds[n][e] = s[n][e] * (ds[n][e] - sD[c]);
+  if (i0 < ni) {
+    auto load = [&](int i) {
+      load_rows<DP, kVec>(sm.rawQ, qb, p.st[0][2], i * kTile, p.Nq, p.d_k);
+      load_rows<DP, kVec>(sm.rawG, gb, p.st[4][2], i * kTile, p.Nq, p.d_v);
+      copy_commit();
+    };
+    for (int s = tid; s <= kRelMaxSeg; s += kThreads) rel_load(sm.rs, rel, h, s, 1.f);
+    const float k_inv =
+        own_rows<DP, kVec>(sm.K, sm.rawQ, sm.red[0], p.K + b * p.st[1][0] + h * p.st[1][1],
+                           p.st[1][2], k0, L, p.d_k) * p.scale;
+    const float v_inv =
+        own_rows<DP, kVec>(sm.V, sm.rawQ, sm.red[0], p.V + b * p.st[2][0] + h * p.st[2][1],
+                           p.st[2][2], k0, L, p.d_v);
+    int seg_start = INT_MAX;
+    float seg_bias = 0.f;
+    load(i0);
+    for (int i = i0; i < ni; ++i) {
+      const int q0 = i * kTile;
+      const int d0 = k0 - (q0 + kTile - 1);  // distances d0 + e, e = key row + 31 - query
+      if (d0 + kDist - 1 < seg_start) {
+        const int seg = rel_segment(sm.rs, rel_steps(rel.nseg), d0 + kDist - 1);
+        seg_start = sm.rs.start[seg];
+        seg_bias = sm.rs.bias[seg];
       }
-    product_rows<DP, kNT>(dv, s, sG, g, t);
-    product_rows<DP, kNT>(dk, ds, sQ, g, t);
+      const bool near = d0 < seg_start;
+      copy_wait();
+      __syncthreads();  // the tile is there, the previous one done with
+      if (tid < kTile) {
+        sm.D[tid] = q0 + tid < p.Nq ? p.Dv[bh * p.Nq + q0 + tid] : 0.f;
+        sm.lse[tid] = q0 + tid < p.Nq ? p.lse[bh * p.Nq + q0 + tid] : INFINITY;
+      }
+      if (near && tid < kDist)
+        sm.table[tid] = sm.rs.bias[rel_segment(sm.rs, rel_steps(rel.nseg), d0 + tid)];
+      float q_inv, g_inv;
+      {
+        Share<DP> q, o;
+        const uint32_t tq = __reduce_max_sync(0xffffffffu, q.read(sm.rawQ));
+        const uint32_t tg = block_max(o.read(sm.rawG), (sm.red[1][warp] = tq, sm.red[0]));
+        const Scale fq = scale_for(max(max(sm.red[1][0], sm.red[1][1]),
+                                       max(sm.red[1][2], sm.red[1][3])));
+        const Scale fg = scale_for(tg);
+        q.write(fq.mul, sm.Q, kTile, 0, sm.Qp);
+        o.write(fg.mul, sm.G, kTile, 0, sm.Gp);
+        q_inv = fq.inv;
+        g_inv = fg.inv;
+      }
+      __syncthreads();
+      if (i + 1 < ni) load(i + 1);
+      float s[kNT][4], ds[kNT][4];
+      product_d<DP>(s, sm.K, 16 * warp, sm.Q, g, t);
+      product_d<DP>(ds, sm.V, 16 * warp, sm.G, g, t);
+      const float f = q_inv * k_inv, fg = g_inv * v_inv;
+#pragma unroll
+      for (int n = 0; n < kNT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int c = 8 * n + 2 * t + (e & 1), j = key[e >> 1];
+          const float bias = near ? sm.table[j - k0 - c + kTile - 1] : seg_bias;
+          const bool ok = j < L && (p.mask != 1 || j <= q0 + c);
+          s[n][e] = weight(s[n][e], f, bias, sm.lse[c], ok);
+          ds[n][e] = s[n][e] * fmaf(ds[n][e], fg, -sm.D[c]);
+        }
+      const Scale fs = score_scale(s), fd = score_scale(ds);
+      product_rows<DP>(dv, ScoreFrags(s, fs.mul), sm.Gp, fs.inv * g_inv, g, t);
+      product_rows<DP>(dk, ScoreFrags(ds, fd.mul), sm.Qp, fd.inv * q_inv, g, t);
+    }
   }
-  copy_wait<0>();  // K and V, where no step waited for them
   float* ok = p.dK + b * p.st[6][0] + h * p.st[6][1];
   float* ov = p.dV + b * p.st[7][0] + h * p.st[7][1];
 #pragma unroll
@@ -566,9 +750,10 @@ __global__ void __launch_bounds__(kRelGradThreads)
 }
 
 template <class F>
-cudaError_t go(F* kernel, dim3 grid, int smem, const RelF32& p, const RelBias& rel,
+cudaError_t go(F* kernel, dim3 grid, size_t smem, const RelF32& p, const RelBias& rel,
                cudaStream_t s) {
-  cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(kernel), smem, nullptr);
+  cudaError_t e =
+      prepare_kernel(reinterpret_cast<const void*>(kernel), static_cast<int>(smem), nullptr);
   if (e != cudaSuccess) return e;
   return launch_pdl(kernel, grid, dim3(kThreads), smem, s, p, rel);
 }
@@ -599,10 +784,10 @@ cudaError_t launch_sdpa_rel_f32(const SdpaArgs& a, const RelBias& rel, cudaStrea
                    quads(a.V, p.st[2], a.d_v) && quads(a.O, p.st[3], a.d_v);
   const dim3 grid((a.Nq + kRows - 1) / kRows, a.H, a.B);
   if (a.d_k <= 64 && a.d_v <= 64)
-    return vec ? go(sdpa_rel_f32_kernel<64, true>, grid, fwd_smem<64>(), p, rel, s)
-               : go(sdpa_rel_f32_kernel<64, false>, grid, fwd_smem<64>(), p, rel, s);
-  return vec ? go(sdpa_rel_f32_kernel<128, true>, grid, fwd_smem<128>(), p, rel, s)
-             : go(sdpa_rel_f32_kernel<128, false>, grid, fwd_smem<128>(), p, rel, s);
+    return vec ? go(sdpa_rel_f32_kernel<64, true>, grid, sizeof(FwdSmem<64>), p, rel, s)
+               : go(sdpa_rel_f32_kernel<64, false>, grid, sizeof(FwdSmem<64>), p, rel, s);
+  return vec ? go(sdpa_rel_f32_kernel<128, true>, grid, sizeof(FwdSmem<128>), p, rel, s)
+             : go(sdpa_rel_f32_kernel<128, false>, grid, sizeof(FwdSmem<128>), p, rel, s);
 }
 
 int rel_bwd_tiles(int Nq, int Nk, int dtype) {
@@ -637,18 +822,18 @@ cudaError_t launch_sdpa_rel_bwd_f32(const SdpaBwdArgs& a, const RelBias& rel, vo
   const dim3 gq((a.Nq + kRows - 1) / kRows, a.H, a.B), gk((a.Nk + kRows - 1) / kRows, a.H, a.B);
   cudaError_t e;
   if (small)
-    e = vec ? go(sdpa_rel_dq_f32_kernel<64, true>, gq, dq_smem<64>(), p, rel, s)
-            : go(sdpa_rel_dq_f32_kernel<64, false>, gq, dq_smem<64>(), p, rel, s);
+    e = vec ? go(sdpa_rel_dq_f32_kernel<64, true>, gq, sizeof(DqSmem<64>), p, rel, s)
+            : go(sdpa_rel_dq_f32_kernel<64, false>, gq, sizeof(DqSmem<64>), p, rel, s);
   else
-    e = vec ? go(sdpa_rel_dq_f32_kernel<128, true>, gq, dq_smem<128>(), p, rel, s)
-            : go(sdpa_rel_dq_f32_kernel<128, false>, gq, dq_smem<128>(), p, rel, s);
+    e = vec ? go(sdpa_rel_dq_f32_kernel<128, true>, gq, sizeof(DqSmem<128>), p, rel, s)
+            : go(sdpa_rel_dq_f32_kernel<128, false>, gq, sizeof(DqSmem<128>), p, rel, s);
   if (e != cudaSuccess) return e;
   if (small)
-    e = vec ? go(sdpa_rel_dkdv_f32_kernel<64, true>, gk, dkdv_smem<64>(), p, rel, s)
-            : go(sdpa_rel_dkdv_f32_kernel<64, false>, gk, dkdv_smem<64>(), p, rel, s);
+    e = vec ? go(sdpa_rel_dkdv_f32_kernel<64, true>, gk, sizeof(DkdvSmem<64>), p, rel, s)
+            : go(sdpa_rel_dkdv_f32_kernel<64, false>, gk, sizeof(DkdvSmem<64>), p, rel, s);
   else
-    e = vec ? go(sdpa_rel_dkdv_f32_kernel<128, true>, gk, dkdv_smem<128>(), p, rel, s)
-            : go(sdpa_rel_dkdv_f32_kernel<128, false>, gk, dkdv_smem<128>(), p, rel, s);
+    e = vec ? go(sdpa_rel_dkdv_f32_kernel<128, true>, gk, sizeof(DkdvSmem<128>), p, rel, s)
+            : go(sdpa_rel_dkdv_f32_kernel<128, false>, gk, sizeof(DkdvSmem<128>), p, rel, s);
   return e == cudaSuccess ? launch_rel_table_grad(rel, dtable, a.B, rel_bwd_tiles(a.Nq, a.Nk, 0), s)
                           : e;
 }
