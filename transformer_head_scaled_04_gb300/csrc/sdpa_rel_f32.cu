@@ -71,22 +71,34 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const float* src, bool 
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
-// rows n0 .. n0 + kTile - 1 of a [N, d] matrix with row stride sn into raw [kTile][DP]; rows from
-// `limit` on and columns from d on become zeros (nothing of them is read)
+// This thread's part of copying tiles of rows of a [N, d] matrix with row stride sn into raw
+// [kTile][DP]: rows from `limit` on and columns from d on become zeros (nothing of them is read).
 template <int DP, bool kVec>
-__device__ __forceinline__ void load_rows(float* raw, const float* src, int64_t sn, int n0,
-                                          int limit, int d) {
-  constexpr int kUnit = kVec ? 4 : 1, kPer = DP / kUnit;
-  static_assert(kTile * kPer % kThreads == 0, "");
-#pragma unroll 4
-  for (int i = 0; i < kTile * kPer / kThreads; ++i) {
-    const int e = i * kThreads + threadIdx.x;
-    const int r = e / kPer, c = e % kPer * kUnit;
-    const bool ok = n0 + r < limit && c < d;
-    copy_async<kVec>(smem_u32(raw + r * DP + c),
-                     ok ? src + static_cast<int64_t>(n0 + r) * sn + c : src, ok);
+struct TileCopy {
+  static constexpr int kUnit = kVec ? 4 : 1, kPer = DP / kUnit;
+  static constexpr int kStep = kThreads / kPer;  // rows between a thread's copies (kPer <= kThreads)
+  static_assert(kThreads % kPer == 0 && kTile % kStep == 0, "");
+  const float* src;  // the thread's column of row 0
+  int64_t sn;
+  int limit;         // 0 where the column lies past d
+  __device__ __forceinline__ TileCopy(const float* m, int64_t sn_, int rows, int d) {
+    const int c = static_cast<int>(threadIdx.x) % kPer * kUnit;
+    src = m + c;
+    sn = sn_;
+    limit = c < d ? rows : 0;
   }
-}
+  __device__ __forceinline__ void operator()(float* raw, int n0) const {
+    const int r0 = static_cast<int>(threadIdx.x) / kPer;
+    const float* from = src + static_cast<int64_t>(n0 + r0) * sn;
+    const uint32_t to = smem_u32(raw) + (r0 * DP + static_cast<int>(threadIdx.x) % kPer * kUnit) * 4;
+#pragma unroll(kVec ? kTile / kStep : 4)
+    for (int i = 0; i < kTile / kStep; ++i) {
+      const bool ok = n0 + r0 + i * kStep < limit;
+      copy_async<kVec>(to + i * kStep * DP * 4, ok ? from : src, ok);
+      from += kStep * sn;
+    }
+  }
+};
 
 // ---- scales: powers of two, the largest value goes to 2^13 .. 2^14 (below 2^-112 to less)
 struct Scale {
@@ -185,11 +197,12 @@ __device__ __forceinline__ uint32_t block_max(uint32_t top, uint32_t* red) {
 template <int DP, bool kVec>
 __device__ __forceinline__ float own_rows(uint8_t* to, float* raw, uint32_t* red, const float* src,
                                           int64_t sn, int n0, int limit, int d) {
+  const TileCopy<DP, kVec> copy(src, sn, limit, d);
   Share<DP> s[2];
   uint32_t top = 0u;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    load_rows<DP, kVec>(raw, src, sn, n0 + i * kTile, limit, d);
+    copy(raw, n0 + i * kTile);
     copy_commit();
     copy_wait();
     __syncthreads();
@@ -214,7 +227,7 @@ template <int DP>
 __device__ __forceinline__ void product_d(float (&s)[kNT][4], const uint8_t* A, int a_row,
                                           const uint8_t* B, int g, int t) {
   constexpr int kLoA = kRows * DP * 2, kLoB = kTile * DP * 2;
-  float hi[kNT][4] = {}, lo[kNT][4] = {};
+  float hi[kNT][4], lo[kNT][4];
 #pragma unroll
   for (int h = 0; h < DP / 32; ++h) {
     const uint4 x = unit16<DP>(A, a_row + g, t + 4 * h), y = unit16<DP>(A, a_row + g + 8, t + 4 * h);
@@ -226,9 +239,14 @@ __device__ __forceinline__ void product_d(float (&s)[kNT][4], const uint8_t* A, 
     for (int n = 0; n < kNT; ++n) {
       const uint4 b = unit16<DP>(B, 8 * n + g, t + 4 * h);
       const uint4 bl = unit16<DP>(B + kLoB, 8 * n + g, t + 4 * h);
-      mma16816(lo[n], l0, b.x, b.y);
+      if (h == 0) {
+        mma16816_zero(lo[n], l0, b.x, b.y);
+        mma16816_zero(hi[n], a0, b.x, b.y);
+      } else {
+        mma16816(lo[n], l0, b.x, b.y);
+        mma16816(hi[n], a0, b.x, b.y);
+      }
       mma16816(lo[n], a0, bl.x, bl.y);
-      mma16816(hi[n], a0, b.x, b.y);
       mma16816(lo[n], l1, b.z, b.w);
       mma16816(lo[n], a1, bl.z, bl.w);
       mma16816(hi[n], a1, b.z, b.w);
@@ -271,27 +289,38 @@ __device__ __forceinline__ void product_rows(float (&o)[DP / 8][4], const ScoreF
   constexpr int kP = pair_pitch<DP>(), kLo = kTile / 2 * kP;
 #pragma unroll
   for (int u = 0; u < DP / 32; ++u) {
-    float hi[4][4] = {}, lo[4][4] = {};
+    uint4 b0[kNT / 2], b1[kNT / 2];
+    float sum[4][4];  // the small terms first, then the large: a chain of two where cuts matter
 #pragma unroll
     for (int s = 0; s < kNT / 2; ++s) {
       const uint32_t* at = B + (8 * s + t) * kP + 32 * u + 4 * g;
-      const uint4 b0 = *reinterpret_cast<const uint4*>(at);
-      const uint4 b1 = *reinterpret_cast<const uint4*>(at + 4 * kP);
+      b0[s] = *reinterpret_cast<const uint4*>(at);
+      b1[s] = *reinterpret_cast<const uint4*>(at + 4 * kP);
       const uint4 l0 = *reinterpret_cast<const uint4*>(at + kLo);
       const uint4 l1 = *reinterpret_cast<const uint4*>(at + kLo + 4 * kP);
-      const uint32_t x0[4] = {b0.x, b0.y, b0.z, b0.w}, x1[4] = {b1.x, b1.y, b1.z, b1.w};
+      const uint32_t x0[4] = {b0[s].x, b0[s].y, b0[s].z, b0[s].w};
+      const uint32_t x1[4] = {b1[s].x, b1[s].y, b1[s].z, b1[s].w};
       const uint32_t y0[4] = {l0.x, l0.y, l0.z, l0.w}, y1[4] = {l1.x, l1.y, l1.z, l1.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        mma16816(lo[e], p.lo[s], x0[e], x1[e]);
-        mma16816(lo[e], p.hi[s], y0[e], y1[e]);
-        mma16816(hi[e], p.hi[s], x0[e], x1[e]);
+        if (s == 0)
+          mma16816_zero(sum[e], p.lo[s], x0[e], x1[e]);
+        else
+          mma16816(sum[e], p.lo[s], x0[e], x1[e]);
+        mma16816(sum[e], p.hi[s], y0[e], y1[e]);
       }
+    }
+#pragma unroll
+    for (int s = 0; s < kNT / 2; ++s) {
+      const uint32_t x0[4] = {b0[s].x, b0[s].y, b0[s].z, b0[s].w};
+      const uint32_t x1[4] = {b1[s].x, b1[s].y, b1[s].z, b1[s].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) mma16816(sum[e], p.hi[s], x0[e], x1[e]);
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[4 * u + e][i] = fmaf(hi[e][i] + lo[e][i], inv, o[4 * u + e][i]);
+      for (int i = 0; i < 4; ++i) o[4 * u + e][i] = fmaf(sum[e][i], inv, o[4 * u + e][i]);
   }
 }
 
@@ -323,6 +352,24 @@ __device__ __forceinline__ int keys_of(const RelF32& p, int b) {
   return p.mask == 2 ? min(max(__ldg(p.key_len + b), 0), p.Nk) : p.Nk;
 }
 
+// x = s f + t: t the constant, or of the lane's columns 8 n + 2 t, + 1 and rows g, g + 8 from the table
+// (at: its entry for column 0 and row g; a row less is a distance more)
+__device__ __forceinline__ void add_bias(float (&s)[kNT][4], float f, bool near, float constant,
+                                         const float* at) {
+  if (near) {
+#pragma unroll
+    for (int n = 0; n < kNT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        s[n][i] = fmaf(s[n][i], f, at[8 * n + (i & 1) - 8 * (i >> 1)]);
+  } else {
+#pragma unroll
+    for (int n = 0; n < kNT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[n][i] = fmaf(s[n][i], f, constant);
+  }
+}
+
 // ============================================================================ forward
 template <int DP>
 struct FwdSmem {
@@ -349,11 +396,11 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 3 : 2)
   const int L = keys_of(p, b);
   const int last = min(q0 + kRows, p.Nq) - 1;
   const int nt = p.mask == 1 ? last / kTile + 1 : (L + kTile - 1) / kTile;
-  const float* kb = p.K + b * p.st[1][0] + h * p.st[1][1];
-  const float* vb = p.V + b * p.st[2][0] + h * p.st[2][1];
+  const TileCopy<DP, kVec> copy_k(p.K + b * p.st[1][0] + h * p.st[1][1], p.st[1][2], L, p.d_k);
+  const TileCopy<DP, kVec> copy_v(p.V + b * p.st[2][0] + h * p.st[2][1], p.st[2][2], L, p.d_v);
   auto load = [&](int j) {
-    load_rows<DP, kVec>(sm.rawK, kb, p.st[1][2], j * kTile, L, p.d_k);
-    load_rows<DP, kVec>(sm.rawV, vb, p.st[2][2], j * kTile, L, p.d_v);
+    copy_k(sm.rawK, j * kTile);
+    copy_v(sm.rawV, j * kTile);
     copy_commit();
   };
   for (int s = threadIdx.x; s <= kRelMaxSeg; s += kThreads) rel_load(sm.rs, rel, h, s, 1.f);
@@ -400,16 +447,18 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 3 : 2)
       product_d<DP>(s, sm.Q, 16 * warp, sm.K, g, t);
       const float f = k_inv * q_inv;
       float mx[2] = {-INFINITY, -INFINITY};
+      add_bias(s, f, near, seg_bias, sm.table + 2 * t - (16 * warp + g) + kRows - 1);
+      if (j * kTile + kTile - 1 > (p.mask == 1 ? q0 + 16 * warp : L - 1)) {
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (j * kTile + 8 * n + 2 * t + (i & 1) > limit[i >> 1]) s[n][i] = -INFINITY;
+      }
 #pragma unroll
       for (int n = 0; n < kNT; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int c = 8 * n + 2 * t + (i & 1);  // the tile's key
-          const float bias =
-              near ? sm.table[c - (16 * warp + g + 8 * (i >> 1)) + kRows - 1] : seg_bias;
-          s[n][i] = j * kTile + c <= limit[i >> 1] ? fmaf(s[n][i], f, bias) : -INFINITY;
-          mx[i >> 1] = fmaxf(mx[i >> 1], s[n][i]);
-        }
+        for (int i = 0; i < 4; ++i) mx[i >> 1] = fmaxf(mx[i >> 1], s[n][i]);
       float alpha[2], ref[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -453,11 +502,6 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 3 : 2)
 }
 
 // ============================================================================ backward
-// p = exp(x - lse), x = s f + bias; 0 where the pair is not allowed
-__device__ __forceinline__ float weight(float s, float f, float bias, float lse, bool ok) {
-  return ok ? ex2_approx(fmaf(s, f, bias - lse) * kLog2e) : 0.f;
-}
-
 template <int DP>
 struct DqSmem {
   uint8_t Q[rows_bytes<DP>(kRows)], G[rows_bytes<DP>(kRows)];  // G: dO
@@ -492,12 +536,12 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
   const int last = min(q0 + kRows, p.Nq) - 1;
   const int nt = p.mask == 1 ? last / kTile + 1 : (L + kTile - 1) / kTile;
   const int64_t bh = static_cast<int64_t>(b) * p.H + h;
-  const float* kb = p.K + b * p.st[1][0] + h * p.st[1][1];
-  const float* vb = p.V + b * p.st[2][0] + h * p.st[2][1];
+  const TileCopy<DP, kVec> copy_k(p.K + b * p.st[1][0] + h * p.st[1][1], p.st[1][2], L, p.d_k);
+  const TileCopy<DP, kVec> copy_v(p.V + b * p.st[2][0] + h * p.st[2][1], p.st[2][2], L, p.d_v);
   const float* gb = p.dO + b * p.st[4][0] + h * p.st[4][1];
   auto load = [&](int j) {
-    load_rows<DP, kVec>(sm.rawK, kb, p.st[1][2], j * kTile, L, p.d_k);
-    load_rows<DP, kVec>(sm.rawV, vb, p.st[2][2], j * kTile, L, p.d_v);
+    copy_k(sm.rawK, j * kTile);
+    copy_v(sm.rawV, j * kTile);
     copy_commit();
   };
   for (int s = tid; s <= kRelMaxSeg; s += kThreads) rel_load(sm.rs, rel, h, s, 1.f);
@@ -575,16 +619,19 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
       product_d<DP>(s, sm.Q, 16 * warp, sm.K, g, t);
       product_d<DP>(dp, sm.G, 16 * warp, sm.V, g, t);
       const float f = k_inv * q_inv, fg = v_inv * g_inv;
+      add_bias(s, f, near, seg_bias, sm.table + 2 * t - r_loc[0] + kRows - 1);
+      if (j * kTile + kTile - 1 > (p.mask == 1 ? q0 + 16 * warp : L - 1)) {
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (j * kTile + 8 * n + 2 * t + (i & 1) > limit[i >> 1]) s[n][i] = -INFINITY;
+      }
 #pragma unroll
       for (int n = 0; n < kNT; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int c = 8 * n + 2 * t + (i & 1);
-          const float bias = near ? sm.table[c - r_loc[i >> 1] + kRows - 1] : seg_bias;
-          const float w =
-              weight(s[n][i], f, bias, lse[i >> 1], j * kTile + c <= limit[i >> 1]);
-          s[n][i] = w * fmaf(dp[n][i], fg, -D[i >> 1]);
-        }
+        for (int i = 0; i < 4; ++i)
+          s[n][i] = ex2_approx((s[n][i] - lse[i >> 1]) * kLog2e) * fmaf(dp[n][i], fg, -D[i >> 1]);
     }
     if (near) {
       __syncthreads();  // K and V as rows are done with
@@ -658,16 +705,16 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
   const int h = blockIdx.y, b = blockIdx.z, k0 = static_cast<int>(blockIdx.x) * kRows;
   const int L = keys_of(p, b);
   const int64_t bh = static_cast<int64_t>(b) * p.H + h;
-  const float* qb = p.Q + b * p.st[0][0] + h * p.st[0][1];
-  const float* gb = p.dO + b * p.st[4][0] + h * p.st[4][1];
+  const TileCopy<DP, kVec> copy_q(p.Q + b * p.st[0][0] + h * p.st[0][1], p.st[0][2], p.Nq, p.d_k);
+  const TileCopy<DP, kVec> copy_g(p.dO + b * p.st[4][0] + h * p.st[4][1], p.st[4][2], p.Nq, p.d_v);
   const int i0 = p.mask == 1 ? k0 / kTile : 0;  // the first tile of queries that sees a key
   const int ni = k0 < L ? (p.Nq + kTile - 1) / kTile : 0;
   const int key[2] = {k0 + 16 * warp + g, k0 + 16 * warp + g + 8};
   float dk[DP / 8][4] = {}, dv[DP / 8][4] = {};
   if (i0 < ni) {
     auto load = [&](int i) {
-      load_rows<DP, kVec>(sm.rawQ, qb, p.st[0][2], i * kTile, p.Nq, p.d_k);
-      load_rows<DP, kVec>(sm.rawG, gb, p.st[4][2], i * kTile, p.Nq, p.d_v);
+      copy_q(sm.rawQ, i * kTile);
+      copy_g(sm.rawG, i * kTile);
       copy_commit();
     };
     for (int s = tid; s <= kRelMaxSeg; s += kThreads) rel_load(sm.rs, rel, h, s, 1.f);
@@ -716,16 +763,39 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
       product_d<DP>(s, sm.K, 16 * warp, sm.Q, g, t);
       product_d<DP>(ds, sm.V, 16 * warp, sm.G, g, t);
       const float f = q_inv * k_inv, fg = g_inv * v_inv;
+      // the table by row (key) minus column (query): a row more is a distance more
+      if (near) {
+        const float* at = sm.table + 16 * warp + g - 2 * t + kTile - 1;
 #pragma unroll
-      for (int n = 0; n < kNT; ++n)
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            s[n][e] = fmaf(s[n][e], f, at[8 * (e >> 1) - 8 * n - (e & 1)]);
+      } else {
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[n][e] = fmaf(s[n][e], f, seg_bias);
+      }
+      if (k0 + 16 * warp + 15 >= L || (p.mask == 1 && k0 + 16 * warp + 15 > q0)) {
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = key[e >> 1];
+            if (j >= L || (p.mask == 1 && j > q0 + 8 * n + 2 * t + (e & 1))) s[n][e] = -INFINITY;
+          }
+      }
+#pragma unroll
+      for (int n = 0; n < kNT; ++n) {
+        const float2 lse = *reinterpret_cast<const float2*>(sm.lse + 8 * n + 2 * t);
+        const float2 D = *reinterpret_cast<const float2*>(sm.D + 8 * n + 2 * t);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int c = 8 * n + 2 * t + (e & 1), j = key[e >> 1];
-          const float bias = near ? sm.table[j - k0 - c + kTile - 1] : seg_bias;
-          const bool ok = j < L && (p.mask != 1 || j <= q0 + c);
-          s[n][e] = weight(s[n][e], f, bias, sm.lse[c], ok);
-          ds[n][e] = s[n][e] * fmaf(ds[n][e], fg, -sm.D[c]);
+          s[n][e] = ex2_approx((s[n][e] - (e & 1 ? lse.y : lse.x)) * kLog2e);
+          ds[n][e] = s[n][e] * fmaf(ds[n][e], fg, -(e & 1 ? D.y : D.x));
         }
+      }
       const Scale fs = score_scale(s), fd = score_scale(ds);
       product_rows<DP>(dv, ScoreFrags(s, fs.mul), sm.Gp, fs.inv * g_inv, g, t);
       product_rows<DP>(dk, ScoreFrags(ds, fd.mul), sm.Qp, fd.inv * q_inv, g, t);
