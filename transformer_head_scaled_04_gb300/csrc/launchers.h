@@ -272,7 +272,7 @@ cudaError_t launch_sdpa_rel_bf16(const CUtensorMap& tmQ, const CUtensorMap& tmK,
 cudaError_t launch_sdpa_rel_f32(const SdpaArgs& a, const RelBias& rel, cudaStream_t s);
 // rel.partial: fp32 [B, H, rel_bwd_tiles(..), nseg] sums of dS, written by every tile, from which the
 // last launch takes dtable [num_buckets, H] (the table's type); a.Dv as for the launches without bias
-// (fp32: written by the first of the kernels)
+// (fp32: written here)
 cudaError_t launch_sdpa_rel_bwd_bf16(const CUtensorMap& tmQ, const CUtensorMap& tmK,
                                      const CUtensorMap& tmV, const CUtensorMap& tmG,
                                      const CUtensorMap& tmDQ, const SdpaBwdArgs& a,

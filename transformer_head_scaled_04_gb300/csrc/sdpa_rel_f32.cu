@@ -47,10 +47,10 @@ constexpr int kDist = kRows + kTile - 1;  // distances of a tile
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct RelF32 {
-  const float *Q, *K, *V, *O, *dO;
+  const float *Q, *K, *V, *dO;
   float *out, *dQ, *dK, *dV;   // out: the forward's O
   float* lse;                  // forward: written if not null; backward: read
-  float* Dv;                   // backward: [B, H, Nq] rowsum(dO O)
+  const float* Dv;             // backward: [B, H, Nq] rowsum(dO O)
   int64_t st[8][3];            // strides b, h, n of Q, K, V, O, dO, dQ, dK, dV (d: 1)
   int H, Nq, Nk, d_k, d_v, mask;
   const int32_t* key_len;
@@ -514,24 +514,20 @@ struct DqSmem {
   };
   float rawK[kTile * DP], rawV[kTile * DP];
   float D[kRows], lse[kRows];
-  float table[kDist + 1], diag[kDist + 1];
+  float table[kDist + 1];
   uint32_t red[2][kWarps];
   float far[kWarps];
+  float part[kWarps][32];  // a warp's sums of the segments span[..][0] .. span[..][1]
+  int span[kWarps][2];
   RelShared rs;
 };
 
-// One CTA per 64 queries: D, dQ and the tile's sums of dS per segment (thread s owns segment s).
+// 64 queries' dQ and their sums of dS per segment (thread s owns segment s)
 template <int DP, bool kVec>
-__global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
-    sdpa_rel_dq_f32_kernel(const RelF32 p, const __grid_constant__ RelBias rel) {
-  pdl_launch_dependents();
-  pdl_wait();  // the previous kernel's output is complete from here on
-  extern __shared__ __align__(16) uint8_t smem[];
-  DqSmem<DP>& sm = *reinterpret_cast<DqSmem<DP>*>(smem);
+__device__ __forceinline__ void queries_part(const RelF32& p, const RelBias& rel, DqSmem<DP>& sm,
+                                             int tile, int tiles) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int h = blockIdx.y, b = blockIdx.z;
-  const int q0 = (p.mask == 1 ? static_cast<int>(gridDim.x - 1 - blockIdx.x)
-                              : static_cast<int>(blockIdx.x)) * kRows;
+  const int h = blockIdx.y, b = blockIdx.z, q0 = tile * kRows;
   const int L = keys_of(p, b);
   const int last = min(q0 + kRows, p.Nq) - 1;
   const int nt = p.mask == 1 ? last / kTile + 1 : (L + kTile - 1) / kTile;
@@ -545,22 +541,10 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
     copy_commit();
   };
   for (int s = tid; s <= kRelMaxSeg; s += kThreads) rel_load(sm.rs, rel, h, s, 1.f);
-  {  // D, two threads to a row
-    const int r = tid >> 1;
-    const bool live = q0 + r < p.Nq;
-    float acc = 0.f;
-    if (live) {
-      const float* orow = p.O + b * p.st[3][0] + h * p.st[3][1] +
-                          static_cast<int64_t>(q0 + r) * p.st[3][2];
-      const float* grow = gb + static_cast<int64_t>(q0 + r) * p.st[4][2];
-      for (int d = tid & 1; d < p.d_v; d += 2) acc = fmaf(grow[d], orow[d], acc);
-    }
-    acc += __shfl_xor_sync(0xffffffffu, acc, 1);
-    if ((tid & 1) == 0) {
-      sm.D[r] = acc;
-      sm.lse[r] = live ? p.lse[bh * p.Nq + q0 + r] : INFINITY;
-      if (live) p.Dv[bh * p.Nq + q0 + r] = acc;
-    }
+  if (tid < kRows) {
+    const int64_t i = bh * p.Nq + q0 + tid;
+    sm.D[tid] = q0 + tid < p.Nq ? p.Dv[i] : 0.f;
+    sm.lse[tid] = q0 + tid < p.Nq ? p.lse[i] : INFINITY;
   }
   const float q_inv =
       own_rows<DP, kVec>(sm.Q, sm.rawK, sm.red[0], p.Q + b * p.st[0][0] + h * p.st[0][1], p.st[0][2],
@@ -595,8 +579,11 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
     const bool near = d0 + kDist - 1 >= seg_next;
     copy_wait();
     __syncthreads();  // the tile is there, the previous one done with
-    if (near && tid < kDist)
-      sm.table[tid] = sm.rs.bias[rel_segment(sm.rs, rel_steps(rel.nseg), d0 + tid)];
+    int dist_seg = 0;  // the segment of distance d0 + tid
+    if (near) {
+      dist_seg = rel_segment(sm.rs, rel_steps(rel.nseg), d0 + tid);
+      if (tid < kDist) sm.table[tid] = sm.rs.bias[dist_seg];
+    }
     float k_inv, v_inv;
     {
       Share<DP> k, v;
@@ -648,31 +635,36 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
       const Scale f = score_scale(s);
       product_rows<DP>(dq, ScoreFrags(s, f.mul), sm.Kp, f.inv * k_inv, g, t);
     }
-    if (near) {  // sums over the diagonals, then over each segment's diagonals
+    if (near) {  // sums over the diagonals, one per thread, then over each warp's segments
       __syncthreads();
-      if (tid < kDist) {
-        float acc = 0.f;
+      float acc = 0.f;
 #pragma unroll 8
-        for (int r = 0; r < kRows; ++r) {
-          const int c = r + tid - (kRows - 1);
-          if (c >= 0 && c < kTile) acc += sm.S[r * (kTile + 1) + c];
-        }
-        sm.diag[tid] = acc;
+      for (int r = 0; r < kRows; ++r) {
+        const int c = r + tid - (kRows - 1);
+        if (c >= 0 && c < kTile) acc += sm.S[r * (kTile + 1) + c];
       }
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const float up = __shfl_up_sync(0xffffffffu, acc, off);
+        const int other = __shfl_up_sync(0xffffffffu, dist_seg, off);
+        if (lane >= off && other == dist_seg) acc += up;
+      }
+      const int first = __shfl_sync(0xffffffffu, dist_seg, 0);
+      const int next = __shfl_down_sync(0xffffffffu, dist_seg, 1);
+      if (lane == 31 || next != dist_seg) sm.part[warp][dist_seg - first] = acc;
+      if (lane == 0) sm.span[warp][0] = first;
+      if (lane == 31) sm.span[warp][1] = dist_seg;
       __syncthreads();
-      if (tid < rel.nseg) {
-        const int lo = sm.rs.start[tid] <= d0 ? 0 : min(sm.rs.start[tid] - d0, kDist);
-        const int hi = sm.rs.start[tid + 1] > d0 + kDist - 1 ? kDist - 1
-                                                             : sm.rs.start[tid + 1] - 1 - d0;
-        for (int e = lo; e <= hi; ++e) own += sm.diag[e];
-      }
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w)
+        if (tid >= sm.span[w][0] && tid <= sm.span[w][1]) own += sm.part[w][tid - sm.span[w][0]];
     }
   }
   if (nt > 0) {
     __syncthreads();
     flush_far();
   }
-  if (tid < rel.nseg) rel.partial[(bh * gridDim.x + blockIdx.x) * rel.nseg + tid] = own;
+  if (tid < rel.nseg) rel.partial[(bh * tiles + tile) * rel.nseg + tid] = own;
   float* out = p.dQ + b * p.st[5][0] + h * p.st[5][1];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
@@ -693,16 +685,12 @@ struct DkdvSmem {
   RelShared rs;
 };
 
-// One CTA per 64 keys: dK and dV from tiles of 32 queries (after the dq kernel, which leaves D).
+// 64 keys' dK and dV from tiles of 32 queries
 template <int DP, bool kVec>
-__global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
-    sdpa_rel_dkdv_f32_kernel(const RelF32 p, const __grid_constant__ RelBias rel) {
-  pdl_launch_dependents();
-  pdl_wait();  // the previous kernel's output is complete from here on
-  extern __shared__ __align__(16) uint8_t smem[];
-  DkdvSmem<DP>& sm = *reinterpret_cast<DkdvSmem<DP>*>(smem);
+__device__ __forceinline__ void keys_part(const RelF32& p, const RelBias& rel, DkdvSmem<DP>& sm,
+                                          int tile) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int h = blockIdx.y, b = blockIdx.z, k0 = static_cast<int>(blockIdx.x) * kRows;
+  const int h = blockIdx.y, b = blockIdx.z, k0 = tile * kRows;
   const int L = keys_of(p, b);
   const int64_t bh = static_cast<int64_t>(b) * p.H + h;
   const TileCopy<DP, kVec> copy_q(p.Q + b * p.st[0][0] + h * p.st[0][1], p.st[0][2], p.Nq, p.d_k);
@@ -811,6 +799,32 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
     }
 }
 
+// A CTA takes 64 queries or 64 keys of a head, in turn along x while there are both, those with the most
+// tiles to go over first under the causal mask: one launch keeps the GPU filled where one kind alone
+// leaves it waiting for its longest CTAs (4 x 8 heads of 500, causal: 112 us in two launches, xx in one).
+template <int DP>
+struct BwdSmem {
+  union {
+    DqSmem<DP> q;
+    DkdvSmem<DP> k;
+  };
+};
+template <int DP, bool kVec>
+__global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
+    sdpa_rel_bwd_f32_kernel(const RelF32 p, const __grid_constant__ RelBias rel) {
+  pdl_launch_dependents();
+  pdl_wait();  // the previous kernel's output (D among it) is complete from here on
+  extern __shared__ __align__(16) uint8_t smem[];
+  BwdSmem<DP>& sm = *reinterpret_cast<BwdSmem<DP>*>(smem);
+  const int x = static_cast<int>(blockIdx.x);
+  const int nq = (p.Nq + kRows - 1) / kRows, nk = (p.Nk + kRows - 1) / kRows, both = min(nq, nk);
+  const int i = x < 2 * both ? x >> 1 : x - both;
+  if (x < 2 * both ? (x & 1) == 0 : nq > nk)
+    queries_part<DP, kVec>(p, rel, sm.q, p.mask == 1 ? nq - 1 - i : i, nq);
+  else
+    keys_part<DP, kVec>(p, rel, sm.k, i);
+}
+
 // the gradient of the table alone, one block per head
 __global__ void __launch_bounds__(kRelGradThreads)
     rel_table_grad_kernel(const __grid_constant__ RelBias rel, void* dtable, int B, int tiles) {
@@ -870,7 +884,6 @@ cudaError_t launch_sdpa_rel_bwd_f32(const SdpaBwdArgs& a, const RelBias& rel, vo
   p.Q = static_cast<const float*>(a.Q);
   p.K = static_cast<const float*>(a.K);
   p.V = static_cast<const float*>(a.V);
-  p.O = static_cast<const float*>(a.O);
   p.dO = static_cast<const float*>(a.dO);
   p.dQ = static_cast<float*>(a.dQ);
   p.dK = static_cast<float*>(a.dK);
@@ -888,22 +901,15 @@ cudaError_t launch_sdpa_rel_bwd_f32(const SdpaBwdArgs& a, const RelBias& rel, vo
   p.mask = a.mask;
   p.key_len = a.key_len;
   p.scale = a.scale;
-  const bool small = a.d_k <= 64 && a.d_v <= 64;
-  const dim3 gq((a.Nq + kRows - 1) / kRows, a.H, a.B), gk((a.Nk + kRows - 1) / kRows, a.H, a.B);
-  cudaError_t e;
-  if (small)
-    e = vec ? go(sdpa_rel_dq_f32_kernel<64, true>, gq, sizeof(DqSmem<64>), p, rel, s)
-            : go(sdpa_rel_dq_f32_kernel<64, false>, gq, sizeof(DqSmem<64>), p, rel, s);
-  else
-    e = vec ? go(sdpa_rel_dq_f32_kernel<128, true>, gq, sizeof(DqSmem<128>), p, rel, s)
-            : go(sdpa_rel_dq_f32_kernel<128, false>, gq, sizeof(DqSmem<128>), p, rel, s);
+  cudaError_t e = launch_sdpa_bwd_rowdot(a, 0, s);  // D
   if (e != cudaSuccess) return e;
-  if (small)
-    e = vec ? go(sdpa_rel_dkdv_f32_kernel<64, true>, gk, sizeof(DkdvSmem<64>), p, rel, s)
-            : go(sdpa_rel_dkdv_f32_kernel<64, false>, gk, sizeof(DkdvSmem<64>), p, rel, s);
+  const dim3 grid((a.Nq + kRows - 1) / kRows + (a.Nk + kRows - 1) / kRows, a.H, a.B);
+  if (a.d_k <= 64 && a.d_v <= 64)
+    e = vec ? go(sdpa_rel_bwd_f32_kernel<64, true>, grid, sizeof(BwdSmem<64>), p, rel, s)
+            : go(sdpa_rel_bwd_f32_kernel<64, false>, grid, sizeof(BwdSmem<64>), p, rel, s);
   else
-    e = vec ? go(sdpa_rel_dkdv_f32_kernel<128, true>, gk, sizeof(DkdvSmem<128>), p, rel, s)
-            : go(sdpa_rel_dkdv_f32_kernel<128, false>, gk, sizeof(DkdvSmem<128>), p, rel, s);
+    e = vec ? go(sdpa_rel_bwd_f32_kernel<128, true>, grid, sizeof(BwdSmem<128>), p, rel, s)
+            : go(sdpa_rel_bwd_f32_kernel<128, false>, grid, sizeof(BwdSmem<128>), p, rel, s);
   return e == cudaSuccess ? launch_rel_table_grad(rel, dtable, a.B, rel_bwd_tiles(a.Nq, a.Nk, 0), s)
                           : e;
 }
