@@ -312,8 +312,9 @@ int mha_kv_evict_q8(int B, int H, int Lmax, int Lmax_out, int d_k, int d_v, int 
  * This is position information from the neighbourhood that [JY] Self-Attention的优势 speaks of, put
  * where the softmax weighs the positions; the pages themselves add positions to the embeddings.
  *   bias     [num_buckets, H], contiguous, of type bias_dtype (fp32 or bf16, whatever dtype is; the
- *            layout of an embedding over the buckets).  Read as fp32.  A value below -1e30 (-inf, the
- *            lowest value of a type) excludes its bucket; +inf and NaN give NaN.
+ *            layout of an embedding over the buckets).  Read as fp32.  A value below -1e6 (what masks
+ *            use: -1e9, the lowest value of a type, -inf) excludes its bucket; values above 1e6,
+ *            +inf and NaN are not supported (their rows hold anything).
  *   buckets  2 <= num_buckets <= 128.  bidirectional = 1: num_buckets even and at least 4, keys
  *            after the query (d > 0) have the upper half of the buckets, the others the lower half;
  *            bidirectional = 0: all buckets are for keys up to the query, and keys after it share

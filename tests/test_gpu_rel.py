@@ -187,7 +187,7 @@ def test_large_bias_far_away(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F])
-@pytest.mark.parametrize("low", [-np.inf, -1e38])
+@pytest.mark.parametrize("low", [-np.inf, -1e38, -1e9])
 def test_excluded_buckets(dtype, low):
     # head 0: keys before the query are out, so a row's first tiles hold nothing; head 1: the query
     # itself and the keys after it are out, so row 0 holds nothing at all; head 2: all are out
@@ -203,7 +203,7 @@ def test_excluded_buckets(dtype, low):
     q, k, v, g = (dev(a, dtype) for a in (Q, K, V, dO))
     t = dev(np.maximum(T, -3.4e38) if low > -np.inf else T, F)
     O, lse = mha.sdpa_rel_with_lse(q, k, v, t, **how)
-    Tr = np.where(T < -1e30, -np.inf, T)
+    Tr = np.where(T < -1e6, -np.inf, T)
     with np.errstate(invalid="ignore"):
         rO, rl = ref.sdpa_rel_ref(Q, K, V, Tr, **how)
     check_lse(lse.cpu().numpy(), rl, atol=1e-3)
@@ -215,7 +215,7 @@ def test_excluded_buckets(dtype, low):
         mha.set_deterministic(False)
         for x in (dq, dk, dv, dt):
             assert torch.all(torch.isfinite(x))
-        assert torch.all(dt[t < -1e30] == 0) and torch.all(dq[:, 2] == 0) and torch.all(dv[:, 2] == 0)
+        assert torch.all(dt[t < -1e6] == 0) and torch.all(dq[:, 2] == 0) and torch.all(dv[:, 2] == 0)
         with np.errstate(invalid="ignore"):
             rq, rk, rv, _ = ref.sdpa_rel_bwd_ref(Q, K, V, Tr, dO, **how)
             near_enough(dtype, [(O, rO, "O"), (dq, rq, "dQ"), (dk, rk, "dK"), (dv, rv, "dV")], rl,
@@ -343,6 +343,111 @@ def test_gradient_of_the_table_against_differences():
         size = (O.double().abs() * g.double().abs())[:, 1].sum()
         tol = float(size) * (h * h + 2.0 ** -22 / h)
         assert abs(float(diff - dt[u, 1])) <= tol
+
+
+def plain64(q, k, v, t, do, causal, reach, both, given=None):
+    """(O, lse, dQ, dK, dV, dtable) in float64 on the GPU, elementary operations only."""
+    q, k, v, t, do = (x.double() for x in (q, k, v, t, do))
+    N, M = q.shape[2], k.shape[2]
+    lo = -(N - 1)
+    u = torch.tensor(ref.bucket_table(lo, M - 1, t.shape[0], reach, both), device="cuda")
+    d = torch.arange(M, device="cuda") - torch.arange(N, device="cuda")[:, None]
+    s = q.shape[3] ** -0.5
+    x = q @ k.transpose(2, 3) * s + t[u[d - lo]].permute(2, 0, 1)
+    if causal:
+        x = x.masked_fill(d > 0, -float("inf"))
+    lse = torch.logsumexp(x, -1)
+    p = torch.exp(x - lse[..., None])
+    del x
+    O = p @ v
+    base, weights = (O, p) if given is None else (given[0].double(), None)
+    if weights is None:
+        weights = p * torch.exp(lse - given[1].double())[..., None]
+    dS = weights * (do @ v.transpose(2, 3) - (do * base).sum(-1, keepdim=True))
+    dt = torch.zeros_like(t)
+    for e in range(M + N - 1):
+        dt[u[e]] += dS.diagonal(lo + e, 2, 3).sum((0, 2))
+    return O, lse, s * dS @ k, s * dS.transpose(2, 3) @ q, weights.transpose(2, 3) @ do, dt
+
+
+@pytest.mark.parametrize("dtype,N,causal", [(BF, 6001, False), (BF, 5000, True), (F, 2500, False)])
+def test_long_sequences(dtype, N, causal):
+    # hundreds of tiles per row: relative norms against 64 bits, the table's gradient element by element
+    torch.manual_seed(N)
+    q, k, v, do = (torch.randn(1, 2, N, 64, device="cuda").to(dtype) for _ in range(4))
+    t = torch.randn(32, 2, device="cuda") * 1.5
+    how = dict(mask="causal" if causal else "none", max_distance=128, bidirectional=not causal)
+    O, lse = mha.sdpa_rel_with_lse(q, k, v, t, **how)
+    got = (O, lse) + mha.sdpa_rel_backward(q, k, v, t, O, do, lse, **how)
+    want = plain64(q, k, v, t, do, causal, 128, not causal, given=(O, lse))
+    most = BF16_REL_L2 if dtype is BF else 1e-5
+    for i, (a, b) in enumerate(zip(got[:5], want[:5])):
+        rel = float((a.double() - b).norm() / b.norm())
+        assert rel <= (1e-6 if i == 1 else most), (i, rel)
+    # a sum of N N / 2 terms p (dP - D): fp32 arithmetic is off by 2^-15 of a weight's term (its
+    # exponent's roundings), of random sign over the N rows, whose own weights sum to 1 at most
+    size = float((do.double() ** 2).sum(-1).mean() ** 0.5) * 8 ** 0.5  # of dP, per row
+    tol = 2.0 ** -15 * size * N ** 0.5 * 4
+    assert float((got[5].double() - want[5]).abs().max()) <= tol
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_many_short_sequences(dtype):
+    B, H, N = 3000, 8, 5
+    torch.manual_seed(1)
+    q, k, v, do = (torch.randn(B, H, N, 64, device="cuda").to(dtype) for _ in range(4))
+    t = torch.randn(8, H, device="cuda")
+    how = dict(mask="causal", max_distance=20, bidirectional=False)
+    O, lse = mha.sdpa_rel_with_lse(q, k, v, t, **how)
+    got = (O, lse) + mha.sdpa_rel_backward(q, k, v, t, O, do, lse, **how)
+    want = plain64(q, k, v, t, do, True, 20, False, given=(O, lse))
+    for i, (a, b) in enumerate(zip(got, want)):
+        rel = float((a.double() - b).norm() / b.norm())
+        # O, and gradients of a handful of terms each: at most two roundings of 2^-8, on average less
+        assert rel <= (1e-6 if i == 1 else 2.0 ** -7 if dtype is BF and i < 5 else 1e-5), (i, rel)
+    n = torch.randint(0, N + 1, (B,), device="cuda").to(torch.int32)
+    a = mha.sdpa_rel_decode(q[:, :, :1], k, v, t, n, max_distance=20)
+    for b in (0, 1, 777, B - 1):
+        L = int(n[b])
+        want = ref.sdpa_rel_decode_ref(*(host(x[b:b + 1]) for x in (q[:, :, :1], k, v)), host(t), [L],
+                                       max_distance=20)
+        close(dtype)(host(a[b:b + 1]), want, "rel decode of many")
+
+
+def test_fp32_is_reproducible():
+    Q, K, V, dO, T = draw(2, 3, 500, 500, F, 911)
+    q, k, v, g, t = (dev(a, F) for a in (Q, K, V, dO, T))
+    O, lse = mha.sdpa_rel_with_lse(q, k, v, t)
+    runs = [(O, lse) + mha.sdpa_rel_backward(q, k, v, t, O, g, lse)]
+    for _ in range(3):
+        O, lse = mha.sdpa_rel_with_lse(q, k, v, t)
+        runs.append((O, lse) + mha.sdpa_rel_backward(q, k, v, t, O, g, lse))
+    for r in runs[1:]:
+        for a, b in zip(runs[0], r):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("size", [1e-30, 1e-12, 1e12])
+def test_fp32_values_of_any_size(size):
+    # operands are scaled tile by tile: V and dO of any size, and rows of very different sizes, keep
+    # fp32's relative accuracy
+    Q, K, V, dO, T = draw(1, 2, 200, 200, F, 912)
+    V = np.asarray(V * size, np.float32).astype(np.float64)
+    g = np.random.Generator(np.random.PCG64(5))
+    dO = np.asarray(dO * 10.0 ** g.integers(-6, 7, (1, 2, 200, 1)), np.float32).astype(np.float64)
+    q, k, v, do, t = (dev(a, F) for a in (Q, K, V, dO, T))
+    O, lse = mha.sdpa_rel_with_lse(q, k, v, t)
+    rO, _ = ref.sdpa_rel_ref(Q, K, V, T)
+    assert errors(O.double().cpu().numpy() / size, rO / size)[1] <= 1e-6
+    dq, dk, dv, dt = mha.sdpa_rel_backward(q, k, v, t, O, do, lse)
+    for a, b in zip((dq, dk, dv, dt), ref.sdpa_rel_bwd_ref(Q, K, V, T, dO)):
+        unit = np.abs(b).max()
+        assert errors(a.double().cpu().numpy() / unit, b / unit)[1] <= 1e-5
+    # every row of dQ goes by its own row of dO: rows a million times smaller than their neighbours
+    # are exact to 2^-22 of the tile's largest operand times their own
+    want = ref.sdpa_rel_bwd_ref(Q, K, V, T, dO)[0]
+    row = np.linalg.norm(dq.double().cpu().numpy() - want, axis=-1) / np.linalg.norm(want, axis=-1)
+    assert row.max() <= 1e-4
 
 
 # ------------------------------------------------------------------ generation step

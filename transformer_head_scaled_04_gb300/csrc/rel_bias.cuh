@@ -37,7 +37,11 @@ struct RelShared {
 static_assert(sizeof(RelShared) == 8 * (kRelMaxSeg + 1), "");
 
 // Entry s of the copy, for head h, the bias times `mul` (log2 e where exponentials are powers of
-// two).  A value below -1e30 (a mask's lowest value, -inf) leaves its bucket out: it becomes -inf.
+// two).  A value below kRelOut (a mask's: -1e9, a type's lowest, -inf) leaves its bucket out: it becomes
+// -inf.  At that size fp32 sums of a score and a bias have lost all but a few bits of the score, so a
+// softmax among such keys alone says nothing; and (t - m) c of such a t could pass the exponent's range
+// by its rounding.
+constexpr float kRelOut = -1e6f;
 __device__ __forceinline__ void rel_load(RelShared& sh, const RelBias& r, int h, int s, float mul) {
   if (s > kRelMaxSeg) return;
   int at = INT_MAX;
@@ -48,7 +52,7 @@ __device__ __forceinline__ void rel_load(RelShared& sh, const RelBias& r, int h,
     const int64_t i = static_cast<int64_t>(rel_row(seg)) * r.H + h;
     v = r.table_f32 ? __ldg(static_cast<const float*>(r.table) + i)
                     : __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(r.table) + i));
-    v = v < -1e30f ? -INFINITY : v * mul;
+    v = v < kRelOut ? -INFINITY : v * mul;
   }
   sh.start[s] = at;
   sh.bias[s] = v;

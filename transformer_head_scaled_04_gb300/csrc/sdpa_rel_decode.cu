@@ -632,26 +632,30 @@ __global__ void __launch_bounds__(kJoinThreads)
 
 // Runs of a head and positions of a run (a multiple of 64, 16 for each warp).  A round of CTAs that fit
 // on the GPU at once takes about the time of a run's positions and 96 more (start and the warps' join),
-// the second launch that of 150 and of some per run; of 1 to 8 full rounds the cheapest is taken.
-// Measured (us) for the rounds taken and for others: 64 x 16 heads of 4096 in bf16 166 with 4 runs
-// against 169 with 1 and 174 with 3, 8 x 16 heads of 16384 with 4 queries 87 with 19 runs against 119
-// with 5 and 93 with 29, 8 heads of 131072 44 with 76 runs against 48 with 228.
+// the second launch that of 150 and of some per run.  Of 1 to 8 full rounds the most whose time is within
+// 8% of the least are taken: caches that are not full leave short runs better balanced.  Measured (us,
+// full caches / lengths drawn evenly): 64 x 16 heads of 4096 in bf16 168 / 88 with the 4 runs taken,
+// 176 / 92 with 2, 185 / 101 with 16; 8 x 16 heads of 16384 with 4 queries 88 / 55 with 19, 107 / 57
+// with 6; 16 x 8 heads of 4096 31 / 18 with 8, 29 / 23 with 4.
 void plan(int B, int H, int Nq, int Lmax, int dp, int dtype, int* chunk, int* n_split) {
   const int64_t heads = static_cast<int64_t>(B) * H;
   const int64_t fit = 152 * (dtype == 1 ? 4 : dp == 64 ? (Nq == 2 ? 3 : 4) : (Nq == 1 ? 3 : 2));
-  int64_t best = -1;
-  for (int rounds = 1; rounds <= 8; ++rounds) {
-    int64_t n = std::max<int64_t>(1, rounds * fit / heads);
+  constexpr int kRounds = 8;
+  int64_t runs[kRounds], positions[kRounds], cost[kRounds], least = -1;
+  for (int i = 0; i < kRounds; ++i) {
+    int64_t n = std::max<int64_t>(1, (i + 1) * fit / heads);
     n = std::min<int64_t>({n, (Lmax + 63) / 64, kMaxSplit});
     const int64_t c = ((Lmax + n - 1) / n + 63) / 64 * 64;
     n = (Lmax + c - 1) / c;
-    const int64_t cost = (heads * n + fit - 1) / fit * (c + 96) + (n > 1 ? 150 + n * (Nq + 3) / 10 : 0);
-    if (best < 0 || cost < best) {
-      best = cost;
-      *chunk = static_cast<int>(c);
-      *n_split = static_cast<int>(n);
-    }
+    cost[i] = (heads * n + fit - 1) / fit * (c + 96) + (n > 1 ? 150 + n * (Nq + 3) / 10 : 0);
+    runs[i] = n;
+    positions[i] = c;
+    if (least < 0 || cost[i] < least) least = cost[i];
   }
+  int i = kRounds - 1;
+  while (cost[i] * 100 > least * 108) --i;
+  *chunk = static_cast<int>(positions[i]);
+  *n_split = static_cast<int>(runs[i]);
 }
 
 int padded(int dtype, int d_k, int d_v) { return dtype == 1 || (d_k <= 64 && d_v <= 64) ? 64 : 128; }

@@ -5,11 +5,13 @@
 //   backward  p = exp(x - lse), D = rowsum(dO O), dS = p (dO.v - D),
 //             dQ = scale dS K, dK = scale dS^T Q, dV = p^T dO, dt(segment) = sum of its dS
 //
-// Every operand is scaled by a power of two that brings its tile's largest value to 2^13 .. 2^14 and
-// split into two fp16 terms, a = hi + lo (mma_f16.cuh); a product is hi hi + hi lo + lo hi with fp32 sums.  What is
-// left of a value is at most 2^-23 of it or 2^-39 of the tile's largest, and the dropped lo lo is at
-// most 2^-22 of the product: fp32's own accuracy.  (Two tf32 terms give the same at twice the time of
-// the tensor cores: 322 us forward for 8 x 8 heads of 1001, xxx in fp16.)  The tensor cores cut sums
+// Operands are scaled by powers of two that bring their largest value to 2^13 .. 2^14 and split into
+// two fp16 terms, a = hi + lo (mma_f16.cuh); a product is hi hi + hi lo + lo hi with fp32 sums.  The left
+// operand has a scale for every row (whose results it only touches), the right one, whose rows are
+// summed over, one for its tile of 32 rows.  What is left of a value is at most 2^-23 of it or 2^-39 of
+// the largest that shares its scale, and the dropped lo lo is at most 2^-22 of the product: fp32's own
+// accuracy.  (Two tf32 terms give the same at twice the time of the tensor cores: 8 x 8 heads of 1001
+// forward 322 us, with fp16 215.)  The tensor cores cut sums
 // off instead of rounding them, 2^-24 of the sum per step towards zero (9e-6 of a gradient over 900
 // keys in one chain), so the large products are kept apart from the small ones, a chain spans one
 // tile at most, and tiles are added up with ordinary additions.
@@ -155,9 +157,33 @@ struct Share {
   __device__ __forceinline__ void write(float mul, uint8_t* to_rows, int rows, int row0,
                                         uint32_t* to_pairs) const {
 #pragma unroll
+    for (int i = 0; i < kItems; ++i) write_item(i, mul, mul, to_rows, rows, row0, to_pairs);
+  }
+  // the factors that undo the scales of rows row0 .. go to inv
+  __device__ __forceinline__ void write_by_row(uint8_t* to_rows, int rows, int row0,
+                                               float* inv) const {
+#pragma unroll
     for (int i = 0; i < kItems; ++i) {
-      const float4 x = make_float4(a[i].x * mul, a[i].y * mul, a[i].z * mul, a[i].w * mul);
-      const float4 y = make_float4(b[i].x * mul, b[i].y * mul, b[i].z * mul, b[i].w * mul);
+      float x = fmaxf(fmaxf(fabsf(a[i].x), fabsf(a[i].y)), fmaxf(fabsf(a[i].z), fabsf(a[i].w)));
+      float y = fmaxf(fmaxf(fabsf(b[i].x), fabsf(b[i].y)), fmaxf(fabsf(b[i].z), fabsf(b[i].w)));
+#pragma unroll
+      for (int off = 1; off < DP / 4; off <<= 1) {  // the DP / 4 lanes of a pair of rows
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
+        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, off));
+      }
+      const Scale fx = scale_for(__float_as_uint(x)), fy = scale_for(__float_as_uint(y));
+      write_item(i, fx.mul, fy.mul, to_rows, rows, row0, nullptr);
+      if (col(i) == 0) {
+        inv[row0 + 2 * pair(i)] = fx.inv;
+        inv[row0 + 2 * pair(i) + 1] = fy.inv;
+      }
+    }
+  }
+  __device__ __forceinline__ void write_item(int i, float mul_a, float mul_b, uint8_t* to_rows,
+                                             int rows, int row0, uint32_t* to_pairs) const {
+    {
+      const float4 x = make_float4(a[i].x * mul_a, a[i].y * mul_a, a[i].z * mul_a, a[i].w * mul_a);
+      const float4 y = make_float4(b[i].x * mul_b, b[i].y * mul_b, b[i].z * mul_b, b[i].w * mul_b);
       const uint2 xh = make_uint2(pack_half(x.x, x.y), pack_half(x.z, x.w));
       const uint2 yh = make_uint2(pack_half(y.x, y.y), pack_half(y.z, y.w));
       const uint2 xl = make_uint2(pack_rest(x.x, x.y, xh.x), pack_rest(x.z, x.w, xh.y));
@@ -193,27 +219,23 @@ __device__ __forceinline__ uint32_t block_max(uint32_t top, uint32_t* red) {
   return max(max(red[0], red[1]), max(red[2], red[3]));
 }
 
-// The CTA's own 64 rows, split as rows; returns the factor that undoes their scale.  raw is scratch.
+// The CTA's own 64 rows, split as rows, and the factors that undo their scales; raw is scratch.
 template <int DP, bool kVec>
-__device__ __forceinline__ float own_rows(uint8_t* to, float* raw, uint32_t* red, const float* src,
-                                          int64_t sn, int n0, int limit, int d) {
+__device__ __forceinline__ void own_rows(uint8_t* to, float* inv, float* raw, const float* src,
+                                         int64_t sn, int n0, int limit, int d) {
+  static_assert(DP / 4 <= 32 && 32 % (DP / 4) == 0, "a pair of rows within a warp");
   const TileCopy<DP, kVec> copy(src, sn, limit, d);
-  Share<DP> s[2];
-  uint32_t top = 0u;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    copy(raw, n0 + i * kTile);
+#pragma unroll 1
+  for (int i = 0; i < kRows; i += kTile) {
+    copy(raw, n0 + i);
     copy_commit();
     copy_wait();
     __syncthreads();
-    top = max(top, s[i].read(raw));
+    Share<DP> s;
+    s.read(raw);
+    s.write_by_row(to, kRows, i, inv);
     __syncthreads();
   }
-  const Scale f = scale_for(block_max(top, red));
-#pragma unroll
-  for (int i = 0; i < 2; ++i) s[i].write(f.mul, to, kRows, i * kTile, nullptr);
-  __syncthreads();  // red may be used again
-  return f.inv;
 }
 
 // ---- products
@@ -258,34 +280,38 @@ __device__ __forceinline__ void product_d(float (&s)[kNT][4], const uint8_t* A, 
     for (int i = 0; i < 4; ++i) s[n][i] = hi[n][i] + lo[n][i];
 }
 
-// the fragments of 16 x 32 scores, times mul, as the operand of a product over rows
+// the fragments of 16 x 32 scores, rows g and g + 8 times mul0 and mul1, as the operand of a product
+// over rows
 struct ScoreFrags {
   uint32_t hi[kNT / 2][4], lo[kNT / 2][4];
-  __device__ __forceinline__ ScoreFrags(const float (&p)[kNT][4], float mul) {
+  __device__ __forceinline__ ScoreFrags(const float (&p)[kNT][4], float mul0, float mul1) {
 #pragma unroll
     for (int s = 0; s < kNT / 2; ++s)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {  // (g, 2 t), (g + 8, 2 t), then the next eight columns
         const float* c = p[2 * s + (i >> 1)];
+        const float mul = i & 1 ? mul1 : mul0;
         const float x = c[2 * (i & 1)] * mul, y = c[2 * (i & 1) + 1] * mul;
         hi[s][i] = pack_half(x, y);
         lo[s][i] = pack_rest(x, y, hi[s][i]);
       }
   }
 };
-// the scale for a warp's scores
-__device__ __forceinline__ Scale score_scale(const float (&p)[kNT][4]) {
+// the scale for row g (half 0) or g + 8 (half 1) of a warp's scores
+__device__ __forceinline__ Scale score_scale(const float (&p)[kNT][4], int half) {
   float m = 0.f;
 #pragma unroll
-  for (int n = 0; n < kNT; ++n)
-    m = fmaxf(fmax3(m, fabsf(p[n][0]), fabsf(p[n][1])), fmaxf(fabsf(p[n][2]), fabsf(p[n][3])));
-  return scale_for(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+  for (int n = 0; n < kNT; ++n) m = fmax3(m, fabsf(p[n][2 * half]), fabsf(p[n][2 * half + 1]));
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  return scale_for(__float_as_uint(m));
 }
 
-// o[4 u + e] += inv * P B over the tile's rows (B as pairs)
+// o[4 u + e] += P B over the tile's rows (B as pairs), rows g and g + 8 times inv0 and inv1
 template <int DP>
 __device__ __forceinline__ void product_rows(float (&o)[DP / 8][4], const ScoreFrags& p,
-                                             const uint32_t* B, float inv, int g, int t) {
+                                             const uint32_t* B, float inv0, float inv1, int g,
+                                             int t) {
   constexpr int kP = pair_pitch<DP>(), kLo = kTile / 2 * kP;
 #pragma unroll
   for (int u = 0; u < DP / 32; ++u) {
@@ -320,7 +346,8 @@ __device__ __forceinline__ void product_rows(float (&o)[DP / 8][4], const ScoreF
 #pragma unroll
     for (int e = 0; e < 4; ++e)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[4 * u + e][i] = fmaf(sum[e][i], inv, o[4 * u + e][i]);
+      for (int i = 0; i < 4; ++i)
+        o[4 * u + e][i] = fmaf(sum[e][i], i < 2 ? inv0 : inv1, o[4 * u + e][i]);
   }
 }
 
@@ -352,21 +379,21 @@ __device__ __forceinline__ int keys_of(const RelF32& p, int b) {
   return p.mask == 2 ? min(max(__ldg(p.key_len + b), 0), p.Nk) : p.Nk;
 }
 
-// x = s f + t: t the constant, or of the lane's columns 8 n + 2 t, + 1 and rows g, g + 8 from the table
+// x = s f + t (f0, f1: rows g and g + 8): t the constant, or of the lane's columns 8 n + 2 t, + 1 and rows g, g + 8 from the table
 // (at: its entry for column 0 and row g; a row less is a distance more)
-__device__ __forceinline__ void add_bias(float (&s)[kNT][4], float f, bool near, float constant,
-                                         const float* at) {
+__device__ __forceinline__ void add_bias(float (&s)[kNT][4], float f0, float f1, bool near,
+                                         float constant, const float* at) {
   if (near) {
 #pragma unroll
     for (int n = 0; n < kNT; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        s[n][i] = fmaf(s[n][i], f, at[8 * n + (i & 1) - 8 * (i >> 1)]);
+        s[n][i] = fmaf(s[n][i], i < 2 ? f0 : f1, at[8 * n + (i & 1) - 8 * (i >> 1)]);
   } else {
 #pragma unroll
     for (int n = 0; n < kNT; ++n)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[n][i] = fmaf(s[n][i], f, constant);
+      for (int i = 0; i < 4; ++i) s[n][i] = fmaf(s[n][i], i < 2 ? f0 : f1, constant);
   }
 }
 
@@ -376,7 +403,7 @@ struct FwdSmem {
   uint8_t Q[rows_bytes<DP>(kRows)], K[rows_bytes<DP>(kTile)];
   uint32_t V[pairs_bytes<DP>() / 4];
   float rawK[kTile * DP], rawV[kTile * DP];
-  float table[kDist + 1];
+  float table[kDist + 1], q_inv[kRows];
   uint32_t red[2][kWarps];
   RelShared rs;
 };
@@ -404,9 +431,9 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 3 : 2)
     copy_commit();
   };
   for (int s = threadIdx.x; s <= kRelMaxSeg; s += kThreads) rel_load(sm.rs, rel, h, s, 1.f);
-  const float q_inv =
-      own_rows<DP, kVec>(sm.Q, sm.rawK, sm.red[0], p.Q + b * p.st[0][0] + h * p.st[0][1], p.st[0][2],
-                         q0, p.Nq, p.d_k) * p.scale;
+  own_rows<DP, kVec>(sm.Q, sm.q_inv, sm.rawK, p.Q + b * p.st[0][0] + h * p.st[0][1], p.st[0][2], q0,
+                     p.Nq, p.d_k);
+  const float q_inv[2] = {sm.q_inv[16 * warp + g] * p.scale, sm.q_inv[16 * warp + g + 8] * p.scale};
   const int row[2] = {q0 + 16 * warp + g, q0 + 16 * warp + g + 8};
   const int limit[2] = {p.mask == 1 ? row[0] : L - 1, p.mask == 1 ? row[1] : L - 1};
   float o[DP / 8][4] = {};
@@ -445,9 +472,8 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 3 : 2)
     if (p.mask != 1 || j * kTile <= q0 + 16 * warp + 15) {
       float s[kNT][4];
       product_d<DP>(s, sm.Q, 16 * warp, sm.K, g, t);
-      const float f = k_inv * q_inv;
       float mx[2] = {-INFINITY, -INFINITY};
-      add_bias(s, f, near, seg_bias, sm.table + 2 * t - (16 * warp + g) + kRows - 1);
+      add_bias(s, k_inv * q_inv[0], k_inv * q_inv[1], near, seg_bias, sm.table + 2 * t - (16 * warp + g) + kRows - 1);
       if (j * kTile + kTile - 1 > (p.mask == 1 ? q0 + 16 * warp : L - 1)) {
 #pragma unroll
         for (int n = 0; n < kNT; ++n)
@@ -483,7 +509,8 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 3 : 2)
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[u][i] *= alpha[i >> 1];
       }
-      product_rows<DP>(o, ScoreFrags(s, 0x1p14f), sm.V, v_inv * 0x1p-14f, g, t);
+      const float inv = v_inv * 0x1p-14f;
+      product_rows<DP>(o, ScoreFrags(s, 0x1p14f, 0x1p14f), sm.V, inv, inv, g, t);
     }
   }
   float* ob = p.out + b * p.st[3][0] + h * p.st[3][1];
@@ -513,7 +540,7 @@ struct DqSmem {
     float S[kRows * (kTile + 1)];  // dS where segments meet, when K and V are done with
   };
   float rawK[kTile * DP], rawV[kTile * DP];
-  float D[kRows], lse[kRows];
+  float D[kRows], lse[kRows], q_inv[kRows], g_inv[kRows];
   float table[kDist + 1];
   uint32_t red[2][kWarps];
   float far[kWarps];
@@ -546,14 +573,14 @@ __device__ __forceinline__ void queries_part(const RelF32& p, const RelBias& rel
     sm.D[tid] = q0 + tid < p.Nq ? p.Dv[i] : 0.f;
     sm.lse[tid] = q0 + tid < p.Nq ? p.lse[i] : INFINITY;
   }
-  const float q_inv =
-      own_rows<DP, kVec>(sm.Q, sm.rawK, sm.red[0], p.Q + b * p.st[0][0] + h * p.st[0][1], p.st[0][2],
-                         q0, p.Nq, p.d_k) * p.scale;
-  const float g_inv =
-      own_rows<DP, kVec>(sm.G, sm.rawK, sm.red[0], gb, p.st[4][2], q0, p.Nq, p.d_v);
+  own_rows<DP, kVec>(sm.Q, sm.q_inv, sm.rawK, p.Q + b * p.st[0][0] + h * p.st[0][1], p.st[0][2], q0,
+                     p.Nq, p.d_k);
+  own_rows<DP, kVec>(sm.G, sm.g_inv, sm.rawK, gb, p.st[4][2], q0, p.Nq, p.d_v);
   const int r_loc[2] = {16 * warp + g, 16 * warp + g + 8};
   const int limit[2] = {p.mask == 1 ? q0 + r_loc[0] : L - 1, p.mask == 1 ? q0 + r_loc[1] : L - 1};
   const float lse[2] = {sm.lse[r_loc[0]], sm.lse[r_loc[1]]}, D[2] = {sm.D[r_loc[0]], sm.D[r_loc[1]]};
+  const float q_inv[2] = {sm.q_inv[r_loc[0]] * p.scale, sm.q_inv[r_loc[1]] * p.scale};
+  const float g_inv[2] = {sm.g_inv[r_loc[0]], sm.g_inv[r_loc[1]]};
   float dq[DP / 8][4] = {};
   float far = 0.f, own = 0.f;
   int seg = 0, seg_next = INT_MIN;
@@ -605,8 +632,9 @@ __device__ __forceinline__ void queries_part(const RelF32& p, const RelBias& rel
       float dp[kNT][4];
       product_d<DP>(s, sm.Q, 16 * warp, sm.K, g, t);
       product_d<DP>(dp, sm.G, 16 * warp, sm.V, g, t);
-      const float f = k_inv * q_inv, fg = v_inv * g_inv;
-      add_bias(s, f, near, seg_bias, sm.table + 2 * t - r_loc[0] + kRows - 1);
+      const float fg[2] = {v_inv * g_inv[0], v_inv * g_inv[1]};
+      add_bias(s, k_inv * q_inv[0], k_inv * q_inv[1], near, seg_bias,
+               sm.table + 2 * t - r_loc[0] + kRows - 1);
       if (j * kTile + kTile - 1 > (p.mask == 1 ? q0 + 16 * warp : L - 1)) {
 #pragma unroll
         for (int n = 0; n < kNT; ++n)
@@ -618,7 +646,8 @@ __device__ __forceinline__ void queries_part(const RelF32& p, const RelBias& rel
       for (int n = 0; n < kNT; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          s[n][i] = ex2_approx((s[n][i] - lse[i >> 1]) * kLog2e) * fmaf(dp[n][i], fg, -D[i >> 1]);
+          s[n][i] = ex2_approx((s[n][i] - lse[i >> 1]) * kLog2e) *
+                    fmaf(dp[n][i], fg[i >> 1], -D[i >> 1]);
     }
     if (near) {
       __syncthreads();  // K and V as rows are done with
@@ -632,8 +661,9 @@ __device__ __forceinline__ void queries_part(const RelF32& p, const RelBias& rel
       for (int n = 0; n < kNT; ++n) far += (s[n][0] + s[n][1]) + (s[n][2] + s[n][3]);
     }
     if (!skip) {
-      const Scale f = score_scale(s);
-      product_rows<DP>(dq, ScoreFrags(s, f.mul), sm.Kp, f.inv * k_inv, g, t);
+      const Scale f0 = score_scale(s, 0), f1 = score_scale(s, 1);
+      product_rows<DP>(dq, ScoreFrags(s, f0.mul, f1.mul), sm.Kp, f0.inv * k_inv, f1.inv * k_inv, g,
+                       t);
     }
     if (near) {  // sums over the diagonals, one per thread, then over each warp's segments
       __syncthreads();
@@ -679,7 +709,7 @@ struct DkdvSmem {
   uint8_t Q[rows_bytes<DP>(kTile)], G[rows_bytes<DP>(kTile)];  // G: dO
   uint32_t Qp[pairs_bytes<DP>() / 4], Gp[pairs_bytes<DP>() / 4];
   float rawQ[kTile * DP], rawG[kTile * DP];
-  float D[kTile], lse[kTile];
+  float D[kTile], lse[kTile], k_inv[kRows], v_inv[kRows];
   float table[kDist + 1];
   uint32_t red[2][kWarps];
   RelShared rs;
@@ -706,12 +736,13 @@ __device__ __forceinline__ void keys_part(const RelF32& p, const RelBias& rel, D
       copy_commit();
     };
     for (int s = tid; s <= kRelMaxSeg; s += kThreads) rel_load(sm.rs, rel, h, s, 1.f);
-    const float k_inv =
-        own_rows<DP, kVec>(sm.K, sm.rawQ, sm.red[0], p.K + b * p.st[1][0] + h * p.st[1][1],
-                           p.st[1][2], k0, L, p.d_k) * p.scale;
-    const float v_inv =
-        own_rows<DP, kVec>(sm.V, sm.rawQ, sm.red[0], p.V + b * p.st[2][0] + h * p.st[2][1],
-                           p.st[2][2], k0, L, p.d_v);
+    own_rows<DP, kVec>(sm.K, sm.k_inv, sm.rawQ, p.K + b * p.st[1][0] + h * p.st[1][1], p.st[1][2],
+                       k0, L, p.d_k);
+    own_rows<DP, kVec>(sm.V, sm.v_inv, sm.rawQ, p.V + b * p.st[2][0] + h * p.st[2][1], p.st[2][2],
+                       k0, L, p.d_v);
+    const int r = 16 * warp + g;
+    const float k_inv[2] = {sm.k_inv[r] * p.scale, sm.k_inv[r + 8] * p.scale};
+    const float v_inv[2] = {sm.v_inv[r], sm.v_inv[r + 8]};
     int seg_start = INT_MAX;
     float seg_bias = 0.f;
     load(i0);
@@ -750,7 +781,8 @@ __device__ __forceinline__ void keys_part(const RelF32& p, const RelBias& rel, D
       float s[kNT][4], ds[kNT][4];
       product_d<DP>(s, sm.K, 16 * warp, sm.Q, g, t);
       product_d<DP>(ds, sm.V, 16 * warp, sm.G, g, t);
-      const float f = q_inv * k_inv, fg = g_inv * v_inv;
+      const float f[2] = {q_inv * k_inv[0], q_inv * k_inv[1]};
+      const float fg[2] = {g_inv * v_inv[0], g_inv * v_inv[1]};
       // the table by row (key) minus column (query): a row more is a distance more
       if (near) {
         const float* at = sm.table + 16 * warp + g - 2 * t + kTile - 1;
@@ -758,12 +790,12 @@ __device__ __forceinline__ void keys_part(const RelF32& p, const RelBias& rel, D
         for (int n = 0; n < kNT; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            s[n][e] = fmaf(s[n][e], f, at[8 * (e >> 1) - 8 * n - (e & 1)]);
+            s[n][e] = fmaf(s[n][e], f[e >> 1], at[8 * (e >> 1) - 8 * n - (e & 1)]);
       } else {
 #pragma unroll
         for (int n = 0; n < kNT; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[n][e] = fmaf(s[n][e], f, seg_bias);
+          for (int e = 0; e < 4; ++e) s[n][e] = fmaf(s[n][e], f[e >> 1], seg_bias);
       }
       if (k0 + 16 * warp + 15 >= L || (p.mask == 1 && k0 + 16 * warp + 15 > q0)) {
 #pragma unroll
@@ -781,12 +813,14 @@ __device__ __forceinline__ void keys_part(const RelF32& p, const RelBias& rel, D
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           s[n][e] = ex2_approx((s[n][e] - (e & 1 ? lse.y : lse.x)) * kLog2e);
-          ds[n][e] = s[n][e] * fmaf(ds[n][e], fg, -(e & 1 ? D.y : D.x));
+          ds[n][e] = s[n][e] * fmaf(ds[n][e], fg[e >> 1], -(e & 1 ? D.y : D.x));
         }
       }
-      const Scale fs = score_scale(s), fd = score_scale(ds);
-      product_rows<DP>(dv, ScoreFrags(s, fs.mul), sm.Gp, fs.inv * g_inv, g, t);
-      product_rows<DP>(dk, ScoreFrags(ds, fd.mul), sm.Qp, fd.inv * q_inv, g, t);
+      const Scale s0 = score_scale(s, 0), s1 = score_scale(s, 1);
+      product_rows<DP>(dv, ScoreFrags(s, s0.mul, s1.mul), sm.Gp, s0.inv * g_inv, s1.inv * g_inv, g, t);
+      const Scale d0s = score_scale(ds, 0), d1s = score_scale(ds, 1);
+      product_rows<DP>(dk, ScoreFrags(ds, d0s.mul, d1s.mul), sm.Qp, d0s.inv * q_inv, d1s.inv * q_inv,
+                       g, t);
     }
   }
   float* ok = p.dK + b * p.st[6][0] + h * p.st[6][1];
