@@ -833,9 +833,11 @@ __device__ __forceinline__ void keys_part(const RelF32& p, const RelBias& rel, D
     }
 }
 
-// A CTA takes 64 queries or 64 keys of a head, in turn along x while there are both, those with the most
-// tiles to go over first under the causal mask: one launch keeps the GPU filled where one kind alone
-// leaves it waiting for its longest CTAs (4 x 8 heads of 500, causal: 112 us in two launches, xx in one).
+// A CTA takes 64 keys or 64 queries of a head: one launch keeps the GPU filled where one kind alone would
+// leave it waiting for its longest CTAs (4 x 8 heads of 500, causal: 112 us in two launches, 101 in one;
+// 2 x 8 heads of 500 122 and 75).  A tile takes a CTA alone on its SM 4 us and two CTAs 2 us each: what
+// bounds it is latency between barriers with eight warps on an SM; 228 registers and 86 KB of shared
+// memory leave no third CTA room.
 template <int DP>
 struct BwdSmem {
   union {
@@ -851,12 +853,11 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
   extern __shared__ __align__(16) uint8_t smem[];
   BwdSmem<DP>& sm = *reinterpret_cast<BwdSmem<DP>*>(smem);
   const int x = static_cast<int>(blockIdx.x);
-  const int nq = (p.Nq + kRows - 1) / kRows, nk = (p.Nk + kRows - 1) / kRows, both = min(nq, nk);
-  const int i = x < 2 * both ? x >> 1 : x - both;
-  if (x < 2 * both ? (x & 1) == 0 : nq > nk)
-    queries_part<DP, kVec>(p, rel, sm.q, p.mask == 1 ? nq - 1 - i : i, nq);
-  else
-    keys_part<DP, kVec>(p, rel, sm.k, i);
+  const int nq = (p.Nq + kRows - 1) / kRows, nk = (p.Nk + kRows - 1) / kRows;
+  if (x < nk)
+    keys_part<DP, kVec>(p, rel, sm.k, x);
+  else  // the longest first under the causal mask, as the keys
+    queries_part<DP, kVec>(p, rel, sm.q, p.mask == 1 ? nq - 1 - (x - nk) : x - nk, nq);
 }
 
 // the gradient of the table alone, one block per head
