@@ -54,7 +54,7 @@ struct RelF32 {
   float* lse;                  // forward: written if not null; backward: read
   const float* Dv;             // backward: [B, H, Nq] rowsum(dO O)
   int64_t st[8][3];            // strides b, h, n of Q, K, V, O, dO, dQ, dK, dV (d: 1)
-  int H, Nq, Nk, d_k, d_v, mask;
+  int B, H, Nq, Nk, d_k, d_v, mask;
   const int32_t* key_len;
   float scale;
 };
@@ -552,9 +552,9 @@ struct DqSmem {
 // 64 queries' dQ and their sums of dS per segment (thread s owns segment s)
 template <int DP, bool kVec>
 __device__ __forceinline__ void queries_part(const RelF32& p, const RelBias& rel, DqSmem<DP>& sm,
-                                             int tile, int tiles) {
+                                             int h, int b, int tile, int tiles) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int h = blockIdx.y, b = blockIdx.z, q0 = tile * kRows;
+  const int q0 = tile * kRows;
   const int L = keys_of(p, b);
   const int last = min(q0 + kRows, p.Nq) - 1;
   const int nt = p.mask == 1 ? last / kTile + 1 : (L + kTile - 1) / kTile;
@@ -718,9 +718,9 @@ struct DkdvSmem {
 // 64 keys' dK and dV from tiles of 32 queries
 template <int DP, bool kVec>
 __device__ __forceinline__ void keys_part(const RelF32& p, const RelBias& rel, DkdvSmem<DP>& sm,
-                                          int tile) {
+                                          int h, int b, int tile) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int h = blockIdx.y, b = blockIdx.z, k0 = tile * kRows;
+  const int k0 = tile * kRows;
   const int L = keys_of(p, b);
   const int64_t bh = static_cast<int64_t>(b) * p.H + h;
   const TileCopy<DP, kVec> copy_q(p.Q + b * p.st[0][0] + h * p.st[0][1], p.st[0][2], p.Nq, p.d_k);
@@ -833,11 +833,12 @@ __device__ __forceinline__ void keys_part(const RelF32& p, const RelBias& rel, D
     }
 }
 
-// A CTA takes 64 keys or 64 queries of a head: one launch keeps the GPU filled where one kind alone would
-// leave it waiting for its longest CTAs (4 x 8 heads of 500, causal: 112 us in two launches, 101 in one;
-// 2 x 8 heads of 500 122 and 75).  A tile takes a CTA alone on its SM 4 us and two CTAs 2 us each: what
-// bounds it is latency between barriers with eight warps on an SM; 228 registers and 86 KB of shared
-// memory leave no third CTA room.
+// A CTA takes 64 keys or 64 queries of a head, first the keys of all heads, then the queries: one launch
+// keeps the GPU filled where one kind alone would leave it waiting for its longest CTAs (4 x 8 heads of
+// 500, causal: 112 us in two launches, 77 in one), and the two kinds' code meets on an SM only in
+// between (keys and queries of a head side by side, 8 x 8 heads of 1001: 858 us).  A tile takes a
+// CTA alone on its SM 4 us and two CTAs 2 us each: what bounds it is latency between barriers with
+// eight warps on an SM; 228 registers and 86 KB of shared memory leave no third CTA room.
 template <int DP>
 struct BwdSmem {
   union {
@@ -852,12 +853,20 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1)
   pdl_wait();  // the previous kernel's output (D among it) is complete from here on
   extern __shared__ __align__(16) uint8_t smem[];
   BwdSmem<DP>& sm = *reinterpret_cast<BwdSmem<DP>*>(smem);
-  const int x = static_cast<int>(blockIdx.x);
-  const int nq = (p.Nq + kRows - 1) / kRows, nk = (p.Nk + kRows - 1) / kRows;
-  if (x < nk)
-    keys_part<DP, kVec>(p, rel, sm.k, x);
-  else  // the longest first under the causal mask, as the keys
-    queries_part<DP, kVec>(p, rel, sm.q, p.mask == 1 ? nq - 1 - (x - nk) : x - nk, nq);
+  const uint32_t nq = (p.Nq + kRows - 1) / kRows, nk = (p.Nk + kRows - 1) / kRows;
+  const uint32_t heads = static_cast<uint32_t>(p.B) * p.H;
+  const bool keys = blockIdx.x < heads * nk;
+  const uint32_t x = keys ? blockIdx.x : blockIdx.x - heads * nk, tiles = keys ? nk : nq;
+  uint32_t bh = x / tiles, tile = x % tiles;
+  if (p.mask == 1) {  // the longest of all heads first
+    bh = x % heads;
+    tile = keys ? x / heads : tiles - 1 - x / heads;
+  }
+  const int h = static_cast<int>(bh % p.H), b = static_cast<int>(bh / p.H);
+  if (keys)
+    keys_part<DP, kVec>(p, rel, sm.k, h, b, static_cast<int>(tile));
+  else
+    queries_part<DP, kVec>(p, rel, sm.q, h, b, static_cast<int>(tile), static_cast<int>(tiles));
 }
 
 // the gradient of the table alone, one block per head
@@ -895,7 +904,7 @@ cudaError_t launch_sdpa_rel_f32(const SdpaArgs& a, const RelBias& rel, cudaStrea
   const int64_t* st[4] = {a.sq, a.sk, a.sv, a.so};
   for (int t = 0; t < 4; ++t)
     for (int i = 0; i < 3; ++i) p.st[t][i] = st[t][i];
-  p.H = a.H; p.Nq = a.Nq; p.Nk = a.Nk; p.d_k = a.d_k; p.d_v = a.d_v;
+  p.B = a.B; p.H = a.H; p.Nq = a.Nq; p.Nk = a.Nk; p.d_k = a.d_k; p.d_v = a.d_v;
   p.mask = a.mask;
   p.key_len = a.key_len;
   p.scale = a.scale;
@@ -932,13 +941,16 @@ cudaError_t launch_sdpa_rel_bwd_f32(const SdpaBwdArgs& a, const RelBias& rel, vo
     for (int i = 0; i < 3; ++i) p.st[t][i] = a.st[t][i];
     if (t != 3) vec = vec && quads(ptr[t], p.st[t], dims[t]);
   }
-  p.H = a.H; p.Nq = a.Nq; p.Nk = a.Nk; p.d_k = a.d_k; p.d_v = a.d_v;
+  p.B = a.B; p.H = a.H; p.Nq = a.Nq; p.Nk = a.Nk; p.d_k = a.d_k; p.d_v = a.d_v;
   p.mask = a.mask;
   p.key_len = a.key_len;
   p.scale = a.scale;
   cudaError_t e = launch_sdpa_bwd_rowdot(a, 0, s);  // D
   if (e != cudaSuccess) return e;
-  const dim3 grid((a.Nq + kRows - 1) / kRows + (a.Nk + kRows - 1) / kRows, a.H, a.B);
+  const int64_t blocks = static_cast<int64_t>(a.B) * a.H *
+                         ((a.Nq + kRows - 1) / kRows + (a.Nk + kRows - 1) / kRows);
+  if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;  // 64 rows each: past any memory
+  const dim3 grid(static_cast<unsigned>(blocks));
   if (a.d_k <= 64 && a.d_v <= 64)
     e = vec ? go(sdpa_rel_bwd_f32_kernel<64, true>, grid, sizeof(BwdSmem<64>), p, rel, s)
             : go(sdpa_rel_bwd_f32_kernel<64, false>, grid, sizeof(BwdSmem<64>), p, rel, s);
