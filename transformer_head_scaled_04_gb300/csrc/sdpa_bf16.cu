@@ -330,7 +330,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       [[maybe_unused]] bool from_table = false;
       if constexpr (kRel) {
         const int d0 = (kt0 + j) * kBKV - (wr0 + 31);  // the warp's smallest distance
-        from_table = waiting || d0 + kBKV + 30 >= seg_next;
+        from_table = waiting || d0 + kBKV + 30 >= seg_next ||
+                     (p.mask == 2 && j == nt - 1);  // where rows past key_len are dealt with
         if (from_table) {
           constexpr int kN = kRelTable / 32;
           int d[kN], seg[kN];
@@ -396,7 +397,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         // excluded keys get -inf (p = 0): one compare against a per-row bound per key,
         // one-sided where no row of the warp has the other end inside the tile
         if constexpr (kRel) {
-          if (mask_hi && (!kNear || p.mask != 1)) {  // the table has the causal mask
+          // (the table has the causal mask)
+          if (mask_hi && (kNear ? p.mask != 1 : p.mask == 0)) {
 #pragma unroll
             for (int q = 0; q < 128; ++q) sv[q] = q > hi ? -INFINITY : sv[q];
           }
@@ -516,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           tmem_st32(tP + 32, hi32);
         }
         l += tile_sum;
-        if constexpr (kRel) {
+        if constexpr (kRel && kNear) {
           // rows of V past key_len may hold anything, and 0 times that may not be 0
           if (p.mask == 2 && j == nt - 1 && (kt0 + j + 1) * kBKV > L) {
             if (!warp_all(mbar_wait(bar(kBarVFull + j % kVRing), (j / kVRing) & 1, p.timeout_ns))) {

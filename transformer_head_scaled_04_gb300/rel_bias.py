@@ -83,10 +83,7 @@ def _forward(what, q, k, v, rel_bias, mask, key_len, scale, max_distance, bidire
         out = _new(q, B, H, Nq, d_v)
     else:
         _same(out, q, (B, H, Nq, d_v), dev, f"{what}: out")
-    if lse:
-        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
-    else:
-        lse = None
+    lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device) if lse else None
     _call(dev, "mha_sdpa_rel_fwd", B, H, Nq, Nk, d_k, d_v, dt, _mask(mask), _p(key_len),
           float(scale or 0.0), q.data_ptr(), k.data_ptr(), v.data_ptr(), rel_bias.data_ptr(), bt,
           nb, int(max_distance), 1 if bidirectional else 0, out.data_ptr(),
