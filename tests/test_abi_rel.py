@@ -136,6 +136,15 @@ def test_sizes_and_buckets(lib):
         mha.rel_bucket(1, 32, 8)
 
 
+def test_numbers_past_an_int(lib):
+    assert mha.rel_bucket(2 ** 32) == mha.rel_bucket(10 ** 6) == 31
+    assert mha.rel_bucket(-2 ** 32 - 3) == mha.rel_bucket(-10 ** 6) == 15
+    for kw in (dict(max_distance=2 ** 32 + 128), dict(num_buckets=2 ** 32 + 32),
+               dict(max_distance=-2 ** 32 + 128)):
+        with pytest.raises(C.MhaError):
+            mha.rel_bucket(3, **kw)
+
+
 def test_wrappers_refuse_host_tensors():
     x = torch.zeros(1, 2, 4, 64)
     t = torch.zeros(32, 2)

@@ -17,9 +17,14 @@ from .api import _DTYPES, _dt, _mask
 from .cache_q8 import _call, _dense, _i32, _p, _same, _workspace
 
 
+def _int(n):
+    """n as the C ABI's int holds it: what lies past it is as good as its ends."""
+    return max(-2 ** 31, min(2 ** 31 - 1, int(n)))
+
+
 def rel_bucket(distance, num_buckets=32, max_distance=128, bidirectional=True) -> int:
     """The bucket of ``distance`` (key's position - query's position) via ``mha_rel_bucket``."""
-    u = C.load().mha_rel_bucket(int(distance), int(num_buckets), int(max_distance),
+    u = C.load().mha_rel_bucket(_int(distance), _int(num_buckets), _int(max_distance),
                                 1 if bidirectional else 0)
     if u < 0:
         C.check(u, "mha_rel_bucket")
@@ -86,7 +91,7 @@ def _forward(what, q, k, v, rel_bias, mask, key_len, scale, max_distance, bidire
     lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device) if lse else None
     _call(dev, "mha_sdpa_rel_fwd", B, H, Nq, Nk, d_k, d_v, dt, _mask(mask), _p(key_len),
           float(scale or 0.0), q.data_ptr(), k.data_ptr(), v.data_ptr(), rel_bias.data_ptr(), bt,
-          nb, int(max_distance), 1 if bidirectional else 0, out.data_ptr(),
+          nb, _int(max_distance), 1 if bidirectional else 0, out.data_ptr(),
           _strides(q, k, v, out), _p(lse))
     return out, lse
 
@@ -140,7 +145,7 @@ def sdpa_rel_backward(q, k, v, rel_bias, o, do, lse, mask="none", key_len=None, 
                            what)
     _call(dev, "mha_sdpa_rel_bwd", B, H, Nq, Nk, d_k, d_v, dt, _mask(mask), _p(key_len),
           float(scale or 0.0), q.data_ptr(), k.data_ptr(), v.data_ptr(), rel_bias.data_ptr(), bt,
-          nb, int(max_distance), 1 if bidirectional else 0, o.data_ptr(), do.data_ptr(),
+          nb, _int(max_distance), 1 if bidirectional else 0, o.data_ptr(), do.data_ptr(),
           lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dbias.data_ptr(),
           _strides(q, k, v, o, do, dq, dk, dv), workspace.data_ptr(), workspace.numel())
     return dq, dk, dv, dbias
@@ -181,7 +186,7 @@ def sdpa_rel_decode(q, k_cache, v_cache, rel_bias, cache_len, causal=True, scale
         _workspace(workspace, 0, q, dev, what)
     _call(dev, "mha_sdpa_rel_decode_fwd", B, H, Nq, Lmax, d_k, d_v, dt, 1 if causal else 0,
           cache_len.data_ptr(), float(scale or 0.0), q.data_ptr(), k_cache.data_ptr(),
-          v_cache.data_ptr(), rel_bias.data_ptr(), bt, nb, int(max_distance),
+          v_cache.data_ptr(), rel_bias.data_ptr(), bt, nb, _int(max_distance),
           1 if bidirectional else 0, out.data_ptr(), _strides(q, k_cache, v_cache, out),
           _p(workspace), 0 if workspace is None else workspace.numel())
     return out
