@@ -25,7 +25,7 @@
  *   - Row-major layouts; "stride" always counts ELEMENTS, not bytes.
  *   - dtype MHA_BF16: bf16 storage, fp32 accumulation, bf16 (round-to-nearest-even) outputs,
  *     tensor-core (tcgen05) kernels.  dtype MHA_F32: fp32 storage and arithmetic (SIMT
- *     kernels, no TF32).
+ *     kernels, no TF32, where an entry point does not say otherwise).
  *   - Return value: MHA_OK or a negative mha_status.  Argument errors are found on the host
  *     before anything is launched.  MHA_ERR_CUDA means a CUDA launch or API call failed.
  *     Device-side problems (a bounded wait that ran out) are recorded in a device status
@@ -326,9 +326,16 @@ int mha_kv_evict_q8(int B, int H, int Lmax, int Lmax_out, int d_k, int d_v, int 
  *            max_distance > e (and < 2^24), from which on all distances share a side's last bucket.
  *   lengths  up to 2^24 positions.
  *   scale    as for mha_sdpa_fwd, within [2^-64, 2^64] where it is given.
- *   d_k, d_v bf16: 64.  fp32: 1..128, computed on the tensor cores with every value split into two
- *            tf32 terms (relative error 2^-22 per factor; sums in fp32).
- * Keys past key_len[b] (cache_len[b]) may hold anything, infinities and NaN included.
+ *   d_k, d_v bf16: 64.  fp32: 1..128.  Unlike the other fp32 entry points these use the tensor cores:
+ *            forward and backward split every value into two fp16 terms under power-of-two scales (off
+ *            by at most 2^-23 of the value or 2^-39 of the largest one that it shares a scale with, in
+ *            its row or in 32 neighbouring rows), the generation step takes fused multiply-adds for
+ *            Nq <= 2 and two tf32 terms per value for more (2^-22 of the value).  Sums are fp32.
+ *   special  Keys past key_len[b] (cache_len[b]) may hold anything, infinities and NaN included.  Under
+ *   values   the causal mask an infinity or NaN in a row of K reaches only queries that see the key, but
+ *            one in V may reach any query (0 times it is no number), and so may one in the backward.
+ *            fp32: a query that sees an infinity in K gets NaN.
+ *   aliasing outputs (and the workspace) may not overlap inputs or one another.
  */
 
 /*

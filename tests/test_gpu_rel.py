@@ -250,6 +250,33 @@ def test_anything_in_padding(dtype, bad, det_mode):
     assert torch.all(O[1] == 0) and torch.all(lse[1] == np.inf) and torch.all(dq[1] == 0)
 
 
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
+def test_keys_to_come_may_hold_anything(dtype, bad):
+    # under the causal mask: queries before the key keep their results, to the bit where none after it
+    # shares their warp (a raised reference of the exponentials takes the warp's other rows along)
+    B, H, N, j = 2, 2, 300, 137
+    Q, K, V, _, T = draw(B, H, N, N, dtype, 907)
+    K[:, :, j] = 0.0  # so that the row leaves the others' scales as they are
+    q, k, v, t = dev(Q, dtype), dev(K, dtype), dev(V, dtype), dev(T, F)
+    want = mha.sdpa_rel_with_lse(q, k, v, t, mask="causal")
+    k[:, :, j] = bad
+    got = mha.sdpa_rel_with_lse(q, k, v, t, mask="causal")
+    for a, b in zip(want, got):
+        assert torch.equal(a[:, :, :128], b[:, :, :128])
+    # weights and outputs rounded to bf16 in both (each half a step of at most max |V|); fp32: 2^-22 of
+    # a term, exponentials 2^-21
+    tol = (4 * 2.0 ** -8 if dtype is BF else 2.0 ** -18) * float(v.abs().max())
+    assert float((want[0] - got[0])[:, :, :j].abs().max()) <= tol
+    assert float((want[1] - got[1])[:, :, :j].abs().max()) <= 1e-5  # logarithms of about 10
+    if not bad == bad:
+        assert torch.all(torch.isnan(got[0][:, :, j:]))
+    # and in a step of several queries
+    n, Nq = i32([N, 140]), 5
+    step = [mha.sdpa_rel_decode(q[:, :, :Nq].contiguous(), c, v, t, n) for c in (dev(K, dtype), k)]
+    assert float((step[0] - step[1])[1, :, :2].abs().max()) <= tol  # positions 135 and 136
+
+
 def test_reproducible_and_determinism_switch(det_mode):
     Q, K, V, dO, T = draw(2, 3, 700, 700, BF, 905)
     q, k, v, g, t = (dev(a, BF) for a in (Q, K, V, dO, T))

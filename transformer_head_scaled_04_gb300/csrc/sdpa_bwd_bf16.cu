@@ -905,7 +905,7 @@ __global__ void __launch_bounds__(kKThreads, 1)
       }
       // Rel: a step that takes the table and one of two blocks of one segment each run code of their
       // own, with marks at both ends that keep the compiler from merging parts of them: moves between
-      // the variants' registers cost 200 instructions a step (2025 us for the big model's heads)
+      // the variants' registers cost 200 instructions a step (2025 us for the big model's heads, 1669 so)
       auto step = [&](auto kind) -> bool {
         [[maybe_unused]] constexpr bool kTable = decltype(kind)::value;
         tc_fence_after();

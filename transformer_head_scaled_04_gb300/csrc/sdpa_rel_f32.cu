@@ -11,7 +11,7 @@
 // summed over, one for its tile of 32 rows.  What is left of a value is at most 2^-23 of it or 2^-39 of
 // the largest that shares its scale, and the dropped lo lo is at most 2^-22 of the product: fp32's own
 // accuracy.  (Two tf32 terms give the same at twice the time of the tensor cores: 8 x 8 heads of 1001
-// forward 322 us, with fp16 215.)  The tensor cores cut sums
+// forward 322 us, with fp16 220.)  The tensor cores cut sums
 // off instead of rounding them, 2^-24 of the sum per step towards zero (9e-6 of a gradient over 900
 // keys in one chain), so the large products are kept apart from the small ones, a chain spans one
 // tile at most, and tiles are added up with ordinary additions.
@@ -151,6 +151,17 @@ struct Share {
       m = fmaxf(fmax3(m, fabsf(a[i].x), fabsf(a[i].y)), fmaxf(fabsf(a[i].z), fabsf(a[i].w)));
       m = fmaxf(fmax3(m, fabsf(b[i].x), fabsf(b[i].y)), fmaxf(fabsf(b[i].z), fabsf(b[i].w)));
     }
+    return __float_as_uint(m);
+  }
+  // that of its largest finite one
+  __device__ __forceinline__ uint32_t finite() const {
+    float m = 0.f;
+    auto take = [&m](const float4& x) {
+      for (float v : {x.x, x.y, x.z, x.w})
+        if (fabsf(v) < INFINITY) m = fmaxf(m, fabsf(v));
+    };
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) take(a[i]), take(b[i]);
     return __float_as_uint(m);
   }
   // writes its terms as rows (at row0 of an array of `rows`) and as pairs, either may be null
@@ -379,8 +390,8 @@ __device__ __forceinline__ int keys_of(const RelF32& p, int b) {
   return p.mask == 2 ? min(max(__ldg(p.key_len + b), 0), p.Nk) : p.Nk;
 }
 
-// x = s f + t (f0, f1: rows g and g + 8): t the constant, or of the lane's columns 8 n + 2 t, + 1 and rows g, g + 8 from the table
-// (at: its entry for column 0 and row g; a row less is a distance more)
+// x = s f + t (f0, f1: rows g and g + 8): t the constant, or of the lane's columns 8 n + 2 t, + 1 and
+// rows g, g + 8 from the table (at: its entry for column 0 and row g; a row less is a distance more)
 __device__ __forceinline__ void add_bias(float (&s)[kNT][4], float f0, float f1, bool near,
                                          float constant, const float* at) {
   if (near) {
@@ -457,11 +468,18 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 3 : 2)
     float k_inv, v_inv;
     {
       Share<DP> k, v;
-      const uint32_t tk = __reduce_max_sync(0xffffffffu, k.read(sm.rawK));
-      const uint32_t tv = block_max(v.read(sm.rawV), (sm.red[1][warp] = tk, sm.red[0]));
-      const Scale fk = scale_for(max(max(sm.red[1][0], sm.red[1][1]),
-                                     max(sm.red[1][2], sm.red[1][3])));
-      const Scale fv = scale_for(tv);
+      uint32_t tk = 0, tv = 0;
+      auto tops = [&](uint32_t ks, uint32_t vs) {
+        ks = __reduce_max_sync(0xffffffffu, ks);
+        tv = block_max(vs, (sm.red[1][warp] = ks, sm.red[0]));
+        tk = max(max(sm.red[1][0], sm.red[1][1]), max(sm.red[1][2], sm.red[1][3]));
+      };
+      tops(k.read(sm.rawK), v.read(sm.rawV));
+      if (max(tk, tv) == 0x7f800000u) {  // an infinity leaves the keys that a row sees their scale
+        __syncthreads();
+        tops(k.finite(), v.finite());
+      }
+      const Scale fk = scale_for(tk), fv = scale_for(tv);
       k.write(fk.mul, sm.K, kTile, 0, nullptr);
       v.write(fv.mul, nullptr, 0, 0, sm.V);
       k_inv = fk.inv;
@@ -473,7 +491,8 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 3 : 2)
       float s[kNT][4];
       product_d<DP>(s, sm.Q, 16 * warp, sm.K, g, t);
       float mx[2] = {-INFINITY, -INFINITY};
-      add_bias(s, k_inv * q_inv[0], k_inv * q_inv[1], near, seg_bias, sm.table + 2 * t - (16 * warp + g) + kRows - 1);
+      add_bias(s, k_inv * q_inv[0], k_inv * q_inv[1], near, seg_bias,
+               sm.table + 2 * t - (16 * warp + g) + kRows - 1);
       if (j * kTile + kTile - 1 > (p.mask == 1 ? q0 + 16 * warp : L - 1)) {
 #pragma unroll
         for (int n = 0; n < kNT; ++n)
