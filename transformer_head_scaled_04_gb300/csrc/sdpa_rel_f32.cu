@@ -11,7 +11,7 @@
 // summed over, one for its tile of 32 rows.  What is left of a value is at most 2^-23 of it or 2^-39 of
 // the largest that shares its scale, and the dropped lo lo is at most 2^-22 of the product: fp32's own
 // accuracy.  (Two tf32 terms give the same at twice the time of the tensor cores: 8 x 8 heads of 1001
-// forward 322 us, with fp16 220.)  The tensor cores cut sums
+// forward 322 us, with fp16 223 then.)  The tensor cores cut sums
 // off instead of rounding them, 2^-24 of the sum per step towards zero (9e-6 of a gradient over 900
 // keys in one chain), so the large products are kept apart from the small ones, a chain spans one
 // tile at most, and tiles are added up with ordinary additions.
@@ -23,9 +23,13 @@
 //          neighbouring d, as the inner positions of two steps (any order of the inner dimension
 //          gives the same sum); 16-byte units of odd rows are swapped by 4, which frees the reads of
 //          bank conflicts
-//   pairs  [row / 2][d] words of two rows' halves, for products over rows: the inner positions of a
-//          score fragment are the columns a lane holds, 2 t and 2 t + 1, and the output's columns are
-//          d = 4 g + e + 32 u, so that a lane reads the words of four d at once
+//   pairs  words of two neighbouring rows' halves, for products over rows: the inner positions of a
+//          score fragment are the columns a lane holds, 2 t and 2 t + 1, and 2 t + 8 and + 9, whose two
+//          words for a d lie side by side, so that 16 bytes are the fragments of two d; the output's
+//          columns are d = 16 v + 2 g + e
+// and the CTA's own rows once into fragments, 16 bytes per lane and step: a lane's registers are filled
+// in the order in which the product takes them, with no moves between (8 x 8 heads of 1001: with moves
+// and unpaired arithmetic 223 us forward and 768 backward, without 196 and 705),
 // so that scores go into the next product without any exchange.  d is padded to 64 or 128 with zeros.
 // The bias of a tile that lies within one segment is a constant; otherwise the CTA looks its distances
 // up once into a table.  Bound by the products: three per multiply-add of the formulas, and in the
@@ -47,6 +51,7 @@ constexpr int kTile = 32;   // rows of the other operand's tile
 constexpr int kNT = kTile / 8;
 constexpr int kDist = kRows + kTile - 1;  // distances of a tile
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
 struct RelF32 {
   const float *Q, *K, *V, *dO;
@@ -120,7 +125,7 @@ __device__ __forceinline__ int unit_at(int r, int u) {
 }
 template <int DP>
 __host__ __device__ constexpr int pair_pitch() {
-  return DP + 8;  // words
+  return 2 * DP + 8;  // words of a group: row pairs 8 s + t and 8 s + t + 4, group 4 s + t
 }
 template <int DP>
 __host__ __device__ constexpr int rows_bytes(int rows) {
@@ -128,95 +133,124 @@ __host__ __device__ constexpr int rows_bytes(int rows) {
 }
 template <int DP>
 __host__ __device__ constexpr int pairs_bytes() {
-  return 2 * kTile / 2 * pair_pitch<DP>() * 4;
+  return 2 * kTile / 4 * pair_pitch<DP>() * 4;
 }
 
-// This thread's share of a raw tile: two rows x four columns per item.
+// the halves of x, and what they leave, rounded to halves
+__device__ __forceinline__ uint32_t halves(float2 x) { return pack_half(x.x, x.y); }
+__device__ __forceinline__ uint32_t rest_of(float2 x, uint32_t hi) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  return halves(ffma2(f, make_float2(-1.f, -1.f), x));
+}
+
+// This thread's share of a raw tile: per item four columns of the rows of two pairs, 8 s + t and
+// 8 s + t + 4.
 template <int DP>
 struct Share {
-  static constexpr int kItems = kTile / 2 * (DP / 4) / kThreads;
-  float4 a[kItems], b[kItems];
-  __device__ __forceinline__ static int pair(int i) { return (i * kThreads + threadIdx.x) / (DP / 4); }
+  static constexpr int kItems = kTile / 4 * (DP / 4) / kThreads;
+  float4 x[kItems][4];
+  __device__ __forceinline__ static int group(int i) { return (i * kThreads + threadIdx.x) / (DP / 4); }
   __device__ __forceinline__ static int col(int i) {
     return (i * kThreads + threadIdx.x) % (DP / 4) * 4;
+  }
+  __device__ __forceinline__ static int row(int i, int k) {  // of x[i][k]
+    return 16 * (group(i) >> 2) + 2 * (group(i) & 3) + (k & 1) + 8 * (k >> 1);
+  }
+  __device__ __forceinline__ static float top(const float4& v) {
+    return fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
   }
   // reads the share; the bits of its largest |value|
   __device__ __forceinline__ uint32_t read(const float* raw) {
     float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-      const float* at = raw + 2 * pair(i) * DP + col(i);
-      a[i] = *reinterpret_cast<const float4*>(at);
-      b[i] = *reinterpret_cast<const float4*>(at + DP);
-      m = fmaxf(fmax3(m, fabsf(a[i].x), fabsf(a[i].y)), fmaxf(fabsf(a[i].z), fabsf(a[i].w)));
-      m = fmaxf(fmax3(m, fabsf(b[i].x), fabsf(b[i].y)), fmaxf(fabsf(b[i].z), fabsf(b[i].w)));
-    }
+    for (int i = 0; i < kItems; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float4 v = *reinterpret_cast<const float4*>(raw + row(i, k) * DP + col(i));
+        x[i][k] = v;
+        m = fmaxf(fmax3(m, fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
+      }
     return __float_as_uint(m);
   }
   // that of its largest finite one
   __device__ __forceinline__ uint32_t finite() const {
     float m = 0.f;
-    auto take = [&m](const float4& x) {
-      for (float v : {x.x, x.y, x.z, x.w})
-        if (fabsf(v) < INFINITY) m = fmaxf(m, fabsf(v));
-    };
 #pragma unroll
-    for (int i = 0; i < kItems; ++i) take(a[i]), take(b[i]);
+    for (int i = 0; i < kItems; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        for (float v : {x[i][k].x, x[i][k].y, x[i][k].z, x[i][k].w})
+          if (fabsf(v) < INFINITY) m = fmaxf(m, fabsf(v));
     return __float_as_uint(m);
   }
-  // writes its terms as rows (at row0 of an array of `rows`) and as pairs, either may be null
-  __device__ __forceinline__ void write(float mul, uint8_t* to_rows, int rows, int row0,
-                                        uint32_t* to_pairs) const {
-#pragma unroll
-    for (int i = 0; i < kItems; ++i) write_item(i, mul, mul, to_rows, rows, row0, to_pairs);
-  }
-  // the factors that undo the scales of rows row0 .. go to inv
-  __device__ __forceinline__ void write_by_row(uint8_t* to_rows, int rows, int row0,
-                                               float* inv) const {
+  // writes its terms as rows and as pairs, either may be null
+  __device__ __forceinline__ void write(float mul, uint8_t* to_rows, uint32_t* to_pairs) const {
+    const float2 mul2 = make_float2(mul, mul);
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
-      float x = fmaxf(fmaxf(fabsf(a[i].x), fabsf(a[i].y)), fmaxf(fabsf(a[i].z), fabsf(a[i].w)));
-      float y = fmaxf(fmaxf(fabsf(b[i].x), fabsf(b[i].y)), fmaxf(fabsf(b[i].z), fabsf(b[i].w)));
+      const int c = col(i);
+      float2 v[4][2];  // row k, columns c + 2 u, + 1
 #pragma unroll
-      for (int off = 1; off < DP / 4; off <<= 1) {  // the DP / 4 lanes of a pair of rows
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
-        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, off));
+      for (int k = 0; k < 4; ++k) {
+        v[k][0] = fmul2(make_float2(x[i][k].x, x[i][k].y), mul2);
+        v[k][1] = fmul2(make_float2(x[i][k].z, x[i][k].w), mul2);
       }
-      const Scale fx = scale_for(__float_as_uint(x)), fy = scale_for(__float_as_uint(y));
-      write_item(i, fx.mul, fy.mul, to_rows, rows, row0, nullptr);
-      if (col(i) == 0) {
-        inv[row0 + 2 * pair(i)] = fx.inv;
-        inv[row0 + 2 * pair(i) + 1] = fy.inv;
+      uint32_t h[4][2], l[4][2];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          h[k][u] = halves(v[k][u]);
+          l[k][u] = rest_of(v[k][u], h[k][u]);
+        }
+      if (to_rows != nullptr) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint8_t* at = to_rows + unit_at<DP>(row(i, k), c >> 3) * 16 + (c & 4) * 2;
+          *reinterpret_cast<uint2*>(at) = make_uint2(h[k][0], h[k][1]);
+          *reinterpret_cast<uint2*>(at + kTile * DP * 2) = make_uint2(l[k][0], l[k][1]);
+        }
+      }
+      if (to_pairs != nullptr) {
+        uint32_t* at = to_pairs + group(i) * pair_pitch<DP>() + 2 * c;
+        constexpr int kLo = kTile / 4 * pair_pitch<DP>();
+        auto put = [&](uint32_t* to, const uint32_t (&w)[4][2], int u) {
+          *reinterpret_cast<uint4*>(to + 4 * u) = make_uint4(
+              __byte_perm(w[0][u], w[1][u], 0x5410), __byte_perm(w[2][u], w[3][u], 0x5410),
+              __byte_perm(w[0][u], w[1][u], 0x7632), __byte_perm(w[2][u], w[3][u], 0x7632));
+        };
+        put(at, h, 0);
+        put(at, h, 1);
+        put(at + kLo, l, 0);
+        put(at + kLo, l, 1);
       }
     }
   }
-  __device__ __forceinline__ void write_item(int i, float mul_a, float mul_b, uint8_t* to_rows,
-                                             int rows, int row0, uint32_t* to_pairs) const {
-    {
-      const float4 x = make_float4(a[i].x * mul_a, a[i].y * mul_a, a[i].z * mul_a, a[i].w * mul_a);
-      const float4 y = make_float4(b[i].x * mul_b, b[i].y * mul_b, b[i].z * mul_b, b[i].w * mul_b);
-      const uint2 xh = make_uint2(pack_half(x.x, x.y), pack_half(x.z, x.w));
-      const uint2 yh = make_uint2(pack_half(y.x, y.y), pack_half(y.z, y.w));
-      const uint2 xl = make_uint2(pack_rest(x.x, x.y, xh.x), pack_rest(x.z, x.w, xh.y));
-      const uint2 yl = make_uint2(pack_rest(y.x, y.y, yh.x), pack_rest(y.z, y.w, yh.y));
-      const int p = pair(i), c = col(i);
-      if (to_rows != nullptr) {
-        const int r = row0 + 2 * p, half = (c & 4) * 2;
-        uint8_t* h0 = to_rows + unit_at<DP>(r, c >> 3) * 16 + half;
-        uint8_t* h1 = to_rows + unit_at<DP>(r + 1, c >> 3) * 16 + half;
-        *reinterpret_cast<uint2*>(h0) = xh;
-        *reinterpret_cast<uint2*>(h1) = yh;
-        *reinterpret_cast<uint2*>(h0 + rows * DP * 2) = xl;
-        *reinterpret_cast<uint2*>(h1 + rows * DP * 2) = yl;
-      }
-      if (to_pairs != nullptr) {
-        auto mix = [](const uint2& u, const uint2& v) {
-          return make_uint4(__byte_perm(u.x, v.x, 0x5410), __byte_perm(u.x, v.x, 0x7632),
-                            __byte_perm(u.y, v.y, 0x5410), __byte_perm(u.y, v.y, 0x7632));
-        };
-        uint32_t* w = to_pairs + p * pair_pitch<DP>() + c;
-        *reinterpret_cast<uint4*>(w) = mix(xh, yh);
-        *reinterpret_cast<uint4*>(w + kTile / 2 * pair_pitch<DP>()) = mix(xl, yl);
+  // writes its terms, rows row0 .. of the CTA's own, as fragments, every row under a scale of its own;
+  // the factors that undo the scales go to inv
+  __device__ __forceinline__ void write_own(uint32_t* to, int row0, float* inv) const {
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+      const int c = col(i), unit = c >> 3, step = 2 * (unit >> 2) + ((c >> 2) & 1);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float m = top(x[i][k]);
+#pragma unroll
+        for (int off = 1; off < DP / 4; off <<= 1)  // the DP / 4 lanes of a row
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        const Scale f = scale_for(__float_as_uint(m));
+        const float2 mul2 = make_float2(f.mul, f.mul);
+        const int r = row0 + row(i, k), g = r & 7;
+        uint32_t* at = to + (((r >> 4) * (DP / 16) + step) * 32 + 4 * g + (unit & 3)) * 4 +
+                       ((r >> 3) & 1);
+        const float2 v0 = fmul2(make_float2(x[i][k].x, x[i][k].y), mul2);
+        const float2 v1 = fmul2(make_float2(x[i][k].z, x[i][k].w), mul2);
+        const uint32_t h0 = halves(v0), h1 = halves(v1);
+        at[0] = h0;
+        at[2] = h1;
+        at[kRows * DP / 2] = rest_of(v0, h0);
+        at[kRows * DP / 2 + 2] = rest_of(v1, h1);
+        if (c == 0) inv[r] = f.inv;
       }
     }
   }
@@ -230,11 +264,11 @@ __device__ __forceinline__ uint32_t block_max(uint32_t top, uint32_t* red) {
   return max(max(red[0], red[1]), max(red[2], red[3]));
 }
 
-// The CTA's own 64 rows, split as rows, and the factors that undo their scales; raw is scratch.
+// The CTA's own 64 rows, split into fragments, and the factors that undo their scales; raw is scratch.
 template <int DP, bool kVec>
-__device__ __forceinline__ void own_rows(uint8_t* to, float* inv, float* raw, const float* src,
+__device__ __forceinline__ void own_rows(uint32_t* to, float* inv, float* raw, const float* src,
                                          int64_t sn, int n0, int limit, int d) {
-  static_assert(DP / 4 <= 32 && 32 % (DP / 4) == 0, "a pair of rows within a warp");
+  static_assert(DP / 4 <= 32 && 32 % (DP / 4) == 0, "a row within a warp");
   const TileCopy<DP, kVec> copy(src, sn, limit, d);
 #pragma unroll 1
   for (int i = 0; i < kRows; i += kTile) {
@@ -244,7 +278,7 @@ __device__ __forceinline__ void own_rows(uint8_t* to, float* inv, float* raw, co
     __syncthreads();
     Share<DP> s;
     s.read(raw);
-    s.write_by_row(to, kRows, i, inv);
+    s.write_own(to, i, inv);
     __syncthreads();
   }
 }
@@ -254,20 +288,28 @@ template <int DP>
 __device__ __forceinline__ uint4 unit16(const uint8_t* rows, int r, int u) {
   return *reinterpret_cast<const uint4*>(rows + unit_at<DP>(r, u) * 16);
 }
+__device__ __forceinline__ float2 pair_of(const float (&s)[4], int half) {
+  return make_float2(s[2 * half], s[2 * half + 1]);
+}
+__device__ __forceinline__ void set_pair(float (&s)[4], int half, float2 v) {
+  s[2 * half] = v.x;
+  s[2 * half + 1] = v.y;
+}
 
-// s[n] = A B^T over d: A's rows a_row + g, + 8 of kRows, B's rows 8 n + g of kTile
+// s[n] = A B^T over d: A the warp's own 16 rows, B's rows 8 n + g of kTile
 template <int DP>
-__device__ __forceinline__ void product_d(float (&s)[kNT][4], const uint8_t* A, int a_row,
-                                          const uint8_t* B, int g, int t) {
-  constexpr int kLoA = kRows * DP * 2, kLoB = kTile * DP * 2;
+__device__ __forceinline__ void product_d(float (&s)[kNT][4], const uint32_t* A, int warp, int lane,
+                                          const uint8_t* B) {
+  constexpr int kLoA = kRows * DP / 8, kLoB = kTile * DP * 2;
+  const int g = lane >> 2, t = lane & 3;
+  const uint4* a4 = reinterpret_cast<const uint4*>(A) + warp * (DP / 16) * 32 + lane;
   float hi[kNT][4], lo[kNT][4];
 #pragma unroll
   for (int h = 0; h < DP / 32; ++h) {
-    const uint4 x = unit16<DP>(A, a_row + g, t + 4 * h), y = unit16<DP>(A, a_row + g + 8, t + 4 * h);
-    const uint4 xl = unit16<DP>(A + kLoA, a_row + g, t + 4 * h);
-    const uint4 yl = unit16<DP>(A + kLoA, a_row + g + 8, t + 4 * h);
-    const uint32_t a0[4] = {x.x, y.x, x.y, y.y}, a1[4] = {x.z, y.z, x.w, y.w};
-    const uint32_t l0[4] = {xl.x, yl.x, xl.y, yl.y}, l1[4] = {xl.z, yl.z, xl.w, yl.w};
+    const uint4 x0 = a4[2 * h * 32], x1 = a4[(2 * h + 1) * 32];
+    const uint4 y0 = a4[2 * h * 32 + kLoA], y1 = a4[(2 * h + 1) * 32 + kLoA];
+    const uint32_t a0[4] = {x0.x, x0.y, x0.z, x0.w}, a1[4] = {x1.x, x1.y, x1.z, x1.w};
+    const uint32_t l0[4] = {y0.x, y0.y, y0.z, y0.w}, l1[4] = {y1.x, y1.y, y1.z, y1.w};
 #pragma unroll
     for (int n = 0; n < kNT; ++n) {
       const uint4 b = unit16<DP>(B, 8 * n + g, t + 4 * h);
@@ -288,7 +330,7 @@ __device__ __forceinline__ void product_d(float (&s)[kNT][4], const uint8_t* A, 
 #pragma unroll
   for (int n = 0; n < kNT; ++n)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[n][i] = hi[n][i] + lo[n][i];
+    for (int i = 0; i < 2; ++i) set_pair(s[n], i, fadd2(pair_of(hi[n], i), pair_of(lo[n], i)));
 }
 
 // the fragments of 16 x 32 scores, rows g and g + 8 times mul0 and mul1, as the operand of a product
@@ -300,11 +342,10 @@ struct ScoreFrags {
     for (int s = 0; s < kNT / 2; ++s)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {  // (g, 2 t), (g + 8, 2 t), then the next eight columns
-        const float* c = p[2 * s + (i >> 1)];
         const float mul = i & 1 ? mul1 : mul0;
-        const float x = c[2 * (i & 1)] * mul, y = c[2 * (i & 1) + 1] * mul;
-        hi[s][i] = pack_half(x, y);
-        lo[s][i] = pack_rest(x, y, hi[s][i]);
+        const float2 x = fmul2(pair_of(p[2 * s + (i >> 1)], i & 1), make_float2(mul, mul));
+        hi[s][i] = halves(x);
+        lo[s][i] = rest_of(x, hi[s][i]);
       }
   }
 };
@@ -318,47 +359,47 @@ __device__ __forceinline__ Scale score_scale(const float (&p)[kNT][4], int half)
   return scale_for(__float_as_uint(m));
 }
 
-// o[4 u + e] += P B over the tile's rows (B as pairs), rows g and g + 8 times inv0 and inv1
+// o[2 v + e] (d = 16 v + 2 g + e) += P B over the tile's rows (B as pairs), rows g and g + 8 times inv0
+// and inv1
 template <int DP>
 __device__ __forceinline__ void product_rows(float (&o)[DP / 8][4], const ScoreFrags& p,
                                              const uint32_t* B, float inv0, float inv1, int g,
                                              int t) {
-  constexpr int kP = pair_pitch<DP>(), kLo = kTile / 2 * kP;
+  constexpr int kP = pair_pitch<DP>(), kLo = kTile / 4 * kP;
+  const float2 inv[2] = {make_float2(inv0, inv0), make_float2(inv1, inv1)};
 #pragma unroll
   for (int u = 0; u < DP / 32; ++u) {
-    uint4 b0[kNT / 2], b1[kNT / 2];
+    uint4 b[kNT / 2][2];
     float sum[4][4];  // the small terms first, then the large: a chain of two where cuts matter
 #pragma unroll
-    for (int s = 0; s < kNT / 2; ++s) {
-      const uint32_t* at = B + (8 * s + t) * kP + 32 * u + 4 * g;
-      b0[s] = *reinterpret_cast<const uint4*>(at);
-      b1[s] = *reinterpret_cast<const uint4*>(at + 4 * kP);
-      const uint4 l0 = *reinterpret_cast<const uint4*>(at + kLo);
-      const uint4 l1 = *reinterpret_cast<const uint4*>(at + kLo + 4 * kP);
-      const uint32_t x0[4] = {b0[s].x, b0[s].y, b0[s].z, b0[s].w};
-      const uint32_t x1[4] = {b1[s].x, b1[s].y, b1[s].z, b1[s].w};
-      const uint32_t y0[4] = {l0.x, l0.y, l0.z, l0.w}, y1[4] = {l1.x, l1.y, l1.z, l1.w};
+    for (int s = 0; s < kNT / 2; ++s)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (s == 0)
-          mma16816_zero(sum[e], p.lo[s], x0[e], x1[e]);
-        else
-          mma16816(sum[e], p.lo[s], x0[e], x1[e]);
-        mma16816(sum[e], p.hi[s], y0[e], y1[e]);
+      for (int v = 0; v < 2; ++v) {
+        const uint32_t* at = B + (4 * s + t) * kP + 2 * (32 * u + 16 * v + 2 * g);
+        b[s][v] = *reinterpret_cast<const uint4*>(at);
+        const uint4 l = *reinterpret_cast<const uint4*>(at + kLo);
+        if (s == 0) {
+          mma16816_zero(sum[2 * v], p.lo[s], b[s][v].x, b[s][v].y);
+          mma16816_zero(sum[2 * v + 1], p.lo[s], b[s][v].z, b[s][v].w);
+        } else {
+          mma16816(sum[2 * v], p.lo[s], b[s][v].x, b[s][v].y);
+          mma16816(sum[2 * v + 1], p.lo[s], b[s][v].z, b[s][v].w);
+        }
+        mma16816(sum[2 * v], p.hi[s], l.x, l.y);
+        mma16816(sum[2 * v + 1], p.hi[s], l.z, l.w);
       }
-    }
 #pragma unroll
-    for (int s = 0; s < kNT / 2; ++s) {
-      const uint32_t x0[4] = {b0[s].x, b0[s].y, b0[s].z, b0[s].w};
-      const uint32_t x1[4] = {b1[s].x, b1[s].y, b1[s].z, b1[s].w};
+    for (int s = 0; s < kNT / 2; ++s)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) mma16816(sum[e], p.hi[s], x0[e], x1[e]);
-    }
+      for (int v = 0; v < 2; ++v) {
+        mma16816(sum[2 * v], p.hi[s], b[s][v].x, b[s][v].y);
+        mma16816(sum[2 * v + 1], p.hi[s], b[s][v].z, b[s][v].w);
+      }
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
+    for (int n = 0; n < 4; ++n)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        o[4 * u + e][i] = fmaf(sum[e][i], i < 2 ? inv0 : inv1, o[4 * u + e][i]);
+      for (int i = 0; i < 2; ++i)
+        set_pair(o[4 * u + n], i, ffma2(pair_of(sum[n], i), inv[i], pair_of(o[4 * u + n], i)));
   }
 }
 
@@ -367,21 +408,17 @@ template <int DP, bool kVec>
 __device__ __forceinline__ void store_row(float* dst, const float (&o)[DP / 8][4], int half, int t,
                                           int d, float mul) {
 #pragma unroll
-  for (int u = 0; u < DP / 32; ++u) {
-#pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      const int c = 32 * u + 8 * t + 4 * v;
-      const float4 x = make_float4(o[4 * u][2 * half + v] * mul, o[4 * u + 1][2 * half + v] * mul,
-                                   o[4 * u + 2][2 * half + v] * mul,
-                                   o[4 * u + 3][2 * half + v] * mul);
-      if (kVec) {
-        if (c < d) *reinterpret_cast<float4*>(dst + c) = x;
-      } else {
-        if (c < d) dst[c] = x.x;
-        if (c + 1 < d) dst[c + 1] = x.y;
-        if (c + 2 < d) dst[c + 2] = x.z;
-        if (c + 3 < d) dst[c + 3] = x.w;
-      }
+  for (int v = 0; v < DP / 16; ++v) {
+    const int c = 16 * v + 4 * t;
+    const float4 x = make_float4(o[2 * v][2 * half] * mul, o[2 * v + 1][2 * half] * mul,
+                                 o[2 * v][2 * half + 1] * mul, o[2 * v + 1][2 * half + 1] * mul);
+    if (kVec) {
+      if (c < d) *reinterpret_cast<float4*>(dst + c) = x;
+    } else {
+      if (c < d) dst[c] = x.x;
+      if (c + 1 < d) dst[c + 1] = x.y;
+      if (c + 2 < d) dst[c + 2] = x.z;
+      if (c + 3 < d) dst[c + 3] = x.w;
     }
   }
 }
@@ -394,24 +431,28 @@ __device__ __forceinline__ int keys_of(const RelF32& p, int b) {
 // rows g, g + 8 from the table (at: its entry for column 0 and row g; a row less is a distance more)
 __device__ __forceinline__ void add_bias(float (&s)[kNT][4], float f0, float f1, bool near,
                                          float constant, const float* at) {
+  const float2 f[2] = {make_float2(f0, f0), make_float2(f1, f1)};
   if (near) {
 #pragma unroll
     for (int n = 0; n < kNT; ++n)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        s[n][i] = fmaf(s[n][i], i < 2 ? f0 : f1, at[8 * n + (i & 1) - 8 * (i >> 1)]);
+      for (int i = 0; i < 2; ++i)
+        set_pair(s[n], i, ffma2(pair_of(s[n], i), f[i],
+                                make_float2(at[8 * n - 8 * i], at[8 * n + 1 - 8 * i])));
   } else {
 #pragma unroll
     for (int n = 0; n < kNT; ++n)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[n][i] = fmaf(s[n][i], i < 2 ? f0 : f1, constant);
+      for (int i = 0; i < 2; ++i)
+        set_pair(s[n], i, ffma2(pair_of(s[n], i), f[i], make_float2(constant, constant)));
   }
 }
 
 // ============================================================================ forward
 template <int DP>
 struct FwdSmem {
-  uint8_t Q[rows_bytes<DP>(kRows)], K[rows_bytes<DP>(kTile)];
+  uint32_t Q[rows_bytes<DP>(kRows) / 4];
+  uint8_t K[rows_bytes<DP>(kTile)];
   uint32_t V[pairs_bytes<DP>() / 4];
   float rawK[kTile * DP], rawV[kTile * DP];
   float table[kDist + 1], q_inv[kRows];
@@ -441,14 +482,16 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 3 : 2)
     copy_v(sm.rawV, j * kTile);
     copy_commit();
   };
-  for (int s = threadIdx.x; s <= kRelMaxSeg; s += kThreads) rel_load(sm.rs, rel, h, s, 1.f);
+  for (int s = threadIdx.x; s <= kRelMaxSeg; s += kThreads) rel_load(sm.rs, rel, h, s, kLog2e);
   own_rows<DP, kVec>(sm.Q, sm.q_inv, sm.rawK, p.Q + b * p.st[0][0] + h * p.st[0][1], p.st[0][2], q0,
                      p.Nq, p.d_k);
-  const float q_inv[2] = {sm.q_inv[16 * warp + g] * p.scale, sm.q_inv[16 * warp + g + 8] * p.scale};
+  const float unit = p.scale * kLog2e;  // scores in powers of two
+  const float q_inv[2] = {sm.q_inv[16 * warp + g] * unit, sm.q_inv[16 * warp + g + 8] * unit};
   const int row[2] = {q0 + 16 * warp + g, q0 + 16 * warp + g + 8};
   const int limit[2] = {p.mask == 1 ? row[0] : L - 1, p.mask == 1 ? row[1] : L - 1};
   float o[DP / 8][4] = {};
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  float m[2] = {-INFINITY, -INFINITY};
+  float2 l[2] = {};
   int seg_next = INT_MIN;
   float seg_bias = 0.f;
   if (nt > 0) load(0);
@@ -480,8 +523,8 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 3 : 2)
         tops(k.finite(), v.finite());
       }
       const Scale fk = scale_for(tk), fv = scale_for(tv);
-      k.write(fk.mul, sm.K, kTile, 0, nullptr);
-      v.write(fv.mul, nullptr, 0, 0, sm.V);
+      k.write(fk.mul, sm.K, nullptr);
+      v.write(fv.mul, nullptr, sm.V);
       k_inv = fk.inv;
       v_inv = fv.inv;
     }
@@ -489,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 3 : 2)
     if (j + 1 < nt) load(j + 1);
     if (p.mask != 1 || j * kTile <= q0 + 16 * warp + 15) {
       float s[kNT][4];
-      product_d<DP>(s, sm.Q, 16 * warp, sm.K, g, t);
+      product_d<DP>(s, sm.Q, warp, lane, sm.K);
       float mx[2] = {-INFINITY, -INFINITY};
       add_bias(s, k_inv * q_inv[0], k_inv * q_inv[1], near, seg_bias,
                sm.table + 2 * t - (16 * warp + g) + kRows - 1);
@@ -511,22 +554,25 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 3 : 2)
         mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
         const float m_new = fmaxf(m[i], mx[i]);
         ref[i] = m_new == -INFINITY ? 0.f : m_new;
-        alpha[i] = ex2_approx((m[i] - ref[i]) * kLog2e);
+        alpha[i] = ex2_approx(m[i] - ref[i]);
         m[i] = m_new;
-        l[i] *= alpha[i];
+        l[i] = fmul2(l[i], make_float2(alpha[i], alpha[i]));
       }
 #pragma unroll
       for (int n = 0; n < kNT; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          s[n][i] = ex2_approx((s[n][i] - ref[i >> 1]) * kLog2e);
-          l[i >> 1] += s[n][i];
+        for (int i = 0; i < 2; ++i) {
+          float2 x = fadd2(pair_of(s[n], i), make_float2(-ref[i], -ref[i]));
+          x = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+          set_pair(s[n], i, x);
+          l[i] = fadd2(l[i], x);
         }
       if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
 #pragma unroll
         for (int u = 0; u < DP / 8; ++u)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[u][i] *= alpha[i >> 1];
+          for (int i = 0; i < 2; ++i)
+            set_pair(o[u], i, fmul2(pair_of(o[u], i), make_float2(alpha[i], alpha[i])));
       }
       const float inv = v_inv * 0x1p-14f;
       product_rows<DP>(o, ScoreFrags(s, 0x1p14f, 0x1p14f), sm.V, inv, inv, g, t);
@@ -535,14 +581,15 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 3 : 2)
   float* ob = p.out + b * p.st[3][0] + h * p.st[3][1];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+    float sum = l[i].x + l[i].y;
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
     if (row[i] < p.Nq) {
       store_row<DP, kVec>(ob + static_cast<int64_t>(row[i]) * p.st[3][2], o, i, t, p.d_v,
-                          l[i] > 0.f ? 1.f / l[i] : 0.f);
+                          sum > 0.f ? 1.f / sum : 0.f);
       if (t == 0 && p.lse != nullptr)
         p.lse[(static_cast<int64_t>(b) * p.H + h) * p.Nq + row[i]] =
-            l[i] > 0.f ? m[i] + logf(l[i]) : INFINITY;
+            sum > 0.f ? fmaf(m[i], kLn2, logf(sum)) : INFINITY;
     }
   }
 }
@@ -550,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 3 : 2)
 // ============================================================================ backward
 template <int DP>
 struct DqSmem {
-  uint8_t Q[rows_bytes<DP>(kRows)], G[rows_bytes<DP>(kRows)];  // G: dO
+  uint32_t Q[rows_bytes<DP>(kRows) / 4], G[rows_bytes<DP>(kRows) / 4];  // G: dO
   uint32_t Kp[pairs_bytes<DP>() / 4];
   union {
     struct {
@@ -638,8 +685,8 @@ __device__ __forceinline__ void queries_part(const RelF32& p, const RelBias& rel
       const Scale fk = scale_for(max(max(sm.red[1][0], sm.red[1][1]),
                                      max(sm.red[1][2], sm.red[1][3])));
       const Scale fv = scale_for(tv);
-      k.write(fk.mul, sm.K, kTile, 0, sm.Kp);
-      v.write(fv.mul, sm.V, kTile, 0, nullptr);
+      k.write(fk.mul, sm.K, sm.Kp);
+      v.write(fv.mul, sm.V, nullptr);
       k_inv = fk.inv;
       v_inv = fv.inv;
     }
@@ -649,8 +696,8 @@ __device__ __forceinline__ void queries_part(const RelF32& p, const RelBias& rel
     float s[kNT][4] = {};
     if (!skip) {
       float dp[kNT][4];
-      product_d<DP>(s, sm.Q, 16 * warp, sm.K, g, t);
-      product_d<DP>(dp, sm.G, 16 * warp, sm.V, g, t);
+      product_d<DP>(s, sm.Q, warp, lane, sm.K);
+      product_d<DP>(dp, sm.G, warp, lane, sm.V);
       const float fg[2] = {v_inv * g_inv[0], v_inv * g_inv[1]};
       add_bias(s, k_inv * q_inv[0], k_inv * q_inv[1], near, seg_bias,
                sm.table + 2 * t - r_loc[0] + kRows - 1);
@@ -664,9 +711,13 @@ __device__ __forceinline__ void queries_part(const RelF32& p, const RelBias& rel
 #pragma unroll
       for (int n = 0; n < kNT; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          s[n][i] = ex2_approx((s[n][i] - lse[i >> 1]) * kLog2e) *
-                    fmaf(dp[n][i], fg[i >> 1], -D[i >> 1]);
+        for (int i = 0; i < 2; ++i) {
+          float2 x = fadd2(pair_of(s[n], i), make_float2(-lse[i], -lse[i]));
+          x = fmul2(x, make_float2(kLog2e, kLog2e));
+          x = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+          set_pair(s[n], i, fmul2(x, ffma2(pair_of(dp[n], i), make_float2(fg[i], fg[i]),
+                                           make_float2(-D[i], -D[i]))));
+        }
     }
     if (near) {
       __syncthreads();  // K and V as rows are done with
@@ -677,7 +728,10 @@ __device__ __forceinline__ void queries_part(const RelF32& p, const RelBias& rel
           sm.S[r_loc[i >> 1] * (kTile + 1) + 8 * n + 2 * t + (i & 1)] = s[n][i];
     } else {
 #pragma unroll
-      for (int n = 0; n < kNT; ++n) far += (s[n][0] + s[n][1]) + (s[n][2] + s[n][3]);
+      for (int n = 0; n < kNT; ++n) {
+        const float2 x = fadd2(pair_of(s[n], 0), pair_of(s[n], 1));
+        far += x.x + x.y;
+      }
     }
     if (!skip) {
       const Scale f0 = score_scale(s, 0), f1 = score_scale(s, 1);
@@ -724,11 +778,12 @@ __device__ __forceinline__ void queries_part(const RelF32& p, const RelBias& rel
 
 template <int DP>
 struct DkdvSmem {
-  uint8_t K[rows_bytes<DP>(kRows)], V[rows_bytes<DP>(kRows)];
+  uint32_t K[rows_bytes<DP>(kRows) / 4], V[rows_bytes<DP>(kRows) / 4];
   uint8_t Q[rows_bytes<DP>(kTile)], G[rows_bytes<DP>(kTile)];  // G: dO
   uint32_t Qp[pairs_bytes<DP>() / 4], Gp[pairs_bytes<DP>() / 4];
   float rawQ[kTile * DP], rawG[kTile * DP];
-  float D[kTile], lse[kTile], k_inv[kRows], v_inv[kRows];
+  float D[kTile], lse[kTile];  // both negated
+  float k_inv[kRows], v_inv[kRows];
   float table[kDist + 1];
   uint32_t red[2][kWarps];
   RelShared rs;
@@ -777,8 +832,8 @@ __device__ __forceinline__ void keys_part(const RelF32& p, const RelBias& rel, D
       copy_wait();
       __syncthreads();  // the tile is there, the previous one done with
       if (tid < kTile) {
-        sm.D[tid] = q0 + tid < p.Nq ? p.Dv[bh * p.Nq + q0 + tid] : 0.f;
-        sm.lse[tid] = q0 + tid < p.Nq ? p.lse[bh * p.Nq + q0 + tid] : INFINITY;
+        sm.D[tid] = q0 + tid < p.Nq ? -p.Dv[bh * p.Nq + q0 + tid] : 0.f;
+        sm.lse[tid] = q0 + tid < p.Nq ? -p.lse[bh * p.Nq + q0 + tid] : -INFINITY;
       }
       if (near && tid < kDist)
         sm.table[tid] = sm.rs.bias[rel_segment(sm.rs, rel_steps(rel.nseg), d0 + tid)];
@@ -790,16 +845,16 @@ __device__ __forceinline__ void keys_part(const RelF32& p, const RelBias& rel, D
         const Scale fq = scale_for(max(max(sm.red[1][0], sm.red[1][1]),
                                        max(sm.red[1][2], sm.red[1][3])));
         const Scale fg = scale_for(tg);
-        q.write(fq.mul, sm.Q, kTile, 0, sm.Qp);
-        o.write(fg.mul, sm.G, kTile, 0, sm.Gp);
+        q.write(fq.mul, sm.Q, sm.Qp);
+        o.write(fg.mul, sm.G, sm.Gp);
         q_inv = fq.inv;
         g_inv = fg.inv;
       }
       __syncthreads();
       if (i + 1 < ni) load(i + 1);
       float s[kNT][4], ds[kNT][4];
-      product_d<DP>(s, sm.K, 16 * warp, sm.Q, g, t);
-      product_d<DP>(ds, sm.V, 16 * warp, sm.G, g, t);
+      product_d<DP>(s, sm.K, warp, lane, sm.Q);
+      product_d<DP>(ds, sm.V, warp, lane, sm.G);
       const float f[2] = {q_inv * k_inv[0], q_inv * k_inv[1]};
       const float fg[2] = {g_inv * v_inv[0], g_inv * v_inv[1]};
       // the table by row (key) minus column (query): a row more is a distance more
@@ -808,13 +863,16 @@ __device__ __forceinline__ void keys_part(const RelF32& p, const RelBias& rel, D
 #pragma unroll
         for (int n = 0; n < kNT; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            s[n][e] = fmaf(s[n][e], f[e >> 1], at[8 * (e >> 1) - 8 * n - (e & 1)]);
+          for (int e = 0; e < 2; ++e)
+            set_pair(s[n], e, ffma2(pair_of(s[n], e), make_float2(f[e], f[e]),
+                                    make_float2(at[8 * e - 8 * n], at[8 * e - 8 * n - 1])));
       } else {
 #pragma unroll
         for (int n = 0; n < kNT; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[n][e] = fmaf(s[n][e], f[e >> 1], seg_bias);
+          for (int e = 0; e < 2; ++e)
+            set_pair(s[n], e, ffma2(pair_of(s[n], e), make_float2(f[e], f[e]),
+                                    make_float2(seg_bias, seg_bias)));
       }
       if (k0 + 16 * warp + 15 >= L || (p.mask == 1 && k0 + 16 * warp + 15 > q0)) {
 #pragma unroll
@@ -830,9 +888,12 @@ __device__ __forceinline__ void keys_part(const RelF32& p, const RelBias& rel, D
         const float2 lse = *reinterpret_cast<const float2*>(sm.lse + 8 * n + 2 * t);
         const float2 D = *reinterpret_cast<const float2*>(sm.D + 8 * n + 2 * t);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          s[n][e] = ex2_approx((s[n][e] - (e & 1 ? lse.y : lse.x)) * kLog2e);
-          ds[n][e] = s[n][e] * fmaf(ds[n][e], fg[e >> 1], -(e & 1 ? D.y : D.x));
+        for (int e = 0; e < 2; ++e) {
+          float2 x = fadd2(pair_of(s[n], e), lse);
+          x = fmul2(x, make_float2(kLog2e, kLog2e));
+          x = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+          set_pair(s[n], e, x);
+          set_pair(ds[n], e, fmul2(x, ffma2(pair_of(ds[n], e), make_float2(fg[e], fg[e]), D)));
         }
       }
       const Scale s0 = score_scale(s, 0), s1 = score_scale(s, 1);
