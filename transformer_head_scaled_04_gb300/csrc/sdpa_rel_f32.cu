@@ -311,20 +311,33 @@ __device__ __forceinline__ void product_d(float (&s)[kNT][4], const uint32_t* A,
     const uint32_t a0[4] = {x0.x, x0.y, x0.z, x0.w}, a1[4] = {x1.x, x1.y, x1.z, x1.w};
     const uint32_t l0[4] = {y0.x, y0.y, y0.z, y0.w}, l1[4] = {y1.x, y1.y, y1.z, y1.w};
 #pragma unroll
-    for (int n = 0; n < kNT; ++n) {
-      const uint4 b = unit16<DP>(B, 8 * n + g, t + 4 * h);
-      const uint4 bl = unit16<DP>(B + kLoB, 8 * n + g, t + 4 * h);
-      if (h == 0) {
-        mma16816_zero(lo[n], l0, b.x, b.y);
-        mma16816_zero(hi[n], a0, b.x, b.y);
-      } else {
-        mma16816(lo[n], l0, b.x, b.y);
-        mma16816(hi[n], a0, b.x, b.y);
+    for (int n = 0; n < kNT; n += 2) {  // two columns' chains side by side
+      uint4 b[2], bl[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        b[i] = unit16<DP>(B, 8 * (n + i) + g, t + 4 * h);
+        bl[i] = unit16<DP>(B + kLoB, 8 * (n + i) + g, t + 4 * h);
       }
-      mma16816(lo[n], a0, bl.x, bl.y);
-      mma16816(lo[n], l1, b.z, b.w);
-      mma16816(lo[n], a1, bl.z, bl.w);
-      mma16816(hi[n], a1, b.z, b.w);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (h == 0)
+          mma16816_zero(lo[n + i], l0, b[i].x, b[i].y);
+        else
+          mma16816(lo[n + i], l0, b[i].x, b[i].y);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (h == 0)
+          mma16816_zero(hi[n + i], a0, b[i].x, b[i].y);
+        else
+          mma16816(hi[n + i], a0, b[i].x, b[i].y);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) mma16816(lo[n + i], l1, b[i].z, b[i].w);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) mma16816(hi[n + i], a1, b[i].z, b[i].w);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) mma16816(lo[n + i], a0, bl[i].x, bl[i].y);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) mma16816(lo[n + i], a1, bl[i].z, bl[i].w);
     }
   }
 #pragma unroll
@@ -372,12 +385,16 @@ __device__ __forceinline__ void product_rows(float (&o)[DP / 8][4], const ScoreF
     uint4 b[kNT / 2][2];
     float sum[4][4];  // the small terms first, then the large: a chain of two where cuts matter
 #pragma unroll
-    for (int s = 0; s < kNT / 2; ++s)
+    for (int s = 0; s < kNT / 2; ++s) {
+      uint4 l[2];
 #pragma unroll
       for (int v = 0; v < 2; ++v) {
         const uint32_t* at = B + (4 * s + t) * kP + 2 * (32 * u + 16 * v + 2 * g);
         b[s][v] = *reinterpret_cast<const uint4*>(at);
-        const uint4 l = *reinterpret_cast<const uint4*>(at + kLo);
+        l[v] = *reinterpret_cast<const uint4*>(at + kLo);
+      }
+#pragma unroll
+      for (int v = 0; v < 2; ++v)
         if (s == 0) {
           mma16816_zero(sum[2 * v], p.lo[s], b[s][v].x, b[s][v].y);
           mma16816_zero(sum[2 * v + 1], p.lo[s], b[s][v].z, b[s][v].w);
@@ -385,9 +402,12 @@ __device__ __forceinline__ void product_rows(float (&o)[DP / 8][4], const ScoreF
           mma16816(sum[2 * v], p.lo[s], b[s][v].x, b[s][v].y);
           mma16816(sum[2 * v + 1], p.lo[s], b[s][v].z, b[s][v].w);
         }
-        mma16816(sum[2 * v], p.hi[s], l.x, l.y);
-        mma16816(sum[2 * v + 1], p.hi[s], l.z, l.w);
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        mma16816(sum[2 * v], p.hi[s], l[v].x, l[v].y);
+        mma16816(sum[2 * v + 1], p.hi[s], l[v].z, l[v].w);
       }
+    }
 #pragma unroll
     for (int s = 0; s < kNT / 2; ++s)
 #pragma unroll
