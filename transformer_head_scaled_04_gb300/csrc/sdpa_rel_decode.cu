@@ -138,14 +138,21 @@ struct Where {
     }
     const bool near = d0 + 8 * NS + Nq - 2 >= seg_next;
 #pragma unroll
-    for (int n = 0; n < NS; ++n)
+    for (int n = 0; n < NS; ++n) {
+      const int j = j0 + 8 * n + 2 * t;
+      float bias[4] = {seg_bias, seg_bias, seg_bias, seg_bias};
+      if (near) {
+        const int d = j - (L - Nq + row[0]);
+        const int at[4] = {d, d + 1, d - 8, d - 7};  // rows g and g + 8
+        int seg[4];
+        rel_segments<4>(rs, steps, at, seg);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int j = j0 + 8 * n + 2 * t + (i & 1);
-        float bias = seg_bias;
-        if (near) bias = rs.bias[rel_segment(rs, steps, j - (L - Nq + row[i >> 1]))];
-        x[n][i] = j <= limit[i >> 1] ? fmaf(x[n][i], c, bias) : -INFINITY;
+        for (int i = 0; i < 4; ++i) bias[i] = rs.bias[seg[i]];
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        x[n][i] = j + (i & 1) <= limit[i >> 1] ? fmaf(x[n][i], c, bias[i]) : -INFINITY;
+    }
   }
 };
 
