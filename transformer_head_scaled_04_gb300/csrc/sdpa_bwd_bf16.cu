@@ -242,25 +242,46 @@ __device__ __forceinline__ void diagonal_sums(const uint32_t (&g)[32], int lane,
   down += b[0] + b[1];
 }
 
-// Adds v of the lanes of each segment (seg, which does not fall with the lane) up and the sums to
-// their owners, by way of part[0..31] (one float per segment from `first` on).  own is indexed by a
-// variable on purpose: it stays in local memory, away from the registers of steps that need none.
-__device__ __forceinline__ void segment_sums(float v, int seg, int lane, float* part,
+// Adds the values of the lanes of each segment up and the sums to their owners.  v[e] of the lanes belong
+// to segments seg[e], which do not fall with the lane; part: 32 floats for each e (one per segment from
+// its first on).  The three scans run side by side (one after the other: 5 x 3 heads of 777 37.4 us, so 34.6).
+// own is indexed by a variable on purpose: it stays in local memory, away from the registers of steps that
+// need none.
+__device__ __forceinline__ void segment_sums(float (&v)[3], const int (&seg)[3], int lane, float* part,
                                              float (&own)[kRelMaxSeg / 32]) {
-  const int first = __shfl_sync(0xffffffffu, seg, 0), last = __shfl_sync(0xffffffffu, seg, 31);
+  int first[3], last[3];
+#pragma unroll
+  for (int e = 0; e < 3; ++e) {
+    first[e] = __shfl_sync(0xffffffffu, seg[e], 0);
+    last[e] = __shfl_sync(0xffffffffu, seg[e], 31);
+  }
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const float up = __shfl_up_sync(0xffffffffu, v, off);
-    const int other = __shfl_up_sync(0xffffffffu, seg, off);
-    if (lane >= off && other == seg) v += up;
+    float up[3];
+    int other[3];
+#pragma unroll
+    for (int e = 0; e < 3; ++e) {
+      up[e] = __shfl_up_sync(0xffffffffu, v[e], off);
+      other[e] = __shfl_up_sync(0xffffffffu, seg[e], off);
+    }
+#pragma unroll
+    for (int e = 0; e < 3; ++e)
+      if (lane >= off && other[e] == seg[e]) v[e] += up[e];
   }
-  const int next = __shfl_down_sync(0xffffffffu, seg, 1);
-  if (lane == 31 || next != seg) part[seg - first] = v;  // the segment's last lane
+#pragma unroll
+  for (int e = 0; e < 3; ++e) {
+    const int next = __shfl_down_sync(0xffffffffu, seg[e], 1);
+    if (lane == 31 || next != seg[e]) part[32 * e + seg[e] - first[e]] = v[e];  // the segment's last lane
+  }
   __syncwarp();
 #pragma unroll 1
-  for (int k = first >> 5; k <= last >> 5; ++k) {
+  for (int k = first[2] >> 5; k <= last[0] >> 5; ++k) {
     const int s = lane + 32 * k;
-    if (s >= first && s <= last) own[k] += part[s - first];
+    float sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < 3; ++e)
+      if (s >= first[e] && s <= last[e]) sum += part[32 * e + s - first[e]];
+    own[k] += sum;
   }
   __syncwarp();
 }
@@ -595,7 +616,7 @@ __host__ __device__ constexpr int k_off_bar(bool fused) {
   return fused ? kKOffStage + kMathWarps * kStageBytes : kKOffDS;
 }
 // with a relative bias: borders and biases, then 128 floats per math warp (the table of 95
-// distances, 32 for segments' sums; at the end the warp's sums of all segments), 64 of -inf
+// distances, then segments' sums; at the end the warp's sums of all segments), 64 of -inf
 __host__ __device__ constexpr int k_off_rel(bool fused) { return k_off_bar(fused) + 256; }
 __host__ __device__ constexpr int k_off_table(bool fused) {
   return k_off_rel(fused) + static_cast<int>(sizeof(RelShared));
@@ -860,6 +881,7 @@ __global__ void __launch_bounds__(kKThreads, 1)
         reinterpret_cast<float*>(smem + k_off_table(kFused)) + kMathWarps * kRelMaxSeg;
     [[maybe_unused]] int seg = 0, seg_start = INT_MAX;
     [[maybe_unused]] float seg_bias = 0.f, far = 0.f;
+    [[maybe_unused]] bool seg_used = false;
     if constexpr (kRel) {  // while the first tiles arrive; every math warp passes here
       if (threadIdx.x <= kRelMaxSeg) rel_load(rs, rel, h, threadIdx.x, kLog2e);
       if (threadIdx.x >= 192) none[threadIdx.x - 192] = -INFINITY;
@@ -886,7 +908,8 @@ __global__ void __launch_bounds__(kKThreads, 1)
         const int db = k0 + quarter * 32 - (q0 + half * 64);
         table = db - 63 < seg_start || key_last >= L || (p.mask == 1 && db + 31 > 0);
         if (table) {
-          flush_far();
+          if (seg_used) flush_far();
+          seg_used = false;
           const int d[3] = {db + lane, db + lane - 32, db + lane - 64};
           rel_segments<3>(rs, rel_steps(rel.nseg), d, at);
 #pragma unroll
@@ -896,6 +919,8 @@ __global__ void __launch_bounds__(kKThreads, 1)
           seg_start = rs.start[seg];
           seg_bias = rs.bias[seg];
           __syncwarp();
+        } else {
+          seg_used = true;
         }
       }
       if (!warp_all(mbar_wait(bar(kKBarSFull), t & 1, p.timeout_ns))) {
@@ -905,7 +930,7 @@ __global__ void __launch_bounds__(kKThreads, 1)
       }
       // Rel: a step that takes the table and one of two blocks of one segment each run code of their
       // own, with marks at both ends that keep the compiler from merging parts of them: moves between
-      // the variants' registers cost 200 instructions a step (2025 us for the big model's heads, 1669 so)
+      // the variants' registers cost 200 instructions a step (2025 us for the big model's heads, 1652 so)
       auto step = [&](auto kind) -> bool {
         [[maybe_unused]] constexpr bool kTable = decltype(kind)::value;
         tc_fence_after();
@@ -975,10 +1000,9 @@ __global__ void __launch_bounds__(kKThreads, 1)
         if constexpr (kRel) {
           if constexpr (kTable) {  // after the products have what they wait for
             float v[3] = {0.f, 0.f, 0.f};
-            diagonal_sums(g0, lane, v[0], v[1]);
+            diagonal_sums(g0, lane, v[0], v[1]);  // shuffles: all lanes have read the table
             diagonal_sums(g1, lane, v[1], v[2]);
-#pragma unroll
-            for (int e = 0; e < 3; ++e) segment_sums(v[e], at[e], lane, buf + 96, own);
+            segment_sums(v, at, lane, buf, own);  // (the table is done with)
           }
         }
         return true;
