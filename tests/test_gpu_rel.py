@@ -350,6 +350,50 @@ def test_fp32_rows_of_odd_strides_and_addresses():
     assert torch.equal(a, b)
 
 
+def test_fp32_keys_that_heads_share():
+    # inputs may have a head stride of 0; gradients come per head
+    B, H, N = 2, 4, 150
+    Q, K, V, dO, T = draw(B, H, N, N, F, 909)
+    q, g, t = dev(Q, F), dev(dO, F), dev(T, F)
+    k, v = (dev(a[:, :1], F).expand(B, H, N, 64) for a in (K, V))
+    assert k.stride(1) == 0
+    runs = []
+    for kk, vv in ((k, v), (k.contiguous(), v.contiguous())):
+        O, lse = mha.sdpa_rel_with_lse(q, kk, vv, t, "causal")
+        runs.append((O, lse) + mha.sdpa_rel_backward(q, kk, vv, t, O, g, lse, "causal") +
+                    (mha.sdpa_rel_decode(q[:, :, :2], kk, vv, t, i32([150, 33])),))
+    for a, b in zip(*runs):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_two_backwards_at_once(dtype, det_mode):
+    # on two streams, a workspace each
+    B, H, N = 4, 4, 700
+    Q, K, V, dO, T = draw(B, H, N, N, dtype, 943)
+    q, k, v, g = (dev(a, dtype) for a in (Q, K, V, dO))
+    t = dev(T, F)
+    O, lse = mha.sdpa_rel_with_lse(q, k, v, t, "causal")
+    want = mha.sdpa_rel_backward(q, k, v, t, O, g, lse, "causal")
+    n = mha.sdpa_rel_bwd_workspace_size(B, H, N, N, dtype, 32)
+    ws = [torch.empty(n, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(3):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(mha.sdpa_rel_backward(q, k, v, t, O, g, lse, "causal",
+                                                    workspace=ws[i]))
+    torch.cuda.synchronize()
+    for run in got[0] + got[1]:
+        for i, (a, b) in enumerate(zip(run, want)):
+            if i == 0 and dtype is BF and not det_mode:  # dQ's sums come in any order
+                assert torch.allclose(a.float(), b.float(), rtol=2.0 ** -6, atol=1e-3)
+            else:
+                assert torch.equal(a, b)
+
+
 def test_gradient_of_the_table_against_differences():
     # a loss sum(O dO) in fp32, differences of the fp32 forward in single buckets
     Q, K, V, dO, T = draw(2, 2, 120, 120, F, 909, num=8)
