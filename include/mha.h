@@ -327,10 +327,11 @@ int mha_kv_evict_q8(int B, int H, int Lmax, int Lmax_out, int d_k, int d_v, int 
  *   lengths  up to 2^24 positions.
  *   scale    as for mha_sdpa_fwd, within [2^-64, 2^64] where it is given.
  *   d_k, d_v bf16: 64.  fp32: 1..128.  Unlike the other fp32 entry points these use the tensor cores:
- *            forward and backward split every value into two fp16 terms under power-of-two scales (off
- *            by at most 2^-23 of the value or 2^-39 of the largest one that it shares a scale with, in
- *            its row or in 32 neighbouring rows), the generation step takes fused multiply-adds for
- *            Nq <= 2 and two tf32 terms per value for more (2^-22 of the value).  Sums are fp32.
+ *            forward and backward split every value into two fp16 terms under a power-of-two scale per
+ *            row of Q, K, V and dO (off by at most 2^-23 of the value or 2^-38 of the largest in its
+ *            row; softmax weights and their gradients likewise, with the rows that they multiply); the
+ *            generation step takes fused multiply-adds for Nq <= 2 and two tf32 terms per value for
+ *            more (2^-22 of the value).  Sums are fp32.
  *   special  Keys past key_len[b] (cache_len[b]) may hold anything, infinities and NaN included.  Under
  *   values   the causal mask an infinity or NaN in a row of K reaches only queries that see the key, but
  *            one in V may reach any query (0 times it is no number), and so may one in the backward.

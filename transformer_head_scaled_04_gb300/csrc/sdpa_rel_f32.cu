@@ -6,19 +6,24 @@
 //             dQ = scale dS K, dK = scale dS^T Q, dV = p^T dO, dt(segment) = sum of its dS
 //
 // Operands are scaled by powers of two that bring their largest value to 2^13 .. 2^14 and split into
-// two fp16 terms, a = hi + lo (mma_f16.cuh); a product is hi hi + hi lo + lo hi with fp32 sums.  The left
-// operand has a scale for every row (whose results it only touches), the right one, whose rows are
-// summed over, one for its tile of 32 rows.  What is left of a value is at most 2^-23 of it or 2^-39 of
-// the largest that shares its scale, and the dropped lo lo is at most 2^-22 of the product: fp32's own
-// accuracy.  (Two tf32 terms give the same at twice the time of the tensor cores: 8 x 8 heads of 1001
-// forward 322 us, with fp16 223 then.)  The tensor cores cut sums
-// off instead of rounding them, 2^-24 of the sum per step towards zero (9e-6 of a gradient over 900
-// keys in one chain), so the large products are kept apart from the small ones, a chain spans one
+// two fp16 terms, a = hi + lo (mma_f16.cuh); a product is hi hi + hi lo + lo hi with fp32 sums.  Every row
+// of Q, K, V and dO has a scale of its own, so no row costs another one its accuracy, whether a mask hides
+// it or not.  Scores take the two rows' factors back after the product over d.  In a product over rows the
+// right operand's factors go into the left one (p_ij with the factor of V's row j, dS_ij with K's) before
+// that is split, row by row of a tile under a scale that follows from its largest value: what no query
+// sees has a weight of 0 there.  What is left of a value is at most 2^-23 of it or 2^-38 of the largest in
+// its row (half a step of fp16's least, 2^-25, beside 2^13), and the dropped lo lo is at most 2^-22 of the
+// product: fp32's own accuracy for values that are not far below their row's largest.  (Two tf32 terms
+// give the same at twice the time of the tensor cores: the first form with fp16 terms took the forward of
+// 8 x 8 heads of 1001 from 322 us to 239.  One scale for a tile's 32 rows on the right, which a hidden row
+// of 1e8 spoils, took 195 there where this takes 214, and 695 against 710 in the backward.)  The tensor
+// cores cut sums off instead of rounding them, 2^-24 of the sum per step towards zero (9e-6 of a gradient
+// over 900 keys in one chain), so the large products are kept apart from the small ones, a chain spans one
 // tile at most, and tiles are added up with ordinary additions.
 //
 // A CTA owns 64 rows (16 per warp) and goes over the other operand in tiles of 32 rows: while one tile
-// is computed the next one's fp32 values arrive (asynchronous copies); then its largest value is
-// found and it is split into one or both of
+// is computed the next one's fp32 values arrive (asynchronous copies); then its rows' largest values
+// are found and it is split into one or both of
 //   rows   [row][d] halves, for products over d: a lane (lane = 4 g + t) reads 16 bytes of a row, eight
 //          neighbouring d, as the inner positions of two steps (any order of the inner dimension
 //          gives the same sum); 16-byte units of odd rows are swapped by 4, which frees the reads of
@@ -164,39 +169,45 @@ struct Share {
   __device__ __forceinline__ static float top(const float4& v) {
     return fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
   }
-  // reads the share; the bits of its largest |value|
-  __device__ __forceinline__ uint32_t read(const float* raw) {
-    float m = 0.f;
-#pragma unroll
-    for (int i = 0; i < kItems; ++i)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float4 v = *reinterpret_cast<const float4*>(raw + row(i, k) * DP + col(i));
-        x[i][k] = v;
-        m = fmaxf(fmax3(m, fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
-      }
-    return __float_as_uint(m);
-  }
-  // that of its largest finite one
-  __device__ __forceinline__ uint32_t finite() const {
-    float m = 0.f;
+  __device__ __forceinline__ void read(const float* raw) {
 #pragma unroll
     for (int i = 0; i < kItems; ++i)
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        for (float v : {x[i][k].x, x[i][k].y, x[i][k].z, x[i][k].w})
-          if (fabsf(v) < INFINITY) m = fmaxf(m, fabsf(v));
-    return __float_as_uint(m);
+        x[i][k] = *reinterpret_cast<const float4*>(raw + row(i, k) * DP + col(i));
   }
-  // writes its terms as rows and as pairs, either may be null
-  __device__ __forceinline__ void write(float mul, uint8_t* to_rows, uint32_t* to_pairs) const {
-    const float2 mul2 = make_float2(mul, mul);
+  // the scales of the four rows of x[i], from the largest |value| in each: its exponent is the top of
+  // the upper 16 bits, two rows' of which meet in one word
+  __device__ __forceinline__ void scales(int i, Scale (&f)[4]) const {
+    uint32_t w[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      w[u] = __byte_perm(__float_as_uint(top(x[i][2 * u])), __float_as_uint(top(x[i][2 * u + 1])),
+                         0x7632);
+#pragma unroll
+    for (int off = 1; off < DP / 4; off <<= 1)  // the DP / 4 lanes of a row
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        w[u] = __vmaxu2(w[u], __shfl_xor_sync(0xffffffffu, w[u], off));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) f[k] = scale_for(k & 1 ? w[k >> 1] : w[k >> 1] << 16);
+  }
+  // writes its terms as rows and as pairs, either may be null, every row under a scale of its own; the
+  // factors that undo the scales go to inv
+  __device__ __forceinline__ void write(uint8_t* to_rows, uint32_t* to_pairs, float* inv) const {
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
       const int c = col(i);
+      Scale f[4];
+      scales(i, f);
+      if (c == 0) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) inv[row(i, k)] = f[k].inv;
+      }
       float2 v[4][2];  // row k, columns c + 2 u, + 1
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
+        const float2 mul2 = make_float2(f[k].mul, f[k].mul);
         v[k][0] = fmul2(make_float2(x[i][k].x, x[i][k].y), mul2);
         v[k][1] = fmul2(make_float2(x[i][k].z, x[i][k].w), mul2);
       }
@@ -231,20 +242,16 @@ struct Share {
       }
     }
   }
-  // writes its terms, rows row0 .. of the CTA's own, as fragments, every row under a scale of its own;
-  // the factors that undo the scales go to inv
+  // the same for rows row0 .. of the CTA's own, as fragments
   __device__ __forceinline__ void write_own(uint32_t* to, int row0, float* inv) const {
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
       const int c = col(i), unit = c >> 3, step = 2 * (unit >> 2) + ((c >> 2) & 1);
+      Scale f[4];
+      scales(i, f);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        float m = top(x[i][k]);
-#pragma unroll
-        for (int off = 1; off < DP / 4; off <<= 1)  // the DP / 4 lanes of a row
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-        const Scale f = scale_for(__float_as_uint(m));
-        const float2 mul2 = make_float2(f.mul, f.mul);
+        const float2 mul2 = make_float2(f[k].mul, f[k].mul);
         const int r = row0 + row(i, k), g = r & 7;
         uint32_t* at = to + (((r >> 4) * (DP / 16) + step) * 32 + 4 * g + (unit & 3)) * 4 +
                        ((r >> 3) & 1);
@@ -255,19 +262,11 @@ struct Share {
         at[2] = h1;
         at[kRows * DP / 2] = rest_of(v0, h0);
         at[kRows * DP / 2 + 2] = rest_of(v1, h1);
-        if (c == 0) inv[r] = f.inv;
+        if (c == 0) inv[r] = f[k].inv;
       }
     }
   }
 };
-
-// the largest of all threads' bits, by way of one word per warp (a barrier inside)
-__device__ __forceinline__ uint32_t block_max(uint32_t top, uint32_t* red) {
-  top = __reduce_max_sync(0xffffffffu, top);
-  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = top;
-  __syncthreads();
-  return max(max(red[0], red[1]), max(red[2], red[3]));
-}
 
 // The CTA's own 64 rows, split into fragments, and the factors that undo their scales; raw is scratch.
 template <int DP, bool kVec>
@@ -377,6 +376,16 @@ __device__ __forceinline__ Scale score_scale(const float (&p)[kNT][4], int half)
   return scale_for(__float_as_uint(m));
 }
 
+// the scores of columns 8 n + 2 t and + 1 times mul[column]
+__device__ __forceinline__ void scale_columns(float (&p)[kNT][4], const float* mul, int t) {
+#pragma unroll
+  for (int n = 0; n < kNT; ++n) {
+    const float2 f = *reinterpret_cast<const float2*>(mul + 8 * n + 2 * t);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) set_pair(p[n], i, fmul2(pair_of(p[n], i), f));
+  }
+}
+
 // o[2 v + e] (d = 16 v + 2 g + e) += P B over the tile's rows (B as pairs), rows g and g + 8 times inv0
 // and inv1
 template <int DP>
@@ -452,24 +461,29 @@ __device__ __forceinline__ int keys_of(const RelF32& p, int b) {
   return p.mask == 2 ? min(max(__ldg(p.key_len + b), 0), p.Nk) : p.Nk;
 }
 
-// x = s f + t (f0, f1: rows g and g + 8): t the constant, or of the lane's columns 8 n + 2 t, + 1 and
-// rows g, g + 8 from the table (at: its entry for column 0 and row g; a row less is a distance more)
-__device__ __forceinline__ void add_bias(float (&s)[kNT][4], float f0, float f1, bool near,
-                                         float constant, const float* at) {
+// x = s f + t, f = f0 (row g) or f1 (g + 8) times col[column]; t the constant, or of the lane's columns
+// 8 n + 2 t, + 1 and rows g, g + 8 from the table (at: its entry for column 2 t and row g; a row less is
+// a distance more)
+__device__ __forceinline__ void add_bias(float (&s)[kNT][4], float f0, float f1, const float* col,
+                                         int t, bool near, float constant, const float* at) {
   const float2 f[2] = {make_float2(f0, f0), make_float2(f1, f1)};
   if (near) {
 #pragma unroll
-    for (int n = 0; n < kNT; ++n)
+    for (int n = 0; n < kNT; ++n) {
+      const float2 c = *reinterpret_cast<const float2*>(col + 8 * n + 2 * t);
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        set_pair(s[n], i, ffma2(pair_of(s[n], i), f[i],
+        set_pair(s[n], i, ffma2(pair_of(s[n], i), fmul2(f[i], c),
                                 make_float2(at[8 * n - 8 * i], at[8 * n + 1 - 8 * i])));
+    }
   } else {
 #pragma unroll
-    for (int n = 0; n < kNT; ++n)
+    for (int n = 0; n < kNT; ++n) {
+      const float2 c = *reinterpret_cast<const float2*>(col + 8 * n + 2 * t);
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        set_pair(s[n], i, ffma2(pair_of(s[n], i), f[i], make_float2(constant, constant)));
+        set_pair(s[n], i, ffma2(pair_of(s[n], i), fmul2(f[i], c), make_float2(constant, constant)));
+    }
   }
 }
 
@@ -480,8 +494,7 @@ struct FwdSmem {
   uint8_t K[rows_bytes<DP>(kTile)];
   uint32_t V[pairs_bytes<DP>() / 4];
   float rawK[kTile * DP], rawV[kTile * DP];
-  float table[kDist + 1], q_inv[kRows];
-  uint32_t red[2][kWarps];
+  float table[kDist + 1], q_inv[kRows], k_inv[kTile], v_inv[kTile];
   RelShared rs;
 };
 
@@ -533,25 +546,12 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 3 : 2)
     if (near && threadIdx.x < kDist)
       sm.table[threadIdx.x] =
           sm.rs.bias[rel_segment(sm.rs, rel_steps(rel.nseg), d0 + threadIdx.x)];
-    float k_inv, v_inv;
     {
       Share<DP> k, v;
-      uint32_t tk = 0, tv = 0;
-      auto tops = [&](uint32_t ks, uint32_t vs) {
-        ks = __reduce_max_sync(0xffffffffu, ks);
-        tv = block_max(vs, (sm.red[1][warp] = ks, sm.red[0]));
-        tk = max(max(sm.red[1][0], sm.red[1][1]), max(sm.red[1][2], sm.red[1][3]));
-      };
-      tops(k.read(sm.rawK), v.read(sm.rawV));
-      if (max(tk, tv) == 0x7f800000u) {  // an infinity leaves the keys that a row sees their scale
-        __syncthreads();
-        tops(k.finite(), v.finite());
-      }
-      const Scale fk = scale_for(tk), fv = scale_for(tv);
-      k.write(fk.mul, sm.K, nullptr);
-      v.write(fv.mul, nullptr, sm.V);
-      k_inv = fk.inv;
-      v_inv = fv.inv;
+      k.read(sm.rawK);
+      v.read(sm.rawV);
+      k.write(sm.K, nullptr, sm.k_inv);
+      v.write(nullptr, sm.V, sm.v_inv);
     }
     __syncthreads();
     if (j + 1 < nt) load(j + 1);
@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 3 : 2)
       float s[kNT][4];
       product_d<DP>(s, sm.Q, warp, lane, sm.K);
       float mx[2] = {-INFINITY, -INFINITY};
-      add_bias(s, k_inv * q_inv[0], k_inv * q_inv[1], near, seg_bias,
+      add_bias(s, q_inv[0], q_inv[1], sm.k_inv, t, near, seg_bias,
                sm.table + 2 * t - (16 * warp + g) + kRows - 1);
       if (j * kTile + kTile - 1 > (p.mask == 1 ? q0 + 16 * warp : L - 1)) {
 #pragma unroll
@@ -599,8 +599,9 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 3 : 2)
           for (int i = 0; i < 2; ++i)
             set_pair(o[u], i, fmul2(pair_of(o[u], i), make_float2(alpha[i], alpha[i])));
       }
-      const float inv = v_inv * 0x1p-14f;
-      product_rows<DP>(o, ScoreFrags(s, 0x1p14f, 0x1p14f), sm.V, inv, inv, g, t);
+      scale_columns(s, sm.v_inv, t);
+      const Scale f0 = score_scale(s, 0), f1 = score_scale(s, 1);
+      product_rows<DP>(o, ScoreFrags(s, f0.mul, f1.mul), sm.V, f0.inv, f1.inv, g, t);
     }
   }
   float* ob = p.out + b * p.st[3][0] + h * p.st[3][1];
@@ -632,8 +633,8 @@ struct DqSmem {
   };
   float rawK[kTile * DP], rawV[kTile * DP];
   float D[kRows], lse[kRows], q_inv[kRows], g_inv[kRows];
+  float k_inv[kTile], v_inv[kTile];
   float table[kDist + 1];
-  uint32_t red[2][kWarps];
   float far[kWarps];
   float part[kWarps][32];  // a warp's sums of the segments span[..][0] .. span[..][1]
   int span[kWarps][2];
@@ -702,18 +703,12 @@ __device__ __forceinline__ void queries_part(const RelF32& p, const RelBias& rel
       dist_seg = rel_segment(sm.rs, rel_steps(rel.nseg), d0 + tid);
       if (tid < kDist) sm.table[tid] = sm.rs.bias[dist_seg];
     }
-    float k_inv, v_inv;
     {
       Share<DP> k, v;
-      const uint32_t tk = __reduce_max_sync(0xffffffffu, k.read(sm.rawK));
-      const uint32_t tv = block_max(v.read(sm.rawV), (sm.red[1][warp] = tk, sm.red[0]));
-      const Scale fk = scale_for(max(max(sm.red[1][0], sm.red[1][1]),
-                                     max(sm.red[1][2], sm.red[1][3])));
-      const Scale fv = scale_for(tv);
-      k.write(fk.mul, sm.K, sm.Kp);
-      v.write(fv.mul, sm.V, nullptr);
-      k_inv = fk.inv;
-      v_inv = fv.inv;
+      k.read(sm.rawK);
+      v.read(sm.rawV);
+      k.write(sm.K, sm.Kp, sm.k_inv);
+      v.write(sm.V, nullptr, sm.v_inv);
     }
     __syncthreads();
     if (j + 1 < nt) load(j + 1);
@@ -723,8 +718,7 @@ __device__ __forceinline__ void queries_part(const RelF32& p, const RelBias& rel
       float dp[kNT][4];
       product_d<DP>(s, sm.Q, warp, lane, sm.K);
       product_d<DP>(dp, sm.G, warp, lane, sm.V);
-      const float fg[2] = {v_inv * g_inv[0], v_inv * g_inv[1]};
-      add_bias(s, k_inv * q_inv[0], k_inv * q_inv[1], near, seg_bias,
+      add_bias(s, q_inv[0], q_inv[1], sm.k_inv, t, near, seg_bias,
                sm.table + 2 * t - r_loc[0] + kRows - 1);
       if (j * kTile + kTile - 1 > (p.mask == 1 ? q0 + 16 * warp : L - 1)) {
 #pragma unroll
@@ -734,15 +728,17 @@ __device__ __forceinline__ void queries_part(const RelF32& p, const RelBias& rel
             if (j * kTile + 8 * n + 2 * t + (i & 1) > limit[i >> 1]) s[n][i] = -INFINITY;
       }
 #pragma unroll
-      for (int n = 0; n < kNT; ++n)
+      for (int n = 0; n < kNT; ++n) {
+        const float2 c = *reinterpret_cast<const float2*>(sm.v_inv + 8 * n + 2 * t);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           float2 x = fadd2(pair_of(s[n], i), make_float2(-lse[i], -lse[i]));
           x = fmul2(x, make_float2(kLog2e, kLog2e));
           x = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-          set_pair(s[n], i, fmul2(x, ffma2(pair_of(dp[n], i), make_float2(fg[i], fg[i]),
-                                           make_float2(-D[i], -D[i]))));
+          const float2 fg = fmul2(make_float2(g_inv[i], g_inv[i]), c);
+          set_pair(s[n], i, fmul2(x, ffma2(pair_of(dp[n], i), fg, make_float2(-D[i], -D[i]))));
         }
+      }
     }
     if (near) {
       __syncthreads();  // K and V as rows are done with
@@ -759,9 +755,9 @@ __device__ __forceinline__ void queries_part(const RelF32& p, const RelBias& rel
       }
     }
     if (!skip) {
+      scale_columns(s, sm.k_inv, t);
       const Scale f0 = score_scale(s, 0), f1 = score_scale(s, 1);
-      product_rows<DP>(dq, ScoreFrags(s, f0.mul, f1.mul), sm.Kp, f0.inv * k_inv, f1.inv * k_inv, g,
-                       t);
+      product_rows<DP>(dq, ScoreFrags(s, f0.mul, f1.mul), sm.Kp, f0.inv, f1.inv, g, t);
     }
     if (near) {  // sums over the diagonals, one per thread, then over each warp's segments
       __syncthreads();
@@ -808,9 +804,9 @@ struct DkdvSmem {
   uint32_t Qp[pairs_bytes<DP>() / 4], Gp[pairs_bytes<DP>() / 4];
   float rawQ[kTile * DP], rawG[kTile * DP];
   float D[kTile], lse[kTile];  // both negated
+  float q_inv[kTile], g_inv[kTile];
   float k_inv[kRows], v_inv[kRows];
   float table[kDist + 1];
-  uint32_t red[2][kWarps];
   RelShared rs;
 };
 
@@ -862,42 +858,29 @@ __device__ __forceinline__ void keys_part(const RelF32& p, const RelBias& rel, D
       }
       if (near && tid < kDist)
         sm.table[tid] = sm.rs.bias[rel_segment(sm.rs, rel_steps(rel.nseg), d0 + tid)];
-      float q_inv, g_inv;
       {
         Share<DP> q, o;
-        const uint32_t tq = __reduce_max_sync(0xffffffffu, q.read(sm.rawQ));
-        const uint32_t tg = block_max(o.read(sm.rawG), (sm.red[1][warp] = tq, sm.red[0]));
-        const Scale fq = scale_for(max(max(sm.red[1][0], sm.red[1][1]),
-                                       max(sm.red[1][2], sm.red[1][3])));
-        const Scale fg = scale_for(tg);
-        q.write(fq.mul, sm.Q, sm.Qp);
-        o.write(fg.mul, sm.G, sm.Gp);
-        q_inv = fq.inv;
-        g_inv = fg.inv;
+        q.read(sm.rawQ);
+        o.read(sm.rawG);
+        q.write(sm.Q, sm.Qp, sm.q_inv);
+        o.write(sm.G, sm.Gp, sm.g_inv);
       }
       __syncthreads();
       if (i + 1 < ni) load(i + 1);
       float s[kNT][4], ds[kNT][4];
       product_d<DP>(s, sm.K, warp, lane, sm.Q);
       product_d<DP>(ds, sm.V, warp, lane, sm.G);
-      const float f[2] = {q_inv * k_inv[0], q_inv * k_inv[1]};
-      const float fg[2] = {g_inv * v_inv[0], g_inv * v_inv[1]};
       // the table by row (key) minus column (query): a row more is a distance more
-      if (near) {
-        const float* at = sm.table + 16 * warp + g - 2 * t + kTile - 1;
+      const float* at = sm.table + 16 * warp + g - 2 * t + kTile - 1;
 #pragma unroll
-        for (int n = 0; n < kNT; ++n)
+      for (int n = 0; n < kNT; ++n) {
+        const float2 c = *reinterpret_cast<const float2*>(sm.q_inv + 8 * n + 2 * t);
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            set_pair(s[n], e, ffma2(pair_of(s[n], e), make_float2(f[e], f[e]),
-                                    make_float2(at[8 * e - 8 * n], at[8 * e - 8 * n - 1])));
-      } else {
-#pragma unroll
-        for (int n = 0; n < kNT; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            set_pair(s[n], e, ffma2(pair_of(s[n], e), make_float2(f[e], f[e]),
-                                    make_float2(seg_bias, seg_bias)));
+        for (int e = 0; e < 2; ++e) {
+          const float2 bias = near ? make_float2(at[8 * e - 8 * n], at[8 * e - 8 * n - 1])
+                                   : make_float2(seg_bias, seg_bias);
+          set_pair(s[n], e, ffma2(pair_of(s[n], e), fmul2(make_float2(k_inv[e], k_inv[e]), c), bias));
+        }
       }
       if (k0 + 16 * warp + 15 >= L || (p.mask == 1 && k0 + 16 * warp + 15 > q0)) {
 #pragma unroll
@@ -912,20 +895,23 @@ __device__ __forceinline__ void keys_part(const RelF32& p, const RelBias& rel, D
       for (int n = 0; n < kNT; ++n) {
         const float2 lse = *reinterpret_cast<const float2*>(sm.lse + 8 * n + 2 * t);
         const float2 D = *reinterpret_cast<const float2*>(sm.D + 8 * n + 2 * t);
+        const float2 c = *reinterpret_cast<const float2*>(sm.g_inv + 8 * n + 2 * t);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           float2 x = fadd2(pair_of(s[n], e), lse);
           x = fmul2(x, make_float2(kLog2e, kLog2e));
           x = make_float2(ex2_approx(x.x), ex2_approx(x.y));
           set_pair(s[n], e, x);
-          set_pair(ds[n], e, fmul2(x, ffma2(pair_of(ds[n], e), make_float2(fg[e], fg[e]), D)));
+          const float2 fg = fmul2(make_float2(v_inv[e], v_inv[e]), c);
+          set_pair(ds[n], e, fmul2(x, ffma2(pair_of(ds[n], e), fg, D)));
         }
       }
+      scale_columns(s, sm.g_inv, t);
       const Scale s0 = score_scale(s, 0), s1 = score_scale(s, 1);
-      product_rows<DP>(dv, ScoreFrags(s, s0.mul, s1.mul), sm.Gp, s0.inv * g_inv, s1.inv * g_inv, g, t);
+      product_rows<DP>(dv, ScoreFrags(s, s0.mul, s1.mul), sm.Gp, s0.inv, s1.inv, g, t);
+      scale_columns(ds, sm.q_inv, t);
       const Scale d0s = score_scale(ds, 0), d1s = score_scale(ds, 1);
-      product_rows<DP>(dk, ScoreFrags(ds, d0s.mul, d1s.mul), sm.Qp, d0s.inv * q_inv, d1s.inv * q_inv,
-                       g, t);
+      product_rows<DP>(dk, ScoreFrags(ds, d0s.mul, d1s.mul), sm.Qp, d0s.inv, d1s.inv, g, t);
     }
   }
   float* ok = p.dK + b * p.st[6][0] + h * p.st[6][1];
