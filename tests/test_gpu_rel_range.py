@@ -70,3 +70,41 @@ def test_fp32_rows_that_are_not_seen_may_be_of_any_size(hidden, where, size, d):
         w = ref.sdpa_rel_bwd_ref(Q, K, V, T, dO, given=given, **how)[3]
         tol = ref.table_grad_bound(Q, K, V, T, dO, *given, **how)
     within(host(got[3]), w, tol + 2.0 ** -24 * np.abs(w), "dtable")
+
+
+# ------------------------------------------------------------------ lengths that the last launch writes
+@pytest.mark.parametrize("bias", [False, True])
+def test_lengths_from_the_kernel_before(bias):
+    # an eviction writes the lengths that the attention right behind it goes by, in one graph: the
+    # attention's blocks may start before the eviction is through, but read no length before that
+    B, H, L, N = 16, 16, 8192, 300
+    cache, small = (mha.kv_cache_q8(B, H, n) for n in (L, N))
+    cache.weights.uniform_()
+    lens = i32([L if b % 3 else 17 * b for b in range(B)])
+    n, kept = torch.zeros_like(lens), torch.empty((B, H, N), dtype=torch.int32, device="cuda")
+    torch.manual_seed(2)
+    q, k, v = (torch.randn(B, H, N, 64, device="cuda").to(BF) for _ in range(3))
+    t = torch.randn(32, H, device="cuda")
+
+    def attend():
+        if bias:
+            return mha.sdpa_rel_with_lse(q, k, v, t, "key_padding", n)
+        return mha.sdpa_with_lse(q, k, v, "key_padding", n)
+
+    def both():
+        mha.kv_evict_q8(cache, small, lens, keep=N, len_out=n, kept=kept)
+        return attend()
+
+    both()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = both()
+    for _ in range(20):
+        n.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert n.tolist() == [min(x, N) for x in lens.tolist()]
+        for a, b in zip(got, attend()):
+            assert torch.equal(a, b)

@@ -156,8 +156,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   const int q0 = qt * kBQ;
   int L = p.Nk;
-  if (p.mask == 2 && bounds_ok(b, p.B, p.status, kSiteKeyLen))
+  if (p.mask == 2 && bounds_ok(b, p.B, p.status, kSiteKeyLen)) {
+    pdl_wait();  // the lengths may be the previous kernel's output
     L = min(max(__ldg(p.key_len + b), 0), p.Nk);
+  }
   const int last = min(q0 + kBQ, p.Nq) - 1;
   int kt0 = 0, nt;
   if (p.mask == 1) {
