@@ -108,3 +108,22 @@ def test_lengths_from_the_kernel_before(bias):
         assert n.tolist() == [min(x, N) for x in lens.tolist()]
         for a, b in zip(got, attend()):
             assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------ NaN and infinities that are seen
+@pytest.mark.parametrize("dtype,Nq", [(BF, 1), (BF, 5), (F, 1), (F, 2), (F, 5)])
+@pytest.mark.parametrize("bad", [np.nan, np.inf])
+@pytest.mark.parametrize("L", [40, 3000])
+def test_step_shows_nan_that_a_query_sees(dtype, Nq, bad, L):
+    # a NaN among a query's scores makes its row NaN, not zeros (those say that it sees no key)
+    Q, K, V, _, T = draw(3, 2, Nq, L, dtype, 970)
+    q, k, v, t = (dev(a, dtype) for a in (Q, K, V, T))
+    n = i32([L, L // 2, 0])
+    want = mha.sdpa_rel_decode(q, k, v, t, n)
+    k[:2, :, 7] = bad
+    k[2] = bad
+    got = mha.sdpa_rel_decode(q, k, v, t, n)
+    assert torch.all(torch.isnan(got[:2])) and torch.all(got[2] == 0)
+    k[1] = dev(K, dtype)[1]  # the sequences beside it are as before
+    got = mha.sdpa_rel_decode(q, k, v, t, n)
+    assert torch.all(torch.isnan(got[0])) and torch.equal(got[1], want[1])

@@ -163,7 +163,7 @@ __device__ __forceinline__ void join_warps(const Params& p, const float* so, con
                                            float unit, int64_t bh, int split, T* O) {
   const int Nq = p.Nq;
   __syncthreads();
-  for (int e = threadIdx.x; e < Nq * DP; e += kThreads) {
+  for (int e = threadIdx.x; e < Nq * DP; e += kThreads) {  // (a sum of 0: no key; NaN stays NaN)
     const int row = e / DP, d = e % DP;
     float m = -INFINITY;
 #pragma unroll
@@ -177,7 +177,7 @@ __device__ __forceinline__ void join_warps(const Params& p, const float* so, con
       o = fmaf(a, so[(w * Nq + row) * DP + d], o);
     }
     if (p.n_split == 1) {
-      if (d < p.d_v) O[row * p.so[2] + d] = static_cast<T>(l > 0.f ? o / l : 0.f);
+      if (d < p.d_v) O[row * p.so[2] + d] = static_cast<T>(l == 0.f ? 0.f : o / l);
     } else {
       const int64_t i = (bh * p.n_split + split) * Nq + row;
       p.part[i * DP + d] = o;
@@ -633,7 +633,7 @@ __global__ void __launch_bounds__(kJoinThreads)
 #pragma unroll
     for (int i = 1; i < kGroups; ++i) o += sum[i * DP + tid];
     T* O = static_cast<T*>(p.O) + b * p.so[0] + h * p.so[1] + row * p.so[2];
-    O[tid] = static_cast<T>(l > 0.f ? o / l : 0.f);
+    O[tid] = static_cast<T>(l == 0.f ? 0.f : o / l);
   }
 }
 
