@@ -6,7 +6,7 @@ import torch
 
 from oracle import rel_bias as ref
 from parity_util import assert_f32_close
-from test_gpu_rel import BF, F, dev, draw, host, i32, within
+from test_gpu_rel import BF, F, det_mode, dev, draw, host, i32, plain64, within  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -127,3 +127,56 @@ def test_step_shows_nan_that_a_query_sees(dtype, Nq, bad, L):
     k[1] = dev(K, dtype)[1]  # the sequences beside it are as before
     got = mha.sdpa_rel_decode(q, k, v, t, n)
     assert torch.all(torch.isnan(got[0])) and torch.equal(got[1], want[1])
+
+
+# ------------------------------------------------------------------ long sums of the table's gradient
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("B,H,N", [(65535, 1, 2), (1, 1, 131072)])
+def test_table_gradient_over_long_sums(dtype, B, H, N, det_mode):
+    # Every pair's dS is the same number: with Q = K = 0, a table of zeros, lse = 0 and O = 0 the weight is
+    # 2^0 and dS = dO.V = x.  x has 18 bits, so 64 of them add up exactly; what is left are the roundings
+    # of sums over lanes, warps and tiles, fewer than 32 of 2^-24 in a row of additions whose length does
+    # not count.  (One running sum of 1024 x is off by 6.6e-6 of it, one of 8192 by 8e-5.)
+    if det_mode and dtype is F:
+        pytest.skip("the switch works on bf16 alone")
+    zero = torch.zeros(B, H, N, 64, dtype=dtype, device="cuda")
+    v, do = zero.clone(), zero.clone()
+    v[..., 3], v[..., 17], v[..., 40] = 129, 131 / 256, 3 / 1024
+    do[..., 3] = do[..., 17] = do[..., 40] = 1
+    x = 129 + 131 / 256 + 3 / 1024
+    t = torch.zeros(4, H, device="cuda")  # at the query; before it; none; after it
+    lse = torch.zeros(B, H, N, device="cuda")
+    dq, dk, dv, dt = mha.sdpa_rel_backward(zero, zero, v, t, zero, do, lse, max_distance=2)
+    pairs = B * N * (N - 1) / 2
+    want = np.array([B * N * x, pairs * x, 0, pairs * x])[:, None].repeat(H, 1)
+    within(host(dt), want, 32 * 2.0 ** -24 * want, "dtable")
+    assert torch.all(dq == 0) and torch.all(dk == 0)
+
+
+@pytest.mark.parametrize("dtype,N,causal", [(BF, 4001, False), (BF, 3500, True), (F, 2500, False),
+                                            (F, 2100, True)])
+def test_table_gradient_of_long_sequences_bucket_by_bucket(dtype, N, causal):
+    # every bucket within its own bound (table_grad_bound's, in 64 bits on the GPU), from the stored O and
+    # lse; the largest gradients are far above theirs
+    torch.manual_seed(N)
+    q, k, v, do = (torch.randn(1, 2, N, 64, device="cuda").to(dtype) for _ in range(4))
+    t = torch.randn(32, 2, device="cuda") * 1.5
+    how = dict(mask="causal" if causal else "none", max_distance=128, bidirectional=not causal)
+    O, lse = mha.sdpa_rel_with_lse(q, k, v, t, **how)
+    got = mha.sdpa_rel_backward(q, k, v, t, O, do, lse, **how)[3].double()
+    want = plain64(q, k, v, t, do, causal, 128, not causal, given=(O, lse))[5]
+    q, k, v, do, O = (x.double() for x in (q, k, v, do, O))
+    u = torch.tensor(ref.bucket_table(-(N - 1), N - 1, 32, 128, not causal), device="cuda")
+    d = torch.arange(N, device="cuda") - torch.arange(N, device="cuda")[:, None]
+    x = q @ k.transpose(2, 3) / 8 + t.double()[u[d + N - 1]].permute(2, 0, 1) - lse.double()[..., None]
+    if causal:
+        x = x.masked_fill(d > 0, -float("inf"))
+    dP, D = do @ v.transpose(2, 3), (do * O).sum(-1, keepdim=True)
+    size = do.abs() @ v.abs().transpose(2, 3) + (do * O).abs().sum(-1, keepdim=True)
+    e = torch.exp(x) * (2.0 ** -15 * (dP.abs() + D.abs()) + 2.0 ** -17 * size)
+    tol = torch.zeros_like(want)
+    for i in range(2 * N - 1):
+        tol[u[i]] += e.diagonal(i - (N - 1), 2, 3).sum((0, 2))
+    within(got.cpu().numpy(), want.cpu().numpy(), (tol + 2.0 ** -24 * want.abs()).cpu().numpy(),
+           "dtable")
+    assert float((want.abs() / tol.clamp(min=1e-30)).max()) > 50  # (a bucket is empty)

@@ -82,6 +82,17 @@ __device__ __forceinline__ int rel_segment(const RelShared& sh, int steps, int d
   return s[0];
 }
 
+// A sum of any number of terms, with the rounding errors carried along (Kahan's summation): off by 2^-23
+// of the terms' sizes, however many there are.
+struct LongSum {
+  float sum = 0.f, over = 0.f;  // over: what sum holds too much
+  __device__ __forceinline__ void add(float x) {
+    const float y = x - over, next = sum + y;
+    over = (next - sum) - y;
+    sum = next;
+  }
+};
+
 // The gradient of head h's column of the table, by a block of kRelGradThreads threads:
 // dtable[bucket of s, h] = sum over batch elements and tiles of partial[b, h, tile, s], in a fixed
 // order; buckets without a segment get 0.
@@ -106,7 +117,7 @@ __device__ __forceinline__ void rel_table_grad(const RelBias& rel, void* dtable,
   }
   for (int s0 = 0; s0 < rel.nseg; s0 += 32) {
     const int s = s0 + lane;
-    float v = 0.f;
+    LongSum v;
     if (s < rel.nseg) {
       const float* head = rel.partial + static_cast<int64_t>(h) * tiles * rel.nseg + s;
       const int64_t rows = static_cast<int64_t>(B) * tiles;
@@ -115,12 +126,12 @@ __device__ __forceinline__ void rel_table_grad(const RelBias& rel, void* dtable,
       while (tile >= tiles) tile -= tiles, ++b;
 #pragma unroll 4
       for (int64_t r = warp; r < rows; r += kWarps) {
-        v += head[(r + b * skip) * rel.nseg];
+        v.add(head[(r + b * skip) * rel.nseg]);
         tile += kWarps;
         while (tile >= tiles) tile -= tiles, ++b;
       }
     }
-    part[warp][lane] = v;
+    part[warp][lane] = v.sum;
     __syncthreads();
     if (warp == 0 && s < rel.nseg) {
       float sum = 0.f;

@@ -40,7 +40,8 @@
 // from a table of the warp's 95 distances in shared memory (-inf where masked), and after the products
 // have what they wait for dS is summed along the diagonals: lane r takes column i's value from lane
 // (r + i) % 32, which puts a distance's values into one lane, and a segmented scan over the lanes gives
-// the segments' sums.  Lane s % 32 owns segment s; the CTA writes one sum per segment, and a last launch
+// the segments' sums.  Lane s % 32 owns segment s (sums over steps carry their roundings along, LongSum:
+// their number is up to the caller); the CTA writes one sum per segment, and a last launch
 // adds those of a head in a fixed order, so the gradient is bitwise reproducible.  Keys past key_len[b]
 // may hold anything there: their rows of K and V are cleared before the first product.
 #include <cuda_bf16.h>
@@ -248,7 +249,7 @@ __device__ __forceinline__ void diagonal_sums(const uint32_t (&g)[32], int lane,
 // own is indexed by a variable on purpose: it stays in local memory, away from the registers of steps that
 // need none.
 __device__ __forceinline__ void segment_sums(float (&v)[3], const int (&seg)[3], int lane, float* part,
-                                             float (&own)[kRelMaxSeg / 32]) {
+                                             LongSum (&own)[kRelMaxSeg / 32]) {
   int first[3], last[3];
 #pragma unroll
   for (int e = 0; e < 3; ++e) {
@@ -281,7 +282,7 @@ __device__ __forceinline__ void segment_sums(float (&v)[3], const int (&seg)[3],
 #pragma unroll
     for (int e = 0; e < 3; ++e)
       if (s >= first[e] && s <= last[e]) sum += part[32 * e + s - first[e]];
-    own[k] += sum;
+    own[k].add(sum);
   }
   __syncwarp();
 }
@@ -880,7 +881,8 @@ __global__ void __launch_bounds__(kKThreads, 1)
     [[maybe_unused]] float* none =  // 64 of -inf, the table of a key past key_len
         reinterpret_cast<float*>(smem + k_off_table(kFused)) + kMathWarps * kRelMaxSeg;
     [[maybe_unused]] int seg = 0, seg_start = INT_MAX;
-    [[maybe_unused]] float seg_bias = 0.f, far = 0.f;
+    [[maybe_unused]] float seg_bias = 0.f;
+    [[maybe_unused]] LongSum far;
     [[maybe_unused]] bool seg_used = false;
     if constexpr (kRel) {  // while the first tiles arrive; every math warp passes here
       if (threadIdx.x <= kRelMaxSeg) rel_load(rs, rel, h, threadIdx.x, kLog2e);
@@ -890,12 +892,13 @@ __global__ void __launch_bounds__(kKThreads, 1)
       seg_start = rs.start[seg];
       seg_bias = rs.bias[seg];
     }
-    [[maybe_unused]] float own[kRelMaxSeg / 32] = {};
+    [[maybe_unused]] LongSum own[kRelMaxSeg / 32];
     [[maybe_unused]] auto flush_far = [&]() {
+      float v = far.sum;
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) far += __shfl_xor_sync(0xffffffffu, far, off);
-      if (lane == (seg & 31)) own[seg >> 5] += far;
-      far = 0.f;
+      for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+      if (lane == (seg & 31)) own[seg >> 5].add(v);
+      far = LongSum();
     };
     const int key_last = k0 + quarter * 32 + 31;  // the warp's last key
     bool ok = true;
@@ -960,7 +963,7 @@ __global__ void __launch_bounds__(kKThreads, 1)
           float2 f = make_float2(0.f, 0.f);
           dkdv_half_rel<kTable>(s0, s1, g0, g1, c, seg_bias, key < L ? buf + 64 + lane : none + 63, f,
                                 pp, ds);
-          if (!kTable) far += f.x + f.y;
+          if (!kTable) far.add(f.x + f.y);
         }
         // the previous dV product must have read P^T, and the previous dK (and dQ) product
         // dS^T, before they change
@@ -1026,7 +1029,7 @@ __global__ void __launch_bounds__(kKThreads, 1)
       flush_far();
       __syncwarp();
 #pragma unroll
-      for (int k = 0; k < kRelMaxSeg / 32; ++k) buf[lane + 32 * k] = own[k];
+      for (int k = 0; k < kRelMaxSeg / 32; ++k) buf[lane + 32 * k] = own[k].sum;
     }
     if constexpr (kFused) {
       // the last query tile's dQ box

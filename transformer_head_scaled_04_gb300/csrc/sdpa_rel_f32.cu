@@ -674,23 +674,24 @@ __device__ __forceinline__ void queries_part(const RelF32& p, const RelBias& rel
   const float q_inv[2] = {sm.q_inv[r_loc[0]] * p.scale, sm.q_inv[r_loc[1]] * p.scale};
   const float g_inv[2] = {sm.g_inv[r_loc[0]], sm.g_inv[r_loc[1]]};
   float dq[DP / 8][4] = {};
-  float far = 0.f, own = 0.f;
+  LongSum far, own;
   int seg = 0, seg_next = INT_MIN;
   float seg_bias = 0.f;
   auto flush_far = [&]() {  // by all threads
+    float v = far.sum;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) far += __shfl_xor_sync(0xffffffffu, far, off);
-    if (lane == 0) sm.far[warp] = far;
-    far = 0.f;
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    if (lane == 0) sm.far[warp] = v;
+    far = LongSum();
     __syncthreads();
-    if (tid == seg) own += (sm.far[0] + sm.far[1]) + (sm.far[2] + sm.far[3]);
+    if (tid == seg) own.add((sm.far[0] + sm.far[1]) + (sm.far[2] + sm.far[3]));
     __syncthreads();
   };
   if (nt > 0) load(0);
   for (int j = 0; j < nt; ++j) {
     const int d0 = j * kTile - (q0 + kRows - 1);
-    if (d0 >= seg_next || (j & 63) == 0) {
-      if (j > 0) flush_far();  // also every 64 tiles, which bounds the length of a sum
+    if (d0 >= seg_next) {
+      if (j > 0) flush_far();
       seg = rel_segment(sm.rs, rel_steps(rel.nseg), d0);
       seg_next = sm.rs.start[seg + 1];
       seg_bias = sm.rs.bias[seg];
@@ -748,11 +749,10 @@ __device__ __forceinline__ void queries_part(const RelF32& p, const RelBias& rel
         for (int i = 0; i < 4; ++i)
           sm.S[r_loc[i >> 1] * (kTile + 1) + 8 * n + 2 * t + (i & 1)] = s[n][i];
     } else {
+      float2 x = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int n = 0; n < kNT; ++n) {
-        const float2 x = fadd2(pair_of(s[n], 0), pair_of(s[n], 1));
-        far += x.x + x.y;
-      }
+      for (int n = 0; n < kNT; ++n) x = fadd2(x, fadd2(pair_of(s[n], 0), pair_of(s[n], 1)));
+      far.add(x.x + x.y);
     }
     if (!skip) {
       scale_columns(s, sm.k_inv, t);
@@ -781,14 +781,15 @@ __device__ __forceinline__ void queries_part(const RelF32& p, const RelBias& rel
       __syncthreads();
 #pragma unroll
       for (int w = 0; w < kWarps; ++w)
-        if (tid >= sm.span[w][0] && tid <= sm.span[w][1]) own += sm.part[w][tid - sm.span[w][0]];
+        if (tid >= sm.span[w][0] && tid <= sm.span[w][1])
+          own.add(sm.part[w][tid - sm.span[w][0]]);
     }
   }
   if (nt > 0) {
     __syncthreads();
     flush_far();
   }
-  if (tid < rel.nseg) rel.partial[(bh * tiles + tile) * rel.nseg + tid] = own;
+  if (tid < rel.nseg) rel.partial[(bh * tiles + tile) * rel.nseg + tid] = own.sum;
   float* out = p.dQ + b * p.st[5][0] + h * p.st[5][1];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
