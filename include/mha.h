@@ -332,6 +332,11 @@ int mha_kv_evict_q8(int B, int H, int Lmax, int Lmax_out, int d_k, int d_v, int 
  *            row; softmax weights and their gradients likewise, with the rows that they multiply); the
  *            generation step takes fused multiply-adds for Nq <= 2 and two tf32 terms per value for
  *            more (2^-22 of the value).  Sums are fp32.
+ *   scores   Weights are exponentials of differences of fp32 numbers.  A score is off by at most 2^-17 of
+ *            scale sum |Q K|, lse as the backward takes it by 2^-24 of itself, and a weight, relatively, by
+ *            as much as the two together: large scores cost accuracy.  bf16: scores of 2^27 and more are
+ *            not supported (rows and gradients hold anything), and where those errors pass 80 the
+ *            backward's gradients may pass bf16's range.  fp32: the backward's weights are at most 1.
  *   special  Keys past key_len[b] (cache_len[b]) may hold anything, infinities and NaN included.  Under
  *   values   the causal mask an infinity or NaN in a row of K reaches only queries that see the key, but
  *            one in V may reach any query (0 times it is no number), and so may one in the backward.

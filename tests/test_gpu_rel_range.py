@@ -6,7 +6,8 @@ import torch
 
 from oracle import rel_bias as ref
 from parity_util import assert_f32_close
-from test_gpu_rel import BF, F, det_mode, dev, draw, host, i32, plain64, within  # noqa: F401
+from test_gpu_rel import (BF, F, check_lse, close, det_mode, dev, draw, host, i32,  # noqa: F401
+                          near_enough, plain64, within)
 
 pytestmark = pytest.mark.gpu
 
@@ -180,3 +181,58 @@ def test_table_gradient_of_long_sequences_bucket_by_bucket(dtype, N, causal):
     within(got.cpu().numpy(), want.cpu().numpy(), (tol + 2.0 ** -24 * want.abs()).cpu().numpy(),
            "dtable")
     assert float((want.abs() / tol.clamp(min=1e-30)).max()) > 50  # (a bucket is empty)
+
+
+# ------------------------------------------------------------------ scales and scores of any size
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("scale", [2.0 ** 64, 2.0 ** -64])
+def test_scale_at_its_ends(dtype, scale, det_mode):
+    # queries that are that much smaller or larger: ordinary scores
+    B, H, N = 1, 2, 200
+    Q, K, V, dO, T = draw(B, H, N, N, dtype, 980)
+    Q = Q / (8 * scale)
+    q, k, v, g, t = (dev(a, dtype) for a in (Q, K, V, dO, T))
+    how = dict(scale=scale)
+    O, lse = mha.sdpa_rel_with_lse(q, k, v, t, **how)
+    got = mha.sdpa_rel_backward(q, k, v, t, O, g, lse, **how)
+    rO, rl = ref.sdpa_rel_ref(Q, K, V, T, **how)
+    check_lse(lse.cpu().numpy(), rl)
+    want = (rO,) + ref.sdpa_rel_bwd_ref(Q, K, V, T, dO, **how)[:3]
+    near_enough(dtype, list(zip((O,) + got[:3], want, ("O", "dQ", "dK", "dV"))), rl,
+                (Q, K, V, T, dO), how, "rel scale", plain=False)
+    n = i32([N])
+    close(dtype)(host(mha.sdpa_rel_decode(q[:, :, :3], k, v, t, n, **how)),
+                 ref.sdpa_rel_decode_ref(Q[:, :, :3], K, V, T, [N], **how), "rel decode scale")
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("mask", ["none", "causal"])
+def test_large_scores(dtype, mask, det_mode):
+    # 2^10 times the scores that the bounds' 2^-15 of a weight goes with: 2^-5, and lse's rounding
+    B, H, N, scale = 1, 2, 300, 128.0
+    Q, K, V, dO, T = draw(B, H, N, N, dtype, 982)
+    q, k, v, g, t = (dev(a, dtype) for a in (Q, K, V, dO, T))
+    how = dict(mask=mask, scale=scale)
+    O, lse = mha.sdpa_rel_with_lse(q, k, v, t, **how)
+    got = mha.sdpa_rel_backward(q, k, v, t, O, g, lse, **how)
+    rO, rl = ref.sdpa_rel_ref(Q, K, V, T, **how)
+    want = (rO,) + ref.sdpa_rel_bwd_ref(Q, K, V, T, dO, **how)[:3]
+    half = 2.0 ** -8 if dtype is BF else 2.0 ** -24
+    bounds = ref.element_bounds(Q, K, V, T, dO, half, 2.0 ** -5 + 2.0 ** -24 * np.abs(rl).max(), **how)
+    for a, w, tol, n in zip((O,) + got[:3], want, bounds, ("O", "dQ", "dK", "dV")):
+        within(host(a), w, tol, n)
+
+
+@pytest.mark.parametrize("dtype,scale", [(BF, 2.0 ** 18), (F, 2.0 ** 18), (F, 2.0 ** 30), (F, 2.0 ** 64)])
+@pytest.mark.parametrize("mask", ["none", "causal"])
+def test_gradients_of_huge_scores_are_finite(dtype, scale, mask, det_mode):
+    # scores of up to 2^24 (fp32: 2^70) and an lse as large, whose difference is mostly rounding
+    B, H, N = 1, 2, 300
+    Q, K, V, dO, T = draw(B, H, N, N, dtype, 981)
+    q, k, v, g, t = (dev(a, dtype) for a in (Q, K, V, dO, T))
+    O, lse = mha.sdpa_rel_with_lse(q, k, v, t, mask, scale=scale)
+    dq, dk, dv, dt = mha.sdpa_rel_backward(q, k, v, t, O, g, lse, mask, scale=scale)
+    for x in (O, lse, dq, dk, dv, dt):
+        assert torch.all(torch.isfinite(x))
+    if dtype is F:  # weights of at most 1, times factors off by 2^-22, added up
+        assert np.all(np.abs(host(dv)) <= np.abs(dO).sum(2, keepdims=True) * (1 + 2.0 ** -15))

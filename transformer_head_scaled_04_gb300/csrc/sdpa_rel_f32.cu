@@ -461,6 +461,14 @@ __device__ __forceinline__ int keys_of(const RelF32& p, int b) {
   return p.mask == 2 ? min(max(__ldg(p.key_len + b), 0), p.Nk) : p.Nk;
 }
 
+// x, at most 0 (NaN stays NaN): the exponent x - lse of a weight that the backward rebuilds.  Scores and
+// lse may be so large that their difference is rounding, several hundred from 2^30 on; no weight passes 1.
+__device__ __forceinline__ float at_most_0(float x) {
+  float y;
+  asm("min.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // x = s f + t, f = f0 (row g) or f1 (g + 8) times col[column]; t the constant, or of the lane's columns
 // 8 n + 2 t, + 1 and rows g, g + 8 from the table (at: its entry for column 2 t and row g; a row less is
 // a distance more)
@@ -735,7 +743,7 @@ __device__ __forceinline__ void queries_part(const RelF32& p, const RelBias& rel
         for (int i = 0; i < 2; ++i) {
           float2 x = fadd2(pair_of(s[n], i), make_float2(-lse[i], -lse[i]));
           x = fmul2(x, make_float2(kLog2e, kLog2e));
-          x = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+          x = make_float2(ex2_approx(at_most_0(x.x)), ex2_approx(at_most_0(x.y)));
           const float2 fg = fmul2(make_float2(g_inv[i], g_inv[i]), c);
           set_pair(s[n], i, fmul2(x, ffma2(pair_of(dp[n], i), fg, make_float2(-D[i], -D[i]))));
         }
@@ -901,7 +909,7 @@ __device__ __forceinline__ void keys_part(const RelF32& p, const RelBias& rel, D
         for (int e = 0; e < 2; ++e) {
           float2 x = fadd2(pair_of(s[n], e), lse);
           x = fmul2(x, make_float2(kLog2e, kLog2e));
-          x = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+          x = make_float2(ex2_approx(at_most_0(x.x)), ex2_approx(at_most_0(x.y)));
           set_pair(s[n], e, x);
           const float2 fg = fmul2(make_float2(v_inv[e], v_inv[e]), c);
           set_pair(ds[n], e, fmul2(x, ffma2(pair_of(ds[n], e), fg, D)));
