@@ -103,3 +103,20 @@ def test_decode_is_the_last_rows_of_the_causal_forward():
     assert np.allclose(short[0], O[0, :, 3:5], atol=1e-14)
     # one cached position, two queries: the first has none to see, the second sees that one
     assert np.all(short[1, :, 0] == 0) and np.allclose(short[1, :, 1], V[1, :, 0])
+
+
+@pytest.mark.parametrize("num,reach,both,n", [
+    (7, 8020466, False, 198349), (8, 15688794, False, 352539), (16, 15688794, True, 352539),
+    (10, 5497271, False, 340339), (16, 2382133, False, 492869), (31, 10443359, False, 29016),
+    (64, 13251718, True, 79977), (64, 1124401, False, 584535), (128, 16723489, True, 11082401),
+    # and borders that are whole numbers
+    (32, 128, True, 16), (32, 128, True, 64), (8, 32, False, 32), (128, 64 * 2 ** 16, False, 128)])
+def test_library_buckets_next_to_a_border(num, reach, both, n):
+    # a border lies at n or above it by less than 1e-12 of it (n then belongs to the nearer bucket)
+    import transformer_head_scaled_04_gb300 as mha
+    from transformer_head_scaled_04_gb300 import build
+
+    build.build()
+    for d in (n - 1, n, n + 1):
+        for s in (1, -1):
+            assert mha.rel_bucket(s * d, num, reach, both) == bucket_ref(s * d, num, reach, both)

@@ -13,13 +13,44 @@
 namespace mha {
 namespace {
 
-// The first n of bucket e + t: the least whole n with n >= e (max_distance / e)^(t / (per - e)).
-// Where that border is a whole number (16 = 8 * 16^(2/8)) its double may come out a little above;
-// 1e-12 of it covers the rounding of pow and lies far below the next whole number's distance.
+// A whole number of up to 64 factors below 2^24.
+struct Product {
+  uint32_t w[48] = {1};
+  int n = 1;
+  void times(uint32_t f, int count) {
+    for (; count > 0; --count) {
+      uint64_t carry = 0;
+      for (int i = 0; i < n; ++i) {
+        carry += static_cast<uint64_t>(w[i]) * f;
+        w[i] = static_cast<uint32_t>(carry);
+        carry >>= 32;
+      }
+      if (carry != 0) w[n++] = static_cast<uint32_t>(carry);
+    }
+  }
+  bool at_least(const Product& o) const {
+    if (n != o.n) return n > o.n;
+    for (int i = n - 1; i >= 0; --i)
+      if (w[i] != o.w[i]) return w[i] > o.w[i];
+    return true;
+  }
+};
+
+// The first n of bucket e + t: the least whole n with n >= e (max_distance / e)^(t / (per - e)).  Where
+// that border is a whole number (16 = 8 * 16^(2/8)) its double may come out on either side of it; others lie
+// as close to one without being one (8 of per = 8, max_distance = 15688794: 3e-13 of it above 352539).
+// 1e-12 covers the rounding of pow and lies far below the next whole number's distance: within that a
+// comparison of whole numbers decides, n^(per - e) >= e^(per - e - t) max_distance^t.
 int first_of(int t, int per, int e, int max_distance) {
   const double b = e * std::pow(static_cast<double>(max_distance) / e,
                                 static_cast<double>(t) / (per - e));
-  return static_cast<int>(std::ceil(b * (1.0 - 1e-12)));
+  const int n = static_cast<int>(std::ceil(b * (1.0 - 1e-12)));
+  if (n > b * (1.0 + 1e-12)) return n;
+  Product left, right;
+  left.times(n, per - e);
+  right.times(e, per - e - t);
+  right.times(max_distance, t);
+  return left.at_least(right) ? n : n + 1;
 }
 
 }  // namespace
