@@ -331,7 +331,7 @@ int mha_kv_evict_q8(int B, int H, int Lmax, int Lmax_out, int d_k, int d_v, int 
  *            row of Q, K, V and dO (off by at most 2^-23 of the value or 2^-38 of the largest in its
  *            row; softmax weights and their gradients likewise, with the rows that they multiply); the
  *            generation step takes fused multiply-adds for Nq <= 2 and two tf32 terms per value for
- *            more (2^-22 of the value).  Sums are fp32.
+ *            more (off by at most 2^-23 of the value).  A product drops at most 2^-22 of itself.  Sums are fp32.
  *   scores   Weights are exponentials of differences of fp32 numbers.  A score is off by at most 2^-17 of
  *            scale sum |Q K|, lse as the backward takes it by 2^-24 of itself, and a weight, relatively, by
  *            as much as the two together: large scores cost accuracy.  bf16: scores of 2^27 and more are

@@ -1,9 +1,10 @@
 // mma_tf32.cuh -- products of fp32 values on the tensor cores: every value is split into two tf32
 // terms, x = hi + lo (hi the nearest tf32, lo what is left), and a b is taken as
-// hi_a hi_b + hi_a lo_b + lo_a hi_b with fp32 sums.  hi keeps 11 bits and lo, at most 2^-12 |x|, is cut
-// to 11 bits by the product, so a factor is off by at most 2^-22 of itself and the dropped lo_a lo_b
-// is at most 2^-24 |a b|: fp32's own accuracy but for a few bits, at 3 products of a tf32 rate that
-// is four times the FMA units' (298 against 74 TFLOP/s measured and computed for 152 SMs).
+// hi_a hi_b + hi_a lo_b + lo_a hi_b with fp32 sums.  A tf32 keeps 10 stored bits, so lo is at most
+// 2^-11 |x|; it has 12 bits and the product cuts it to 11, which leaves a factor off by at most 2^-23 of
+// itself.  The dropped lo_a lo_b is at most 2^-22 |a b|: fp32's own accuracy but for a few bits, at 3
+// products of a tf32 rate that is four times the FMA units' (298 against 74 TFLOP/s measured and
+// computed for 152 SMs).
 #pragma once
 
 #include <cstdint>
