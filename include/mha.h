@@ -339,8 +339,10 @@ int mha_kv_evict_q8(int B, int H, int Lmax, int Lmax_out, int d_k, int d_v, int 
  *            backward's gradients may pass bf16's range.  fp32: the backward's weights are at most 1.
  *   special  Keys past key_len[b] (cache_len[b]) may hold anything, infinities and NaN included.  Under
  *   values   the causal mask an infinity or NaN in a row of K reaches only queries that see the key, but
- *            one in V may reach any query (0 times it is no number), and so may one in the backward.
- *            fp32: a query that sees an infinity in K gets NaN.
+ *            one in V may reach any query (0 times it is no number), and so may one in the backward,
+ *            given or come of a product's overflow.  A key that its bucket alone excludes counts as seen.
+ *            fp32: a query that sees an infinity in K gets NaN.  Finite rows that are not seen change
+ *            nothing.
  *   aliasing outputs (and the workspace) may not overlap inputs or one another.
  */
 
