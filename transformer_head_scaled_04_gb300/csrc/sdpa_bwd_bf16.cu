@@ -245,7 +245,8 @@ __device__ __forceinline__ void diagonal_sums(const uint32_t (&g)[32], int lane,
 
 // Adds the values of the lanes of each segment up and the sums to their owners.  v[e] of the lanes belong
 // to segments seg[e], which do not fall with the lane; part: 32 floats for each e (one per segment from
-// its first on).  The three scans run side by side (one after the other: 5 x 3 heads of 777 37.4 us, so 34.6).
+// its first on).  The three scans run side by side (one after the other: 5 x 3 heads of 777 37.4 us, so 34.6;
+// 35.6 with LongSum).
 // own is indexed by a variable on purpose: it stays in local memory, away from the registers of steps that
 // need none.
 __device__ __forceinline__ void segment_sums(float (&v)[3], const int (&seg)[3], int lane, float* part,
@@ -933,7 +934,8 @@ __global__ void __launch_bounds__(kKThreads, 1)
       }
       // Rel: a step that takes the table and one of two blocks of one segment each run code of their
       // own, with marks at both ends that keep the compiler from merging parts of them: moves between
-      // the variants' registers cost 200 instructions a step (2025 us for the big model's heads, 1652 so)
+      // the variants' registers cost 200 instructions a step (2025 us for the big model's heads, 1652 so; 1663
+      // with LongSum)
       auto step = [&](auto kind) -> bool {
         [[maybe_unused]] constexpr bool kTable = decltype(kind)::value;
         tc_fence_after();

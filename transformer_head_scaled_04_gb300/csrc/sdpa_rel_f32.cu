@@ -33,17 +33,18 @@
 //          words for a d lie side by side, so that 16 bytes are the fragments of two d; the output's
 //          columns are d = 16 v + 2 g + e
 // and the CTA's own rows once into fragments, 16 bytes per lane and step: a lane's registers are filled
-// in the order in which the product takes them, with no moves between (8 x 8 heads of 1001: with moves
-// and unpaired arithmetic 223 us forward and 768 backward, without 196 and 698),
+// in the order in which the product takes them, with no moves between (8 x 8 heads of 1001, with a scale
+// per tile: with moves and unpaired arithmetic 223 us forward and 768 backward, without 196 and 705),
 // so that scores go into the next product without any exchange.  d is padded to 64 or 128 with zeros.
 // The bias of a tile that lies within one segment is a constant; otherwise the CTA looks its distances
 // up once into a table.  Bound by the products, three per multiply-add of the formulas, and in the
 // backward S and dP twice (dQ by its own kernel: no atomics, reproducible), and by the latencies between
-// the barriers of a tile: the forward reaches half of the 590 TFLOP/s that these products measured alone
-// (2 x 16 heads of 4096 1376 us), with 12 warps on an SM that issue in 38% of the cycles.  Not taken: 32
-// rows per warp, which halves the reads of K and V (1257 us there, but 52 instead of 41 for 4 x 8 causal
-// heads of 500 and nothing gained at 8 x 8 of 1001), two buffers for the terms and a barrier less (206
-// us instead of 195 at 8 x 8 heads of 1001).
+// the barriers of a tile: the forward reaches 272 of the 590 TFLOP/s that these products measured alone
+// (2 x 16 heads of 4096 1514 us), with 12 warps on an SM that issue in 40% of the cycles.  Not taken
+// (measured with a scale per tile, when that case took 1376 us): 32 rows per warp, which halves the reads of
+// K and V (1257 us there, but 52 instead of 41 for 4 x 8 causal heads of 500 and nothing gained at 8 x 8 of
+// 1001), two buffers for the terms (206 us instead of 195 at 8 x 8 heads of 1001); and, with a scale per
+// row, weights' scales from their rows' maxima where a tile's rows of V are alike (218 us instead of 214).
 #include <cmath>
 
 #include "device_common.cuh"
@@ -935,10 +936,10 @@ __device__ __forceinline__ void keys_part(const RelF32& p, const RelBias& rel, D
 
 // A CTA takes 64 keys or 64 queries of a head, first the keys of all heads, then the queries: one launch
 // keeps the GPU filled where one kind alone would leave it waiting for its longest CTAs (4 x 8 heads of
-// 500, causal: 112 us in two launches, 77 in one, 70 since), and the two kinds' code meets on an SM only in
+// 500, causal: 112 us in two launches, 77 in one, 72 now), and the two kinds' code meets on an SM only in
 // between (keys and queries of a head side by side, 8 x 8 heads of 1001: 858 us).  A tile takes a
 // CTA alone on its SM 4 us and two CTAs 2 us each: what bounds it is latency between barriers with
-// eight warps on an SM; 242 registers leave no third CTA room.
+// eight warps on an SM; 248 registers leave no third CTA room.
 template <int DP>
 struct BwdSmem {
   union {
