@@ -35,6 +35,8 @@ def test_fp32_rows_that_are_not_seen_may_be_of_any_size(hidden, where, size, d):
     # One huge row that no row of ordinary size sees (or only at a weight of e^-60): the others keep
     # fp32's accuracy.  The last key is seen by the last query alone, whose own row is 0, so that its
     # scores and gradients stay ordinary; the first query sees the first key alone, likewise 0.
+    if hidden == "faint" and size > 1e12:
+        pytest.skip("at e^-60 it is not faint any more")
     B, H, N = 1, 2, 150
     Q, K, V, dO, T = draw(B, H, N, N, F, 960, dk=d, dv=d)
     if where == "keys":
@@ -47,8 +49,6 @@ def test_fp32_rows_that_are_not_seen_may_be_of_any_size(hidden, where, size, d):
         K[:, :, 0] = V[:, :, 0] = 0
         if hidden != "faint":
             Q[:, :, 0] *= size
-    if hidden == "faint" and size > 1e12:
-        return  # at e^-60 it is not faint any more
     Q, K, V, dO = (np.asarray(a, np.float32).astype(np.float64) for a in (Q, K, V, dO))
     if hidden != "causal":  # keys after the query
         T[16:] = -np.inf if hidden == "excluded" else -60.0
@@ -56,7 +56,7 @@ def test_fp32_rows_that_are_not_seen_may_be_of_any_size(hidden, where, size, d):
     q, k, v, g, t = (dev(a, F) for a in (Q, K, V, dO, T))
     O, lse = mha.sdpa_rel_with_lse(q, k, v, t, **how)
     got = mha.sdpa_rel_backward(q, k, v, t, O, g, lse, **how)
-    with np.errstate(invalid="ignore"):
+    with np.errstate(invalid="ignore", over="ignore"):
         rO, rl = ref.sdpa_rel_ref(Q, K, V, T, **how)
         want = (rO,) + ref.sdpa_rel_bwd_ref(Q, K, V, T, dO, **how)[:3]
         bounds = ref.element_bounds(Q, K, V, T, dO, 2.0 ** -24, 2.0 ** -15 + 2.0 ** -24 * 16, **how)
@@ -67,7 +67,7 @@ def test_fp32_rows_that_are_not_seen_may_be_of_any_size(hidden, where, size, d):
         plain = slice(1, -1)  # the rows of ordinary size, held to the fp32 path's own bounds
         assert_f32_close(host(a)[:, :, plain], w[:, :, plain], f"rel hidden rows {n}")
     given = (host(O), lse.cpu().numpy())
-    with np.errstate(invalid="ignore"):
+    with np.errstate(invalid="ignore", over="ignore"):
         w = ref.sdpa_rel_bwd_ref(Q, K, V, T, dO, given=given, **how)[3]
         tol = ref.table_grad_bound(Q, K, V, T, dO, *given, **how)
     within(host(got[3]), w, tol + 2.0 ** -24 * np.abs(w), "dtable")
