@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 import torch
 
+import seeded_inputs as si
 from oracle import rel_bias as ref
 from parity_util import assert_f32_close
 from test_gpu_rel import (BF, F, check_lse, close, det_mode, dev, draw, host, i32,  # noqa: F401
@@ -71,6 +72,38 @@ def test_fp32_rows_that_are_not_seen_may_be_of_any_size(hidden, where, size, d):
         w = ref.sdpa_rel_bwd_ref(Q, K, V, T, dO, given=given, **how)[3]
         tol = ref.table_grad_bound(Q, K, V, T, dO, *given, **how)
     within(host(got[3]), w, tol + 2.0 ** -24 * np.abs(w), "dtable")
+
+
+@pytest.mark.parametrize("size", [1e8, 1e30])
+@pytest.mark.parametrize("where", ["keys", "queries"])
+@pytest.mark.parametrize("hidden", ["causal", "excluded"])
+def test_bf16_rows_that_are_not_seen_may_be_of_any_size(hidden, where, size, det_mode):
+    # the same inputs in bf16: every element within its own bound
+    B, H, N = 1, 2, 150
+    Q, K, V, dO, T = draw(B, H, N, N, BF, 961)
+    if where == "keys":
+        K[:, :, -1] *= size
+        V[:, :, -1] *= size
+        Q[:, :, -1] = dO[:, :, -1] = 0
+    else:
+        Q[:, :, 0] *= size
+        dO[:, :, 0] *= size
+        K[:, :, 0] = V[:, :, 0] = 0
+    Q, K, V, dO = (si.round_bf16(a) for a in (Q, K, V, dO))
+    if hidden == "excluded":
+        T[16:] = -np.inf
+    how = dict(mask="causal" if hidden == "causal" else "none", max_distance=128)
+    q, k, v, g = (dev(a, BF) for a in (Q, K, V, dO))
+    t = dev(T, F)
+    O, lse = mha.sdpa_rel_with_lse(q, k, v, t, **how)
+    got = mha.sdpa_rel_backward(q, k, v, t, O, g, lse, **how)
+    with np.errstate(invalid="ignore", over="ignore"):
+        rO, rl = ref.sdpa_rel_ref(Q, K, V, T, **how)
+        want = (rO,) + ref.sdpa_rel_bwd_ref(Q, K, V, T, dO, **how)[:3]
+        bounds = ref.element_bounds(Q, K, V, T, dO, 2.0 ** -8, 2.0 ** -15 + 2.0 ** -24 * 16, **how)
+    check_lse(lse.cpu().numpy(), rl)
+    for a, w, tol, n in zip((O,) + got[:3], want, bounds, ("O", "dQ", "dK", "dV")):
+        within(host(a), w, tol, n)
 
 
 # ------------------------------------------------------------------ lengths that the last launch writes
